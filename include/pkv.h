@@ -66,6 +66,8 @@ typedef enum pkv_status {
 #define PKV_DEVERR_SLOT 2u       /* slot_mapping entry >= num_blocks*16       */
 #define PKV_DEVERR_CONTEXT 4u    /* context_lens[r] > max_blocks_per_seq*16   */
 #define PKV_DEVERR_TIMEOUT 8u    /* a pipeline wait gave up (never expected)  */
+#define PKV_DEVERR_POSITION 16u  /* a position outside the rotation table     */
+#define PKV_DEVERR_ACCEPTED 32u  /* accepted drafts not a rising list of drafts */
 
 /* Geometry of one layer's paged cache (both K and V use it). */
 typedef struct pkv_cache_desc {
@@ -549,6 +551,146 @@ pkv_status pkv_copy_blocks_fp8_e4m3(void* k_cache, void* v_cache, const pkv_cach
                                     const int32_t* src_blocks, const int32_t* dst_blocks, int32_t num_pairs,
                                     void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A verification step of drafted tokens (§8.5.2: verifying several drafted
+ * positions reads the same KV as one decode step), layer by layer:
+ *   pkv_qk_norm_rope_append   the drafts' queries, keys and values: norms,
+ *                             rotation, store
+ *   pkv_paged_attention_tree  each draft against the committed context and
+ *                             its own ancestors (pkv_paged_attention_window in
+ *                             layers with a sliding window)
+ * and, once the accepted path is known,
+ *   pkv_kv_compact            the accepted drafts' K and V to the places behind
+ *                             the committed context, in every layer.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum pkv_kv_format { PKV_KV_BF16 = 0, PKV_KV_Q8_0 = 1, PKV_KV_FP8_E4M3 = 2 } pkv_kv_format;
+
+/* Drafted tokens per request (tree_len of the calls below) at most. */
+#define PKV_MAX_TREE_LEN 1024
+
+/*
+ * pkv_qk_norm_rope_append -- norms of every query and key head, rotation by
+ * position, and the append of K and V, in one pass over the projections'
+ * output.  Per head vector x (FP32):
+ *     y = x * rsqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ *     z = y with its first rot_dim values rotated in pairs by the position's
+ *         angles:  z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin
+ * and one rounding: q_out to BF16, K to the pool's format (its append's
+ * rounding, applied to the FP32 value).  V is stored as the append stores it.
+ *   q_out        : device BF16 [num_tokens][num_q_heads][128].  May be q itself
+ *                  when q_stride is num_q_heads * 128; no other overlap.
+ *   k_cache, v_cache, cache, slot_mapping : as for the append of kv_format;
+ *                  a token with a slot < 0 gets its q_out and is not stored.
+ *   q, k, v      : device BF16; token t's heads start q_stride (k_stride,
+ *                  v_stride) elements after token t - 1's and are contiguous
+ *                  [num_q_heads or num_kv_heads][128].  Strides are multiples
+ *                  of 8, at least one token's heads; pointers 16-byte aligned.
+ *   q_weight, k_weight : device BF16 [128], shared by the heads; NULL = no norm.
+ *   rope_table   : device FP32 [max_positions][rot_dim]: the position's
+ *                  rot_dim/2 cosines, then its rot_dim/2 sines; 16-byte aligned.
+ *   positions    : device int32 [num_tokens]; outside [0, max_positions) sets
+ *                  PKV_DEVERR_POSITION (the nearest row is used).
+ *   rot_dim      : 0 (no rotation: rope_table and positions may be NULL) or a
+ *                  multiple of 16 up to 128.
+ *   interleaved  : 0 = pairs (i, i + rot_dim/2), else pairs (2i, 2i + 1).
+ *   eps          : finite, >= 0.
+ */
+pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                                   int32_t kv_format, const int64_t* slot_mapping, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   int32_t num_q_heads, const void* q_weight, const void* k_weight, float eps,
+                                   const float* rope_table, int32_t max_positions, int32_t rot_dim,
+                                   int32_t interleaved, const int32_t* positions, int32_t num_tokens, void* stream);
+
+/*
+ * pkv_paged_attention_tree -- attention of a tree of drafted tokens over the
+ * cache.  Request r's last n_r tokens (n_r = tree_lens[r]) are its drafts, in
+ * any order that puts a parent before its children; with base = context_lens[r]
+ * - n_r, draft i sees the keys 0 .. base - 1 and the drafts j whose bit is set
+ * in its mask row (normally its ancestors and itself, but any mask will do).
+ *   out, q       : device BF16 [num_seqs][tree_len][num_q_heads][128].  Rows
+ *                  i >= n_r, rows that see no key, and all rows of a request
+ *                  with context_lens[r] <= 0 get zeros.
+ *   context_lens : int32 [num_seqs], the drafts included (append, then attend).
+ *   tree_lens    : device int32 [num_seqs], each in [0, tree_len] (clamped);
+ *                  NULL = tree_len for every request.
+ *   tree_mask    : device uint64 [num_seqs][tree_len][ceil(tree_len / 64)]: bit
+ *                  j % 64 of word j / 64 = draft j is visible.  Bits >= n_r are
+ *                  ignored.
+ *   tree_len     : 1 .. PKV_MAX_TREE_LEN.
+ *   scale        : > 0.
+ *   kv_blocks_per_split : 0 = pkv_choose_kv_blocks_per_split_tree; otherwise
+ *                  rounded up to whole tiles of the kernel (4 or 8 blocks).
+ *                  >= max_blocks_per_seq = one pass.
+ *   workspace    : device, 256-byte aligned, pkv_workspace_size_tree(...) bytes
+ *                  for the same kv_blocks_per_split (may be NULL when 0).
+ * The other arguments are those of pkv_paged_attention.  K and V of every
+ * token of the context must be finite; slots past it may hold anything.
+ */
+int32_t pkv_choose_kv_blocks_per_split_tree(int32_t num_seqs, int32_t num_kv_heads, int32_t tree_len,
+                                            int32_t max_blocks_per_seq, int32_t sm_count);
+size_t pkv_workspace_size_tree(int32_t num_seqs, int32_t tree_len, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                               int32_t kv_blocks_per_split);
+pkv_status pkv_paged_attention_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                    const pkv_cache_desc* cache, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                    const int32_t* tree_lens, const uint64_t* tree_mask, int32_t num_seqs,
+                                    int32_t tree_len, int32_t num_q_heads, float scale, int32_t kv_blocks_per_split,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pkv_paged_attention_window -- attention with a sliding window whose first
+ * tokens stay visible: the query at position p sees the keys t <= p with
+ * t > p - window or t < num_sinks.  q_len, context_lens, out and q as for
+ * pkv_paged_attention (1 = decode, more = a causal chunk of any length).
+ *   window       : >= 1, the query's own token included.
+ *   num_sinks    : >= 0.
+ *   scale        : > 0.
+ *   kv_blocks_per_split, workspace : as for pkv_paged_attention_tree, counted in
+ *                  the blocks that a request's queries see.
+ * Blocks that no query of the call sees are neither read nor looked up: their
+ * table entries may be stale (the pages given back).
+ */
+int32_t pkv_choose_kv_blocks_per_split_window(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
+                                              int32_t max_blocks_per_seq, int32_t window, int32_t num_sinks,
+                                              int32_t sm_count);
+size_t pkv_workspace_size_window(int32_t num_seqs, int32_t q_len, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                 int32_t window, int32_t num_sinks, int32_t kv_blocks_per_split);
+pkv_status pkv_paged_attention_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                      const pkv_cache_desc* cache, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t q_len, int32_t num_q_heads, int32_t window, int32_t num_sinks,
+                                      float scale, int32_t kv_blocks_per_split, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * pkv_kv_compact -- keep the accepted drafts: in every layer, K and V of
+ * request r's draft accepted[r][j] move to position base + j, j <
+ * num_accepted[r], base = context_lens[r] - tree_lens[r] (context_lens as in
+ * the verification call, the drafts included).  The caller then sets
+ * context_lens[r] to base + num_accepted[r].  Bit for bit; one launch per 64
+ * layers.
+ *   k_caches, v_caches : host arrays of num_layers device pointers (pools of
+ *                  kv_format, geometry `cache`).
+ *   tree_lens    : as for pkv_paged_attention_tree (NULL = tree_len).
+ *   accepted     : device int32 [num_seqs][max_accepted], the accepted drafts
+ *                  of each request in rising order.
+ *   num_accepted : device int32 [num_seqs], in [0, max_accepted].
+ *   max_accepted : 1 .. tree_len.
+ * A request whose list does not rise, leaves [0, n_r) or is longer than n_r or
+ * max_accepted sets PKV_DEVERR_ACCEPTED; one whose context is shorter than its
+ * tree or longer than the table sets PKV_DEVERR_CONTEXT; one with a needed
+ * block id outside the pool sets PKV_DEVERR_BLOCK_ID: nothing of it is moved.
+ * The drafts' blocks must not be shared with another request.
+ */
+pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                          const pkv_cache_desc* cache, int32_t kv_format, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* tree_lens,
+                          int32_t num_seqs, int32_t tree_len, const int32_t* accepted, const int32_t* num_accepted,
+                          int32_t max_accepted, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* pkv_status_string(pkv_status status);
 
@@ -600,8 +742,6 @@ const char* pkv_status_string(pkv_status status);
  * both graphs; the caller must not destroy a graph while a launch of it may
  * still run.  The device error word behaves as for the direct calls.
  */
-typedef enum pkv_kv_format { PKV_KV_BF16 = 0, PKV_KV_Q8_0 = 1, PKV_KV_FP8_E4M3 = 2 } pkv_kv_format;
-
 typedef struct pkv_decode_graph_buffers {
   const void* q;
   const void* k_new;

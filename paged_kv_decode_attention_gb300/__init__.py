@@ -28,6 +28,9 @@ __all__ = [
     "choose_kv_blocks_per_split_q8_0", "choose_kv_blocks_per_split_fp8_e4m3", "workspace_size_q8_0", "copy_blocks_q8_0", "FP8_TILE_BYTES",
     "kv_append_fp8_e4m3", "paged_attention_fp8_e4m3", "paged_attention_fp8_e4m3_append",
     "paged_attention_q8_0_append", "copy_blocks_fp8_e4m3",
+    "qk_norm_rope_append", "paged_attention_tree", "choose_kv_blocks_per_split_tree", "workspace_size_tree",
+    "paged_attention_window", "choose_kv_blocks_per_split_window", "workspace_size_window", "KvPools", "kv_compact",
+    "MAX_TREE_LEN", "DEVERR_POSITION", "DEVERR_ACCEPTED",
     "DecodeGraph", "KV_BF16", "KV_Q8_0", "KV_FP8_E4M3", "selftest_bounded_wait",
 ]
 
@@ -35,6 +38,8 @@ DEVERR_BLOCK_ID = 1
 DEVERR_SLOT = 2
 DEVERR_CONTEXT = 4
 DEVERR_TIMEOUT = 8
+DEVERR_POSITION = 16
+DEVERR_ACCEPTED = 32
 
 BLOCK_SIZE = 16
 HEAD_DIM = 128
@@ -144,6 +149,24 @@ def _load():
     lib.pkv_paged_attention_fp8_e4m3_append.restype = ctypes.c_int
     lib.pkv_paged_attention_q8_0_append.argtypes = lib.pkv_paged_attention_fp8_e4m3_append.argtypes
     lib.pkv_paged_attention_q8_0_append.restype = ctypes.c_int
+    cd = ctypes.POINTER(CacheDesc)
+    lib.pkv_qk_norm_rope_append.argtypes = [p, p, p, cd, i32, p, p, i64, p, i64, p, i64, i32, p, p, f32, p, i32, i32,
+                                            i32, p, i32, p]
+    lib.pkv_qk_norm_rope_append.restype = ctypes.c_int
+    lib.pkv_choose_kv_blocks_per_split_tree.argtypes = [i32, i32, i32, i32, i32]
+    lib.pkv_choose_kv_blocks_per_split_tree.restype = i32
+    lib.pkv_workspace_size_tree.argtypes = [i32, i32, i32, i32, i32]
+    lib.pkv_workspace_size_tree.restype = sz
+    lib.pkv_paged_attention_tree.argtypes = [p, p, p, p, cd, p, i32, p, p, p, i32, i32, i32, f32, i32, p, sz, p]
+    lib.pkv_paged_attention_tree.restype = ctypes.c_int
+    lib.pkv_choose_kv_blocks_per_split_window.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.pkv_choose_kv_blocks_per_split_window.restype = i32
+    lib.pkv_workspace_size_window.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.pkv_workspace_size_window.restype = sz
+    lib.pkv_paged_attention_window.argtypes = [p, p, p, p, cd, p, i32, p, i32, i32, i32, i32, i32, f32, i32, p, sz, p]
+    lib.pkv_paged_attention_window.restype = ctypes.c_int
+    lib.pkv_kv_compact.argtypes = [p, p, i32, cd, i32, p, i32, p, p, i32, i32, p, p, i32, p]
+    lib.pkv_kv_compact.restype = ctypes.c_int
     lib.pkv_decode_graph_create.argtypes = [ctypes.POINTER(DecodeGraphDesc), ctypes.POINTER(ctypes.c_void_p)]
     lib.pkv_decode_graph_create.restype = ctypes.c_int
     lib.pkv_decode_graph_launch.argtypes = [p, i32, p]
@@ -156,7 +179,6 @@ def _load():
     lib.pkv_selftest_bounded_wait.restype = ctypes.c_int
     lib.pkv_status_string.argtypes = [ctypes.c_int]
     lib.pkv_status_string.restype = ctypes.c_char_p
-    del i64
     return lib, path
 
 
@@ -678,6 +700,243 @@ def copy_blocks_fp8_e4m3(k_cache: torch.Tensor, v_cache: torch.Tensor, src_block
     _check(_lib.pkv_copy_blocks_fp8_e4m3(k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
                                          src_blocks.data_ptr(), dst_blocks.data_ptr(), src_blocks.numel(),
                                          _stream_ptr(stream)), "pkv_copy_blocks_fp8_e4m3")
+
+
+# ---------------------------------------------------------------------------
+# A verification step of drafted tokens, and sliding-window attention
+# ---------------------------------------------------------------------------
+MAX_TREE_LEN = 1024
+
+_BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
+_I32_ONLY = (torch.int32,)
+_I64_ONLY = (torch.int64,)
+_MASK_WORDS = (torch.int64, torch.uint64)
+
+
+def _on_device(dev: int, t: torch.Tensor, name: str, dtypes) -> int:
+    """Address of a contiguous tensor of one of `dtypes` on CUDA device `dev`."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must hold {dtypes[0]} values, got {t.dtype}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _workspace(dev: int, t) -> tuple:
+    if t is None:
+        return 0, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _pool(dev: int, t: torch.Tensor, name: str, kv_format: int) -> tuple:
+    """(address, CacheDesc) of one pool of the given format."""
+    if kv_format == KV_BF16:
+        addr = _on_device(dev, t, name, _BF16_LIKE)
+        shape = t.shape
+        if len(shape) != 4:
+            raise ValueError(f"{name} must be [num_blocks][num_kv_heads][16][128]")
+        return addr, CacheDesc(shape[0], shape[2], shape[1], shape[3])
+    addr = _on_device(dev, t, name, (torch.uint8, torch.int8))
+    shape = t.shape
+    if kv_format == KV_Q8_0:
+        if len(shape) != 3 or shape[2] != Q8_TILE_BYTES:
+            raise ValueError(f"{name} must be [num_blocks][num_kv_heads][{Q8_TILE_BYTES}]")
+    elif kv_format == KV_FP8_E4M3:
+        if len(shape) != 4 or shape[2] != BLOCK_SIZE or shape[3] != HEAD_DIM:
+            raise ValueError(f"{name} must be [num_blocks][num_kv_heads][16][128]")
+    else:
+        raise ValueError(f"unknown kv_format {kv_format}")
+    return addr, CacheDesc(shape[0], BLOCK_SIZE, shape[1], HEAD_DIM)
+
+
+def _heads(dev: int, t: torch.Tensor, name: str, tokens: int, heads: int) -> tuple:
+    """(address, token stride) of BF16 [tokens][heads][128] whose heads are contiguous."""
+    if t.dtype not in _BF16_LIKE:
+        raise TypeError(f"{name} must hold BF16 values, got {t.dtype}")
+    if t.get_device() != dev or t.dim() != 3 or tuple(t.shape) != (tokens, heads, HEAD_DIM):
+        raise ValueError(f"{name} must be [num_tokens][{heads}][{HEAD_DIM}] on the current CUDA device")
+    st, sh, sd = t.stride()
+    if tokens > 0 and (sd != 1 or (heads > 1 and sh != HEAD_DIM)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (st if tokens > 1 else heads * HEAD_DIM)
+
+
+def qk_norm_rope_append(q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        slot_mapping: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor | None = None, rope_table: torch.Tensor | None = None,
+                        q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                        eps: float = 1e-6, interleaved: bool = False, kv_format: int = KV_BF16, stream=None) -> None:
+    """RMS norms of the query and key heads, rotation by position, and the append of K and V, in one pass.
+
+    q [T][Hq][128], k, v [T][Hkv][128] (BF16; views into a projection's output: only a token's heads must be
+    contiguous); q_out [T][Hq][128]; slot_mapping int64 [T] (< 0: not stored); positions int32 [T]; rope_table
+    float32 [max_positions][rot_dim], cosines then sines (None: no rotation); q_weight, k_weight BF16 [128]
+    (None: no norm); pools of `kv_format`.  See include/pkv.h."""
+    dev = torch.cuda.current_device()
+    kc, desc = _pool(dev, k_cache, "k_cache", kv_format)
+    vc, _ = _pool(dev, v_cache, "v_cache", kv_format)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    slots = _on_device(dev, slot_mapping, "slot_mapping", _I64_ONLY)
+    tokens, hkv = slot_mapping.numel(), desc.num_kv_heads
+    hq = q.shape[1] if q.dim() == 3 else 0
+    qa, qs = _heads(dev, q, "q", tokens, hq)
+    ka, ks = _heads(dev, k, "k", tokens, hkv)
+    va, vs = _heads(dev, v, "v", tokens, hkv)
+    out = _on_device(dev, q_out, "q_out", _BF16_LIKE)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out and q differ in shape")
+    qw = kw = 0
+    if q_weight is not None:
+        qw = _on_device(dev, q_weight, "q_weight", _BF16_LIKE)
+    if k_weight is not None:
+        kw = _on_device(dev, k_weight, "k_weight", _BF16_LIKE)
+    if (qw and q_weight.numel() != HEAD_DIM) or (kw and k_weight.numel() != HEAD_DIM):
+        raise ValueError("q_weight and k_weight must have 128 values")
+    table = pos = rows = rot = 0
+    if rope_table is not None:
+        table = _on_device(dev, rope_table, "rope_table", (torch.float32,))
+        if rope_table.dim() != 2 or positions is None:
+            raise ValueError("rope_table must be [max_positions][rot_dim], with positions beside it")
+        rows, rot = rope_table.shape
+        pos = _on_device(dev, positions, "positions", _I32_ONLY)
+        if positions.numel() != tokens:
+            raise ValueError("positions must have one entry per token")
+    _check(_lib.pkv_qk_norm_rope_append(out, kc, vc, desc, kv_format, slots, qa, qs, ka, ks, va, vs, hq, qw, kw, eps,
+                                        table, rows, rot, 1 if interleaved else 0, pos, tokens, _stream_ptr(stream)),
+           "pkv_qk_norm_rope_append")
+
+
+def choose_kv_blocks_per_split_tree(num_seqs: int, num_kv_heads: int, tree_len: int, max_blocks_per_seq: int,
+                                    sm_count: int = 0) -> int:
+    return int(_lib.pkv_choose_kv_blocks_per_split_tree(num_seqs, num_kv_heads, tree_len, max_blocks_per_seq,
+                                                        sm_count))
+
+
+def workspace_size_tree(num_seqs: int, tree_len: int, num_q_heads: int, max_blocks_per_seq: int,
+                        kv_blocks_per_split: int = 0) -> int:
+    """Bytes paged_attention_tree needs for the same kv_blocks_per_split (0 = the library's choice)."""
+    return int(_lib.pkv_workspace_size_tree(num_seqs, tree_len, num_q_heads, max_blocks_per_seq, kv_blocks_per_split))
+
+
+def choose_kv_blocks_per_split_window(num_seqs: int, num_kv_heads: int, q_len: int, max_blocks_per_seq: int,
+                                      window: int, num_sinks: int, sm_count: int = 0) -> int:
+    return int(_lib.pkv_choose_kv_blocks_per_split_window(num_seqs, num_kv_heads, q_len, max_blocks_per_seq, window,
+                                                          num_sinks, sm_count))
+
+
+def workspace_size_window(num_seqs: int, q_len: int, num_q_heads: int, max_blocks_per_seq: int, window: int,
+                          num_sinks: int, kv_blocks_per_split: int = 0) -> int:
+    """Bytes paged_attention_window needs for the same kv_blocks_per_split (0 = the library's choice)."""
+    return int(_lib.pkv_workspace_size_window(num_seqs, q_len, num_q_heads, max_blocks_per_seq, window, num_sinks,
+                                              kv_blocks_per_split))
+
+
+def _masked_args(out, q, k_cache, v_cache, block_tables, context_lens, workspace):
+    dev = torch.cuda.current_device()
+    kc, desc = _pool(dev, k_cache, "k_cache", KV_BF16)
+    vc = _on_device(dev, v_cache, "v_cache", _BF16_LIKE)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    bt = _on_device(dev, block_tables, "block_tables", _I32_ONLY)
+    cl = _on_device(dev, context_lens, "context_lens", _I32_ONLY)
+    o, qa = _on_device(dev, out, "out", _BF16_LIKE), _on_device(dev, q, "q", _BF16_LIKE)
+    b, shape = context_lens.numel(), q.shape
+    if len(shape) != 4 or shape[0] != b or shape[3] != HEAD_DIM or out.shape != shape:
+        raise ValueError("q/out must be [num_seqs][query tokens][num_q_heads][128]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
+    ws, ws_bytes = _workspace(dev, workspace)
+    return dev, o, qa, kc, vc, desc, bt, block_tables.shape[1], cl, b, shape[1], shape[2], ws, ws_bytes
+
+
+def paged_attention_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, tree_mask: torch.Tensor,
+                         scale: float, tree_lens: torch.Tensor | None = None, kv_blocks_per_split: int = 0,
+                         workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of each request's drafted tokens (its context's last tree_lens[r] tokens; None: all tree_len)
+    over the committed context and the drafts that tree_mask shows.
+
+    q, out [B][tree_len][Hq][128]; tree_mask int64 or uint64 [B][tree_len][ceil(tree_len/64)], bit j = draft j is
+    visible; workspace >= workspace_size_tree(...) bytes.  Rows past tree_lens[r] get zeros."""
+    dev, o, qa, kc, vc, desc, bt, maxb, cl, b, n, hq, ws, wsb = _masked_args(out, q, k_cache, v_cache, block_tables,
+                                                                              context_lens, workspace)
+    mask = _on_device(dev, tree_mask, "tree_mask", _MASK_WORDS)
+    if tuple(tree_mask.shape) != (b, n, (n + 63) // 64):
+        raise ValueError("tree_mask must be [num_seqs][tree_len][ceil(tree_len / 64)]")
+    tl = 0
+    if tree_lens is not None:
+        tl = _on_device(dev, tree_lens, "tree_lens", _I32_ONLY)
+        if tree_lens.numel() != b:
+            raise ValueError("tree_lens must have one entry per request")
+    _check(_lib.pkv_paged_attention_tree(o, qa, kc, vc, desc, bt, maxb, cl, tl, mask, b, n, hq, scale,
+                                         kv_blocks_per_split, ws, wsb, _stream_ptr(stream)),
+           "pkv_paged_attention_tree")
+
+
+def paged_attention_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor, q_len: int, window: int,
+                           num_sinks: int, scale: float, kv_blocks_per_split: int = 0,
+                           workspace: torch.Tensor | None = None, stream=None) -> None:
+    """paged_attention with a sliding window: the query at position p sees the keys t <= p with t > p - window or
+    t < num_sinks.  Blocks no query sees are not looked up.  workspace >= workspace_size_window(...) bytes."""
+    _, o, qa, kc, vc, desc, bt, maxb, cl, b, n, hq, ws, wsb = _masked_args(out, q, k_cache, v_cache, block_tables,
+                                                                            context_lens, workspace)
+    if n != q_len:
+        raise ValueError("q/out must be [num_seqs][q_len][num_q_heads][128]")
+    _check(_lib.pkv_paged_attention_window(o, qa, kc, vc, desc, bt, maxb, cl, b, n, hq, window, num_sinks, scale,
+                                           kv_blocks_per_split, ws, wsb, _stream_ptr(stream)),
+           "pkv_paged_attention_window")
+
+
+class KvPools:
+    """The K and V pools of a model's layers (tensors of `kv_format`, one shape), checked once, for the calls
+    that work on all layers."""
+
+    def __init__(self, k_caches, v_caches, kv_format: int = KV_BF16):
+        n = len(k_caches)
+        if n == 0 or len(v_caches) != n:
+            raise ValueError("one K and one V pool per layer are required")
+        self.tensors = list(k_caches) + list(v_caches)
+        self.device = self.tensors[0].get_device()
+        self.kv_format, self.num_layers = kv_format, n
+        addrs = []
+        for i, t in enumerate(self.tensors):
+            addr, self.desc = _pool(self.device, t, f"pool {i}", kv_format)
+            if t.shape != self.tensors[0].shape:
+                raise ValueError("the layers' pools differ in shape")
+            addrs.append(addr)
+        if self.device < 0 or len(set(addrs)) != len(addrs):
+            raise ValueError("the pools must be distinct CUDA tensors")
+        self.k_array, self.v_array = (ctypes.c_void_p * n)(*addrs[:n]), (ctypes.c_void_p * n)(*addrs[n:])
+
+
+def kv_compact(pools: KvPools, block_tables: torch.Tensor, context_lens: torch.Tensor, accepted: torch.Tensor,
+               num_accepted: torch.Tensor, tree_len: int, tree_lens: torch.Tensor | None = None, stream=None) -> None:
+    """Keep the accepted drafts: in every layer, draft accepted[r][j] (rising) moves to the j-th place behind
+    request r's committed context.  context_lens includes the drafts, as in paged_attention_tree."""
+    dev = torch.cuda.current_device()
+    if pools.device != dev:
+        raise ValueError("the pools must be on the current CUDA device")
+    bt = _on_device(dev, block_tables, "block_tables", _I32_ONLY)
+    cl = _on_device(dev, context_lens, "context_lens", _I32_ONLY)
+    acc = _on_device(dev, accepted, "accepted", _I32_ONLY)
+    na = _on_device(dev, num_accepted, "num_accepted", _I32_ONLY)
+    b = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
+    if accepted.dim() != 2 or accepted.shape[0] != b or num_accepted.numel() != b:
+        raise ValueError("accepted must be [num_seqs][max_accepted] and num_accepted [num_seqs]")
+    tl = 0
+    if tree_lens is not None:
+        tl = _on_device(dev, tree_lens, "tree_lens", _I32_ONLY)
+        if tree_lens.numel() != b:
+            raise ValueError("tree_lens must have one entry per request")
+    _check(_lib.pkv_kv_compact(pools.k_array, pools.v_array, pools.num_layers, pools.desc, pools.kv_format, bt,
+                               block_tables.shape[1], cl, tl, b, tree_len, acc, na, accepted.shape[1],
+                               _stream_ptr(stream)), "pkv_kv_compact")
 
 
 def _addr(x) -> int:

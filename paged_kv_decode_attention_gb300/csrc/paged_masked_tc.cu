@@ -1,0 +1,629 @@
+// paged_masked_tc.cu -- attention of several query positions per request
+// under a mask other than the plain causal one, on the 5th-generation tensor
+// cores, over a paged BF16 KV cache:
+//
+//   tree   : the last n tokens of the context are drafted tokens; draft i sees
+//            every committed token and the drafts whose bits are set in its
+//            mask row (its ancestors and itself).  "Chapter 8: Inference
+//            Optimization" (clxhxhhr.top/posts/4341), §8.5.2: verifying several
+//            drafted positions reads the same KV as one decode step.
+//   window : the query at position p sees the keys p - W + 1 .. p and the first
+//            `num_sinks` tokens; blocks that no query of the call sees are
+//            neither read nor looked up.
+//
+// Mathematics: softmax over the visible keys, evaluated tile by tile with a
+// running maximum and sum (FP32), S = Q K^T and O = P V with FP32 accumulators
+// in tensor memory.  A mask is a 64-bit word per (row, 64 keys), computed once
+// per tile and only for the tiles that some row of the CTA sees partly.
+//
+// Rows of a CTA = query positions x the 4 query heads of one KV head, so each
+// K/V byte is read once for all of them.  What bounds it: HBM up to about 64
+// positions (256 rows: 256 FLOP per byte of K/V, the tensor cores' ridge),
+// the tensor cores beyond (positions x window).  Two shapes:
+//   kQTiles 1: 128 rows (32 positions), 64-token K/V tiles, 2 CTAs per SM.
+//              The wait of one CTA (first tiles, softmax latency, epilogue) is
+//              filled by the other.  P.V carries the weights as a BF16 part
+//              plus the BF16 rounding of the remainder (about 2^-17
+//              relative): the tensor cores have the time, HBM is the bound.
+//   kQTiles 2: 256 rows (64 positions), 128-token tiles, 1 CTA per SM; while
+//              one row tile's softmax runs the tensor cores work on the other's
+//              products.  S has N = 128 because an MMA with N = 64 takes as
+//              long.  The weights enter P.V rounded to BF16 (2^-8 relative at
+//              most, unbiased, so the output moves by less than its own BF16
+//              rounding): the remainder's products would make the tensor cores
+//              the bound (3 instead of 2 products per tile).
+//
+// CTA = 3 + 4 kQTiles warps:
+//   warp 0, last: TMA producers of K and of V (16 x 64 boxes, 128-byte
+//             swizzle, one per block and 64-dim half; blocks past the range
+//             arrive as zeros).
+//   warp 1  : MMA issuer (one thread), polling per row tile for a scored K tile
+//             to issue and for weights to multiply.
+//   warps 2..: softmax, one thread per row (TMEM lane).  Warps whose rows are
+//             all padding only keep the barriers in step.
+#include <climits>
+#include <cmath>
+
+#include "pkv_common.cuh"
+#include "pkv_kernels.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr float kRescaleThreshold = 8.f;  // log2 units: weights stay below 2^8
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRowsPerTile = 128;                          // TMEM lanes
+constexpr int kPosPerTile = kRowsPerTile / kGroup;         // query positions of a row tile: 32
+constexpr int kQTileBytes = kRowsPerTile * kHeadDim * 2;   // 32 KiB, two 64-dim halves
+constexpr int kQHalfBytes = kQTileBytes / 2;
+
+template <int kQTiles>
+struct Shape {
+  static constexpr int kTileBlocks = kQTiles == 1 ? 4 : 8;
+  static constexpr int kTileTokens = kTileBlocks * kBlockSize;
+  static constexpr int kNB = kQTiles == 1 ? 2 : 1;  // S/P buffers per row tile
+  static constexpr int kKStages = 3;
+  static constexpr int kVStages = 2;
+  static constexpr int kHalfBytes = kTileTokens * 128;
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kWarps = 3 + 4 * kQTiles;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kVProdWarp = kWarps - 1;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kQTiles * kQTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kStageBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kStageBytes;
+  static constexpr int kSmem = kOffBar + 256;
+  static constexpr uint32_t kColO = kNB * kTileTokens;        // S/P buffers, then O (128 columns)
+  static constexpr uint32_t kTileCols = kColO + kHeadDim;     // 256 columns per row tile
+  static constexpr uint32_t kTmemCols = kQTiles * kTileCols;  // 256 or 512
+  static constexpr bool kRemainder = kQTiles == 1;
+  static constexpr int kCtasPerSm = kQTiles == 1 ? 2 : 1;
+  static_assert(kSmem <= (kQTiles == 1 ? 113 : 227) * 1024, "shared memory per CTA");
+};
+
+template <int kQTiles>
+struct Bars {
+  using S = Shape<kQTiles>;
+  uint64_t k_full[S::kKStages];
+  uint64_t k_empty[S::kKStages];
+  uint64_t v_full[S::kVStages];
+  uint64_t v_empty[S::kVStages];
+  uint64_t s_full[kQTiles][S::kNB];
+  uint64_t p_full[kQTiles][S::kNB];
+  uint64_t o_done[kQTiles][S::kNB];
+  uint64_t q_full;
+  uint32_t tmem_base;
+};
+
+// The x lowest bits (x may lie outside 0..64).
+__device__ __forceinline__ uint64_t low_bits(int x) {
+  return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1ull);
+}
+
+template <int kQTiles, MaskKind kMask, bool kSplit>
+__device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                                     const MaskedArgs& a) {
+  using S = Shape<kQTiles>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(sizeof(Bars<kQTiles>) <= 256, "barrier area");
+  Bars<kQTiles>* bars = reinterpret_cast<Bars<kQTiles>*>(smem + S::kOffBar);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // ---------------- set-up: barriers, TMEM (reads no input) ----------------
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kKStages; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], kQTiles);
+    }
+    for (int s = 0; s < S::kVStages; ++s) {
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], kQTiles);
+    }
+    for (int t = 0; t < kQTiles; ++t)
+      for (int s = 0; s < S::kNB; ++s) {
+        mbar_init(&bars->s_full[t][s], 1);
+        mbar_init(&bars->p_full[t][s], 128);
+        mbar_init(&bars->o_done[t][s], 1);
+      }
+    mbar_init(&bars->q_full, 128 * kQTiles);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem_base, S::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_tensor_map(&k_map);
+    tc::prefetch_tensor_map(&v_map);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  pdl_wait();  // everything below may read what earlier grids in the stream write
+  pdl_trigger();
+
+  // ---------------- what this CTA reduces (uniform over the CTA) ----------------
+  constexpr int kPos = kPosPerTile * kQTiles;  // query positions per CTA
+  const int n_rt = (a.d.q_len + kPos - 1) / kPos;
+  const int r = blockIdx.x / n_rt;
+  const int pos0 = (blockIdx.x - r * n_rt) * kPos;  // first query index of this CTA
+  const int split = blockIdx.y;
+  const int kvh = blockIdx.z;
+  const int hq = a.d.num_kv_heads * kGroup;
+  const int cap = a.d.max_blocks * kBlockSize;
+  int ctx = a.d.context_lens[r];
+  int n_new = a.d.q_len;  // queries of this request
+  if constexpr (kMask == MaskKind::kTree) {
+    if (a.tree_lens != nullptr) n_new = min(max(a.tree_lens[r], 0), a.d.q_len);
+  }
+  if (ctx > cap && threadIdx.x == 0 && split == 0 && kvh == 0 && pos0 == 0) report(a.d.err, PKV_DEVERR_CONTEXT);
+  ctx = min(max(ctx, 0), cap);
+  const int base = ctx - n_new;            // position of query 0
+  const int n_pos = min(kPos, n_new - pos0);  // queries of this CTA (<= 0: none)
+  // keys [0, sink_blocks*16) and [first_block*16, key_end) are read; the rest is not looked up
+  int sink_blocks = 0, first_block = 0, key_end = 0, first_key = 0;
+  if (n_pos > 0 && ctx > 0) {
+    if constexpr (kMask == MaskKind::kTree) {
+      key_end = ctx;
+    } else {
+      const int p_first = base + pos0;
+      key_end = max(p_first + n_pos, 0);  // the last query sees its own position
+      first_key = max(0, max(p_first, 0) - a.window + 1);
+      first_block = first_key / kBlockSize;
+      sink_blocks = (min(a.num_sinks, first_key) + kBlockSize - 1) / kBlockSize;
+      if (sink_blocks >= first_block) {  // one contiguous range
+        sink_blocks = 0;
+        first_block = 0;
+      }
+    }
+  }
+  const int end_block = (key_end + kBlockSize - 1) / kBlockSize;
+  const int sink_tiles = (sink_blocks + S::kTileBlocks - 1) / S::kTileBlocks;
+  const int all_tiles = sink_tiles + (max(0, end_block - first_block) + S::kTileBlocks - 1) / S::kTileBlocks;
+  const int t_first = split * a.tiles_per_split;  // first tile of this split
+  const int n_tiles = min(all_tiles - t_first, a.tiles_per_split);
+  // first token of tile j of the split
+  auto tile_token = [&](int j) -> int {
+    const int i = t_first + j;
+    return (i < sink_tiles ? i * S::kTileBlocks : first_block + (i - sink_tiles) * S::kTileBlocks) * kBlockSize;
+  };
+  const int q_tiles = n_pos > kPosPerTile ? 2 : 1;  // row tiles with queries (kQTiles 1: always 1)
+
+  // rows of the softmax threads
+  const bool softmax_warp = warp >= 2 && warp < 2 + 4 * kQTiles;
+  const int qt = softmax_warp ? (warp - 2) >> 2 : 0;
+  const int quad = warp & 3;  // TMEM sub-partition of this warp
+  const int row = quad * 32 + lane;
+  const int qi = pos0 + qt * kPosPerTile + (row >> 2);  // query index
+  const bool in_shape = softmax_warp && qi < a.d.q_len;
+  const bool row_valid = in_shape && qi < n_new;
+  const int64_t orow = (static_cast<int64_t>(r) * a.d.q_len + qi) * hq + kvh * kGroup + (row & 3);
+  const int64_t slot = orow * a.d.part_slots + split;
+
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t sbase = smem_addr(smem);
+  bool ok = true;
+
+  // zeros for a row without a result (padding, or nothing visible)
+  auto write_empty = [&]() {
+    if constexpr (kSplit) {
+      a.d.part_lse[slot] = -INFINITY;
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + orow * kHeadDim);
+#pragma unroll
+      for (int c = 0; c < kHeadDim * 2 / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
+    }
+  };
+
+  if (n_tiles <= 0) {
+    if (in_shape) write_empty();
+  } else if (warp == 0 || warp == S::kVProdWarp) {
+    // ---------------------------- TMA producers ----------------------------
+    const bool is_v = warp == S::kVProdWarp;
+    const int stages = is_v ? S::kVStages : S::kKStages;
+    uint64_t* full = is_v ? bars->v_full : bars->k_full;
+    uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+    uint8_t* ring = smem + (is_v ? S::kOffV : S::kOffK);
+    const CUtensorMap* map = is_v ? &v_map : &k_map;
+    // read once, unless several row tiles of the request read the same blocks
+    const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+    const int32_t* table = a.d.block_tables + static_cast<int64_t>(r) * a.d.max_blocks;
+    const int oob_row = a.d.num_blocks * a.d.num_kv_heads * kBlockSize;  // first row past the pool
+    // entry i of the list of blocks (whole tiles of sinks, then the window):
+    // its block id, or INT_MIN for a hole or past the range
+    auto entry = [&](int i) -> int {
+      if (i >= n_tiles * S::kTileBlocks) return INT_MIN;
+      i += t_first * S::kTileBlocks;
+      const int sink_entries = sink_tiles * S::kTileBlocks;
+      const int lb = i < sink_entries ? (i < sink_blocks ? i : INT_MAX) : first_block + i - sink_entries;
+      return lb < end_block ? table[lb] : INT_MIN;
+    };
+    auto row_of = [&](int blk) -> int {
+      if (blk == INT_MIN) return oob_row;
+      if (blk < 0 || blk >= a.d.num_blocks) {
+        report(a.d.err, PKV_DEVERR_BLOCK_ID);
+        blk = 0;
+      }
+      return (blk * a.d.num_kv_heads + kvh) * kBlockSize;
+    };
+    constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
+    int cur = row_of(entry(lane)), nxt = INT_MIN;
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      const int in_chunk = j % kTilesPerChunk;
+      if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
+      const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
+      if (in_chunk == kTilesPerChunk - 1) cur = row_of(nxt);
+      const int st = j % stages;
+      if (j >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((j / stages) & 1) ^ 1));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStageBytes);
+      __syncwarp();
+      if (lane < 2 * S::kTileBlocks) {
+        const int b = lane >> 1, c = lane & 1;
+        tc::tma_load_2d(ring + st * S::kStageBytes + c * S::kHalfBytes + b * 2048, map, c * 64, yy, &full[st], policy);
+      }
+    }
+    if (lane == 0) {
+      if (!ok) report(a.d.err, PKV_DEVERR_TIMEOUT);
+      // the last tiles' copies must land before shared memory is released
+      for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------------------- MMA issuer ----------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
+      constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
+      int js[kQTiles], jp[kQTiles];
+#pragma unroll
+      for (int t = 0; t < kQTiles; ++t) js[t] = jp[t] = t < q_tiles ? 0 : n_tiles;
+      uint64_t t_idle = 0;
+      ok = mbar_wait(&bars->q_full, 0);
+      bool done = false;
+      while (ok && !done) {
+        bool progressed = false;
+        done = true;
+#pragma unroll
+        for (int t = 0; t < kQTiles; ++t) {
+          const uint32_t tcol = tmem + t * S::kTileCols;
+          if (js[t] < n_tiles) {
+            const int j = js[t], st = j % S::kKStages, sb = j % S::kNB;
+            bool ready = mbar_test_wait(&bars->k_full[st], (j / S::kKStages) & 1);
+            if (ready && j >= S::kNB) ready = mbar_test_wait(&bars->o_done[t][sb], ((j / S::kNB) - 1) & 1);
+            if (ready) {
+              tc::fence_after_sync();
+              const uint32_t kst = sbase + S::kOffK + st * S::kStageBytes;
+              const uint32_t qst = sbase + S::kOffQ + t * kQTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc::mma_bf16(tcol + sb * S::kTileTokens,
+                             tc::smem_desc(qst + (kk >> 2) * kQHalfBytes + 32 * (kk & 3), 16, 1024),
+                             tc::smem_desc(kst + (kk >> 2) * S::kHalfBytes + 32 * (kk & 3), 16, 1024), kIdS, kk > 0);
+              tc::commit(&bars->s_full[t][sb]);
+              tc::commit(&bars->k_empty[st]);
+              if (q_tiles < kQTiles) tc::commit(&bars->k_empty[st]);  // the empty row tile's share
+              ++js[t];
+              progressed = true;
+            }
+          }
+          if (jp[t] < js[t]) {
+            const int j = jp[t], st = j % S::kVStages, sb = j % S::kNB;
+            if (mbar_test_wait(&bars->p_full[t][sb], (j / S::kNB) & 1) &&
+                mbar_test_wait(&bars->v_full[st], (j / S::kVStages) & 1)) {
+              tc::fence_after_sync();
+              const uint32_t ptm = tcol + sb * S::kTileTokens;
+              const uint32_t vst = sbase + S::kOffV + st * S::kStageBytes;
+#pragma unroll
+              for (int part = 0; part < (S::kRemainder ? 2 : 1); ++part)
+#pragma unroll
+                for (int kk = 0; kk < S::kTileBlocks; ++kk)
+                  tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + (S::kTileTokens / 2) * part + 8 * kk,
+                                      tc::smem_desc(vst + 2048 * kk, S::kHalfBytes, 1024), kIdO,
+                                      (j > 0 || part > 0 || kk > 0) ? 1u : 0u);
+              tc::commit(&bars->o_done[t][sb]);
+              tc::commit(&bars->v_empty[st]);
+              if (q_tiles < kQTiles) tc::commit(&bars->v_empty[st]);
+              ++jp[t];
+              progressed = true;
+            }
+          }
+          if (jp[t] < n_tiles) done = false;
+        }
+        if (progressed) {
+          t_idle = 0;
+        } else if (t_idle == 0) {
+          t_idle = global_timer_ns();
+        } else if (global_timer_ns() - t_idle > kWaitLimitNs) {
+          ok = false;
+        }
+      }
+      if (!ok) report(a.d.err, PKV_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------- softmax ----------------------------
+    {
+      // this row tile's queries -> 128-byte swizzled K-major tile, two 64-dim
+      // halves; thread t loads 16-byte chunk t % 16 of rows t / 16 + 8k
+      const int t = (threadIdx.x - 64) & 127;
+      const int ch = t & 15;
+      const uint16_t* qbase = static_cast<const uint16_t*>(a.d.q);
+      uint8_t* qs = smem + S::kOffQ + qt * kQTileBytes;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int m = (t >> 4) + 8 * (k + 8 * half);
+          const int qim = pos0 + qt * kPosPerTile + (m >> 2);
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (qim < n_new)
+            v[k] = *reinterpret_cast<const uint4*>(
+                qbase + ((static_cast<int64_t>(r) * a.d.q_len + qim) * hq + kvh * kGroup + (m & 3)) * kHeadDim + ch * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int m = (t >> 4) + 8 * (k + 8 * half);
+          *reinterpret_cast<uint4*>(qs + (ch >> 3) * kQHalfBytes + tc::sw128_offset(m, (ch & 7) * 8)) = v[k];
+        }
+      }
+      tc::fence_proxy_async_smem();
+      mbar_arrive(&bars->q_full);
+    }
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tcol = tmem + lane_off + qt * S::kTileCols;
+    const float c = a.d.scale_log2;  // > 0: the max of raw scores scales to the max of scaled ones
+    const bool tile_live = qt < q_tiles;
+    const bool warp_live = pos0 + qt * kPosPerTile + quad * 8 < n_new;  // some row of the warp has a query
+    // the keys a row sees in [tok, tok + 64), one bit per key
+    const uint64_t* mrow = nullptr;
+    if constexpr (kMask == MaskKind::kTree)
+      mrow = a.tree_mask + (static_cast<int64_t>(r) * a.d.q_len + (row_valid ? qi : 0)) * a.mask_words;
+    // (in_sinks: the range belongs to a tile of sink blocks, whose places past
+    // them are holes: the window's keys are read by the tiles after it)
+    auto visible = [&](int tok, bool in_sinks) -> uint64_t {
+      if constexpr (kMask == MaskKind::kTree) {
+        const int d = base - tok;  // committed tokens of the range
+        uint64_t m = low_bits(d);
+        if (d < 64) {
+          const int o = -d;  // draft at bit 0 (negative: drafts start at bit d)
+          if (o < 0) {
+            m |= mrow[0] << d;
+          } else {
+            const int w = o >> 6, sh = o & 63;
+            if (w < a.mask_words) m |= mrow[w] >> sh;
+            if (sh != 0 && w + 1 < a.mask_words) m |= mrow[w + 1] << (64 - sh);
+          }
+        }
+        return m & low_bits(key_end - tok);
+      } else {
+        const int p = base + qi;
+        const int hi = p + 1 - tok;
+        const uint64_t sinks = low_bits(min(a.num_sinks - tok, hi));
+        return in_sinks ? sinks : sinks | (low_bits(hi) & ~low_bits(p - a.window + 1 - tok));
+      }
+    };
+    // does some row of this CTA see the tile only in part?
+    auto partial = [&](int tok) -> bool {
+      if constexpr (kMask == MaskKind::kTree) return tok + S::kTileTokens > base;
+      const int p_first = base + pos0, p_last = base + pos0 + n_pos - 1;
+      return tok + S::kTileTokens - 1 > p_first ||
+             !(tok > p_last - a.window || tok + S::kTileTokens <= a.num_sinks);
+    };
+    float m_stale = -INFINITY;  // scaled max the weights are taken against (lags the true max by < 2^8)
+    float l = 0.f;              // the row's weight sum
+    for (int j = 0; j < n_tiles && ok && tile_live; ++j) {
+      const int sb = j % S::kNB;
+      const int st = j % S::kVStages;
+      const int tok = tile_token(j);
+      // keep `ok` warp-uniform: the tcgen05 loads below are warp-collective
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[qt][sb], (j / S::kNB) & 1));
+      if (!ok) break;
+      const bool part = partial(tok);
+      if (warp_live) {
+        tc::fence_after_sync();
+        float s[S::kTileTokens];
+#pragma unroll
+        for (int cc = 0; cc < S::kTileTokens / 32; ++cc) tc::tmem_ld32(tcol + sb * S::kTileTokens + 32 * cc, s + 32 * cc);
+        tc::tmem_wait_ld();
+        if (part) {
+#pragma unroll
+          for (int w = 0; w < S::kTileTokens / 64; ++w) {
+            const uint64_t m = row_valid ? visible(tok + 64 * w, tok < first_block * kBlockSize) : 0ull;
+            const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(lo & (1u << e))) s[64 * w + e] = -INFINITY;
+              if (!(hi & (1u << e))) s[64 * w + 32 + e] = -INFINITY;
+            }
+          }
+        }
+        float mx;
+        {
+          float t8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t8[e] = s[e];
+#pragma unroll
+          for (int k = 8; k < S::kTileTokens; k += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              t8[e] = k + 8 < S::kTileTokens ? fmaxf(fmaxf(t8[e], s[k + e]), s[k + 8 + e]) : fmaxf(t8[e], s[k + e]);
+          mx = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7]))) * c;
+        }
+        const bool grow = mx > m_stale + kRescaleThreshold;  // also true the first time a row sees a key
+        const float m_new = grow ? mx : m_stale;
+        const float alpha = grow ? exp2_approx(m_stale - m_new) : 1.f;  // 0 while m_stale is -inf
+        if (__any_sync(0xffffffffu, grow && j > 0 && m_stale != -INFINITY)) {
+          // O holds weights taken against the old maxima: rescale this warp's rows
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(j - 1) % S::kNB], ((j - 1) / S::kNB) & 1));
+          tc::fence_after_sync();
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            float o[32];
+            tc::tmem_ld32(tcol + S::kColO + 32 * cc, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tc::tmem_st32(tcol + S::kColO + 32 * cc, o);
+          }
+          tc::tmem_wait_st();
+        }
+        l *= alpha;
+        m_stale = m_new;
+        const float nm = (m_stale == -INFINITY) ? 0.f : -m_stale;
+        const float2 c2 = make_float2(c, c);
+        const float2 nm2 = make_float2(nm, nm);
+        float2 acc2 = make_float2(0.f, 0.f);
+        // P_j overwrites the S_j buffer it came from, 2 BF16 per 32-bit column
+#pragma unroll
+        for (int cc = 0; cc < S::kTileTokens / 32; ++cc) {
+          uint32_t pk[16], pr[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(s[32 * cc + 2 * e], s[32 * cc + 2 * e + 1]), c2, nm2);
+            const float p0 = exp2_approx(x.x);
+            const float p1 = exp2_approx(x.y);
+            acc2 = __fadd2_rn(acc2, make_float2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+            if constexpr (S::kRemainder)
+              pr[e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
+          }
+          tc::tmem_st16u(tcol + sb * S::kTileTokens + 16 * cc, pk);
+          if constexpr (S::kRemainder) tc::tmem_st16u(tcol + sb * S::kTileTokens + S::kTileTokens / 2 + 16 * cc, pr);
+        }
+        l += acc2.x + acc2.y;
+      }
+      // V rows that no query of this CTA sees have weight 0 but may hold
+      // anything (slots past the context): zero them
+      if (part) {
+        const bool tail = tok + S::kTileTokens > key_end && key_end > tok && (key_end & (kBlockSize - 1)) != 0;
+        bool head = false;
+        if constexpr (kMask == MaskKind::kWindow)
+          head = tok < first_key && tok + S::kTileTokens > a.num_sinks;
+        if (tail || head) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (j / S::kVStages) & 1));
+          uint8_t* vt = smem + S::kOffV + st * S::kStageBytes;
+          const int t128 = (threadIdx.x - 64) & 127;
+          for (int idx = t128; idx < S::kTileTokens * 16; idx += 128) {
+            const int tk = idx >> 4, ch = idx & 15, t = tok + tk;
+            bool dead = t >= key_end;
+            if constexpr (kMask == MaskKind::kWindow) dead = dead || (t >= a.num_sinks && t < first_key);
+            if (dead)
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * S::kHalfBytes + tk * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      tc::tmem_wait_st();
+      tc::fence_proxy_async_smem();  // zeroed V rows, if any, before the PV MMA reads them
+      tc::fence_before_sync();
+      mbar_arrive(&bars->p_full[qt][sb]);
+    }
+    if (!ok && lane == 0) report(a.d.err, PKV_DEVERR_TIMEOUT);
+    // ---- epilogue: one row per thread ----
+    if (ok && tile_live)
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(n_tiles - 1) % S::kNB], ((n_tiles - 1) / S::kNB) & 1));
+    if (tile_live && warp_live && ok) {
+      tc::fence_after_sync();
+      const bool live = row_valid && l > 0.f;
+      const float inv = live ? 1.f / l : 0.f;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        float o[32];
+        tc::tmem_ld32(tcol + S::kColO + 32 * cc, o);
+        tc::tmem_wait_ld();
+        if (!live) continue;
+        if constexpr (kSplit) {
+          float4* dst = reinterpret_cast<float4*>(a.d.part_o + slot * kHeadDim + 32 * cc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + orow * kHeadDim + 32 * cc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 w;
+            w.x = pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv);
+            w.y = pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+            w.z = pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+            w.w = pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+            dst[e] = w;
+          }
+        }
+      }
+      if constexpr (kSplit) {
+        if (live) a.d.part_lse[slot] = (m_stale + log2f(l)) * kLn2;
+      }
+      if (in_shape && !live) write_empty();
+    } else if (in_shape && ok) {
+      write_empty();
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
+template <int kQTiles, MaskKind kMask, bool kSplit>
+__global__ void __launch_bounds__(Shape<kQTiles>::kThreads, Shape<kQTiles>::kCtasPerSm)
+    paged_masked_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                           const MaskedArgs a) {
+  paged_masked_tc_body<kQTiles, kMask, kSplit>(k_map, v_map, a);
+}
+
+template <int kQTiles, MaskKind kMask, bool kSplit>
+cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a,
+                           cudaStream_t stream) {
+  using S = Shape<kQTiles>;
+  static std::atomic<bool> done[64];  // per device; host threads may race on a first call
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kernel = paged_masked_tc_kernel<kQTiles, kMask, kSplit>;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  constexpr int kPos = kPosPerTile * kQTiles;
+  const int64_t x = static_cast<int64_t>(a.d.num_seqs) * ((a.d.q_len + kPos - 1) / kPos);
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.d.num_splits),
+                  static_cast<unsigned>(a.d.num_kv_heads));
+  return launch_pdl(kernel, grid, dim3(S::kThreads), S::kSmem, stream, 1, kmap, vmap, a);
+}
+
+template <int kQTiles>
+cudaError_t launch_shape(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a, MaskKind mask,
+                         cudaStream_t stream) {
+  const bool split = a.d.part_o != nullptr;
+  if (mask == MaskKind::kTree)
+    return split ? launch_variant<kQTiles, MaskKind::kTree, true>(kmap, vmap, a, stream)
+                 : launch_variant<kQTiles, MaskKind::kTree, false>(kmap, vmap, a, stream);
+  return split ? launch_variant<kQTiles, MaskKind::kWindow, true>(kmap, vmap, a, stream)
+               : launch_variant<kQTiles, MaskKind::kWindow, false>(kmap, vmap, a, stream);
+}
+
+}  // namespace
+
+int masked_tile_blocks(int q_len) {
+  return q_len <= kPosPerTile ? Shape<1>::kTileBlocks : Shape<2>::kTileBlocks;
+}
+int masked_positions_per_cta(int q_len) { return q_len <= kPosPerTile ? kPosPerTile : 2 * kPosPerTile; }
+int masked_ctas_per_sm(int q_len) { return q_len <= kPosPerTile ? Shape<1>::kCtasPerSm : Shape<2>::kCtasPerSm; }
+
+cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.d.num_blocks) * a.d.num_kv_heads * kBlockSize;
+  if (rows + kBlockSize >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+  CUtensorMap kmap, vmap;
+  if (!make_pool_map(&kmap, a.d.k_cache, rows) || !make_pool_map(&vmap, a.d.v_cache, rows)) return cudaErrorInvalidValue;
+  return a.d.q_len <= kPosPerTile ? launch_shape<1>(kmap, vmap, a, mask, stream)
+                                  : launch_shape<2>(kmap, vmap, a, mask, stream);
+}
+
+}  // namespace pkv

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "pkv.h"
 #include "pkv_common.cuh"
@@ -832,6 +833,309 @@ pkv_status pkv_get_device_error(uint32_t* host_word, int32_t reset) {
   if (reset) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero) != cudaSuccess) return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
+
+pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                                   int32_t kv_format, const int64_t* slot_mapping, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   int32_t num_q_heads, const void* q_weight, const void* k_weight, float eps,
+                                   const float* rope_table, int32_t max_positions, int32_t rot_dim,
+                                   int32_t interleaved, const int32_t* positions, int32_t num_tokens, void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (kv_format != PKV_KV_BF16 && kv_format != PKV_KV_Q8_0 && kv_format != PKV_KV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+  if (num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || rot_dim < 0 || max_positions < 0) return PKV_ERR_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.f) return PKV_ERR_SHAPE;
+  if (rot_dim > kHeadDim || rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (rot_dim > 0 && max_positions == 0) return PKV_ERR_SHAPE;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * kHeadDim;
+  const int64_t kv_row = static_cast<int64_t>(cache->num_kv_heads) * kHeadDim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row) return PKV_ERR_SHAPE;
+  if ((q_stride | k_stride | v_stride) & 7) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  if (!q_out || !k_cache || !v_cache || !slot_mapping || !q || !k || !v) return PKV_ERR_NULL;
+  if (rot_dim > 0 && (!rope_table || !positions)) return PKV_ERR_NULL;
+  uintptr_t all = 0;
+  for (const void* p : {static_cast<const void*>(q_out), static_cast<const void*>(k_cache),
+                        static_cast<const void*>(v_cache), q, k, v, q_weight, k_weight,
+                        static_cast<const void*>(rope_table)})
+    all |= reinterpret_cast<uintptr_t>(p);
+  if (all & 15) return PKV_ERR_UNSUPPORTED;
+  if (q_out == q && q_stride != q_row) return PKV_ERR_SHAPE;
+  if ((static_cast<int64_t>(num_tokens) * cache->num_kv_heads + 7) / 8 > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  QkNormRopeArgs a{};
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.rope_table = rope_table;
+  a.positions = positions;
+  a.err = error_word();
+  a.eps = eps;
+  a.max_positions = max_positions;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved;
+  a.num_tokens = num_tokens;
+  a.num_blocks = cache->num_blocks;
+  a.num_kv_heads = cache->num_kv_heads;
+  return launch_qk_norm_rope_append(a, kv_format, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                                    : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The masked attention calls (tree, window): tiles a CTA reads at most, and
+// how they are split.
+struct MaskedPlan {
+  int32_t tiles;            // at most
+  int32_t tiles_per_split;
+  int32_t splits;
+};
+
+// Longest contexts the masked kernels' 32-bit positions are kept to.
+constexpr int32_t kMaskedMaxBlocks = 1 << 26;
+constexpr int32_t kMaskedMaxQLen = 1 << 26;
+constexpr int32_t kMaskedMaxSpan = 1 << 30;  // windows and sinks beyond it are as good as endless
+
+// Tiles of blocks a CTA reads at most.  window 0: the whole table (tree).
+int32_t masked_max_tiles(int32_t q_len, int32_t max_blocks, int32_t window, int32_t num_sinks) {
+  const int32_t tb = masked_tile_blocks(q_len);
+  const int32_t all = (max_blocks + tb - 1) / tb;
+  if (window == 0) return all;
+  const int64_t pos = q_len < masked_positions_per_cta(q_len) ? q_len : masked_positions_per_cta(q_len);
+  const int64_t span = (static_cast<int64_t>(window) + pos - 1 + kBlockSize - 2) / kBlockSize + 1;  // any alignment
+  const int64_t sinks = (static_cast<int64_t>(num_sinks) + kBlockSize - 1) / kBlockSize;
+  const int64_t tiles = (span + tb - 1) / tb + (sinks + tb - 1) / tb;
+  return static_cast<int32_t>(tiles < all + 1 ? tiles : all + 1);  // + 1: sinks and window each end in a part tile
+}
+
+// Splits only when the row tiles leave at least half of the resident CTAs
+// unused, and of at least 256 tokens.
+constexpr int32_t kMaskedMinSplitTokens = 256;
+
+MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t window,
+                       int32_t num_sinks, int32_t kv_blocks_per_split, int32_t sm_count) {
+  const int32_t tb = masked_tile_blocks(q_len);
+  MaskedPlan p{masked_max_tiles(q_len, max_blocks, window, num_sinks), 0, 1};
+  p.tiles_per_split = p.tiles;
+  if (kv_blocks_per_split >= max_blocks) return p;
+  if (kv_blocks_per_split > 0) {
+    p.tiles_per_split = (kv_blocks_per_split + tb - 1) / tb;
+  } else {
+    const int32_t pos = masked_positions_per_cta(q_len);
+    const int64_t ctas = num_seqs * num_kv_heads * ((q_len + pos - 1) / pos);
+    const int64_t slots = static_cast<int64_t>(masked_ctas_per_sm(q_len)) * (sm_count > 0 ? sm_count : device_sm_count());
+    const int64_t splits = ctas > 0 ? slots / ctas : 1;
+    if (splits > 1) {
+      const int32_t least = kMaskedMinSplitTokens / (tb * kBlockSize);
+      p.tiles_per_split = static_cast<int32_t>((p.tiles + splits - 1) / splits);
+      if (p.tiles_per_split < least) p.tiles_per_split = least;
+    }
+  }
+  if (p.tiles_per_split > p.tiles) p.tiles_per_split = p.tiles;
+  p.splits = (p.tiles + p.tiles_per_split - 1) / p.tiles_per_split;
+  return p;
+}
+
+size_t masked_workspace(int64_t rows, int32_t splits) {
+  if (splits <= 1) return 0;
+  const size_t n = static_cast<size_t>(rows) * splits;
+  return align_up(n * kHeadDim * sizeof(float), 256) + align_up(n * sizeof(float), 256);
+}
+
+bool masked_sizes_ok(int32_t num_seqs, int32_t num_heads, int32_t q_len, int32_t max_blocks, int32_t window,
+                     int32_t num_sinks, bool tree) {
+  return num_seqs > 0 && num_heads > 0 && q_len > 0 && q_len <= (tree ? kMaxTree : kMaskedMaxQLen) && max_blocks > 0 &&
+         max_blocks <= kMaskedMaxBlocks && (tree || (window > 0 && num_sinks >= 0));
+}
+
+int32_t span_limit(int32_t x) { return x < kMaskedMaxSpan ? x : kMaskedMaxSpan; }
+
+// pkv_paged_attention_tree / _window: checks, plan, launches.
+pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_cache, const void* v_cache,
+                       const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* tree_lens, const uint64_t* tree_mask,
+                       int32_t num_seqs, int32_t q_len, int32_t num_q_heads, int32_t window, int32_t num_sinks,
+                       float scale, int32_t kv_blocks_per_split, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  const bool tree = mask == MaskKind::kTree;
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || q_len < 1 || max_blocks_per_seq < 1 || kv_blocks_per_split < 0) return PKV_ERR_SHAPE;
+  if (!tree && (window < 1 || num_sinks < 0)) return PKV_ERR_SHAPE;
+  if (num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PKV_ERR_SHAPE;
+  if (q_len > (tree ? kMaxTree : kMaskedMaxQLen) || max_blocks_per_seq > kMaskedMaxBlocks) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_seqs) * q_len * num_q_heads > 0x7fffffff || cache->num_kv_heads > 65535)
+    return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > ((int64_t{1} << 31) - 1) / kBlockSize - 1)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_NULL;
+  if (tree && !tree_mask) return PKV_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(tree_mask) & 7) return PKV_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache)) & 15)
+    return PKV_ERR_UNSUPPORTED;
+  if (cache->num_blocks == 0) return PKV_ERR_SHAPE;  // no block that a table could name
+
+  MaskedArgs a{};
+  a.window = span_limit(window);
+  a.num_sinks = span_limit(num_sinks);
+  const MaskedPlan plan = masked_plan(num_seqs, cache->num_kv_heads, q_len, max_blocks_per_seq, tree ? 0 : a.window,
+                                      a.num_sinks, kv_blocks_per_split, 0);
+  if (plan.splits > 65535) return PKV_ERR_UNSUPPORTED;
+  a.tree_lens = tree_lens;
+  a.tree_mask = tree_mask;
+  a.mask_words = (q_len + 63) / 64;
+  a.tiles_per_split = plan.tiles_per_split;
+  a.d.out = out;
+  a.d.q = q;
+  a.d.k_cache = k_cache;
+  a.d.v_cache = v_cache;
+  a.d.block_tables = block_tables;
+  a.d.context_lens = context_lens;
+  a.d.err = error_word();
+  a.d.max_blocks = max_blocks_per_seq;
+  a.d.num_blocks = cache->num_blocks;
+  a.d.num_kv_heads = cache->num_kv_heads;
+  a.d.num_seqs = num_seqs;
+  a.d.q_len = q_len;
+  a.d.num_splits = plan.splits;
+  a.d.scale_log2 = scale * 1.4426950408889634f;
+  a.d.part_slots = plan.splits;
+  const int64_t rows = static_cast<int64_t>(num_seqs) * q_len * num_q_heads;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (plan.splits > 1) {
+    if (workspace == nullptr || workspace_bytes < masked_workspace(rows, plan.splits)) return PKV_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
+    a.d.part_o = static_cast<float*>(workspace);
+    a.d.part_lse = reinterpret_cast<float*>(
+        static_cast<uint8_t*>(workspace) +
+        align_up(static_cast<size_t>(rows) * plan.splits * kHeadDim * sizeof(float), 256));
+  }
+  if (launch_paged_masked_tc(a, mask, s) != cudaSuccess) return PKV_ERR_CUDA;
+  if (plan.splits > 1 && launch_attn_combine(out, nullptr, a.d.part_o, a.d.part_lse, static_cast<int32_t>(rows),
+                                             plan.splits, s) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t pkv_choose_kv_blocks_per_split_tree(int32_t num_seqs, int32_t num_kv_heads, int32_t tree_len,
+                                            int32_t max_blocks_per_seq, int32_t sm_count) {
+  if (!masked_sizes_ok(num_seqs, num_kv_heads, tree_len, max_blocks_per_seq, 0, 0, true))
+    return max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
+  const MaskedPlan p = masked_plan(num_seqs, num_kv_heads, tree_len, max_blocks_per_seq, 0, 0, 0, sm_count);
+  return p.splits == 1 ? max_blocks_per_seq : p.tiles_per_split * masked_tile_blocks(tree_len);
+}
+
+size_t pkv_workspace_size_tree(int32_t num_seqs, int32_t tree_len, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                               int32_t kv_blocks_per_split) {
+  if (!masked_sizes_ok(num_seqs, num_q_heads, tree_len, max_blocks_per_seq, 0, 0, true) || kv_blocks_per_split < 0)
+    return 0;
+  const MaskedPlan p = masked_plan(num_seqs, num_q_heads / kGroup, tree_len, max_blocks_per_seq, 0, 0,
+                                   kv_blocks_per_split, 0);
+  return masked_workspace(static_cast<int64_t>(num_seqs) * tree_len * num_q_heads, p.splits);
+}
+
+pkv_status pkv_paged_attention_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                    const pkv_cache_desc* cache, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                    const int32_t* tree_lens, const uint64_t* tree_mask, int32_t num_seqs,
+                                    int32_t tree_len, int32_t num_q_heads, float scale, int32_t kv_blocks_per_split,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  return masked_impl(MaskKind::kTree, out, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, context_lens,
+                     tree_lens, tree_mask, num_seqs, tree_len, num_q_heads, 0, 0, scale, kv_blocks_per_split,
+                     workspace, workspace_bytes, stream);
+}
+
+int32_t pkv_choose_kv_blocks_per_split_window(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
+                                              int32_t max_blocks_per_seq, int32_t window, int32_t num_sinks,
+                                              int32_t sm_count) {
+  if (!masked_sizes_ok(num_seqs, num_kv_heads, q_len, max_blocks_per_seq, window, num_sinks, false))
+    return max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
+  const MaskedPlan p = masked_plan(num_seqs, num_kv_heads, q_len, max_blocks_per_seq, span_limit(window),
+                                   span_limit(num_sinks), 0, sm_count);
+  return p.splits == 1 ? max_blocks_per_seq : p.tiles_per_split * masked_tile_blocks(q_len);
+}
+
+size_t pkv_workspace_size_window(int32_t num_seqs, int32_t q_len, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                 int32_t window, int32_t num_sinks, int32_t kv_blocks_per_split) {
+  if (!masked_sizes_ok(num_seqs, num_q_heads, q_len, max_blocks_per_seq, window, num_sinks, false) ||
+      kv_blocks_per_split < 0)
+    return 0;
+  const MaskedPlan p = masked_plan(num_seqs, num_q_heads / kGroup, q_len, max_blocks_per_seq, span_limit(window),
+                                   span_limit(num_sinks), kv_blocks_per_split, 0);
+  return masked_workspace(static_cast<int64_t>(num_seqs) * q_len * num_q_heads, p.splits);
+}
+
+pkv_status pkv_paged_attention_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                      const pkv_cache_desc* cache, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t q_len, int32_t num_q_heads, int32_t window, int32_t num_sinks,
+                                      float scale, int32_t kv_blocks_per_split, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  return masked_impl(MaskKind::kWindow, out, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                     context_lens, nullptr, nullptr, num_seqs, q_len, num_q_heads, window, num_sinks, scale,
+                     kv_blocks_per_split, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                          const pkv_cache_desc* cache, int32_t kv_format, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* tree_lens,
+                          int32_t num_seqs, int32_t tree_len, const int32_t* accepted, const int32_t* num_accepted,
+                          int32_t max_accepted, void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (kv_format != PKV_KV_BF16 && kv_format != PKV_KV_Q8_0 && kv_format != PKV_KV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+  if (num_layers < 0 || num_seqs < 0 || max_blocks_per_seq < 1 || tree_len < 1 || max_accepted < 1 ||
+      max_accepted > tree_len)
+    return PKV_ERR_SHAPE;
+  if (tree_len > kMaxTree || max_blocks_per_seq > kMaskedMaxBlocks || num_layers > 65535) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_layers == 0) return PKV_OK;
+  if (!k_caches || !v_caches || !block_tables || !context_lens || !accepted || !num_accepted) return PKV_ERR_NULL;
+  for (int32_t l = 0; l < num_layers; ++l) {  // every check before the first launch
+    if (!k_caches[l] || !v_caches[l]) return PKV_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(k_caches[l]) | reinterpret_cast<uintptr_t>(v_caches[l])) & 15)
+      return PKV_ERR_UNSUPPORTED;
+  }
+  CompactArgs a{};
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.tree_lens = tree_lens;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.err = error_word();
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = cache->num_blocks;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.tree_len = tree_len;
+  a.max_accepted = max_accepted;
+  for (int32_t l0 = 0; l0 < num_layers; l0 += kCompactLayers) {
+    const int32_t n = num_layers - l0 < kCompactLayers ? num_layers - l0 : kCompactLayers;
+    for (int32_t l = 0; l < n; ++l) {
+      a.k_caches[l] = k_caches[l0 + l];
+      a.v_caches[l] = v_caches[l0 + l];
+    }
+    if (launch_kv_compact(a, num_seqs, n, kv_format, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return PKV_ERR_CUDA;
   }
   return PKV_OK;
 }

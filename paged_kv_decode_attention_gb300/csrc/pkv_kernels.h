@@ -135,6 +135,74 @@ bool make_pool_map_e4m3(CUtensorMap* map, const void* pool, int64_t rows);
 // workspace partials for the combine kernel (paged_decode_tc.cu).
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int32_t grid, cudaStream_t stream);
 
+// Attention of several query positions per request under a tree or window
+// mask (paged_masked_tc.cu).  d.q_len = query positions per request (the
+// padded tree size); d.num_splits > 1 or d.part_o set = partials to the
+// workspace for the combine kernel.  A split is tiles_per_split tiles of
+// masked_tile_blocks(q_len) blocks of the list of blocks a CTA reads.
+enum class MaskKind { kTree, kWindow };
+struct MaskedArgs {
+  DecodeArgs d;
+  const int32_t* tree_lens;   // tree: [B] drafted tokens at the end of each context; NULL = q_len
+  const uint64_t* tree_mask;  // tree: [B][q_len][mask_words], bit j = draft j is visible
+  int32_t mask_words;
+  int32_t window;             // window: keys p - window + 1 .. p, and
+  int32_t num_sinks;          //         keys 0 .. num_sinks - 1
+  int32_t tiles_per_split;
+};
+cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream);
+int masked_tile_blocks(int q_len);
+int masked_positions_per_cta(int q_len);
+int masked_ctas_per_sm(int q_len);
+
+// Norms of queries and keys, rotation and append in one pass (qk_norm_rope.cu).
+struct QkNormRopeArgs {
+  void* q_out;               // BF16 [T][Hq][D]
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slot_mapping;
+  const void* q;             // BF16, token t's heads at q + t * q_stride (elements)
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const void* q_weight;      // BF16 [D] or NULL (no norm)
+  const void* k_weight;
+  const float* rope_table;   // FP32 [max_positions][rot_dim]: cosines, then sines
+  const int32_t* positions;
+  unsigned int* err;
+  float eps;
+  int32_t max_positions;
+  int32_t rot_dim;           // 0, or a multiple of 16 up to D
+  int32_t interleaved;
+  int32_t num_tokens;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+};
+cudaError_t launch_qk_norm_rope_append(const QkNormRopeArgs& a, int32_t kv_format, cudaStream_t stream);
+
+// Compaction of accepted drafts (kv_compact.cu), up to kCompactLayers layers per launch.
+constexpr int kCompactLayers = 64;
+constexpr int kMaxTree = 1024;  // drafted tokens per request
+struct CompactArgs {
+  void* k_caches[kCompactLayers];
+  void* v_caches[kCompactLayers];
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* tree_lens;  // NULL = tree_len
+  const int32_t* accepted;   // [B][max_accepted]
+  const int32_t* num_accepted;
+  unsigned int* err;
+  int32_t max_blocks;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t tree_len;
+  int32_t max_accepted;
+};
+cudaError_t launch_kv_compact(const CompactArgs& a, int32_t num_seqs, int32_t layers, int32_t kv_format,
+                              cudaStream_t stream);
+
 // Members per cascade group: 16 requests x 4 heads = one 64-row tile.
 constexpr int kCascadeGroup = 16;
 
