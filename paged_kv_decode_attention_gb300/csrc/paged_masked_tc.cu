@@ -33,12 +33,11 @@
 //              rounding): the remainder's products would make the tensor cores
 //              the bound (3 instead of 2 products per tile).
 //
-// CTA = 3 + 4 kQTiles warps:
-//   warp 0, last: TMA producers of K and of V (16 x 64 boxes, 128-byte
+// CTA = 2 + 5 kQTiles warps:
+//   warp 0, 2 + 4 kQTiles: TMA producers of K and of V (16 x 64 boxes, 128-byte
 //             swizzle, one per block and 64-dim half; blocks past the range
 //             arrive as zeros).
-//   warp 1  : MMA issuer (one thread), polling per row tile for a scored K tile
-//             to issue and for weights to multiply.
+//   warp 1 (and the last, for the second row tile): MMA issuers.
 //   warps 2..: softmax, one thread per row (TMEM lane).  Warps whose rows are
 //             all padding only keep the barriers in step.
 #include <climits>
@@ -60,21 +59,21 @@ constexpr int kQHalfBytes = kQTileBytes / 2;
 
 template <int kQTiles>
 struct Shape {
-  static constexpr int kTileBlocks = kQTiles == 1 ? 4 : 8;
+  static constexpr int kTileBlocks = 4;
   static constexpr int kTileTokens = kTileBlocks * kBlockSize;
-  static constexpr int kNB = kQTiles == 1 ? 2 : 1;  // S/P buffers per row tile
-  static constexpr int kKStages = 3;
-  static constexpr int kVStages = 2;
+  static constexpr int kNB = 2;  // S/P buffers per row tile
+  static constexpr int kKStages = kQTiles == 1 ? 3 : 5;
+  static constexpr int kVStages = kQTiles == 1 ? 2 : 5;
   static constexpr int kHalfBytes = kTileTokens * 128;
   static constexpr int kStageBytes = 2 * kHalfBytes;
-  static constexpr int kWarps = 3 + 4 * kQTiles;
+  static constexpr int kWarps = 2 + 5 * kQTiles;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kVProdWarp = kWarps - 1;
+  static constexpr int kVProdWarp = 2 + 4 * kQTiles;  // the second row tile's MMA warp follows
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kQTiles * kQTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kStageBytes;
   static constexpr int kOffBar = kOffV + kVStages * kStageBytes;
-  static constexpr int kSmem = kOffBar + 256;
+  static constexpr int kSmem = kOffBar + 512;
   static constexpr uint32_t kColO = kNB * kTileTokens;        // S/P buffers, then O (128 columns)
   static constexpr uint32_t kTileCols = kColO + kHeadDim;     // 256 columns per row tile
   static constexpr uint32_t kTmemCols = kQTiles * kTileCols;  // 256 or 512
@@ -107,7 +106,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
                                                      const MaskedArgs& a) {
   using S = Shape<kQTiles>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(sizeof(Bars<kQTiles>) <= 256, "barrier area");
+  static_assert(sizeof(Bars<kQTiles>) <= 512, "barrier area");
   Bars<kQTiles>* bars = reinterpret_cast<Bars<kQTiles>*>(smem + S::kOffBar);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -200,8 +199,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   const int qi = pos0 + qt * kPosPerTile + (row >> 2);  // query index
   const bool in_shape = softmax_warp && qi < a.d.q_len;
   const bool row_valid = in_shape && qi < n_new;
-  const int64_t orow = (static_cast<int64_t>(r) * a.d.q_len + qi) * hq + kvh * kGroup + (row & 3);
-  const int64_t slot = orow * a.d.part_slots + split;
+  auto out_row = [&]() -> int64_t { return (static_cast<int64_t>(r) * a.d.q_len + qi) * hq + kvh * kGroup + (row & 3); };
+  auto part_slot = [&]() -> int64_t { return out_row() * a.d.part_slots + split; };
 
   const uint32_t tmem = bars->tmem_base;
   const uint32_t sbase = smem_addr(smem);
@@ -210,9 +209,9 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   // zeros for a row without a result (padding, or nothing visible)
   auto write_empty = [&]() {
     if constexpr (kSplit) {
-      a.d.part_lse[slot] = -INFINITY;
+      a.d.part_lse[part_slot()] = -INFINITY;
     } else {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + orow * kHeadDim);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + out_row() * kHeadDim);
 #pragma unroll
       for (int c = 0; c < kHeadDim * 2 / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
     }
@@ -271,76 +270,91 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       // the last tiles' copies must land before shared memory is released
       for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp > S::kVProdWarp) {
     // ---------------------------- MMA issuer ----------------------------
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
-      constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
-      int js[kQTiles], jp[kQTiles];
+    // One warp per row tile, so that neither tile's chain waits for the
+    // other's (issuing a product of 64 tokens takes about as long as its
+    // execution).  The whole warp walks the schedule and lane 0 issues: S of
+    // the next tile, then P.V of this one, so that a product is always queued
+    // while a softmax runs.
+    constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
+    constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
+    const uint64_t q_desc = tc::smem_desc(sbase + S::kOffQ, 16, 1024);
+    const uint64_t k_desc = tc::smem_desc(sbase + S::kOffK, 16, 1024);
+    const uint64_t v_desc = tc::smem_desc(sbase + S::kOffV, S::kHalfBytes, 1024);
+    const bool leader = lane == 0;
+    const int t = warp == 1 ? 0 : 1;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    };
+    // S_j into buffer j % 2
+    auto issue_s = [&](int j, int st) {
+      const uint32_t d = tmem + t * S::kTileCols + (j & 1) * S::kTileTokens;
+      const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
+      const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
+      tc::fence_after_sync();
+      if (leader) {
 #pragma unroll
-      for (int t = 0; t < kQTiles; ++t) js[t] = jp[t] = t < q_tiles ? 0 : n_tiles;
-      uint64_t t_idle = 0;
-      ok = mbar_wait(&bars->q_full, 0);
-      bool done = false;
-      while (ok && !done) {
-        bool progressed = false;
-        done = true;
-#pragma unroll
-        for (int t = 0; t < kQTiles; ++t) {
-          const uint32_t tcol = tmem + t * S::kTileCols;
-          if (js[t] < n_tiles) {
-            const int j = js[t], st = j % S::kKStages, sb = j % S::kNB;
-            bool ready = mbar_test_wait(&bars->k_full[st], (j / S::kKStages) & 1);
-            if (ready && j >= S::kNB) ready = mbar_test_wait(&bars->o_done[t][sb], ((j / S::kNB) - 1) & 1);
-            if (ready) {
-              tc::fence_after_sync();
-              const uint32_t kst = sbase + S::kOffK + st * S::kStageBytes;
-              const uint32_t qst = sbase + S::kOffQ + t * kQTileBytes;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc::mma_bf16(tcol + sb * S::kTileTokens,
-                             tc::smem_desc(qst + (kk >> 2) * kQHalfBytes + 32 * (kk & 3), 16, 1024),
-                             tc::smem_desc(kst + (kk >> 2) * S::kHalfBytes + 32 * (kk & 3), 16, 1024), kIdS, kk > 0);
-              tc::commit(&bars->s_full[t][sb]);
-              tc::commit(&bars->k_empty[st]);
-              if (q_tiles < kQTiles) tc::commit(&bars->k_empty[st]);  // the empty row tile's share
-              ++js[t];
-              progressed = true;
-            }
-          }
-          if (jp[t] < js[t]) {
-            const int j = jp[t], st = j % S::kVStages, sb = j % S::kNB;
-            if (mbar_test_wait(&bars->p_full[t][sb], (j / S::kNB) & 1) &&
-                mbar_test_wait(&bars->v_full[st], (j / S::kVStages) & 1)) {
-              tc::fence_after_sync();
-              const uint32_t ptm = tcol + sb * S::kTileTokens;
-              const uint32_t vst = sbase + S::kOffV + st * S::kStageBytes;
-#pragma unroll
-              for (int part = 0; part < (S::kRemainder ? 2 : 1); ++part)
-#pragma unroll
-                for (int kk = 0; kk < S::kTileBlocks; ++kk)
-                  tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + (S::kTileTokens / 2) * part + 8 * kk,
-                                      tc::smem_desc(vst + 2048 * kk, S::kHalfBytes, 1024), kIdO,
-                                      (j > 0 || part > 0 || kk > 0) ? 1u : 0u);
-              tc::commit(&bars->o_done[t][sb]);
-              tc::commit(&bars->v_empty[st]);
-              if (q_tiles < kQTiles) tc::commit(&bars->v_empty[st]);
-              ++jp[t];
-              progressed = true;
-            }
-          }
-          if (jp[t] < n_tiles) done = false;
-        }
-        if (progressed) {
-          t_idle = 0;
-        } else if (t_idle == 0) {
-          t_idle = global_timer_ns();
-        } else if (global_timer_ns() - t_idle > kWaitLimitNs) {
-          ok = false;
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16(d, qd + (((kk >> 2) * kQHalfBytes + 32 * (kk & 3)) >> 4),
+                       kd + (((kk >> 2) * S::kHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
+        tc::commit(&bars->s_full[t][j & 1]);
+        tc::commit(&bars->k_empty[st]);
       }
-      if (!ok) report(a.d.err, PKV_DEVERR_TIMEOUT);
+      __syncwarp();
+    };
+    auto issue_pv = [&](int j, int st) {
+      const uint32_t tcol = tmem + t * S::kTileCols;
+      const uint32_t ptm = tcol + (j & 1) * S::kTileTokens;
+      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4);
+      tc::fence_after_sync();
+      if (leader) {
+#pragma unroll
+        for (int part = 0; part < (S::kRemainder ? 2 : 1); ++part)
+#pragma unroll
+          for (int kk = 0; kk < S::kTileBlocks; ++kk)
+            tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + (S::kTileTokens / 2) * part + 8 * kk, vd + ((2048 * kk) >> 4),
+                                kIdO, (j > 0 || part > 0 || kk > 0) ? 1u : 0u);
+        tc::commit(&bars->o_done[t][j & 1]);
+        tc::commit(&bars->v_empty[st]);
+      }
+      __syncwarp();
+    };
+    const bool live = t < q_tiles;
+    if (live) {
+      ok = wait(&bars->q_full, 0) && wait(&bars->k_full[0], 0);
+      if (ok) issue_s(0, 0);
     }
+    int ks = 0, kph = 0, vs = 0, vph = 0;
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      if (live) {
+        if (++ks == S::kKStages) {
+          ks = 0;
+          kph ^= 1;
+        }
+        if (j + 1 < n_tiles) {  // its buffer is free once the P.V that read it is done
+          ok = wait(&bars->k_full[ks], kph);
+          if (ok && j > 0) ok = wait(&bars->o_done[t][(j + 1) & 1], ((j - 1) >> 1) & 1);
+          if (ok) issue_s(j + 1, ks);
+        }
+        ok = ok && wait(&bars->v_full[vs], vph) && wait(&bars->p_full[t][j & 1], (j >> 1) & 1);
+        if (ok) issue_pv(j, vs);
+      } else {  // a row tile without queries only gives the stages back
+        ok = wait(&bars->k_full[ks], kph);
+        if (ok && leader) mbar_arrive(&bars->k_empty[ks]);
+        if (++ks == S::kKStages) {
+          ks = 0;
+          kph ^= 1;
+        }
+        ok = ok && wait(&bars->v_full[vs], vph);
+        if (ok && leader) mbar_arrive(&bars->v_empty[vs]);
+      }
+      if (++vs == S::kVStages) {
+        vs = 0;
+        vph ^= 1;
+      }
+    }
+    if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
     __syncwarp();
   } else {
     // ---------------------------- softmax ----------------------------
@@ -475,7 +489,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         const float nm = (m_stale == -INFINITY) ? 0.f : -m_stale;
         const float2 c2 = make_float2(c, c);
         const float2 nm2 = make_float2(nm, nm);
-        float2 acc2 = make_float2(0.f, 0.f);
+        float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // P_j overwrites the S_j buffer it came from, 2 BF16 per 32-bit column
 #pragma unroll
         for (int cc = 0; cc < S::kTileTokens / 32; ++cc) {
@@ -485,7 +499,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
             const float2 x = __ffma2_rn(make_float2(s[32 * cc + 2 * e], s[32 * cc + 2 * e + 1]), c2, nm2);
             const float p0 = exp2_approx(x.x);
             const float p1 = exp2_approx(x.y);
-            acc2 = __fadd2_rn(acc2, make_float2(p0, p1));
+            acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
             if constexpr (S::kRemainder)
               pr[e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
@@ -493,7 +507,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           tc::tmem_st16u(tcol + sb * S::kTileTokens + 16 * cc, pk);
           if constexpr (S::kRemainder) tc::tmem_st16u(tcol + sb * S::kTileTokens + S::kTileTokens / 2 + 16 * cc, pr);
         }
-        l += acc2.x + acc2.y;
+        l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
       }
       // V rows that no query of this CTA sees have weight 0 but may hold
       // anything (slots past the context): zero them
@@ -535,12 +549,12 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         tc::tmem_wait_ld();
         if (!live) continue;
         if constexpr (kSplit) {
-          float4* dst = reinterpret_cast<float4*>(a.d.part_o + slot * kHeadDim + 32 * cc);
+          float4* dst = reinterpret_cast<float4*>(a.d.part_o + part_slot() * kHeadDim + 32 * cc);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + orow * kHeadDim + 32 * cc);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + out_row() * kHeadDim + 32 * cc);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint4 w;
@@ -553,7 +567,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         }
       }
       if constexpr (kSplit) {
-        if (live) a.d.part_lse[slot] = (m_stale + log2f(l)) * kLn2;
+        if (live) a.d.part_lse[part_slot()] = (m_stale + log2f(l)) * kLn2;
       }
       if (in_shape && !live) write_empty();
     } else if (in_shape && ok) {
