@@ -33,12 +33,12 @@
 //              rounding): the remainder's products would make the tensor cores
 //              the bound (3 instead of 2 products per tile).
 //
-// CTA = 2 + 5 kQTiles warps:
-//   warp 0, 2 + 4 kQTiles: TMA producers of K and of V (16 x 64 boxes, 128-byte
+// CTA = 4 + 4 kQTiles warps:
+//   warps 0, 2: TMA producers of K and of V (16 x 64 boxes, 128-byte
 //             swizzle, one per block and 64-dim half; blocks past the range
 //             arrive as zeros).
-//   warp 1 (and the last, for the second row tile): MMA issuers.
-//   warps 2..: softmax, one thread per row (TMEM lane).  Warps whose rows are
+//   warps 1, 3: MMA issuers, one per row tile.
+//   warps 4..: softmax, one thread per row (TMEM lane).  Warps whose rows are
 //             all padding only keep the barriers in step.
 #include <climits>
 #include <cmath>
@@ -66,9 +66,15 @@ struct Shape {
   static constexpr int kVStages = kQTiles == 1 ? 2 : 5;
   static constexpr int kHalfBytes = kTileTokens * 128;
   static constexpr int kStageBytes = 2 * kHalfBytes;
-  static constexpr int kWarps = 2 + 5 * kQTiles;
+  static constexpr int kWarps = 4 + 4 * kQTiles;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kVProdWarp = 2 + 4 * kQTiles;  // the second row tile's MMA warp follows
+  // Registers per thread: the launch's share (65536 / (threads x CTAs)) is
+  // moved from the four issuing warps to the softmax warps, which hold a
+  // tile's scores; the sum stays within what the block was launched with.
+  static constexpr int kLaunchRegs = kQTiles == 1 ? 128 : 168;
+  static constexpr int kIssueRegs = kQTiles == 1 ? 64 : 80;
+  static constexpr int kSoftmaxRegs = kQTiles == 1 ? 192 : 208;
+  static_assert((kIssueRegs + kQTiles * kSoftmaxRegs) * 128 <= kLaunchRegs * (4 + 4 * kQTiles) * 32, "register split");
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kQTiles * kQTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kStageBytes;
@@ -95,6 +101,16 @@ struct Bars {
   uint64_t q_full;
   uint32_t tmem_base;
 };
+
+// Move registers between warpgroups (all warps of one execute it).
+template <int kRegs>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // The x lowest bits (x may lie outside 0..64).
 __device__ __forceinline__ uint64_t low_bits(int x) {
@@ -192,8 +208,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   const int q_tiles = n_pos > kPosPerTile ? 2 : 1;  // row tiles with queries (kQTiles 1: always 1)
 
   // rows of the softmax threads
-  const bool softmax_warp = warp >= 2 && warp < 2 + 4 * kQTiles;
-  const int qt = softmax_warp ? (warp - 2) >> 2 : 0;
+  const bool softmax_warp = warp >= 4;
+  const int qt = softmax_warp ? (warp >> 2) - 1 : 0;
   const int quad = warp & 3;  // TMEM sub-partition of this warp
   const int row = quad * 32 + lane;
   const int qi = pos0 + qt * kPosPerTile + (row >> 2);  // query index
@@ -219,9 +235,11 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
 
   if (n_tiles <= 0) {
     if (in_shape) write_empty();
-  } else if (warp == 0 || warp == S::kVProdWarp) {
+  } else if (!softmax_warp) {
+   set_max_regs_down<S::kIssueRegs>();
+   if (warp == 0 || warp == 2) {
     // ---------------------------- TMA producers ----------------------------
-    const bool is_v = warp == S::kVProdWarp;
+    const bool is_v = warp == 2;
     const int stages = is_v ? S::kVStages : S::kKStages;
     uint64_t* full = is_v ? bars->v_full : bars->k_full;
     uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
@@ -270,7 +288,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       // the last tiles' copies must land before shared memory is released
       for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
     }
-  } else if (warp == 1 || warp > S::kVProdWarp) {
+   } else if (kQTiles == 2 || warp == 1) {
     // ---------------------------- MMA issuer ----------------------------
     // One warp per row tile, so that neither tile's chain waits for the
     // other's (issuing a product of 64 tokens takes about as long as its
@@ -283,11 +301,21 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     const uint64_t k_desc = tc::smem_desc(sbase + S::kOffK, 16, 1024);
     const uint64_t v_desc = tc::smem_desc(sbase + S::kOffV, S::kHalfBytes, 1024);
     const bool leader = lane == 0;
-    const int t = warp == 1 ? 0 : 1;
+    const int t = warp >> 1;  // warp 1 or 3
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
     // S_j into buffer j % 2
+    // Stages go back by plain arrivals once a later wait has shown that the
+    // products that read them are done (a commit costs this warp 46 cycles).
+    auto give_back = [&](uint64_t* bar) {
+      if (leader) mbar_arrive(bar);
+    };
+    // both barriers tried before either result is looked at
+    auto wait2 = [&](uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp) -> bool {
+      const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
+      return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
+    };
     auto issue_s = [&](int j, int st) {
       const uint32_t d = tmem + t * S::kTileCols + (j & 1) * S::kTileTokens;
       const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
@@ -299,7 +327,6 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           tc::mma_bf16(d, qd + (((kk >> 2) * kQHalfBytes + 32 * (kk & 3)) >> 4),
                        kd + (((kk >> 2) * S::kHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
         tc::commit(&bars->s_full[t][j & 1]);
-        tc::commit(&bars->k_empty[st]);
       }
       __syncwarp();
     };
@@ -316,7 +343,6 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
             tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + (S::kTileTokens / 2) * part + 8 * kk, vd + ((2048 * kk) >> 4),
                                 kIdO, (j > 0 || part > 0 || kk > 0) ? 1u : 0u);
         tc::commit(&bars->o_done[t][j & 1]);
-        tc::commit(&bars->v_empty[st]);
       }
       __syncwarp();
     };
@@ -333,12 +359,19 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           kph ^= 1;
         }
         if (j + 1 < n_tiles) {  // its buffer is free once the P.V that read it is done
-          ok = wait(&bars->k_full[ks], kph);
-          if (ok && j > 0) ok = wait(&bars->o_done[t][(j + 1) & 1], ((j - 1) >> 1) & 1);
+          if (j > 0) {
+            ok = wait2(&bars->k_full[ks], kph, &bars->o_done[t][(j + 1) & 1], ((j - 1) >> 1) & 1);
+            if (ok) give_back(&bars->v_empty[vs == 0 ? S::kVStages - 1 : vs - 1]);
+          } else {
+            ok = wait(&bars->k_full[ks], kph);
+          }
           if (ok) issue_s(j + 1, ks);
         }
-        ok = ok && wait(&bars->v_full[vs], vph) && wait(&bars->p_full[t][j & 1], (j >> 1) & 1);
-        if (ok) issue_pv(j, vs);
+        ok = ok && wait2(&bars->v_full[vs], vph, &bars->p_full[t][j & 1], (j >> 1) & 1);
+        if (ok) {
+          give_back(&bars->k_empty[ks == 0 ? S::kKStages - 1 : ks - 1]);  // the weights were made from S_j
+          issue_pv(j, vs);
+        }
       } else {  // a row tile without queries only gives the stages back
         ok = wait(&bars->k_full[ks], kph);
         if (ok && leader) mbar_arrive(&bars->k_empty[ks]);
@@ -356,12 +389,14 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     }
     if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
     __syncwarp();
+   }
   } else {
     // ---------------------------- softmax ----------------------------
+    set_max_regs_up<S::kSoftmaxRegs>();
     {
       // this row tile's queries -> 128-byte swizzled K-major tile, two 64-dim
       // halves; thread t loads 16-byte chunk t % 16 of rows t / 16 + 8k
-      const int t = (threadIdx.x - 64) & 127;
+      const int t = threadIdx.x & 127;
       const int ch = t & 15;
       const uint16_t* qbase = static_cast<const uint16_t*>(a.d.q);
       uint8_t* qs = smem + S::kOffQ + qt * kQTileBytes;
@@ -519,7 +554,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         if (tail || head) {
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (j / S::kVStages) & 1));
           uint8_t* vt = smem + S::kOffV + st * S::kStageBytes;
-          const int t128 = (threadIdx.x - 64) & 127;
+          const int t128 = threadIdx.x & 127;
           for (int idx = t128; idx < S::kTileTokens * 16; idx += 128) {
             const int tk = idx >> 4, ch = idx & 15, t = tok + tk;
             bool dead = t >= key_end;
