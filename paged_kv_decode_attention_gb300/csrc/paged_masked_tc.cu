@@ -37,7 +37,7 @@
 //   warps 0, 2: TMA producers of K and of V (16 x 64 boxes, 128-byte
 //             swizzle, one per block and 64-dim half; blocks past the range
 //             arrive as zeros).
-//   warps 1, 3: MMA issuers, one per row tile.
+//   warp 1  : MMA issuer (warp 3 idles).
 //   warps 4..: softmax, one thread per row (TMEM lane).  Warps whose rows are
 //             all padding only keep the barriers in step.
 #include <climits>
@@ -59,11 +59,12 @@ constexpr int kQHalfBytes = kQTileBytes / 2;
 
 template <int kQTiles>
 struct Shape {
-  static constexpr int kTileBlocks = 4;
+  static constexpr int kTileBlocks = kQTiles == 1 ? 4 : 8;
   static constexpr int kTileTokens = kTileBlocks * kBlockSize;
-  static constexpr int kNB = 2;  // S/P buffers per row tile
-  static constexpr int kKStages = kQTiles == 1 ? 3 : 5;
-  static constexpr int kVStages = kQTiles == 1 ? 2 : 5;
+  static constexpr int kNB = kQTiles == 1 ? 2 : 1;     // S/P buffers per row tile
+  static constexpr int kParts = kQTiles == 1 ? 1 : 2;  // weights are handed over in this many 64-token parts
+  static constexpr int kKStages = 3;
+  static constexpr int kVStages = 2;
   static constexpr int kHalfBytes = kTileTokens * 128;
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kWarps = 4 + 4 * kQTiles;
@@ -96,7 +97,7 @@ struct Bars {
   uint64_t v_full[S::kVStages];
   uint64_t v_empty[S::kVStages];
   uint64_t s_full[kQTiles][S::kNB];
-  uint64_t p_full[kQTiles][S::kNB];
+  uint64_t p_full[kQTiles][2];  // per S/P buffer, or per part
   uint64_t o_done[kQTiles][S::kNB];
   uint64_t q_full;
   uint32_t tmem_base;
@@ -124,24 +125,28 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(sizeof(Bars<kQTiles>) <= 512, "barrier area");
   Bars<kQTiles>* bars = reinterpret_cast<Bars<kQTiles>*>(smem + S::kOffBar);
-  const int warp = threadIdx.x >> 5;
+  // Warp indexes, tile counts and addresses go through a broadcast so that the
+  // compiler knows them to be uniform: the issuing warps' descriptors then
+  // live in uniform registers, where the MMA instructions read them.
+  auto uniform = [](int x) -> int { return __shfl_sync(0xffffffffu, x, 0); };
+  const int warp = uniform(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
 
   // ---------------- set-up: barriers, TMEM (reads no input) ----------------
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kKStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], kQTiles);
+      mbar_init(&bars->k_empty[s], 1);
     }
     for (int s = 0; s < S::kVStages; ++s) {
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], kQTiles);
+      mbar_init(&bars->v_empty[s], 1);
     }
     for (int t = 0; t < kQTiles; ++t)
-      for (int s = 0; s < S::kNB; ++s) {
-        mbar_init(&bars->s_full[t][s], 1);
+      for (int s = 0; s < 2; ++s) {
+        if (s < S::kNB) mbar_init(&bars->s_full[t][s], 1);
         mbar_init(&bars->p_full[t][s], 128);
-        mbar_init(&bars->o_done[t][s], 1);
+        if (s < S::kNB) mbar_init(&bars->o_done[t][s], 1);
       }
     mbar_init(&bars->q_full, 128 * kQTiles);
     fence_barrier_init();
@@ -199,13 +204,13 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   const int sink_tiles = (sink_blocks + S::kTileBlocks - 1) / S::kTileBlocks;
   const int all_tiles = sink_tiles + (max(0, end_block - first_block) + S::kTileBlocks - 1) / S::kTileBlocks;
   const int t_first = split * a.tiles_per_split;  // first tile of this split
-  const int n_tiles = min(all_tiles - t_first, a.tiles_per_split);
+  const int n_tiles = uniform(min(all_tiles - t_first, a.tiles_per_split));
   // first token of tile j of the split
   auto tile_token = [&](int j) -> int {
     const int i = t_first + j;
     return (i < sink_tiles ? i * S::kTileBlocks : first_block + (i - sink_tiles) * S::kTileBlocks) * kBlockSize;
   };
-  const int q_tiles = n_pos > kPosPerTile ? 2 : 1;  // row tiles with queries (kQTiles 1: always 1)
+  const int q_tiles = uniform(n_pos > kPosPerTile ? 2 : 1);  // row tiles with queries (kQTiles 1: always 1)
 
   // rows of the softmax threads
   const bool softmax_warp = warp >= 4;
@@ -218,8 +223,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   auto out_row = [&]() -> int64_t { return (static_cast<int64_t>(r) * a.d.q_len + qi) * hq + kvh * kGroup + (row & 3); };
   auto part_slot = [&]() -> int64_t { return out_row() * a.d.part_slots + split; };
 
-  const uint32_t tmem = bars->tmem_base;
-  const uint32_t sbase = smem_addr(smem);
+  const uint32_t tmem = uniform(bars->tmem_base);
+  const uint32_t sbase = uniform(smem_addr(smem));
   bool ok = true;
 
   // zeros for a row without a result (padding, or nothing visible)
@@ -288,36 +293,35 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       // the last tiles' copies must land before shared memory is released
       for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
     }
-   } else if (kQTiles == 2 || warp == 1) {
+   } else if (warp == 1) {
     // ---------------------------- MMA issuer ----------------------------
-    // One warp per row tile, so that neither tile's chain waits for the
-    // other's (issuing a product of 64 tokens takes about as long as its
-    // execution).  The whole warp walks the schedule and lane 0 issues: S of
-    // the next tile, then P.V of this one, so that a product is always queued
-    // while a softmax runs.
+    // One warp, a fixed order (the whole warp walks it, lane 0 issues):
+    //   kQTiles 1: S of tile j + 1, then P.V of tile j;
+    //   kQTiles 2: S of row tile 1, P.V of row tile 0, S of row tile 0 for the
+    //     next tile, P.V of row tile 1 -- the row tiles stay half a period
+    //     apart, so that one's softmax runs under the other's products.
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
     const uint64_t q_desc = tc::smem_desc(sbase + S::kOffQ, 16, 1024);
     const uint64_t k_desc = tc::smem_desc(sbase + S::kOffK, 16, 1024);
     const uint64_t v_desc = tc::smem_desc(sbase + S::kOffV, S::kHalfBytes, 1024);
     const bool leader = lane == 0;
-    const int t = warp >> 1;  // warp 1 or 3
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-    };
-    // S_j into buffer j % 2
-    // Stages go back by plain arrivals once a later wait has shown that the
-    // products that read them are done (a commit costs this warp 46 cycles).
-    auto give_back = [&](uint64_t* bar) {
-      if (leader) mbar_arrive(bar);
     };
     // both barriers tried before either result is looked at
     auto wait2 = [&](uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp) -> bool {
       const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
       return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
     };
-    auto issue_s = [&](int j, int st) {
-      const uint32_t d = tmem + t * S::kTileCols + (j & 1) * S::kTileTokens;
+    // Stages go back by plain arrivals once a later wait has shown that the
+    // products that read them are done (a commit costs this warp 46 cycles).
+    auto give_back = [&](uint64_t* bar) {
+      if (leader) mbar_arrive(bar);
+    };
+    // S of row tile t over the tile in K stage st, into buffer buf
+    auto issue_s = [&](int t, int buf, int st) {
+      const uint32_t d = tmem + t * S::kTileCols + buf * S::kTileTokens;
       const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
       const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
       tc::fence_after_sync();
@@ -326,65 +330,91 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         for (int kk = 0; kk < 8; ++kk)
           tc::mma_bf16(d, qd + (((kk >> 2) * kQHalfBytes + 32 * (kk & 3)) >> 4),
                        kd + (((kk >> 2) * S::kHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
-        tc::commit(&bars->s_full[t][j & 1]);
+        tc::commit(&bars->s_full[t][buf]);
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int j, int st) {
+    // O += P V over the 64 tokens of part `part` of the tile in V stage st
+    auto issue_pv = [&](int t, int buf, int st, int part, bool first) {
       const uint32_t tcol = tmem + t * S::kTileCols;
-      const uint32_t ptm = tcol + (j & 1) * S::kTileTokens;
-      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4);
+      const uint32_t ptm = tcol + buf * S::kTileTokens + 32 * part;
+      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4) + part * ((4 * 2048) >> 4);
       tc::fence_after_sync();
       if (leader) {
+        // (P's remainders follow its BF16 parts: column 8 kk, kk 4 .. 7)
 #pragma unroll
-        for (int part = 0; part < (S::kRemainder ? 2 : 1); ++part)
-#pragma unroll
-          for (int kk = 0; kk < S::kTileBlocks; ++kk)
-            tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + (S::kTileTokens / 2) * part + 8 * kk, vd + ((2048 * kk) >> 4),
-                                kIdO, (j > 0 || part > 0 || kk > 0) ? 1u : 0u);
-        tc::commit(&bars->o_done[t][j & 1]);
+        for (int kk = 0; kk < (S::kRemainder ? 8 : 4); ++kk)
+          tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + 8 * kk, vd + (kk & 3) * (2048 >> 4), kIdO,
+                              (!first || kk > 0) ? 1u : 0u);
+        if (part == S::kParts - 1) tc::commit(&bars->o_done[t][buf]);
       }
       __syncwarp();
     };
-    const bool live = t < q_tiles;
-    if (live) {
-      ok = wait(&bars->q_full, 0) && wait(&bars->k_full[0], 0);
-      if (ok) issue_s(0, 0);
-    }
-    int ks = 0, kph = 0, vs = 0, vph = 0;
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      if (live) {
-        if (++ks == S::kKStages) {
-          ks = 0;
-          kph ^= 1;
-        }
-        if (j + 1 < n_tiles) {  // its buffer is free once the P.V that read it is done
-          if (j > 0) {
-            ok = wait2(&bars->k_full[ks], kph, &bars->o_done[t][(j + 1) & 1], ((j - 1) >> 1) & 1);
-            if (ok) give_back(&bars->v_empty[vs == 0 ? S::kVStages - 1 : vs - 1]);
-          } else {
-            ok = wait(&bars->k_full[ks], kph);
-          }
-          if (ok) issue_s(j + 1, ks);
-        }
-        ok = ok && wait2(&bars->v_full[vs], vph, &bars->p_full[t][j & 1], (j >> 1) & 1);
-        if (ok) {
-          give_back(&bars->k_empty[ks == 0 ? S::kKStages - 1 : ks - 1]);  // the weights were made from S_j
-          issue_pv(j, vs);
-        }
-      } else {  // a row tile without queries only gives the stages back
-        ok = wait(&bars->k_full[ks], kph);
-        if (ok && leader) mbar_arrive(&bars->k_empty[ks]);
-        if (++ks == S::kKStages) {
-          ks = 0;
-          kph ^= 1;
-        }
-        ok = ok && wait(&bars->v_full[vs], vph);
-        if (ok && leader) mbar_arrive(&bars->v_empty[vs]);
+    int ks = 0, kph = 0, vs = 0, vph = 0;  // stages and phases of the next S and the next P.V
+    auto next_k = [&]() {
+      if (++ks == S::kKStages) {
+        ks = 0;
+        kph ^= 1;
       }
+    };
+    auto last = [](int st, int stages) -> int { return st == 0 ? stages - 1 : st - 1; };
+    auto next_v = [&]() {
       if (++vs == S::kVStages) {
         vs = 0;
         vph ^= 1;
+      }
+    };
+    ok = wait(&bars->q_full, 0) && wait(&bars->k_full[0], 0);
+    if (ok) issue_s(0, 0, 0);
+    if constexpr (kQTiles == 1) {
+      for (int j = 0; j < n_tiles && ok; ++j, next_v()) {
+        const bool more = j + 1 < n_tiles;
+        next_k();  // the stage of tile j + 1
+        if (more) {  // its buffer is free once P.V of tile j - 1 is done
+          if (j > 0) {
+            ok = wait2(&bars->k_full[ks], kph, &bars->o_done[0][(j + 1) & 1], ((j - 1) >> 1) & 1);
+            if (ok) give_back(&bars->v_empty[last(vs, S::kVStages)]);
+          } else {
+            ok = wait(&bars->k_full[ks], kph);
+          }
+          if (ok) issue_s(0, (j + 1) & 1, ks);
+        }
+        ok = ok && wait2(&bars->v_full[vs], vph, &bars->p_full[0][j & 1], (j >> 1) & 1);
+        if (ok) {
+          give_back(&bars->k_empty[last(ks, S::kKStages)]);  // the weights were made from S_j
+          issue_pv(0, j & 1, vs, 0, j == 0);
+        }
+      }
+    } else {
+      const bool two = q_tiles == 2;
+      for (int j = 0; j < n_tiles && ok; ++j, next_v()) {
+        const bool more = j + 1 < n_tiles;
+        if (two) {
+          if (j > 0) {
+            ok = wait(&bars->o_done[1][0], (j - 1) & 1);
+            if (ok) give_back(&bars->v_empty[last(vs, S::kVStages)]);
+          }
+          if (ok) issue_s(1, 0, ks);
+        }
+        ok = ok && wait2(&bars->v_full[vs], vph, &bars->p_full[0][0], j & 1);
+        if (ok && !two) give_back(&bars->k_empty[ks]);
+        if (ok) issue_pv(0, 0, vs, 0, j == 0);
+        ok = ok && wait(&bars->p_full[0][1], j & 1);
+        if (ok) issue_pv(0, 0, vs, 1, false);
+        const int k_now = ks;
+        next_k();
+        if (more) {
+          ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[0][0], j & 1);
+          if (ok && !two) give_back(&bars->v_empty[vs]);
+          if (ok) issue_s(0, 0, ks);
+        }
+        if (two) {
+          ok = ok && wait(&bars->p_full[1][0], j & 1);
+          if (ok) give_back(&bars->k_empty[k_now]);  // both row tiles have their weights
+          if (ok) issue_pv(1, 0, vs, 0, j == 0);
+          ok = ok && wait(&bars->p_full[1][1], j & 1);
+          if (ok) issue_pv(1, 0, vs, 1, false);
+        }
       }
     }
     if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
@@ -471,13 +501,13 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[qt][sb], (j / S::kNB) & 1));
       if (!ok) break;
       const bool part = partial(tok);
+      float s[S::kTileTokens];
       if (warp_live) {
         tc::fence_after_sync();
-        float s[S::kTileTokens];
 #pragma unroll
         for (int cc = 0; cc < S::kTileTokens / 32; ++cc) tc::tmem_ld32(tcol + sb * S::kTileTokens + 32 * cc, s + 32 * cc);
         tc::tmem_wait_ld();
-        if (part) {
+        if (__builtin_expect(part, 0)) {
 #pragma unroll
           for (int w = 0; w < S::kTileTokens / 64; ++w) {
             const uint64_t m = row_valid ? visible(tok + 64 * w, tok < first_block * kBlockSize) : 0ull;
@@ -504,7 +534,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         const bool grow = mx > m_stale + kRescaleThreshold;  // also true the first time a row sees a key
         const float m_new = grow ? mx : m_stale;
         const float alpha = grow ? exp2_approx(m_stale - m_new) : 1.f;  // 0 while m_stale is -inf
-        if (__any_sync(0xffffffffu, grow && j > 0 && m_stale != -INFINITY)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, grow && j > 0 && m_stale != -INFINITY), 0)) {
           // O holds weights taken against the old maxima: rescale this warp's rows
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(j - 1) % S::kNB], ((j - 1) / S::kNB) & 1));
           tc::fence_after_sync();
@@ -521,32 +551,10 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         }
         l *= alpha;
         m_stale = m_new;
-        const float nm = (m_stale == -INFINITY) ? 0.f : -m_stale;
-        const float2 c2 = make_float2(c, c);
-        const float2 nm2 = make_float2(nm, nm);
-        float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // P_j overwrites the S_j buffer it came from, 2 BF16 per 32-bit column
-#pragma unroll
-        for (int cc = 0; cc < S::kTileTokens / 32; ++cc) {
-          uint32_t pk[16], pr[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = __ffma2_rn(make_float2(s[32 * cc + 2 * e], s[32 * cc + 2 * e + 1]), c2, nm2);
-            const float p0 = exp2_approx(x.x);
-            const float p1 = exp2_approx(x.y);
-            acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);
-            if constexpr (S::kRemainder)
-              pr[e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
-          }
-          tc::tmem_st16u(tcol + sb * S::kTileTokens + 16 * cc, pk);
-          if constexpr (S::kRemainder) tc::tmem_st16u(tcol + sb * S::kTileTokens + S::kTileTokens / 2 + 16 * cc, pr);
-        }
-        l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
       }
       // V rows that no query of this CTA sees have weight 0 but may hold
       // anything (slots past the context): zero them
-      if (part) {
+      if (__builtin_expect(part, 0)) {
         const bool tail = tok + S::kTileTokens > key_end && key_end > tok && (key_end & (kBlockSize - 1)) != 0;
         bool head = false;
         if constexpr (kMask == MaskKind::kWindow)
@@ -564,10 +572,37 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           }
         }
       }
-      tc::tmem_wait_st();
-      tc::fence_proxy_async_smem();  // zeroed V rows, if any, before the PV MMA reads them
-      tc::fence_before_sync();
-      mbar_arrive(&bars->p_full[qt][sb]);
+#pragma unroll
+      for (int part_i = 0; part_i < S::kParts; ++part_i) {
+        if (warp_live) {
+          const float nm = (m_stale == -INFINITY) ? 0.f : -m_stale;
+          const float2 c2 = make_float2(c, c);
+          const float2 nm2 = make_float2(nm, nm);
+          float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // P_j overwrites the S_j buffer it came from, 2 BF16 per 32-bit column
+#pragma unroll
+          for (int cc = 2 * part_i; cc < 2 * part_i + 2; ++cc) {
+            uint32_t pk[16], pr[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = __ffma2_rn(make_float2(s[32 * cc + 2 * e], s[32 * cc + 2 * e + 1]), c2, nm2);
+              const float p0 = exp2_approx(x.x);
+              const float p1 = exp2_approx(x.y);
+              acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
+              pk[e] = pack_bf16x2(p0, p1);
+              if constexpr (S::kRemainder)
+                pr[e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
+            }
+            tc::tmem_st16u(tcol + sb * S::kTileTokens + 16 * cc, pk);
+            if constexpr (S::kRemainder) tc::tmem_st16u(tcol + sb * S::kTileTokens + S::kTileTokens / 2 + 16 * cc, pr);
+          }
+          l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
+        }
+        tc::tmem_wait_st();
+        tc::fence_proxy_async_smem();  // zeroed V rows, if any, before the PV MMA reads them
+        tc::fence_before_sync();
+        mbar_arrive(&bars->p_full[qt][S::kNB == 2 ? sb : part_i]);
+      }
     }
     if (!ok && lane == 0) report(a.d.err, PKV_DEVERR_TIMEOUT);
     // ---- epilogue: one row per thread ----
