@@ -50,7 +50,10 @@
 namespace pkv {
 namespace {
 
-constexpr float kRescaleThreshold = 8.f;  // log2 units: weights stay below 2^8
+// Log2 units: weights stay below 2^16.  FP32 sums and BF16 weights have the
+// range; a tile of few keys first (sinks) would make a bound of 2^8 rescale
+// now and then (470 cycles each).
+constexpr float kRescaleThreshold = 16.f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRowsPerTile = 128;                          // TMEM lanes
 constexpr int kPosPerTile = kRowsPerTile / kGroup;         // query positions of a row tile: 32
@@ -59,12 +62,10 @@ constexpr int kQHalfBytes = kQTileBytes / 2;
 
 template <int kQTiles>
 struct Shape {
-  static constexpr int kTileBlocks = kQTiles == 1 ? 4 : 8;
-  static constexpr int kTileTokens = kTileBlocks * kBlockSize;
-  static constexpr int kNB = kQTiles == 1 ? 2 : 1;     // S/P buffers per row tile
-  static constexpr int kParts = kQTiles == 1 ? 1 : 2;  // weights are handed over in this many 64-token parts
-  static constexpr int kKStages = 3;
-  static constexpr int kVStages = 2;
+  static constexpr int kTileBlocks = 4;
+  static constexpr int kTileTokens = kTileBlocks * kBlockSize;  // 64
+  static constexpr int kKStages = kQTiles == 1 ? 3 : 5;
+  static constexpr int kVStages = kQTiles == 1 ? 2 : 5;
   static constexpr int kHalfBytes = kTileTokens * 128;
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kWarps = 4 + 4 * kQTiles;
@@ -75,13 +76,13 @@ struct Shape {
   static constexpr int kLaunchRegs = kQTiles == 1 ? 128 : 168;
   static constexpr int kIssueRegs = kQTiles == 1 ? 64 : 80;
   static constexpr int kSoftmaxRegs = kQTiles == 1 ? 192 : 208;
-  static_assert((kIssueRegs + kQTiles * kSoftmaxRegs) * 128 <= kLaunchRegs * (4 + 4 * kQTiles) * 32, "register split");
+  static_assert((kIssueRegs + kQTiles * kSoftmaxRegs) * 128 <= kLaunchRegs * kThreads, "register split");
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kQTiles * kQTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kStageBytes;
   static constexpr int kOffBar = kOffV + kVStages * kStageBytes;
   static constexpr int kSmem = kOffBar + 512;
-  static constexpr uint32_t kColO = kNB * kTileTokens;        // S/P buffers, then O (128 columns)
+  static constexpr uint32_t kColO = 2 * kTileTokens;          // two S/P buffers, then O (128 columns)
   static constexpr uint32_t kTileCols = kColO + kHeadDim;     // 256 columns per row tile
   static constexpr uint32_t kTmemCols = kQTiles * kTileCols;  // 256 or 512
   static constexpr bool kRemainder = kQTiles == 1;
@@ -96,12 +97,13 @@ struct Bars {
   uint64_t k_empty[S::kKStages];
   uint64_t v_full[S::kVStages];
   uint64_t v_empty[S::kVStages];
-  uint64_t s_full[kQTiles][S::kNB];
-  uint64_t p_full[kQTiles][2];  // per S/P buffer, or per part
-  uint64_t o_done[kQTiles][S::kNB];
+  uint64_t s_full[kQTiles][2];
+  uint64_t p_full[kQTiles][2];
+  uint64_t o_done[kQTiles][2];
   uint64_t q_full;
   uint32_t tmem_base;
 };
+static_assert(sizeof(Bars<2>) <= 512, "barrier area");
 
 // Move registers between warpgroups (all warps of one execute it).
 template <int kRegs>
@@ -123,7 +125,6 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
                                                      const MaskedArgs& a) {
   using S = Shape<kQTiles>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(sizeof(Bars<kQTiles>) <= 512, "barrier area");
   Bars<kQTiles>* bars = reinterpret_cast<Bars<kQTiles>*>(smem + S::kOffBar);
   // Warp indexes, tile counts and addresses go through a broadcast so that the
   // compiler knows them to be uniform: the issuing warps' descriptors then
@@ -136,17 +137,17 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kKStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->k_empty[s], kQTiles);
     }
     for (int s = 0; s < S::kVStages; ++s) {
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v_empty[s], kQTiles);
     }
     for (int t = 0; t < kQTiles; ++t)
       for (int s = 0; s < 2; ++s) {
-        if (s < S::kNB) mbar_init(&bars->s_full[t][s], 1);
+        mbar_init(&bars->s_full[t][s], 1);
         mbar_init(&bars->p_full[t][s], 128);
-        if (s < S::kNB) mbar_init(&bars->o_done[t][s], 1);
+        mbar_init(&bars->o_done[t][s], 1);
       }
     mbar_init(&bars->q_full, 128 * kQTiles);
     fence_barrier_init();
@@ -293,19 +294,21 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       // the last tiles' copies must land before shared memory is released
       for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
     }
-   } else if (warp == 1) {
+   } else if (kQTiles == 2 || warp == 1) {
     // ---------------------------- MMA issuer ----------------------------
-    // One warp, a fixed order (the whole warp walks it, lane 0 issues):
-    //   kQTiles 1: S of tile j + 1, then P.V of tile j;
-    //   kQTiles 2: S of row tile 1, P.V of row tile 0, S of row tile 0 for the
-    //     next tile, P.V of row tile 1 -- the row tiles stay half a period
-    //     apart, so that one's softmax runs under the other's products.
+    // One warp per row tile, so that neither tile's products wait for the
+    // other's weights.  The whole warp walks the loop and lane 0 issues.
+    // Per tile: P.V as soon as its weights are there, then S two tiles ahead
+    // (into the buffer that this P.V reads, so after its completion): the
+    // softmax always has a scored tile to go on with.
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
     const uint64_t q_desc = tc::smem_desc(sbase + S::kOffQ, 16, 1024);
     const uint64_t k_desc = tc::smem_desc(sbase + S::kOffK, 16, 1024);
     const uint64_t v_desc = tc::smem_desc(sbase + S::kOffV, S::kHalfBytes, 1024);
     const bool leader = lane == 0;
+    const int t = warp >> 1;  // warp 1 or 3
+    const uint32_t tcol = tmem + t * S::kTileCols;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
@@ -319,9 +322,9 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     auto give_back = [&](uint64_t* bar) {
       if (leader) mbar_arrive(bar);
     };
-    // S of row tile t over the tile in K stage st, into buffer buf
-    auto issue_s = [&](int t, int buf, int st) {
-      const uint32_t d = tmem + t * S::kTileCols + buf * S::kTileTokens;
+    // S of the tile in K stage st, into buffer buf
+    auto issue_s = [&](int buf, int st) {
+      const uint32_t d = tcol + buf * S::kTileTokens;
       const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
       const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
       tc::fence_after_sync();
@@ -334,87 +337,63 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       }
       __syncwarp();
     };
-    // O += P V over the 64 tokens of part `part` of the tile in V stage st
-    auto issue_pv = [&](int t, int buf, int st, int part, bool first) {
-      const uint32_t tcol = tmem + t * S::kTileCols;
-      const uint32_t ptm = tcol + buf * S::kTileTokens + 32 * part;
-      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4) + part * ((4 * 2048) >> 4);
+    // O += P V, P in buffer buf (its BF16 parts, then their remainders), V in stage st
+    auto issue_pv = [&](int buf, int st, bool first) {
+      const uint32_t ptm = tcol + buf * S::kTileTokens;
+      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4);
       tc::fence_after_sync();
       if (leader) {
-        // (P's remainders follow its BF16 parts: column 8 kk, kk 4 .. 7)
 #pragma unroll
         for (int kk = 0; kk < (S::kRemainder ? 8 : 4); ++kk)
           tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + 8 * kk, vd + (kk & 3) * (2048 >> 4), kIdO,
                               (!first || kk > 0) ? 1u : 0u);
-        if (part == S::kParts - 1) tc::commit(&bars->o_done[t][buf]);
+        tc::commit(&bars->o_done[t][buf]);
       }
       __syncwarp();
     };
-    int ks = 0, kph = 0, vs = 0, vph = 0;  // stages and phases of the next S and the next P.V
-    auto next_k = [&]() {
-      if (++ks == S::kKStages) {
-        ks = 0;
-        kph ^= 1;
-      }
-    };
-    auto last = [](int st, int stages) -> int { return st == 0 ? stages - 1 : st - 1; };
-    auto next_v = [&]() {
-      if (++vs == S::kVStages) {
-        vs = 0;
-        vph ^= 1;
-      }
-    };
-    ok = wait(&bars->q_full, 0) && wait(&bars->k_full[0], 0);
-    if (ok) issue_s(0, 0, 0);
-    if constexpr (kQTiles == 1) {
-      for (int j = 0; j < n_tiles && ok; ++j, next_v()) {
-        const bool more = j + 1 < n_tiles;
-        next_k();  // the stage of tile j + 1
-        if (more) {  // its buffer is free once P.V of tile j - 1 is done
-          if (j > 0) {
-            ok = wait2(&bars->k_full[ks], kph, &bars->o_done[0][(j + 1) & 1], ((j - 1) >> 1) & 1);
-            if (ok) give_back(&bars->v_empty[last(vs, S::kVStages)]);
-          } else {
-            ok = wait(&bars->k_full[ks], kph);
-          }
-          if (ok) issue_s(0, (j + 1) & 1, ks);
+    if (t < q_tiles) {
+      int ks = 0, kph = 0;          // stage and phase of the next S
+      int vs = 0, vph = 0, pk = 0;  // of the next P.V, and its tile's K stage
+      auto next_k = [&]() {
+        if (++ks == S::kKStages) {
+          ks = 0;
+          kph ^= 1;
         }
-        ok = ok && wait2(&bars->v_full[vs], vph, &bars->p_full[0][j & 1], (j >> 1) & 1);
-        if (ok) {
-          give_back(&bars->k_empty[last(ks, S::kKStages)]);  // the weights were made from S_j
-          issue_pv(0, j & 1, vs, 0, j == 0);
-        }
-      }
-    } else {
-      const bool two = q_tiles == 2;
-      for (int j = 0; j < n_tiles && ok; ++j, next_v()) {
-        const bool more = j + 1 < n_tiles;
-        if (two) {
-          if (j > 0) {
-            ok = wait(&bars->o_done[1][0], (j - 1) & 1);
-            if (ok) give_back(&bars->v_empty[last(vs, S::kVStages)]);
-          }
-          if (ok) issue_s(1, 0, ks);
-        }
-        ok = ok && wait2(&bars->v_full[vs], vph, &bars->p_full[0][0], j & 1);
-        if (ok && !two) give_back(&bars->k_empty[ks]);
-        if (ok) issue_pv(0, 0, vs, 0, j == 0);
-        ok = ok && wait(&bars->p_full[0][1], j & 1);
-        if (ok) issue_pv(0, 0, vs, 1, false);
-        const int k_now = ks;
+      };
+      ok = wait(&bars->q_full, 0);
+      for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
+        ok = wait(&bars->k_full[ks], kph);
+        if (ok) issue_s(j, ks);
         next_k();
-        if (more) {
-          ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[0][0], j & 1);
-          if (ok && !two) give_back(&bars->v_empty[vs]);
-          if (ok) issue_s(0, 0, ks);
+      }
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const int buf = j & 1, ph = (j >> 1) & 1;
+        ok = wait2(&bars->v_full[vs], vph, &bars->p_full[t][buf], ph);
+        if (ok) {
+          give_back(&bars->k_empty[pk]);  // the weights were made from S_j
+          issue_pv(buf, vs, j == 0);
         }
-        if (two) {
-          ok = ok && wait(&bars->p_full[1][0], j & 1);
-          if (ok) give_back(&bars->k_empty[k_now]);  // both row tiles have their weights
-          if (ok) issue_pv(1, 0, vs, 0, j == 0);
-          ok = ok && wait(&bars->p_full[1][1], j & 1);
-          if (ok) issue_pv(1, 0, vs, 1, false);
+        if (++pk == S::kKStages) pk = 0;
+        if (j + 2 < n_tiles) {
+          ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[t][buf], ph);
+          if (ok) {
+            give_back(&bars->v_empty[vs]);
+            issue_s(buf, ks);
+          }
+          next_k();
         }
+        if (++vs == S::kVStages) {
+          vs = 0;
+          vph ^= 1;
+        }
+      }
+    } else {  // a row tile without queries only gives the stages back
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const int ks = j % S::kKStages, vs = j % S::kVStages;
+        ok = wait(&bars->k_full[ks], (j / S::kKStages) & 1);
+        if (ok) give_back(&bars->k_empty[ks]);
+        ok = ok && wait(&bars->v_full[vs], (j / S::kVStages) & 1);
+        if (ok) give_back(&bars->v_empty[vs]);
       }
     }
     if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
@@ -423,19 +402,21 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   } else {
     // ---------------------------- softmax ----------------------------
     set_max_regs_up<S::kSoftmaxRegs>();
+    const int tid = threadIdx.x & 127;  // within the row tile
     {
       // this row tile's queries -> 128-byte swizzled K-major tile, two 64-dim
-      // halves; thread t loads 16-byte chunk t % 16 of rows t / 16 + 8k
-      const int t = threadIdx.x & 127;
-      const int ch = t & 15;
+      // halves; thread t loads 16-byte chunk t % 16 of every (threads / 16)-th
+      // row, eight loads in flight
+      const int ch = tid & 15;
       const uint16_t* qbase = static_cast<const uint16_t*>(a.d.q);
       uint8_t* qs = smem + S::kOffQ + qt * kQTileBytes;
+      constexpr int kStep = 128 / 16;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int k0 = 0; k0 < kRowsPerTile / kStep; k0 += 8) {
         uint4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int m = (t >> 4) + 8 * (k + 8 * half);
+          const int m = (tid >> 4) + kStep * (k0 + k);
           const int qim = pos0 + qt * kPosPerTile + (m >> 2);
           v[k] = make_uint4(0, 0, 0, 0);
           if (qim < n_new)
@@ -444,7 +425,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int m = (t >> 4) + 8 * (k + 8 * half);
+          const int m = (tid >> 4) + kStep * (k0 + k);
           *reinterpret_cast<uint4*>(qs + (ch >> 3) * kQHalfBytes + tc::sw128_offset(m, (ch & 7) * 8)) = v[k];
         }
       }
@@ -491,156 +472,178 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       return tok + S::kTileTokens - 1 > p_first ||
              !(tok > p_last - a.window || tok + S::kTileTokens <= a.num_sinks);
     };
-    float m_stale = -INFINITY;  // scaled max the weights are taken against (lags the true max by < 2^8)
-    float l = 0.f;              // the row's weight sum
-    for (int j = 0; j < n_tiles && ok && tile_live; ++j) {
-      const int sb = j % S::kNB;
-      const int st = j % S::kVStages;
+    float m_stale = -INFINITY;  // scaled max the weights are taken against (lags the true max by < 2^16)
+    float l = 0.f;              // the sum of the weights
+    for (int j = 0; j < n_tiles && tile_live; ++j) {
+      const int buf = j & 1, ph = (j >> 1) & 1;
       const int tok = tile_token(j);
+      const uint32_t scol = tcol + buf * S::kTileTokens;
       // keep `ok` warp-uniform: the tcgen05 loads below are warp-collective
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[qt][sb], (j / S::kNB) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[qt][buf], ph));
       if (!ok) break;
       const bool part = partial(tok);
-      float s[S::kTileTokens];
+      float s[64];  // raw scores of the tile's tokens
       if (warp_live) {
         tc::fence_after_sync();
-#pragma unroll
-        for (int cc = 0; cc < S::kTileTokens / 32; ++cc) tc::tmem_ld32(tcol + sb * S::kTileTokens + 32 * cc, s + 32 * cc);
+        tc::tmem_ld32(scol, s);
+        tc::tmem_ld32(scol + 32, s + 32);
         tc::tmem_wait_ld();
         if (__builtin_expect(part, 0)) {
+          const uint64_t m = row_valid ? visible(tok, tok < first_block * kBlockSize) : 0ull;
+          const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
 #pragma unroll
-          for (int w = 0; w < S::kTileTokens / 64; ++w) {
-            const uint64_t m = row_valid ? visible(tok + 64 * w, tok < first_block * kBlockSize) : 0ull;
-            const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(lo & (1u << e))) s[64 * w + e] = -INFINITY;
-              if (!(hi & (1u << e))) s[64 * w + 32 + e] = -INFINITY;
-            }
+          for (int e = 0; e < 32; ++e) {
+            if (!(lo & (1u << e))) s[e] = -INFINITY;
+            if (!(hi & (1u << e))) s[32 + e] = -INFINITY;
           }
         }
         float mx;
         {
           float t8[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t8[e] = s[e];
+          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(s[e], s[e + 8]), s[e + 16]);
 #pragma unroll
-          for (int k = 8; k < S::kTileTokens; k += 16)
+          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(t8[e], s[e + 24]), s[e + 32]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              t8[e] = k + 8 < S::kTileTokens ? fmaxf(fmaxf(t8[e], s[k + e]), s[k + 8 + e]) : fmaxf(t8[e], s[k + e]);
-          mx = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7]))) * c;
+          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(t8[e], s[e + 40]), fmaxf(s[e + 48], s[e + 56]));
+          mx = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
         }
+        mx *= c;
         const bool grow = mx > m_stale + kRescaleThreshold;  // also true the first time a row sees a key
         const float m_new = grow ? mx : m_stale;
         const float alpha = grow ? exp2_approx(m_stale - m_new) : 1.f;  // 0 while m_stale is -inf
         if (__builtin_expect(__any_sync(0xffffffffu, grow && j > 0 && m_stale != -INFINITY), 0)) {
           // O holds weights taken against the old maxima: rescale this warp's rows
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(j - 1) % S::kNB], ((j - 1) / S::kNB) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(j - 1) & 1], ((j - 1) >> 1) & 1));
           tc::fence_after_sync();
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
             float o[32];
-            tc::tmem_ld32(tcol + S::kColO + 32 * cc, o);
+            const uint32_t ocol = tcol + S::kColO + 32 * cc;
+            tc::tmem_ld32(ocol, o);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tc::tmem_st32(tcol + S::kColO + 32 * cc, o);
+            tc::tmem_st32(ocol, o);
           }
           tc::tmem_wait_st();
         }
         l *= alpha;
         m_stale = m_new;
       }
-      // V rows that no query of this CTA sees have weight 0 but may hold
-      // anything (slots past the context): zero them
-      if (__builtin_expect(part, 0)) {
-        const bool tail = tok + S::kTileTokens > key_end && key_end > tok && (key_end & (kBlockSize - 1)) != 0;
-        bool head = false;
-        if constexpr (kMask == MaskKind::kWindow)
-          head = tok < first_key && tok + S::kTileTokens > a.num_sinks;
-        if (tail || head) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (j / S::kVStages) & 1));
-          uint8_t* vt = smem + S::kOffV + st * S::kStageBytes;
-          const int t128 = threadIdx.x & 127;
-          for (int idx = t128; idx < S::kTileTokens * 16; idx += 128) {
-            const int tk = idx >> 4, ch = idx & 15, t = tok + tk;
-            bool dead = t >= key_end;
-            if constexpr (kMask == MaskKind::kWindow) dead = dead || (t >= a.num_sinks && t < first_key);
-            if (dead)
-              *reinterpret_cast<uint4*>(vt + (ch >> 3) * S::kHalfBytes + tk * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+      // V rows of the slots past the context (weight 0, but they may hold
+      // anything): zero them
+      if (__builtin_expect(part && ctx > tok && ctx < tok + S::kTileTokens && (ctx & (kBlockSize - 1)) != 0, 0)) {
+        const int st = j % S::kVStages;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (j / S::kVStages) & 1));
+        uint8_t* vt = smem + S::kOffV + st * S::kStageBytes;
+        const int t0 = ctx - tok, t1 = (t0 + kBlockSize - 1) & ~(kBlockSize - 1);
+        for (int idx = tid; idx < (t1 - t0) * 16; idx += 128) {
+          const int tk = t0 + (idx >> 4), ch = idx & 15;
+          *reinterpret_cast<uint4*>(vt + (ch >> 3) * S::kHalfBytes + tk * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
+        tc::fence_proxy_async_smem();  // before the MMA that the weights' arrival lets go
       }
+      if (warp_live) {
+        const float nm = (m_stale == -INFINITY) ? 0.f : -m_stale;
+        const float2 c2 = make_float2(c, c);
+        const float2 nm2 = make_float2(nm, nm);
+        float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // P_j overwrites the S_j buffer it came from, 2 BF16 per 32-bit column
 #pragma unroll
-      for (int part_i = 0; part_i < S::kParts; ++part_i) {
-        if (warp_live) {
-          const float nm = (m_stale == -INFINITY) ? 0.f : -m_stale;
-          const float2 c2 = make_float2(c, c);
-          const float2 nm2 = make_float2(nm, nm);
-          float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // P_j overwrites the S_j buffer it came from, 2 BF16 per 32-bit column
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t pk[16], pr[16];
 #pragma unroll
-          for (int cc = 2 * part_i; cc < 2 * part_i + 2; ++cc) {
-            uint32_t pk[16], pr[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = __ffma2_rn(make_float2(s[32 * cc + 2 * e], s[32 * cc + 2 * e + 1]), c2, nm2);
-              const float p0 = exp2_approx(x.x);
-              const float p1 = exp2_approx(x.y);
-              acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
-              pk[e] = pack_bf16x2(p0, p1);
-              if constexpr (S::kRemainder)
-                pr[e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
-            }
-            tc::tmem_st16u(tcol + sb * S::kTileTokens + 16 * cc, pk);
-            if constexpr (S::kRemainder) tc::tmem_st16u(tcol + sb * S::kTileTokens + S::kTileTokens / 2 + 16 * cc, pr);
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(s[32 * cc + 2 * e], s[32 * cc + 2 * e + 1]), c2, nm2);
+            const float p0 = exp2_approx(x.x);
+            const float p1 = exp2_approx(x.y);
+            acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+            if constexpr (S::kRemainder)
+              pr[e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16), p1 - __uint_as_float(pk[e] & 0xffff0000u));
           }
-          l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
+          tc::tmem_st16u(scol + 16 * cc, pk);
+          if constexpr (S::kRemainder) tc::tmem_st16u(scol + 32 + 16 * cc, pr);
         }
-        tc::tmem_wait_st();
-        tc::fence_proxy_async_smem();  // zeroed V rows, if any, before the PV MMA reads them
-        tc::fence_before_sync();
-        mbar_arrive(&bars->p_full[qt][S::kNB == 2 ? sb : part_i]);
+        l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
       }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(&bars->p_full[qt][buf]);
     }
     if (!ok && lane == 0) report(a.d.err, PKV_DEVERR_TIMEOUT);
-    // ---- epilogue: one row per thread ----
+    // ---- epilogue ----
+    // Results go through the row tile's query area (no product reads it any
+    // more) so that the rows are written as whole 256-byte lines: a thread's
+    // own row in 16-byte pieces costs 32 separate lines an instruction.
     if (ok && tile_live)
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(n_tiles - 1) % S::kNB], ((n_tiles - 1) / S::kNB) & 1));
-    if (tile_live && warp_live && ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1));
+    if (tile_live && warp_live) {
       tc::fence_after_sync();
-      const bool live = row_valid && l > 0.f;
+      const bool live = row_valid && l > 0.f && ok;
       const float inv = live ? 1.f / l : 0.f;
+      uint8_t* stage = smem + S::kOffQ + qt * kQTileBytes + quad * 32 * 256;  // this warp's 32 rows of 256 bytes
+      // 16-byte chunk ch of row m sits at chunk ch ^ (m % 8): four wavefronts either way
+      auto chunk = [&](int m, int ch) -> uint4* { return reinterpret_cast<uint4*>(stage + m * 256 + ((ch ^ (m & 7)) << 4)); };
+      if constexpr (!kSplit) {
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        float o[32];
-        tc::tmem_ld32(tcol + S::kColO + 32 * cc, o);
-        tc::tmem_wait_ld();
-        if (!live) continue;
-        if constexpr (kSplit) {
-          float4* dst = reinterpret_cast<float4*>(a.d.part_o + part_slot() * kHeadDim + 32 * cc);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + out_row() * kHeadDim + 32 * cc);
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tc::tmem_ld32(tcol + S::kColO + 32 * cc, o);
+          tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint4 w;
-            w.x = pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv);
-            w.y = pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
-            w.z = pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
-            w.w = pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
-            dst[e] = w;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live) {
+              w.x = pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv);
+              w.y = pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+              w.z = pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+              w.w = pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+            }
+            *chunk(lane, 4 * cc + e) = w;
           }
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int m = 2 * i + (lane >> 4), ch = lane & 15;
+          const int mq = pos0 + qt * kPosPerTile + ((quad * 32 + m) >> 2);
+          if (mq < a.d.q_len)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) +
+                                     ((static_cast<int64_t>(r) * a.d.q_len + mq) * hq + kvh * kGroup + (m & 3)) * kHeadDim)[ch] =
+                *chunk(m, ch);
+        }
+      } else {
+        // FP32 partials, 64 dims (256 bytes) of each row at a time
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float o[32];
+            tc::tmem_ld32(tcol + S::kColO + 64 * pass + 32 * cc, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(chunk(lane, 8 * cc + e)) =
+                  make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int m = 2 * i + (lane >> 4), ch = lane & 15;
+            const int mq = pos0 + qt * kPosPerTile + ((quad * 32 + m) >> 2);
+            if (mq < n_new) {  // (a row that sees nothing is skipped by the combine kernel)
+              const int64_t orow = (static_cast<int64_t>(r) * a.d.q_len + mq) * hq + kvh * kGroup + (m & 3);
+              *reinterpret_cast<uint4*>(a.d.part_o + (orow * a.d.part_slots + split) * kHeadDim + 64 * pass + 4 * ch) =
+                  *chunk(m, ch);
+            }
+          }
+          if (pass == 0) __syncwarp();
+        }
+        if (in_shape) a.d.part_lse[part_slot()] = live ? (m_stale + log2f(l)) * kLn2 : -INFINITY;
       }
-      if constexpr (kSplit) {
-        if (live) a.d.part_lse[part_slot()] = (m_stale + log2f(l)) * kLn2;
-      }
-      if (in_shape && !live) write_empty();
-    } else if (in_shape && ok) {
+    } else if (in_shape) {
       write_empty();
     }
   }
