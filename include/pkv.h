@@ -622,8 +622,8 @@ pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, co
  *   tree_len     : 1 .. PKV_MAX_TREE_LEN.
  *   scale        : > 0.
  *   kv_blocks_per_split : 0 = pkv_choose_kv_blocks_per_split_tree; otherwise
- *                  rounded up to whole tiles of the kernel (4 or 8 blocks).
- *                  >= max_blocks_per_seq = one pass.
+ *                  rounded up to whole tiles of 4 blocks.  >=
+ *                  max_blocks_per_seq = one pass.  Up to 8 splits merge on chip.
  *   workspace    : device, 256-byte aligned, pkv_workspace_size_tree(...) bytes
  *                  for the same kv_blocks_per_split (may be NULL when 0).
  * The other arguments are those of pkv_paged_attention.  K and V of every

@@ -82,6 +82,11 @@ struct Shape {
   static constexpr int kOffV = kOffK + kKStages * kStageBytes;
   static constexpr int kOffBar = kOffV + kVStages * kStageBytes;
   static constexpr int kSmem = kOffBar + 512;
+  // kCluster: partial O [row][128] FP32 over the K and V rings once they are
+  // drained, then (max, sum) per row
+  static constexpr int kOffPartO = kOffK;
+  static constexpr int kOffPartML = kOffPartO + kQTiles * kRowsPerTile * kHeadDim * 4;
+  static_assert(kOffPartML + kQTiles * kRowsPerTile * 8 <= kOffBar, "the partials fit in the rings");
   static constexpr uint32_t kColO = 2 * kTileTokens;          // two S/P buffers, then O (128 columns)
   static constexpr uint32_t kTileCols = kColO + kHeadDim;     // 256 columns per row tile
   static constexpr uint32_t kTmemCols = kQTiles * kTileCols;  // 256 or 512
@@ -102,8 +107,16 @@ struct Bars {
   uint64_t o_done[kQTiles][2];
   uint64_t q_full;
   uint32_t tmem_base;
+  int32_t request;  // longest_first: the request of this CTA
 };
 static_assert(sizeof(Bars<2>) <= 512, "barrier area");
+
+// How the splits of one (row tile, KV head) come together.
+enum class MaskedMode {
+  kDirect,     // one split: BF16 out
+  kWorkspace,  // FP32 partials to the workspace, merged by the combine kernel
+  kCluster     // one thread-block cluster: merged through distributed shared memory
+};
 
 // Move registers between warpgroups (all warps of one execute it).
 template <int kRegs>
@@ -120,7 +133,7 @@ __device__ __forceinline__ uint64_t low_bits(int x) {
   return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1ull);
 }
 
-template <int kQTiles, MaskKind kMask, bool kSplit>
+template <int kQTiles, MaskKind kMask, MaskedMode kMode>
 __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, const CUtensorMap& v_map,
                                                      const MaskedArgs& a) {
   using S = Shape<kQTiles>;
@@ -169,12 +182,37 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   // ---------------- what this CTA reduces (uniform over the CTA) ----------------
   constexpr int kPos = kPosPerTile * kQTiles;  // query positions per CTA
   const int n_rt = (a.d.q_len + kPos - 1) / kPos;
-  const int r = blockIdx.x / n_rt;
+  // grid x: request (or its place by length), KV head, row tile (fastest)
+  int r = blockIdx.x / n_rt;
   const int pos0 = (blockIdx.x - r * n_rt) * kPos;  // first query index of this CTA
+  const int kvh = r % a.d.num_kv_heads;
+  r /= a.d.num_kv_heads;
   const int split = blockIdx.y;
-  const int kvh = blockIdx.z;
+  if (a.longest_first) {
+    // More CTAs than fit at once: the requests with the most to read start
+    // first, so that none of them is left for the end.  Place r = the number
+    // of requests that come before it.
+    int32_t* len = reinterpret_cast<int32_t*>(smem + S::kOffQ);  // [num_seqs], before the queries come here
+    for (int i = threadIdx.x; i < a.d.num_seqs; i += S::kThreads) len[i] = min(a.d.context_lens[i], a.span);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.d.num_seqs; i += S::kThreads) {
+      const int mine = len[i];
+      int before = 0;
+      for (int k = 0; k < a.d.num_seqs; ++k) before += (len[k] > mine || (len[k] == mine && k < i)) ? 1 : 0;
+      if (before == r) bars->request = i;
+    }
+    __syncthreads();
+    r = bars->request;
+  }
+  r = uniform(r);
   const int hq = a.d.num_kv_heads * kGroup;
   const int cap = a.d.max_blocks * kBlockSize;
+  // The first block ids, read before the context length is known (ids past
+  // the range are dropped below): one trip less before the first copies.
+  int first_ids = 0;
+  if (kMask == MaskKind::kTree && (warp == 0 || warp == 2))
+    first_ids = a.d.block_tables[static_cast<int64_t>(r) * a.d.max_blocks +
+                                 min(split * a.tiles_per_split * S::kTileBlocks + lane, a.d.max_blocks - 1)];
   int ctx = a.d.context_lens[r];
   int n_new = a.d.q_len;  // queries of this request
   if constexpr (kMask == MaskKind::kTree) {
@@ -228,10 +266,13 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   const uint32_t sbase = uniform(smem_addr(smem));
   bool ok = true;
 
+  float2* part_ml = reinterpret_cast<float2*>(smem + S::kOffPartML);
   // zeros for a row without a result (padding, or nothing visible)
   auto write_empty = [&]() {
-    if constexpr (kSplit) {
+    if constexpr (kMode == MaskedMode::kWorkspace) {
       a.d.part_lse[part_slot()] = -INFINITY;
+    } else if constexpr (kMode == MaskedMode::kCluster) {
+      part_ml[qt * kRowsPerTile + row] = make_float2(-INFINITY, 0.f);
     } else {
       uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + out_row() * kHeadDim);
 #pragma unroll
@@ -259,6 +300,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     // its block id, or INT_MIN for a hole or past the range
     auto entry = [&](int i) -> int {
       if (i >= n_tiles * S::kTileBlocks) return INT_MIN;
+      if (kMask == MaskKind::kTree && i < 32)  // read above
+        return t_first * S::kTileBlocks + i < end_block ? first_ids : INT_MIN;
       i += t_first * S::kTileBlocks;
       const int sink_entries = sink_tiles * S::kTileBlocks;
       const int lb = i < sink_entries ? (i < sink_blocks ? i : INT_MAX) : first_block + i - sink_entries;
@@ -579,14 +622,33 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     // own row in 16-byte pieces costs 32 separate lines an instruction.
     if (ok && tile_live)
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1));
+    if constexpr (kMode == MaskedMode::kCluster) {
+      // the partials go over the rings: no row tile's products may still read them
+      if constexpr (kQTiles == 2) named_barrier_sync(1, 128 * kQTiles);
+    }
     if (tile_live && warp_live) {
       tc::fence_after_sync();
-      const bool live = row_valid && l > 0.f && ok;
+      const bool live = row_valid && l != 0.f && ok;  // (a NaN sum stays one)
       const float inv = live ? 1.f / l : 0.f;
       uint8_t* stage = smem + S::kOffQ + qt * kQTileBytes + quad * 32 * 256;  // this warp's 32 rows of 256 bytes
       // 16-byte chunk ch of row m sits at chunk ch ^ (m % 8): four wavefronts either way
       auto chunk = [&](int m, int ch) -> uint4* { return reinterpret_cast<uint4*>(stage + m * 256 + ((ch ^ (m & 7)) << 4)); };
-      if constexpr (!kSplit) {
+      if constexpr (kMode == MaskedMode::kCluster) {
+        // un-normalised FP32 row, 16-byte chunk ch at ch ^ (row % 8)
+        const int m = qt * kRowsPerTile + row;
+        uint8_t* po = smem + S::kOffPartO + m * kHeadDim * 4;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tc::tmem_ld32(tcol + S::kColO + 32 * cc, o);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(po + (((8 * cc + e) ^ (row & 7)) << 4)) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        part_ml[m] = live ? make_float2(m_stale, l) : make_float2(-INFINITY, 0.f);
+      } else if constexpr (kMode == MaskedMode::kDirect) {
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           float o[32];
@@ -654,16 +716,62 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, S::kTmemCols);
   }
+
+  if constexpr (kMode == MaskedMode::kCluster) {
+    // Each CTA merges its share of the rows (one per warp at a time, 4 dims a
+    // lane) from every split's partial: O = sum_s 2^(m_s - m) O_s / sum_s
+    // 2^(m_s - m) l_s.
+    cluster_sync_all();
+    const uint32_t splits = gridDim.y, rank = cluster_cta_rank();
+    const int rows = min(kPos, a.d.q_len - pos0) * kGroup;  // rows of the shape, padding included
+    for (int m = static_cast<int>(rank) * S::kWarps + warp; m < rows; m += static_cast<int>(splits) * S::kWarps) {
+      float ms[kMaxClusterSplits], ls[kMaxClusterSplits];
+      float4 os[kMaxClusterSplits];
+#pragma unroll
+      for (int k = 0; k < kMaxClusterSplits; ++k) {
+        ms[k] = -INFINITY;
+        ls[k] = 0.f;
+        if (k < static_cast<int>(splits)) {
+          const uint32_t ml = map_shared_to_rank(part_ml + m, k);
+          ms[k] = ld_cluster_f32(ml);
+          ls[k] = ld_cluster_f32(ml + 4);
+          os[k] = ld_cluster_f32x4(map_shared_to_rank(smem + S::kOffPartO + m * kHeadDim * 4 + ((lane ^ (m & 7)) << 4), k));
+        }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kMaxClusterSplits; ++k) mx = fmaxf(mx, ms[k]);
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxClusterSplits; ++k) {
+        if (ms[k] == -INFINITY) continue;  // saw nothing: its O holds anything
+        const float w = exp2_approx(ms[k] - mx);
+        sum = fmaf(ls[k], w, sum);
+        o.x = fmaf(os[k].x, w, o.x);
+        o.y = fmaf(os[k].y, w, o.y);
+        o.z = fmaf(os[k].z, w, o.z);
+        o.w = fmaf(os[k].w, w, o.w);
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      uint2 packed;
+      packed.x = pack_bf16x2(o.x * inv, o.y * inv);
+      packed.y = pack_bf16x2(o.z * inv, o.w * inv);
+      const int64_t mrow = (static_cast<int64_t>(r) * a.d.q_len + pos0 + (m >> 2)) * hq + kvh * kGroup + (m & 3);
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.d.out) + mrow * kHeadDim)[lane] = packed;
+    }
+    cluster_sync_all();  // a partial stays until every CTA has read it
+  }
 }
 
-template <int kQTiles, MaskKind kMask, bool kSplit>
+template <int kQTiles, MaskKind kMask, MaskedMode kMode>
 __global__ void __launch_bounds__(Shape<kQTiles>::kThreads, Shape<kQTiles>::kCtasPerSm)
     paged_masked_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                            const MaskedArgs a) {
-  paged_masked_tc_body<kQTiles, kMask, kSplit>(k_map, v_map, a);
+  paged_masked_tc_body<kQTiles, kMask, kMode>(k_map, v_map, a);
 }
 
-template <int kQTiles, MaskKind kMask, bool kSplit>
+template <int kQTiles, MaskKind kMask, MaskedMode kMode>
 cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a,
                            cudaStream_t stream) {
   using S = Shape<kQTiles>;
@@ -672,28 +780,32 @@ cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, con
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = paged_masked_tc_kernel<kQTiles, kMask, kSplit>;
+  auto kernel = paged_masked_tc_kernel<kQTiles, kMask, kMode>;
   if (!done[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   constexpr int kPos = kPosPerTile * kQTiles;
-  const int64_t x = static_cast<int64_t>(a.d.num_seqs) * ((a.d.q_len + kPos - 1) / kPos);
-  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.d.num_splits),
-                  static_cast<unsigned>(a.d.num_kv_heads));
-  return launch_pdl(kernel, grid, dim3(S::kThreads), S::kSmem, stream, 1, kmap, vmap, a);
+  const int64_t x = static_cast<int64_t>(a.d.num_seqs) * a.d.num_kv_heads * ((a.d.q_len + kPos - 1) / kPos);
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.d.num_splits));
+  return launch_pdl(kernel, grid, dim3(S::kThreads), S::kSmem, stream,
+                    kMode == MaskedMode::kCluster ? static_cast<unsigned>(a.d.num_splits) : 1u, kmap, vmap, a);
+}
+
+template <int kQTiles, MaskKind kMask>
+cudaError_t launch_mask(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a, cudaStream_t stream) {
+  if (a.d.num_splits == 1) return launch_variant<kQTiles, kMask, MaskedMode::kDirect>(kmap, vmap, a, stream);
+  if (a.d.part_o != nullptr) return launch_variant<kQTiles, kMask, MaskedMode::kWorkspace>(kmap, vmap, a, stream);
+  if (a.d.num_splits > kMaxClusterSplits) return cudaErrorInvalidValue;
+  return launch_variant<kQTiles, kMask, MaskedMode::kCluster>(kmap, vmap, a, stream);
 }
 
 template <int kQTiles>
 cudaError_t launch_shape(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a, MaskKind mask,
                          cudaStream_t stream) {
-  const bool split = a.d.part_o != nullptr;
-  if (mask == MaskKind::kTree)
-    return split ? launch_variant<kQTiles, MaskKind::kTree, true>(kmap, vmap, a, stream)
-                 : launch_variant<kQTiles, MaskKind::kTree, false>(kmap, vmap, a, stream);
-  return split ? launch_variant<kQTiles, MaskKind::kWindow, true>(kmap, vmap, a, stream)
-               : launch_variant<kQTiles, MaskKind::kWindow, false>(kmap, vmap, a, stream);
+  return mask == MaskKind::kTree ? launch_mask<kQTiles, MaskKind::kTree>(kmap, vmap, a, stream)
+                                 : launch_mask<kQTiles, MaskKind::kWindow>(kmap, vmap, a, stream);
 }
 
 }  // namespace

@@ -923,8 +923,10 @@ int32_t masked_max_tiles(int32_t q_len, int32_t max_blocks, int32_t window, int3
 }
 
 // Splits only when the row tiles leave at least half of the resident CTAs
-// unused, and of at least 256 tokens.
-constexpr int32_t kMaskedMinSplitTokens = 256;
+// unused.  Up to kMaxClusterSplits splits merge in a cluster; more go through
+// the workspace and the combine kernel, whose launch and traffic cost about as
+// much as kCombineTiles tiles of work.
+constexpr int32_t kCombineTiles = 5;
 
 MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t window,
                        int32_t num_sinks, int32_t kv_blocks_per_split, int32_t sm_count) {
@@ -940,9 +942,10 @@ MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, in
     const int64_t slots = static_cast<int64_t>(masked_ctas_per_sm(q_len)) * (sm_count > 0 ? sm_count : device_sm_count());
     const int64_t splits = ctas > 0 ? slots / ctas : 1;
     if (splits > 1) {
-      const int32_t least = kMaskedMinSplitTokens / (tb * kBlockSize);
-      p.tiles_per_split = static_cast<int32_t>((p.tiles + splits - 1) / splits);
-      if (p.tiles_per_split < least) p.tiles_per_split = least;
+      const int32_t in_cluster = static_cast<int32_t>(splits < kMaxClusterSplits ? splits : kMaxClusterSplits);
+      const int32_t near = (p.tiles + in_cluster - 1) / in_cluster;
+      const int32_t far = static_cast<int32_t>((p.tiles + splits - 1) / splits);
+      p.tiles_per_split = far + kCombineTiles < near ? far : near;
     }
   }
   if (p.tiles_per_split > p.tiles) p.tiles_per_split = p.tiles;
@@ -951,7 +954,7 @@ MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, in
 }
 
 size_t masked_workspace(int64_t rows, int32_t splits) {
-  if (splits <= 1) return 0;
+  if (splits <= kMaxClusterSplits) return 0;
   const size_t n = static_cast<size_t>(rows) * splits;
   return align_up(n * kHeadDim * sizeof(float), 256) + align_up(n * sizeof(float), 256);
 }
@@ -1017,9 +1020,18 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
   a.d.num_splits = plan.splits;
   a.d.scale_log2 = scale * 1.4426950408889634f;
   a.d.part_slots = plan.splits;
+  // more CTAs than are resident at once: longest requests first
+  const int32_t pos = masked_positions_per_cta(q_len);
+  const int64_t ctas = static_cast<int64_t>(num_seqs) * cache->num_kv_heads * ((q_len + pos - 1) / pos);
+  if (ctas > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  a.longest_first = num_seqs <= kMaxRanked && plan.splits == 1 &&
+                    ctas > static_cast<int64_t>(masked_ctas_per_sm(q_len)) * device_sm_count();
+  const int64_t span = tree ? int64_t{0x7fffffff} : static_cast<int64_t>(a.window) + q_len + a.num_sinks;
+  a.span = static_cast<int32_t>(span < 0x7fffffff ? span : 0x7fffffff);
   const int64_t rows = static_cast<int64_t>(num_seqs) * q_len * num_q_heads;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (plan.splits > 1) {
+  const bool combine = plan.splits > kMaxClusterSplits;
+  if (combine) {
     if (workspace == nullptr || workspace_bytes < masked_workspace(rows, plan.splits)) return PKV_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
     a.d.part_o = static_cast<float*>(workspace);
@@ -1028,7 +1040,7 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
         align_up(static_cast<size_t>(rows) * plan.splits * kHeadDim * sizeof(float), 256));
   }
   if (launch_paged_masked_tc(a, mask, s) != cudaSuccess) return PKV_ERR_CUDA;
-  if (plan.splits > 1 && launch_attn_combine(out, nullptr, a.d.part_o, a.d.part_lse, static_cast<int32_t>(rows),
+  if (combine && launch_attn_combine(out, nullptr, a.d.part_o, a.d.part_lse, static_cast<int32_t>(rows),
                                              plan.splits, s) != cudaSuccess)
     return PKV_ERR_CUDA;
   return PKV_OK;

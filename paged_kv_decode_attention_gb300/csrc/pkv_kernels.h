@@ -137,9 +137,10 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int32_t grid, cudaStream
 
 // Attention of several query positions per request under a tree or window
 // mask (paged_masked_tc.cu).  d.q_len = query positions per request (the
-// padded tree size); d.num_splits > 1 or d.part_o set = partials to the
-// workspace for the combine kernel.  A split is tiles_per_split tiles of
-// masked_tile_blocks(q_len) blocks of the list of blocks a CTA reads.
+// padded tree size).  A split is tiles_per_split tiles of
+// masked_tile_blocks(q_len) blocks of the list of blocks a CTA reads; more
+// than one split: partials to the workspace for the combine kernel when
+// d.part_o is set, else (<= kMaxClusterSplits) merged in a cluster.
 enum class MaskKind { kTree, kWindow };
 struct MaskedArgs {
   DecodeArgs d;
@@ -149,7 +150,10 @@ struct MaskedArgs {
   int32_t window;             // window: keys p - window + 1 .. p, and
   int32_t num_sinks;          //         keys 0 .. num_sinks - 1
   int32_t tiles_per_split;
+  int32_t longest_first;      // CTAs in the order of min(context, span), longest first (num_seqs <= kMaxRanked)
+  int32_t span;
 };
+constexpr int kMaxRanked = 1024;
 cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream);
 int masked_tile_blocks(int q_len);
 int masked_positions_per_cta(int q_len);

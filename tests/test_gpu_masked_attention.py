@@ -98,6 +98,22 @@ def test_tree_masks_of_any_kind(width):
     check_tree(ctx, lens, width, seed=11, rows=rows)
 
 
+@pytest.mark.parametrize("width", [5, 40])
+def test_more_requests_than_fit_at_once(width):
+    """Row tiles beyond one wave, which start in the order of their lengths: zero, equal and different ones."""
+    rng = np.random.default_rng(width)
+    ctx = [width + int(c) for c in rng.integers(0, 300, 75)]
+    ctx[3] = ctx[4] = ctx[70] = 900
+    ctx[10] = ctx[20] = 0
+    lens = [min(c, int(n)) for c, n in zip(ctx, rng.integers(0, width + 1, 75))]
+    check_tree(ctx, lens, width, hkv=8, seed=width)
+    window, sinks = 100, 3
+    d = _cuda(V.paged_case(ctx, width, 8, 5, hold=V.window_hold(ctx, width, window, sinks)))
+    out = run_window(d, window, sinks)
+    ref, tol = V.attention64(d, V.window_allowed(ctx, width, window, sinks))
+    V.assert_within(out, ref, tol, "window")
+
+
 def test_tree_longer_than_its_context():
     """Drafts whose place lies before the first token have no key."""
     width = 20

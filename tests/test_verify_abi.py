@@ -100,8 +100,10 @@ def test_splits_and_workspaces_are_host_arithmetic():
     splits = -(-528 // bps)
     rows = 16 * 32
     assert pkv.workspace_size_tree(1, 16, 32, 528, bps) == rows * splits * 512 + -(-rows * splits * 4 // 256) * 256
-    # wide trees read 8-block tiles
-    assert pkv.choose_kv_blocks_per_split_tree(1, 8, 64, 528, 152) % 8 == 0
+    assert pkv.choose_kv_blocks_per_split_tree(1, 8, 64, 528, 152) % 4 == 0
+    # up to 8 splits merge on chip
+    assert pkv.workspace_size_tree(1, 16, 32, 528, 528 // 8) == 0
+    assert pkv.workspace_size_tree(1, 16, 32, 528, 56) > 0
     # a window reads its own span, however long the table
     a = pkv.workspace_size_window(1, 1, 32, 1 << 20, 1000, 4)
     assert a == pkv.workspace_size_window(1, 1, 32, 1 << 24, 1000, 4) and a < 1 << 21
