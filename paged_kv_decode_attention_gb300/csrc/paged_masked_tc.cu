@@ -482,8 +482,15 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     const bool warp_live = pos0 + qt * kPosPerTile + quad * 8 < n_new;  // some row of the warp has a query
     // the keys a row sees in [tok, tok + 64), one bit per key
     const uint64_t* mrow = nullptr;
-    if constexpr (kMask == MaskKind::kTree)
+    uint64_t mask0 = 0, mask1 = 0;  // its first words, read before they are needed
+    if constexpr (kMask == MaskKind::kTree) {
       mrow = a.tree_mask + (static_cast<int64_t>(r) * a.d.q_len + (row_valid ? qi : 0)) * a.mask_words;
+      mask0 = mrow[0];
+      if (a.mask_words > 1) mask1 = mrow[1];
+    }
+    auto mask_word = [&](int w) -> uint64_t {
+      return w >= a.mask_words ? 0ull : (w == 0 ? mask0 : (w == 1 ? mask1 : mrow[w]));
+    };
     // (in_sinks: the range belongs to a tile of sink blocks, whose places past
     // them are holes: the window's keys are read by the tiles after it)
     auto visible = [&](int tok, bool in_sinks) -> uint64_t {
@@ -493,11 +500,11 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         if (d < 64) {
           const int o = -d;  // draft at bit 0 (negative: drafts start at bit d)
           if (o < 0) {
-            m |= mrow[0] << d;
+            m |= mask0 << d;
           } else {
             const int w = o >> 6, sh = o & 63;
-            if (w < a.mask_words) m |= mrow[w] >> sh;
-            if (sh != 0 && w + 1 < a.mask_words) m |= mrow[w + 1] << (64 - sh);
+            m |= mask_word(w) >> sh;
+            if (sh != 0) m |= mask_word(w + 1) << (64 - sh);
           }
         }
         return m & low_bits(key_end - tok);

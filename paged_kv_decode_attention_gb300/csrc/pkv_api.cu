@@ -1020,11 +1020,12 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
   a.d.num_splits = plan.splits;
   a.d.scale_log2 = scale * 1.4426950408889634f;
   a.d.part_slots = plan.splits;
-  // more CTAs than are resident at once: longest requests first
+  // more CTAs than are resident at once: longest requests first (row tiles of
+  // one request all read about as much: with several, their order stays)
   const int32_t pos = masked_positions_per_cta(q_len);
   const int64_t ctas = static_cast<int64_t>(num_seqs) * cache->num_kv_heads * ((q_len + pos - 1) / pos);
   if (ctas > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
-  a.longest_first = num_seqs <= kMaxRanked && plan.splits == 1 &&
+  a.longest_first = q_len <= pos && num_seqs <= kMaxRanked && plan.splits == 1 &&
                     ctas > static_cast<int64_t>(masked_ctas_per_sm(q_len)) * device_sm_count();
   const int64_t span = tree ? int64_t{0x7fffffff} : static_cast<int64_t>(a.window) + q_len + a.num_sinks;
   a.span = static_cast<int32_t>(span < 0x7fffffff ? span : 0x7fffffff);
