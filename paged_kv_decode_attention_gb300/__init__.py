@@ -13,6 +13,8 @@ torch.bfloat16 (or int16/uint16 holding BF16 bit patterns).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -183,6 +185,18 @@ def _load():
 
 
 _lib, _path = _load()
+
+
+def _load_binding():
+    """The C++ entry points (csrc/py_binding.cpp) of the calls that serve single tokens."""
+    loader = importlib.machinery.ExtensionFileLoader("_pkv_binding", _build.BINDING)
+    spec = importlib.util.spec_from_file_location("_pkv_binding", _build.BINDING, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    return module
+
+
+_binding = _load_binding()
 
 
 def library_path() -> str:
@@ -707,60 +721,14 @@ def copy_blocks_fp8_e4m3(k_cache: torch.Tensor, v_cache: torch.Tensor, src_block
 # ---------------------------------------------------------------------------
 MAX_TREE_LEN = 1024
 
-_BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
-_I32_ONLY = (torch.int32,)
-_I64_ONLY = (torch.int64,)
-_MASK_WORDS = (torch.int64, torch.uint64)
+
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _on_device(dev: int, t: torch.Tensor, name: str, dtypes) -> int:
-    """Address of a contiguous tensor of one of `dtypes` on CUDA device `dev`."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must hold {dtypes[0]} values, got {t.dtype}")
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on the current CUDA device")
-    return t.data_ptr()
-
-
-def _workspace(dev: int, t) -> tuple:
-    if t is None:
-        return 0, 0
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _pool(dev: int, t: torch.Tensor, name: str, kv_format: int) -> tuple:
-    """(address, CacheDesc) of one pool of the given format."""
-    if kv_format == KV_BF16:
-        addr = _on_device(dev, t, name, _BF16_LIKE)
-        shape = t.shape
-        if len(shape) != 4:
-            raise ValueError(f"{name} must be [num_blocks][num_kv_heads][16][128]")
-        return addr, CacheDesc(shape[0], shape[2], shape[1], shape[3])
-    addr = _on_device(dev, t, name, (torch.uint8, torch.int8))
-    shape = t.shape
-    if kv_format == KV_Q8_0:
-        if len(shape) != 3 or shape[2] != Q8_TILE_BYTES:
-            raise ValueError(f"{name} must be [num_blocks][num_kv_heads][{Q8_TILE_BYTES}]")
-    elif kv_format == KV_FP8_E4M3:
-        if len(shape) != 4 or shape[2] != BLOCK_SIZE or shape[3] != HEAD_DIM:
-            raise ValueError(f"{name} must be [num_blocks][num_kv_heads][16][128]")
-    else:
-        raise ValueError(f"unknown kv_format {kv_format}")
-    return addr, CacheDesc(shape[0], BLOCK_SIZE, shape[1], HEAD_DIM)
-
-
-def _heads(dev: int, t: torch.Tensor, name: str, tokens: int, heads: int) -> tuple:
-    """(address, token stride) of BF16 [tokens][heads][128] whose heads are contiguous."""
-    if t.dtype not in _BF16_LIKE:
-        raise TypeError(f"{name} must hold BF16 values, got {t.dtype}")
-    if t.get_device() != dev or t.dim() != 3 or tuple(t.shape) != (tokens, heads, HEAD_DIM):
-        raise ValueError(f"{name} must be [num_tokens][{heads}][{HEAD_DIM}] on the current CUDA device")
-    st, sh, sd = t.stride()
-    if tokens > 0 and (sd != 1 or (heads > 1 and sh != HEAD_DIM)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (st if tokens > 1 else heads * HEAD_DIM)
+def _done(status: int, where: str) -> None:
+    if status:
+        raise PkvError(status, where)
 
 
 def qk_norm_rope_append(q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -774,39 +742,9 @@ def qk_norm_rope_append(q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     contiguous); q_out [T][Hq][128]; slot_mapping int64 [T] (< 0: not stored); positions int32 [T]; rope_table
     float32 [max_positions][rot_dim], cosines then sines (None: no rotation); q_weight, k_weight BF16 [128]
     (None: no norm); pools of `kv_format`.  See include/pkv.h."""
-    dev = torch.cuda.current_device()
-    kc, desc = _pool(dev, k_cache, "k_cache", kv_format)
-    vc, _ = _pool(dev, v_cache, "v_cache", kv_format)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    slots = _on_device(dev, slot_mapping, "slot_mapping", _I64_ONLY)
-    tokens, hkv = slot_mapping.numel(), desc.num_kv_heads
-    hq = q.shape[1] if q.dim() == 3 else 0
-    qa, qs = _heads(dev, q, "q", tokens, hq)
-    ka, ks = _heads(dev, k, "k", tokens, hkv)
-    va, vs = _heads(dev, v, "v", tokens, hkv)
-    out = _on_device(dev, q_out, "q_out", _BF16_LIKE)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out and q differ in shape")
-    qw = kw = 0
-    if q_weight is not None:
-        qw = _on_device(dev, q_weight, "q_weight", _BF16_LIKE)
-    if k_weight is not None:
-        kw = _on_device(dev, k_weight, "k_weight", _BF16_LIKE)
-    if (qw and q_weight.numel() != HEAD_DIM) or (kw and k_weight.numel() != HEAD_DIM):
-        raise ValueError("q_weight and k_weight must have 128 values")
-    table = pos = rows = rot = 0
-    if rope_table is not None:
-        table = _on_device(dev, rope_table, "rope_table", (torch.float32,))
-        if rope_table.dim() != 2 or positions is None:
-            raise ValueError("rope_table must be [max_positions][rot_dim], with positions beside it")
-        rows, rot = rope_table.shape
-        pos = _on_device(dev, positions, "positions", _I32_ONLY)
-        if positions.numel() != tokens:
-            raise ValueError("positions must have one entry per token")
-    _check(_lib.pkv_qk_norm_rope_append(out, kc, vc, desc, kv_format, slots, qa, qs, ka, ks, va, vs, hq, qw, kw, eps,
-                                        table, rows, rot, 1 if interleaved else 0, pos, tokens, _stream_ptr(stream)),
-           "pkv_qk_norm_rope_append")
+    _done(_binding.qk_norm_rope_append(q_out, kv_format, k_cache, v_cache, slot_mapping, q, k, v, positions,
+                                       rope_table, q_weight, k_weight, eps, interleaved, _raw(stream)),
+          "pkv_qk_norm_rope_append")
 
 
 def choose_kv_blocks_per_split_tree(num_seqs: int, num_kv_heads: int, tree_len: int, max_blocks_per_seq: int,
@@ -834,24 +772,6 @@ def workspace_size_window(num_seqs: int, q_len: int, num_q_heads: int, max_block
                                               kv_blocks_per_split))
 
 
-def _masked_args(out, q, k_cache, v_cache, block_tables, context_lens, workspace):
-    dev = torch.cuda.current_device()
-    kc, desc = _pool(dev, k_cache, "k_cache", KV_BF16)
-    vc = _on_device(dev, v_cache, "v_cache", _BF16_LIKE)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    bt = _on_device(dev, block_tables, "block_tables", _I32_ONLY)
-    cl = _on_device(dev, context_lens, "context_lens", _I32_ONLY)
-    o, qa = _on_device(dev, out, "out", _BF16_LIKE), _on_device(dev, q, "q", _BF16_LIKE)
-    b, shape = context_lens.numel(), q.shape
-    if len(shape) != 4 or shape[0] != b or shape[3] != HEAD_DIM or out.shape != shape:
-        raise ValueError("q/out must be [num_seqs][query tokens][num_q_heads][128]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != b:
-        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
-    ws, ws_bytes = _workspace(dev, workspace)
-    return dev, o, qa, kc, vc, desc, bt, block_tables.shape[1], cl, b, shape[1], shape[2], ws, ws_bytes
-
-
 def paged_attention_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                          block_tables: torch.Tensor, context_lens: torch.Tensor, tree_mask: torch.Tensor,
                          scale: float, tree_lens: torch.Tensor | None = None, kv_blocks_per_split: int = 0,
@@ -861,19 +781,9 @@ def paged_attention_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
 
     q, out [B][tree_len][Hq][128]; tree_mask int64 or uint64 [B][tree_len][ceil(tree_len/64)], bit j = draft j is
     visible; workspace >= workspace_size_tree(...) bytes.  Rows past tree_lens[r] get zeros."""
-    dev, o, qa, kc, vc, desc, bt, maxb, cl, b, n, hq, ws, wsb = _masked_args(out, q, k_cache, v_cache, block_tables,
-                                                                              context_lens, workspace)
-    mask = _on_device(dev, tree_mask, "tree_mask", _MASK_WORDS)
-    if tuple(tree_mask.shape) != (b, n, (n + 63) // 64):
-        raise ValueError("tree_mask must be [num_seqs][tree_len][ceil(tree_len / 64)]")
-    tl = 0
-    if tree_lens is not None:
-        tl = _on_device(dev, tree_lens, "tree_lens", _I32_ONLY)
-        if tree_lens.numel() != b:
-            raise ValueError("tree_lens must have one entry per request")
-    _check(_lib.pkv_paged_attention_tree(o, qa, kc, vc, desc, bt, maxb, cl, tl, mask, b, n, hq, scale,
-                                         kv_blocks_per_split, ws, wsb, _stream_ptr(stream)),
-           "pkv_paged_attention_tree")
+    _done(_binding.paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, tree_lens,
+                                        scale, kv_blocks_per_split, workspace, _raw(stream)),
+          "pkv_paged_attention_tree")
 
 
 def paged_attention_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -882,61 +792,51 @@ def paged_attention_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                            workspace: torch.Tensor | None = None, stream=None) -> None:
     """paged_attention with a sliding window: the query at position p sees the keys t <= p with t > p - window or
     t < num_sinks.  Blocks no query sees are not looked up.  workspace >= workspace_size_window(...) bytes."""
-    _, o, qa, kc, vc, desc, bt, maxb, cl, b, n, hq, ws, wsb = _masked_args(out, q, k_cache, v_cache, block_tables,
-                                                                            context_lens, workspace)
-    if n != q_len:
-        raise ValueError("q/out must be [num_seqs][q_len][num_q_heads][128]")
-    _check(_lib.pkv_paged_attention_window(o, qa, kc, vc, desc, bt, maxb, cl, b, n, hq, window, num_sinks, scale,
-                                           kv_blocks_per_split, ws, wsb, _stream_ptr(stream)),
-           "pkv_paged_attention_window")
+    _done(_binding.paged_attention_window(out, q, k_cache, v_cache, block_tables, context_lens, q_len, window,
+                                          num_sinks, scale, kv_blocks_per_split, workspace, _raw(stream)),
+          "pkv_paged_attention_window")
 
 
 class KvPools:
-    """The K and V pools of a model's layers (tensors of `kv_format`, one shape), checked once, for the calls
-    that work on all layers."""
+    """The K and V pools of a model's layers (distinct tensors of `kv_format`, one shape), checked once, for the
+    calls that work on all layers."""
 
     def __init__(self, k_caches, v_caches, kv_format: int = KV_BF16):
         n = len(k_caches)
         if n == 0 or len(v_caches) != n:
             raise ValueError("one K and one V pool per layer are required")
+        if kv_format not in (KV_BF16, KV_Q8_0, KV_FP8_E4M3):
+            raise ValueError(f"unknown kv_format {kv_format}")
         self.tensors = list(k_caches) + list(v_caches)
-        self.device = self.tensors[0].get_device()
         self.kv_format, self.num_layers = kv_format, n
-        addrs = []
+        first = self.tensors[0]
+        self.device = first.get_device()
         for i, t in enumerate(self.tensors):
-            addr, self.desc = _pool(self.device, t, f"pool {i}", kv_format)
-            if t.shape != self.tensors[0].shape:
-                raise ValueError("the layers' pools differ in shape")
-            addrs.append(addr)
-        if self.device < 0 or len(set(addrs)) != len(addrs):
-            raise ValueError("the pools must be distinct CUDA tensors")
-        self.k_array, self.v_array = (ctypes.c_void_p * n)(*addrs[:n]), (ctypes.c_void_p * n)(*addrs[n:])
+            if kv_format == KV_BF16:
+                _bf16(t, f"pool {i}")
+                ok = t.dim() == 4 and tuple(t.shape[2:]) == (BLOCK_SIZE, HEAD_DIM)
+            elif t.dtype not in (torch.uint8, torch.int8) or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"pool {i} must be a contiguous CUDA uint8 tensor")
+            elif kv_format == KV_Q8_0:
+                ok = t.dim() == 3 and t.shape[2] == Q8_TILE_BYTES
+            else:
+                ok = t.dim() == 4 and tuple(t.shape[2:]) == (BLOCK_SIZE, HEAD_DIM)
+            if not ok or t.shape != first.shape or t.get_device() != self.device:
+                raise ValueError(f"pool {i}: the layers' pools must have the format's shape, on one device")
+        addrs = [t.data_ptr() for t in self.tensors]
+        if len(set(addrs)) != len(addrs):
+            raise ValueError("the layers' pools must be distinct")
+        self._arrays = [(ctypes.c_void_p * n)(*addrs[:n]), (ctypes.c_void_p * n)(*addrs[n:])]
+        self._args = (ctypes.addressof(self._arrays[0]), ctypes.addressof(self._arrays[1]), n, first.shape[0],
+                      first.shape[1], kv_format, self.device)
 
 
 def kv_compact(pools: KvPools, block_tables: torch.Tensor, context_lens: torch.Tensor, accepted: torch.Tensor,
                num_accepted: torch.Tensor, tree_len: int, tree_lens: torch.Tensor | None = None, stream=None) -> None:
     """Keep the accepted drafts: in every layer, draft accepted[r][j] (rising) moves to the j-th place behind
     request r's committed context.  context_lens includes the drafts, as in paged_attention_tree."""
-    dev = torch.cuda.current_device()
-    if pools.device != dev:
-        raise ValueError("the pools must be on the current CUDA device")
-    bt = _on_device(dev, block_tables, "block_tables", _I32_ONLY)
-    cl = _on_device(dev, context_lens, "context_lens", _I32_ONLY)
-    acc = _on_device(dev, accepted, "accepted", _I32_ONLY)
-    na = _on_device(dev, num_accepted, "num_accepted", _I32_ONLY)
-    b = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != b:
-        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
-    if accepted.dim() != 2 or accepted.shape[0] != b or num_accepted.numel() != b:
-        raise ValueError("accepted must be [num_seqs][max_accepted] and num_accepted [num_seqs]")
-    tl = 0
-    if tree_lens is not None:
-        tl = _on_device(dev, tree_lens, "tree_lens", _I32_ONLY)
-        if tree_lens.numel() != b:
-            raise ValueError("tree_lens must have one entry per request")
-    _check(_lib.pkv_kv_compact(pools.k_array, pools.v_array, pools.num_layers, pools.desc, pools.kv_format, bt,
-                               block_tables.shape[1], cl, tl, b, tree_len, acc, na, accepted.shape[1],
-                               _stream_ptr(stream)), "pkv_kv_compact")
+    _done(_binding.kv_compact(*pools._args, block_tables, context_lens, accepted, num_accepted, tree_len, tree_lens,
+                              _raw(stream)), "pkv_kv_compact")
 
 
 def _addr(x) -> int:

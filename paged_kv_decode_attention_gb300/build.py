@@ -1,6 +1,8 @@
 """Build libpkv.so in-tree (paged_kv_decode_attention_gb300/_build/) with nvcc
 for sm_103a only.  Translation units compile in parallel, then link into one
-shared library with the CUDA runtime linked statically."""
+shared library with the CUDA runtime linked statically.  Beside it, with g++
+against the installed torch's headers, the Python entry points of the calls
+that serve single tokens (_pkv_binding.so, csrc/py_binding.cpp)."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -9,6 +11,7 @@ import os
 import platform
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 # one build folder per host architecture (the box that runs the GPU may differ)
 BUILD = os.path.join(HERE, "_build", platform.machine())
 LIB = os.path.join(BUILD, "libpkv.so")
+BINDING_SRC = os.path.join(CSRC, "py_binding.cpp")
+BINDING = os.path.join(BUILD, "_pkv_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", f"-I{INCLUDE}", f"-I{CSRC}",
@@ -46,6 +51,26 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    import torch
+
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _binding_compile(obj: str):
+    torch_dir = _torch_dir()
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.sep in _nvcc() else "/usr/local/cuda"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj, f"-I{INCLUDE}",
+            "-I" + sysconfig.get_paths()["include"], "-I" + inc,
+            "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), f"-I{os.path.join(cuda, 'include')}"]
+
+
+def _binding_link(obj: str, out: str):
+    return ["g++", "-shared", "-o", out, obj, "-L" + BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -58,6 +83,10 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
         if force or ptxas_info or _stale(obj, [src] + hdrs):
             cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append(cmd)
+    cuda_jobs = len(jobs)
+    binding_obj = os.path.join(BUILD, "py_binding.o")
+    if force or _stale(binding_obj, [BINDING_SRC] + hdrs):
+        jobs.append(_binding_compile(binding_obj))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -69,8 +98,8 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
                 if verbose or ptxas_info or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
-    if force or jobs or _stale(LIB, objs):
+                    raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}")
+    if force or cuda_jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -78,6 +107,13 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libpkv.so failed")
         os.replace(tmp, LIB)
+    if force or _stale(BINDING, [binding_obj]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        r = subprocess.run(_binding_link(binding_obj, tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link of _pkv_binding.so failed")
+        os.replace(tmp, BINDING)
     return LIB
 
 
