@@ -739,10 +739,13 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         ms[k] = -INFINITY;
         ls[k] = 0.f;
         if (k < static_cast<int>(splits)) {
-          const uint32_t ml = map_shared_to_rank(part_ml + m, k);
+          // its own partials first, then round the cluster: reads of one CTA's
+          // memory by all at once would queue there
+          const uint32_t src = rank + k < splits ? rank + k : rank + k - splits;
+          const uint32_t ml = map_shared_to_rank(part_ml + m, src);
           ms[k] = ld_cluster_f32(ml);
           ls[k] = ld_cluster_f32(ml + 4);
-          os[k] = ld_cluster_f32x4(map_shared_to_rank(smem + S::kOffPartO + m * kHeadDim * 4 + ((lane ^ (m & 7)) << 4), k));
+          os[k] = ld_cluster_f32x4(map_shared_to_rank(smem + S::kOffPartO + m * kHeadDim * 4 + ((lane ^ (m & 7)) << 4), src));
         }
       }
       float mx = -INFINITY;
@@ -778,21 +781,64 @@ __global__ void __launch_bounds__(Shape<kQTiles>::kThreads, Shape<kQTiles>::kCta
   paged_masked_tc_body<kQTiles, kMask, kMode>(k_map, v_map, a);
 }
 
+// Opt the kernel in to its dynamic shared memory, once per device.
+template <int kQTiles, MaskKind kMask, MaskedMode kMode>
+cudaError_t allow_smem(int* device) {
+  static std::atomic<bool> done[64];  // per device; host threads may race on a first call
+  cudaError_t e = cudaGetDevice(device);
+  if (e != cudaSuccess) return e;
+  if (*device < 0 || *device >= 64) return cudaErrorInvalidDevice;
+  if (!done[*device]) {
+    e = cudaFuncSetAttribute(paged_masked_tc_kernel<kQTiles, kMask, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<kQTiles>::kSmem);
+    if (e != cudaSuccess) return e;
+    done[*device] = true;
+  }
+  return cudaSuccess;
+}
+
+// Clusters of `splits` CTAs that are resident at once on device `dev` (the
+// current one); 0 when that cannot be asked (no device).
+template <int kQTiles>
+int max_clusters(int splits, int dev) {
+  static std::atomic<int> known[64][kMaxClusterSplits + 1];  // per device, + 1
+  int n = known[dev][splits].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (allow_smem<kQTiles, MaskKind::kTree, MaskedMode::kCluster>(&dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1, static_cast<unsigned>(splits));
+    cfg.blockDim = dim3(Shape<kQTiles>::kThreads);
+    cfg.dynamicSmemBytes = Shape<kQTiles>::kSmem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1;
+    attr.val.clusterDim.y = static_cast<unsigned>(splits);
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, paged_masked_tc_kernel<kQTiles, MaskKind::kTree, MaskedMode::kCluster>, &cfg) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      c = 0;
+    }
+    n = c + 1;
+    known[dev][splits].store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
 template <int kQTiles, MaskKind kMask, MaskedMode kMode>
 cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a,
                            cudaStream_t stream) {
   using S = Shape<kQTiles>;
-  static std::atomic<bool> done[64];  // per device; host threads may race on a first call
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem<kQTiles, kMask, kMode>(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   auto kernel = paged_masked_tc_kernel<kQTiles, kMask, kMode>;
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
-    done[dev] = true;
-  }
   constexpr int kPos = kPosPerTile * kQTiles;
   const int64_t x = static_cast<int64_t>(a.d.num_seqs) * a.d.num_kv_heads * ((a.d.q_len + kPos - 1) / kPos);
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.d.num_splits));
@@ -822,6 +868,10 @@ int masked_tile_blocks(int q_len) {
 }
 int masked_positions_per_cta(int q_len) { return q_len <= kPosPerTile ? kPosPerTile : 2 * kPosPerTile; }
 int masked_ctas_per_sm(int q_len) { return q_len <= kPosPerTile ? Shape<1>::kCtasPerSm : Shape<2>::kCtasPerSm; }
+
+int masked_max_clusters(int q_len, int splits, int device) {
+  return q_len <= kPosPerTile ? max_clusters<1>(splits, device) : max_clusters<2>(splits, device);
+}
 
 cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.d.num_blocks) * a.d.num_kv_heads * kBlockSize;

@@ -865,7 +865,7 @@ pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, co
     all |= reinterpret_cast<uintptr_t>(p);
   if (all & 15) return PKV_ERR_UNSUPPORTED;
   if (q_out == q && q_stride != q_row) return PKV_ERR_SHAPE;
-  if ((static_cast<int64_t>(num_tokens) * cache->num_kv_heads + 7) / 8 > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(num_tokens) * cache->num_kv_heads + 1) / 2 > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   QkNormRopeArgs a{};
   a.q_out = q_out;
   a.k_cache = k_cache;
@@ -922,12 +922,16 @@ int32_t masked_max_tiles(int32_t q_len, int32_t max_blocks, int32_t window, int3
   return static_cast<int32_t>(tiles < all + 1 ? tiles : all + 1);  // + 1: sinks and window each end in a part tile
 }
 
-// Splits only when the row tiles leave at least half of the resident CTAs
-// unused.  Up to kMaxClusterSplits splits merge in a cluster; more go through
-// the workspace and the combine kernel, whose launch and traffic cost about as
-// much as kCombineTiles tiles of work.
-constexpr int32_t kCombineTiles = 5;
-
+// The split of the masked kernels by its estimated time, in hundredths of a
+// microsecond (fitted to measurements from 1 to 20 requests, 1 to 128 queries,
+// 2K to 32K tokens; the estimates are within about 15 %):
+//   a tile of 64 tokens takes 0.64 us in a CTA that has its SM to itself, 1.05
+//   with two CTAs per SM (0.72 in the 256-row shape), in as many waves as the
+//   CTAs, or the clusters, need;
+//   merging in a cluster takes 0.018 us per row of a CTA (its partials cross the
+//   SM-to-SM network), the combine kernel 3 us and the partials' way to memory
+//   and back.
+// Up to kMaxClusterSplits splits merge in a cluster, more through the workspace.
 MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t window,
                        int32_t num_sinks, int32_t kv_blocks_per_split, int32_t sm_count) {
   const int32_t tb = masked_tile_blocks(q_len);
@@ -937,15 +941,36 @@ MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, in
   if (kv_blocks_per_split > 0) {
     p.tiles_per_split = (kv_blocks_per_split + tb - 1) / tb;
   } else {
-    const int32_t pos = masked_positions_per_cta(q_len);
+    const int32_t pos = masked_positions_per_cta(q_len), per_sm = masked_ctas_per_sm(q_len);
+    const int64_t sms = sm_count > 0 ? sm_count : device_sm_count();
+    const int64_t slots = per_sm * sms;
     const int64_t ctas = num_seqs * num_kv_heads * ((q_len + pos - 1) / pos);
-    const int64_t slots = static_cast<int64_t>(masked_ctas_per_sm(q_len)) * (sm_count > 0 ? sm_count : device_sm_count());
-    const int64_t splits = ctas > 0 ? slots / ctas : 1;
-    if (splits > 1) {
-      const int32_t in_cluster = static_cast<int32_t>(splits < kMaxClusterSplits ? splits : kMaxClusterSplits);
-      const int32_t near = (p.tiles + in_cluster - 1) / in_cluster;
-      const int32_t far = static_cast<int32_t>((p.tiles + splits - 1) / splits);
-      p.tiles_per_split = far + kCombineTiles < near ? far : near;
+    const int64_t rows = (q_len < pos ? q_len : pos) * kGroup;  // of a CTA
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices) device = -1;
+    int64_t best = INT64_MAX;
+    for (int32_t want = 1; want <= 64 && want <= p.tiles && (want == 1 || ctas * want <= 2 * slots); ++want) {
+      const int32_t tps = (p.tiles + want - 1) / want;
+      const int32_t splits = (p.tiles + tps - 1) / tps;
+      if (splits != want) continue;  // the same as a smaller count
+      int64_t resident = slots / splits;
+      if (device >= 0 && splits > 1 && splits <= kMaxClusterSplits) {
+        // (the query counts one CTA per SM for kernels with tensor memory; per_sm of them do run)
+        const int64_t clusters = per_sm * static_cast<int64_t>(masked_max_clusters(q_len, splits, device));
+        if (clusters > 0 && clusters < resident) resident = clusters;
+      }
+      if (resident < 1) continue;
+      const int64_t waves = (ctas + resident - 1) / resident;
+      const int64_t tile = per_sm == 1 ? 72 : (ctas * splits <= sms ? 64 : 105);
+      int64_t cost = waves * tps * tile;
+      if (splits > kMaxClusterSplits)
+        cost += 300 + ctas * rows * splits / 60;  // 1 KB a row and split at 6 GB/ms
+      else if (splits > 1)
+        cost += rows * 18 / 10;
+      if (cost < best) {
+        best = cost;
+        p.tiles_per_split = tps;
+      }
     }
   }
   if (p.tiles_per_split > p.tiles) p.tiles_per_split = p.tiles;

@@ -158,6 +158,9 @@ cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStrea
 int masked_tile_blocks(int q_len);
 int masked_positions_per_cta(int q_len);
 int masked_ctas_per_sm(int q_len);
+// Thread-block clusters of `splits` CTAs resident at once on the current
+// device, whose number is `device` (0: no device to ask).
+int masked_max_clusters(int q_len, int splits, int device);
 
 // Norms of queries and keys, rotation and append in one pass (qk_norm_rope.cu).
 struct QkNormRopeArgs {
