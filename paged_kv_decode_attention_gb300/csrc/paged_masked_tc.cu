@@ -192,13 +192,19 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     // More CTAs than fit at once: the requests with the most to read start
     // first, so that none of them is left for the end.  Place r = the number
     // of requests that come before it.
-    int32_t* len = reinterpret_cast<int32_t*>(smem + S::kOffQ);  // [num_seqs], before the queries come here
-    for (int i = threadIdx.x; i < a.d.num_seqs; i += S::kThreads) len[i] = min(a.d.context_lens[i], a.span);
+    int32_t* len = reinterpret_cast<int32_t*>(smem + S::kOffQ);  // [num_seqs, + up to 3], before the queries come here
+    const int padded = (a.d.num_seqs + 3) & ~3;
+    for (int i = threadIdx.x; i < padded; i += S::kThreads)
+      len[i] = i < a.d.num_seqs ? min(a.d.context_lens[i], a.span) : INT_MIN;
     __syncthreads();
     for (int i = threadIdx.x; i < a.d.num_seqs; i += S::kThreads) {
       const int mine = len[i];
       int before = 0;
-      for (int k = 0; k < a.d.num_seqs; ++k) before += (len[k] > mine || (len[k] == mine && k < i)) ? 1 : 0;
+      for (int k = 0; k < padded; k += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(len + k);
+        before += (v.x > mine || (v.x == mine && k < i)) + (v.y > mine || (v.y == mine && k + 1 < i)) +
+                  (v.z > mine || (v.z == mine && k + 2 < i)) + (v.w > mine || (v.w == mine && k + 3 < i));
+      }
       if (before == r) bars->request = i;
     }
     __syncthreads();
