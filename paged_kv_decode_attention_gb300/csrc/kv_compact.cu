@@ -16,6 +16,13 @@
 // lengths -> accepted -> block table -> row -> store.  One CTA per (request,
 // layer): the chain is walked once for K and V and all heads, by the lanes of
 // one warp, and the layers run side by side in one launch.
+//
+// Measured (q8_0, 36 layers x 128 requests, up to 8 of 61 drafts accepted):
+// 12.0 us with the rows in L2, 20 us from HBM, where it reads 50 MB for 33 MB
+// of rows: a row's scales are 8 bytes, a DRAM access brings 64.  CTAs that
+// stay and let one warp walk ahead took 25 and 30 us, several layers per CTA
+// with the loads of one before the stores of another 14 to 26 and 20 to 31:
+// the many small CTAs hide the chain better.  One request alone: 2.7 us.
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
 

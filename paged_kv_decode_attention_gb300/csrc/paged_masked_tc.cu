@@ -17,29 +17,47 @@
 // per tile and only for the tiles that some row of the CTA sees partly.
 //
 // Rows of a CTA = query positions x the 4 query heads of one KV head, so each
-// K/V byte is read once for all of them.  What bounds it: HBM up to about 64
-// positions (256 rows: 256 FLOP per byte of K/V, the tensor cores' ridge),
-// the tensor cores beyond (positions x window).  Two shapes:
-//   kQTiles 1: 128 rows (32 positions), 64-token K/V tiles, 2 CTAs per SM.
-//              The wait of one CTA (first tiles, softmax latency, epilogue) is
-//              filled by the other.  P.V carries the weights as a BF16 part
-//              plus the BF16 rounding of the remainder (about 2^-17
-//              relative): the tensor cores have the time, HBM is the bound.
-//   kQTiles 2: 256 rows (64 positions), 128-token tiles, 1 CTA per SM; while
-//              one row tile's softmax runs the tensor cores work on the other's
-//              products.  S has N = 128 because an MMA with N = 64 takes as
-//              long.  The weights enter P.V rounded to BF16 (2^-8 relative at
-//              most, unbiased, so the output moves by less than its own BF16
-//              rounding): the remainder's products would make the tensor cores
-//              the bound (3 instead of 2 products per tile).
+// K/V byte is read once for all of them.  What bounds it: HBM up to about 32
+// positions; beyond, shared memory and the tensor pipe together: an MMA with
+// N = 64 re-reads its 128-row A operand for every 64 keys and takes 48 cycles
+// where its multiplications need 32, so S of a 64-token tile costs 384 cycles
+// per row tile and P.V (A in tensor memory, N = 128) 256.  K/V tiles are 64
+// tokens in both shapes: two buffers of scores, then O, fill the 256 columns
+// of a row tile, and the second buffer (S two tiles ahead of the P.V that is
+// under way) is worth more than S with N = 128 from a single buffer (16 trees
+// of 61 positions: 102 us against 114; 2000-token chunks: 390 against 480).
+//   kQTiles 1: 128 rows (32 positions), 2 CTAs per SM.  The wait of one CTA
+//              (first tiles, softmax latency, epilogue) is filled by the
+//              other.  P.V carries the weights as a BF16 part plus the BF16
+//              rounding of the remainder (about 2^-17 relative): the tensor
+//              cores have the time, HBM is the bound.
+//   kQTiles 2: 256 rows (64 positions), 1 CTA per SM; each row tile has its
+//              own MMA warp, and while one's softmax runs the tensor cores
+//              work on the other's products.  The weights enter P.V rounded
+//              to BF16 (2^-8 relative at most, to nearest, so the errors
+//              average out over the keys: 0.0023 of the output's norm against
+//              0.0017 from the output's own rounding).  The remainder's
+//              products would take 150 and 548 us where these take 102 and 390.
 //
 // CTA = 4 + 4 kQTiles warps:
 //   warps 0, 2: TMA producers of K and of V (16 x 64 boxes, 128-byte
 //             swizzle, one per block and 64-dim half; blocks past the range
 //             arrive as zeros).
-//   warp 1  : MMA issuer (warp 3 idles).
+//   warps 1, 3: MMA issuers, one per row tile (warp 3 idles in kQTiles 1).
 //   warps 4..: softmax, one thread per row (TMEM lane).  Warps whose rows are
 //             all padding only keep the barriers in step.
+//
+// Splits of a long context come together in one of three ways (MaskedMode);
+// up to 8 of them form a cluster and merge through distributed shared memory
+// (one request of 26 positions over 600 tokens: 8.4 us in one launch).
+//
+// Measured (32 query and 8 KV heads, BF16, back-to-back calls, one GB300):
+//   tree, 37 requests x 16 positions after about 2,100 tokens   52 us: 6.5 TB/s
+//   tree, 16 x 61 positions after about 8,300 tokens  102 us: 5.5 TB/s, tensor
+//                              pipe 71 % active (85 % on the busiest SM)
+//   window 2000 + 4 sinks, 64 single queries   43 us: 5.2 TB/s; the tail of
+//                              unequal lengths is what is left
+//   window 4096 + 4 sinks, 4 chunks of 2000    390 us: tensor pipe 64 %
 #include <climits>
 #include <cmath>
 
@@ -289,165 +307,165 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   if (n_tiles <= 0) {
     if (in_shape) write_empty();
   } else if (!softmax_warp) {
-   set_max_regs_down<S::kIssueRegs>();
-   if (warp == 0 || warp == 2) {
-    // ---------------------------- TMA producers ----------------------------
-    const bool is_v = warp == 2;
-    const int stages = is_v ? S::kVStages : S::kKStages;
-    uint64_t* full = is_v ? bars->v_full : bars->k_full;
-    uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
-    uint8_t* ring = smem + (is_v ? S::kOffV : S::kOffK);
-    const CUtensorMap* map = is_v ? &v_map : &k_map;
-    // read once, unless several row tiles of the request read the same blocks
-    const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-    const int32_t* table = a.d.block_tables + static_cast<int64_t>(r) * a.d.max_blocks;
-    const int oob_row = a.d.num_blocks * a.d.num_kv_heads * kBlockSize;  // first row past the pool
-    // entry i of the list of blocks (whole tiles of sinks, then the window):
-    // its block id, or INT_MIN for a hole or past the range
-    auto entry = [&](int i) -> int {
-      if (i >= n_tiles * S::kTileBlocks) return INT_MIN;
-      if (kMask == MaskKind::kTree && i < 32)  // read above
-        return t_first * S::kTileBlocks + i < end_block ? first_ids : INT_MIN;
-      i += t_first * S::kTileBlocks;
-      const int sink_entries = sink_tiles * S::kTileBlocks;
-      const int lb = i < sink_entries ? (i < sink_blocks ? i : INT_MAX) : first_block + i - sink_entries;
-      return lb < end_block ? table[lb] : INT_MIN;
-    };
-    auto row_of = [&](int blk) -> int {
-      if (blk == INT_MIN) return oob_row;
-      if (blk < 0 || blk >= a.d.num_blocks) {
-        report(a.d.err, PKV_DEVERR_BLOCK_ID);
-        blk = 0;
-      }
-      return (blk * a.d.num_kv_heads + kvh) * kBlockSize;
-    };
-    constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
-    int cur = row_of(entry(lane)), nxt = INT_MIN;
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      const int in_chunk = j % kTilesPerChunk;
-      if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
-      const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
-      if (in_chunk == kTilesPerChunk - 1) cur = row_of(nxt);
-      const int st = j % stages;
-      if (j >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((j / stages) & 1) ^ 1));
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStageBytes);
-      __syncwarp();
-      if (lane < 2 * S::kTileBlocks) {
-        const int b = lane >> 1, c = lane & 1;
-        tc::tma_load_2d(ring + st * S::kStageBytes + c * S::kHalfBytes + b * 2048, map, c * 64, yy, &full[st], policy);
-      }
-    }
-    if (lane == 0) {
-      if (!ok) report(a.d.err, PKV_DEVERR_TIMEOUT);
-      // the last tiles' copies must land before shared memory is released
-      for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
-    }
-   } else if (kQTiles == 2 || warp == 1) {
-    // ---------------------------- MMA issuer ----------------------------
-    // One warp per row tile, so that neither tile's products wait for the
-    // other's weights.  The whole warp walks the loop and lane 0 issues.
-    // Per tile: P.V as soon as its weights are there, then S two tiles ahead
-    // (into the buffer that this P.V reads, so after its completion): the
-    // softmax always has a scored tile to go on with.
-    constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
-    constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
-    const uint64_t q_desc = tc::smem_desc(sbase + S::kOffQ, 16, 1024);
-    const uint64_t k_desc = tc::smem_desc(sbase + S::kOffK, 16, 1024);
-    const uint64_t v_desc = tc::smem_desc(sbase + S::kOffV, S::kHalfBytes, 1024);
-    const bool leader = lane == 0;
-    const int t = warp >> 1;  // warp 1 or 3
-    const uint32_t tcol = tmem + t * S::kTileCols;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-    };
-    // both barriers tried before either result is looked at
-    auto wait2 = [&](uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp) -> bool {
-      const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
-      return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
-    };
-    // Stages go back by plain arrivals once a later wait has shown that the
-    // products that read them are done (a commit costs this warp 46 cycles).
-    auto give_back = [&](uint64_t* bar) {
-      if (leader) mbar_arrive(bar);
-    };
-    // S of the tile in K stage st, into buffer buf
-    auto issue_s = [&](int buf, int st) {
-      const uint32_t d = tcol + buf * S::kTileTokens;
-      const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
-      const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
-      tc::fence_after_sync();
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16(d, qd + (((kk >> 2) * kQHalfBytes + 32 * (kk & 3)) >> 4),
-                       kd + (((kk >> 2) * S::kHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
-        tc::commit(&bars->s_full[t][buf]);
-      }
-      __syncwarp();
-    };
-    // O += P V, P in buffer buf (its BF16 parts, then their remainders), V in stage st
-    auto issue_pv = [&](int buf, int st, bool first) {
-      const uint32_t ptm = tcol + buf * S::kTileTokens;
-      const uint64_t vd = v_desc + st * (S::kStageBytes >> 4);
-      tc::fence_after_sync();
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < (S::kRemainder ? 8 : 4); ++kk)
-          tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + 8 * kk, vd + (kk & 3) * (2048 >> 4), kIdO,
-                              (!first || kk > 0) ? 1u : 0u);
-        tc::commit(&bars->o_done[t][buf]);
-      }
-      __syncwarp();
-    };
-    if (t < q_tiles) {
-      int ks = 0, kph = 0;          // stage and phase of the next S
-      int vs = 0, vph = 0, pk = 0;  // of the next P.V, and its tile's K stage
-      auto next_k = [&]() {
-        if (++ks == S::kKStages) {
-          ks = 0;
-          kph ^= 1;
-        }
+    set_max_regs_down<S::kIssueRegs>();
+    if (warp == 0 || warp == 2) {
+      // ---------------------------- TMA producers ----------------------------
+      const bool is_v = warp == 2;
+      const int stages = is_v ? S::kVStages : S::kKStages;
+      uint64_t* full = is_v ? bars->v_full : bars->k_full;
+      uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+      uint8_t* ring = smem + (is_v ? S::kOffV : S::kOffK);
+      const CUtensorMap* map = is_v ? &v_map : &k_map;
+      // read once, unless several row tiles of the request read the same blocks
+      const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+      const int32_t* table = a.d.block_tables + static_cast<int64_t>(r) * a.d.max_blocks;
+      const int oob_row = a.d.num_blocks * a.d.num_kv_heads * kBlockSize;  // first row past the pool
+      // entry i of the list of blocks (whole tiles of sinks, then the window):
+      // its block id, or INT_MIN for a hole or past the range
+      auto entry = [&](int i) -> int {
+        if (i >= n_tiles * S::kTileBlocks) return INT_MIN;
+        if (kMask == MaskKind::kTree && i < 32)  // read above
+          return t_first * S::kTileBlocks + i < end_block ? first_ids : INT_MIN;
+        i += t_first * S::kTileBlocks;
+        const int sink_entries = sink_tiles * S::kTileBlocks;
+        const int lb = i < sink_entries ? (i < sink_blocks ? i : INT_MAX) : first_block + i - sink_entries;
+        return lb < end_block ? table[lb] : INT_MIN;
       };
-      ok = wait(&bars->q_full, 0);
-      for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
-        ok = wait(&bars->k_full[ks], kph);
-        if (ok) issue_s(j, ks);
-        next_k();
-      }
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        const int buf = j & 1, ph = (j >> 1) & 1;
-        ok = wait2(&bars->v_full[vs], vph, &bars->p_full[t][buf], ph);
-        if (ok) {
-          give_back(&bars->k_empty[pk]);  // the weights were made from S_j
-          issue_pv(buf, vs, j == 0);
+      auto row_of = [&](int blk) -> int {
+        if (blk == INT_MIN) return oob_row;
+        if (blk < 0 || blk >= a.d.num_blocks) {
+          report(a.d.err, PKV_DEVERR_BLOCK_ID);
+          blk = 0;
         }
-        if (++pk == S::kKStages) pk = 0;
-        if (j + 2 < n_tiles) {
-          ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[t][buf], ph);
-          if (ok) {
-            give_back(&bars->v_empty[vs]);
-            issue_s(buf, ks);
+        return (blk * a.d.num_kv_heads + kvh) * kBlockSize;
+      };
+      constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
+      int cur = row_of(entry(lane)), nxt = INT_MIN;
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const int in_chunk = j % kTilesPerChunk;
+        if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
+        const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
+        if (in_chunk == kTilesPerChunk - 1) cur = row_of(nxt);
+        const int st = j % stages;
+        if (j >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((j / stages) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStageBytes);
+        __syncwarp();
+        if (lane < 2 * S::kTileBlocks) {
+          const int b = lane >> 1, c = lane & 1;
+          tc::tma_load_2d(ring + st * S::kStageBytes + c * S::kHalfBytes + b * 2048, map, c * 64, yy, &full[st], policy);
+        }
+      }
+      if (lane == 0) {
+        if (!ok) report(a.d.err, PKV_DEVERR_TIMEOUT);
+        // the last tiles' copies must land before shared memory is released
+        for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
+      }
+    } else if (kQTiles == 2 || warp == 1) {
+      // ---------------------------- MMA issuer ----------------------------
+      // One warp per row tile, so that neither tile's products wait for the
+      // other's weights.  The whole warp walks the loop and lane 0 issues.
+      // Per tile: P.V as soon as its weights are there, then S two tiles ahead
+      // (into the buffer that this P.V reads, so after its completion): the
+      // softmax always has a scored tile to go on with.
+      constexpr uint32_t kIdS = tc::idesc_bf16_f32(kRowsPerTile, S::kTileTokens, false, false);
+      constexpr uint32_t kIdO = tc::idesc_bf16_f32(kRowsPerTile, kHeadDim, false, true);
+      const uint64_t q_desc = tc::smem_desc(sbase + S::kOffQ, 16, 1024);
+      const uint64_t k_desc = tc::smem_desc(sbase + S::kOffK, 16, 1024);
+      const uint64_t v_desc = tc::smem_desc(sbase + S::kOffV, S::kHalfBytes, 1024);
+      const bool leader = lane == 0;
+      const int t = warp >> 1;  // warp 1 or 3
+      const uint32_t tcol = tmem + t * S::kTileCols;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+      };
+      // both barriers tried before either result is looked at
+      auto wait2 = [&](uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp) -> bool {
+        const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
+        return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
+      };
+      // Stages go back by plain arrivals once a later wait has shown that the
+      // products that read them are done (a commit costs this warp 46 cycles).
+      auto give_back = [&](uint64_t* bar) {
+        if (leader) mbar_arrive(bar);
+      };
+      // S of the tile in K stage st, into buffer buf
+      auto issue_s = [&](int buf, int st) {
+        const uint32_t d = tcol + buf * S::kTileTokens;
+        const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
+        const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_bf16(d, qd + (((kk >> 2) * kQHalfBytes + 32 * (kk & 3)) >> 4),
+                         kd + (((kk >> 2) * S::kHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
+          tc::commit(&bars->s_full[t][buf]);
+        }
+        __syncwarp();
+      };
+      // O += P V, P in buffer buf (its BF16 parts, then their remainders), V in stage st
+      auto issue_pv = [&](int buf, int st, bool first) {
+        const uint32_t ptm = tcol + buf * S::kTileTokens;
+        const uint64_t vd = v_desc + st * (S::kStageBytes >> 4);
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < (S::kRemainder ? 8 : 4); ++kk)
+            tc::mma_bf16_tmem_a(tcol + S::kColO, ptm + 8 * kk, vd + (kk & 3) * (2048 >> 4), kIdO,
+                                (!first || kk > 0) ? 1u : 0u);
+          tc::commit(&bars->o_done[t][buf]);
+        }
+        __syncwarp();
+      };
+      if (t < q_tiles) {
+        int ks = 0, kph = 0;          // stage and phase of the next S
+        int vs = 0, vph = 0, pk = 0;  // of the next P.V, and its tile's K stage
+        auto next_k = [&]() {
+          if (++ks == S::kKStages) {
+            ks = 0;
+            kph ^= 1;
           }
+        };
+        ok = wait(&bars->q_full, 0);
+        for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
+          ok = wait(&bars->k_full[ks], kph);
+          if (ok) issue_s(j, ks);
           next_k();
         }
-        if (++vs == S::kVStages) {
-          vs = 0;
-          vph ^= 1;
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          const int buf = j & 1, ph = (j >> 1) & 1;
+          ok = wait2(&bars->v_full[vs], vph, &bars->p_full[t][buf], ph);
+          if (ok) {
+            give_back(&bars->k_empty[pk]);  // the weights were made from S_j
+            issue_pv(buf, vs, j == 0);
+          }
+          if (++pk == S::kKStages) pk = 0;
+          if (j + 2 < n_tiles) {
+            ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[t][buf], ph);
+            if (ok) {
+              give_back(&bars->v_empty[vs]);
+              issue_s(buf, ks);
+            }
+            next_k();
+          }
+          if (++vs == S::kVStages) {
+            vs = 0;
+            vph ^= 1;
+          }
+        }
+      } else {  // a row tile without queries only gives the stages back
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          const int ks = j % S::kKStages, vs = j % S::kVStages;
+          ok = wait(&bars->k_full[ks], (j / S::kKStages) & 1);
+          if (ok) give_back(&bars->k_empty[ks]);
+          ok = ok && wait(&bars->v_full[vs], (j / S::kVStages) & 1);
+          if (ok) give_back(&bars->v_empty[vs]);
         }
       }
-    } else {  // a row tile without queries only gives the stages back
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        const int ks = j % S::kKStages, vs = j % S::kVStages;
-        ok = wait(&bars->k_full[ks], (j / S::kKStages) & 1);
-        if (ok) give_back(&bars->k_empty[ks]);
-        ok = ok && wait(&bars->v_full[vs], (j / S::kVStages) & 1);
-        if (ok) give_back(&bars->v_empty[vs]);
-      }
+      if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
+      __syncwarp();
     }
-    if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
-    __syncwarp();
-   }
   } else {
     // ---------------------------- softmax ----------------------------
     set_max_regs_up<S::kSoftmaxRegs>();
