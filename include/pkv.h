@@ -673,14 +673,16 @@ pkv_status pkv_paged_attention_window(void* out, const void* q, const void* k_ca
  * context_lens[r] to base + num_accepted[r].  Bit for bit; one launch per 64
  * layers.
  *   k_caches, v_caches : host arrays of num_layers device pointers (pools of
- *                  kv_format, geometry `cache`).
- *   tree_lens    : as for pkv_paged_attention_tree (NULL = tree_len).
+ *                  kv_format, geometry `cache`), no pool twice.
+ *   tree_lens    : device int32 [num_seqs], each in [0, tree_len]; NULL =
+ *                  tree_len for every request.
  *   accepted     : device int32 [num_seqs][max_accepted], the accepted drafts
  *                  of each request in rising order.
  *   num_accepted : device int32 [num_seqs], in [0, max_accepted].
  *   max_accepted : 1 .. tree_len.
  * A request whose list does not rise, leaves [0, n_r) or is longer than n_r or
- * max_accepted sets PKV_DEVERR_ACCEPTED; one whose context is shorter than its
+ * max_accepted, or whose n_r = tree_lens[r] is outside [0, tree_len], sets
+ * PKV_DEVERR_ACCEPTED; one whose context is shorter than its
  * tree or longer than the table sets PKV_DEVERR_CONTEXT; one with a needed
  * block id outside the pool sets PKV_DEVERR_BLOCK_ID: nothing of it is moved.
  * The drafts' blocks must not be shared with another request.
