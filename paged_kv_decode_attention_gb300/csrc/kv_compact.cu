@@ -18,18 +18,22 @@
 // one warp, and the layers run side by side in one launch.
 //
 // Measured (q8_0, 36 layers x 128 requests, up to 8 of 61 drafts accepted):
-// 12.0 us with the rows in L2, 20 us from HBM, where it reads 50 MB for 33 MB
-// of rows: a row's scales are 8 bytes, a DRAM access brings 64.  CTAs that
-// stay and let one warp walk ahead took 25 and 30 us, several layers per CTA
-// with the loads of one before the stores of another 14 to 26 and 20 to 31:
-// the many small CTAs hide the chain better.  One request alone: 2.7 us.
+// 11.8 us with the rows in L2, 19 us from HBM, where it reads 50 MB for 33 MB
+// of rows: a row's scales are 8 bytes, a DRAM access brings 64.  One thread
+// per piece, the scales beside the codes, in equal passes of at most 192
+// threads (up to 320: 12.8 us in L2; always 128 with the scales after the
+// codes: 12.4 and 20.4, and 7.0 instead of 5.2 with one KV head); 8 rows in
+// flight instead of 4: 13.8 and 19.2.  CTAs that stay and let one warp walk
+// ahead took 25 and 30 us, several layers per CTA with the loads of one before
+// the stores of another 14 to 26 and 20 to 31: the many small CTAs hide the
+// chain better.  One request alone: 2.6 us.
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
 
 namespace pkv {
 namespace {
 
-constexpr int kCompactThreads = 128;
+constexpr int kMaxThreads = 192;
 constexpr int kBatch = 4;  // rows in flight per thread
 
 struct Move {
@@ -66,7 +70,7 @@ __device__ __forceinline__ void move_piece(uint8_t* pool, const Move* moves, int
 }
 
 template <int kFormat>
-__global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __grid_constant__ CompactArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) kv_compact_kernel(const __grid_constant__ CompactArgs a) {
   using R = RowShape<kFormat>;
   extern __shared__ Move moves[];  // [max_accepted]
   __shared__ int s_moves;
@@ -121,17 +125,18 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
   if (n == 0) return;
   const int64_t block_bytes = static_cast<int64_t>(a.num_kv_heads) * R::kTile;
   const int per_pool = a.num_kv_heads * R::kPieces;
-  for (int idx = threadIdx.x; idx < 2 * per_pool; idx += kCompactThreads) {
-    const int which = idx >= per_pool;
-    const int p = idx - which * per_pool;
-    const int h = p / R::kPieces;
-    uint8_t* pool = static_cast<uint8_t*>(which ? a.v_caches[layer] : a.k_caches[layer]);
-    move_piece<uint4>(pool, moves, n, static_cast<int64_t>(h) * R::kTile, block_bytes, (p - h * R::kPieces) * 16, R::kRow);
-  }
-  if constexpr (kFormat == PKV_KV_Q8_0) {  // the scales: 4 FP16 per token
-    for (int idx = threadIdx.x; idx < 2 * a.num_kv_heads; idx += kCompactThreads) {
-      const int which = idx >= a.num_kv_heads;
-      const int h = idx - which * a.num_kv_heads;
+  // pieces of 16 bytes, then (q8_0) the 8 bytes of scales of each head
+  const int total = 2 * per_pool + (kFormat == PKV_KV_Q8_0 ? 2 * a.num_kv_heads : 0);
+  for (int idx = threadIdx.x; idx < total; idx += blockDim.x) {
+    if (idx < 2 * per_pool) {
+      const int which = idx >= per_pool;
+      const int p = idx - which * per_pool;
+      const int h = p / R::kPieces;
+      uint8_t* pool = static_cast<uint8_t*>(which ? a.v_caches[layer] : a.k_caches[layer]);
+      move_piece<uint4>(pool, moves, n, static_cast<int64_t>(h) * R::kTile, block_bytes, (p - h * R::kPieces) * 16, R::kRow);
+    } else {
+      const int which = idx - 2 * per_pool >= a.num_kv_heads;
+      const int h = idx - 2 * per_pool - which * a.num_kv_heads;
       uint8_t* pool = static_cast<uint8_t*>(which ? a.v_caches[layer] : a.k_caches[layer]);
       move_piece<uint2>(pool, moves, n, static_cast<int64_t>(h) * R::kTile, block_bytes, kQ8CodeBytes, 8);
     }
@@ -140,8 +145,13 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
 
 template <int kFormat>
 cudaError_t launch_format(const CompactArgs& a, int32_t num_seqs, int32_t layers, cudaStream_t stream) {
+  // as many threads as a row of K and V has pieces, in equal passes
+  using R = RowShape<kFormat>;
+  const int items = 2 * a.num_kv_heads * (R::kPieces + (kFormat == PKV_KV_Q8_0 ? 1 : 0));
+  const int passes = (items + kMaxThreads - 1) / kMaxThreads;
+  const unsigned threads = static_cast<unsigned>(((items + passes - 1) / passes + 31) / 32 * 32);
   return launch_pdl(kv_compact_kernel<kFormat>, dim3(static_cast<unsigned>(num_seqs), static_cast<unsigned>(layers)),
-                    dim3(kCompactThreads), a.max_accepted * sizeof(Move), stream, 1, a);
+                    dim3(threads), a.max_accepted * sizeof(Move), stream, 1, a);
 }
 
 }  // namespace

@@ -846,7 +846,7 @@ pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, co
   pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
   if (kv_format != PKV_KV_BF16 && kv_format != PKV_KV_Q8_0 && kv_format != PKV_KV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
-  if (num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+  if (cache->num_kv_heads > 65535 || num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
   if (num_tokens < 0 || rot_dim < 0 || max_positions < 0) return PKV_ERR_SHAPE;
   if (!std::isfinite(eps) || eps < 0.f) return PKV_ERR_SHAPE;
   if (rot_dim > kHeadDim || rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
@@ -1004,11 +1004,10 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || q_len < 1 || max_blocks_per_seq < 1 || kv_blocks_per_split < 0) return PKV_ERR_SHAPE;
   if (!tree && (window < 1 || num_sinks < 0)) return PKV_ERR_SHAPE;
-  if (num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+  if (cache->num_kv_heads > 65535 || num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
   if (!std::isfinite(scale) || !(scale > 0.f)) return PKV_ERR_SHAPE;
   if (q_len > (tree ? kMaxTree : kMaskedMaxQLen) || max_blocks_per_seq > kMaskedMaxBlocks) return PKV_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(num_seqs) * q_len * num_q_heads > 0x7fffffff || cache->num_kv_heads > 65535)
-    return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_seqs) * q_len * num_q_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > ((int64_t{1} << 31) - 1) / kBlockSize - 1)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
@@ -1146,7 +1145,8 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
   if (num_layers < 0 || num_seqs < 0 || max_blocks_per_seq < 1 || tree_len < 1 || max_accepted < 1 ||
       max_accepted > tree_len)
     return PKV_ERR_SHAPE;
-  if (tree_len > kMaxTree || max_blocks_per_seq > kMaskedMaxBlocks || num_layers > 65535) return PKV_ERR_UNSUPPORTED;
+  if (tree_len > kMaxTree || max_blocks_per_seq > kMaskedMaxBlocks || num_layers > 65535 || cache->num_kv_heads > 65535)
+    return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_layers == 0) return PKV_OK;
   if (!k_caches || !v_caches || !block_tables || !context_lens || !accepted || !num_accepted) return PKV_ERR_NULL;
   for (int32_t l = 0; l < num_layers; ++l) {  // every check before the first launch

@@ -89,6 +89,15 @@ def test_kv_compact(change, status):
     assert _call("pkv_kv_compact", COMP_ORDER, COMP, **change) == status
 
 
+@pytest.mark.parametrize("name,order,base", [
+    ("pkv_qk_norm_rope_append", ROPE_ORDER, dict(ROPE, hq=0, qs=0)), ("pkv_paged_attention_tree", TREE_ORDER, TREE),
+    ("pkv_paged_attention_window", WIN_ORDER, WIN), ("pkv_kv_compact", COMP_ORDER, COMP)])
+def test_head_counts_beyond_the_kernels_grids(name, order, base):
+    # (4 << 30 heads would wrap to 0 in 32 bits)
+    for heads in (65536, 1 << 30):
+        assert _call(name, order, base, desc=_desc(num_kv_heads=heads)) == 3
+
+
 def test_splits_and_workspaces_are_host_arithmetic():
     # enough row tiles: no split, no workspace
     assert pkv.choose_kv_blocks_per_split_tree(37, 8, 16, 144, 152) == 144
