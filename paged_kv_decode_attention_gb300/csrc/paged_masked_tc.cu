@@ -58,6 +58,7 @@
 //   window 2000 + 4 sinks, 64 single queries   43 us: 5.2 TB/s; the tail of
 //                              unequal lengths is what is left
 //   window 4096 + 4 sinks, 4 chunks of 2000    390 us: tensor pipe 64 %
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -123,15 +124,16 @@ struct Bars {
   uint64_t s_full[kQTiles][2];
   uint64_t p_full[kQTiles][2];
   uint64_t o_done[kQTiles][2];
-  uint64_t q_full;
+  uint64_t q_full[kQTiles];  // per unit whose row tile has queries
   uint32_t tmem_base;
-  int32_t request;  // longest_first: the request of this CTA
+  int32_t request;              // longest_first: the request of this CTA
 };
 static_assert(sizeof(Bars<2>) <= 512, "barrier area");
 
 // How the splits of one (row tile, KV head) come together.
 enum class MaskedMode {
   kDirect,     // one split: BF16 out
+  kRounds,     // the same, several units per CTA
   kWorkspace,  // FP32 partials to the workspace, merged by the combine kernel
   kCluster     // one thread-block cluster: merged through distributed shared memory
 };
@@ -180,7 +182,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         mbar_init(&bars->p_full[t][s], 128);
         mbar_init(&bars->o_done[t][s], 1);
       }
-    mbar_init(&bars->q_full, 128 * kQTiles);
+    for (int t = 0; t < kQTiles; ++t) mbar_init(&bars->q_full[t], 128);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -197,16 +199,84 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   pdl_wait();  // everything below may read what earlier grids in the stream write
   pdl_trigger();
 
-  // ---------------- what this CTA reduces (uniform over the CTA) ----------------
+  // ---------------- the units of this CTA ----------------
+  // A unit: up to kPos query positions of one request for one KV head (row
+  // tile fastest, then KV head, then request), one per CTA.  kRounds: the grid
+  // is what is resident at once and a CTA takes a unit per round, forth and
+  // back over the grid; the rings run on, so that a unit's copies are under
+  // way while the one before ends.
   constexpr int kPos = kPosPerTile * kQTiles;  // query positions per CTA
+  constexpr bool kMany = kMode == MaskedMode::kRounds;
+  constexpr bool kToOut = kMode == MaskedMode::kDirect || kMany;
   const int n_rt = (a.d.q_len + kPos - 1) / kPos;
-  // grid x: request (or its place by length), KV head, row tile (fastest)
-  int r = blockIdx.x / n_rt;
-  const int pos0 = (blockIdx.x - r * n_rt) * kPos;  // first query index of this CTA
-  const int kvh = r % a.d.num_kv_heads;
-  r /= a.d.num_kv_heads;
+  const uint32_t n_units = static_cast<uint32_t>(a.d.num_seqs) * a.d.num_kv_heads * n_rt;
+  const int rounds = kMany ? (n_units + gridDim.x - 1) / gridDim.x : 1;
   const int split = blockIdx.y;
-  if (a.longest_first) {
+  const int hq = a.d.num_kv_heads * kGroup;
+  const int cap = a.d.max_blocks * kBlockSize;
+  const int t_first = split * a.tiles_per_split;  // first tile of this split
+  struct Unit {
+    int r, kvh, pos0;  // request, KV head, first query index
+    int ctx;
+    int n_new;    // queries of this request
+    int base;     // position of query 0
+    int n_pos;    // queries of this unit (<= 0: none)
+    // keys [0, sink_blocks*16) and [first_block*16, key_end) are read; the rest is not looked up
+    int sink_blocks, first_block, key_end, end_block, sink_tiles;
+    int n_tiles;  // of this split
+    int q_tiles;  // row tiles with queries (kQTiles 1: always 1)
+  };
+  // unit of a round, or false past the last one
+  auto place = [&](int round, Unit& w) -> bool {
+    uint32_t u = blockIdx.x;
+    if constexpr (kMany) {
+      u = static_cast<uint32_t>(round) * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (u >= n_units) return false;
+    }
+    int x = u / n_rt;
+    w.pos0 = static_cast<int>(u - x * n_rt) * kPos;
+    w.kvh = x % a.d.num_kv_heads;
+    w.r = uniform(x / a.d.num_kv_heads);
+    return true;
+  };
+  // what the unit reads
+  auto measure = [&](Unit& w) {
+    w.ctx = a.d.context_lens[w.r];
+    w.n_new = a.d.q_len;
+    if constexpr (kMask == MaskKind::kTree) {
+      if (a.tree_lens != nullptr) w.n_new = min(max(a.tree_lens[w.r], 0), a.d.q_len);
+    }
+    if (w.ctx > cap && threadIdx.x == 0 && split == 0 && w.kvh == 0 && w.pos0 == 0) report(a.d.err, PKV_DEVERR_CONTEXT);
+    w.ctx = min(max(w.ctx, 0), cap);
+    w.base = w.ctx - w.n_new;
+    w.n_pos = min(kPos, w.n_new - w.pos0);
+    w.sink_blocks = w.first_block = w.key_end = 0;
+    if (w.n_pos > 0 && w.ctx > 0) {
+      if constexpr (kMask == MaskKind::kTree) {
+        w.key_end = w.ctx;
+      } else {
+        const int p_first = w.base + w.pos0;
+        w.key_end = max(p_first + w.n_pos, 0);  // the last query sees its own position
+        const int first_key = max(0, max(p_first, 0) - a.window + 1);
+        w.first_block = first_key / kBlockSize;
+        w.sink_blocks = (min(a.num_sinks, first_key) + kBlockSize - 1) / kBlockSize;
+        if (w.sink_blocks >= w.first_block) w.sink_blocks = w.first_block = 0;  // one contiguous range
+      }
+    }
+    w.end_block = (w.key_end + kBlockSize - 1) / kBlockSize;
+    w.sink_tiles = (w.sink_blocks + S::kTileBlocks - 1) / S::kTileBlocks;
+    const int all_tiles =
+        w.sink_tiles + (max(0, w.end_block - w.first_block) + S::kTileBlocks - 1) / S::kTileBlocks;
+    w.n_tiles = uniform(min(all_tiles - t_first, a.tiles_per_split));
+    w.q_tiles = uniform(w.n_pos > kPosPerTile ? 2 : 1);
+  };
+
+  // the first unit, before the roles part: every warp waits for its length once
+  // (kRounds: each role measures its units when it comes to them; carrying the
+  // first one over costs registers, 417 us instead of 366 for 4 chunks of 2000)
+  Unit unit0{};
+  if (!kMany) place(0, unit0);
+  if (kMode == MaskedMode::kDirect && a.longest_first) {
     // More CTAs than fit at once: the requests with the most to read start
     // first, so that none of them is left for the end.  Place r = the number
     // of requests that come before it.
@@ -223,90 +293,25 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         before += (v.x > mine || (v.x == mine && k < i)) + (v.y > mine || (v.y == mine && k + 1 < i)) +
                   (v.z > mine || (v.z == mine && k + 2 < i)) + (v.w > mine || (v.w == mine && k + 3 < i));
       }
-      if (before == r) bars->request = i;
+      if (before == unit0.r) bars->request = i;
     }
     __syncthreads();
-    r = bars->request;
+    unit0.r = uniform(bars->request);
   }
-  r = uniform(r);
-  const int hq = a.d.num_kv_heads * kGroup;
-  const int cap = a.d.max_blocks * kBlockSize;
-  // The first block ids, read before the context length is known (ids past
-  // the range are dropped below): one trip less before the first copies.
-  int first_ids = 0;
-  if (kMask == MaskKind::kTree && (warp == 0 || warp == 2))
-    first_ids = a.d.block_tables[static_cast<int64_t>(r) * a.d.max_blocks +
-                                 min(split * a.tiles_per_split * S::kTileBlocks + lane, a.d.max_blocks - 1)];
-  int ctx = a.d.context_lens[r];
-  int n_new = a.d.q_len;  // queries of this request
-  if constexpr (kMask == MaskKind::kTree) {
-    if (a.tree_lens != nullptr) n_new = min(max(a.tree_lens[r], 0), a.d.q_len);
-  }
-  if (ctx > cap && threadIdx.x == 0 && split == 0 && kvh == 0 && pos0 == 0) report(a.d.err, PKV_DEVERR_CONTEXT);
-  ctx = min(max(ctx, 0), cap);
-  const int base = ctx - n_new;            // position of query 0
-  const int n_pos = min(kPos, n_new - pos0);  // queries of this CTA (<= 0: none)
-  // keys [0, sink_blocks*16) and [first_block*16, key_end) are read; the rest is not looked up
-  int sink_blocks = 0, first_block = 0, key_end = 0, first_key = 0;
-  if (n_pos > 0 && ctx > 0) {
-    if constexpr (kMask == MaskKind::kTree) {
-      key_end = ctx;
-    } else {
-      const int p_first = base + pos0;
-      key_end = max(p_first + n_pos, 0);  // the last query sees its own position
-      first_key = max(0, max(p_first, 0) - a.window + 1);
-      first_block = first_key / kBlockSize;
-      sink_blocks = (min(a.num_sinks, first_key) + kBlockSize - 1) / kBlockSize;
-      if (sink_blocks >= first_block) {  // one contiguous range
-        sink_blocks = 0;
-        first_block = 0;
-      }
-    }
-  }
-  const int end_block = (key_end + kBlockSize - 1) / kBlockSize;
-  const int sink_tiles = (sink_blocks + S::kTileBlocks - 1) / S::kTileBlocks;
-  const int all_tiles = sink_tiles + (max(0, end_block - first_block) + S::kTileBlocks - 1) / S::kTileBlocks;
-  const int t_first = split * a.tiles_per_split;  // first tile of this split
-  const int n_tiles = uniform(min(all_tiles - t_first, a.tiles_per_split));
-  // first token of tile j of the split
-  auto tile_token = [&](int j) -> int {
-    const int i = t_first + j;
-    return (i < sink_tiles ? i * S::kTileBlocks : first_block + (i - sink_tiles) * S::kTileBlocks) * kBlockSize;
-  };
-  const int q_tiles = uniform(n_pos > kPosPerTile ? 2 : 1);  // row tiles with queries (kQTiles 1: always 1)
-
-  // rows of the softmax threads
+  // Its first block ids are read before the context length is known (ids past
+  // the range are dropped later): one trip less before the copies.
+  int ids0 = 0;
+  if (!kMany && kMask == MaskKind::kTree && (warp == 0 || warp == 2))
+    ids0 = a.d.block_tables[static_cast<int64_t>(unit0.r) * a.d.max_blocks +
+                            min(t_first * S::kTileBlocks + lane, a.d.max_blocks - 1)];
+  if (!kMany) measure(unit0);
   const bool softmax_warp = warp >= 4;
-  const int qt = softmax_warp ? (warp >> 2) - 1 : 0;
-  const int quad = warp & 3;  // TMEM sub-partition of this warp
-  const int row = quad * 32 + lane;
-  const int qi = pos0 + qt * kPosPerTile + (row >> 2);  // query index
-  const bool in_shape = softmax_warp && qi < a.d.q_len;
-  const bool row_valid = in_shape && qi < n_new;
-  auto out_row = [&]() -> int64_t { return (static_cast<int64_t>(r) * a.d.q_len + qi) * hq + kvh * kGroup + (row & 3); };
-  auto part_slot = [&]() -> int64_t { return out_row() * a.d.part_slots + split; };
-
   const uint32_t tmem = uniform(bars->tmem_base);
   const uint32_t sbase = uniform(smem_addr(smem));
   bool ok = true;
-
   float2* part_ml = reinterpret_cast<float2*>(smem + S::kOffPartML);
-  // zeros for a row without a result (padding, or nothing visible)
-  auto write_empty = [&]() {
-    if constexpr (kMode == MaskedMode::kWorkspace) {
-      a.d.part_lse[part_slot()] = -INFINITY;
-    } else if constexpr (kMode == MaskedMode::kCluster) {
-      part_ml[qt * kRowsPerTile + row] = make_float2(-INFINITY, 0.f);
-    } else {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + out_row() * kHeadDim);
-#pragma unroll
-      for (int c = 0; c < kHeadDim * 2 / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
-    }
-  };
 
-  if (n_tiles <= 0) {
-    if (in_shape) write_empty();
-  } else if (!softmax_warp) {
+  if (!softmax_warp) {
     set_max_regs_down<S::kIssueRegs>();
     if (warp == 0 || warp == 2) {
       // ---------------------------- TMA producers ----------------------------
@@ -318,48 +323,59 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       const CUtensorMap* map = is_v ? &v_map : &k_map;
       // read once, unless several row tiles of the request read the same blocks
       const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-      const int32_t* table = a.d.block_tables + static_cast<int64_t>(r) * a.d.max_blocks;
       const int oob_row = a.d.num_blocks * a.d.num_kv_heads * kBlockSize;  // first row past the pool
-      // entry i of the list of blocks (whole tiles of sinks, then the window):
-      // its block id, or INT_MIN for a hole or past the range
-      auto entry = [&](int i) -> int {
-        if (i >= n_tiles * S::kTileBlocks) return INT_MIN;
-        if (kMask == MaskKind::kTree && i < 32)  // read above
-          return t_first * S::kTileBlocks + i < end_block ? first_ids : INT_MIN;
-        i += t_first * S::kTileBlocks;
-        const int sink_entries = sink_tiles * S::kTileBlocks;
-        const int lb = i < sink_entries ? (i < sink_blocks ? i : INT_MAX) : first_block + i - sink_entries;
-        return lb < end_block ? table[lb] : INT_MIN;
-      };
-      auto row_of = [&](int blk) -> int {
-        if (blk == INT_MIN) return oob_row;
-        if (blk < 0 || blk >= a.d.num_blocks) {
-          report(a.d.err, PKV_DEVERR_BLOCK_ID);
-          blk = 0;
+      int filled = 0;  // tiles so far
+      for (int round = 0; round < rounds && ok; ++round) {
+        Unit w = unit0;
+        int first_ids = ids0;
+        if (kMany) {
+          if (!place(round, w)) continue;
+          if (kMask == MaskKind::kTree)
+            first_ids = a.d.block_tables[static_cast<int64_t>(w.r) * a.d.max_blocks + min(lane, a.d.max_blocks - 1)];
+          measure(w);
         }
-        return (blk * a.d.num_kv_heads + kvh) * kBlockSize;
-      };
-      constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
-      int cur = row_of(entry(lane)), nxt = INT_MIN;
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        const int in_chunk = j % kTilesPerChunk;
-        if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
-        const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
-        if (in_chunk == kTilesPerChunk - 1) cur = row_of(nxt);
-        const int st = j % stages;
-        if (j >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((j / stages) & 1) ^ 1));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStageBytes);
-        __syncwarp();
-        if (lane < 2 * S::kTileBlocks) {
-          const int b = lane >> 1, c = lane & 1;
-          tc::tma_load_2d(ring + st * S::kStageBytes + c * S::kHalfBytes + b * 2048, map, c * 64, yy, &full[st], policy);
+        const int32_t* table = a.d.block_tables + static_cast<int64_t>(w.r) * a.d.max_blocks;
+        // entry i of the list of blocks (whole tiles of sinks, then the window):
+        // its block id, or INT_MIN for a hole or past the range
+        auto entry = [&](int i) -> int {
+          if (i >= w.n_tiles * S::kTileBlocks) return INT_MIN;
+          if (kMask == MaskKind::kTree && i < 32)  // read above
+            return t_first * S::kTileBlocks + i < w.end_block ? first_ids : INT_MIN;
+          i += t_first * S::kTileBlocks;
+          const int sink_entries = w.sink_tiles * S::kTileBlocks;
+          const int lb = i < sink_entries ? (i < w.sink_blocks ? i : INT_MAX) : w.first_block + i - sink_entries;
+          return lb < w.end_block ? table[lb] : INT_MIN;
+        };
+        auto row_of = [&](int blk) -> int {
+          if (blk == INT_MIN) return oob_row;
+          if (blk < 0 || blk >= a.d.num_blocks) {
+            report(a.d.err, PKV_DEVERR_BLOCK_ID);
+            blk = 0;
+          }
+          return (blk * a.d.num_kv_heads + w.kvh) * kBlockSize;
+        };
+        constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
+        int cur = row_of(entry(lane)), nxt = INT_MIN;
+        for (int j = 0; j < w.n_tiles && ok; ++j, ++filled) {
+          const int in_chunk = j % kTilesPerChunk;
+          if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
+          const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
+          if (in_chunk == kTilesPerChunk - 1) cur = row_of(nxt);
+          const int st = filled % stages;
+          if (filled >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((filled / stages) & 1) ^ 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStageBytes);
+          __syncwarp();
+          if (lane < 2 * S::kTileBlocks) {
+            const int b = lane >> 1, c = lane & 1;
+            tc::tma_load_2d(ring + st * S::kStageBytes + c * S::kHalfBytes + b * 2048, map, c * 64, yy, &full[st], policy);
+          }
         }
       }
       if (lane == 0) {
         if (!ok) report(a.d.err, PKV_DEVERR_TIMEOUT);
         // the last tiles' copies must land before shared memory is released
-        for (int j = max(0, n_tiles - stages); j < n_tiles; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
+        for (int j = max(0, filled - stages); j < filled; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
       }
     } else if (kQTiles == 2 || warp == 1) {
       // ---------------------------- MMA issuer ----------------------------
@@ -418,29 +434,56 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         }
         __syncwarp();
       };
-      if (t < q_tiles) {
-        int ks = 0, kph = 0;          // stage and phase of the next S
-        int vs = 0, vph = 0, pk = 0;  // of the next P.V, and its tile's K stage
-        auto next_k = [&]() {
-          if (++ks == S::kKStages) {
-            ks = 0;
-            kph ^= 1;
+      uint32_t g = 0;               // tiles of this row tile so far
+      int q_phase = 0;
+      int ks = 0, kph = 0;          // stage and phase of the next S
+      int vs = 0, vph = 0, pk = 0;  // of the next P.V, and its tile's K stage
+      auto next_k = [&]() {
+        if (++ks == S::kKStages) {
+          ks = 0;
+          kph ^= 1;
+        }
+      };
+      auto next_v = [&]() {
+        if (++vs == S::kVStages) {
+          vs = 0;
+          vph ^= 1;
+        }
+        if (++pk == S::kKStages) pk = 0;
+      };
+      for (int round = 0; round < rounds && ok; ++round) {
+        Unit w = unit0;
+        if (kMany) {
+          if (!place(round, w)) continue;
+          measure(w);
+        }
+        const int n_tiles = w.n_tiles;
+        if (n_tiles <= 0) continue;
+        if (t >= w.q_tiles) {  // a row tile without queries only gives the stages back
+          for (int j = 0; j < n_tiles && ok; ++j) {
+            ok = wait(&bars->k_full[ks], kph);
+            if (ok) give_back(&bars->k_empty[ks]);
+            ok = ok && wait(&bars->v_full[vs], vph);
+            if (ok) give_back(&bars->v_empty[vs]);
+            next_k();
+            next_v();
           }
-        };
-        ok = wait(&bars->q_full, 0);
+          continue;
+        }
+        ok = wait(&bars->q_full[t], q_phase);
+        q_phase ^= 1;
         for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
           ok = wait(&bars->k_full[ks], kph);
-          if (ok) issue_s(j, ks);
+          if (ok) issue_s((g + j) & 1, ks);
           next_k();
         }
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          const int buf = j & 1, ph = (j >> 1) & 1;
+        for (int j = 0; j < n_tiles && ok; ++j, ++g) {
+          const int buf = g & 1, ph = (g >> 1) & 1;
           ok = wait2(&bars->v_full[vs], vph, &bars->p_full[t][buf], ph);
           if (ok) {
             give_back(&bars->k_empty[pk]);  // the weights were made from S_j
             issue_pv(buf, vs, j == 0);
           }
-          if (++pk == S::kKStages) pk = 0;
           if (j + 2 < n_tiles) {
             ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[t][buf], ph);
             if (ok) {
@@ -449,18 +492,14 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
             }
             next_k();
           }
-          if (++vs == S::kVStages) {
-            vs = 0;
-            vph ^= 1;
-          }
+          next_v();
         }
-      } else {  // a row tile without queries only gives the stages back
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          const int ks = j % S::kKStages, vs = j % S::kVStages;
-          ok = wait(&bars->k_full[ks], (j / S::kKStages) & 1);
-          if (ok) give_back(&bars->k_empty[ks]);
-          ok = ok && wait(&bars->v_full[vs], (j / S::kVStages) & 1);
-          if (ok) give_back(&bars->v_empty[vs]);
+        // the last two tiles' V, once their products are done
+        for (int back = kMany ? min(n_tiles, 2) : 0; back > 0 && ok; --back) {
+          const uint32_t gt = g - back;
+          const int st = vs >= back ? vs - back : vs - back + S::kVStages;
+          ok = wait(&bars->o_done[t][gt & 1], (gt >> 1) & 1);
+          if (ok) give_back(&bars->v_empty[st]);
         }
       }
       if (!ok && leader) report(a.d.err, PKV_DEVERR_TIMEOUT);
@@ -470,6 +509,59 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     // ---------------------------- softmax ----------------------------
     set_max_regs_up<S::kSoftmaxRegs>();
     const int tid = threadIdx.x & 127;  // within the row tile
+    const int qt = (warp >> 2) - 1;
+    const int quad = warp & 3;  // TMEM sub-partition of this warp
+    const int row = quad * 32 + lane;
+    uint32_t g = 0;       // tiles of this row tile so far
+    uint32_t v_tile = 0;  // tiles through the V ring so far
+    bool fresh = true;    // no unit has used the query area yet
+    for (int round = 0; round < rounds; ++round) {
+    Unit w = unit0;
+    if (kMany) {
+      if (!place(round, w)) continue;
+      measure(w);
+    }
+    const int r = w.r, kvh = w.kvh, pos0 = w.pos0, ctx = w.ctx, n_new = w.n_new, base = w.base, n_pos = w.n_pos;
+    const int first_block = w.first_block, key_end = w.key_end, n_tiles = w.n_tiles;
+    const int qi = pos0 + qt * kPosPerTile + (row >> 2);  // query index
+    const bool in_shape = qi < a.d.q_len;
+    const bool row_valid = in_shape && qi < n_new;
+    auto out_row = [&]() -> int64_t {
+      return (static_cast<int64_t>(r) * a.d.q_len + qi) * hq + kvh * kGroup + (row & 3);
+    };
+    auto part_slot = [&]() -> int64_t { return out_row() * a.d.part_slots + split; };
+    // zeros for a row without a result (padding, or nothing visible)
+    auto write_empty = [&]() {
+      if constexpr (kMode == MaskedMode::kWorkspace) {
+        a.d.part_lse[part_slot()] = -INFINITY;
+      } else if constexpr (kMode == MaskedMode::kCluster) {
+        part_ml[qt * kRowsPerTile + row] = make_float2(-INFINITY, 0.f);
+      } else {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) + out_row() * kHeadDim);
+#pragma unroll
+        for (int c = 0; c < kHeadDim * 2 / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    // first token of tile j of the split
+    auto tile_token = [&](int j) -> int {
+      const int i = t_first + j;
+      return (i < w.sink_tiles ? i * S::kTileBlocks : first_block + (i - w.sink_tiles) * S::kTileBlocks) * kBlockSize;
+    };
+    if (n_tiles <= 0) {
+      if (in_shape) write_empty();
+      continue;
+    }
+    const bool tile_live = qt < w.q_tiles;
+    if (kMany && !tile_live) {
+      if (in_shape) write_empty();
+      v_tile += n_tiles;
+      continue;
+    }
+    // the unit before has left its results' way, the query area (all four warps)
+    if constexpr (kMany) {
+      if (!fresh) named_barrier_sync(1 + qt, 128);
+      fresh = false;
+    }
     {
       // this row tile's queries -> 128-byte swizzled K-major tile, two 64-dim
       // halves; thread t loads 16-byte chunk t % 16 of every (threads / 16)-th
@@ -497,12 +589,11 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         }
       }
       tc::fence_proxy_async_smem();
-      mbar_arrive(&bars->q_full);
+      mbar_arrive(&bars->q_full[qt]);
     }
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tcol = tmem + lane_off + qt * S::kTileCols;
     const float c = a.d.scale_log2;  // > 0: the max of raw scores scales to the max of scaled ones
-    const bool tile_live = qt < q_tiles;
     const bool warp_live = pos0 + qt * kPosPerTile + quad * 8 < n_new;  // some row of the warp has a query
     // the keys a row sees in [tok, tok + 64), one bit per key
     const uint64_t* mrow = nullptr;
@@ -549,7 +640,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     float m_stale = -INFINITY;  // scaled max the weights are taken against (lags the true max by < 2^16)
     float l = 0.f;              // the sum of the weights
     for (int j = 0; j < n_tiles && tile_live; ++j) {
-      const int buf = j & 1, ph = (j >> 1) & 1;
+      const int buf = (g + j) & 1, ph = ((g + j) >> 1) & 1;
       const int tok = tile_token(j);
       const uint32_t scol = tcol + buf * S::kTileTokens;
       // keep `ok` warp-uniform: the tcgen05 loads below are warp-collective
@@ -588,7 +679,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         const float alpha = grow ? exp2_approx(m_stale - m_new) : 1.f;  // 0 while m_stale is -inf
         if (__builtin_expect(__any_sync(0xffffffffu, grow && j > 0 && m_stale != -INFINITY), 0)) {
           // O holds weights taken against the old maxima: rescale this warp's rows
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(j - 1) & 1], ((j - 1) >> 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][buf ^ 1], ((g + j - 1) >> 1) & 1));
           tc::fence_after_sync();
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
@@ -608,8 +699,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       // V rows of the slots past the context (weight 0, but they may hold
       // anything): zero them
       if (__builtin_expect(part && ctx > tok && ctx < tok + S::kTileTokens && (ctx & (kBlockSize - 1)) != 0, 0)) {
-        const int st = j % S::kVStages;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (j / S::kVStages) & 1));
+        const int st = (v_tile + j) % S::kVStages;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], ((v_tile + j) / S::kVStages) & 1));
         uint8_t* vt = smem + S::kOffV + st * S::kStageBytes;
         const int t0 = ctx - tok, t1 = (t0 + kBlockSize - 1) & ~(kBlockSize - 1);
         for (int idx = tid; idx < (t1 - t0) * 16; idx += 128) {
@@ -646,13 +737,14 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       tc::fence_before_sync();
       mbar_arrive(&bars->p_full[qt][buf]);
     }
-    if (!ok && lane == 0) report(a.d.err, PKV_DEVERR_TIMEOUT);
+    v_tile += n_tiles;
+    if (tile_live) g += n_tiles;
     // ---- epilogue ----
     // Results go through the row tile's query area (no product reads it any
     // more) so that the rows are written as whole 256-byte lines: a thread's
     // own row in 16-byte pieces costs 32 separate lines an instruction.
     if (ok && tile_live)
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[qt][(g - 1) & 1], ((g - 1) >> 1) & 1));
     if constexpr (kMode == MaskedMode::kCluster) {
       // the partials go over the rings: no row tile's products may still read them
       if constexpr (kQTiles == 2) named_barrier_sync(1, 128 * kQTiles);
@@ -679,7 +771,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
         part_ml[m] = live ? make_float2(m_stale, l) : make_float2(-INFINITY, 0.f);
-      } else if constexpr (kMode == MaskedMode::kDirect) {
+      } else if constexpr (kToOut) {
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           float o[32];
@@ -739,6 +831,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     } else if (in_shape) {
       write_empty();
     }
+    }
+    if (!ok && lane == 0) report(a.d.err, PKV_DEVERR_TIMEOUT);
   }
 
   tc::fence_before_sync();
@@ -754,7 +848,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     // 2^(m_s - m) l_s.
     cluster_sync_all();
     const uint32_t splits = gridDim.y, rank = cluster_cta_rank();
-    const int rows = min(kPos, a.d.q_len - pos0) * kGroup;  // rows of the shape, padding included
+    const Unit& w = unit0;
+    const int rows = min(kPos, a.d.q_len - w.pos0) * kGroup;  // rows of the shape, padding included
     for (int m = static_cast<int>(rank) * S::kWarps + warp; m < rows; m += static_cast<int>(splits) * S::kWarps) {
       float ms[kMaxClusterSplits], ls[kMaxClusterSplits];
       float4 os[kMaxClusterSplits];
@@ -791,7 +886,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       uint2 packed;
       packed.x = pack_bf16x2(o.x * inv, o.y * inv);
       packed.y = pack_bf16x2(o.z * inv, o.w * inv);
-      const int64_t mrow = (static_cast<int64_t>(r) * a.d.q_len + pos0 + (m >> 2)) * hq + kvh * kGroup + (m & 3);
+      const int64_t mrow =
+          (static_cast<int64_t>(w.r) * a.d.q_len + w.pos0 + (m >> 2)) * hq + w.kvh * kGroup + (m & 3);
       reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.d.out) + mrow * kHeadDim)[lane] = packed;
     }
     cluster_sync_all();  // a partial stays until every CTA has read it
@@ -864,7 +960,8 @@ cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, con
   if (e != cudaSuccess) return e;
   auto kernel = paged_masked_tc_kernel<kQTiles, kMask, kMode>;
   constexpr int kPos = kPosPerTile * kQTiles;
-  const int64_t x = static_cast<int64_t>(a.d.num_seqs) * a.d.num_kv_heads * ((a.d.q_len + kPos - 1) / kPos);
+  int64_t x = static_cast<int64_t>(a.d.num_seqs) * a.d.num_kv_heads * ((a.d.q_len + kPos - 1) / kPos);
+  if (kMode == MaskedMode::kRounds) x = std::min(x, static_cast<int64_t>(a.resident));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.d.num_splits));
   return launch_pdl(kernel, grid, dim3(S::kThreads), S::kSmem, stream,
                     kMode == MaskedMode::kCluster ? static_cast<unsigned>(a.d.num_splits) : 1u, kmap, vmap, a);
@@ -872,6 +969,7 @@ cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, con
 
 template <int kQTiles, MaskKind kMask>
 cudaError_t launch_mask(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a, cudaStream_t stream) {
+  if (a.d.num_splits == 1 && a.rounds) return launch_variant<kQTiles, kMask, MaskedMode::kRounds>(kmap, vmap, a, stream);
   if (a.d.num_splits == 1) return launch_variant<kQTiles, kMask, MaskedMode::kDirect>(kmap, vmap, a, stream);
   if (a.d.part_o != nullptr) return launch_variant<kQTiles, kMask, MaskedMode::kWorkspace>(kmap, vmap, a, stream);
   if (a.d.num_splits > kMaxClusterSplits) return cudaErrorInvalidValue;

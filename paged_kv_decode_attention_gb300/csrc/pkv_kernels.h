@@ -150,8 +150,10 @@ struct MaskedArgs {
   int32_t window;             // window: keys p - window + 1 .. p, and
   int32_t num_sinks;          //         keys 0 .. num_sinks - 1
   int32_t tiles_per_split;
-  int32_t longest_first;      // CTAs in the order of min(context, span), longest first (num_seqs <= kMaxRanked)
+  int32_t longest_first;      // one split: CTAs in the order of min(context, span), longest first (num_seqs <= kMaxRanked)
   int32_t span;
+  int32_t rounds;             // one split: CTAs take several units, the grid is
+  int32_t resident;           //            the CTAs resident at once
 };
 constexpr int kMaxRanked = 256;  // every CTA orders the lengths: about 1 us for 256
 cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream);
