@@ -240,12 +240,12 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     return true;
   };
   // what the unit reads
-  auto measure = [&](Unit& w) {
-    w.ctx = a.d.context_lens[w.r];
-    w.n_new = a.d.q_len;
-    if constexpr (kMask == MaskKind::kTree) {
-      if (a.tree_lens != nullptr) w.n_new = min(max(a.tree_lens[w.r], 0), a.d.q_len);
-    }
+  auto tree_len = [&](int r) -> int {
+    return kMask == MaskKind::kTree && a.tree_lens != nullptr ? a.tree_lens[r] : a.d.q_len;
+  };
+  auto measure = [&](Unit& w, int ctx, int n_new) {
+    w.ctx = ctx;
+    w.n_new = min(max(n_new, 0), a.d.q_len);
     if (w.ctx > cap && threadIdx.x == 0 && split == 0 && w.kvh == 0 && w.pos0 == 0) report(a.d.err, PKV_DEVERR_CONTEXT);
     w.ctx = min(max(w.ctx, 0), cap);
     w.base = w.ctx - w.n_new;
@@ -304,7 +304,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   if (!kMany && kMask == MaskKind::kTree && (warp == 0 || warp == 2))
     ids0 = a.d.block_tables[static_cast<int64_t>(unit0.r) * a.d.max_blocks +
                             min(t_first * S::kTileBlocks + lane, a.d.max_blocks - 1)];
-  if (!kMany) measure(unit0);
+  if (!kMany) measure(unit0, a.d.context_lens[unit0.r], tree_len(unit0.r));
   const bool softmax_warp = warp >= 4;
   const uint32_t tmem = uniform(bars->tmem_base);
   const uint32_t sbase = uniform(smem_addr(smem));
@@ -332,7 +332,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           if (!place(round, w)) continue;
           if (kMask == MaskKind::kTree)
             first_ids = a.d.block_tables[static_cast<int64_t>(w.r) * a.d.max_blocks + min(lane, a.d.max_blocks - 1)];
-          measure(w);
+          measure(w, a.d.context_lens[w.r], tree_len(w.r));
         }
         const int32_t* table = a.d.block_tables + static_cast<int64_t>(w.r) * a.d.max_blocks;
         // entry i of the list of blocks (whole tiles of sinks, then the window):
@@ -455,7 +455,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         Unit w = unit0;
         if (kMany) {
           if (!place(round, w)) continue;
-          measure(w);
+          measure(w, a.d.context_lens[w.r], tree_len(w.r));
         }
         const int n_tiles = w.n_tiles;
         if (n_tiles <= 0) continue;
@@ -515,11 +515,25 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     uint32_t g = 0;       // tiles of this row tile so far
     uint32_t v_tile = 0;  // tiles through the V ring so far
     bool fresh = true;    // no unit has used the query area yet
+    // kRounds: the next unit, its lengths read a round ahead
+    Unit ahead;
+    bool more = kMany && place(0, ahead);
+    int ahead_ctx = 0, ahead_len = 0;
+    if (more) {
+      ahead_ctx = a.d.context_lens[ahead.r];
+      ahead_len = tree_len(ahead.r);
+    }
     for (int round = 0; round < rounds; ++round) {
     Unit w = unit0;
     if (kMany) {
-      if (!place(round, w)) continue;
-      measure(w);
+      if (!more) break;
+      w = ahead;
+      measure(w, ahead_ctx, ahead_len);
+      more = round + 1 < rounds && place(round + 1, ahead);
+      if (more) {
+        ahead_ctx = a.d.context_lens[ahead.r];
+        ahead_len = tree_len(ahead.r);
+      }
     }
     const int r = w.r, kvh = w.kvh, pos0 = w.pos0, ctx = w.ctx, n_new = w.n_new, base = w.base, n_pos = w.n_pos;
     const int first_block = w.first_block, key_end = w.key_end, n_tiles = w.n_tiles;
@@ -570,11 +584,12 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       const uint16_t* qbase = static_cast<const uint16_t*>(a.d.q);
       uint8_t* qs = smem + S::kOffQ + qt * kQTileBytes;
       constexpr int kStep = 128 / 16;
+      constexpr int kDeep = kMany ? 16 : 8;  // loads in flight (16: one trip, 8: fewer registers)
 #pragma unroll
-      for (int k0 = 0; k0 < kRowsPerTile / kStep; k0 += 8) {
-        uint4 v[8];
+      for (int k0 = 0; k0 < kRowsPerTile / kStep; k0 += kDeep) {
+        uint4 v[kDeep];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kDeep; ++k) {
           const int m = (tid >> 4) + kStep * (k0 + k);
           const int qim = pos0 + qt * kPosPerTile + (m >> 2);
           v[k] = make_uint4(0, 0, 0, 0);
@@ -583,13 +598,23 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
                 qbase + ((static_cast<int64_t>(r) * a.d.q_len + qim) * hq + kvh * kGroup + (m & 3)) * kHeadDim + ch * 8);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kDeep; ++k) {
           const int m = (tid >> 4) + kStep * (k0 + k);
           *reinterpret_cast<uint4*>(qs + (ch >> 3) * kQHalfBytes + tc::sw128_offset(m, (ch & 7) * 8)) = v[k];
         }
       }
       tc::fence_proxy_async_smem();
       mbar_arrive(&bars->q_full[qt]);
+    }
+    if (kMany && more) {  // the next unit's queries towards L2
+      const int qa = ahead.pos0 + qt * kPosPerTile + (row >> 2);
+      if (qa < a.d.q_len) {
+        const uint16_t* next_q =
+            static_cast<const uint16_t*>(a.d.q) +
+            ((static_cast<int64_t>(ahead.r) * a.d.q_len + qa) * hq + ahead.kvh * kGroup + (row & 3)) * kHeadDim;
+        prefetch_l2(next_q);
+        prefetch_l2(next_q + kHeadDim / 2);
+      }
     }
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tcol = tmem + lane_off + qt * S::kTileCols;
@@ -790,14 +815,17 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           }
         }
         __syncwarp();
+        // a position's four heads lie together: 1 KB, two stores of the warp
+        const int q0 = pos0 + qt * kPosPerTile + quad * 8;  // the warp's first position
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) +
+                                            ((static_cast<int64_t>(r) * a.d.q_len + q0) * hq + kvh * kGroup) * kHeadDim) +
+                   lane;
+        const int n_out = a.d.q_len - q0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int m = 2 * i + (lane >> 4), ch = lane & 15;
-          const int mq = pos0 + qt * kPosPerTile + ((quad * 32 + m) >> 2);
-          if (mq < a.d.q_len)
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d.out) +
-                                     ((static_cast<int64_t>(r) * a.d.q_len + mq) * hq + kvh * kGroup + (m & 3)) * kHeadDim)[ch] =
-                *chunk(m, ch);
+          if ((i >> 1) < n_out) o[(i & 1) * 32] = *chunk(m, ch);
+          if (i & 1) o += hq * (kHeadDim / 8);
         }
       } else {
         // FP32 partials, 64 dims (256 bytes) of each row at a time
