@@ -26,6 +26,8 @@
 // of a row tile, and the second buffer (S two tiles ahead of the P.V that is
 // under way) is worth more than S with N = 128 from a single buffer (16 trees
 // of 61 positions: 102 us against 114; 2000-token chunks: 390 against 480).
+// Half of the queries in tensor memory, with one buffer each for S and P,
+// takes 110 and 421 us: an MMA whose A lies there is not faster at N = 64.
 //   kQTiles 1: 128 rows (32 positions), 2 CTAs per SM.  The wait of one CTA
 //              (first tiles, softmax latency, epilogue) is filled by the
 //              other.  P.V carries the weights as a BF16 part plus the BF16
@@ -53,11 +55,13 @@
 //
 // Measured (32 query and 8 KV heads, BF16, back-to-back calls, one GB300):
 //   tree, 37 requests x 16 positions after about 2,100 tokens   52 us: 6.5 TB/s
-//   tree, 16 x 61 positions after about 8,300 tokens  102 us: 5.5 TB/s, tensor
+//   tree, 16 x 61 positions after about 8,300 tokens  100 us: 5.6 TB/s, tensor
 //                              pipe 71 % active (85 % on the busiest SM)
 //   window 2000 + 4 sinks, 64 single queries   43 us: 5.2 TB/s; the tail of
 //                              unequal lengths is what is left
-//   window 4096 + 4 sinks, 4 chunks of 2000    390 us: tensor pipe 64 %
+//   window 4096 + 4 sinks, 4 chunks of 2000    370 us: 1380 cycles a tile and
+//                              pair of row tiles where the pipe needs 1280, and
+//                              7 % around a unit (kRounds; one unit per CTA 395)
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -81,7 +85,7 @@ constexpr int kQHalfBytes = kQTileBytes / 2;
 
 template <int kQTiles>
 struct Shape {
-  static constexpr int kTileBlocks = 4;
+  static constexpr int kTileBlocks = kMaskedTileBlocks;
   static constexpr int kTileTokens = kTileBlocks * kBlockSize;  // 64
   static constexpr int kKStages = kQTiles == 1 ? 3 : 5;
   static constexpr int kVStages = kQTiles == 1 ? 2 : 5;
@@ -1013,14 +1017,11 @@ cudaError_t launch_shape(const CUtensorMap& kmap, const CUtensorMap& vmap, const
 
 }  // namespace
 
-int masked_tile_blocks(int q_len) {
-  return q_len <= kPosPerTile ? Shape<1>::kTileBlocks : Shape<2>::kTileBlocks;
-}
-int masked_positions_per_cta(int q_len) { return q_len <= kPosPerTile ? kPosPerTile : 2 * kPosPerTile; }
-int masked_ctas_per_sm(int q_len) { return q_len <= kPosPerTile ? Shape<1>::kCtasPerSm : Shape<2>::kCtasPerSm; }
+int masked_positions_per_cta(bool wide) { return wide ? 2 * kPosPerTile : kPosPerTile; }
+int masked_ctas_per_sm(bool wide) { return wide ? Shape<2>::kCtasPerSm : Shape<1>::kCtasPerSm; }
 
-int masked_max_clusters(int q_len, int splits, int device) {
-  return q_len <= kPosPerTile ? max_clusters<1>(splits, device) : max_clusters<2>(splits, device);
+int masked_max_clusters(bool wide, int splits, int device) {
+  return wide ? max_clusters<2>(splits, device) : max_clusters<1>(splits, device);
 }
 
 cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream) {
@@ -1028,8 +1029,8 @@ cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStrea
   if (rows + kBlockSize >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
   CUtensorMap kmap, vmap;
   if (!make_pool_map(&kmap, a.d.k_cache, rows) || !make_pool_map(&vmap, a.d.v_cache, rows)) return cudaErrorInvalidValue;
-  return a.d.q_len <= kPosPerTile ? launch_shape<1>(kmap, vmap, a, mask, stream)
-                                  : launch_shape<2>(kmap, vmap, a, mask, stream);
+  return a.wide ? launch_shape<2>(kmap, vmap, a, mask, stream)
+                                  : launch_shape<1>(kmap, vmap, a, mask, stream);
 }
 
 }  // namespace pkv

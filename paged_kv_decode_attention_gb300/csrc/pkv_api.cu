@@ -900,6 +900,7 @@ namespace {
 // The masked attention calls (tree, window): tiles a CTA reads at most, and
 // how they are split.
 struct MaskedPlan {
+  bool wide;                // CTAs of 256 rows
   int32_t tiles;            // at most
   int32_t tiles_per_split;
   int32_t splits;
@@ -911,38 +912,55 @@ constexpr int32_t kMaskedMaxQLen = 1 << 26;
 constexpr int32_t kMaskedMaxSpan = 1 << 30;  // windows and sinks beyond it are as good as endless
 
 // Tiles of blocks a CTA reads at most.  window 0: the whole table (tree).
-int32_t masked_max_tiles(int32_t q_len, int32_t max_blocks, int32_t window, int32_t num_sinks) {
-  const int32_t tb = masked_tile_blocks(q_len);
+int32_t masked_max_tiles(bool wide, int32_t q_len, int32_t max_blocks, int32_t window, int32_t num_sinks) {
+  constexpr int32_t tb = kMaskedTileBlocks;
   const int32_t all = (max_blocks + tb - 1) / tb;
   if (window == 0) return all;
-  const int64_t pos = q_len < masked_positions_per_cta(q_len) ? q_len : masked_positions_per_cta(q_len);
+  const int64_t pos = q_len < masked_positions_per_cta(wide) ? q_len : masked_positions_per_cta(wide);
   const int64_t span = (static_cast<int64_t>(window) + pos - 1 + kBlockSize - 2) / kBlockSize + 1;  // any alignment
   const int64_t sinks = (static_cast<int64_t>(num_sinks) + kBlockSize - 1) / kBlockSize;
   const int64_t tiles = (span + tb - 1) / tb + (sinks + tb - 1) / tb;
   return static_cast<int32_t>(tiles < all + 1 ? tiles : all + 1);  // + 1: sinks and window each end in a part tile
 }
 
+// CTAs of 256 rows, or of 128?  The first where a request has more positions
+// than fit into 128 rows, but for calls of a few tiles whose 128-row CTAs find
+// an SM each: there the time is one CTA's way through them, which is shorter
+// (one request of 64 drafts after 600 tokens 9.3 us instead of 11.5; 2 chunks of
+// 200, window 200: 9.5 instead of 11.9).  With more tiles or CTAs the 256 rows'
+// K and V, read once for twice the positions, win (16 x 61 drafts after 8,300
+// tokens: 100 us against 148).
+bool masked_wide(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t window,
+                 int32_t num_sinks, int64_t sms) {
+  constexpr int32_t kTiles = 16;
+  const int32_t pos = masked_positions_per_cta(false);
+  if (q_len <= pos) return false;
+  return num_seqs * num_kv_heads * ((q_len + pos - 1) / pos) > sms ||
+         masked_max_tiles(false, q_len, max_blocks, window, num_sinks) > kTiles;
+}
+
 // The split of the masked kernels by its estimated time, in hundredths of a
 // microsecond (fitted to measurements from 1 to 20 requests, 1 to 128 queries,
 // 2K to 32K tokens; the estimates are within about 15 %):
 //   a tile of 64 tokens takes 0.64 us in a CTA that has its SM to itself, 1.05
-//   with two CTAs per SM (0.72 in the 256-row shape), in as many waves as the
-//   CTAs, or the clusters, need;
+//   with two CTAs per SM (0.72 in the 256-row shape), and a CTA's start and end
+//   4 us, in as many waves as the CTAs, or the clusters, need;
 //   merging in a cluster takes 0.018 us per row of a CTA (its partials cross the
 //   SM-to-SM network), the combine kernel 3 us and the partials' way to memory
 //   and back.
 // Up to kMaxClusterSplits splits merge in a cluster, more through the workspace.
 MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t window,
                        int32_t num_sinks, int32_t kv_blocks_per_split, int32_t sm_count) {
-  const int32_t tb = masked_tile_blocks(q_len);
-  MaskedPlan p{masked_max_tiles(q_len, max_blocks, window, num_sinks), 0, 1};
+  constexpr int32_t tb = kMaskedTileBlocks;
+  const int64_t sms = sm_count > 0 ? sm_count : device_sm_count();
+  MaskedPlan p{masked_wide(num_seqs, num_kv_heads, q_len, max_blocks, window, num_sinks, sms), 0, 0, 1};
+  p.tiles = masked_max_tiles(p.wide, q_len, max_blocks, window, num_sinks);
   p.tiles_per_split = p.tiles;
   if (kv_blocks_per_split >= max_blocks) return p;
   if (kv_blocks_per_split > 0) {
     p.tiles_per_split = (kv_blocks_per_split + tb - 1) / tb;
   } else {
-    const int32_t pos = masked_positions_per_cta(q_len), per_sm = masked_ctas_per_sm(q_len);
-    const int64_t sms = sm_count > 0 ? sm_count : device_sm_count();
+    const int32_t pos = masked_positions_per_cta(p.wide), per_sm = masked_ctas_per_sm(p.wide);
     const int64_t slots = per_sm * sms;
     const int64_t ctas = num_seqs * num_kv_heads * ((q_len + pos - 1) / pos);
     const int64_t rows = (q_len < pos ? q_len : pos) * kGroup;  // of a CTA
@@ -956,13 +974,13 @@ MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, in
       int64_t resident = slots / splits;
       if (device >= 0 && splits > 1 && splits <= kMaxClusterSplits) {
         // (the query counts one CTA per SM for kernels with tensor memory; per_sm of them do run)
-        const int64_t clusters = per_sm * static_cast<int64_t>(masked_max_clusters(q_len, splits, device));
+        const int64_t clusters = per_sm * static_cast<int64_t>(masked_max_clusters(p.wide, splits, device));
         if (clusters > 0 && clusters < resident) resident = clusters;
       }
       if (resident < 1) continue;
       const int64_t waves = (ctas + resident - 1) / resident;
       const int64_t tile = per_sm == 1 ? 72 : (ctas * splits <= sms ? 64 : 105);
-      int64_t cost = waves * tps * tile;
+      int64_t cost = waves * (tps * tile + 400);
       if (splits > kMaxClusterSplits)
         cost += 300 + ctas * rows * splits / 60;  // 1 KB a row and split at 6 GB/ms
       else if (splits > 1)
@@ -1027,6 +1045,7 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
   const MaskedPlan plan = masked_plan(num_seqs, cache->num_kv_heads, q_len, max_blocks_per_seq, tree ? 0 : a.window,
                                       a.num_sinks, kv_blocks_per_split, 0);
   if (plan.splits > 65535) return PKV_ERR_UNSUPPORTED;
+  a.wide = plan.wide;
   a.tree_lens = tree_lens;
   a.tree_mask = tree_mask;
   a.mask_words = (q_len + 63) / 64;
@@ -1053,10 +1072,10 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
   // little: 4 chunks of 2000, window 4096: 366 us against 395; 83 single
   // queries, window 17: 17.1 against 20.5; but 64 of contexts from 16 to
   // 32,000, window 2000: 47 against 43.
-  const int32_t pos = masked_positions_per_cta(q_len);
+  const int32_t pos = masked_positions_per_cta(plan.wide);
   const int64_t ctas = static_cast<int64_t>(num_seqs) * cache->num_kv_heads * ((q_len + pos - 1) / pos);
   if (ctas > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
-  a.resident = masked_ctas_per_sm(q_len) * device_sm_count();
+  a.resident = masked_ctas_per_sm(plan.wide) * device_sm_count();
   const bool waves = plan.splits == 1 && ctas > a.resident;
   a.rounds = waves && (plan.tiles <= kFewTiles || (!tree && q_len > pos));
   a.longest_first = waves && !a.rounds && q_len <= pos && num_seqs <= kMaxRanked;
@@ -1089,7 +1108,7 @@ int32_t pkv_choose_kv_blocks_per_split_tree(int32_t num_seqs, int32_t num_kv_hea
   if (!masked_sizes_ok(num_seqs, num_kv_heads, tree_len, max_blocks_per_seq, 0, 0, true))
     return max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
   const MaskedPlan p = masked_plan(num_seqs, num_kv_heads, tree_len, max_blocks_per_seq, 0, 0, 0, sm_count);
-  return p.splits == 1 ? max_blocks_per_seq : p.tiles_per_split * masked_tile_blocks(tree_len);
+  return p.splits == 1 ? max_blocks_per_seq : p.tiles_per_split * kMaskedTileBlocks;
 }
 
 size_t pkv_workspace_size_tree(int32_t num_seqs, int32_t tree_len, int32_t num_q_heads, int32_t max_blocks_per_seq,
@@ -1119,7 +1138,7 @@ int32_t pkv_choose_kv_blocks_per_split_window(int32_t num_seqs, int32_t num_kv_h
     return max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
   const MaskedPlan p = masked_plan(num_seqs, num_kv_heads, q_len, max_blocks_per_seq, span_limit(window),
                                    span_limit(num_sinks), 0, sm_count);
-  return p.splits == 1 ? max_blocks_per_seq : p.tiles_per_split * masked_tile_blocks(q_len);
+  return p.splits == 1 ? max_blocks_per_seq : p.tiles_per_split * kMaskedTileBlocks;
 }
 
 size_t pkv_workspace_size_window(int32_t num_seqs, int32_t q_len, int32_t num_q_heads, int32_t max_blocks_per_seq,

@@ -137,8 +137,8 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int32_t grid, cudaStream
 
 // Attention of several query positions per request under a tree or window
 // mask (paged_masked_tc.cu).  d.q_len = query positions per request (the
-// padded tree size).  A split is tiles_per_split tiles of
-// masked_tile_blocks(q_len) blocks of the list of blocks a CTA reads; more
+// padded tree size).  A split is tiles_per_split tiles of kMaskedTileBlocks
+// blocks of the list of blocks a CTA reads; more
 // than one split: partials to the workspace for the combine kernel when
 // d.part_o is set, else (<= kMaxClusterSplits) merged in a cluster.
 enum class MaskKind { kTree, kWindow };
@@ -147,6 +147,7 @@ struct MaskedArgs {
   const int32_t* tree_lens;   // tree: [B] drafted tokens at the end of each context; NULL = q_len
   const uint64_t* tree_mask;  // tree: [B][q_len][mask_words], bit j = draft j is visible
   int32_t mask_words;
+  int32_t wide;               // CTAs of 256 rows (64 positions), else of 128
   int32_t window;             // window: keys p - window + 1 .. p, and
   int32_t num_sinks;          //         keys 0 .. num_sinks - 1
   int32_t tiles_per_split;
@@ -157,12 +158,12 @@ struct MaskedArgs {
 };
 constexpr int kMaxRanked = 256;  // every CTA orders the lengths: about 1 us for 256
 cudaError_t launch_paged_masked_tc(const MaskedArgs& a, MaskKind mask, cudaStream_t stream);
-int masked_tile_blocks(int q_len);
-int masked_positions_per_cta(int q_len);
-int masked_ctas_per_sm(int q_len);
+constexpr int kMaskedTileBlocks = 4;
+int masked_positions_per_cta(bool wide);
+int masked_ctas_per_sm(bool wide);
 // Thread-block clusters of `splits` CTAs resident at once on the current
 // device, whose number is `device` (0: no device to ask).
-int masked_max_clusters(int q_len, int splits, int device);
+int masked_max_clusters(bool wide, int splits, int device);
 
 // Norms of queries and keys, rotation and append in one pass (qk_norm_rope.cu).
 struct QkNormRopeArgs {
