@@ -1008,7 +1008,7 @@ bool masked_sizes_ok(int32_t num_seqs, int32_t num_heads, int32_t q_len, int32_t
          max_blocks <= kMaskedMaxBlocks && (tree || (window > 0 && num_sinks >= 0));
 }
 
-constexpr int32_t kFewTiles = 8;
+constexpr int32_t kFewTiles = 8;  // of 64 tokens: below, a unit costs more beside its tiles than in them
 
 int32_t span_limit(int32_t x) { return x < kMaskedMaxSpan ? x : kMaskedMaxSpan; }
 
@@ -1068,16 +1068,18 @@ pkv_status masked_impl(MaskKind mask, void* out, const void* q, const void* k_ca
   // More CTAs than are resident at once: either each takes several units
   // (what a unit costs beside its tiles, about 5 us, is then partly hidden), or
   // the longest requests start first and the hardware deals out the rest.  The
-  // first where the units read about as much, the chunks of a window, or
-  // little: 4 chunks of 2000, window 4096: 366 us against 395; 83 single
-  // queries, window 17: 17.1 against 20.5; but 64 of contexts from 16 to
-  // 32,000, window 2000: 47 against 43.
+  // first where the units read little, or about as much (long chunks of a
+  // window): 83 single queries, window 17: 16 us against 20.5; 32 x 128, window
+  // 500: 58.5 against 62.6; 4 chunks of 2000, window 4096: 370 against 395; but
+  // 64 of contexts from 16 to 32,000, window 2000: 47 against 43, and 40 x 100,
+  // window 2000: 85 against 77.
   const int32_t pos = masked_positions_per_cta(plan.wide);
   const int64_t ctas = static_cast<int64_t>(num_seqs) * cache->num_kv_heads * ((q_len + pos - 1) / pos);
   if (ctas > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   a.resident = masked_ctas_per_sm(plan.wide) * device_sm_count();
   const bool waves = plan.splits == 1 && ctas > a.resident;
-  a.rounds = waves && (plan.tiles <= kFewTiles || (!tree && q_len > pos));
+  a.rounds = waves && (plan.tiles <= kFewTiles ||
+                       (!tree && q_len > pos && (plan.tiles <= 2 * kFewTiles || q_len >= 8 * pos)));
   a.longest_first = waves && !a.rounds && q_len <= pos && num_seqs <= kMaxRanked;
   const int64_t span = tree ? int64_t{0x7fffffff} : static_cast<int64_t>(a.window) + q_len + a.num_sinks;
   a.span = static_cast<int32_t>(span < 0x7fffffff ? span : 0x7fffffff);

@@ -140,3 +140,25 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for x, want in got:
         assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_captured_and_replayed_with_new_inputs(q_len):
+    window, sinks = 60, 3
+    ctx = contexts(np.random.default_rng(8), 70, 200)
+    d = _cuda(V.paged_case(ctx, q_len, 16, 7))
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(max(256, pkv.workspace_size_window(70, q_len, 64, d["block_tables"].shape[1], window, sinks)),
+                     dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.paged_attention_window(out, d["q"], d["k_cache"], d["v_cache"], d["block_tables"], d["context_lens"],
+                                   q_len, window, sinks, V.SCALE, workspace=ws)
+    for shift in (0, 11):  # the second time every request takes another's length, tables and queries
+        for k in ("q", "block_tables", "context_lens"):
+            d[k].copy_(d[k].roll(shift, 0))
+        ctx = ctx[-shift:] + ctx[:-shift] if shift else ctx
+        g.replay()
+        ref, tol = V.attention64(d, V.window_allowed(ctx, q_len, window, sinks))
+        torch.cuda.synchronize()
+        V.assert_within(out, ref, tol, f"replay after a shift of {shift}")
