@@ -651,7 +651,9 @@ pkv_status pkv_paged_attention_tree(void* out, const void* q, const void* k_cach
  *   kv_blocks_per_split, workspace : as for pkv_paged_attention_tree, counted in
  *                  the blocks that a request's queries see.
  * Blocks that no query of the call sees are neither read nor looked up: their
- * table entries may be stale (the pages given back).
+ * table entries may be stale (the pages given back).  In the blocks that are
+ * read, K and V of every token of the context must be finite (a block that is
+ * seen in part is read whole); slots past the context may hold anything.
  */
 int32_t pkv_choose_kv_blocks_per_split_window(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
                                               int32_t max_blocks_per_seq, int32_t window, int32_t num_sinks,
