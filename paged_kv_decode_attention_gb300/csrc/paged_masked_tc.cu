@@ -59,7 +59,7 @@
 //                              pipe 71 % active (85 % on the busiest SM)
 //   window 2000 + 4 sinks, 64 single queries   43 us: 5.2 TB/s; the tail of
 //                              unequal lengths is what is left
-//   window 4096 + 4 sinks, 4 chunks of 2000    370 us: 1380 cycles a tile and
+//   window 4096 + 4 sinks, 4 chunks of 2000    355 to 370 us: 1380 cycles a tile and
 //                              pair of row tiles where the pipe needs 1280, and
 //                              7 % around a unit (kRounds; one unit per CTA 395)
 #include <algorithm>
@@ -83,12 +83,15 @@ constexpr int kPosPerTile = kRowsPerTile / kGroup;         // query positions of
 constexpr int kQTileBytes = kRowsPerTile * kHeadDim * 2;   // 32 KiB, two 64-dim halves
 constexpr int kQHalfBytes = kQTileBytes / 2;
 
-template <int kQTiles>
+// kTwoQ: two query buffers, so that the next unit's queries come while the
+// present one is worked on (three stages a ring are as good as five for that).
+template <int kQTiles, bool kTwoQ = false>
 struct Shape {
+  static constexpr int kQBufs = kTwoQ ? 2 : 1;
   static constexpr int kTileBlocks = kMaskedTileBlocks;
   static constexpr int kTileTokens = kTileBlocks * kBlockSize;  // 64
-  static constexpr int kKStages = kQTiles == 1 ? 3 : 5;
-  static constexpr int kVStages = kQTiles == 1 ? 2 : 5;
+  static constexpr int kKStages = kQTiles == 1 || kTwoQ ? 3 : 5;
+  static constexpr int kVStages = kQTiles == 1 ? 2 : (kTwoQ ? 3 : 5);
   static constexpr int kHalfBytes = kTileTokens * 128;
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kWarps = 4 + 4 * kQTiles;
@@ -101,7 +104,7 @@ struct Shape {
   static constexpr int kSoftmaxRegs = kQTiles == 1 ? 192 : 208;
   static_assert((kIssueRegs + kQTiles * kSoftmaxRegs) * 128 <= kLaunchRegs * kThreads, "register split");
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kQTiles * kQTileBytes;
+  static constexpr int kOffK = kQBufs * kQTiles * kQTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kStageBytes;
   static constexpr int kOffBar = kOffV + kVStages * kStageBytes;
   static constexpr int kSmem = kOffBar + 512;
@@ -109,7 +112,7 @@ struct Shape {
   // drained, then (max, sum) per row
   static constexpr int kOffPartO = kOffK;
   static constexpr int kOffPartML = kOffPartO + kQTiles * kRowsPerTile * kHeadDim * 4;
-  static_assert(kOffPartML + kQTiles * kRowsPerTile * 8 <= kOffBar, "the partials fit in the rings");
+  static_assert(kTwoQ || kOffPartML + kQTiles * kRowsPerTile * 8 <= kOffBar, "the partials fit in the rings");
   static constexpr uint32_t kColO = 2 * kTileTokens;          // two S/P buffers, then O (128 columns)
   static constexpr uint32_t kTileCols = kColO + kHeadDim;     // 256 columns per row tile
   static constexpr uint32_t kTmemCols = kQTiles * kTileCols;  // 256 or 512
@@ -118,9 +121,9 @@ struct Shape {
   static_assert(kSmem <= (kQTiles == 1 ? 113 : 227) * 1024, "shared memory per CTA");
 };
 
-template <int kQTiles>
+template <int kQTiles, bool kTwoQ = false>
 struct Bars {
-  using S = Shape<kQTiles>;
+  using S = Shape<kQTiles, kTwoQ>;
   uint64_t k_full[S::kKStages];
   uint64_t k_empty[S::kKStages];
   uint64_t v_full[S::kVStages];
@@ -128,11 +131,11 @@ struct Bars {
   uint64_t s_full[kQTiles][2];
   uint64_t p_full[kQTiles][2];
   uint64_t o_done[kQTiles][2];
-  uint64_t q_full[kQTiles];  // per unit whose row tile has queries
+  uint64_t q_full[kQTiles][S::kQBufs];  // per unit whose row tile has queries
   uint32_t tmem_base;
   int32_t request;              // longest_first: the request of this CTA
 };
-static_assert(sizeof(Bars<2>) <= 512, "barrier area");
+static_assert(sizeof(Bars<2>) <= 512 && sizeof(Bars<2, true>) <= 512, "barrier area");
 
 // How the splits of one (row tile, KV head) come together.
 enum class MaskedMode {
@@ -141,6 +144,9 @@ enum class MaskedMode {
   kWorkspace,  // FP32 partials to the workspace, merged by the combine kernel
   kCluster     // one thread-block cluster: merged through distributed shared memory
 };
+
+template <int kQTiles, MaskedMode kMode>
+using ShapeOf = Shape<kQTiles, kMode == MaskedMode::kRounds && kQTiles == 2>;
 
 // Move registers between warpgroups (all warps of one execute it).
 template <int kRegs>
@@ -160,9 +166,11 @@ __device__ __forceinline__ uint64_t low_bits(int x) {
 template <int kQTiles, MaskKind kMask, MaskedMode kMode>
 __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, const CUtensorMap& v_map,
                                                      const MaskedArgs& a) {
-  using S = Shape<kQTiles>;
+  constexpr bool kMany = kMode == MaskedMode::kRounds;
+  using S = ShapeOf<kQTiles, kMode>;
+  constexpr bool kTwoQ = S::kQBufs == 2;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Bars<kQTiles>* bars = reinterpret_cast<Bars<kQTiles>*>(smem + S::kOffBar);
+  auto* bars = reinterpret_cast<Bars<kQTiles, kTwoQ>*>(smem + S::kOffBar);
   // Warp indexes, tile counts and addresses go through a broadcast so that the
   // compiler knows them to be uniform: the issuing warps' descriptors then
   // live in uniform registers, where the MMA instructions read them.
@@ -186,7 +194,8 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         mbar_init(&bars->p_full[t][s], 128);
         mbar_init(&bars->o_done[t][s], 1);
       }
-    for (int t = 0; t < kQTiles; ++t) mbar_init(&bars->q_full[t], 128);
+    for (int t = 0; t < kQTiles; ++t)
+      for (int b = 0; b < S::kQBufs; ++b) mbar_init(&bars->q_full[t][b], 128);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -210,7 +219,6 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
   // back over the grid; the rings run on, so that a unit's copies are under
   // way while the one before ends.
   constexpr int kPos = kPosPerTile * kQTiles;  // query positions per CTA
-  constexpr bool kMany = kMode == MaskedMode::kRounds;
   constexpr bool kToOut = kMode == MaskedMode::kDirect || kMany;
   const int n_rt = (a.d.q_len + kPos - 1) / kPos;
   const uint32_t n_units = static_cast<uint32_t>(a.d.num_seqs) * a.d.num_kv_heads * n_rt;
@@ -410,9 +418,9 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         if (leader) mbar_arrive(bar);
       };
       // S of the tile in K stage st, into buffer buf
-      auto issue_s = [&](int buf, int st) {
+      auto issue_s = [&](int buf, int st, int qb) {
         const uint32_t d = tcol + buf * S::kTileTokens;
-        const uint64_t qd = q_desc + t * (kQTileBytes >> 4);
+        const uint64_t qd = q_desc + (qb * kQTiles + t) * (kQTileBytes >> 4);
         const uint64_t kd = k_desc + st * (S::kStageBytes >> 4);
         tc::fence_after_sync();
         if (leader) {
@@ -439,7 +447,14 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
         __syncwarp();
       };
       uint32_t g = 0;               // tiles of this row tile so far
-      int q_phase = 0;
+      int units = 0;                // of this row tile so far
+      int ahead_ctx = 0, ahead_len = 0;  // kRounds: the next unit's lengths, read a round ahead
+      Unit ahead;
+      bool more = kMany && place(0, ahead);
+      if (more) {
+        ahead_ctx = a.d.context_lens[ahead.r];
+        ahead_len = tree_len(ahead.r);
+      }
       int ks = 0, kph = 0;          // stage and phase of the next S
       int vs = 0, vph = 0, pk = 0;  // of the next P.V, and its tile's K stage
       auto next_k = [&]() {
@@ -458,8 +473,14 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       for (int round = 0; round < rounds && ok; ++round) {
         Unit w = unit0;
         if (kMany) {
-          if (!place(round, w)) continue;
-          measure(w, a.d.context_lens[w.r], tree_len(w.r));
+          if (!more) break;
+          w = ahead;
+          measure(w, ahead_ctx, ahead_len);
+          more = round + 1 < rounds && place(round + 1, ahead);
+          if (more) {
+            ahead_ctx = a.d.context_lens[ahead.r];
+            ahead_len = tree_len(ahead.r);
+          }
         }
         const int n_tiles = w.n_tiles;
         if (n_tiles <= 0) continue;
@@ -474,11 +495,12 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           }
           continue;
         }
-        ok = wait(&bars->q_full[t], q_phase);
-        q_phase ^= 1;
+        const int qb = S::kQBufs == 2 ? units & 1 : 0;
+        ok = wait(&bars->q_full[t][qb], (S::kQBufs == 2 ? units >> 1 : units) & 1);
+        ++units;
         for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
           ok = wait(&bars->k_full[ks], kph);
-          if (ok) issue_s((g + j) & 1, ks);
+          if (ok) issue_s((g + j) & 1, ks, qb);
           next_k();
         }
         for (int j = 0; j < n_tiles && ok; ++j, ++g) {
@@ -492,7 +514,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
             ok = ok && wait2(&bars->k_full[ks], kph, &bars->o_done[t][buf], ph);
             if (ok) {
               give_back(&bars->v_empty[vs]);
-              issue_s(buf, ks);
+              issue_s(buf, ks, qb);
             }
             next_k();
           }
@@ -518,26 +540,30 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
     const int row = quad * 32 + lane;
     uint32_t g = 0;       // tiles of this row tile so far
     uint32_t v_tile = 0;  // tiles through the V ring so far
-    bool fresh = true;    // no unit has used the query area yet
-    // kRounds: the next unit, its lengths read a round ahead
-    Unit ahead;
-    bool more = kMany && place(0, ahead);
-    int ahead_ctx = 0, ahead_len = 0;
-    if (more) {
-      ahead_ctx = a.d.context_lens[ahead.r];
-      ahead_len = tree_len(ahead.r);
+    int units = 0;        // of this row tile so far
+    bool loaded = false;  // kTwoQ: the unit's queries are in their buffer
+    // kRounds: the next two units, their lengths read that much ahead
+    // (their places are worked out again: registers are dearer than that)
+    int ahead_ctx = 0, ahead_len = 0, far_ctx = 0, far_len = 0;
+    auto read_lengths = [&](int round, int& ctx, int& n_new) {
+      Unit u;
+      if (round < rounds && place(round, u)) {
+        ctx = a.d.context_lens[u.r];
+        n_new = tree_len(u.r);
+      }
+    };
+    if constexpr (kMany) {
+      read_lengths(0, ahead_ctx, ahead_len);
+      read_lengths(1, far_ctx, far_len);
     }
     for (int round = 0; round < rounds; ++round) {
     Unit w = unit0;
     if (kMany) {
-      if (!more) break;
-      w = ahead;
+      if (!place(round, w)) break;
       measure(w, ahead_ctx, ahead_len);
-      more = round + 1 < rounds && place(round + 1, ahead);
-      if (more) {
-        ahead_ctx = a.d.context_lens[ahead.r];
-        ahead_len = tree_len(ahead.r);
-      }
+      ahead_ctx = far_ctx;
+      ahead_len = far_len;
+      read_lengths(round + 2, far_ctx, far_len);
     }
     const int r = w.r, kvh = w.kvh, pos0 = w.pos0, ctx = w.ctx, n_new = w.n_new, base = w.base, n_pos = w.n_pos;
     const int first_block = w.first_block, key_end = w.key_end, n_tiles = w.n_tiles;
@@ -575,18 +601,19 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       v_tile += n_tiles;
       continue;
     }
-    // the unit before has left its results' way, the query area (all four warps)
+    // the unit before has left its results' way, its query buffer (all four warps)
     if constexpr (kMany) {
-      if (!fresh) named_barrier_sync(1 + qt, 128);
-      fresh = false;
+      if (units > 0) named_barrier_sync(1 + qt, 128);
     }
-    {
+    const int qb = S::kQBufs == 2 ? units & 1 : 0;
+    ++units;
+    uint8_t* qarea = smem + S::kOffQ + (qb * kQTiles + qt) * kQTileBytes;  // queries, then results on their way out
+    if (!loaded) {
       // this row tile's queries -> 128-byte swizzled K-major tile, two 64-dim
       // halves; thread t loads 16-byte chunk t % 16 of every (threads / 16)-th
       // row, eight loads in flight
       const int ch = tid & 15;
       const uint16_t* qbase = static_cast<const uint16_t*>(a.d.q);
-      uint8_t* qs = smem + S::kOffQ + qt * kQTileBytes;
       constexpr int kStep = 128 / 16;
       constexpr int kDeep = kMany ? 16 : 8;  // loads in flight (16: one trip, 8: fewer registers)
 #pragma unroll
@@ -604,20 +631,46 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
 #pragma unroll
         for (int k = 0; k < kDeep; ++k) {
           const int m = (tid >> 4) + kStep * (k0 + k);
-          *reinterpret_cast<uint4*>(qs + (ch >> 3) * kQHalfBytes + tc::sw128_offset(m, (ch & 7) * 8)) = v[k];
+          *reinterpret_cast<uint4*>(qarea + (ch >> 3) * kQHalfBytes + tc::sw128_offset(m, (ch & 7) * 8)) = v[k];
         }
       }
       tc::fence_proxy_async_smem();
-      mbar_arrive(&bars->q_full[qt]);
+      mbar_arrive(&bars->q_full[qt][qb]);
     }
-    if (kMany && more) {  // the next unit's queries towards L2
-      const int qa = ahead.pos0 + qt * kPosPerTile + (row >> 2);
+    loaded = false;
+    Unit next;
+    if (kMany && !kTwoQ && round + 1 < rounds && place(round + 1, next)) {  // the next unit's queries towards L2
+      const int qa = next.pos0 + qt * kPosPerTile + (row >> 2);
       if (qa < a.d.q_len) {
         const uint16_t* next_q =
             static_cast<const uint16_t*>(a.d.q) +
-            ((static_cast<int64_t>(ahead.r) * a.d.q_len + qa) * hq + ahead.kvh * kGroup + (row & 3)) * kHeadDim;
+            ((static_cast<int64_t>(next.r) * a.d.q_len + qa) * hq + next.kvh * kGroup + (row & 3)) * kHeadDim;
         prefetch_l2(next_q);
         prefetch_l2(next_q + kHeadDim / 2);
+      }
+    }
+    if constexpr (kTwoQ) {
+      // The next unit's queries into the other buffer, if it has some here.
+      // (Before the tiles: inside their loop it costs every tile 4 %.  With one
+      // buffer, 4 x 1480 queries of window 90 take 93.5 us instead of 85.7.)
+      Unit n;
+      if (round + 1 < rounds && place(round + 1, n)) {
+        measure(n, ahead_ctx, ahead_len);
+        loaded = n.n_tiles > 0 && qt < n.q_tiles;
+        if (loaded) {
+          const uint16_t* qn = static_cast<const uint16_t*>(a.d.q) +
+                               ((static_cast<int64_t>(n.r) * a.d.q_len + n.pos0 + qt * kPosPerTile) * hq +
+                                n.kvh * kGroup) * kHeadDim;
+          const uint32_t dst = smem_addr(smem + S::kOffQ + ((qb ^ 1) * kQTiles + qt) * kQTileBytes);
+          const int ch = tid & 15, n_q = n.n_new - n.pos0 - qt * kPosPerTile;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int m = (tid >> 4) + 8 * k;
+            const bool in = (m >> 2) < n_q;
+            cp_async16(dst + (ch >> 3) * kQHalfBytes + tc::sw128_offset(m, (ch & 7) * 8),
+                       qn + (in ? (static_cast<int64_t>(m >> 2) * hq + (m & 3)) * kHeadDim + ch * 8 : 0), in ? 16 : 0);
+          }
+        }
       }
     }
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -766,6 +819,11 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       tc::fence_before_sync();
       mbar_arrive(&bars->p_full[qt][buf]);
     }
+    if (kTwoQ && loaded) {
+      cp_async_wait_all();
+      tc::fence_proxy_async_smem();
+      mbar_arrive(&bars->q_full[qt][qb ^ 1]);
+    }
     v_tile += n_tiles;
     if (tile_live) g += n_tiles;
     // ---- epilogue ----
@@ -782,7 +840,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       tc::fence_after_sync();
       const bool live = row_valid && l != 0.f && ok;  // (a NaN sum stays one)
       const float inv = live ? 1.f / l : 0.f;
-      uint8_t* stage = smem + S::kOffQ + qt * kQTileBytes + quad * 32 * 256;  // this warp's 32 rows of 256 bytes
+      uint8_t* stage = qarea + quad * 32 * 256;  // this warp's 32 rows of 256 bytes
       // 16-byte chunk ch of row m sits at chunk ch ^ (m % 8): four wavefronts either way
       auto chunk = [&](int m, int ch) -> uint4* { return reinterpret_cast<uint4*>(stage + m * 256 + ((ch ^ (m & 7)) << 4)); };
       if constexpr (kMode == MaskedMode::kCluster) {
@@ -927,7 +985,7 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
 }
 
 template <int kQTiles, MaskKind kMask, MaskedMode kMode>
-__global__ void __launch_bounds__(Shape<kQTiles>::kThreads, Shape<kQTiles>::kCtasPerSm)
+__global__ void __launch_bounds__(ShapeOf<kQTiles, kMode>::kThreads, ShapeOf<kQTiles, kMode>::kCtasPerSm)
     paged_masked_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                            const MaskedArgs a) {
   paged_masked_tc_body<kQTiles, kMask, kMode>(k_map, v_map, a);
@@ -942,7 +1000,7 @@ cudaError_t allow_smem(int* device) {
   if (*device < 0 || *device >= 64) return cudaErrorInvalidDevice;
   if (!done[*device]) {
     e = cudaFuncSetAttribute(paged_masked_tc_kernel<kQTiles, kMask, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<kQTiles>::kSmem);
+                             ShapeOf<kQTiles, kMode>::kSmem);
     if (e != cudaSuccess) return e;
     done[*device] = true;
   }
@@ -986,7 +1044,7 @@ int max_clusters(int splits, int dev) {
 template <int kQTiles, MaskKind kMask, MaskedMode kMode>
 cudaError_t launch_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, const MaskedArgs& a,
                            cudaStream_t stream) {
-  using S = Shape<kQTiles>;
+  using S = ShapeOf<kQTiles, kMode>;
   int dev = 0;
   const cudaError_t e = allow_smem<kQTiles, kMask, kMode>(&dev);
   if (e != cudaSuccess) return e;

@@ -220,6 +220,15 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// Asynchronous copy of 16 bytes from global to shared memory, `bytes` (0 or
+// 16) of them read and the rest zeros.
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* gmem_src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst),
+               "l"(reinterpret_cast<uint64_t>(gmem_src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Hint: bring the 128-byte line holding `p` into this SM's L1.
 __device__ __forceinline__ void prefetch_l1(const void* p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)) : "memory");
