@@ -61,7 +61,7 @@
 //                              unequal lengths is what is left
 //   window 4096 + 4 sinks, 4 chunks of 2000    355 to 370 us: 1380 cycles a tile and
 //                              pair of row tiles where the pipe needs 1280, and
-//                              7 % around a unit (kRounds; one unit per CTA 395)
+//                              some 5 % around a unit (kRounds; one unit per CTA 395)
 #include <algorithm>
 #include <climits>
 #include <cmath>
