@@ -347,19 +347,24 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           measure(w, a.d.context_lens[w.r], tree_len(w.r));
         }
         const int32_t* table = a.d.block_tables + static_cast<int64_t>(w.r) * a.d.max_blocks;
-        // entry i of the list of blocks (whole tiles of sinks, then the window):
-        // its block id, or INT_MIN for a hole or past the range
-        auto entry = [&](int i) -> int {
-          if (i >= w.n_tiles * S::kTileBlocks) return INT_MIN;
-          if (kMask == MaskKind::kTree && i < 32)  // read above
-            return t_first * S::kTileBlocks + i < w.end_block ? first_ids : INT_MIN;
+        // logical block of entry i of the list of blocks (whole tiles of sinks,
+        // then the window), or -1 for a hole or past the range.  Kept apart
+        // from the table's entries, which may hold any value.
+        auto logical = [&](int i) -> int {
+          if (i >= w.n_tiles * S::kTileBlocks) return -1;
           i += t_first * S::kTileBlocks;
           const int sink_entries = w.sink_tiles * S::kTileBlocks;
           const int lb = i < sink_entries ? (i < w.sink_blocks ? i : INT_MAX) : w.first_block + i - sink_entries;
-          return lb < w.end_block ? table[lb] : INT_MIN;
+          return lb < w.end_block ? lb : -1;
         };
-        auto row_of = [&](int blk) -> int {
-          if (blk == INT_MIN) return oob_row;
+        // its block id, checked where it is used
+        auto entry = [&](int i) -> int {
+          if (kMask == MaskKind::kTree && i < 32) return first_ids;  // read above
+          const int lb = logical(i);
+          return lb >= 0 ? table[lb] : 0;
+        };
+        auto row_of = [&](int i, int blk) -> int {
+          if (logical(i) < 0) return oob_row;
           if (blk < 0 || blk >= a.d.num_blocks) {
             report(a.d.err, PKV_DEVERR_BLOCK_ID);
             blk = 0;
@@ -367,12 +372,12 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           return (blk * a.d.num_kv_heads + w.kvh) * kBlockSize;
         };
         constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
-        int cur = row_of(entry(lane)), nxt = INT_MIN;
+        int cur = row_of(lane, entry(lane)), nxt = 0;
         for (int j = 0; j < w.n_tiles && ok; ++j, ++filled) {
           const int in_chunk = j % kTilesPerChunk;
           if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
           const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
-          if (in_chunk == kTilesPerChunk - 1) cur = row_of(nxt);
+          if (in_chunk == kTilesPerChunk - 1) cur = row_of((j + 1) * S::kTileBlocks + lane, nxt);
           const int st = filled % stages;
           if (filled >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((filled / stages) & 1) ^ 1));
           if (!ok) break;

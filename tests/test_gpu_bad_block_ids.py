@@ -1,0 +1,71 @@
+"""A block table entry that names no block of the pool is reported, whatever
+its value: the lowest 32-bit integer too, in the block ids that a kernel reads
+first and in those that it reads later, and in the last block of a context."""
+import pytest
+import torch
+
+import verify_util as V
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import paged_kv_decode_attention_gb300 as pkv
+else:  # collected on CPU-only machines, every test skipped
+    pkv = None
+
+LOWEST = -2 ** 31
+CTX = [1000, 1000]
+PLACES = (0, 17, 31, 32, 50, 62)  # logical blocks of request 1
+
+
+@pytest.fixture(autouse=True)
+def _clear_device_error():
+    if pkv is not None:
+        pkv.get_device_error(reset=True)
+    yield
+    if pkv is not None:
+        assert pkv.get_device_error(reset=True) == 0
+
+
+def _case(q_len, hkv, seed, ctx=CTX):
+    d = {k: v.cuda() for k, v in V.paged_case(ctx, q_len, hkv, seed).items()}
+    d["k_cache"][0] = d["v_cache"][0] = 0.25  # what a bad id reads may be a block nobody holds
+    return d
+
+
+def _reported(call, out, tables):
+    """call() with request 1's entries replaced one at a time: the error word is set, request 0 keeps its result, and
+    request 1's is that of block 0 in the entry's place (what the kernels read for a bad id)."""
+    call()
+    good = out.clone()
+    assert pkv.get_device_error(reset=True) == 0
+    for at in PLACES:
+        saved = int(tables[1, at])
+        tables[1, at] = 0
+        call()
+        block0 = out.clone()
+        assert pkv.get_device_error(reset=True) == 0
+        for bad in (LOWEST, LOWEST + 1, -1):
+            tables[1, at] = bad
+            call()
+            assert pkv.get_device_error(reset=True) == pkv.DEVERR_BLOCK_ID, (at, bad)
+            assert torch.equal(out[0], good[0]), (at, bad)
+            assert torch.equal(out[1], block0[1]), (at, bad)
+        tables[1, at] = saved
+
+
+@pytest.mark.parametrize("q_len", [1, 16, 40, 70])
+@pytest.mark.parametrize("bps", [0, 4, 20, 1 << 20])
+@pytest.mark.parametrize("mask", ["tree", "window"])
+def test_masked_attention(mask, q_len, bps):
+    d = _case(q_len, 2, q_len + bps % 7)
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    words = V.masks_to_words([[list(range(i + 1)) for i in range(q_len)]] * 2, q_len).cuda()
+    args = (out, d["q"], d["k_cache"], d["v_cache"], d["block_tables"], d["context_lens"])
+    if mask == "tree":
+        call = lambda: pkv.paged_attention_tree(*args, words, V.SCALE, kv_blocks_per_split=bps, workspace=ws)
+    else:  # a window that sees every block
+        call = lambda: pkv.paged_attention_window(*args, q_len, 2000, 4, V.SCALE, kv_blocks_per_split=bps,
+                                                  workspace=ws)
+    _reported(call, out, d["block_tables"])
