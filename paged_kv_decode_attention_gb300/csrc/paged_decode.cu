@@ -51,7 +51,6 @@
 //              second kernel;
 //   kWorkspace more splits: each writes its normalised FP32 output and
 //              natural-log lse to the workspace for the combine kernel.
-#include <climits>
 #include <cmath>
 
 #include "pkv_common.cuh"
@@ -280,18 +279,19 @@ __device__ __forceinline__ void paged_decode_body(const DecodeArgs& a) {
       const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache);
       bool ok = true;
       int issued = 0;
-      // block ids of a 32-block chunk, one per lane (INT_MIN past the range);
-      // validated only when the chunk is used (a bad id reads block 0), so the
-      // load of the next chunk stays in flight while this one streams
-      auto chunk = [&](int base) -> int { return base + lane < n_iter ? table[base + lane] : INT_MIN; };
+      // block ids of a 32-block chunk, one per lane (past the range 0, never
+      // used); validated only when the chunk is used (a bad id, of any value,
+      // reads block 0), so the load of the next chunk stays in flight while
+      // this one streams
+      auto chunk = [&](int base) -> int { return base + lane < n_iter ? table[base + lane] : 0; };
       auto checked = [&](int b) -> int {
-        if (b != INT_MIN && (b < 0 || b >= a.num_blocks)) {
+        if (b < 0 || b >= a.num_blocks) {
           report(a.err, PKV_DEVERR_BLOCK_ID);
           b = 0;
         }
         return b;
       };
-      int blk_next = lane < n_iter ? first_ids : INT_MIN;  // chunk(0), loaded at the top
+      int blk_next = lane < n_iter ? first_ids : 0;  // chunk(0), loaded at the top
       for (int base = 0; base < n_iter && ok; base += 32) {
         const int blk = checked(blk_next);
         blk_next = chunk(base + 32);  // the next chunk's ids, read while this one streams

@@ -69,3 +69,15 @@ def test_masked_attention(mask, q_len, bps):
         call = lambda: pkv.paged_attention_window(*args, q_len, 2000, 4, V.SCALE, kv_blocks_per_split=bps,
                                                   workspace=ws)
     _reported(call, out, d["block_tables"])
+
+
+@pytest.mark.parametrize("q_len", [1, 3])
+@pytest.mark.parametrize("bps", [0, 1, 4, 13, 1 << 20])
+def test_decode_one_cta_per_row(q_len, bps):
+    """The CTA-per-row decode: one pass, splits merged in a cluster, splits through the workspace."""
+    d = _case(q_len, 2, q_len + bps % 7)
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    _reported(lambda: pkv.paged_attention(out, d["q"], d["k_cache"], d["v_cache"], d["block_tables"],
+                                          d["context_lens"], q_len, V.SCALE, kv_blocks_per_split=bps, workspace=ws),
+              out, d["block_tables"])
