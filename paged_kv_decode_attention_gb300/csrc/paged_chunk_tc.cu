@@ -202,12 +202,12 @@ __device__ __forceinline__ void paged_chunk_tc_body(const CUtensorMap& k_map, co
     const int32_t* table = a.block_tables + static_cast<int64_t>(table_row) * a.max_blocks;
     const int oob_row = a.num_blocks * a.num_kv_heads * kBlockSize;  // first row past the pool
     const int n_blocks = b1 - b0;
-    // block id of block base + lane of the range, INT_MIN past it
-    auto chunk = [&](int base) -> int { return base + lane < n_blocks ? table[b0 + base + lane] : INT_MIN; };
-    // its pool row (a bad id reads block 0); past the range, the first row
-    // past the pool (zero fill)
-    auto row_of = [&](int blk) -> int {
-      if (blk == INT_MIN) return oob_row;
+    // block id of block base + lane of the range, checked where it is used
+    auto chunk = [&](int base) -> int { return base + lane < n_blocks ? table[b0 + base + lane] : 0; };
+    // its pool row (a bad id, of any value, reads block 0); past the range,
+    // the first row past the pool (zero fill)
+    auto row_of = [&](int base, int blk) -> int {
+      if (base + lane >= n_blocks) return oob_row;
       if (blk < 0 || blk >= a.num_blocks) {
         report(a.err, PKV_DEVERR_BLOCK_ID);
         blk = 0;
@@ -218,12 +218,12 @@ __device__ __forceinline__ void paged_chunk_tc_body(const CUtensorMap& k_map, co
     // only when their chunk is used, so the next chunk's load stays in flight.
     // The 8 boxes of a tile (4 blocks x two 64-dim halves) are issued by 8
     // lanes at once: lane 2b + c takes block b, half c.
-    int cur = row_of(chunk(0)), nxt = INT_MIN;
+    int cur = row_of(0, chunk(0)), nxt = 0;
     for (int j = 0; j < n_tiles && ok; ++j) {
       const int slot = j & 7;
       if (slot == 0) nxt = chunk((j + 8) * kTileBlocks);
       const int yy = __shfl_sync(0xffffffffu, cur, slot * kTileBlocks + ((lane >> 1) & 3));
-      if (slot == 7) cur = row_of(nxt);
+      if (slot == 7) cur = row_of((j + 1) * kTileBlocks, nxt);
       const int st = j % kTcStages;
       if (j >= kTcStages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((j / kTcStages) & 1) ^ 1));
       if (!ok) break;

@@ -182,12 +182,10 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
     const int32_t* table = a.block_tables + static_cast<int64_t>(x.r) * a.max_blocks;
     // the load stays inside the table row whatever the context length, so it
     // need not wait for that length; entries past the unit's blocks are dropped
-    auto entry = [&](int bi) -> int {
-      const int raw = table[min(bi, a.max_blocks - 1)];
-      return bi < x.b1 ? raw : INT_MIN;  // checked where used
-    };
+    // where they would be used, and the others (of any value) checked there
+    auto entry = [&](int bi) -> int { return table[min(bi, a.max_blocks - 1)]; };
     int cur = entry(x.b0 + lane);
-    int nxt = INT_MIN;
+    int nxt = 0;
     for (int j = 0; j < x.n_tiles; ++j, ++i) {
       const int slot = j & 1;  // this tile's 16 entries in the current 32-entry chunk
       if (slot == 0) nxt = entry(x.b0 + j * kFtTileBlocks + 32 + lane);
@@ -200,7 +198,7 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
       __syncwarp();
       if (lane < kFtTileBlocks) {
         int y = oob_row;
-        if (blk != INT_MIN) {
+        if (x.b0 + j * kFtTileBlocks + lane < x.b1) {
           int b = blk;
           if (b < 0 || b >= a.num_blocks) {
             report(a.err, PKV_DEVERR_BLOCK_ID);

@@ -81,3 +81,48 @@ def test_decode_one_cta_per_row(q_len, bps):
     _reported(lambda: pkv.paged_attention(out, d["q"], d["k_cache"], d["v_cache"], d["block_tables"],
                                           d["context_lens"], q_len, V.SCALE, kv_blocks_per_split=bps, workspace=ws),
               out, d["block_tables"])
+
+
+@pytest.mark.parametrize("q_len", [16, 40])
+@pytest.mark.parametrize("bps", [0, 4, 13, 1 << 20])
+def test_causal_chunk(q_len, bps):
+    d = _case(q_len, 2, q_len + bps % 7)
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    _reported(lambda: pkv.paged_attention(out, d["q"], d["k_cache"], d["v_cache"], d["block_tables"],
+                                          d["context_lens"], q_len, V.SCALE, kv_blocks_per_split=bps, workspace=ws),
+              out, d["block_tables"])
+
+
+@pytest.mark.parametrize("bps", [0, 8, 20, 1 << 20])
+def test_decode_of_a_large_batch(bps):
+    """Enough rows for the tensor-core decode (two per SM)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    d = _case(1, 8, 3, ctx=CTX + [40] * (-(-2 * sms // 8) - 2))
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    _reported(lambda: pkv.paged_attention(out, d["q"], d["k_cache"], d["v_cache"], d["block_tables"],
+                                          d["context_lens"], 1, V.SCALE, kv_blocks_per_split=bps, workspace=ws),
+              out, d["block_tables"])
+
+
+@pytest.mark.parametrize("bps", [0, 16, 20, 1 << 20])
+@pytest.mark.parametrize("fmt", ["e4m3", "q8_0"])
+def test_decode_of_quantised_caches(fmt, bps):
+    d = _case(1, 2, 5)
+    n = d["k_cache"].shape[0]
+    gen = torch.Generator().manual_seed(7)
+    pools = []
+    for _ in range(2):
+        x = torch.randn((n, 2, 16, 128), generator=gen)
+        if fmt == "e4m3":
+            pools.append(x.to(torch.float8_e4m3fn).view(torch.uint8).cuda())
+        else:  # a tile: 16 x 128 codes, then 16 x 4 scales
+            codes = (x * 30).clamp(-127, 127).to(torch.int8).view(n, 2, 2048).view(torch.uint8)
+            scales = torch.full((n, 2, 64), 1 / 30, dtype=torch.float16).view(torch.uint8)
+            pools.append(torch.cat([codes, scales], -1).contiguous().cuda())
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    attend = pkv.paged_attention_fp8_e4m3 if fmt == "e4m3" else pkv.paged_attention_q8_0
+    _reported(lambda: attend(out, d["q"], *pools, d["block_tables"], d["context_lens"], V.SCALE,
+                             kv_blocks_per_split=bps, workspace=ws), out, d["block_tables"])
