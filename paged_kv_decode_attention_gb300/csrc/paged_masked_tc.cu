@@ -969,7 +969,9 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kMaxClusterSplits; ++k) {
-        if (ms[k] == -INFINITY) continue;  // saw nothing: its O holds anything
+        // saw nothing: its O holds anything (a row whose scores are all NaN
+        // leaves the maximum at -inf too, but its sum is NaN)
+        if (ls[k] == 0.f) continue;
         const float w = exp2_approx(ms[k] - mx);
         sum = fmaf(ls[k], w, sum);
         o.x = fmaf(os[k].x, w, o.x);
