@@ -311,7 +311,8 @@ pkv_status pkv_paged_attention_static_workspace(void* out, const void* q, const 
  *   out_lse     : optional device FP32 [num_rows] (NULL to skip): the merged
  *                 log-sum-exp.
  * out = sum_s exp(lse_s - lse) * O_s with lse = log sum_s exp(lse_s); a row
- * whose splits are all empty gets zeros (and out_lse = -inf).
+ * whose splits are all empty gets zeros (and out_lse = -inf), one with a NaN
+ * lse gets NaN.
  */
 pkv_status pkv_attn_combine(void* out, float* out_lse, const float* partial_o,
                             const float* partial_lse, int32_t num_rows, int32_t head_dim,

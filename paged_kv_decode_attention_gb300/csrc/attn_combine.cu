@@ -5,7 +5,8 @@
 // the same identity the blockwise (FlashAttention-style) evaluation named in
 // "Chapter 8: Inference Optimization" §8.3.1 applies inside one CTA, applied
 // here across CTAs.  One warp per output row; lane l owns dims 4l..4l+3.
-// Splits with lse = -inf (no keys) are skipped without reading their output.
+// Splits with lse = -inf (no keys) are skipped without reading their output;
+// a NaN lse makes the row NaN, whatever the other splits hold.
 #include <cmath>
 
 #include "pkv_common.cuh"
@@ -41,9 +42,9 @@ __global__ void __launch_bounds__(kThreadsCombine) attn_combine_kernel(uint16_t*
 
   float mx = -INFINITY;
   if (live)
-    for (int s = lane; s < num_splits; s += 32) mx = fmaxf(mx, lse[s]);
+    for (int s = lane; s < num_splits; s += 32) mx = fmax_nan(mx, lse[s]);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  for (int off = 16; off > 0; off >>= 1) mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 
   float o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f, sum = 0.f;
   if (live && mx != -INFINITY) {

@@ -220,6 +220,13 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// The larger of two values, NaN if either is (fmaxf drops a NaN).
+__device__ __forceinline__ float fmax_nan(float x, float y) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
+
 // Asynchronous copy of 16 bytes from global to shared memory, `bytes` (0 or
 // 16) of them read and the rest zeros.
 __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* gmem_src, int bytes) {
