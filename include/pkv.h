@@ -649,8 +649,10 @@ pkv_status pkv_paged_attention_tree(void* out, const void* q, const void* k_cach
  *   window       : >= 1, the query's own token included.
  *   num_sinks    : >= 0.
  *   scale        : > 0.
- *   kv_blocks_per_split, workspace : as for pkv_paged_attention_tree, counted in
- *                  the blocks that a request's queries see.
+ *   kv_blocks_per_split, workspace : as for pkv_paged_attention_tree, but the
+ *                  split cuts the list of blocks that 32 or 64 neighbouring
+ *                  queries of a request (those of one CTA) see: the sinks'
+ *                  blocks in whole tiles of 4, then the window's.
  * Blocks that no query of the call sees are neither read nor looked up: their
  * table entries may be stale (the pages given back).  In the blocks that are
  * read, K and V of every token of the context must be finite (a block that is

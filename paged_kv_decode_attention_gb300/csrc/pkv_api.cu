@@ -971,6 +971,9 @@ MaskedPlan masked_plan(int64_t num_seqs, int64_t num_kv_heads, int32_t q_len, in
       const int32_t tps = (p.tiles + want - 1) / want;
       const int32_t splits = (p.tiles + tps - 1) / tps;
       if (splits != want) continue;  // the same as a smaller count
+      // (a window's list can be a tile longer than the table: a split as long
+      // as the table could not be told from one pass when it is asked for)
+      if (splits > 1 && tps * tb >= max_blocks) continue;
       int64_t resident = slots / splits;
       if (device >= 0 && splits > 1 && splits <= kMaxClusterSplits) {
         // (the query counts one CTA per SM for kernels with tensor memory; per_sm of them do run)
