@@ -189,8 +189,9 @@ _lib, _path = _load()
 
 def _load_binding():
     """The C++ entry points (csrc/py_binding.cpp) of the calls that serve single tokens."""
-    loader = importlib.machinery.ExtensionFileLoader("_pkv_binding", _build.BINDING)
-    spec = importlib.util.spec_from_file_location("_pkv_binding", _build.BINDING, loader=loader)
+    path = _build.binding_path()
+    loader = importlib.machinery.ExtensionFileLoader("_pkv_binding", path)
+    spec = importlib.util.spec_from_file_location("_pkv_binding", path, loader=loader)
     module = importlib.util.module_from_spec(spec)
     loader.exec_module(module)
     return module

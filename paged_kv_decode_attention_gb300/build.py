@@ -2,13 +2,15 @@
 for sm_103a only.  Translation units compile in parallel, then link into one
 shared library with the CUDA runtime linked statically.  Beside it, with g++
 against the installed torch's headers, the Python entry points of the calls
-that serve single tokens (_pkv_binding.so, csrc/py_binding.cpp)."""
+that serve single tokens (_pkv_binding.<torch and Python>.so,
+csrc/py_binding.cpp)."""
 from __future__ import annotations
 
 import concurrent.futures
 import glob
 import os
 import platform
+import re
 import subprocess
 import sys
 import sysconfig
@@ -21,7 +23,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build", platform.machine())
 LIB = os.path.join(BUILD, "libpkv.so")
 BINDING_SRC = os.path.join(CSRC, "py_binding.cpp")
-BINDING = os.path.join(BUILD, "_pkv_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", f"-I{INCLUDE}", f"-I{CSRC}",
@@ -57,6 +58,18 @@ def _torch_dir() -> str:
     return os.path.dirname(os.path.abspath(torch.__file__))
 
 
+def _binding_tag() -> str:
+    """What the binding's machine code depends on besides its sources: torch's C++ classes and Python's."""
+    import torch
+
+    commit = (getattr(torch.version, "git_version", None) or "")[:8]
+    return re.sub(r"[^\w.+-]", "_", f"{torch.__version__}-{commit}-{sysconfig.get_config_var('SOABI')}")
+
+
+def binding_path() -> str:
+    return os.path.join(BUILD, f"_pkv_binding.{_binding_tag()}.so")
+
+
 def _binding_compile(obj: str):
     torch_dir = _torch_dir()
     inc = os.path.join(torch_dir, "include")
@@ -84,7 +97,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append(cmd)
     cuda_jobs = len(jobs)
-    binding_obj = os.path.join(BUILD, "py_binding.o")
+    binding, binding_obj = binding_path(), os.path.join(BUILD, f"py_binding.{_binding_tag()}.o")
     if force or _stale(binding_obj, [BINDING_SRC] + hdrs):
         jobs.append(_binding_compile(binding_obj))
 
@@ -107,13 +120,13 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libpkv.so failed")
         os.replace(tmp, LIB)
-    if force or _stale(BINDING, [binding_obj]):
-        tmp = BINDING + f".tmp{os.getpid()}"
+    if force or _stale(binding, [binding_obj]):
+        tmp = binding + f".tmp{os.getpid()}"
         r = subprocess.run(_binding_link(binding_obj, tmp), capture_output=True, text=True)
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of _pkv_binding.so failed")
-        os.replace(tmp, BINDING)
+        os.replace(tmp, binding)
     return LIB
 
 
