@@ -16,6 +16,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -80,7 +81,7 @@ class DecodeGraphDesc(ctypes.Structure):
 
 
 def _load():
-    path = _build.build()
+    path = _build.build(binding=False)
     lib = ctypes.CDLL(path)
     p, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     lib.pkv_kv_append.argtypes = [p, p, ctypes.POINTER(CacheDesc), p, p, p, i32, p]
@@ -187,17 +188,24 @@ def _load():
 _lib, _path = _load()
 
 
-def _load_binding():
-    """The C++ entry points (csrc/py_binding.cpp) of the calls that serve single tokens."""
-    path = _build.binding_path()
-    loader = importlib.machinery.ExtensionFileLoader("_pkv_binding", path)
-    spec = importlib.util.spec_from_file_location("_pkv_binding", path, loader=loader)
-    module = importlib.util.module_from_spec(spec)
-    loader.exec_module(module)
-    return module
+_binding_module = None
+_binding_lock = threading.Lock()
 
 
-_binding = _load_binding()
+def _binding():
+    """The C++ entry points (csrc/py_binding.cpp) of the calls that serve single tokens, built (if stale) and loaded
+    on their first use: the other calls need neither g++ nor torch's headers."""
+    global _binding_module
+    if _binding_module is None:
+        with _binding_lock:
+            if _binding_module is None:
+                path = _build.build_binding()
+                loader = importlib.machinery.ExtensionFileLoader("_pkv_binding", path)
+                spec = importlib.util.spec_from_file_location("_pkv_binding", path, loader=loader)
+                module = importlib.util.module_from_spec(spec)
+                loader.exec_module(module)
+                _binding_module = module
+    return _binding_module
 
 
 def library_path() -> str:
@@ -743,8 +751,8 @@ def qk_norm_rope_append(q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     contiguous); q_out [T][Hq][128]; slot_mapping int64 [T] (< 0: not stored); positions int32 [T]; rope_table
     float32 [max_positions][rot_dim], cosines then sines (None: no rotation); q_weight, k_weight BF16 [128]
     (None: no norm); pools of `kv_format`.  See include/pkv.h."""
-    _done(_binding.qk_norm_rope_append(q_out, kv_format, k_cache, v_cache, slot_mapping, q, k, v, positions,
-                                       rope_table, q_weight, k_weight, eps, interleaved, _raw(stream)),
+    _done(_binding().qk_norm_rope_append(q_out, kv_format, k_cache, v_cache, slot_mapping, q, k, v, positions,
+                                         rope_table, q_weight, k_weight, eps, interleaved, _raw(stream)),
           "pkv_qk_norm_rope_append")
 
 
@@ -782,8 +790,8 @@ def paged_attention_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
 
     q, out [B][tree_len][Hq][128]; tree_mask int64 or uint64 [B][tree_len][ceil(tree_len/64)], bit j = draft j is
     visible; workspace >= workspace_size_tree(...) bytes.  Rows past tree_lens[r] get zeros."""
-    _done(_binding.paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, tree_lens,
-                                        scale, kv_blocks_per_split, workspace, _raw(stream)),
+    _done(_binding().paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, tree_lens,
+                                          scale, kv_blocks_per_split, workspace, _raw(stream)),
           "pkv_paged_attention_tree")
 
 
@@ -793,8 +801,8 @@ def paged_attention_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                            workspace: torch.Tensor | None = None, stream=None) -> None:
     """paged_attention with a sliding window: the query at position p sees the keys t <= p with t > p - window or
     t < num_sinks.  Blocks no query sees are not looked up.  workspace >= workspace_size_window(...) bytes."""
-    _done(_binding.paged_attention_window(out, q, k_cache, v_cache, block_tables, context_lens, q_len, window,
-                                          num_sinks, scale, kv_blocks_per_split, workspace, _raw(stream)),
+    _done(_binding().paged_attention_window(out, q, k_cache, v_cache, block_tables, context_lens, q_len, window,
+                                            num_sinks, scale, kv_blocks_per_split, workspace, _raw(stream)),
           "pkv_paged_attention_window")
 
 
@@ -836,8 +844,8 @@ def kv_compact(pools: KvPools, block_tables: torch.Tensor, context_lens: torch.T
                num_accepted: torch.Tensor, tree_len: int, tree_lens: torch.Tensor | None = None, stream=None) -> None:
     """Keep the accepted drafts: in every layer, draft accepted[r][j] (rising) moves to the j-th place behind
     request r's committed context.  context_lens includes the drafts, as in paged_attention_tree."""
-    _done(_binding.kv_compact(*pools._args, block_tables, context_lens, accepted, num_accepted, tree_len, tree_lens,
-                              _raw(stream)), "pkv_kv_compact")
+    _done(_binding().kv_compact(*pools._args, block_tables, context_lens, accepted, num_accepted, tree_len, tree_lens,
+                                _raw(stream)), "pkv_kv_compact")
 
 
 def _addr(x) -> int:

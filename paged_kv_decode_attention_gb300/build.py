@@ -84,7 +84,31 @@ def _binding_link(obj: str, out: str):
             "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
-def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
+def _run_all(jobs, verbose: bool) -> None:
+    def run(cmd):
+        return cmd, subprocess.run(cmd, capture_output=True, text=True)
+
+    if jobs:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+            for cmd, r in ex.map(run, jobs):
+                if verbose or r.returncode != 0:
+                    sys.stderr.write(r.stdout + r.stderr)
+                if r.returncode != 0:
+                    raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}")
+
+
+def _link(command, out: str) -> None:
+    """Run command(output) into a temporary file beside `out`, then put it in its place."""
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run(command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"link of {os.path.basename(out)} failed")
+    os.replace(tmp, out)
+
+
+def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, binding: bool = True) -> str:
+    """Build what is stale: libpkv.so, and the binding unless it is left to build_binding()."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     hdrs = headers()
@@ -97,37 +121,35 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append(cmd)
     cuda_jobs = len(jobs)
-    binding, binding_obj = binding_path(), os.path.join(BUILD, f"py_binding.{_binding_tag()}.o")
-    if force or _stale(binding_obj, [BINDING_SRC] + hdrs):
-        jobs.append(_binding_compile(binding_obj))
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
-
-    if jobs:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
-            for cmd, r in ex.map(run, jobs):
-                if verbose or ptxas_info or r.returncode != 0:
-                    sys.stderr.write(r.stdout + r.stderr)
-                if r.returncode != 0:
-                    raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}")
+    if binding:
+        jobs += _binding_jobs(force)
+    _run_all(jobs, verbose or ptxas_info)
     if force or cuda_jobs or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link of libpkv.so failed")
-        os.replace(tmp, LIB)
-    if force or _stale(binding, [binding_obj]):
-        tmp = binding + f".tmp{os.getpid()}"
-        r = subprocess.run(_binding_link(binding_obj, tmp), capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link of _pkv_binding.so failed")
-        os.replace(tmp, binding)
+        _link(lambda out: [nvcc] + ARCH + ["-shared", "-o", out] + objs, LIB)
+    if binding:
+        _link_binding(force)
     return LIB
+
+
+def _binding_obj() -> str:
+    return os.path.join(BUILD, f"py_binding.{_binding_tag()}.o")
+
+
+def _binding_jobs(force: bool = False):
+    obj = _binding_obj()
+    return [_binding_compile(obj)] if force or _stale(obj, [BINDING_SRC] + headers()) else []
+
+
+def _link_binding(force: bool = False) -> None:
+    if force or _stale(binding_path(), [_binding_obj()]):
+        _link(lambda out: _binding_link(_binding_obj(), out), binding_path())
+
+
+def build_binding() -> str:
+    """The binding alone, beside a library that is built."""
+    _run_all(_binding_jobs(), False)
+    _link_binding()
+    return binding_path()
 
 
 if __name__ == "__main__":
