@@ -357,14 +357,9 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           const int lb = i < sink_entries ? (i < w.sink_blocks ? i : INT_MAX) : w.first_block + i - sink_entries;
           return lb < w.end_block ? lb : -1;
         };
-        // its block id, checked where it is used
-        auto entry = [&](int i) -> int {
-          if (kMask == MaskKind::kTree && i < 32) return first_ids;  // read above
-          const int lb = logical(i);
-          return lb >= 0 ? table[lb] : 0;
-        };
-        auto row_of = [&](int i, int blk) -> int {
-          if (logical(i) < 0) return oob_row;
+        // its pool row, given its block id
+        auto row_of = [&](int lb, int blk) -> int {
+          if (lb < 0) return oob_row;
           if (blk < 0 || blk >= a.d.num_blocks) {
             report(a.d.err, PKV_DEVERR_BLOCK_ID);
             blk = 0;
@@ -372,12 +367,17 @@ __device__ __forceinline__ void paged_masked_tc_body(const CUtensorMap& k_map, c
           return (blk * a.d.num_kv_heads + w.kvh) * kBlockSize;
         };
         constexpr int kTilesPerChunk = 32 / S::kTileBlocks;
-        int cur = row_of(lane, entry(lane)), nxt = 0;
+        int next_lb = logical(lane), nxt = first_ids;  // (a tree's were read above)
+        if (kMask != MaskKind::kTree && next_lb >= 0) nxt = table[next_lb];
+        int cur = row_of(next_lb, nxt);
         for (int j = 0; j < w.n_tiles && ok; ++j, ++filled) {
           const int in_chunk = j % kTilesPerChunk;
-          if (in_chunk == 0) nxt = entry((j + kTilesPerChunk) * S::kTileBlocks + lane);
+          if (in_chunk == 0) {  // the next chunk's ids, checked when they are used
+            next_lb = logical((j + kTilesPerChunk) * S::kTileBlocks + lane);
+            if (next_lb >= 0) nxt = table[next_lb];
+          }
           const int yy = __shfl_sync(0xffffffffu, cur, in_chunk * S::kTileBlocks + ((lane >> 1) & (S::kTileBlocks - 1)));
-          if (in_chunk == kTilesPerChunk - 1) cur = row_of((j + 1) * S::kTileBlocks + lane, nxt);
+          if (in_chunk == kTilesPerChunk - 1) cur = row_of(next_lb, nxt);
           const int st = filled % stages;
           if (filled >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((filled / stages) & 1) ^ 1));
           if (!ok) break;
