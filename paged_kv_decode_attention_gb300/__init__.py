@@ -833,8 +833,9 @@ class KvPools:
             if not ok or t.shape != first.shape or t.get_device() != self.device:
                 raise ValueError(f"pool {i}: the layers' pools must have the format's shape, on one device")
         addrs = [t.data_ptr() for t in self.tensors]
-        if len(set(addrs)) != len(addrs):
-            raise ValueError("the layers' pools must be distinct")
+        order, size = sorted(addrs), first.numel() * first.element_size()
+        if any(b - a < max(size, 1) for a, b in zip(order, order[1:])):
+            raise ValueError("the layers' pools must be distinct memory")
         self._arrays = [(ctypes.c_void_p * n)(*addrs[:n]), (ctypes.c_void_p * n)(*addrs[n:])]
         self._args = (ctypes.addressof(self._arrays[0]), ctypes.addressof(self._arrays[1]), n, first.shape[0],
                       first.shape[1], kv_format, self.device)
