@@ -57,12 +57,13 @@ def random_tree(rng, n):
     return rows
 
 
-def attention64(d, allowed, scale=SCALE):
+def attention64(d, allowed, scale=SCALE, weights=2.0 ** -8):
     """allowed(r) -> (query rows, positions, visible [rows][positions]) for request r.  Returns the outputs in 64 bits
     and, per output, a bound of the kernels' error from the format's roundings:
 
-    half a BF16 step of the output (2^-8 |o|); the weights' own rounding, at most 2^-8 of each weight, so 2^-8 of
-    A = sum p |v|; and the FP32 logits and sums: a dot product of 128 exact products is off by at most 128 * 2^-24 *
+    half a BF16 step of the output (2^-8 |o|); the weights' own rounding, at most `weights` of each weight (2^-8 as
+    one BF16 value, 2^-16 as a BF16 value and the BF16 rounding of the remainder), so that much of A = sum p |v|; and
+    the FP32 logits and sums: a dot product of 128 exact products is off by at most 128 * 2^-24 *
     sum |q k|, which moves every weight by that much (x scale), numerator and denominator; the base-2 exponential and
     the sums add less than 2^-16 of A."""
     q = d["q"].double()
@@ -90,7 +91,7 @@ def attention64(d, allowed, scale=SCALE):
         o = torch.einsum("nhgt,thd->nhgd", p, v)
         a = torch.einsum("nhgt,thd->nhgd", p, v.abs())
         out[r, rows] = o.reshape(len(rows), hq, dim)
-        tol[r, rows] = (2.0 ** -8 * o.abs() + a * (2.0 ** -8 + 2 * e_s + 2.0 ** -16)).reshape(len(rows), hq, dim)
+        tol[r, rows] = (2.0 ** -8 * o.abs() + a * (weights + 2 * e_s + 2.0 ** -16)).reshape(len(rows), hq, dim)
     return out, tol
 
 
