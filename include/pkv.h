@@ -559,11 +559,18 @@ pkv_status pkv_copy_blocks_fp8_e4m3(void* k_cache, void* v_cache, const pkv_cach
  *   pkv_qk_norm_rope_append   the drafts' queries, keys and values: norms,
  *                             rotation, store
  *   pkv_paged_attention_tree  each draft against the committed context and
- *                             its own ancestors (pkv_paged_attention_window in
- *                             layers with a sliding window)
+ *                             its own ancestors
  * and, once the accepted path is known,
  *   pkv_kv_compact            the accepted drafts' K and V to the places behind
  *                             the committed context, in every layer.
+ * In layers with a sliding window, drafts that form a chain (each the child of
+ * the one before) are verified by pkv_paged_attention_window.  It goes by the
+ * order of the slots alone, so it does NOT fit a tree that branches: a draft
+ * would see earlier siblings, and the window would count them.  There is no
+ * call for a branching tree under a window.
+ * Both attention calls read BF16 pools.  E4M3 and q8_0 pools, which the first
+ * and the last call serve too, are read by their single-token decodes only
+ * (pkv_paged_attention_fp8_e4m3, pkv_paged_attention_q8_0).
  * ---------------------------------------------------------------------------
  */
 typedef enum pkv_kv_format { PKV_KV_BF16 = 0, PKV_KV_Q8_0 = 1, PKV_KV_FP8_E4M3 = 2 } pkv_kv_format;
@@ -597,6 +604,8 @@ typedef enum pkv_kv_format { PKV_KV_BF16 = 0, PKV_KV_Q8_0 = 1, PKV_KV_FP8_E4M3 =
  *                  multiple of 16 up to 128.
  *   interleaved  : 0 = pairs (i, i + rot_dim/2), else pairs (2i, 2i + 1).
  *   eps          : finite, >= 0.
+ * The squares of a head are summed in FP32: exact in effect for heads whose
+ * largest magnitude lies between 2^-60 and 2^60.
  */
 pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
                                    int32_t kv_format, const int64_t* slot_mapping, const void* q, int64_t q_stride,
@@ -629,6 +638,13 @@ pkv_status pkv_qk_norm_rope_append(void* q_out, void* k_cache, void* v_cache, co
  *                  for the same kv_blocks_per_split (may be NULL when 0).
  * The other arguments are those of pkv_paged_attention.  K and V of every
  * token of the context must be finite; slots past it may hold anything.
+ * Rounding: CTAs of 128 rows (up to 32 positions; more in calls of few tiles
+ * and CTAs) carry the softmax weights as two BF16 parts, off by at most 2^-16
+ * of each weight; CTAs of 256 rows as one, off by at most 2^-8, which shows
+ * where few keys hold most of the weight.  The shape and the splits follow
+ * from the call's sizes, so a request's last bits may depend on its batch.
+ * The automatic split counts the tiles of max_blocks_per_seq blocks: where
+ * contexts are much shorter than the table, pass a split made for them.
  */
 int32_t pkv_choose_kv_blocks_per_split_tree(int32_t num_seqs, int32_t num_kv_heads, int32_t tree_len,
                                             int32_t max_blocks_per_seq, int32_t sm_count);
