@@ -24,10 +24,11 @@
 // per row tile and P.V (A in tensor memory, N = 128) 256.  K/V tiles are 64
 // tokens in both shapes: two buffers of scores, then O, fill the 256 columns
 // of a row tile, and the second buffer (S two tiles ahead of the P.V that is
-// under way) is worth more than S with N = 128 from a single buffer (16 trees
-// of 61 positions: 102 us against 114; 2000-token chunks: 390 against 480).
-// Half of the queries in tensor memory, with one buffer each for S and P,
-// takes 110 and 421 us: an MMA whose A lies there is not faster at N = 64.
+// under way) is worth more than S with N = 128 from a single buffer (replayed,
+// in the version that compared them, 16 trees of 61 positions: 102 us against
+// 114; 2000-token chunks: 390 against 480).  Half of the queries in tensor
+// memory, with one buffer each for S and P, took 110 and 421 us there: an MMA
+// whose A lies there is not faster at N = 64.
 //   kQTiles 1: 128 rows (32 positions), 2 CTAs per SM.  The wait of one CTA
 //              (first tiles, softmax latency, epilogue) is filled by the
 //              other.  P.V carries the weights as a BF16 part plus the BF16
@@ -36,10 +37,14 @@
 //   kQTiles 2: 256 rows (64 positions), 1 CTA per SM; each row tile has its
 //              own MMA warp, and while one's softmax runs the tensor cores
 //              work on the other's products.  The weights enter P.V rounded
-//              to BF16 (2^-8 relative at most, to nearest, so the errors
-//              average out over the keys: 0.0023 of the output's norm against
-//              0.0017 from the output's own rounding).  The remainder's
-//              products would take 150 and 548 us where these take 102 and 390.
+//              to BF16, 2^-8 relative at most.  Over many keys of like weight
+//              the errors average out (0.0023 of the output's norm against
+//              0.0017 from the output's own rounding).  Where one key holds
+//              most of the weight they do not: with a maximum that lags (by
+//              up to 2^16) its weight need not be 1, and the sum is that of
+//              the unrounded weights, so up to 2^-8 reaches the output.  In
+//              the version above, the remainder's products took 150 and 548 us
+//              for 102 and 390, sums of the rounded weights 111 and 421.
 //
 // CTA = 4 + 4 kQTiles warps:
 //   warps 0, 2: TMA producers of K and of V (16 x 64 boxes, 128-byte
@@ -53,15 +58,19 @@
 // up to 8 of them form a cluster and merge through distributed shared memory
 // (one request of 26 positions over 600 tokens: 8.4 us in one launch).
 //
-// Measured (32 query and 8 KV heads, BF16, back-to-back calls, one GB300):
-//   tree, 37 requests x 16 positions after about 2,100 tokens   52 us: 6.5 TB/s
-//   tree, 16 x 61 positions after about 8,300 tokens  100 us: 5.6 TB/s, tensor
-//                              pipe 71 % active (85 % on the busiest SM)
-//   window 2000 + 4 sinks, 64 single queries   43 us: 5.2 TB/s; the tail of
-//                              unequal lengths is what is left
-//   window 4096 + 4 sinks, 4 chunks of 2000    355 to 370 us: 1380 cycles a tile and
-//                              pair of row tiles where the pipe needs 1280, and
-//                              some 5 % around a unit (kRounds; one unit per CTA 395)
+// Measured (32 query and 8 KV heads, BF16, one GB300; replayed from a graph
+// over three sets of inputs / through the public call, one after another):
+//   tree, 37 requests x 16 positions after about 2,100 tokens
+//              53 / 54 to 55 us: 6.4 TB/s
+//   tree, 16 x 61 positions after about 8,300 tokens
+//              99 to 102 / 110 to 117 us: 5.6 TB/s, tensor pipe 73.5 % of the
+//              active cycles (88 % on the busiest SM)
+//   window 2000 + 4 sinks, 64 single queries
+//              43 / 44 us: 5.2 TB/s; the tail of unequal lengths is what is left
+//   window 4096 + 4 sinks, 4 chunks of 2000
+//              355 to 377 / 383 to 390 us: 1380 cycles a tile and pair of row
+//              tiles where the pipe needs 1280, and some 5 % around a unit
+//              (kRounds; one unit per CTA 395, replayed)
 #include <algorithm>
 #include <climits>
 #include <cmath>
