@@ -328,6 +328,7 @@ PyObject* kv_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int32_t tree_len = c.i32("tree_len");
     const at::Tensor* tree_lens = c.optional("tree_lens", Kind::kI32);
     const int64_t seqs = lens.numel();
+    if (seqs > INT32_MAX) refuse("context_lens", "has a size beyond 32 bits");
     if (tables.dim() != 2 || tables.size(0) != seqs)
       raise(PyExc_ValueError, "block_tables must be [num_seqs][max_blocks_per_seq]");
     if (accepted.dim() != 2 || accepted.size(0) != seqs || num.numel() != seqs)
@@ -337,7 +338,7 @@ PyObject* kv_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return pkv_kv_compact(static_cast<void* const*>(k), static_cast<void* const*>(v), layers, &d, format,
                           static_cast<const int32_t*>(tables.data_ptr()), size32(tables, 1, "block_tables"),
                           static_cast<const int32_t*>(lens.data_ptr()), static_cast<const int32_t*>(ptr(tree_lens)),
-                          size32(lens, 0, "context_lens"), tree_len, static_cast<const int32_t*>(accepted.data_ptr()),
+                          static_cast<int32_t>(seqs), tree_len, static_cast<const int32_t*>(accepted.data_ptr()),
                           static_cast<const int32_t*>(num.data_ptr()), size32(accepted, 1, "accepted"), c.stream());
   });
 }

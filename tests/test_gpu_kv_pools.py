@@ -1,5 +1,6 @@
 """KvPools: the pools of a model's layers may be parts of one allocation, but
-not parts that share memory (a row would be moved twice)."""
+not parts that share memory (a row would be moved twice).  And the shapes in
+which kv_compact takes its lengths."""
 import pytest
 import torch
 
@@ -38,4 +39,21 @@ def test_pools_that_are_parts_of_one_allocation():
         (db, do), (sb, so) = place(10 + j), place(10 + i)
         want[:, :, db, :, do] = want[:, :, sb, :, so]
     assert torch.equal(whole, want)
+    assert pkv.get_device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("shape", [(3,), (1, 3), (3, 1), (1, 3, 1)])
+def test_lengths_of_any_shape_cover_every_request(shape):
+    """One length per request is asked for, in whatever shape: the other calls take them so too."""
+    pkv.get_device_error(reset=True)
+    k, v = (torch.randn((3, 2, 16, 128), device="cuda").to(torch.bfloat16) for _ in range(2))
+    want = [t.clone() for t in (k, v)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    pkv.kv_compact(pkv.KvPools([k], [v]), i32([[2], [0], [1]]), i32([8, 9, 10]).view(shape), i32([[1, 4], [2, 3], [0, 3]]),
+                   i32([2, 1, 2]).view(shape), 5, i32([5, 4, 5]).view(shape))
+    for t in want:
+        for blk, base, acc in ((2, 3, (1, 4)), (0, 5, (2,)), (1, 5, (0, 3))):
+            for j, i in enumerate(acc):
+                t[blk, :, base + j] = t[blk, :, base + i].clone()
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
     assert pkv.get_device_error(reset=True) == 0
