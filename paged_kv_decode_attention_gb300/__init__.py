@@ -789,7 +789,7 @@ def paged_attention_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
     over the committed context and the drafts that tree_mask shows.
 
     q, out [B][tree_len][Hq][128]; tree_mask int64 or uint64 [B][tree_len][ceil(tree_len/64)], bit j = draft j is
-    visible; workspace >= workspace_size_tree(...) bytes.  Rows past tree_lens[r] get zeros."""
+    visible; BF16 pools; workspace >= workspace_size_tree(...) bytes.  Rows past tree_lens[r] get zeros."""
     _done(_binding().paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, tree_lens,
                                           scale, kv_blocks_per_split, workspace, _raw(stream)),
           "pkv_paged_attention_tree")
@@ -800,7 +800,8 @@ def paged_attention_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                            num_sinks: int, scale: float, kv_blocks_per_split: int = 0,
                            workspace: torch.Tensor | None = None, stream=None) -> None:
     """paged_attention with a sliding window: the query at position p sees the keys t <= p with t > p - window or
-    t < num_sinks.  Blocks no query sees are not looked up.  workspace >= workspace_size_window(...) bytes."""
+    t < num_sinks.  Blocks no query sees are not looked up.  Of drafted tokens it verifies chains; a tree that branches
+    would see earlier siblings.  BF16 pools; workspace >= workspace_size_window(...) bytes."""
     _done(_binding().paged_attention_window(out, q, k_cache, v_cache, block_tables, context_lens, q_len, window,
                                             num_sinks, scale, kv_blocks_per_split, workspace, _raw(stream)),
           "pkv_paged_attention_window")
