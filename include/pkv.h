@@ -68,6 +68,7 @@ typedef enum pkv_status {
 #define PKV_DEVERR_TIMEOUT 8u    /* a pipeline wait gave up (never expected)  */
 #define PKV_DEVERR_POSITION 16u  /* a position outside the rotation table     */
 #define PKV_DEVERR_ACCEPTED 32u  /* accepted drafts not a rising list of drafts */
+#define PKV_DEVERR_SEQLENS 64u   /* cu_seqlens falls, or leaves the tokens    */
 
 /* Geometry of one layer's paged cache (both K and V use it). */
 typedef struct pkv_cache_desc {
@@ -713,6 +714,115 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
                           int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* tree_lens,
                           int32_t num_seqs, int32_t tree_len, const int32_t* accepted, const int32_t* num_accepted,
                           int32_t max_accepted, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A prompt's first step: attention over the prompt itself, from the
+ * projections, and the store of its K and V (§8.1.1: the prefill processes all
+ * prompt tokens at once and stores their K and V).
+ *
+ * Packed sequences: the tokens of num_seqs sequences lie one behind the other,
+ * sequence s at rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device int32
+ * [num_seqs + 1], not falling, from 0 up to num_tokens; lengths may be 0).
+ * Rows behind the last sequence are padding.  Entries that fall or leave
+ * 0 .. num_tokens set PKV_DEVERR_SEQLENS; they are clamped and a sequence of
+ * negative length counts as empty.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * pkv_prompt_attention -- causal attention of packed prompts: token i of a
+ * prompt sees its tokens 0 .. i.
+ *   out          : device BF16 [num_tokens][num_q_heads][128], 16-byte aligned.
+ *                  Rows of no prompt are left as they are.
+ *   out_lse      : device FP32 [num_tokens][num_q_heads] or NULL: the natural
+ *                  log-sum-exp of each row's scaled logits (what
+ *                  pkv_attn_combine takes).
+ *   q, k, v      : device BF16; token t's heads start q_stride (k_stride,
+ *                  v_stride) elements after token t - 1's and are contiguous
+ *                  [num_q_heads or num_kv_heads][128].  Strides are multiples
+ *                  of 8, at least one token's heads; pointers 16-byte aligned.
+ *                  out must not overlap them.
+ *   num_q_heads  : num_kv_heads times 1 .. 128; query head h reads KV head
+ *                  h / (num_q_heads / num_kv_heads).
+ *   head_dim     : 128.
+ *   scale        : > 0.
+ * K and V of a prompt's tokens must be finite; padding rows may hold anything.
+ * The weights enter the second product rounded to BF16, off by at most 2^-8 of
+ * each (2^-9 where they are not next to a power of two); their sum is that of
+ * the unrounded ones.  No workspace; bitwise reproducible, and a prompt's
+ * result does not depend on the other prompts.
+ */
+pkv_status pkv_prompt_attention(void* out, float* out_lse, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_seqlens,
+                                int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, void* stream);
+
+/*
+ * FP8 KV cache with block scales: E4M3 codes in pools of the E4M3 layout
+ * (uint8 [num_blocks][num_kv_heads][16][128]) and one FP32 scale for each
+ * block and KV head, k_scales and v_scales [num_blocks][num_kv_heads];
+ * value = code * scale.  The plain E4M3 pools saturate at 448 and lose what
+ * lies below 2^-9; here a block's largest magnitude takes E4M3's last binade.
+ * (pkv_qk_norm_rope_append, pkv_kv_compact and the decode graphs do not take
+ * this format.)
+ *
+ * pkv_kv_append_fp8_scaled -- store new tokens.  A block's scale becomes the
+ * smallest power of two of 2^-32 .. 2^32 under which its tokens' largest
+ * magnitude is at most 448 (beyond 448 * 2^32 they saturate); codes are
+ * rounded to nearest, ties to even.  A block that holds earlier tokens of the
+ * request keeps a larger scale that it has; where the new tokens need a larger
+ * one, the earlier codes times old / new are rounded to E4M3 again.  A block
+ * whose first token is new starts anew.
+ *   block_tables, max_blocks_per_seq, context_lens : as for
+ *                  pkv_paged_attention, the new tokens included in the
+ *                  lengths: request r's n_r new tokens lie at positions
+ *                  context_lens[r] - n_r .. context_lens[r] - 1.  Positions
+ *                  from there on hold nothing that is kept.
+ *   cu_new       : device int32 [num_seqs + 1]: request r's new tokens are
+ *                  rows cu_new[r] .. cu_new[r + 1] - 1 of k_new and v_new
+ *                  (packed as above); NULL = one each, num_tokens == num_seqs.
+ *   k_new, v_new : device BF16, strides as for pkv_prompt_attention.  Finite.
+ * A request with context_lens[r] <= 0 is a padding row.  One whose context is
+ * shorter than its new tokens or longer than its table sets
+ * PKV_DEVERR_CONTEXT and nothing of it is stored; a block id outside the pool
+ * sets PKV_DEVERR_BLOCK_ID and that block is skipped.  A block that new tokens
+ * fall into must not be shared with another request.
+ */
+pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                                    const pkv_cache_desc* cache, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* cu_new,
+                                    int32_t num_seqs, const void* k_new, int64_t k_stride, const void* v_new,
+                                    int64_t v_stride, int32_t num_tokens, void* stream);
+
+/*
+ * pkv_paged_attention_fp8_scaled -- pkv_paged_attention over such pools: one
+ * query token per request or a causal chunk of q_len (out, q, block_tables,
+ * context_lens, q_len as there).
+ *   k_scales, v_scales : > 0 in every block that is read, of any value between
+ *                  2^-32 and 2^32 (powers of two or not).
+ *   scale        : > 0.
+ *   kv_blocks_per_split : 0 = pkv_choose_kv_blocks_per_split_fp8_scaled.
+ *   workspace    : device, 256-byte aligned, pkv_workspace_size_fp8_scaled(...)
+ *                  bytes for the same kv_blocks_per_split (may be NULL when 0).
+ * Codes of every token of the context must be finite (no 0x7f, 0xff); slots
+ * past it may hold anything.
+ */
+int32_t pkv_choose_kv_blocks_per_split_fp8_scaled(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
+                                                  int32_t max_blocks_per_seq, int32_t sm_count);
+size_t pkv_workspace_size_fp8_scaled(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
+                                     int32_t max_blocks_per_seq, int32_t kv_blocks_per_split);
+pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                          const float* k_scales, const float* v_scales, const pkv_cache_desc* cache,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, int32_t num_seqs, int32_t q_len,
+                                          int32_t num_q_heads, float scale, int32_t kv_blocks_per_split,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* pkv_copy_blocks for pools with block scales: codes and scales. */
+pkv_status pkv_copy_blocks_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                                      const pkv_cache_desc* cache, const int32_t* src_blocks,
+                                      const int32_t* dst_blocks, int32_t num_pairs, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* pkv_status_string(pkv_status status);

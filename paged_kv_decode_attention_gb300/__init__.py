@@ -33,7 +33,9 @@ __all__ = [
     "paged_attention_q8_0_append", "copy_blocks_fp8_e4m3",
     "qk_norm_rope_append", "paged_attention_tree", "choose_kv_blocks_per_split_tree", "workspace_size_tree",
     "paged_attention_window", "choose_kv_blocks_per_split_window", "workspace_size_window", "KvPools", "kv_compact",
-    "MAX_TREE_LEN", "DEVERR_POSITION", "DEVERR_ACCEPTED",
+    "MAX_TREE_LEN", "DEVERR_POSITION", "DEVERR_ACCEPTED", "DEVERR_SEQLENS",
+    "prompt_attention", "kv_append_fp8_scaled", "paged_attention_fp8_scaled",
+    "choose_kv_blocks_per_split_fp8_scaled", "workspace_size_fp8_scaled", "copy_blocks_fp8_scaled",
     "DecodeGraph", "KV_BF16", "KV_Q8_0", "KV_FP8_E4M3", "selftest_bounded_wait",
 ]
 
@@ -43,6 +45,7 @@ DEVERR_CONTEXT = 4
 DEVERR_TIMEOUT = 8
 DEVERR_POSITION = 16
 DEVERR_ACCEPTED = 32
+DEVERR_SEQLENS = 64
 
 BLOCK_SIZE = 16
 HEAD_DIM = 128
@@ -170,6 +173,18 @@ def _load():
     lib.pkv_paged_attention_window.restype = ctypes.c_int
     lib.pkv_kv_compact.argtypes = [p, p, i32, cd, i32, p, i32, p, p, i32, i32, p, p, i32, p]
     lib.pkv_kv_compact.restype = ctypes.c_int
+    lib.pkv_prompt_attention.argtypes = [p, p, p, i64, p, i64, p, i64, p, i32, i32, i32, i32, i32, f32, p]
+    lib.pkv_prompt_attention.restype = ctypes.c_int
+    lib.pkv_kv_append_fp8_scaled.argtypes = [p, p, p, p, cd, p, i32, p, p, i32, p, i64, p, i64, i32, p]
+    lib.pkv_kv_append_fp8_scaled.restype = ctypes.c_int
+    lib.pkv_choose_kv_blocks_per_split_fp8_scaled.argtypes = [i32, i32, i32, i32, i32]
+    lib.pkv_choose_kv_blocks_per_split_fp8_scaled.restype = i32
+    lib.pkv_workspace_size_fp8_scaled.argtypes = [i32, i32, i32, i32, i32]
+    lib.pkv_workspace_size_fp8_scaled.restype = sz
+    lib.pkv_paged_attention_fp8_scaled.argtypes = [p, p, p, p, p, p, cd, p, i32, p, i32, i32, i32, f32, i32, p, sz, p]
+    lib.pkv_paged_attention_fp8_scaled.restype = ctypes.c_int
+    lib.pkv_copy_blocks_fp8_scaled.argtypes = [p, p, p, p, cd, p, p, i32, p]
+    lib.pkv_copy_blocks_fp8_scaled.restype = ctypes.c_int
     lib.pkv_decode_graph_create.argtypes = [ctypes.POINTER(DecodeGraphDesc), ctypes.POINTER(ctypes.c_void_p)]
     lib.pkv_decode_graph_create.restype = ctypes.c_int
     lib.pkv_decode_graph_launch.argtypes = [p, i32, p]
@@ -848,6 +863,65 @@ def kv_compact(pools: KvPools, block_tables: torch.Tensor, context_lens: torch.T
     request r's committed context.  context_lens includes the drafts, as in paged_attention_tree."""
     _done(_binding().kv_compact(*pools._args, block_tables, context_lens, accepted, num_accepted, tree_len, tree_lens,
                                 _raw(stream)), "pkv_kv_compact")
+
+
+# ---------------------------------------------------------------------------
+# A prompt's first step, and the FP8 cache with block scales.
+# ---------------------------------------------------------------------------
+def prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: float, out_lse: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of whole prompts packed one behind the other: prompt s is rows cu_seqlens[s] ..
+    cu_seqlens[s + 1] - 1 (int32 [num_seqs + 1]), and its token i sees its tokens 0 .. i.
+
+    q [T][Hq][128], k, v [T][Hkv][128] (BF16, views into a projection's output: only a token's heads must be
+    contiguous; Hq a multiple of Hkv); out [T][Hq][128]; out_lse float32 [T][Hq] takes the log-sum-exps.  Rows behind
+    the last prompt are left as they are."""
+    _done(_binding().prompt_attention(out, q, k, v, cu_seqlens, scale, out_lse, _raw(stream)), "pkv_prompt_attention")
+
+
+def kv_append_fp8_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, k_new: torch.Tensor,
+                         v_new: torch.Tensor, cu_new: torch.Tensor | None = None, stream=None) -> None:
+    """Store new tokens in pools of E4M3 codes (uint8 [num_blocks][Hkv][16][128]) with a power-of-two scale for each
+    block and KV head (float32 [num_blocks][Hkv]).
+
+    Request r's new tokens, rows cu_new[r] .. cu_new[r + 1] - 1 of k_new, v_new [T][Hkv][128] (BF16, strided like
+    prompt_attention's; cu_new None: one per request), go to its last positions: context_lens includes them.  A block
+    whose scale grows takes its earlier tokens along."""
+    _done(_binding().kv_append_fp8_scaled(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, k_new,
+                                          v_new, cu_new, _raw(stream)), "pkv_kv_append_fp8_scaled")
+
+
+def choose_kv_blocks_per_split_fp8_scaled(num_seqs: int, num_kv_heads: int, q_len: int, max_blocks_per_seq: int,
+                                          sm_count: int = 0) -> int:
+    return int(_lib.pkv_choose_kv_blocks_per_split_fp8_scaled(num_seqs, num_kv_heads, q_len, max_blocks_per_seq,
+                                                              sm_count))
+
+
+def workspace_size_fp8_scaled(num_seqs: int, q_len: int, num_q_heads: int, max_blocks_per_seq: int,
+                              kv_blocks_per_split: int = 0) -> int:
+    """Bytes paged_attention_fp8_scaled needs for the same kv_blocks_per_split (0 = the library's choice)."""
+    return int(_lib.pkv_workspace_size_fp8_scaled(num_seqs, q_len, num_q_heads, max_blocks_per_seq,
+                                                  kv_blocks_per_split))
+
+
+def paged_attention_fp8_scaled(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                               context_lens: torch.Tensor, q_len: int, scale: float, kv_blocks_per_split: int = 0,
+                               workspace: torch.Tensor | None = None, stream=None) -> None:
+    """paged_attention over pools of E4M3 codes with block scales (value = code * scale): one query token per request
+    or a causal chunk of q_len.  q, out [B][q_len][Hq][128]; workspace >= workspace_size_fp8_scaled(...) bytes."""
+    _done(_binding().paged_attention_fp8_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                                                context_lens, q_len, scale, kv_blocks_per_split, workspace,
+                                                _raw(stream)), "pkv_paged_attention_fp8_scaled")
+
+
+def copy_blocks_fp8_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                           v_scales: torch.Tensor, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
+                           stream=None) -> None:
+    """copy_blocks for pools with block scales: codes and scales."""
+    _done(_binding().copy_blocks_fp8_scaled(k_cache, v_cache, k_scales, v_scales, src_blocks, dst_blocks,
+                                            _raw(stream)), "pkv_copy_blocks_fp8_scaled")
 
 
 def _addr(x) -> int:

@@ -78,7 +78,9 @@ constexpr int kOffPt = kOffQp + 2 * kFtOpBytes;            // 2 buffers (tile pa
 constexpr int kOffX = kOffPt + 4 * kFtOpBytes;             // float [2][4 warps][8]: exchanges
 constexpr int kOffKn = kOffX + 2 * 4 * 8 * 4;              // fused append: 2 new K rows (unit parity), E4M3
 constexpr int kOffKnAt = kOffKn + 2 * kHeadDim;            // int [2]: where each row goes (tile << 8 | row), or -1
-constexpr int kOffBar = kOffKnAt + 16;
+constexpr int kFtScaleSlots = 8;                           // block scales: tiles held
+constexpr int kOffScale = kOffKnAt + 16;                   // float [8 tiles][K, V][16 blocks]
+constexpr int kOffBar = kOffScale + kFtScaleSlots * 2 * kFtTileBlocks * 4;
 constexpr int kSmemFt = kOffBar + 512;
 constexpr uint32_t kColS = 0;    // S^T buffers at columns 0 and 32 (16 columns per half)
 constexpr uint32_t kColO = 64;   // O^T buffers at columns 64 and 80
@@ -108,12 +110,20 @@ struct FtBars {
   uint64_t p_empty[2];
   uint64_t o_full[2];
   uint64_t o_empty[2];
+  uint64_t scale_full[kFtScaleSlots];  // kScaled; a slot is written again 8 tiles on, past what the rings let run ahead
   uint32_t tmem_base;
 };
 static_assert(sizeof(FtBars) <= 512, "barrier area");
 
+// The three decodes of this file.
+enum class FtMode {
+  kPlain,
+  kFused,  // stores each request's new token and uses it
+  kScaled  // codes times a scale for each block and KV head; several queries per request
+};
+
 struct FtUnit {
-  int r, kvh, split, b0, b1, n_tiles, ctx_keys, ctx_raw;
+  int r, seq, kvh, split, b0, b1, n_tiles, ctx_keys, ctx_raw;
   // fused append: the tile and tile row holding the request's new token
   // (position ctx - 1) and its logical block; new_tile = -1 when the unit
   // does not hold it or there is no append
@@ -121,16 +131,21 @@ struct FtUnit {
 };
 
 // Unit u: split fastest, then KV head, then request.  kFused: also where the
-// request's new token falls (the fused append).
-template <bool kFused>
+// request's new token falls (the fused append).  kScaled: then the request's
+// query; `r` counts (request, query) rows, and query i of q_len sees the keys
+// up to its own.
+template <FtMode kMode>
 __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
+  constexpr bool kFused = kMode == FtMode::kFused;
   FtUnit x;
   x.split = u % a.num_splits;
   const int row = u / a.num_splits;
   x.r = row / a.num_kv_heads;
   x.kvh = row - x.r * a.num_kv_heads;
-  x.ctx_raw = a.context_lens[x.r];
-  const int ctx = min(max(x.ctx_raw, 0), a.max_blocks * kBlockSize);
+  x.seq = kMode == FtMode::kScaled ? x.r / a.q_len : x.r;
+  x.ctx_raw = a.context_lens[x.seq];
+  int ctx = min(max(x.ctx_raw, 0), a.max_blocks * kBlockSize);
+  if (kMode == FtMode::kScaled) ctx = max(ctx - (a.q_len - 1 - (x.r - x.seq * a.q_len)), 0);
   const int nb = (ctx + kBlockSize - 1) / kBlockSize;
   x.b0 = x.split * a.blocks_per_split;
   x.b1 = min(nb, x.b0 + a.blocks_per_split);
@@ -170,16 +185,21 @@ __device__ __forceinline__ uint32_t ft_row_word(int row, int l) {
 // Producer warp: TMA loads of one tensor's tiles into its ring.  Lane b < 16
 // issues the box of the tile's block b; block ids are read 32 at a time, one
 // chunk ahead.
+// kScaled, `scales` not NULL (the K producer's): lanes b and 16 + b also bring
+// the K and V scale of block b into the tile's slot; their asynchronous copies
+// arrive on the slot's barrier.
+template <FtMode kMode>
 __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMap* map, uint8_t* ring,
-                                           uint64_t* full, uint64_t* empty, int num_units, int lane) {
+                                           uint64_t* full, uint64_t* empty, int num_units, int lane, float* scales,
+                                           uint64_t* scale_full) {
   const uint64_t policy = l2_policy_evict_first();
   const int oob_row = a.num_blocks * a.num_kv_heads * kBlockSize;  // first row past the pool
   bool ok = true;
   int i = 0;
   for (int u = blockIdx.x; u < num_units && ok; u += gridDim.x) {
-    const FtUnit x = ft_unit<false>(a, u);
+    const FtUnit x = ft_unit<kMode>(a, u);
     if (x.n_tiles == 0) continue;
-    const int32_t* table = a.block_tables + static_cast<int64_t>(x.r) * a.max_blocks;
+    const int32_t* table = a.block_tables + static_cast<int64_t>(x.seq) * a.max_blocks;
     // the load stays inside the table row whatever the context length, so it
     // need not wait for that length; entries past the unit's blocks are dropped
     // where they would be used, and the others (of any value) checked there
@@ -196,6 +216,15 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[st], kFtStageBytes);
       __syncwarp();
+      if (kMode == FtMode::kScaled && scales != nullptr) {
+        float* slot_of = scales + (i % kFtScaleSlots) * 2 * kFtTileBlocks + lane;
+        if (x.b0 + j * kFtTileBlocks + (lane & 15) < x.b1) {
+          const int b = blk < 0 || blk >= a.num_blocks ? 0 : blk;
+          cp_async4(smem_addr(slot_of), (lane < kFtTileBlocks ? a.k_scales : a.v_scales) +
+                                            static_cast<int64_t>(b) * a.num_kv_heads + x.kvh);
+        }
+        cp_async_arrive(&scale_full[i % kFtScaleSlots]);
+      }
       if (lane < kFtTileBlocks) {
         int y = oob_row;
         if (x.b0 + j * kFtTileBlocks + lane < x.b1) {
@@ -213,6 +242,7 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
   // copies still in flight must land before shared memory is released
   if (lane == 0)
     for (int k = max(0, i - kFtStages); k < i; ++k) mbar_wait(&full[k % kFtStages], (k / kFtStages) & 1);
+  if (kMode == FtMode::kScaled) cp_async_wait_all();
   return ok;
 }
 
@@ -256,13 +286,24 @@ __device__ __forceinline__ float q_sigma(uint32_t amax_bits) {
 // kFused: the request's new token is stored and used in place of the row
 // read (a.k_new, a.v_new, a.slot_mapping set); an instance of its own, so the
 // plain decode carries none of that work.
-template <bool kFused>
+// kScaled: the values are code * scale, one scale for each block, KV head and
+// tensor.  The K scale multiplies the scores.  The V scale goes into the
+// weights, where the tensor core needs them inside E4M3's range whatever the
+// scales are: with y_t = score_t + log2(v scale_t) the running maximum is that
+// of y, the weights are w_t = 2^(y_t - m), O = sum w_t code_t, and the sum of
+// the softmax's own weights is that of w_t / (v scale_t), all on the CUDA cores
+// in FP32.  (Scales between 2^-32 and 2^32 leave the sum 62 binades.)
+template <FtMode kMode>
 __global__ void __launch_bounds__(kFtThreads, 1)
     paged_decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                                const DecodeArgs a) {
   pdl_trigger();
+  constexpr bool kFused = kMode == FtMode::kFused;
+  constexpr bool kScaled = kMode == FtMode::kScaled;
+  constexpr FtMode kWalk = kScaled ? kMode : FtMode::kPlain;  // of the warps that need not know the new tokens
   extern __shared__ __align__(1024) uint8_t smem[];
   FtBars* bars = reinterpret_cast<FtBars*>(smem + kOffBar);
+  float* scale_ring = reinterpret_cast<float*>(smem + kOffScale);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int num_units = a.num_seqs * a.num_kv_heads * a.num_splits;
@@ -290,6 +331,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_empty[b], 128);
     }
+    for (int s = 0; kScaled && s < kFtScaleSlots; ++s) mbar_init(&bars->scale_full[s], 32);
     fence_barrier_init();
   }
   if (warp == 2) {
@@ -312,8 +354,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 
   if (warp == 0 || warp == 1) {
     // ------------------------------ producers ------------------------------
-    ok = warp == 0 ? ft_produce(a, &k_map, smem + kOffK, bars->k_full, bars->k_empty, num_units, lane)
-                   : ft_produce(a, &v_map, smem + kOffV, bars->v_full, bars->v_empty, num_units, lane);
+    ok = warp == 0 ? ft_produce<kWalk>(a, &k_map, smem + kOffK, bars->k_full, bars->k_empty, num_units, lane,
+                                       scale_ring, bars->scale_full)
+                   : ft_produce<kWalk>(a, &v_map, smem + kOffV, bars->v_full, bars->v_empty, num_units, lane, nullptr, nullptr);
     if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
   } else if (warp == 2) {
     // ------------------------------ MMA issuer ------------------------------
@@ -328,7 +371,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       };
       auto settle = [&](Cursor& c) {  // move to the first unit with a tile, from c.u on
         for (; c.u < num_units; c.u += gridDim.x) {
-          c.n = ft_unit<false>(a, c.u).n_tiles;
+          c.n = ft_unit<kWalk>(a, c.u).n_tiles;
           if (c.n > 0) return;
         }
       };
@@ -429,7 +472,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     const int h = lane >> 3, c = lane & 7;
     int seq = 0;
     for (int u = blockIdx.x; u < num_units && ok; u += gridDim.x) {
-      const FtUnit x = ft_unit<kFused>(a, u);
+      const FtUnit x = ft_unit<kMode>(a, u);
       if (x.n_tiles == 0) continue;
       const int ub = seq & 1;
       const uint4* src = reinterpret_cast<const uint4*>(
@@ -529,7 +572,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     };
     int i = 0, seq = 0;
     for (int u = blockIdx.x; u < num_units && ok_all; u += gridDim.x) {
-      const FtUnit x = ft_unit<kFused>(a, u);
+      const FtUnit x = ft_unit<kMode>(a, u);
       const int64_t orow0 = static_cast<int64_t>(x.r) * hq + x.kvh * kGroup;
       if (threadIdx.x == 128 && x.split == 0 && x.kvh == 0 && x.ctx_raw > a.max_blocks * kBlockSize)
         report(a.err, PKV_DEVERR_CONTEXT);
@@ -597,6 +640,19 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           tc::fence_before_sync();
           mbar_arrive(&bars->s_empty[sb]);
         }
+        // the two tokens' block scales
+        float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, inv_vs[2] = {1.f, 1.f};
+        if (kScaled && ok) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->scale_full[i % kFtScaleSlots], (i / kFtScaleSlots) & 1));
+          const float* sl = scale_ring + (i % kFtScaleSlots) * 2 * kFtTileBlocks + (t >> 4);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            ks[hf] = sl[8 * hf];
+            const float vs = sl[kFtTileBlocks + 8 * hf];
+            lv[hf] = log2f(vs);
+            inv_vs[hf] = 1.f / vs;
+          }
+        }
         const int tok0 = (x.b0 + j * kFtTileBlocks) * kBlockSize + t;  // token of half 0; half 1 is 128 further
         bool valid[2];
         float sc[2][4], mt[4];
@@ -604,7 +660,10 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         for (int hf = 0; hf < 2; ++hf) {
           valid[hf] = tok0 + 128 * hf < x.ctx_keys;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) sc[hf][h] = (ok && valid[hf]) ? c[h] * (s8[hf][h] + s8[hf][4 + h]) : -INFINITY;
+          for (int h = 0; h < 4; ++h) {
+            const float x2 = c[h] * (s8[hf][h] + s8[hf][4 + h]);
+            sc[hf][h] = (ok && valid[hf]) ? (kScaled ? fmaf(x2, ks[hf], lv[hf]) : x2) : -INFINITY;
+          }
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) mt[h] = fmaxf(sc[0][h], sc[1][h]);
@@ -666,7 +725,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             p[h] = (sc[hf][h] == -INFINITY) ? 0.f : exp2_approx(sc[hf][h] - m[h]);
-            l[h] += p[h];
+            if (kScaled) {
+              if (valid[hf]) l[h] = fmaf(p[h], inv_vs[hf], l[h]);
+            } else {
+              l[h] += p[h];
+            }
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -787,7 +850,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   }
 }
 
-template <bool kFused>
+template <FtMode kMode>
 cudaError_t allow_smem_ft() {
   static std::atomic<bool> done[64];  // per device; host threads may race on a first call
   int dev = 0;
@@ -795,33 +858,37 @@ cudaError_t allow_smem_ft() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(paged_decode_fp8_tc_kernel<kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemFt);
+    e = cudaFuncSetAttribute(paged_decode_fp8_tc_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemFt);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   return cudaSuccess;
 }
 
-}  // namespace
-
-cudaError_t launch_paged_decode_fp8_tc(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
-  if (grid <= 0) return cudaSuccess;
-  if (a.q_len != 1 || a.num_splits < 1 || (a.num_splits > 1 && (a.part_o == nullptr || a.part_lse == nullptr)))
-    return cudaErrorInvalidValue;
+template <FtMode kMode>
+cudaError_t launch_ft(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.num_kv_heads * kBlockSize;
   if (rows + kBlockSize >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
   CUtensorMap kmap, vmap;
   if (!make_pool_map_e4m3(&kmap, a.k_cache, rows) || !make_pool_map_e4m3(&vmap, a.v_cache, rows))
     return cudaErrorInvalidValue;
-  const bool fused = a.k_new != nullptr;
-  if (fused && (a.v_new == nullptr || a.slot_mapping == nullptr)) return cudaErrorInvalidValue;
-  cudaError_t e = fused ? allow_smem_ft<true>() : allow_smem_ft<false>();
+  const cudaError_t e = allow_smem_ft<kMode>();
   if (e != cudaSuccess) return e;
-  return fused ? launch_pdl(paged_decode_fp8_tc_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(kFtThreads),
-                            kSmemFt, stream, 1, kmap, vmap, a)
-               : launch_pdl(paged_decode_fp8_tc_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(kFtThreads),
-                            kSmemFt, stream, 1, kmap, vmap, a);
+  return launch_pdl(paged_decode_fp8_tc_kernel<kMode>, dim3(static_cast<unsigned>(grid)), dim3(kFtThreads), kSmemFt,
+                    stream, 1, kmap, vmap, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode_fp8_tc(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
+  if (grid <= 0) return cudaSuccess;
+  const bool scaled = a.k_scales != nullptr, fused = a.k_new != nullptr;
+  if ((!scaled && a.q_len != 1) || a.num_splits < 1 ||
+      (a.num_splits > 1 && (a.part_o == nullptr || a.part_lse == nullptr)))
+    return cudaErrorInvalidValue;
+  if (fused && (a.v_new == nullptr || a.slot_mapping == nullptr || scaled)) return cudaErrorInvalidValue;
+  if (scaled) return launch_ft<FtMode::kScaled>(a, grid, stream);
+  return fused ? launch_ft<FtMode::kFused>(a, grid, stream) : launch_ft<FtMode::kPlain>(a, grid, stream);
 }
 
 }  // namespace pkv

@@ -4,6 +4,7 @@
 // carving and stream-ordered launches.  Nothing here allocates, frees or
 // synchronises device memory (except pkv_get_device_error, which reads the
 // error word and documents that it synchronises).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -1209,6 +1210,211 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
       return PKV_ERR_CUDA;
   }
   return PKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Every pointer a multiple of `align` bytes (NULL counts as one).
+bool aligned(std::initializer_list<const void*> ps, uintptr_t align) {
+  uintptr_t all = 0;
+  for (const void* p : ps) all |= reinterpret_cast<uintptr_t>(p);
+  return (all & (align - 1)) == 0;
+}
+
+// Positions of a chunk over block-scaled pools are kept to 32 bits.
+constexpr int32_t kScaledMaxBlocks = 1 << 26;
+constexpr int32_t kScaledMaxQLen = 1 << 26;
+
+int64_t scaled_rows(int32_t num_seqs, int32_t q_len) { return static_cast<int64_t>(num_seqs) * q_len; }
+
+int32_t scaled_blocks_per_split(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks,
+                                int32_t sm_count) {
+  if (max_blocks <= 0) return 1;
+  if (sm_count <= 0) sm_count = device_sm_count();
+  const int64_t rows = scaled_rows(num_seqs > 0 ? num_seqs : 1, q_len > 0 ? q_len : 1) * (num_kv_heads > 0 ? num_kv_heads : 1);
+  return persistent_blocks_per_split(rows, max_blocks, sm_count, 16);
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_prompt_attention(void* out, float* out_lse, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_seqlens,
+                                int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, void* stream) {
+  if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0) return PKV_ERR_SHAPE;
+  if (head_dim != kHeadDim) return PKV_ERR_UNSUPPORTED;
+  if (num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kMaxPromptGroup) return PKV_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PKV_ERR_SHAPE;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * kHeadDim;
+  if (q_stride < static_cast<int64_t>(num_q_heads) * kHeadDim || k_stride < kv_row || v_stride < kv_row)
+    return PKV_ERR_SHAPE;
+  if ((q_stride | k_stride | v_stride) & 7) return PKV_ERR_UNSUPPORTED;
+  // (a tensor map's strides: below 2^40 bytes; positions and a tile behind them: 32 bits)
+  if (std::max(q_stride, std::max(k_stride, v_stride)) >= (int64_t{1} << 39) || num_tokens > 0x7fffff00)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!out || !q || !k || !v || !cu_seqlens) return PKV_ERR_NULL;
+  if (!aligned({out, q, k, v}, 16) || !aligned({out_lse, cu_seqlens}, 4)) return PKV_ERR_UNSUPPORTED;
+  PromptArgs a{};
+  a.out = out;
+  a.lse = out_lse;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cu_seqlens = cu_seqlens;
+  a.err = error_word();
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_prompt_attention(a, device_sm_count(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                                         : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                                    const pkv_cache_desc* cache, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* cu_new,
+                                    int32_t num_seqs, const void* k_new, int64_t k_stride, const void* v_new,
+                                    int64_t v_stride, int32_t num_tokens, void* stream) {
+  const pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 1) return PKV_ERR_SHAPE;
+  if (max_blocks_per_seq > kScaledMaxBlocks) return PKV_ERR_UNSUPPORTED;
+  if (cu_new == nullptr && num_tokens != num_seqs) return PKV_ERR_SHAPE;
+  const int64_t row = static_cast<int64_t>(cache->num_kv_heads) * kHeadDim;
+  if (k_stride < row || v_stride < row) return PKV_ERR_SHAPE;
+  if ((k_stride | v_stride) & 7) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens || !k_new || !v_new)
+    return PKV_ERR_NULL;
+  if (!aligned({k_cache, v_cache, k_new, v_new}, 16) ||
+      !aligned({k_scales, v_scales, block_tables, context_lens, cu_new}, 4))
+    return PKV_ERR_UNSUPPORTED;
+  AppendScaledArgs a{};
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.cu_new = cu_new;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.err = error_word();
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = cache->num_blocks;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  return launch_kv_append_scaled(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int32_t pkv_choose_kv_blocks_per_split_fp8_scaled(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
+                                                  int32_t max_blocks_per_seq, int32_t sm_count) {
+  return scaled_blocks_per_split(num_seqs, num_kv_heads, q_len, max_blocks_per_seq, sm_count);
+}
+
+size_t pkv_workspace_size_fp8_scaled(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
+                                     int32_t max_blocks_per_seq, int32_t kv_blocks_per_split) {
+  if (num_seqs <= 0 || q_len <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || kv_blocks_per_split < 0) return 0;
+  int32_t bps = kv_blocks_per_split;
+  if (bps == 0) bps = scaled_blocks_per_split(num_seqs, (num_q_heads + kGroup - 1) / kGroup, q_len, max_blocks_per_seq, 0);
+  if (bps >= max_blocks_per_seq) return 0;
+  const size_t splits = (static_cast<size_t>(max_blocks_per_seq) + bps - 1) / bps;
+  const size_t rows = static_cast<size_t>(scaled_rows(num_seqs, q_len)) * num_q_heads;
+  return align_up(rows * splits * kHeadDim * sizeof(float), 256) + align_up(rows * splits * sizeof(float), 256);
+}
+
+pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                          const float* k_scales, const float* v_scales, const pkv_cache_desc* cache,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, int32_t num_seqs, int32_t q_len,
+                                          int32_t num_q_heads, float scale, int32_t kv_blocks_per_split,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  const pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || q_len < 1 || max_blocks_per_seq < 1 || kv_blocks_per_split < 0) return PKV_ERR_SHAPE;
+  if (num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+  if (cache->num_blocks == 0 && num_seqs > 0) return PKV_ERR_SHAPE;
+  if (max_blocks_per_seq > kScaledMaxBlocks || q_len > kScaledMaxQLen ||
+      (static_cast<int64_t>(cache->num_blocks) + 1) * cache->num_kv_heads * kBlockSize + kBlockSize >= (int64_t{1} << 31))
+    return PKV_ERR_UNSUPPORTED;  // (pool rows are 32-bit tensor coordinates)
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PKV_ERR_SHAPE;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens)
+    return PKV_ERR_NULL;
+  if (!aligned({out, q, k_cache, v_cache}, 16) || !aligned({k_scales, v_scales, block_tables, context_lens}, 4))
+    return PKV_ERR_UNSUPPORTED;
+  int32_t bps = kv_blocks_per_split;
+  if (bps == 0) bps = scaled_blocks_per_split(num_seqs, cache->num_kv_heads, q_len, max_blocks_per_seq, 0);
+  bps = std::min(bps, max_blocks_per_seq);
+  const int32_t splits = (max_blocks_per_seq + bps - 1) / bps;
+  const int64_t rows = scaled_rows(num_seqs, q_len);
+  const int64_t units = rows * cache->num_kv_heads * splits;
+  if (rows * num_q_heads > 0x7fffffff || units > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  DecodeArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.err = error_word();
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = cache->num_blocks;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.num_seqs = static_cast<int32_t>(rows);
+  a.q_len = q_len;
+  a.blocks_per_split = bps;
+  a.num_splits = splits;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.part_slots = splits;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (splits > 1) {
+    const size_t need = pkv_workspace_size_fp8_scaled(num_seqs, q_len, num_q_heads, max_blocks_per_seq, bps);
+    if (workspace == nullptr || workspace_bytes < need || !aligned({workspace}, 256)) return PKV_ERR_WORKSPACE;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                          align_up(static_cast<size_t>(rows) * num_q_heads * splits * kHeadDim * sizeof(float), 256));
+  }
+  const int sms = device_sm_count();
+  if (launch_paged_decode_fp8_tc(a, static_cast<int32_t>(units < sms ? units : sms), s) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  if (splits == 1) return PKV_OK;
+  return launch_attn_combine(out, nullptr, a.part_o, a.part_lse, static_cast<int32_t>(rows * num_q_heads), splits, s) ==
+                 cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_copy_blocks_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                                      const pkv_cache_desc* cache, const int32_t* src_blocks,
+                                      const int32_t* dst_blocks, int32_t num_pairs, void* stream) {
+  const pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_pairs < 0) return PKV_ERR_SHAPE;
+  if (num_pairs > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+  if (num_pairs == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !k_scales || !v_scales || !src_blocks || !dst_blocks) return PKV_ERR_NULL;
+  if (!aligned({k_cache, v_cache}, 16) || !aligned({k_scales, v_scales, src_blocks, dst_blocks}, 4))
+    return PKV_ERR_UNSUPPORTED;
+  return launch_copy_blocks_scaled(static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scales, v_scales,
+                                   cache->num_blocks, cache->num_kv_heads, src_blocks, dst_blocks, num_pairs,
+                                   error_word(), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -234,6 +234,14 @@ __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* gmem_s
                "l"(reinterpret_cast<uint64_t>(gmem_src)), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_dst), "l"(reinterpret_cast<uint64_t>(gmem_src))
+               : "memory");
+}
+// Arrive (once, of the barrier's count) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Hint: bring the 128-byte line holding `p` into this SM's L1.

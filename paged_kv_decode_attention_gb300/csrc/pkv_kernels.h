@@ -99,6 +99,10 @@ struct DecodeArgs {
   const void* k_new;
   const void* v_new;
   const int64_t* slot_mapping;
+  // E4M3 pools with block scales: FP32 [num_blocks][Hkv] (paged_decode_fp8_tc.cu
+  // takes q_len queries per request then, num_seqs counting (request, query) rows)
+  const float* k_scales;
+  const float* v_scales;
 };
 
 cudaError_t launch_kv_append(void* k_cache, void* v_cache, int32_t num_blocks, int32_t num_kv_heads,
@@ -130,6 +134,11 @@ bool make_pool_map(CUtensorMap* map, const void* pool, int64_t rows);
 // Tensor map over an E4M3 KV pool viewed as `rows` rows of 128 bytes, boxes
 // of 16 rows x 128 bytes with the 128-byte swizzle (paged_chunk_tc.cu).
 bool make_pool_map_e4m3(CUtensorMap* map, const void* pool, int64_t rows);
+// Tensor map over BF16 [tokens][heads][128] whose tokens lie `stride` elements
+// apart, boxes of `box_tokens` tokens x `box_heads` heads x 64 elements with
+// the 128-byte swizzle (paged_chunk_tc.cu).
+bool make_packed_map(CUtensorMap* map, const void* data, int64_t tokens, int64_t heads, int64_t stride,
+                     int32_t box_heads, int32_t box_tokens);
 // Decode (q_len 1) with QK^T and PV on tensor cores, `grid` persistent CTAs
 // striding over the (request, KV head, split) units; num_splits > 1 writes
 // workspace partials for the combine kernel (paged_decode_tc.cu).
@@ -213,6 +222,28 @@ struct CompactArgs {
 cudaError_t launch_kv_compact(const CompactArgs& a, int32_t num_seqs, int32_t layers, int32_t kv_format,
                               cudaStream_t stream);
 
+// Causal attention of whole prompts, packed (prompt_attn_tc.cu).
+constexpr int kMaxPromptGroup = 128;  // query heads per KV head
+struct PromptArgs {
+  void* out;                  // BF16 [T][Hkv * group][D]
+  float* lse;                 // FP32 [T][Hkv * group] or NULL
+  const void* q;              // BF16, token t's heads at q + t * q_stride (elements)
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* cu_seqlens;  // [num_seqs + 1]
+  unsigned int* err;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t pos_per_tile;       // set by the launcher
+  float scale_log2;
+};
+cudaError_t launch_prompt_attention(const PromptArgs& a, int32_t sm_count, cudaStream_t stream);
+
 // Members per cascade group: 16 requests x 4 heads = one 64-row tile.
 constexpr int kCascadeGroup = 16;
 
@@ -232,6 +263,32 @@ cudaError_t launch_paged_decode_fp8_tc(const DecodeArgs& a, int32_t grid, cudaSt
 cudaError_t launch_kv_append_fp8(void* k_cache, void* v_cache, int32_t num_blocks, int32_t num_kv_heads,
                                  const int64_t* slot_mapping, const void* k_new, const void* v_new,
                                  int32_t num_tokens, unsigned int* err, cudaStream_t stream);
+
+// E4M3 KV with a scale for each block and KV head: append (kv_append_scaled.cu).
+struct AppendScaledArgs {
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scales;              // [num_blocks][Hkv]
+  float* v_scales;
+  const int32_t* block_tables;  // [num_seqs][max_blocks]
+  const int32_t* context_lens;  // [num_seqs], the new tokens included
+  const int32_t* cu_new;        // [num_seqs + 1]; NULL: one new token per request
+  const uint16_t* k_new;        // BF16, token t's heads at k_new + t * k_stride (elements)
+  const uint16_t* v_new;
+  int64_t k_stride;
+  int64_t v_stride;
+  unsigned int* err;
+  int32_t max_blocks;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t num_seqs;
+  int32_t num_tokens;
+};
+cudaError_t launch_kv_append_scaled(const AppendScaledArgs& a, cudaStream_t stream);
+// Copies the two pools' blocks with their scales.
+cudaError_t launch_copy_blocks_scaled(uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                                      int32_t num_blocks, int32_t num_kv_heads, const int32_t* src,
+                                      const int32_t* dst, int32_t num_pairs, unsigned int* err, cudaStream_t stream);
 
 // Device error word of the current device (PKV_DEVERR_* bits).
 unsigned int* device_error_word();

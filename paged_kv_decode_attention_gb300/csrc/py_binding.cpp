@@ -1,5 +1,6 @@
 // py_binding.cpp -- Python entry points of the calls that serve single tokens
-// (the verification step and the sliding window): argument checks and
+// (the verification step, the sliding window, the cache with block scales) and
+// of the prompt attention: argument checks and
 // marshalling in C++, because a call with the same checks in Python, through
 // ctypes, took 15 to 17 us of host time (8 to 10 with the checks pared down;
 // eleven tensors, four attribute reads each), more than the kernels behind
@@ -343,6 +344,123 @@ PyObject* kv_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// Pools with block scales: K and V codes, and the scales of their blocks.
+struct Scaled {
+  const at::Tensor *k, *v, *ks, *vs;
+  pkv_cache_desc desc;
+};
+
+Scaled scaled_pools(Call& c) {
+  Scaled p;
+  p.desc = pools(c, PKV_KV_FP8_E4M3, &p.k, &p.v);
+  p.ks = &c.tensor("k_scales", Kind::kF32);
+  p.vs = &c.tensor("v_scales", Kind::kF32);
+  if (!shape_is(*p.ks, {p.desc.num_blocks, p.desc.num_kv_heads}) || p.vs->sizes() != p.ks->sizes())
+    raise(PyExc_ValueError, "k_scales and v_scales must be [num_blocks][num_kv_heads]");
+  return p;
+}
+
+float* f32_ptr(const at::Tensor* t) { return t == nullptr ? nullptr : static_cast<float*>(t->data_ptr()); }
+const int32_t* i32_ptr(const at::Tensor* t) { return static_cast<const int32_t*>(ptr(t)); }
+
+int32_t count32(const at::Tensor& t, const char* name) {
+  if (t.numel() > INT32_MAX) refuse(name, "has a size beyond 32 bits");
+  return static_cast<int32_t>(t.numel());
+}
+
+// (out, q, k, v, cu_seqlens, scale, out_lse, stream)
+PyObject* prompt_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> pkv_status {
+    Call c(args, n, 8);
+    const at::Tensor& out = c.tensor("out", Kind::kBf16);
+    const at::Tensor& q = c.tensor("q", Kind::kBf16, true);
+    const at::Tensor& k = c.tensor("k", Kind::kBf16, true);
+    const at::Tensor& v = c.tensor("v", Kind::kBf16, true);
+    if (q.dim() != 3 || k.dim() != 3) raise(PyExc_ValueError, "q, k and v must be [num_tokens][heads][128]");
+    const int32_t tokens = size32(q, 0, "q");
+    const int64_t qs = token_stride(q, "q", tokens, q.size(1));
+    const int64_t ks = token_stride(k, "k", tokens, k.size(1));
+    const int64_t vs = token_stride(v, "v", tokens, k.size(1));
+    if (out.sizes() != q.sizes()) raise(PyExc_ValueError, "out and q differ in shape");
+    const at::Tensor& cu = c.tensor("cu_seqlens", Kind::kI32);
+    if (cu.dim() != 1 || cu.numel() < 1) raise(PyExc_ValueError, "cu_seqlens must be [num_seqs + 1]");
+    const float scale = c.f32();
+    const at::Tensor* lse = c.optional("out_lse", Kind::kF32);
+    if (lse != nullptr && !shape_is(*lse, {tokens, q.size(1)}))
+      raise(PyExc_ValueError, "out_lse must be [num_tokens][num_q_heads]");
+    return pkv_prompt_attention(out.data_ptr(), f32_ptr(lse), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                i32_ptr(&cu), count32(cu, "cu_seqlens") - 1, tokens, size32(q, 1, "q"),
+                                size32(k, 1, "k"), kHeadDim, scale, c.stream());
+  });
+}
+
+// (k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, k_new,
+//  v_new, cu_new, stream)
+PyObject* kv_append_fp8_scaled(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> pkv_status {
+    Call c(args, n, 10);
+    const Scaled p = scaled_pools(c);
+    const at::Tensor& tables = c.tensor("block_tables", Kind::kI32);
+    const at::Tensor& lens = c.tensor("context_lens", Kind::kI32);
+    const int32_t seqs = count32(lens, "context_lens");
+    if (tables.dim() != 2 || tables.size(0) != seqs)
+      raise(PyExc_ValueError, "block_tables must be [num_seqs][max_blocks_per_seq]");
+    const at::Tensor& k = c.tensor("k_new", Kind::kBf16, true);
+    const at::Tensor& v = c.tensor("v_new", Kind::kBf16, true);
+    if (k.dim() != 3) refuse("k_new", "must be [num_tokens][heads][128]");
+    const int32_t tokens = size32(k, 0, "k_new");
+    const int64_t ks = token_stride(k, "k_new", tokens, p.desc.num_kv_heads);
+    const int64_t vs = token_stride(v, "v_new", tokens, p.desc.num_kv_heads);
+    const at::Tensor* cu = c.optional("cu_new", Kind::kI32);
+    if (cu != nullptr ? cu->dim() != 1 || cu->numel() != int64_t{seqs} + 1 : tokens != seqs)
+      raise(PyExc_ValueError, "cu_new must be [num_seqs + 1] (None: one new token per request)");
+    return pkv_kv_append_fp8_scaled(p.k->data_ptr(), p.v->data_ptr(), f32_ptr(p.ks), f32_ptr(p.vs), &p.desc,
+                                    i32_ptr(&tables), size32(tables, 1, "block_tables"), i32_ptr(&lens), i32_ptr(cu),
+                                    seqs, k.data_ptr(), ks, v.data_ptr(), vs, tokens, c.stream());
+  });
+}
+
+// (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+//  q_len, scale, kv_blocks_per_split, workspace, stream)
+PyObject* paged_attention_fp8_scaled(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> pkv_status {
+    Call c(args, n, 13);
+    const at::Tensor& out = c.tensor("out", Kind::kBf16);
+    const at::Tensor& q = c.tensor("q", Kind::kBf16);
+    const Scaled p = scaled_pools(c);
+    const at::Tensor& tables = c.tensor("block_tables", Kind::kI32);
+    const at::Tensor& lens = c.tensor("context_lens", Kind::kI32);
+    const int32_t seqs = count32(lens, "context_lens");
+    if (tables.dim() != 2 || tables.size(0) != seqs)
+      raise(PyExc_ValueError, "block_tables must be [num_seqs][max_blocks_per_seq]");
+    const int32_t q_len = c.i32("q_len");
+    if (q.dim() != 4 || q.size(0) != seqs || q.size(1) != q_len || q.size(3) != kHeadDim || out.sizes() != q.sizes())
+      raise(PyExc_ValueError, "q and out must be [num_seqs][q_len][num_q_heads][128]");
+    const float scale = c.f32();
+    const int32_t split = c.i32("kv_blocks_per_split");
+    void* ws;
+    size_t ws_bytes;
+    c.workspace(&ws, &ws_bytes);
+    return pkv_paged_attention_fp8_scaled(out.data_ptr(), q.data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
+                                          f32_ptr(p.ks), f32_ptr(p.vs), &p.desc, i32_ptr(&tables),
+                                          size32(tables, 1, "block_tables"), i32_ptr(&lens), seqs, q_len,
+                                          size32(q, 2, "q"), scale, split, ws, ws_bytes, c.stream());
+  });
+}
+
+// (k_cache, v_cache, k_scales, v_scales, src_blocks, dst_blocks, stream)
+PyObject* copy_blocks_fp8_scaled(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> pkv_status {
+    Call c(args, n, 7);
+    const Scaled p = scaled_pools(c);
+    const at::Tensor& src = c.tensor("src_blocks", Kind::kI32);
+    const at::Tensor& dst = c.tensor("dst_blocks", Kind::kI32);
+    if (src.numel() != dst.numel()) raise(PyExc_ValueError, "src_blocks and dst_blocks differ in length");
+    return pkv_copy_blocks_fp8_scaled(p.k->data_ptr(), p.v->data_ptr(), f32_ptr(p.ks), f32_ptr(p.vs), &p.desc,
+                                      i32_ptr(&src), i32_ptr(&dst), count32(src, "src_blocks"), c.stream());
+  });
+}
+
 template <typename F>
 constexpr PyCFunction fastcall(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
@@ -353,6 +471,10 @@ PyMethodDef kMethods[] = {
     {"paged_attention_tree", fastcall(paged_attention_tree), METH_FASTCALL, nullptr},
     {"paged_attention_window", fastcall(paged_attention_window), METH_FASTCALL, nullptr},
     {"kv_compact", fastcall(kv_compact), METH_FASTCALL, nullptr},
+    {"prompt_attention", fastcall(prompt_attention), METH_FASTCALL, nullptr},
+    {"kv_append_fp8_scaled", fastcall(kv_append_fp8_scaled), METH_FASTCALL, nullptr},
+    {"paged_attention_fp8_scaled", fastcall(paged_attention_fp8_scaled), METH_FASTCALL, nullptr},
+    {"copy_blocks_fp8_scaled", fastcall(copy_blocks_fp8_scaled), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
