@@ -802,22 +802,20 @@ pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scale
  *   k_scales, v_scales : > 0 in every block that is read, of any value between
  *                  2^-32 and 2^32 (powers of two or not).
  *   scale        : > 0.
- *   kv_blocks_per_split : 0 = pkv_choose_kv_blocks_per_split_fp8_scaled.
  *   workspace    : device, 256-byte aligned, pkv_workspace_size_fp8_scaled(...)
- *                  bytes for the same kv_blocks_per_split (may be NULL when 0).
+ *                  bytes (may be NULL when 0).  Its contents are overwritten;
+ *                  calls that share it must be stream-ordered.
  * Codes of every token of the context must be finite (no 0x7f, 0xff); slots
  * past it may hold anything.
  */
-int32_t pkv_choose_kv_blocks_per_split_fp8_scaled(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
-                                                  int32_t max_blocks_per_seq, int32_t sm_count);
 size_t pkv_workspace_size_fp8_scaled(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
-                                     int32_t max_blocks_per_seq, int32_t kv_blocks_per_split);
+                                     int32_t max_blocks_per_seq);
 pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* k_cache, const void* v_cache,
                                           const float* k_scales, const float* v_scales, const pkv_cache_desc* cache,
                                           const int32_t* block_tables, int32_t max_blocks_per_seq,
                                           const int32_t* context_lens, int32_t num_seqs, int32_t q_len,
-                                          int32_t num_q_heads, float scale, int32_t kv_blocks_per_split,
-                                          void* workspace, size_t workspace_bytes, void* stream);
+                                          int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+                                          void* stream);
 
 /* pkv_copy_blocks for pools with block scales: codes and scales. */
 pkv_status pkv_copy_blocks_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,

@@ -35,7 +35,7 @@ __all__ = [
     "paged_attention_window", "choose_kv_blocks_per_split_window", "workspace_size_window", "KvPools", "kv_compact",
     "MAX_TREE_LEN", "DEVERR_POSITION", "DEVERR_ACCEPTED", "DEVERR_SEQLENS",
     "prompt_attention", "kv_append_fp8_scaled", "paged_attention_fp8_scaled",
-    "choose_kv_blocks_per_split_fp8_scaled", "workspace_size_fp8_scaled", "copy_blocks_fp8_scaled",
+    "workspace_size_fp8_scaled", "copy_blocks_fp8_scaled",
     "DecodeGraph", "KV_BF16", "KV_Q8_0", "KV_FP8_E4M3", "selftest_bounded_wait",
 ]
 
@@ -177,11 +177,9 @@ def _load():
     lib.pkv_prompt_attention.restype = ctypes.c_int
     lib.pkv_kv_append_fp8_scaled.argtypes = [p, p, p, p, cd, p, i32, p, p, i32, p, i64, p, i64, i32, p]
     lib.pkv_kv_append_fp8_scaled.restype = ctypes.c_int
-    lib.pkv_choose_kv_blocks_per_split_fp8_scaled.argtypes = [i32, i32, i32, i32, i32]
-    lib.pkv_choose_kv_blocks_per_split_fp8_scaled.restype = i32
-    lib.pkv_workspace_size_fp8_scaled.argtypes = [i32, i32, i32, i32, i32]
+    lib.pkv_workspace_size_fp8_scaled.argtypes = [i32, i32, i32, i32]
     lib.pkv_workspace_size_fp8_scaled.restype = sz
-    lib.pkv_paged_attention_fp8_scaled.argtypes = [p, p, p, p, p, p, cd, p, i32, p, i32, i32, i32, f32, i32, p, sz, p]
+    lib.pkv_paged_attention_fp8_scaled.argtypes = [p, p, p, p, p, p, cd, p, i32, p, i32, i32, i32, f32, p, sz, p]
     lib.pkv_paged_attention_fp8_scaled.restype = ctypes.c_int
     lib.pkv_copy_blocks_fp8_scaled.argtypes = [p, p, p, p, cd, p, p, i32, p]
     lib.pkv_copy_blocks_fp8_scaled.restype = ctypes.c_int
@@ -892,28 +890,19 @@ def kv_append_fp8_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales:
                                           v_new, cu_new, _raw(stream)), "pkv_kv_append_fp8_scaled")
 
 
-def choose_kv_blocks_per_split_fp8_scaled(num_seqs: int, num_kv_heads: int, q_len: int, max_blocks_per_seq: int,
-                                          sm_count: int = 0) -> int:
-    return int(_lib.pkv_choose_kv_blocks_per_split_fp8_scaled(num_seqs, num_kv_heads, q_len, max_blocks_per_seq,
-                                                              sm_count))
-
-
-def workspace_size_fp8_scaled(num_seqs: int, q_len: int, num_q_heads: int, max_blocks_per_seq: int,
-                              kv_blocks_per_split: int = 0) -> int:
-    """Bytes paged_attention_fp8_scaled needs for the same kv_blocks_per_split (0 = the library's choice)."""
-    return int(_lib.pkv_workspace_size_fp8_scaled(num_seqs, q_len, num_q_heads, max_blocks_per_seq,
-                                                  kv_blocks_per_split))
+def workspace_size_fp8_scaled(num_seqs: int, q_len: int, num_q_heads: int, max_blocks_per_seq: int) -> int:
+    """Bytes paged_attention_fp8_scaled needs for these sizes on the current device."""
+    return int(_lib.pkv_workspace_size_fp8_scaled(num_seqs, q_len, num_q_heads, max_blocks_per_seq))
 
 
 def paged_attention_fp8_scaled(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
-                               context_lens: torch.Tensor, q_len: int, scale: float, kv_blocks_per_split: int = 0,
+                               context_lens: torch.Tensor, q_len: int, scale: float,
                                workspace: torch.Tensor | None = None, stream=None) -> None:
     """paged_attention over pools of E4M3 codes with block scales (value = code * scale): one query token per request
     or a causal chunk of q_len.  q, out [B][q_len][Hq][128]; workspace >= workspace_size_fp8_scaled(...) bytes."""
     _done(_binding().paged_attention_fp8_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
-                                                context_lens, q_len, scale, kv_blocks_per_split, workspace,
-                                                _raw(stream)), "pkv_paged_attention_fp8_scaled")
+                                                context_lens, q_len, scale, workspace, _raw(stream)), "pkv_paged_attention_fp8_scaled")
 
 
 def copy_blocks_fp8_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,

@@ -1,0 +1,901 @@
+// paged_chunk_fp8_tc.cu -- attention of several query positions per request
+// over a paged cache of E4M3 codes with a scale for each block and KV head,
+// both contractions on the tensor cores' 8-bit path: a causal chunk behind
+// cached tokens ("Chapter 8: Inference Optimization", clxhxhhr.top/posts/4341,
+// §8.2.3), or a chain of drafted tokens (§8.5.2), with K and V in FP8 (§8.4.4).
+//
+// Mathematics.  Softmax over the visible keys, tile by tile (128 keys) with a
+// running maximum and sum in FP32.  With value = code * scale, ks and vs the
+// scales of a key's block:
+//   S_ij = sum_d (sigma_i q_id) kcode_jd      (tensor cores, codes as they are)
+//   y_ij = S_ij (scale / sigma_i) ks_j + log2(vs_j), in base 2
+//   w_ij = 2^(y_ij - m_i), m_i a running maximum of y: so that the weights are
+//          what the second product needs, inside E4M3's range whatever vs is
+//   O_i  = sum_j w_ij vcode_j,   l_i = sum_j w_ij / vs_j,   out = O_i / l_i
+// Scales are constant over 16 keys, so they cost a few FP32 operations per 16
+// scores.  8-bit products want both operands in 8 bits.  Queries enter as two
+// E4M3 parts (sigma_i a power of two that brings the row's largest magnitude
+// to 2^7 .. 2^8: exact down to 2^-17 of it), weights as two parts times 2^6
+// (2^-8 relative, by way of FP16's 2^-11, down to 2^-16 of the largest).  Two
+// products at twice the BF16 rate cost what one of converted codes would, and
+// the tiles need no conversion pass: the SM's shared memory, which would be
+// the bound (a converted tile is read once and written twice over), carries
+// them once in and twice into the tensor cores.
+//
+// kWide : 256 rows (64 positions x 4 heads) share a CTA's tiles, 128 a row
+//         tile; while one row tile's softmax runs, the tensor cores work on
+//         the other's products.
+// !kWide: up to 128 rows; the two halves of the machine take the even and the
+//         odd tiles of keys and are joined at the end: HBM is the bound, and
+//         one chain of scores, softmax and product would be longer than a
+//         tile's transfer.
+//
+// Work is cut by tiles, not by requests: all (request, row tile, KV head) jobs
+// in a row are divided evenly among the CTAs, one per SM, whatever the
+// contexts' lengths are.  A job cut in two or more leaves un-normalised FP32
+// partials, at most two per CTA, which a second kernel joins.
+//
+// CTA = 12 warps:
+//   warps 0-7: softmax, one thread per row (TMEM lane), a warpgroup per row
+//             tile (or half of the tiles); they also write the query operand.
+//   warp 8  : TMA producer of K and V (16-token boxes of 2 KiB, 128-byte
+//             swizzle; blocks past the range arrive as zeros).
+//   warps 9, 10: MMA issuers, one per row tile (or half).
+//   warp 11 : finds the CTA's pieces and fetches the blocks' scales.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstddef>
+
+#include "pkv_common.cuh"
+#include "pkv_kernels.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kCfTokens = 128;                        // keys of a tile
+constexpr int kCfTileBlocks = kCfTokens / kBlockSize;  // 8
+constexpr int kCfTileBytes = kCfTokens * kHeadDim;    // K or V of a tile: 16 KiB
+constexpr int kCfBoxBytes = kBlockSize * kHeadDim;
+constexpr int kCfSlots = 10;                          // ring: K, V, K, V, ...
+constexpr int kCfScaleSlots = 8;                      // tiles whose scales are held
+constexpr int kCfThreads = 384;
+constexpr int kCfRows = 128;
+constexpr int kCfPos = kCfRows / kGroup;              // positions of a row tile
+constexpr int kCfOffQ = 0;                            // [row tile][high, low parts]; !kWide: one, then the join's buffer
+constexpr int kCfOffJoin = 2 * kCfTileBytes;          // FP32 [128][64]
+constexpr int kCfOffRing = 4 * kCfTileBytes;
+constexpr int kCfOffScale = kCfOffRing + kCfSlots * kCfTileBytes;
+constexpr int kCfScaleFloats = 3 * kCfTileBlocks;     // ks, log2 vs, 1 / vs
+// FP32 [2][128]: scale / sigma of the rows; !kWide: of one row tile, then the other half's sums
+constexpr int kCfOffSigma = kCfOffScale + kCfScaleSlots * kCfScaleFloats * 4;
+constexpr int kCfOffMax = kCfOffSigma + 2 * kCfRows * 4;  // !kWide: FP32 [128], the other half's maxima
+constexpr int kCfOffBar = kCfOffMax + kCfRows * 4;
+constexpr int kCfSmem = kCfOffBar + 528;
+static_assert(kCfSmem <= 227 * 1024, "one CTA per SM");
+static_assert(kCfOffBar % 16 == 0 && kCfOffScale % 16 == 0, "alignment");
+constexpr uint32_t kCfTileCols = 256;                 // S (weights over it), then O
+constexpr uint32_t kCfColO = 128;
+constexpr int kCfSoftmaxRegs = 208;
+constexpr int kCfIssueRegs = 80;
+static_assert((2 * kCfSoftmaxRegs + kCfIssueRegs) * 128 <= 168 * kCfThreads, "register split");
+constexpr float kCfLag = 2.f;     // base 2: weights stay at or below 2^2, 2^8 with the factor below
+constexpr float kCfFactor = 6.f;  // weights enter times 2^6 (E4M3 reaches 448)
+// A CTA's share is at least this many tiles: a shorter one would not pay for its joining.
+constexpr int kCfMinTiles = 2;
+
+struct alignas(16) CfPiece {
+  int32_t r, rt, kvh;   // request, row tile (pair), KV head
+  int32_t begin, take;  // tiles [begin, begin + take)
+  int32_t n;            // of n; 0: no more pieces
+  int32_t pad0, pad1;
+};
+
+struct CfBars {
+  uint64_t full[kCfSlots], empty[kCfSlots];
+  uint64_t sc_full[kCfScaleSlots], sc_empty[kCfScaleSlots];
+  uint64_t q_full[2];
+  uint64_t q_empty;            // !kWide: the other half is done with the queries
+  uint64_t join_full, join_free;
+  uint64_t s_full[2];
+  uint64_t p_full[2][2];
+  uint64_t o_done[2];
+  uint64_t u_full[2], u_empty[2];
+  CfPiece piece[2];
+  uint32_t tmem_base;
+};
+static_assert(sizeof(CfBars) <= 528 && offsetof(CfBars, piece) % 16 == 0, "barrier area");
+
+template <int kRegs>
+__device__ __forceinline__ void cf_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void cf_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], 8-bit floating-point operands (A: four to a column).
+__device__ __forceinline__ void mma_f8_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two FP32 values (the first in the low half) as FP16, as E4M3 and what that leaves as E4M3.
+__device__ __forceinline__ void cf_parts(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t h, back;
+  uint16_t a, b;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
+  hi = a;
+  lo = b;
+}
+
+// The power of two that brings a row's largest |q| (BF16 bits) into [2^7, 2^8); 1 for zeros.
+__device__ __forceinline__ float cf_sigma(uint32_t amax_bits) {
+  if (amax_bits == 0) return 1.f;
+  const int e = max(static_cast<int>((amax_bits >> 7) & 0xffu) - 127, -126);
+  return __int_as_float((127 + min(max(7 - e, -120), 120)) << 23);
+}
+
+// Tiles of keys that a row tile of a request reads.
+__device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int64_t pair, int n_rt, int pos) {
+  const int r = static_cast<int>(pair / n_rt);
+  const int rt = static_cast<int>(pair - static_cast<int64_t>(r) * n_rt);
+  const int ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
+  const int end = ctx - max(a.q_len - (rt + 1) * pos, 0);
+  return end > 0 ? (end + kCfTokens - 1) / kCfTokens : 0;
+}
+
+template <bool kWide>
+__global__ void __launch_bounds__(kCfThreads, 1)
+    paged_chunk_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                              const ChunkScaledArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  auto* bars = reinterpret_cast<CfBars*>(smem + kCfOffBar);
+  auto uniform = [](int x) -> int { return __shfl_sync(0xffffffffu, x, 0); };
+  const int warp = uniform(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kCfSlots; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], kWide ? 2 : 1);
+    }
+    for (int s = 0; s < kCfScaleSlots; ++s) {
+      mbar_init(&bars->sc_full[s], 1);
+      mbar_init(&bars->sc_empty[s], kWide ? 8 : 4);
+    }
+    mbar_init(&bars->q_empty, 5);  // warps 4-7, the second MMA issuer
+    mbar_init(&bars->join_full, 128);
+    mbar_init(&bars->join_free, 128);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 128);
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t][0], 128);
+      mbar_init(&bars->p_full[t][1], 128);
+      mbar_init(&bars->o_done[t], 1);
+      mbar_init(&bars->u_full[t], 1);
+      mbar_init(&bars->u_empty[t], 11);  // every other warp
+    }
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&bars->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tc::prefetch_tensor_map(&k_map);
+    tc::prefetch_tensor_map(&v_map);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  pdl_wait();  // everything below may read what earlier grids in the stream write
+  pdl_trigger();
+
+  constexpr int kPos = kWide ? 2 * kCfPos : kCfPos;  // positions of a piece
+  const int n_rt = (a.q_len + kPos - 1) / kPos;
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * n_rt;
+  const int hq = a.num_kv_heads * kGroup;
+  const uint32_t tmem = uniform(bars->tmem_base);
+  const uint32_t sbase = uniform(smem_addr(smem));
+  bool ok = true;
+
+  uint32_t walked = 0;
+  auto next_piece = [&](CfPiece& u) -> bool {
+    const int slot = walked & 1;
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->u_full[slot], (walked >> 1) & 1));
+    if (!ok) return false;
+    const int4 x = reinterpret_cast<const int4*>(&bars->piece[slot])[0];
+    const int4 y = reinterpret_cast<const int4*>(&bars->piece[slot])[1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->u_empty[slot]);
+    ++walked;
+    u.r = uniform(x.x);
+    u.rt = uniform(x.y);
+    u.kvh = uniform(x.z);
+    u.begin = uniform(x.w);
+    u.take = uniform(y.x);
+    u.n = uniform(y.y);
+    return u.n > 0;
+  };
+  // tiles of the piece that half t works on
+  auto tiles_of = [&](const CfPiece& u, int t) -> int { return kWide ? u.take : (u.take - t + 1) >> 1; };
+
+  if (warp >= 8) {
+    cf_regs_down<kCfIssueRegs>();
+    if (warp == 11) {
+      // ------------------------ pieces and scales ------------------------
+      int64_t total = 0;
+      for (int64_t p = lane; p < pairs; p += 32) total += cf_tiles(a, p, n_rt, kPos);
+      if (blockIdx.x == 0)
+        for (int r = lane; r < a.num_seqs; r += 32)
+          if (a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+      total *= a.num_kv_heads;
+      const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kCfMinTiles));
+      const int64_t t0 = per * blockIdx.x;
+      int64_t left = min(per, total - t0);  // tiles of this CTA (<= 0: none)
+      // the job that tile t0 belongs to
+      int64_t pair = 0;
+      int n = 0, kvh = 0, begin = 0;
+      if (left > 0) {
+        int64_t before = 0;
+        for (int64_t p0 = 0;; p0 += 32) {
+          const int x = p0 + lane < pairs ? cf_tiles(a, p0 + lane, n_rt, kPos) : 0;
+          int64_t upto = static_cast<int64_t>(x) * a.num_kv_heads;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
+          if (past != 0) {
+            const int at = __ffs(past) - 1;
+            n = __shfl_sync(0xffffffffu, x, at);
+            const int64_t start = before + __shfl_sync(0xffffffffu, upto, at) - static_cast<int64_t>(n) * a.num_kv_heads;
+            pair = p0 + at;
+            kvh = static_cast<int>((t0 - start) / n);
+            begin = static_cast<int>((t0 - start) - static_cast<int64_t>(kvh) * n);
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+      if (lane == 0) {  // for the joining kernel
+        CfCut cut{};
+        cut.r = static_cast<int32_t>(pair / n_rt);
+        cut.rt = static_cast<int32_t>(pair - static_cast<int64_t>(cut.r) * n_rt);
+        cut.kvh = kvh;
+        cut.begin = begin;
+        cut.n = n;
+        cut.per = per;
+        a.cuts[blockIdx.x] = cut;
+      }
+      uint32_t tiles = 0;  // scale slots written so far
+      // the scales of a piece's blocks, 32 blocks (4 tiles) at a time, fetched a group ahead
+      auto scales_of = [&](const CfPiece& u) {
+        const int32_t* table = a.block_tables + static_cast<int64_t>(u.r) * a.max_blocks;
+        const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
+        const int last = (ctx + kBlockSize - 1) / kBlockSize;  // blocks past the context have no scale
+        auto fetch = [&](int group, float& ks, float& vs) {
+          const int lb = (u.begin + 4 * group) * kCfTileBlocks + lane;
+          ks = vs = 1.f;
+          if (lb < last && lb < (u.begin + u.take) * kCfTileBlocks) {
+            int b = table[lb];
+            if (b < 0 || b >= a.num_blocks) b = 0;  // (reported by the producer)
+            const int64_t at = static_cast<int64_t>(b) * a.num_kv_heads + u.kvh;
+            ks = a.k_scales[at];
+            vs = a.v_scales[at];
+          }
+        };
+        const int groups = (u.take + 3) >> 2;
+        float ks, vs, ks_next = 1.f, vs_next = 1.f;
+        fetch(0, ks, vs);
+        for (int g = 0; g < groups && ok; ++g) {
+          if (g + 1 < groups) fetch(g + 1, ks_next, vs_next);
+          const float lv = log2f(vs), iv = 1.f / vs;
+          for (int k = 0; k < 4 && 4 * g + k < u.take && ok; ++k, ++tiles) {
+            const int slot = tiles % kCfScaleSlots;
+            if (tiles >= kCfScaleSlots)
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars->sc_empty[slot], ((tiles / kCfScaleSlots) & 1) ^ 1));
+            if (!ok) break;
+            float* dst = reinterpret_cast<float*>(smem + kCfOffScale) + slot * kCfScaleFloats + (lane & 7);
+            if ((lane >> 3) == k) {
+              dst[0] = ks;
+              dst[kCfTileBlocks] = lv;
+              dst[2 * kCfTileBlocks] = iv;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->sc_full[slot]);
+          }
+          ks = ks_next;
+          vs = vs_next;
+        }
+      };
+      CfPiece now{}, was{};
+      for (uint32_t round = 0;; ++round) {
+        was = now;
+        now = CfPiece{};
+        if (left > 0) {
+          now.r = static_cast<int32_t>(pair / n_rt);
+          now.rt = static_cast<int32_t>(pair - static_cast<int64_t>(now.r) * n_rt);
+          now.kvh = kvh;
+          now.begin = begin;
+          now.take = static_cast<int32_t>(min(left, static_cast<int64_t>(n - begin)));
+          now.n = n;
+          left -= now.take;
+          begin = 0;
+          if (++kvh == a.num_kv_heads) {  // (used only if tiles are left: the next job then starts here)
+            kvh = 0;
+            for (++pair; left > 0 && pair < pairs && (n = cf_tiles(a, pair, n_rt, kPos)) == 0; ++pair) {
+            }
+          }
+        }
+        const int slot = round & 1;
+        if (round >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_empty[slot], ((round >> 1) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          bars->piece[slot] = now;
+          mbar_arrive(&bars->u_full[slot]);
+        }
+        __syncwarp();
+        if (round > 0) scales_of(was);
+        if (!ok || now.n == 0) break;
+      }
+      if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
+    } else if (warp == 8) {
+      // ---------------------------- TMA producer ----------------------------
+      // K of a tile: lanes 0-7, V: lanes 8-15.
+      // read once, unless several row tiles of the request read the same blocks
+      const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+      const int oob_row = a.num_blocks * a.num_kv_heads * kBlockSize;  // first row past the pool
+      const bool is_v = lane >= kCfTileBlocks;
+      uint32_t filled = 0;  // tiles so far
+      CfPiece u;
+      while (next_piece(u)) {
+        const int32_t* table = a.block_tables + static_cast<int64_t>(u.r) * a.max_blocks;
+        const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
+        const int last = (ctx + kBlockSize - 1) / kBlockSize;
+        const int b0 = u.begin * kCfTileBlocks, b1 = min(last, b0 + u.take * kCfTileBlocks);
+        auto row_of = [&](int i, int id) -> int {  // pool row of the piece's i-th block
+          if (b0 + i >= b1) return oob_row;
+          if (id < 0 || id >= a.num_blocks) {
+            report(a.err, PKV_DEVERR_BLOCK_ID);
+            id = 0;
+          }
+          return (id * a.num_kv_heads + u.kvh) * kBlockSize;
+        };
+        auto entry = [&](int i) -> int { return table[min(b0 + i, a.max_blocks - 1)]; };
+        int cur = row_of(lane, entry(lane)), next = 0;
+        for (int j = 0; j < u.take && ok; ++j, ++filled) {
+          if ((j & 3) == 0) next = entry(8 * j + 32 + lane);  // the next four tiles' ids
+          const int y = __shfl_sync(0xffffffffu, cur, (j & 3) * kCfTileBlocks + (lane & 7));
+          if ((j & 3) == 3) cur = row_of(8 * (j + 1) + lane, next);
+          const uint32_t place = 2 * filled + (is_v ? 1 : 0);
+          const uint32_t slot = place % kCfSlots;
+          bool mine = true;
+          if (place >= kCfSlots) mine = mbar_wait(&bars->empty[slot], ((place / kCfSlots) & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, mine);
+          if (!ok) break;
+          if (lane == 0 || lane == kCfTileBlocks) mbar_arrive_expect_tx(&bars->full[slot], kCfTileBytes);
+          __syncwarp();
+          if (lane < 2 * kCfTileBlocks)
+            tc::tma_load_2d(smem + kCfOffRing + slot * kCfTileBytes + (lane & 7) * kCfBoxBytes, is_v ? &v_map : &k_map, 0,
+                            y, &bars->full[slot], policy);
+        }
+        if (!ok) break;
+      }
+      if (lane == 0 && !ok) {
+        report(a.err, PKV_DEVERR_TIMEOUT);
+        // copies under way must land before shared memory is released
+        for (uint32_t f = 2 * filled > kCfSlots ? 2 * filled - kCfSlots : 0; f < 2 * filled; ++f)
+          mbar_wait(&bars->full[f % kCfSlots], (f / kCfSlots) & 1);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------- MMA issuers ----------------------------
+      constexpr uint32_t kIdS = tc::idesc_e4m3_f32(kCfRows, kCfTokens, false, false);
+      constexpr uint32_t kIdO = tc::idesc_e4m3_f32(kCfRows, kHeadDim, false, true);
+      const int t = warp - 9;
+      const bool leader = lane == 0;
+      const uint32_t scol = tmem + t * kCfTileCols;
+      const uint64_t q_desc = tc::smem_desc(sbase + kCfOffQ + (kWide ? t * 2 * kCfTileBytes : 0), 16, 1024);
+      const uint64_t ring = tc::smem_desc(sbase + kCfOffRing, 16, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+      };
+      auto wait_full = [&](uint32_t place) -> bool { return wait(&bars->full[place % kCfSlots], (place / kCfSlots) & 1); };
+      auto give_back = [&](uint32_t place) {
+        if (leader) mbar_arrive(&bars->empty[place % kCfSlots]);
+      };
+      // S = (high + low parts of the queries) K^T
+      auto issue_s = [&](uint32_t place) {
+        const uint64_t kd = ring + (place % kCfSlots) * (kCfTileBytes >> 4);
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_f8(scol, q_desc + (((kk >> 2) * kCfTileBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
+                       kk > 0 ? 1u : 0u);
+          tc::commit(&bars->s_full[t]);
+        }
+        __syncwarp();
+      };
+      // O += (high + low parts of the weights) V, 64 keys
+      auto issue_pv = [&](uint32_t place, int half, bool first) {
+        const uint64_t vd = ring + (place % kCfSlots) * (kCfTileBytes >> 4);
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int slice = 2 * half + (kk & 1);  // of 32 keys
+            mma_f8_tmem_a(scol + kCfColO, scol + 32 * (kk >> 1) + 8 * slice, vd + slice * (4096 >> 4), kIdO,
+                          (!first || kk > 0) ? 1u : 0u);
+          }
+          if (half == 1) tc::commit(&bars->o_done[t]);
+        }
+        __syncwarp();
+      };
+      constexpr uint32_t kStep = kWide ? 2 : 4;  // ring places from one of its tiles to the next
+      uint32_t c0 = 0;                           // ring place of the piece's first tile
+      uint32_t g = 0;                            // tiles of this half so far
+      uint32_t pieces = 0;
+      CfPiece u;
+      while (next_piece(u)) {
+        const int n_t = tiles_of(u, t);
+        uint32_t c = c0 + (kWide ? 0 : 2 * t);
+        c0 += 2 * u.take;
+        ok = wait(&bars->q_full[kWide ? t : 0], pieces & 1);
+        ++pieces;
+        if (ok && n_t > 0) {
+          ok = wait_full(c);
+          if (ok) issue_s(c);
+        }
+        for (int j = 0; j < n_t && ok; ++j, ++g, c += kStep) {
+          ok = wait_full(c + 1) && wait(&bars->p_full[t][0], g & 1);
+          if (ok) issue_pv(c + 1, 0, j == 0);
+          ok = ok && wait(&bars->p_full[t][1], g & 1);
+          if (!ok) break;
+          give_back(c);  // the weights were made from this tile's scores
+          issue_pv(c + 1, 1, false);
+          // The next scores go where the weights are, so after this product.
+          if (j + 1 < n_t) ok = wait_full(c + kStep);
+          ok = ok && wait(&bars->o_done[t], g & 1);
+          if (!ok) break;
+          give_back(c + 1);
+          if (j + 1 < n_t) issue_s(c + kStep);
+        }
+        if (!ok) break;
+        if (!kWide && t == 1 && leader) mbar_arrive(&bars->q_empty);
+      }
+      if (!ok && leader) report(a.err, PKV_DEVERR_TIMEOUT);
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------- softmax ----------------------------
+    cf_regs_up<kCfSoftmaxRegs>();
+    const int t = warp >> 2;
+    const int quad = warp & 3;  // TMEM sub-partition of this warp
+    const int row = quad * 32 + lane;
+    const uint32_t scol = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * kCfTileCols;
+    float* inv_sigma = reinterpret_cast<float*>(smem + kCfOffSigma) + (kWide ? t * kCfRows : 0);
+    const int row_tile = kWide ? t : 0;  // row tile of this warpgroup's rows
+
+    // rows that see no key at all belong to no piece: zeros
+    for (int64_t p = blockIdx.x; p < pairs; p += gridDim.x) {
+      if (cf_tiles(a, p, n_rt, kPos) > 0) continue;
+      const int64_t r = p / n_rt;
+      const int pos0 = static_cast<int>(p - r * n_rt) * kPos;
+      const int64_t chunks = static_cast<int64_t>(min(kPos, a.q_len - pos0)) * hq * (kHeadDim * 2 / 16);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (r * a.q_len + pos0) * hq * kHeadDim);
+      for (int64_t i = threadIdx.x; i < chunks; i += 256) o[i] = make_uint4(0, 0, 0, 0);
+    }
+
+    uint32_t g = 0;      // tiles of this half so far
+    uint32_t tile0 = 0;  // tiles of the pieces so far
+    uint32_t pieces = 0;
+    uint32_t joins = 0;
+    CfPiece u;
+    while (next_piece(u)) {
+      const int n_t = tiles_of(u, t);
+      const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
+      const int pos0 = u.rt * kPos + row_tile * kCfPos;  // first query of the row tile
+      const int live_rows = (min(pos0 + kCfPos, a.q_len) - pos0) * kGroup;
+      const bool warp_live = quad * 32 < live_rows;
+      const bool valid = row < live_rows;
+      const int qi = pos0 + (row >> 2);
+      const int seen = ctx - a.q_len + qi + 1;  // keys that this row sees (<= 0: none)
+      const int warp_seen = ctx - a.q_len + pos0 + quad * 8 + 1;  // its warp's first row
+      // ---- the query operand: 8 lanes a row, 16 dims each ----
+      if (kWide || t == 0) {
+        uint8_t* qa = smem + kCfOffQ + row_tile * 2 * kCfTileBytes;
+        if (!kWide && pieces > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (pieces & 1) ^ 1));
+          if (!ok) break;
+        }
+        const int c16 = lane & 7;
+#pragma unroll
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+          if (!warp_live) break;
+          uint4 w[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = quad * 32 + 4 * (i0 + i) + (lane >> 3);
+            w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+            if (m < live_rows) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  static_cast<const uint16_t*>(a.q) +
+                  ((static_cast<int64_t>(u.r) * a.q_len + pos0 + (m >> 2)) * hq + u.kvh * kGroup + (m & 3)) * kHeadDim +
+                  16 * c16);
+              w[i][0] = src[0];
+              w[i][1] = src[1];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = quad * 32 + 4 * (i0 + i) + (lane >> 3);
+            const uint32_t wv[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w,
+                                    w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+            uint32_t amax = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = max(amax, max(wv[e] & 0x7fffu, (wv[e] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+            const float sigma = cf_sigma(amax);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h0, l0, h1, l1;
+              cf_parts(bf16_lo(wv[2 * k]) * sigma, bf16_hi(wv[2 * k]) * sigma, h0, l0);
+              cf_parts(bf16_lo(wv[2 * k + 1]) * sigma, bf16_hi(wv[2 * k + 1]) * sigma, h1, l1);
+              hi[k] = h0 | (h1 << 16);
+              lo[k] = l0 | (l1 << 16);
+            }
+            const uint32_t at = tc::sw128_offset_b8(m, 16 * c16);
+            *reinterpret_cast<uint4*>(qa + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(qa + kCfTileBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (c16 == 0) inv_sigma[m] = a.scale_log2 / sigma;
+          }
+        }
+        tc::fence_proxy_async_smem();
+        mbar_arrive(&bars->q_full[row_tile]);
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[row_tile], pieces & 1));
+      ++pieces;
+      if (!ok) break;
+      const float c = inv_sigma[row];
+      if (!kWide && t == 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_empty);
+      }
+      float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum by at most 2)
+      float l = 0.f;        // sum of w / vs, times 2^6
+      for (int j = 0; j < n_t; ++j, ++g) {
+        const int in_piece = kWide ? j : 2 * j + t;
+        const int tok = (u.begin + in_piece) * kCfTokens;
+        const uint32_t sl = (tile0 + in_piece) % kCfScaleSlots;
+        // (`ok` stays warp-uniform: the loads below are warp-collective)
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&bars->sc_full[sl], ((tile0 + in_piece) / kCfScaleSlots) & 1) &&
+                            mbar_wait(&bars->s_full[t], g & 1));
+        if (!ok) break;
+        // the tile's 8 blocks: ks, log2 vs, 1 / vs (read twice: registers are dearer)
+        const float* sc = reinterpret_cast<const float*>(smem + kCfOffScale) + sl * kCfScaleFloats;
+        tc::fence_after_sync();
+        if (warp_live) {
+          float s[128];
+          tc::tmem_ld32(scol, s);
+          tc::tmem_ld32(scol + 32, s + 32);
+          tc::tmem_ld32(scol + 64, s + 64);
+          tc::tmem_ld32(scol + 96, s + 96);
+          tc::tmem_wait_ld();
+          if (warp_seen - tok < kCfTokens) {  // some row of the warp sees the tile in part
+            const int lim = seen - tok;
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e >= lim) s[e] = -INFINITY;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            float x = fmaxf(s[16 * b], s[16 * b + 1]);
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) x = fmaxf(fmaxf(x, s[16 * b + e]), s[16 * b + e + 1]);
+            mx = fmaxf(mx, fmaf(x, sc[b] * c, sc[kCfTileBlocks + b]));  // (the factor is > 0)
+          }
+          const bool grow = mx > m + kCfLag;  // also true the first time a row sees a key
+          const float m_new = grow ? mx : m;
+          const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
+          if (__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY)) {
+            // O holds weights taken against the old maxima (the products
+            // before this tile's scores are done): rescale this warp's rows
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc) {
+              float o[16];
+              tc::tmem_ld16(scol + kCfColO + 16 * cc, o);
+              tc::tmem_wait_ld();
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+              tc::tmem_st16u(scol + kCfColO + 16 * cc, w);
+            }
+            tc::tmem_wait_st();
+          }
+          l *= alpha;
+          m = m_new;
+          const float nm = (m == -INFINITY ? 0.f : -m) + kCfFactor;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 64 keys
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int blk = 4 * h + b;
+              const float kc = sc[blk] * c, off = sc[kCfTileBlocks + blk] + nm;
+              const float2 k2 = make_float2(kc, kc);
+              const float2 n2 = make_float2(off, off);
+              float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = 16 * blk + 4 * e;
+                const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), k2, n2);
+                const float2 y = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), k2, n2);
+                const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
+                const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
+                acc = __fadd2_rn(acc, make_float2(p0, p1));
+                acc = __fadd2_rn(acc, make_float2(p2, p3));
+                uint32_t h0, l0, h1, l1;
+                cf_parts(p0, p1, h0, l0);
+                cf_parts(p2, p3, h1, l1);
+                hi[4 * b + e] = h0 | (h1 << 16);
+                lo[4 * b + e] = l0 | (l1 << 16);
+              }
+              l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + blk], l);
+            }
+            // the weights overwrite the scores: high parts at columns 0-31, low parts at 32-63
+            tc::tmem_st16u(scol + 16 * h, hi);
+            tc::tmem_st16u(scol + 32 + 16 * h, lo);
+            if (h == 0 && ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
+              // slots past the context may hold any code: V's rows there are
+              // zeroed (a weight of zero is not enough)
+              const uint32_t vp = 2 * (tile0 + in_piece) + 1;
+              ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kCfSlots], (vp / kCfSlots) & 1));
+              const int z0 = max(ctx - tok, 0), z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
+              uint8_t* vt = smem + kCfOffRing + (vp % kCfSlots) * kCfTileBytes;
+              for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) reinterpret_cast<uint4*>(vt)[i] = make_uint4(0, 0, 0, 0);
+              tc::fence_proxy_async_smem();
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            mbar_arrive(&bars->p_full[t][h]);
+          }
+        } else {
+          mbar_arrive(&bars->p_full[t][0]);
+          mbar_arrive(&bars->p_full[t][1]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->sc_empty[sl]);
+      }
+      tile0 += u.take;
+      if (!ok) break;
+      // ---- results ----
+      if (n_t > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t], (g - 1) & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      const bool whole = u.take == u.n;
+      const int64_t out_row = (static_cast<int64_t>(u.r) * a.q_len + qi) * hq + u.kvh * kGroup + (row & 3);
+      const int64_t part_row = static_cast<int64_t>(2 * blockIdx.x + (u.begin == 0 ? 1 : 0)) * a.rows_slot +
+                               row_tile * kCfRows + row;
+      // !kWide: the odd tiles' half hands its sums over, 64 dims at a time
+      const bool join = !kWide && u.take > 1;
+      float4* jbuf = reinterpret_cast<float4*>(smem + kCfOffJoin) + row * 16;  // 16-byte chunk ch at ch ^ (row % 8)
+      float* join_m = reinterpret_cast<float*>(smem + kCfOffMax) + row;
+      float* join_l = reinterpret_cast<float*>(smem + kCfOffSigma) + kCfRows + row;
+      if (!kWide && t == 1) {
+        if (!join) continue;
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+          if (pass == 1) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_free, joins & 1));
+            if (!ok) break;
+          }
+          if (warp_live) {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              float o[32];
+              tc::tmem_ld32(scol + kCfColO + 64 * pass + 32 * cc, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                jbuf[(8 * cc + e) ^ (row & 7)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            if (pass == 0) {
+              *join_m = m;
+              *join_l = l;
+            }
+          }
+          mbar_arrive(&bars->join_full);
+        }
+        ++joins;
+        tc::fence_before_sync();
+        if (!ok) break;
+        continue;
+      }
+      float a0 = 1.f, a1 = 0.f;  // factors of this half's and the other half's sums
+      if (join) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_full, 0));
+        if (!ok) break;
+        const float om = *join_m, ol = *join_l;
+        const float mm = fmaxf(m, om);
+        a0 = m == -INFINITY ? 0.f : exp2_approx(m - mm);
+        a1 = om == -INFINITY ? 0.f : exp2_approx(om - mm);
+        l = l * a0 + ol * a1;
+        m = mm;
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN sum stays one)
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        if (join && pass == 1) {
+          mbar_arrive(&bars->join_free);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_full, 1));
+          if (!ok) break;
+        }
+        if (warp_live) {
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float o[32];
+            tc::tmem_ld32(scol + kCfColO + 64 * pass + 32 * cc, o);
+            tc::tmem_wait_ld();
+            if (join) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 x = jbuf[(8 * cc + e) ^ (row & 7)];
+                o[4 * e] = a0 * o[4 * e] + a1 * x.x;
+                o[4 * e + 1] = a0 * o[4 * e + 1] + a1 * x.y;
+                o[4 * e + 2] = a0 * o[4 * e + 2] + a1 * x.z;
+                o[4 * e + 3] = a0 * o[4 * e + 3] + a1 * x.w;
+              }
+            }
+            if (valid && whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim + 64 * pass + 32 * cc);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (l != 0.f)
+                  w = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                 pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                 pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                 pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                dst[e] = w;
+              }
+            } else if (valid) {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 64 * pass + 32 * cc);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+        }
+      }
+      if (join) ++joins;
+      if (!ok) break;
+      if (valid && !whole) a.part_ml[part_row] = l != 0.f ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      tc::fence_before_sync();  // O is read before the next piece's weights arrive
+    }
+    if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of a job that was cut.  Block x of the grid looks at the
+// cut where CTA x's share starts, and takes the job if that cut is its first;
+// one warp per row, 4 dims a lane.
+__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a, int32_t pos) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x + 1;
+  const CfCut cut = a.cuts[i];
+  if (cut.begin == 0) return;  // no cut here
+  const int64_t start = cut.per * i - cut.begin;  // the job's first tile
+  if (start / cut.per != i - 1) return;           // cut earlier already
+  const int pieces = static_cast<int>((start + cut.n - 1) / cut.per) - (i - 1) + 1;
+  const int lane = threadIdx.x & 31;
+  const int rows = min(pos, a.q_len - cut.rt * pos) * kGroup;
+  const int hq = a.num_kv_heads * kGroup;
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.y * 8) {
+    // the first piece lies in the second place of CTA i - 1, the others in the first of their CTAs
+    auto at = [&](int k) -> int64_t { return static_cast<int64_t>(2 * (i - 1 + k) + (k == 0 ? 1 : 0)) * a.rows_slot + row; };
+    float m = -INFINITY;
+    for (int k = lane; k < pieces; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const int64_t p = at(k);
+      const float2 ml = a.part_ml[p];
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + 4 * lane);
+      if (ml.y == 0.f) continue;  // it saw nothing: its O holds anything
+      const float f = exp2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t out_row = (static_cast<int64_t>(cut.r) * a.q_len + cut.rt * pos + (row >> 2)) * hq + cut.kvh * kGroup + (row & 3);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
+template <bool kWide>
+cudaError_t allow_smem_cf() {
+  static std::atomic<bool> done[64];  // per device; host threads may race on a first call
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(paged_chunk_fp8_tc_kernel<kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfSmem);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+template <bool kWide>
+cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.num_kv_heads * kBlockSize;
+  CUtensorMap kmap, vmap;
+  if (!make_pool_map_e4m3(&kmap, a.k_cache, rows) || !make_pool_map_e4m3(&vmap, a.v_cache, rows))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem_cf<kWide>();
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_chunk_fp8_tc_kernel<kWide>, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), kCfSmem, stream,
+                 1, kmap, vmap, a);
+  if (e != cudaSuccess || grid == 1) return e;
+  // 8 rows a block at a time; a job of few rows is joined by one block
+  const int32_t pos = kWide ? 2 * kCfPos : kCfPos;
+  const unsigned parts = (std::min(pos, a.q_len) * kGroup + 7) / 8;
+  return launch_pdl(chunk_join_kernel, dim3(static_cast<unsigned>(grid - 1), parts), dim3(256), 0, stream, 1, a, pos);
+}
+
+bool cf_wide(int32_t q_len) { return q_len > kCfPos; }
+
+}  // namespace
+
+int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t sm_count) {
+  const int32_t pos = cf_wide(q_len) ? 2 * kCfPos : kCfPos;
+  const int64_t jobs = static_cast<int64_t>(num_seqs) * num_kv_heads * ((q_len + pos - 1) / pos);
+  const int64_t tiles = jobs * ((max_blocks + kCfTileBlocks - 1) / kCfTileBlocks);  // at most
+  return static_cast<int32_t>(std::min<int64_t>(sm_count, (tiles + kCfMinTiles - 1) / kCfMinTiles));
+}
+
+int32_t chunk_scaled_rows(int32_t q_len) { return cf_wide(q_len) ? 2 * kCfRows : kGroup * q_len; }
+
+cudaError_t launch_paged_chunk_fp8_tc(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
+  return cf_wide(a.q_len) ? launch_cf<true>(a, grid, stream) : launch_cf<false>(a, grid, stream);
+}
+
+}  // namespace pkv

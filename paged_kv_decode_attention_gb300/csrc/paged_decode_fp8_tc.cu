@@ -119,11 +119,11 @@ static_assert(sizeof(FtBars) <= 512, "barrier area");
 enum class FtMode {
   kPlain,
   kFused,  // stores each request's new token and uses it
-  kScaled  // codes times a scale for each block and KV head; several queries per request
+  kScaled  // codes times a scale for each block and KV head
 };
 
 struct FtUnit {
-  int r, seq, kvh, split, b0, b1, n_tiles, ctx_keys, ctx_raw;
+  int r, kvh, split, b0, b1, n_tiles, ctx_keys, ctx_raw;
   // fused append: the tile and tile row holding the request's new token
   // (position ctx - 1) and its logical block; new_tile = -1 when the unit
   // does not hold it or there is no append
@@ -131,9 +131,7 @@ struct FtUnit {
 };
 
 // Unit u: split fastest, then KV head, then request.  kFused: also where the
-// request's new token falls (the fused append).  kScaled: then the request's
-// query; `r` counts (request, query) rows, and query i of q_len sees the keys
-// up to its own.
+// request's new token falls (the fused append).
 template <FtMode kMode>
 __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
   constexpr bool kFused = kMode == FtMode::kFused;
@@ -142,10 +140,8 @@ __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
   const int row = u / a.num_splits;
   x.r = row / a.num_kv_heads;
   x.kvh = row - x.r * a.num_kv_heads;
-  x.seq = kMode == FtMode::kScaled ? x.r / a.q_len : x.r;
-  x.ctx_raw = a.context_lens[x.seq];
-  int ctx = min(max(x.ctx_raw, 0), a.max_blocks * kBlockSize);
-  if (kMode == FtMode::kScaled) ctx = max(ctx - (a.q_len - 1 - (x.r - x.seq * a.q_len)), 0);
+  x.ctx_raw = a.context_lens[x.r];
+  const int ctx = min(max(x.ctx_raw, 0), a.max_blocks * kBlockSize);
   const int nb = (ctx + kBlockSize - 1) / kBlockSize;
   x.b0 = x.split * a.blocks_per_split;
   x.b1 = min(nb, x.b0 + a.blocks_per_split);
@@ -199,7 +195,7 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
   for (int u = blockIdx.x; u < num_units && ok; u += gridDim.x) {
     const FtUnit x = ft_unit<kMode>(a, u);
     if (x.n_tiles == 0) continue;
-    const int32_t* table = a.block_tables + static_cast<int64_t>(x.seq) * a.max_blocks;
+    const int32_t* table = a.block_tables + static_cast<int64_t>(x.r) * a.max_blocks;
     // the load stays inside the table row whatever the context length, so it
     // need not wait for that length; entries past the unit's blocks are dropped
     // where they would be used, and the others (of any value) checked there
@@ -883,7 +879,7 @@ cudaError_t launch_ft(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
 cudaError_t launch_paged_decode_fp8_tc(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
   if (grid <= 0) return cudaSuccess;
   const bool scaled = a.k_scales != nullptr, fused = a.k_new != nullptr;
-  if ((!scaled && a.q_len != 1) || a.num_splits < 1 ||
+  if (a.q_len != 1 || a.num_splits < 1 ||
       (a.num_splits > 1 && (a.part_o == nullptr || a.part_lse == nullptr)))
     return cudaErrorInvalidValue;
   if (fused && (a.v_new == nullptr || a.slot_mapping == nullptr || scaled)) return cudaErrorInvalidValue;

@@ -1227,14 +1227,36 @@ bool aligned(std::initializer_list<const void*> ps, uintptr_t align) {
 constexpr int32_t kScaledMaxBlocks = 1 << 26;
 constexpr int32_t kScaledMaxQLen = 1 << 26;
 
-int64_t scaled_rows(int32_t num_seqs, int32_t q_len) { return static_cast<int64_t>(num_seqs) * q_len; }
+// How a call over block-scaled pools runs, and what its workspace holds.
+struct ScaledPlan {
+  int32_t grid = 0;     // CTAs that share the work
+  int32_t bps = 0;      // q_len 1: blocks per split
+  int32_t splits = 1;
+  size_t ml_at = 0, cuts_at = 0;  // offsets in the workspace
+  size_t bytes = 0;
+};
 
-int32_t scaled_blocks_per_split(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks,
-                                int32_t sm_count) {
-  if (max_blocks <= 0) return 1;
-  if (sm_count <= 0) sm_count = device_sm_count();
-  const int64_t rows = scaled_rows(num_seqs > 0 ? num_seqs : 1, q_len > 0 ? q_len : 1) * (num_kv_heads > 0 ? num_kv_heads : 1);
-  return persistent_blocks_per_split(rows, max_blocks, sm_count, 16);
+ScaledPlan scaled_plan(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads, int32_t max_blocks) {
+  ScaledPlan p;
+  const int sms = device_sm_count();
+  if (q_len == 1) {
+    const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
+    p.bps = std::min(persistent_blocks_per_split(rows, max_blocks, sms, 16), max_blocks);
+    p.splits = (max_blocks + p.bps - 1) / p.bps;
+    const int64_t units = rows * p.splits;
+    p.grid = static_cast<int32_t>(units < sms ? units : sms);
+    if (p.splits > 1) {
+      p.ml_at = align_up(static_cast<size_t>(rows) * kGroup * p.splits * kHeadDim * sizeof(float), 256);
+      p.bytes = p.ml_at + align_up(static_cast<size_t>(rows) * kGroup * p.splits * sizeof(float), 256);
+    }
+    return p;
+  }
+  p.grid = chunk_scaled_grid(num_seqs, num_kv_heads, q_len, max_blocks, sms);
+  const size_t rows = static_cast<size_t>(p.grid) * 2 * chunk_scaled_rows(q_len);
+  p.ml_at = align_up(rows * kHeadDim * sizeof(float), 256);
+  p.cuts_at = p.ml_at + align_up(rows * sizeof(float2), 256);
+  p.bytes = p.cuts_at + align_up(static_cast<size_t>(p.grid) * sizeof(CfCut), 256);
+  return p;
 }
 
 }  // namespace
@@ -1319,31 +1341,23 @@ pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scale
   return launch_kv_append_scaled(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-int32_t pkv_choose_kv_blocks_per_split_fp8_scaled(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
-                                                  int32_t max_blocks_per_seq, int32_t sm_count) {
-  return scaled_blocks_per_split(num_seqs, num_kv_heads, q_len, max_blocks_per_seq, sm_count);
-}
-
 size_t pkv_workspace_size_fp8_scaled(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
-                                     int32_t max_blocks_per_seq, int32_t kv_blocks_per_split) {
-  if (num_seqs <= 0 || q_len <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || kv_blocks_per_split < 0) return 0;
-  int32_t bps = kv_blocks_per_split;
-  if (bps == 0) bps = scaled_blocks_per_split(num_seqs, (num_q_heads + kGroup - 1) / kGroup, q_len, max_blocks_per_seq, 0);
-  if (bps >= max_blocks_per_seq) return 0;
-  const size_t splits = (static_cast<size_t>(max_blocks_per_seq) + bps - 1) / bps;
-  const size_t rows = static_cast<size_t>(scaled_rows(num_seqs, q_len)) * num_q_heads;
-  return align_up(rows * splits * kHeadDim * sizeof(float), 256) + align_up(rows * splits * sizeof(float), 256);
+                                     int32_t max_blocks_per_seq) {
+  if (num_seqs <= 0 || q_len <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 ||
+      max_blocks_per_seq > kScaledMaxBlocks || q_len > kScaledMaxQLen)
+    return 0;
+  return scaled_plan(num_seqs, q_len, (num_q_heads + kGroup - 1) / kGroup, max_blocks_per_seq).bytes;
 }
 
 pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* k_cache, const void* v_cache,
                                           const float* k_scales, const float* v_scales, const pkv_cache_desc* cache,
                                           const int32_t* block_tables, int32_t max_blocks_per_seq,
                                           const int32_t* context_lens, int32_t num_seqs, int32_t q_len,
-                                          int32_t num_q_heads, float scale, int32_t kv_blocks_per_split,
-                                          void* workspace, size_t workspace_bytes, void* stream) {
+                                          int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
   const pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
-  if (num_seqs < 0 || q_len < 1 || max_blocks_per_seq < 1 || kv_blocks_per_split < 0) return PKV_ERR_SHAPE;
+  if (num_seqs < 0 || q_len < 1 || max_blocks_per_seq < 1) return PKV_ERR_SHAPE;
   if (num_q_heads != kGroup * cache->num_kv_heads) return PKV_ERR_UNSUPPORTED;
   if (cache->num_blocks == 0 && num_seqs > 0) return PKV_ERR_SHAPE;
   if (max_blocks_per_seq > kScaledMaxBlocks || q_len > kScaledMaxQLen ||
@@ -1355,13 +1369,37 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
     return PKV_ERR_NULL;
   if (!aligned({out, q, k_cache, v_cache}, 16) || !aligned({k_scales, v_scales, block_tables, context_lens}, 4))
     return PKV_ERR_UNSUPPORTED;
-  int32_t bps = kv_blocks_per_split;
-  if (bps == 0) bps = scaled_blocks_per_split(num_seqs, cache->num_kv_heads, q_len, max_blocks_per_seq, 0);
-  bps = std::min(bps, max_blocks_per_seq);
-  const int32_t splits = (max_blocks_per_seq + bps - 1) / bps;
-  const int64_t rows = scaled_rows(num_seqs, q_len);
-  const int64_t units = rows * cache->num_kv_heads * splits;
-  if (rows * num_q_heads > 0x7fffffff || units > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_seqs) * q_len * num_q_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  const ScaledPlan p = scaled_plan(num_seqs, q_len, cache->num_kv_heads, max_blocks_per_seq);
+  if (q_len == 1 && static_cast<int64_t>(num_seqs) * cache->num_kv_heads * p.splits > 0x7fffffff)
+    return PKV_ERR_UNSUPPORTED;
+  if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes || !aligned({workspace}, 256)))
+    return PKV_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (q_len > 1) {
+    ChunkScaledArgs a{};
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
+    a.cuts = reinterpret_cast<CfCut*>(ws + p.cuts_at);
+    a.err = error_word();
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = cache->num_blocks;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.num_seqs = num_seqs;
+    a.q_len = q_len;
+    a.rows_slot = chunk_scaled_rows(q_len);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return launch_paged_chunk_fp8_tc(a, p.grid, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   DecodeArgs a{};
   a.out = out;
   a.q = q;
@@ -1375,26 +1413,19 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
   a.max_blocks = max_blocks_per_seq;
   a.num_blocks = cache->num_blocks;
   a.num_kv_heads = cache->num_kv_heads;
-  a.num_seqs = static_cast<int32_t>(rows);
-  a.q_len = q_len;
-  a.blocks_per_split = bps;
-  a.num_splits = splits;
+  a.num_seqs = num_seqs;
+  a.q_len = 1;
+  a.blocks_per_split = p.bps;
+  a.num_splits = p.splits;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.part_slots = splits;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (splits > 1) {
-    const size_t need = pkv_workspace_size_fp8_scaled(num_seqs, q_len, num_q_heads, max_blocks_per_seq, bps);
-    if (workspace == nullptr || workspace_bytes < need || !aligned({workspace}, 256)) return PKV_ERR_WORKSPACE;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                          align_up(static_cast<size_t>(rows) * num_q_heads * splits * kHeadDim * sizeof(float), 256));
+  a.part_slots = p.splits;
+  if (p.splits > 1) {
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_lse = reinterpret_cast<float*>(ws + p.ml_at);
   }
-  const int sms = device_sm_count();
-  if (launch_paged_decode_fp8_tc(a, static_cast<int32_t>(units < sms ? units : sms), s) != cudaSuccess)
-    return PKV_ERR_CUDA;
-  if (splits == 1) return PKV_OK;
-  return launch_attn_combine(out, nullptr, a.part_o, a.part_lse, static_cast<int32_t>(rows * num_q_heads), splits, s) ==
-                 cudaSuccess
+  if (launch_paged_decode_fp8_tc(a, p.grid, s) != cudaSuccess) return PKV_ERR_CUDA;
+  if (p.splits == 1) return PKV_OK;
+  return launch_attn_combine(out, nullptr, a.part_o, a.part_lse, num_seqs * num_q_heads, p.splits, s) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

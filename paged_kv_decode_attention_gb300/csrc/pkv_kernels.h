@@ -99,8 +99,7 @@ struct DecodeArgs {
   const void* k_new;
   const void* v_new;
   const int64_t* slot_mapping;
-  // E4M3 pools with block scales: FP32 [num_blocks][Hkv] (paged_decode_fp8_tc.cu
-  // takes q_len queries per request then, num_seqs counting (request, query) rows)
+  // E4M3 pools with block scales: FP32 [num_blocks][Hkv] (paged_decode_fp8_tc.cu); NULL = no scales
   const float* k_scales;
   const float* v_scales;
 };
@@ -289,6 +288,38 @@ cudaError_t launch_kv_append_scaled(const AppendScaledArgs& a, cudaStream_t stre
 cudaError_t launch_copy_blocks_scaled(uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
                                       int32_t num_blocks, int32_t num_kv_heads, const int32_t* src,
                                       const int32_t* dst, int32_t num_pairs, unsigned int* err, cudaStream_t stream);
+
+// Attention of several queries per request over such pools (paged_chunk_fp8_tc.cu).
+struct CfCut {  // where a CTA's share of the tiles starts, for the joining kernel
+  int32_t r, rt, kvh;
+  int32_t begin, n;  // tile `begin` of the job's n
+  int32_t pad;
+  int64_t per;       // tiles of a share
+};
+struct ChunkScaledArgs {
+  void* out;                    // BF16 [B][q_len][Hq][D]
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;        // [num_blocks][Hkv]
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* part_o;                // FP32 [grid][2][rows_slot][D], un-normalised
+  float2* part_ml;              // [grid][2][rows_slot]: maximum (base 2), sum
+  CfCut* cuts;                  // [grid]
+  unsigned int* err;
+  int32_t max_blocks;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t num_seqs;
+  int32_t q_len;
+  int32_t rows_slot;            // chunk_scaled_rows
+  float scale_log2;
+};
+int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t sm_count);
+int32_t chunk_scaled_rows(int32_t q_len);
+cudaError_t launch_paged_chunk_fp8_tc(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream);
 
 // Device error word of the current device (PKV_DEVERR_* bits).
 unsigned int* device_error_word();

@@ -28,6 +28,7 @@
 //   warp 11 : finds the CTA's units, one ahead of the others.
 #include <climits>
 #include <cmath>
+#include <cstddef>
 
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
@@ -59,7 +60,7 @@ static_assert(kPaSmem <= 227 * 1024, "one CTA per SM");
 constexpr float kPaLag = 16.f;
 constexpr float kPaLn2 = 0.6931471805599453f;
 
-struct PaUnit {
+struct alignas(16) PaUnit {
   int32_t tok0;  // the prompt's first row
   int32_t len;   // its tokens; 0: no more units
   int32_t pos0;  // the unit's first position
@@ -77,7 +78,7 @@ struct PaBars {
   PaUnit unit[2];
   uint32_t tmem_base;
 };
-static_assert(sizeof(PaBars) <= 512, "barrier area");
+static_assert(sizeof(PaBars) <= 512 && offsetof(PaBars, unit) % 16 == 0, "barrier area");
 
 template <int kRegs>
 __device__ __forceinline__ void pa_regs_up() {

@@ -421,10 +421,10 @@ PyObject* kv_append_fp8_scaled(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-//  q_len, scale, kv_blocks_per_split, workspace, stream)
+//  q_len, scale, workspace, stream)
 PyObject* paged_attention_fp8_scaled(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> pkv_status {
-    Call c(args, n, 13);
+    Call c(args, n, 12);
     const at::Tensor& out = c.tensor("out", Kind::kBf16);
     const at::Tensor& q = c.tensor("q", Kind::kBf16);
     const Scaled p = scaled_pools(c);
@@ -437,14 +437,13 @@ PyObject* paged_attention_fp8_scaled(PyObject*, PyObject* const* args, Py_ssize_
     if (q.dim() != 4 || q.size(0) != seqs || q.size(1) != q_len || q.size(3) != kHeadDim || out.sizes() != q.sizes())
       raise(PyExc_ValueError, "q and out must be [num_seqs][q_len][num_q_heads][128]");
     const float scale = c.f32();
-    const int32_t split = c.i32("kv_blocks_per_split");
     void* ws;
     size_t ws_bytes;
     c.workspace(&ws, &ws_bytes);
     return pkv_paged_attention_fp8_scaled(out.data_ptr(), q.data_ptr(), p.k->data_ptr(), p.v->data_ptr(),
                                           f32_ptr(p.ks), f32_ptr(p.vs), &p.desc, i32_ptr(&tables),
                                           size32(tables, 1, "block_tables"), i32_ptr(&lens), seqs, q_len,
-                                          size32(q, 2, "q"), scale, split, ws, ws_bytes, c.stream());
+                                          size32(q, 2, "q"), scale, ws, ws_bytes, c.stream());
   });
 }
 

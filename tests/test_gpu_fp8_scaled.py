@@ -288,12 +288,12 @@ def reference(q, kc, vc, ks, vs, t, ctx, scale=SCALE):
 
 
 def check(out, ref, ctx, rel=5e-3):
-    """Queries: two E4M3 parts (or FP16), off by at most 2^-17 of the head's largest value; FP32 sums of 128 products.
-    Weights: two E4M3 parts, 2^-8 relative (FP16: 2^-11), down to 2^-16 of the largest weight with its scale.  The
-    result: BF16, 2^-8 relative."""
+    """Queries: two E4M3 parts, off by at most 2^-17 of the head's largest value; FP32 sums of 128 products.  Weights:
+    two E4M3 parts, 2^-8 relative (chunks: by way of FP16, 2^-11 more), down to 2^-16 of the largest weight with its
+    scale.  The result: BF16, 2^-8 relative."""
     want, mass, floor, score = ref
     n = max(max(ctx), 1)
-    w_err = 2.0 ** -8 + 2.0 ** -20 + 2 * score + n * 2.0 ** -23
+    w_err = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20 + 2 * score + n * 2.0 ** -23
     tol = 2.0 ** -8 * want.abs() + 1.02 * (w_err[..., None] * mass + n * 2.0 ** -16 * floor[..., None]) + 1e-30
     err = (out.double() - want).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
@@ -318,13 +318,13 @@ def attention_case(ctx, q_len, hkv, seed=0, power=True, spread=6, extra=1):
     return q, kc, vc, ks, vs, t
 
 
-def run_attention(q, kc, vc, ks, vs, t, ctx, split=0, stream=None):
+def run_attention(q, kc, vc, ks, vs, t, ctx):
     pkv = _pkv()
     b, n, hq, _ = q.shape
     out = torch.full_like(q, 7.0)
-    ws = torch.full((max(pkv.workspace_size_fp8_scaled(b, n, hq, t.shape[1], split), 1),), 0xFF, dtype=torch.uint8,
+    ws = torch.full((max(pkv.workspace_size_fp8_scaled(b, n, hq, t.shape[1]), 1),), 0xFF, dtype=torch.uint8,
                     device="cuda")
-    pkv.paged_attention_fp8_scaled(out, q, kc, vc, ks, vs, dev(t), dev(ctx), n, SCALE, split, ws, stream)
+    pkv.paged_attention_fp8_scaled(out, q, kc, vc, ks, vs, dev(t), dev(ctx), n, SCALE, ws)
     return out
 
 
@@ -341,12 +341,15 @@ def test_attention(q_len, ctx, hkv):
 
 
 @pytest.mark.parametrize("q_len", [1, 5, 40])
-@pytest.mark.parametrize("split", [1, 3, 8, 16, 17, 64, 1000])
-def test_splits(q_len, split):
-    ctx = [1100, 40, 0, 513]
-    case = attention_case(ctx, q_len, 2)
-    out = run_attention(*case, ctx, split)
+@pytest.mark.parametrize("ctx", [[1100, 40, 0, 513], [9000], [20000, 3, 3, 3, 3, 3], [60] * 300, [1] * 500,
+                                 [129, 0, 0, 4000, 257, 0] * 9])
+def test_cuts(q_len, ctx):
+    """Work cut anywhere: within one long context over all CTAs, between short ones, several to a CTA."""
+    case = attention_case(ctx, q_len, 2, extra=7)
+    out = run_attention(*case, ctx)
+    assert _pkv().get_device_error() == 0
     check(out, reference(*case, ctx), ctx)
+    assert torch.equal(out, run_attention(*case, ctx))
 
 
 @pytest.mark.parametrize("q_len", [1, 4, 50])

@@ -61,21 +61,21 @@ def test_append(change, status):
     assert _call("pkv_kv_append_fp8_scaled", APPEND_ORDER, APPEND, **change) == status
 
 
-ATT_ORDER = ["out", "q", "kc", "vc", "ks", "vs", "desc", "bt", "maxb", "cl", "b", "n", "hq", "scale", "bps", "ws", "wsb",
+ATT_ORDER = ["out", "q", "kc", "vc", "ks", "vs", "desc", "bt", "maxb", "cl", "b", "n", "hq", "scale", "ws", "wsb",
              "stream"]
-ATT = dict(out=P, q=P, kc=P, vc=P, ks=P, vs=P, desc=_desc(), bt=P, maxb=64, cl=P, b=2, n=1, hq=32, scale=0.1, bps=4,
+ATT = dict(out=P, q=P, kc=P, vc=P, ks=P, vs=P, desc=_desc(), bt=P, maxb=4096, cl=P, b=2, n=1, hq=32, scale=0.1,
            ws=None, wsb=0, stream=None)
 
 
 @pytest.mark.parametrize("n", [1, 9, 100])
 @pytest.mark.parametrize("change,status", [
     (dict(desc=None), 1), (dict(desc=_desc(head_dim=64)), 3), (dict(hq=16), 3), (dict(n=0), 2), (dict(b=-1), 2),
-    (dict(maxb=0), 2), (dict(maxb=1 << 27), 3), (dict(bps=-1), 2), (dict(scale=0.0), 2), (dict(scale=-0.1), 2),
+    (dict(maxb=0), 2), (dict(maxb=1 << 27), 3), (dict(scale=0.0), 2), (dict(scale=-0.1), 2),
     (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(out=None), 1), (dict(q=None), 1),
     (dict(kc=None), 1), (dict(vc=None), 1), (dict(ks=None), 1), (dict(vs=None), 1), (dict(bt=None), 1),
     (dict(cl=None), 1), (dict(q=off(8)), 3), (dict(out=off(4)), 3), (dict(ks=off(2)), 3), (dict(b=1 << 28), 3),
     (dict(desc=_desc(num_blocks=0)), 2), (dict(desc=_desc(num_blocks=1 << 30)), 3),
-    (dict(), 4), (dict(ws=P, wsb=100), 4), (dict(ws=off(16), wsb=1 << 40), 4), (dict(b=0), 0),
+    (dict(b=2), 4), (dict(ws=P, wsb=100), 4), (dict(ws=off(16), wsb=1 << 40), 4), (dict(b=0), 0),
 ])
 def test_attention(change, status, n):
     assert _call("pkv_paged_attention_fp8_scaled", ATT_ORDER, ATT, **{"n": n, **change}) == status
@@ -96,19 +96,18 @@ def test_copy_blocks(change, status):
 
 @pytest.mark.parametrize("b,n,heads,maxb", [(1, 1, 32, 520), (64, 1, 32, 1001), (128, 1, 32, 530), (37, 7, 32, 150),
                                             (4, 2000, 32, 500), (1, 300, 4, 4000), (1, 1, 4, 1)])
-def test_workspace_follows_the_split(b, n, heads, maxb):
-    bps = pkv.choose_kv_blocks_per_split_fp8_scaled(b, heads // 4, n, maxb)
-    assert bps >= 1
-    assert pkv.workspace_size_fp8_scaled(b, n, heads, maxb) == pkv.workspace_size_fp8_scaled(b, n, heads, maxb, bps)
-    assert pkv.workspace_size_fp8_scaled(b, n, heads, maxb, maxb) == 0
+def test_workspace_is_bounded(b, n, heads, maxb):
+    """Two partials of a CTA's rows and their bookkeeping at most, or the splits of single tokens."""
+    size = pkv.workspace_size_fp8_scaled(b, n, heads, maxb)
+    assert size % 256 == 0
+    assert size <= (152 * 2 * 256 * 520 + 152 * 40 + 768 if n > 1 else b * heads * 64 * 520 + 512)
 
 
 def test_sizes_of_nothing():
     assert pkv.workspace_size_fp8_scaled(0, 1, 32, 10) == 0
     assert pkv.workspace_size_fp8_scaled(1, 0, 32, 10) == 0
     assert pkv.workspace_size_fp8_scaled(1, 1, 32, 0) == 0
-    assert pkv.workspace_size_fp8_scaled(1, 1, 32, 10, -1) == 0
-    assert pkv.choose_kv_blocks_per_split_fp8_scaled(0, 0, 0, 0) >= 1
+    assert pkv.workspace_size_fp8_scaled(1, 1, 32, -1) == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="needs tensors that are not on the current device")
