@@ -25,10 +25,13 @@
 // kWide : 256 rows (64 positions x 4 heads) share a CTA's tiles, 128 a row
 //         tile; while one row tile's softmax runs, the tensor cores work on
 //         the other's products.
-// !kWide: up to 128 rows; the two halves of the machine take the even and the
-//         odd tiles of keys and are joined at the end: HBM is the bound, and
-//         one chain of scores, softmax and product would be longer than a
-//         tile's transfer.
+// !kWide: up to kCols rows, 32, 64 or 128.  HBM is the bound, and a chain of
+//         scores, softmax and product is longer than a tile's transfer.  So
+//         the CTA's two halves take the even and the odd tiles of keys, and
+//         the query rows are laid out 128 / kCols times: a copy's threads do
+//         the softmax of kCols of a tile's 128 keys, with a maximum and a sum
+//         of their own (the other keys' weights are zeros).  At the end all
+//         copies and both halves are joined through shared memory.
 //
 // Work is cut by tiles, not by requests: all (request, row tile, KV head) jobs
 // in a row are divided evenly among the CTAs, one per SM, whatever the
@@ -64,14 +67,12 @@ constexpr int kCfThreads = 384;
 constexpr int kCfRows = 128;
 constexpr int kCfPos = kCfRows / kGroup;              // positions of a row tile
 constexpr int kCfOffQ = 0;                            // [row tile][high, low parts]; !kWide: one, then the join's buffer
-constexpr int kCfOffJoin = 2 * kCfTileBytes;          // FP32 [128][64]
+constexpr int kCfOffJoin = 2 * kCfTileBytes;          // FP32 [2 x 128][32]
 constexpr int kCfOffRing = 4 * kCfTileBytes;
 constexpr int kCfOffScale = kCfOffRing + kCfSlots * kCfTileBytes;
 constexpr int kCfScaleFloats = 3 * kCfTileBlocks;     // ks, log2 vs, 1 / vs
-// FP32 [2][128]: scale / sigma of the rows; !kWide: of one row tile, then the other half's sums
-constexpr int kCfOffSigma = kCfOffScale + kCfScaleSlots * kCfScaleFloats * 4;
-constexpr int kCfOffMax = kCfOffSigma + 2 * kCfRows * 4;  // !kWide: FP32 [128], the other half's maxima
-constexpr int kCfOffBar = kCfOffMax + kCfRows * 4;
+constexpr int kCfOffSigma = kCfOffScale + kCfScaleSlots * kCfScaleFloats * 4;  // FP32 [2][128]: scale / sigma
+constexpr int kCfOffBar = kCfOffSigma + 2 * kCfRows * 4;
 constexpr int kCfSmem = kCfOffBar + 528;
 static_assert(kCfSmem <= 227 * 1024, "one CTA per SM");
 static_assert(kCfOffBar % 16 == 0 && kCfOffScale % 16 == 0, "alignment");
@@ -81,7 +82,12 @@ constexpr int kCfSoftmaxRegs = 208;
 constexpr int kCfIssueRegs = 80;
 static_assert((2 * kCfSoftmaxRegs + kCfIssueRegs) * 128 <= 168 * kCfThreads, "register split");
 constexpr float kCfLag = 2.f;     // base 2: weights stay at or below 2^2, 2^8 with the factor below
-constexpr float kCfFactor = 6.f;  // weights enter times 2^6 (E4M3 reaches 448)
+// Weights enter times 2^6 (E4M3 reaches 448).  They are held in FP16 times
+// 2^-8 of that: FP16's exponent field then is E4M3's, subnormals included, and
+// the parts come by masks and shifts (E4M3 conversions run at an eighth of
+// their rate: five to a pair of weights took 5100 cycles a tile).
+constexpr float kCfFactor = -2.f;
+constexpr float kCfCodeUnit = 256.f;
 // A CTA's share is at least this many tiles: a shorter one would not pay for its joining.
 constexpr int kCfMinTiles = 2;
 
@@ -96,8 +102,8 @@ struct CfBars {
   uint64_t full[kCfSlots], empty[kCfSlots];
   uint64_t sc_full[kCfScaleSlots], sc_empty[kCfScaleSlots];
   uint64_t q_full[2];
-  uint64_t q_empty;            // !kWide: the other half is done with the queries
-  uint64_t join_full, join_free;
+  uint64_t q_empty;               // !kWide: the other half is done with the queries
+  uint64_t join_full, join_free;  // !kWide: the join's buffer is written, is read
   uint64_t s_full[2];
   uint64_t p_full[2][2];
   uint64_t o_done[2];
@@ -140,6 +146,18 @@ __device__ __forceinline__ void cf_parts(float x0, float x1, uint32_t& hi, uint3
   lo = b;
 }
 
+// 4 weights (0 .. 1) as the bytes of their high parts, cut to 4 significant
+// bits, and of what that leaves, rounded to 4.
+__device__ __forceinline__ void cf_weights(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
+  uint32_t h0, h1, r0, r1;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h0) : "f"(p1), "f"(p0));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h1) : "f"(p3), "f"(p2));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(h0), "r"(h0 & 0xff80ff80u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(h1), "r"(h1 & 0xff80ff80u));
+  hi = __byte_perm(h0 << 1, h1 << 1, 0x7531);
+  lo = __byte_perm(r0 * 2 + 0x00800080u, r1 * 2 + 0x00800080u, 0x7531);
+}
+
 // The power of two that brings a row's largest |q| (BF16 bits) into [2^7, 2^8); 1 for zeros.
 __device__ __forceinline__ float cf_sigma(uint32_t amax_bits) {
   if (amax_bits == 0) return 1.f;
@@ -156,7 +174,7 @@ __device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int64_t pair, 
   return end > 0 ? (end + kCfTokens - 1) / kCfTokens : 0;
 }
 
-template <bool kWide>
+template <bool kWide, int kCols>
 __global__ void __launch_bounds__(kCfThreads, 1)
     paged_chunk_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                               const ChunkScaledArgs a) {
@@ -176,8 +194,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       mbar_init(&bars->sc_empty[s], kWide ? 8 : 4);
     }
     mbar_init(&bars->q_empty, 5);  // warps 4-7, the second MMA issuer
-    mbar_init(&bars->join_full, 128);
-    mbar_init(&bars->join_free, 128);
+    mbar_init(&bars->join_full, 256);
+    mbar_init(&bars->join_free, 256);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 128);
       mbar_init(&bars->s_full[t], 1);
@@ -503,21 +521,25 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       for (int64_t i = threadIdx.x; i < chunks; i += 256) o[i] = make_uint4(0, 0, 0, 0);
     }
 
+    // !kWide: this warp's copy of the query rows, and the keys of a tile that are its
+    const int copy = quad * 32 / kCols;
+    const int key0 = copy * kCols;
+    const int qrow = row & (kCols - 1);            // query row
+    const int warp_row = quad * 32 & (kCols - 1);  // its warp's first
     uint32_t g = 0;      // tiles of this half so far
     uint32_t tile0 = 0;  // tiles of the pieces so far
     uint32_t pieces = 0;
-    uint32_t joins = 0;
+    uint32_t passes = 0;  // of the join's buffer
     CfPiece u;
     while (next_piece(u)) {
       const int n_t = tiles_of(u, t);
       const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
       const int pos0 = u.rt * kPos + row_tile * kCfPos;  // first query of the row tile
       const int live_rows = (min(pos0 + kCfPos, a.q_len) - pos0) * kGroup;
-      const bool warp_live = quad * 32 < live_rows;
-      const bool valid = row < live_rows;
-      const int qi = pos0 + (row >> 2);
-      const int seen = ctx - a.q_len + qi + 1;  // keys that this row sees (<= 0: none)
-      const int warp_seen = ctx - a.q_len + pos0 + quad * 8 + 1;  // its warp's first row
+      const bool warp_live = warp_row < live_rows;
+      const int first_key = ctx - a.q_len + pos0 + 1;    // keys that query 0 of the row tile sees
+      const int seen = first_key + (qrow >> 2);          // that this row sees (<= 0: none)
+      const int warp_seen = first_key + (warp_row >> 2);  // its warp's first row
       // ---- the query operand: 8 lanes a row, 16 dims each ----
       if (kWide || t == 0) {
         uint8_t* qa = smem + kCfOffQ + row_tile * 2 * kCfTileBytes;
@@ -532,7 +554,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           uint4 w[4][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int m = quad * 32 + 4 * (i0 + i) + (lane >> 3);
+            const int m = warp_row + 4 * (i0 + i) + (lane >> 3);
             w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
             if (m < live_rows) {
               const uint4* src = reinterpret_cast<const uint4*>(
@@ -581,7 +603,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         if (lane == 0) mbar_arrive(&bars->q_empty);
       }
       float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum by at most 2)
-      float l = 0.f;        // sum of w / vs, times 2^6
+      float l = 0.f;        // sum of w / vs, times 2^-2
       for (int j = 0; j < n_t; ++j, ++g) {
         const int in_piece = kWide ? j : 2 * j + t;
         const int tok = (u.begin + in_piece) * kCfTokens;
@@ -591,25 +613,37 @@ __global__ void __launch_bounds__(kCfThreads, 1)
                         mbar_wait(&bars->sc_full[sl], ((tile0 + in_piece) / kCfScaleSlots) & 1) &&
                             mbar_wait(&bars->s_full[t], g & 1));
         if (!ok) break;
-        // the tile's 8 blocks: ks, log2 vs, 1 / vs (read twice: registers are dearer)
-        const float* sc = reinterpret_cast<const float*>(smem + kCfOffScale) + sl * kCfScaleFloats;
+        // the blocks' ks, log2 vs, 1 / vs (read twice: registers are dearer)
+        const float* sc = reinterpret_cast<const float*>(smem + kCfOffScale) + sl * kCfScaleFloats + key0 / kBlockSize;
         tc::fence_after_sync();
         if (warp_live) {
-          float s[128];
-          tc::tmem_ld32(scol, s);
-          tc::tmem_ld32(scol + 32, s + 32);
-          tc::tmem_ld32(scol + 64, s + 64);
-          tc::tmem_ld32(scol + 96, s + 96);
-          tc::tmem_wait_ld();
-          if (warp_seen - tok < kCfTokens) {  // some row of the warp sees the tile in part
-            const int lim = seen - tok;
+          float s[kCols];
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
+          for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(scol + key0 + e, s + e);
+          tc::tmem_wait_ld();
+          if constexpr (kCols < 128) {  // the other copies' keys: weights of zero
+            const uint32_t zeros[16] = {};
+#pragma unroll
+            for (int o = 1; o < 128 / kCols; ++o) {
+              const uint32_t col = scol + (copy ^ o) * (kCols / 4);
+              if constexpr (kCols == 64) {
+                tc::tmem_st16u(col, zeros);
+                tc::tmem_st16u(col + 32, zeros);
+              } else {
+                tc::tmem_st8(col, zeros);
+                tc::tmem_st8(col + 32, zeros);
+              }
+            }
+          }
+          if (warp_seen - tok - key0 < kCols) {  // some row of the warp sees its keys in part
+            const int lim = seen - tok - key0;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e)
               if (e >= lim) s[e] = -INFINITY;
           }
           float mx = -INFINITY;
 #pragma unroll
-          for (int b = 0; b < 8; ++b) {
+          for (int b = 0; b < kCols / kBlockSize; ++b) {
             float x = fmaxf(s[16 * b], s[16 * b + 1]);
 #pragma unroll
             for (int e = 2; e < 16; e += 2) x = fmaxf(fmaxf(x, s[16 * b + e]), s[16 * b + e + 1]);
@@ -636,12 +670,13 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           l *= alpha;
           m = m_new;
           const float nm = (m == -INFINITY ? 0.f : -m) + kCfFactor;
+          constexpr int kChunk = kCols < 64 ? kCols : 64;  // keys whose weights are stored together
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 64 keys
-            uint32_t hi[16], lo[16];
+          for (int h = 0; h < kCols / kChunk; ++h) {
+            uint32_t hi[kChunk / 4], lo[kChunk / 4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int blk = 4 * h + b;
+            for (int b = 0; b < kChunk / kBlockSize; ++b) {
+              const int blk = kChunk / kBlockSize * h + b;
               const float kc = sc[blk] * c, off = sc[kCfTileBlocks + blk] + nm;
               const float2 k2 = make_float2(kc, kc);
               const float2 n2 = make_float2(off, off);
@@ -655,23 +690,25 @@ __global__ void __launch_bounds__(kCfThreads, 1)
                 const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
                 acc = __fadd2_rn(acc, make_float2(p0, p1));
                 acc = __fadd2_rn(acc, make_float2(p2, p3));
-                uint32_t h0, l0, h1, l1;
-                cf_parts(p0, p1, h0, l0);
-                cf_parts(p2, p3, h1, l1);
-                hi[4 * b + e] = h0 | (h1 << 16);
-                lo[4 * b + e] = l0 | (l1 << 16);
+                cf_weights(p0, p1, p2, p3, hi[4 * b + e], lo[4 * b + e]);
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + blk], l);
             }
             // the weights overwrite the scores: high parts at columns 0-31, low parts at 32-63
-            tc::tmem_st16u(scol + 16 * h, hi);
-            tc::tmem_st16u(scol + 32 + 16 * h, lo);
+            const uint32_t col = scol + copy * (kCols / 4) + 16 * h;
+            if constexpr (kChunk == 64) {
+              tc::tmem_st16u(col, hi);
+              tc::tmem_st16u(col + 32, lo);
+            } else {
+              tc::tmem_st8(col, hi);
+              tc::tmem_st8(col + 32, lo);
+            }
             if (h == 0 && ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
               // slots past the context may hold any code: V's rows there are
               // zeroed (a weight of zero is not enough)
               const uint32_t vp = 2 * (tile0 + in_piece) + 1;
               ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kCfSlots], (vp / kCfSlots) & 1));
-              const int z0 = max(ctx - tok, 0), z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
+              const int z0 = ctx - tok, z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
               uint8_t* vt = smem + kCfOffRing + (vp % kCfSlots) * kCfTileBytes;
               for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) reinterpret_cast<uint4*>(vt)[i] = make_uint4(0, 0, 0, 0);
               tc::fence_proxy_async_smem();
@@ -680,6 +717,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             tc::fence_before_sync();
             mbar_arrive(&bars->p_full[t][h]);
           }
+          if constexpr (kCols < 128) mbar_arrive(&bars->p_full[t][1]);
         } else {
           mbar_arrive(&bars->p_full[t][0]);
           mbar_arrive(&bars->p_full[t][1]);
@@ -689,6 +727,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       }
       tile0 += u.take;
       if (!ok) break;
+      l *= kCfCodeUnit;  // in O's unit
       // ---- results ----
       if (n_t > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t], (g - 1) & 1));
@@ -696,102 +735,125 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         tc::fence_after_sync();
       }
       const bool whole = u.take == u.n;
-      const int64_t out_row = (static_cast<int64_t>(u.r) * a.q_len + qi) * hq + u.kvh * kGroup + (row & 3);
-      const int64_t part_row = static_cast<int64_t>(2 * blockIdx.x + (u.begin == 0 ? 1 : 0)) * a.rows_slot +
-                               row_tile * kCfRows + row;
-      // !kWide: the odd tiles' half hands its sums over, 64 dims at a time
-      const bool join = !kWide && u.take > 1;
-      float4* jbuf = reinterpret_cast<float4*>(smem + kCfOffJoin) + row * 16;  // 16-byte chunk ch at ch ^ (row % 8)
-      float* join_m = reinterpret_cast<float*>(smem + kCfOffMax) + row;
-      float* join_l = reinterpret_cast<float*>(smem + kCfOffSigma) + kCfRows + row;
-      if (!kWide && t == 1) {
-        if (!join) continue;
+      const int64_t out_row0 = (static_cast<int64_t>(u.r) * a.q_len + pos0) * hq + u.kvh * kGroup;  // of query row 0
+      const int64_t part_row0 =
+          static_cast<int64_t>(2 * blockIdx.x + (u.begin == 0 ? 1 : 0)) * a.rows_slot + row_tile * kCfRows;
+      if constexpr (kWide) {
+        if (!warp_live) continue;
+        const bool valid = qrow < live_rows;
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN sum stays one)
+        const int64_t out_row = out_row0 + static_cast<int64_t>(qrow >> 2) * hq + (qrow & 3);
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          if (pass == 1) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_free, joins & 1));
-            if (!ok) break;
-          }
-          if (warp_live) {
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tc::tmem_ld32(scol + kCfColO + 32 * cc, o);
+          tc::tmem_wait_ld();
+          if (valid && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim + 32 * cc);
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              float o[32];
-              tc::tmem_ld32(scol + kCfColO + 64 * pass + 32 * cc, o);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                jbuf[(8 * cc + e) ^ (row & 7)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (l != 0.f)
+                w = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                               pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                               pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                               pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+              dst[e] = w;
             }
-            if (pass == 0) {
-              *join_m = m;
-              *join_l = l;
-            }
+          } else if (valid) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (part_row0 + qrow) * kHeadDim + 32 * cc);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
+        }
+        if (valid && !whole) a.part_ml[part_row0 + qrow] = l != 0.f ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      } else {
+        // Join the two halves' copies: maxima and sums first, then 32 dims a
+        // pass.  A thread joins 4 dims of up to kTake rows.
+        constexpr int kParts = 2 * 128 / kCols;  // partials of a row
+        constexpr int kTake = kCols / 32;
+        float4* buf = reinterpret_cast<float4*>(smem + kCfOffJoin);
+        const int who = t * kCfRows + row;
+        auto written = [&]() -> bool {  // everyone's part of a pass is there
           mbar_arrive(&bars->join_full);
-        }
-        ++joins;
-        tc::fence_before_sync();
-        if (!ok) break;
-        continue;
-      }
-      float a0 = 1.f, a1 = 0.f;  // factors of this half's and the other half's sums
-      if (join) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_full, 0));
-        if (!ok) break;
-        const float om = *join_m, ol = *join_l;
-        const float mm = fmaxf(m, om);
-        a0 = m == -INFINITY ? 0.f : exp2_approx(m - mm);
-        a1 = om == -INFINITY ? 0.f : exp2_approx(om - mm);
-        l = l * a0 + ol * a1;
-        m = mm;
-      }
-      const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN sum stays one)
-#pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        if (join && pass == 1) {
+          return __all_sync(0xffffffffu, mbar_wait(&bars->join_full, passes & 1));
+        };
+        auto may_write = [&]() -> bool {  // everyone has read the pass before
+          return passes == 0 || __all_sync(0xffffffffu, mbar_wait(&bars->join_free, (passes & 1) ^ 1));
+        };
+        auto read = [&]() {
           mbar_arrive(&bars->join_free);
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_full, 1));
-          if (!ok) break;
+          ++passes;
+        };
+        ok = may_write();
+        if (!ok) break;
+        reinterpret_cast<float2*>(buf)[who] = make_float2(m, l);
+        ok = written();
+        if (!ok) break;
+        float f[kTake][kParts];
+        const int ch = threadIdx.x & 7;
+#pragma unroll
+        for (int k = 0; k < kTake; ++k) {
+          const int rr = (threadIdx.x >> 3) + 32 * k;
+          float2 ml[kParts];
+          float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) {
+            ml[q] = reinterpret_cast<const float2*>(buf)[q * kCols + rr];
+            mm = fmaxf(mm, ml[q].x);
+          }
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) {
+            f[k][q] = ml[q].y == 0.f ? 0.f : exp2_approx(ml[q].x - mm);  // (0: it saw nothing)
+            sum = fmaf(ml[q].y, f[k][q], sum);
+          }
+          if (!whole && ch == 0 && rr < live_rows)
+            a.part_ml[part_row0 + rr] = sum != 0.f ? make_float2(mm, sum) : make_float2(-INFINITY, 0.f);
+          const float inv = whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) f[k][q] *= inv;
         }
-        if (warp_live) {
+        read();
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
+        for (int cc = 0; cc < 4; ++cc) {
+          ok = may_write();
+          if (!ok) break;
+          if (warp_live && n_t > 0) {
             float o[32];
-            tc::tmem_ld32(scol + kCfColO + 64 * pass + 32 * cc, o);
+            tc::tmem_ld32(scol + kCfColO + 32 * cc, o);
             tc::tmem_wait_ld();
-            if (join) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 x = jbuf[(8 * cc + e) ^ (row & 7)];
-                o[4 * e] = a0 * o[4 * e] + a1 * x.x;
-                o[4 * e + 1] = a0 * o[4 * e + 1] + a1 * x.y;
-                o[4 * e + 2] = a0 * o[4 * e + 2] + a1 * x.z;
-                o[4 * e + 3] = a0 * o[4 * e + 3] + a1 * x.w;
-              }
+            for (int e = 0; e < 8; ++e)
+              buf[who * 8 + (e ^ (row & 7))] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          ok = written();
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < kTake; ++k) {
+            const int rr = (threadIdx.x >> 3) + 32 * k;
+            if (rr >= live_rows) continue;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) {
+              if (f[k][q] == 0.f) continue;  // nothing was written for it, or it adds nothing
+              const float4 x = buf[(q * kCols + rr) * 8 + (ch ^ (rr & 7))];
+              o.x = fmaf(x.x, f[k][q], o.x);
+              o.y = fmaf(x.y, f[k][q], o.y);
+              o.z = fmaf(x.z, f[k][q], o.z);
+              o.w = fmaf(x.w, f[k][q], o.w);
             }
-            if (valid && whole) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim + 64 * pass + 32 * cc);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (l != 0.f)
-                  w = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                 pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                 pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                 pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                dst[e] = w;
-              }
-            } else if (valid) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 64 * pass + 32 * cc);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            if (whole) {
+              const int64_t out_row = out_row0 + static_cast<int64_t>(rr >> 2) * hq + (rr & 3);
+              reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim + 32 * cc)[ch] =
+                  make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+            } else {
+              reinterpret_cast<float4*>(a.part_o + (part_row0 + rr) * kHeadDim + 32 * cc)[ch] = o;
             }
           }
+          read();
         }
+        if (!ok) break;
       }
-      if (join) ++joins;
-      if (!ok) break;
-      if (valid && !whole) a.part_ml[part_row] = l != 0.f ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
       tc::fence_before_sync();  // O is read before the next piece's weights arrive
     }
     if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
@@ -849,31 +911,24 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a
   }
 }
 
-template <bool kWide>
-cudaError_t allow_smem_cf() {
+template <bool kWide, int kCols>
+cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
   static std::atomic<bool> done[64];  // per device; host threads may race on a first call
+  auto kernel = paged_chunk_fp8_tc_kernel<kWide, kCols>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(paged_chunk_fp8_tc_kernel<kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfSmem);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
-  return cudaSuccess;
-}
-
-template <bool kWide>
-cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.num_kv_heads * kBlockSize;
   CUtensorMap kmap, vmap;
   if (!make_pool_map_e4m3(&kmap, a.k_cache, rows) || !make_pool_map_e4m3(&vmap, a.v_cache, rows))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem_cf<kWide>();
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_chunk_fp8_tc_kernel<kWide>, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), kCfSmem, stream,
-                 1, kmap, vmap, a);
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), kCfSmem, stream, 1, kmap, vmap, a);
   if (e != cudaSuccess || grid == 1) return e;
   // 8 rows a block at a time; a job of few rows is joined by one block
   const int32_t pos = kWide ? 2 * kCfPos : kCfPos;
@@ -895,7 +950,10 @@ int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
 int32_t chunk_scaled_rows(int32_t q_len) { return cf_wide(q_len) ? 2 * kCfRows : kGroup * q_len; }
 
 cudaError_t launch_paged_chunk_fp8_tc(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
-  return cf_wide(a.q_len) ? launch_cf<true>(a, grid, stream) : launch_cf<false>(a, grid, stream);
+  if (cf_wide(a.q_len)) return launch_cf<true, 128>(a, grid, stream);
+  const int32_t rows = kGroup * a.q_len;
+  if (rows <= 32) return launch_cf<false, 32>(a, grid, stream);
+  return rows <= 64 ? launch_cf<false, 64>(a, grid, stream) : launch_cf<false, 128>(a, grid, stream);
 }
 
 }  // namespace pkv

@@ -12,6 +12,9 @@
 #include <cuda_runtime.h>
 #include <initializer_list>
 
+#ifndef PKV_X
+#define PKV_X 0
+#endif
 #include "pkv.h"
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
@@ -1239,7 +1242,7 @@ struct ScaledPlan {
 ScaledPlan scaled_plan(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads, int32_t max_blocks) {
   ScaledPlan p;
   const int sms = device_sm_count();
-  if (q_len == 1) {
+  if (q_len == 1 && !PKV_X) {
     const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
     p.bps = std::min(persistent_blocks_per_split(rows, max_blocks, sms, 16), max_blocks);
     p.splits = (max_blocks + p.bps - 1) / p.bps;
@@ -1377,7 +1380,7 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
     return PKV_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q_len > 1) {
+  if (q_len > 1 || PKV_X) {
     ChunkScaledArgs a{};
     a.out = out;
     a.q = q;

@@ -6,9 +6,16 @@
 // before they are stored in the cache.
 //
 // Mathematics: O_i = sum_{j <= i} w_ij V_j / sum_{j <= i} w_ij, w_ij =
-// exp(scale q_i.k_j - m_i), evaluated over tiles of 128 keys with a running
+// exp(scale q_i.k_j - m_i), evaluated over tiles of 64 keys with a running
 // maximum and sum (FP32); S = Q K^T and O = P V with FP32 accumulators in
 // tensor memory.
+//
+// Tiles are 64 keys because two buffers of scores, then O, fill the 256
+// columns of a row tile: S runs two tiles ahead of the P.V that is under way,
+// so that the softmax always has scores to go on with.  (With 128 keys and one
+// buffer S, softmax and P.V of a row tile are one chain: 3750 cycles per 128
+// keys and pair of row tiles, where the products need 2048, or 2560 with the
+// 64-key tiles, whose S re-reads its 128-row operand twice as often.)
 //
 // A unit of work is (prompt, KV head, 256 rows): rows are query positions x
 // the query heads of the KV head, so that a short prompt still fills them and
@@ -22,7 +29,7 @@
 // CTA = 12 warps:
 //   warps 0-7: softmax, one thread per row (TMEM lane), one warpgroup for each
 //             of the two row tiles.
-//   warp 8  : TMA producer of Q, and of K and V into one ring of 32 KiB stages.
+//   warp 8  : TMA producer of Q, and of K and V into one ring of 16 KiB stages.
 //   warps 9, 10: MMA issuers, one per row tile: while one tile's softmax runs,
 //             the tensor cores work on the other's products.
 //   warp 11 : finds the CTA's units, one ahead of the others.
@@ -38,16 +45,18 @@ namespace pkv {
 namespace {
 
 constexpr int kPaRows = 128;                           // rows of a row tile: TMEM lanes
-constexpr int kPaTokens = 128;                         // keys of a tile
-constexpr int kPaHalfBytes = kPaTokens * 128;          // 64 dims of a tile of K, V or Q: 16 KiB
-constexpr int kPaTileBytes = 2 * kPaHalfBytes;         // 32 KiB
-constexpr int kPaStages = 5;                           // ring of K and V tiles, in turn
+constexpr int kPaTokens = 64;                          // keys of a tile
+constexpr int kPaHalfBytes = kPaTokens * 128;          // 64 dims of a tile of K or V: 8 KiB
+constexpr int kPaTileBytes = 2 * kPaHalfBytes;         // 16 KiB
+constexpr int kPaQHalfBytes = kPaRows * 128;
+constexpr int kPaQBytes = 2 * kPaQHalfBytes;           // a row tile of Q: 32 KiB
+constexpr int kPaStages = 10;                          // ring of K and V tiles, in turn
 constexpr int kPaThreads = 384;
 constexpr int kPaOffQ = 0;                             // 2 row tiles
-constexpr int kPaOffRing = 2 * kPaTileBytes;
+constexpr int kPaOffRing = 2 * kPaQBytes;
 constexpr int kPaOffBar = kPaOffRing + kPaStages * kPaTileBytes;
 constexpr int kPaSmem = kPaOffBar + 512;
-constexpr uint32_t kPaTileCols = 256;                  // per row tile: S (P over it), then O
+constexpr uint32_t kPaTileCols = 256;                  // per row tile: two buffers of S (P over it), then O
 constexpr uint32_t kPaColO = 128;
 // Registers per thread: the launch's 168 x 384, moved from the issuing
 // warpgroup to the two softmax warpgroups, which hold a tile's scores.
@@ -71,9 +80,9 @@ struct PaBars {
   uint64_t full[kPaStages];
   uint64_t empty[kPaStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2];
-  uint64_t p_full[2][2];  // first and second 64 keys
-  uint64_t o_done[2];
+  uint64_t s_full[2][2];  // row tile, buffer
+  uint64_t p_full[2][2];
+  uint64_t o_done[2][2];
   uint64_t u_full[2], u_empty[2];
   PaUnit unit[2];
   uint32_t tmem_base;
@@ -132,10 +141,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
-      mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t][0], 128);
-      mbar_init(&bars->p_full[t][1], 128);
-      mbar_init(&bars->o_done[t], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[t][b], 1);
+        mbar_init(&bars->p_full[t][b], 128);
+        mbar_init(&bars->o_done[t][b], 1);
+      }
       mbar_init(&bars->u_full[t], 1);
       mbar_init(&bars->u_empty[t], 11);  // every other warp
     }
@@ -282,11 +292,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int t = 0; t < 2 && ok; ++t) {
             if (units > 0) ok = mbar_wait(&bars->q_empty[t], (units & 1) ^ 1);
             if (!ok) break;
-            uint8_t* dst = smem + kPaOffQ + t * kPaTileBytes;
+            uint8_t* dst = smem + kPaOffQ + t * kPaQBytes;
             const int tok = u.tok0 + u.pos0 + t * per_tile;  // (past the last token: zeros)
             mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
             tma_load_3d(dst, &q_map, 0, u.kvh * a.group, tok, &bars->q_full[t], once);
-            tma_load_3d(dst + kPaHalfBytes, &q_map, 64, u.kvh * a.group, tok, &bars->q_full[t], once);
+            tma_load_3d(dst + kPaQHalfBytes, &q_map, 64, u.kvh * a.group, tok, &bars->q_full[t], once);
           }
           if (ok) ring(&v_map, u.tok0, u.kvh);
           for (int j = 1; j < n && ok; ++j) {
@@ -314,45 +324,63 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int t = warp - 9;
       const bool leader = lane == 0;
       const uint32_t scol = tmem + t * kPaTileCols;
-      const uint64_t q_desc = tc::smem_desc(sbase + kPaOffQ + t * kPaTileBytes, 16, 1024);
+      const uint64_t q_desc = tc::smem_desc(sbase + kPaOffQ + t * kPaQBytes, 16, 1024);
       const uint64_t k_desc = tc::smem_desc(sbase + kPaOffRing, 16, 1024);
       const uint64_t v_desc = tc::smem_desc(sbase + kPaOffRing, kPaHalfBytes, 1024);
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
-      uint32_t c = 0;  // ring place of the present tile's K; its V is at c + 1
-      auto wait_full = [&](uint32_t place) -> bool {
-        return wait(&bars->full[place % kPaStages], (place / kPaStages) & 1);
+      // both barriers tried before either result is looked at
+      auto wait2 = [&](uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp) -> bool {
+        const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
+        return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
       };
-      auto give_back = [&](uint32_t place) {
-        if (leader) mbar_arrive(&bars->empty[place % kPaStages]);
-      };
-      auto issue_s = [&](uint32_t place) {
-        const uint64_t kd = k_desc + (place % kPaStages) * (kPaTileBytes >> 4);
+      // S of the K tile in stage st, into buffer buf
+      auto issue_s = [&](int buf, uint32_t st, bool last) {
+        const uint32_t d = scol + buf * kPaTokens;
+        const uint64_t kd = k_desc + st * (kPaTileBytes >> 4);
         tc::fence_after_sync();
         if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = ((kk >> 2) * kPaHalfBytes + 32 * (kk & 3)) >> 4;
-            tc::mma_bf16(scol, q_desc + off, kd + off, kIdS, kk > 0);
-          }
-          tc::commit(&bars->s_full[t]);
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_bf16(d, q_desc + (((kk >> 2) * kPaQHalfBytes + 32 * (kk & 3)) >> 4),
+                         kd + (((kk >> 2) * kPaHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
+          tc::commit(&bars->s_full[t][buf]);
+          if (last) tc::commit(&bars->q_empty[t]);  // the next unit's queries may come
         }
         __syncwarp();
       };
-      // O += P V of 64 keys
-      auto issue_pv = [&](uint32_t place, int half, bool first) {
-        const uint64_t vd = v_desc + (place % kPaStages) * (kPaTileBytes >> 4);
+      // O += P V, P in buffer buf, V in stage st
+      auto issue_pv = [&](int buf, uint32_t st, bool first) {
+        const uint32_t p = scol + buf * kPaTokens;
+        const uint64_t vd = v_desc + st * (kPaTileBytes >> 4);
         tc::fence_after_sync();
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::mma_bf16_tmem_a(scol + kPaColO, scol + 32 * half + 8 * kk, vd + (4 * half + kk) * (2048 >> 4), kIdO,
-                                (!first || kk > 0) ? 1u : 0u);
-          if (half == 1) tc::commit(&bars->o_done[t]);
+            tc::mma_bf16_tmem_a(scol + kPaColO, p + 8 * kk, vd + kk * (2048 >> 4), kIdO, (!first || kk > 0) ? 1u : 0u);
+          tc::commit(&bars->o_done[t][buf]);
         }
         __syncwarp();
       };
+      // A place in the ring: K tiles at even places, V tiles at odd ones.
+      struct Place {
+        uint32_t st = 0, ph = 0;
+        __device__ __forceinline__ void step(uint32_t n) {
+          st += n;
+          if (st >= kPaStages) {
+            st -= kPaStages;
+            ph ^= 1;
+          }
+        }
+      };
+      // Stages go back by plain arrivals once a later wait has shown that the
+      // products that read them are done.
+      auto give_back = [&](uint32_t st) {
+        if (leader) mbar_arrive(&bars->empty[st]);
+      };
+      Place k, pk, v;  // of the next S; of the K tile and the V tile of the next P.V
+      v.step(1);
       uint32_t g = 0;  // tiles of this row tile so far
       uint32_t units = 0;
       PaUnit u;
@@ -360,37 +388,45 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const int n_t = tiles_of(u, t);
         const int n = max(tiles_of(u, 0), tiles_of(u, 1));
         ok = wait(&bars->q_full[t], units & 1);
-        if (ok && n_t > 0) {
-          ok = wait_full(c);
-          if (ok) issue_s(c);
+        ++units;
+        for (int j = 0; j < 2 && j < n_t && ok; ++j) {
+          ok = wait(&bars->full[k.st], k.ph);
+          if (ok) issue_s((g + j) & 1, k.st, j == n_t - 1);
+          k.step(2);
         }
-        for (int j = 0; j < n_t && ok; ++j, ++g, c += 2) {
-          ok = wait_full(c + 1) && wait(&bars->p_full[t][0], g & 1);
-          if (ok) issue_pv(c + 1, 0, j == 0);
-          ok = ok && wait(&bars->p_full[t][1], g & 1);
+        for (int j = 0; j < n_t && ok; ++j, ++g) {
+          const int buf = g & 1, ph = (g >> 1) & 1;
+          ok = wait2(&bars->full[v.st], v.ph, &bars->p_full[t][buf], ph);
           if (!ok) break;
-          give_back(c);  // the weights were made from this tile's scores
-          issue_pv(c + 1, 1, false);
-          // The next scores go where the weights are, so after this product.
-          if (j + 1 < n_t) {
-            ok = wait_full(c + 2) && wait(&bars->o_done[t], g & 1);
+          give_back(pk.st);  // the weights were made from this tile's scores
+          issue_pv(buf, v.st, j == 0);
+          if (j + 2 < n_t) {  // into the buffer that this product reads, so after it
+            ok = wait2(&bars->full[k.st], k.ph, &bars->o_done[t][buf], ph);
             if (!ok) break;
-            give_back(c + 1);
-            issue_s(c + 2);
-          } else {
-            if (leader) mbar_arrive(&bars->q_empty[t]);
-            ok = wait(&bars->o_done[t], g & 1);
-            if (ok) give_back(c + 1);
+            give_back(v.st);
+            issue_s(buf, k.st, j + 2 == n_t - 1);
+            k.step(2);
           }
+          pk.step(2);
+          v.step(2);
+        }
+        // the last two tiles' V, once their products are done
+        for (int back = min(n_t, 2); back > 0 && ok; --back) {
+          const uint32_t gt = g - back;
+          const uint32_t st = v.st >= 2 * back ? v.st - 2 * back : v.st + kPaStages - 2 * back;
+          ok = wait(&bars->o_done[t][gt & 1], (gt >> 1) & 1);
+          if (ok) give_back(st);
         }
         if (n_t == 0 && ok && leader) mbar_arrive(&bars->q_empty[t]);
-        for (int j = n_t; j < n && ok; ++j, c += 2) {  // tiles that only the other row tile reads
-          ok = wait_full(c);
-          if (ok) give_back(c);
-          ok = ok && wait_full(c + 1);
-          if (ok) give_back(c + 1);
+        for (int j = n_t; j < n && ok; ++j) {  // tiles that only the other row tile reads
+          ok = wait(&bars->full[k.st], k.ph);
+          if (ok) give_back(k.st);
+          ok = ok && wait(&bars->full[v.st], v.ph);
+          if (ok) give_back(v.st);
+          k.step(2);
+          pk.step(2);
+          v.step(2);
         }
-        ++units;
         if (!ok) break;
       }
       if (!ok && leader) report(a.err, PKV_DEVERR_TIMEOUT);
@@ -421,32 +457,32 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       float m = -INFINITY;  // scaled max the weights are taken against (lags the true max by < 2^16)
       float l = 0.f;        // the sum of the weights
       for (int j = 0; j < n_t; ++j, ++g) {
+        const int buf = g & 1;
         const int tok = j * kPaTokens;
+        const uint32_t col = scol + buf * kPaTokens;
         // (`ok` stays warp-uniform: the loads below are warp-collective)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], g & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t][buf], (g >> 1) & 1));
         if (!ok) break;
         tc::fence_after_sync();
-        float s[128];  // raw scores
-        tc::tmem_ld32(scol, s);
-        tc::tmem_ld32(scol + 32, s + 32);
-        tc::tmem_ld32(scol + 64, s + 64);
-        tc::tmem_ld32(scol + 96, s + 96);
+        float s[64];  // raw scores
+        tc::tmem_ld32(col, s);
+        tc::tmem_ld32(col + 32, s + 32);
         tc::tmem_wait_ld();
         if (u.pos0 + t * per_tile + warp_pos + 1 - tok < kPaTokens) {  // some row of the warp sees the tile in part
           const int lim = pos + 1 - tok;
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
+          for (int e = 0; e < 64; ++e)
             if (e >= lim) s[e] = -INFINITY;
         }
         float mx;
         {
           float t8[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(s[e], s[e + 8]);
+          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(s[e], s[e + 8]), s[e + 16]);
 #pragma unroll
-          for (int k = 16; k < 128; k += 16)
+          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(t8[e], s[e + 24]), s[e + 32]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(t8[e], s[e + k]), s[e + k + 8]);
+          for (int e = 0; e < 8; ++e) t8[e] = fmaxf(fmaxf(t8[e], s[e + 40]), fmaxf(s[e + 48], s[e + 56]));
           mx = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
         }
         mx *= c;
@@ -454,17 +490,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const float m_new = grow ? mx : m;
         const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
         if (__builtin_expect(__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY), 0)) {
-          // O holds weights taken against the old maxima (the products before
-          // this tile's scores are done): rescale this warp's rows
+          // O holds weights taken against the old maxima: rescale this warp's rows
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][buf ^ 1], ((g - 1) >> 1) & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
-            float o[16];
-            tc::tmem_ld16(scol + kPaColO + 16 * cc, o);
+          for (int cc = 0; cc < 4; ++cc) {
+            float o[32];
+            tc::tmem_ld32(scol + kPaColO + 32 * cc, o);
             tc::tmem_wait_ld();
-            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-            tc::tmem_st16u(scol + kPaColO + 16 * cc, w);
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tc::tmem_st32(scol + kPaColO + 32 * cc, o);
           }
           tc::tmem_wait_st();
         }
@@ -474,6 +511,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           // rows of V behind the prompt (weight 0, but they may hold anything): zero them
           const uint32_t vp = place + 2 * j;
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kPaStages], (vp / kPaStages) & 1));
+          if (!ok) break;
           uint8_t* vt = smem + kPaOffRing + (vp % kPaStages) * kPaTileBytes;
           for (int i = (u.len - tok) * 16 + tid; i < kPaTokens * 16; i += 128)
             *reinterpret_cast<uint4*>(vt + ((i & 8) ? kPaHalfBytes : 0) + (i >> 4) * 128 + (i & 7) * 16) =
@@ -486,7 +524,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // the weights overwrite the scores, 2 BF16 per 32-bit column
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < 2; ++cc) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -496,20 +534,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
           }
-          tc::tmem_st16u(scol + 16 * cc, pk);
-          if (cc & 1) {
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            mbar_arrive(&bars->p_full[t][cc >> 1]);
-          }
+          tc::tmem_st16u(col + 16 * cc, pk);
         }
         l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&bars->p_full[t][buf]);
       }
       place += 2 * n;
       if (!ok) break;
       if (n_t == 0) continue;
       // ---- results ----
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t], (g - 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
       if (!ok) break;
       tc::fence_after_sync();
       const float inv = 1.f / l;  // (a row sees its own key: l > 0, or NaN)
