@@ -10,12 +10,18 @@
 // maximum and sum (FP32); S = Q K^T and O = P V with FP32 accumulators in
 // tensor memory.
 //
-// Tiles are 64 keys because two buffers of scores, then O, fill the 256
-// columns of a row tile: S runs two tiles ahead of the P.V that is under way,
-// so that the softmax always has scores to go on with.  (With 128 keys and one
-// buffer S, softmax and P.V of a row tile are one chain: 3750 cycles per 128
-// keys and pair of row tiles, where the products need 2048, or 2560 with the
-// 64-key tiles, whose S re-reads its 128-row operand twice as often.)
+// Tiles are 64 keys: scores (64 columns), two buffers of weights (32 each) and
+// O fill the 256 columns of a row tile.  The next scores are issued as soon as
+// the softmax holds the present ones in registers, ahead of the product that
+// waits for their weights, so neither side waits for the other's latency, and
+// one commit tells the softmax that its next scores are there and that the
+// weights' buffer is free.  What bounds it: the tensor pipe, 1280 cycles a
+// tile and pair of row tiles (an MMA with N = 64 takes 48 cycles where its
+// multiplications need 32, as it re-reads its 128-row operand).  Measured, 2 x
+// 16000 tokens, 32 query and 8 KV heads: with tiles of 128 keys and one buffer
+// for scores and weights (one chain of S, softmax and P.V) 3.27 ms; 64 keys,
+// two such buffers, S two tiles ahead and after the product that frees its
+// buffer 3.15.
 //
 // A unit of work is (prompt, KV head, 256 rows): rows are query positions x
 // the query heads of the KV head, so that a short prompt still fills them and
@@ -56,7 +62,9 @@ constexpr int kPaOffQ = 0;                             // 2 row tiles
 constexpr int kPaOffRing = 2 * kPaQBytes;
 constexpr int kPaOffBar = kPaOffRing + kPaStages * kPaTileBytes;
 constexpr int kPaSmem = kPaOffBar + 512;
-constexpr uint32_t kPaTileCols = 256;                  // per row tile: two buffers of S (P over it), then O
+constexpr uint32_t kPaTileCols = 256;                  // per row tile: S, two buffers of P, O
+constexpr uint32_t kPaColP = 64;
+constexpr uint32_t kPaPCols = kPaTokens / 2;           // 2 BF16 a column
 constexpr uint32_t kPaColO = 128;
 // Registers per thread: the launch's 168 x 384, moved from the issuing
 // warpgroup to the two softmax warpgroups, which hold a tile's scores.
@@ -80,9 +88,9 @@ struct PaBars {
   uint64_t full[kPaStages];
   uint64_t empty[kPaStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2][2];  // row tile, buffer
-  uint64_t p_full[2][2];
-  uint64_t o_done[2][2];
+  uint64_t s_full[2], s_free[2];  // per row tile: scores are there, are in registers
+  uint64_t p_full[2][2];          // row tile, buffer
+  uint64_t o_done[2][2];          // (two: nobody waits for each of them in turn)
   uint64_t u_full[2], u_empty[2];
   PaUnit unit[2];
   uint32_t tmem_base;
@@ -141,11 +149,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&bars->s_full[t][b], 1);
-        mbar_init(&bars->p_full[t][b], 128);
-        mbar_init(&bars->o_done[t][b], 1);
-      }
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->s_free[t], 128);
+      mbar_init(&bars->p_full[t][0], 128);
+      mbar_init(&bars->p_full[t][1], 128);
+      mbar_init(&bars->o_done[t][0], 1);
+      mbar_init(&bars->o_done[t][1], 1);
       mbar_init(&bars->u_full[t], 1);
       mbar_init(&bars->u_empty[t], 11);  // every other warp
     }
@@ -335,24 +344,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
         return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
       };
-      // S of the K tile in stage st, into buffer buf
-      auto issue_s = [&](int buf, uint32_t st, bool last) {
-        const uint32_t d = scol + buf * kPaTokens;
+      // S of the K tile in stage st
+      auto issue_s = [&](uint32_t st, bool last) {
         const uint64_t kd = k_desc + st * (kPaTileBytes >> 4);
         tc::fence_after_sync();
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16(d, q_desc + (((kk >> 2) * kPaQHalfBytes + 32 * (kk & 3)) >> 4),
+            tc::mma_bf16(scol, q_desc + (((kk >> 2) * kPaQHalfBytes + 32 * (kk & 3)) >> 4),
                          kd + (((kk >> 2) * kPaHalfBytes + 32 * (kk & 3)) >> 4), kIdS, kk > 0);
-          tc::commit(&bars->s_full[t][buf]);
+          tc::commit(&bars->s_full[t]);
           if (last) tc::commit(&bars->q_empty[t]);  // the next unit's queries may come
         }
         __syncwarp();
       };
       // O += P V, P in buffer buf, V in stage st
       auto issue_pv = [&](int buf, uint32_t st, bool first) {
-        const uint32_t p = scol + buf * kPaTokens;
+        const uint32_t p = scol + kPaColP + buf * kPaPCols;
         const uint64_t vd = v_desc + st * (kPaTileBytes >> 4);
         tc::fence_after_sync();
         if (leader) {
@@ -379,7 +387,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       auto give_back = [&](uint32_t st) {
         if (leader) mbar_arrive(&bars->empty[st]);
       };
-      Place k, pk, v;  // of the next S; of the K tile and the V tile of the next P.V
+      // the place `tiles` tiles before
+      auto before = [](const Place& p, uint32_t tiles) -> uint32_t {
+        return p.st >= 2 * tiles ? p.st - 2 * tiles : p.st + kPaStages - 2 * tiles;
+      };
+      Place k, v;  // of the present tile's K and V
       v.step(1);
       uint32_t g = 0;  // tiles of this row tile so far
       uint32_t units = 0;
@@ -389,33 +401,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const int n = max(tiles_of(u, 0), tiles_of(u, 1));
         ok = wait(&bars->q_full[t], units & 1);
         ++units;
-        for (int j = 0; j < 2 && j < n_t && ok; ++j) {
+        if (n_t > 0 && ok) {
           ok = wait(&bars->full[k.st], k.ph);
-          if (ok) issue_s((g + j) & 1, k.st, j == n_t - 1);
-          k.step(2);
+          if (ok) issue_s(k.st, n_t == 1);
         }
         for (int j = 0; j < n_t && ok; ++j, ++g) {
-          const int buf = g & 1, ph = (g >> 1) & 1;
-          ok = wait2(&bars->full[v.st], v.ph, &bars->p_full[t][buf], ph);
+          const uint32_t k_now = k.st;
+          k.step(2);
+          // The scores are in registers.  (They were committed after the
+          // product of two tiles before, so that is done too.)
+          ok = j + 1 < n_t ? wait2(&bars->full[k.st], k.ph, &bars->s_free[t], g & 1) : wait(&bars->s_free[t], g & 1);
           if (!ok) break;
-          give_back(pk.st);  // the weights were made from this tile's scores
-          issue_pv(buf, v.st, j == 0);
-          if (j + 2 < n_t) {  // into the buffer that this product reads, so after it
-            ok = wait2(&bars->full[k.st], k.ph, &bars->o_done[t][buf], ph);
-            if (!ok) break;
-            give_back(v.st);
-            issue_s(buf, k.st, j + 2 == n_t - 1);
-            k.step(2);
-          }
-          pk.step(2);
+          give_back(k_now);
+          if (j >= 2) give_back(before(v, 2));
+          if (j + 1 < n_t) issue_s(k.st, j + 2 == n_t);
+          ok = wait2(&bars->full[v.st], v.ph, &bars->p_full[t][g & 1], (g >> 1) & 1);
+          if (!ok) break;
+          issue_pv(g & 1, v.st, j == 0);
           v.step(2);
         }
         // the last two tiles' V, once their products are done
         for (int back = min(n_t, 2); back > 0 && ok; --back) {
-          const uint32_t gt = g - back;
-          const uint32_t st = v.st >= 2 * back ? v.st - 2 * back : v.st + kPaStages - 2 * back;
-          ok = wait(&bars->o_done[t][gt & 1], (gt >> 1) & 1);
-          if (ok) give_back(st);
+          ok = wait(&bars->o_done[t][(g - back) & 1], ((g - back) >> 1) & 1);
+          if (ok) give_back(before(v, back));
         }
         if (n_t == 0 && ok && leader) mbar_arrive(&bars->q_empty[t]);
         for (int j = n_t; j < n && ok; ++j) {  // tiles that only the other row tile reads
@@ -424,7 +432,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           ok = ok && wait(&bars->full[v.st], v.ph);
           if (ok) give_back(v.st);
           k.step(2);
-          pk.step(2);
           v.step(2);
         }
         if (!ok) break;
@@ -459,15 +466,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       for (int j = 0; j < n_t; ++j, ++g) {
         const int buf = g & 1;
         const int tok = j * kPaTokens;
-        const uint32_t col = scol + buf * kPaTokens;
         // (`ok` stays warp-uniform: the loads below are warp-collective)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t][buf], (g >> 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], g & 1));
         if (!ok) break;
         tc::fence_after_sync();
         float s[64];  // raw scores
-        tc::tmem_ld32(col, s);
-        tc::tmem_ld32(col + 32, s + 32);
+        tc::tmem_ld32(scol, s);
+        tc::tmem_ld32(scol + 32, s + 32);
         tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        mbar_arrive(&bars->s_free[t]);
         if (u.pos0 + t * per_tile + warp_pos + 1 - tok < kPaTokens) {  // some row of the warp sees the tile in part
           const int lim = pos + 1 - tok;
 #pragma unroll
@@ -491,7 +499,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
         if (__builtin_expect(__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY), 0)) {
           // O holds weights taken against the old maxima: rescale this warp's rows
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][buf ^ 1], ((g - 1) >> 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll
@@ -522,7 +530,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const float2 c2 = make_float2(c, c);
         const float2 nm2 = make_float2(nm, nm);
         float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the weights overwrite the scores, 2 BF16 per 32-bit column
+        // the weights, 2 BF16 per 32-bit column (their buffer's last product is done: see the issuers)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t pk[16];
@@ -534,7 +542,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
           }
-          tc::tmem_st16u(col + 16 * cc, pk);
+          tc::tmem_st16u(scol + kPaColP + buf * kPaPCols + 16 * cc, pk);
         }
         l += (acc2[0].x + acc2[0].y) + (acc2[1].x + acc2[1].y);
         tc::tmem_wait_st();
