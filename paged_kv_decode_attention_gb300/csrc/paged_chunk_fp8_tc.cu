@@ -4,7 +4,7 @@
 // cached tokens ("Chapter 8: Inference Optimization", clxhxhhr.top/posts/4341,
 // §8.2.3), or a chain of drafted tokens (§8.5.2), with K and V in FP8 (§8.4.4).
 //
-// Mathematics.  Softmax over the visible keys, tile by tile (128 keys) with a
+// Mathematics.  Softmax over the visible keys, tile by tile (64 keys) with a
 // running maximum and sum in FP32.  With value = code * scale, ks and vs the
 // scales of a key's block:
 //   S_ij = sum_d (sigma_i q_id) kcode_jd      (tensor cores, codes as they are)
@@ -25,13 +25,20 @@
 // kWide : 256 rows (64 positions x 4 heads) share a CTA's tiles, 128 a row
 //         tile; while one row tile's softmax runs, the tensor cores work on
 //         the other's products.
-// !kWide: up to kCols rows, 32, 64 or 128.  HBM is the bound, and a chain of
+// !kWide: up to kRows rows, 32, 64 or 128.  HBM is the bound, and a chain of
 //         scores, softmax and product is longer than a tile's transfer.  So
 //         the CTA's two halves take the even and the odd tiles of keys, and
-//         the query rows are laid out 128 / kCols times: a copy's threads do
-//         the softmax of kCols of a tile's 128 keys, with a maximum and a sum
-//         of their own (the other keys' weights are zeros).  At the end all
-//         copies and both halves are joined through shared memory.
+//         the query rows are laid out 128 / kRows times: a copy's threads do
+//         the softmax of kRows / 2 of a tile's 64 keys, with a maximum and a
+//         sum of their own (the other keys' weights are zeros).  At the end
+//         all copies and both halves are joined through shared memory.
+//
+// Scores (64 columns), two buffers of weights (32 each) and O fill a row tile's
+// 256 columns of tensor memory.  The next scores are issued as soon as the
+// softmax holds the present ones in registers, ahead of the product that waits
+// for their weights: neither side waits for the other's latency.  (Tiles of 128
+// keys with scores and weights in one buffer, one chain: 1.09 ms for 4 x 2000
+// queries behind 4000 to 8000 tokens, 57 us for 37 x 7 behind 2,170.)
 //
 // Work is cut by tiles, not by requests: all (request, row tile, KV head) jobs
 // in a row are divided evenly among the CTAs, one per SM, whatever the
@@ -57,26 +64,31 @@
 namespace pkv {
 namespace {
 
-constexpr int kCfTokens = 128;                        // keys of a tile
-constexpr int kCfTileBlocks = kCfTokens / kBlockSize;  // 8
-constexpr int kCfTileBytes = kCfTokens * kHeadDim;    // K or V of a tile: 16 KiB
+constexpr int kCfTokens = 64;                         // keys of a tile
+constexpr int kCfTileBlocks = kCfTokens / kBlockSize;  // 4
+constexpr int kCfTileBytes = kCfTokens * kHeadDim;    // K or V of a tile: 8 KiB
 constexpr int kCfBoxBytes = kBlockSize * kHeadDim;
-constexpr int kCfSlots = 10;                          // ring: K, V, K, V, ...
-constexpr int kCfScaleSlots = 8;                      // tiles whose scales are held
+constexpr int kCfSlots = 20;                          // ring: K, V, K, V, ...
+constexpr int kCfScaleSlots = 16;                     // tiles whose scales are held
+constexpr int kCfGroupTiles = 32 / kCfTileBlocks;     // tiles whose blocks a warp looks up at a time
 constexpr int kCfThreads = 384;
 constexpr int kCfRows = 128;
 constexpr int kCfPos = kCfRows / kGroup;              // positions of a row tile
 constexpr int kCfOffQ = 0;                            // [row tile][high, low parts]; !kWide: one, then the join's buffer
-constexpr int kCfOffJoin = 2 * kCfTileBytes;          // FP32 [2 x 128][32]
-constexpr int kCfOffRing = 4 * kCfTileBytes;
+constexpr int kCfPartBytes = kCfRows * kHeadDim;      // one part of a row tile's queries: 16 KiB
+constexpr int kCfOffJoin = 2 * kCfPartBytes;          // FP32 [2 x 128][32]
+constexpr int kCfOffRing = 4 * kCfPartBytes;
 constexpr int kCfOffScale = kCfOffRing + kCfSlots * kCfTileBytes;
 constexpr int kCfScaleFloats = 3 * kCfTileBlocks;     // ks, log2 vs, 1 / vs
 constexpr int kCfOffSigma = kCfOffScale + kCfScaleSlots * kCfScaleFloats * 4;  // FP32 [2][128]: scale / sigma
 constexpr int kCfOffBar = kCfOffSigma + 2 * kCfRows * 4;
-constexpr int kCfSmem = kCfOffBar + 528;
+constexpr int kCfSmem = kCfOffBar + 832;
 static_assert(kCfSmem <= 227 * 1024, "one CTA per SM");
 static_assert(kCfOffBar % 16 == 0 && kCfOffScale % 16 == 0, "alignment");
-constexpr uint32_t kCfTileCols = 256;                 // S (weights over it), then O
+constexpr uint32_t kCfTileCols = 256;                 // S, two buffers of weights (high parts, low parts), O
+constexpr uint32_t kCfColP = 64;
+constexpr uint32_t kCfPCols = 32;
+constexpr uint32_t kCfColLow = 16;                    // low parts, within a buffer
 constexpr uint32_t kCfColO = 128;
 constexpr int kCfSoftmaxRegs = 208;
 constexpr int kCfIssueRegs = 80;
@@ -89,7 +101,7 @@ constexpr float kCfLag = 2.f;     // base 2: weights stay at or below 2^2, 2^8 w
 constexpr float kCfFactor = -2.f;
 constexpr float kCfCodeUnit = 256.f;
 // A CTA's share is at least this many tiles: a shorter one would not pay for its joining.
-constexpr int kCfMinTiles = 2;
+constexpr int kCfMinTiles = 4;
 
 struct alignas(16) CfPiece {
   int32_t r, rt, kvh;   // request, row tile (pair), KV head
@@ -104,14 +116,14 @@ struct CfBars {
   uint64_t q_full[2];
   uint64_t q_empty;               // !kWide: the other half is done with the queries
   uint64_t join_full, join_free;  // !kWide: the join's buffer is written, is read
-  uint64_t s_full[2];
+  uint64_t s_full[2], s_free[2];
   uint64_t p_full[2][2];
-  uint64_t o_done[2];
+  uint64_t o_done[2][2];
   uint64_t u_full[2], u_empty[2];
   CfPiece piece[2];
   uint32_t tmem_base;
 };
-static_assert(sizeof(CfBars) <= 528 && offsetof(CfBars, piece) % 16 == 0, "barrier area");
+static_assert(sizeof(CfBars) <= 832 && offsetof(CfBars, piece) % 16 == 0, "barrier area");
 
 template <int kRegs>
 __device__ __forceinline__ void cf_regs_up() {
@@ -174,7 +186,7 @@ __device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int64_t pair, 
   return end > 0 ? (end + kCfTokens - 1) / kCfTokens : 0;
 }
 
-template <bool kWide, int kCols>
+template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kCfThreads, 1)
     paged_chunk_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                               const ChunkScaledArgs a) {
@@ -199,9 +211,11 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 128);
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t][0], 128);
-      mbar_init(&bars->p_full[t][1], 128);
-      mbar_init(&bars->o_done[t], 1);
+      mbar_init(&bars->s_free[t], 128);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->p_full[t][b], 128);
+        mbar_init(&bars->o_done[t][b], 1);
+      }
       mbar_init(&bars->u_full[t], 1);
       mbar_init(&bars->u_empty[t], 11);  // every other warp
     }
@@ -302,13 +316,13 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         a.cuts[blockIdx.x] = cut;
       }
       uint32_t tiles = 0;  // scale slots written so far
-      // the scales of a piece's blocks, 32 blocks (4 tiles) at a time, fetched a group ahead
+      // the scales of a piece's blocks, 32 blocks (8 tiles) at a time, fetched a group ahead
       auto scales_of = [&](const CfPiece& u) {
         const int32_t* table = a.block_tables + static_cast<int64_t>(u.r) * a.max_blocks;
         const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
         const int last = (ctx + kBlockSize - 1) / kBlockSize;  // blocks past the context have no scale
         auto fetch = [&](int group, float& ks, float& vs) {
-          const int lb = (u.begin + 4 * group) * kCfTileBlocks + lane;
+          const int lb = (u.begin + kCfGroupTiles * group) * kCfTileBlocks + lane;
           ks = vs = 1.f;
           if (lb < last && lb < (u.begin + u.take) * kCfTileBlocks) {
             int b = table[lb];
@@ -318,19 +332,19 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             vs = a.v_scales[at];
           }
         };
-        const int groups = (u.take + 3) >> 2;
+        const int groups = (u.take + kCfGroupTiles - 1) / kCfGroupTiles;
         float ks, vs, ks_next = 1.f, vs_next = 1.f;
         fetch(0, ks, vs);
         for (int g = 0; g < groups && ok; ++g) {
           if (g + 1 < groups) fetch(g + 1, ks_next, vs_next);
           const float lv = log2f(vs), iv = 1.f / vs;
-          for (int k = 0; k < 4 && 4 * g + k < u.take && ok; ++k, ++tiles) {
+          for (int k = 0; k < kCfGroupTiles && kCfGroupTiles * g + k < u.take && ok; ++k, ++tiles) {
             const int slot = tiles % kCfScaleSlots;
             if (tiles >= kCfScaleSlots)
               ok = __all_sync(0xffffffffu, mbar_wait(&bars->sc_empty[slot], ((tiles / kCfScaleSlots) & 1) ^ 1));
             if (!ok) break;
-            float* dst = reinterpret_cast<float*>(smem + kCfOffScale) + slot * kCfScaleFloats + (lane & 7);
-            if ((lane >> 3) == k) {
+            float* dst = reinterpret_cast<float*>(smem + kCfOffScale) + slot * kCfScaleFloats + lane % kCfTileBlocks;
+            if (lane / kCfTileBlocks == k) {
               dst[0] = ks;
               dst[kCfTileBlocks] = lv;
               dst[2 * kCfTileBlocks] = iv;
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 8) {
       // ---------------------------- TMA producer ----------------------------
-      // K of a tile: lanes 0-7, V: lanes 8-15.
+      // K of a tile: lanes 0-3, V: lanes 4-7.
       // read once, unless several row tiles of the request read the same blocks
       const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
       const int oob_row = a.num_blocks * a.num_kv_heads * kBlockSize;  // first row past the pool
@@ -398,9 +412,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         auto entry = [&](int i) -> int { return table[min(b0 + i, a.max_blocks - 1)]; };
         int cur = row_of(lane, entry(lane)), next = 0;
         for (int j = 0; j < u.take && ok; ++j, ++filled) {
-          if ((j & 3) == 0) next = entry(8 * j + 32 + lane);  // the next four tiles' ids
-          const int y = __shfl_sync(0xffffffffu, cur, (j & 3) * kCfTileBlocks + (lane & 7));
-          if ((j & 3) == 3) cur = row_of(8 * (j + 1) + lane, next);
+          const int in_group = j % kCfGroupTiles;
+          if (in_group == 0) next = entry(kCfTileBlocks * j + 32 + lane);  // the next tiles' ids
+          const int y = __shfl_sync(0xffffffffu, cur, in_group * kCfTileBlocks + lane % kCfTileBlocks);
+          if (in_group == kCfGroupTiles - 1) cur = row_of(kCfTileBlocks * (j + 1) + lane, next);
           const uint32_t place = 2 * filled + (is_v ? 1 : 0);
           const uint32_t slot = place % kCfSlots;
           bool mine = true;
@@ -410,7 +425,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           if (lane == 0 || lane == kCfTileBlocks) mbar_arrive_expect_tx(&bars->full[slot], kCfTileBytes);
           __syncwarp();
           if (lane < 2 * kCfTileBlocks)
-            tc::tma_load_2d(smem + kCfOffRing + slot * kCfTileBytes + (lane & 7) * kCfBoxBytes, is_v ? &v_map : &k_map, 0,
+            tc::tma_load_2d(smem + kCfOffRing + slot * kCfTileBytes + lane % kCfTileBlocks * kCfBoxBytes, is_v ? &v_map : &k_map, 0,
                             y, &bars->full[slot], policy);
         }
         if (!ok) break;
@@ -429,12 +444,21 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       const int t = warp - 9;
       const bool leader = lane == 0;
       const uint32_t scol = tmem + t * kCfTileCols;
-      const uint64_t q_desc = tc::smem_desc(sbase + kCfOffQ + (kWide ? t * 2 * kCfTileBytes : 0), 16, 1024);
+      const uint64_t q_desc = tc::smem_desc(sbase + kCfOffQ + (kWide ? t * 2 * kCfPartBytes : 0), 16, 1024);
       const uint64_t ring = tc::smem_desc(sbase + kCfOffRing, 16, 1024);
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
       auto wait_full = [&](uint32_t place) -> bool { return wait(&bars->full[place % kCfSlots], (place / kCfSlots) & 1); };
+      // a place of the ring and another barrier, both tried before either result is looked at
+      auto wait_both = [&](uint32_t place, uint64_t* y, uint32_t yp) -> bool {
+        uint64_t* x = &bars->full[place % kCfSlots];
+        const uint32_t xp = (place / kCfSlots) & 1;
+        const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
+        return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
+      };
+      // Stages go back by plain arrivals once a later wait has shown that the
+      // products that read them are done.
       auto give_back = [&](uint32_t place) {
         if (leader) mbar_arrive(&bars->empty[place % kCfSlots]);
       };
@@ -442,27 +466,28 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       auto issue_s = [&](uint32_t place) {
         const uint64_t kd = ring + (place % kCfSlots) * (kCfTileBytes >> 4);
         tc::fence_after_sync();
-        if (leader) {
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_f8(scol, q_desc + (((kk >> 2) * kCfTileBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
+            tc::mma_f8(scol, q_desc + (((kk >> 2) * kCfPartBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
                        kk > 0 ? 1u : 0u);
           tc::commit(&bars->s_full[t]);
         }
         __syncwarp();
       };
-      // O += (high + low parts of the weights) V, 64 keys
-      auto issue_pv = [&](uint32_t place, int half, bool first) {
+      // O += (high + low parts of the weights) V
+      auto issue_pv = [&](uint32_t place, uint32_t buf, bool first) {
         const uint64_t vd = ring + (place % kCfSlots) * (kCfTileBytes >> 4);
+        const uint32_t pcol = scol + kCfColP + buf * kCfPCols;
         tc::fence_after_sync();
-        if (leader) {
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const int slice = 2 * half + (kk & 1);  // of 32 keys
-            mma_f8_tmem_a(scol + kCfColO, scol + 32 * (kk >> 1) + 8 * slice, vd + slice * (4096 >> 4), kIdO,
+            const int slice = kk & 1;  // of 32 keys
+            mma_f8_tmem_a(scol + kCfColO, pcol + kCfColLow * (kk >> 1) + 8 * slice, vd + slice * (4096 >> 4), kIdO,
                           (!first || kk > 0) ? 1u : 0u);
           }
-          if (half == 1) tc::commit(&bars->o_done[t]);
+          tc::commit(&bars->o_done[t][buf]);
         }
         __syncwarp();
       };
@@ -473,7 +498,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       CfPiece u;
       while (next_piece(u)) {
         const int n_t = tiles_of(u, t);
-        uint32_t c = c0 + (kWide ? 0 : 2 * t);
+        uint32_t c = c0 + (kWide ? 0 : 2 * t);  // place of the present tile's K; its V is at c + 1
         c0 += 2 * u.take;
         ok = wait(&bars->q_full[kWide ? t : 0], pieces & 1);
         ++pieces;
@@ -482,18 +507,21 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           if (ok) issue_s(c);
         }
         for (int j = 0; j < n_t && ok; ++j, ++g, c += kStep) {
-          ok = wait_full(c + 1) && wait(&bars->p_full[t][0], g & 1);
-          if (ok) issue_pv(c + 1, 0, j == 0);
-          ok = ok && wait(&bars->p_full[t][1], g & 1);
+          // The scores are in registers.  (They were committed after the
+          // product of two tiles before, so that is done too.)
+          ok = j + 1 < n_t ? wait_both(c + kStep, &bars->s_free[t], g & 1) : wait(&bars->s_free[t], g & 1);
           if (!ok) break;
-          give_back(c);  // the weights were made from this tile's scores
-          issue_pv(c + 1, 1, false);
-          // The next scores go where the weights are, so after this product.
-          if (j + 1 < n_t) ok = wait_full(c + kStep);
-          ok = ok && wait(&bars->o_done[t], g & 1);
-          if (!ok) break;
-          give_back(c + 1);
+          give_back(c);
+          if (j >= 2) give_back(c + 1 - 2 * kStep);
           if (j + 1 < n_t) issue_s(c + kStep);
+          ok = wait_both(c + 1, &bars->p_full[t][g & 1], (g >> 1) & 1);
+          if (!ok) break;
+          issue_pv(c + 1, g & 1, j == 0);
+        }
+        // the last two tiles' V, once their products are done
+        for (int back = min(n_t, 2); back > 0 && ok; --back) {
+          ok = wait(&bars->o_done[t][(g - back) & 1], ((g - back) >> 1) & 1);
+          if (ok) give_back(c + 1 - back * kStep);
         }
         if (!ok) break;
         if (!kWide && t == 1 && leader) mbar_arrive(&bars->q_empty);
@@ -521,11 +549,13 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       for (int64_t i = threadIdx.x; i < chunks; i += 256) o[i] = make_uint4(0, 0, 0, 0);
     }
 
-    // !kWide: this warp's copy of the query rows, and the keys of a tile that are its
-    const int copy = quad * 32 / kCols;
+    // this warp's copy of the query rows, and the keys of a tile that are its
+    constexpr int kCopies = kCfRows / kRows;
+    constexpr int kCols = kCfTokens / kCopies;
+    const int copy = quad * 32 / kRows;
     const int key0 = copy * kCols;
-    const int qrow = row & (kCols - 1);            // query row
-    const int warp_row = quad * 32 & (kCols - 1);  // its warp's first
+    const int qrow = row & (kRows - 1);            // query row
+    const int warp_row = quad * 32 & (kRows - 1);  // its warp's first
     uint32_t g = 0;      // tiles of this half so far
     uint32_t tile0 = 0;  // tiles of the pieces so far
     uint32_t pieces = 0;
@@ -542,7 +572,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       const int warp_seen = first_key + (warp_row >> 2);  // its warp's first row
       // ---- the query operand: 8 lanes a row, 16 dims each ----
       if (kWide || t == 0) {
-        uint8_t* qa = smem + kCfOffQ + row_tile * 2 * kCfTileBytes;
+        uint8_t* qa = smem + kCfOffQ + row_tile * 2 * kCfPartBytes;
         if (!kWide && pieces > 0) {
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (pieces & 1) ^ 1));
           if (!ok) break;
@@ -587,7 +617,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             }
             const uint32_t at = tc::sw128_offset_b8(m, 16 * c16);
             *reinterpret_cast<uint4*>(qa + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(qa + kCfTileBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(qa + kCfPartBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (c16 == 0) inv_sigma[m] = a.scale_log2 / sigma;
           }
         }
@@ -618,21 +648,28 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         tc::fence_after_sync();
         if (warp_live) {
           float s[kCols];
+          if constexpr (kCols == 16) {
+            tc::tmem_ld16(scol + key0, s);
+          } else {
 #pragma unroll
-          for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(scol + key0 + e, s + e);
+            for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(scol + key0 + e, s + e);
+          }
           tc::tmem_wait_ld();
-          if constexpr (kCols < 128) {  // the other copies' keys: weights of zero
-            const uint32_t zeros[16] = {};
+          tc::fence_before_sync();
+          mbar_arrive(&bars->s_free[t]);
+          // the weights' buffer: its last product is done (see the issuers)
+          const uint32_t pcol = scol + kCfColP + (g & 1) * kCfPCols;
+          auto store = [&](uint32_t col, const uint32_t* w) {
+            if constexpr (kCols == 64) tc::tmem_st16u(col, w);
+            if constexpr (kCols == 32) tc::tmem_st8(col, w);
+            if constexpr (kCols == 16) tc::tmem_st4(col, reinterpret_cast<const float*>(w));
+          };
+          if constexpr (kCopies > 1) {  // the other copies' keys: weights of zero
+            const uint32_t zeros[kCols / 4] = {};
 #pragma unroll
-            for (int o = 1; o < 128 / kCols; ++o) {
-              const uint32_t col = scol + (copy ^ o) * (kCols / 4);
-              if constexpr (kCols == 64) {
-                tc::tmem_st16u(col, zeros);
-                tc::tmem_st16u(col + 32, zeros);
-              } else {
-                tc::tmem_st8(col, zeros);
-                tc::tmem_st8(col + 32, zeros);
-              }
+            for (int o = 1; o < kCopies; ++o) {
+              store(pcol + (copy ^ o) * (kCols / 4), zeros);
+              store(pcol + kCfColLow + (copy ^ o) * (kCols / 4), zeros);
             }
           }
           if (warp_seen - tok - key0 < kCols) {  // some row of the warp sees its keys in part
@@ -653,8 +690,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           const float m_new = grow ? mx : m;
           const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
           if (__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY)) {
-            // O holds weights taken against the old maxima (the products
-            // before this tile's scores are done): rescale this warp's rows
+            // O holds weights taken against the old maxima: rescale this warp's rows
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
               float o[16];
@@ -670,57 +709,45 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           l *= alpha;
           m = m_new;
           const float nm = (m == -INFINITY ? 0.f : -m) + kCfFactor;
-          constexpr int kChunk = kCols < 64 ? kCols : 64;  // keys whose weights are stored together
+          uint32_t hi[kCols / 4], lo[kCols / 4];
 #pragma unroll
-          for (int h = 0; h < kCols / kChunk; ++h) {
-            uint32_t hi[kChunk / 4], lo[kChunk / 4];
+          for (int b = 0; b < kCols / kBlockSize; ++b) {
+            const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
+            const float2 k2 = make_float2(kc, kc);
+            const float2 n2 = make_float2(off, off);
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int b = 0; b < kChunk / kBlockSize; ++b) {
-              const int blk = kChunk / kBlockSize * h + b;
-              const float kc = sc[blk] * c, off = sc[kCfTileBlocks + blk] + nm;
-              const float2 k2 = make_float2(kc, kc);
-              const float2 n2 = make_float2(off, off);
-              float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = 16 * blk + 4 * e;
-                const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), k2, n2);
-                const float2 y = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), k2, n2);
-                const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
-                const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
-                acc = __fadd2_rn(acc, make_float2(p0, p1));
-                acc = __fadd2_rn(acc, make_float2(p2, p3));
-                cf_weights(p0, p1, p2, p3, hi[4 * b + e], lo[4 * b + e]);
-              }
-              l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + blk], l);
+            for (int e = 0; e < 4; ++e) {
+              const int i = 16 * b + 4 * e;
+              const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), k2, n2);
+              const float2 y = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), k2, n2);
+              const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
+              const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
+              acc = __fadd2_rn(acc, make_float2(p0, p1));
+              acc = __fadd2_rn(acc, make_float2(p2, p3));
+              cf_weights(p0, p1, p2, p3, hi[4 * b + e], lo[4 * b + e]);
             }
-            // the weights overwrite the scores: high parts at columns 0-31, low parts at 32-63
-            const uint32_t col = scol + copy * (kCols / 4) + 16 * h;
-            if constexpr (kChunk == 64) {
-              tc::tmem_st16u(col, hi);
-              tc::tmem_st16u(col + 32, lo);
-            } else {
-              tc::tmem_st8(col, hi);
-              tc::tmem_st8(col + 32, lo);
-            }
-            if (h == 0 && ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
-              // slots past the context may hold any code: V's rows there are
-              // zeroed (a weight of zero is not enough)
-              const uint32_t vp = 2 * (tile0 + in_piece) + 1;
-              ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kCfSlots], (vp / kCfSlots) & 1));
-              const int z0 = ctx - tok, z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
-              uint8_t* vt = smem + kCfOffRing + (vp % kCfSlots) * kCfTileBytes;
-              for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) reinterpret_cast<uint4*>(vt)[i] = make_uint4(0, 0, 0, 0);
-              tc::fence_proxy_async_smem();
-            }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            mbar_arrive(&bars->p_full[t][h]);
+            l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
           }
-          if constexpr (kCols < 128) mbar_arrive(&bars->p_full[t][1]);
+          store(pcol + copy * (kCols / 4), hi);
+          store(pcol + kCfColLow + copy * (kCols / 4), lo);
+          if (ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
+            // slots past the context may hold any code: V's rows there are
+            // zeroed (a weight of zero is not enough)
+            const uint32_t vp = 2 * (tile0 + in_piece) + 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kCfSlots], (vp / kCfSlots) & 1));
+            if (!ok) break;
+            const int z0 = ctx - tok, z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
+            uint8_t* vt = smem + kCfOffRing + (vp % kCfSlots) * kCfTileBytes;
+            for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) reinterpret_cast<uint4*>(vt)[i] = make_uint4(0, 0, 0, 0);
+            tc::fence_proxy_async_smem();
+          }
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          mbar_arrive(&bars->p_full[t][g & 1]);
         } else {
-          mbar_arrive(&bars->p_full[t][0]);
-          mbar_arrive(&bars->p_full[t][1]);
+          mbar_arrive(&bars->s_free[t]);
+          mbar_arrive(&bars->p_full[t][g & 1]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->sc_empty[sl]);
@@ -730,7 +757,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       l *= kCfCodeUnit;  // in O's unit
       // ---- results ----
       if (n_t > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t], (g - 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
         if (!ok) break;
         tc::fence_after_sync();
       }
@@ -770,8 +797,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       } else {
         // Join the two halves' copies: maxima and sums first, then 32 dims a
         // pass.  A thread joins 4 dims of up to kTake rows.
-        constexpr int kParts = 2 * 128 / kCols;  // partials of a row
-        constexpr int kTake = kCols / 32;
+        constexpr int kParts = 2 * kCopies;  // partials of a row
+        constexpr int kTake = kRows / 32;
         float4* buf = reinterpret_cast<float4*>(smem + kCfOffJoin);
         const int who = t * kCfRows + row;
         auto written = [&]() -> bool {  // everyone's part of a pass is there
@@ -799,7 +826,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           float mm = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
-            ml[q] = reinterpret_cast<const float2*>(buf)[q * kCols + rr];
+            ml[q] = reinterpret_cast<const float2*>(buf)[q * kRows + rr];
             mm = fmaxf(mm, ml[q].x);
           }
 #pragma unroll
@@ -836,7 +863,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
 #pragma unroll
             for (int q = 0; q < kParts; ++q) {
               if (f[k][q] == 0.f) continue;  // nothing was written for it, or it adds nothing
-              const float4 x = buf[(q * kCols + rr) * 8 + (ch ^ (rr & 7))];
+              const float4 x = buf[(q * kRows + rr) * 8 + (ch ^ (rr & 7))];
               o.x = fmaf(x.x, f[k][q], o.x);
               o.y = fmaf(x.y, f[k][q], o.y);
               o.z = fmaf(x.z, f[k][q], o.z);
@@ -911,10 +938,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a
   }
 }
 
-template <bool kWide, int kCols>
+template <bool kWide, int kRows>
 cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
   static std::atomic<bool> done[64];  // per device; host threads may race on a first call
-  auto kernel = paged_chunk_fp8_tc_kernel<kWide, kCols>;
+  auto kernel = paged_chunk_fp8_tc_kernel<kWide, kRows>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       auto issue_s = [&](uint32_t st, bool last) {
         const uint64_t kd = k_desc + st * (kPaTileBytes >> 4);
         tc::fence_after_sync();
-        if (leader) {
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc::mma_bf16(scol, q_desc + (((kk >> 2) * kPaQHalfBytes + 32 * (kk & 3)) >> 4),
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const uint32_t p = scol + kPaColP + buf * kPaPCols;
         const uint64_t vd = v_desc + st * (kPaTileBytes >> 4);
         tc::fence_after_sync();
-        if (leader) {
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc::mma_bf16_tmem_a(scol + kPaColO, p + 8 * kk, vd + kk * (2048 >> 4), kIdO, (!first || kk > 0) ? 1u : 0u);
