@@ -13,25 +13,27 @@
 //          what the second product needs, inside E4M3's range whatever vs is
 //   O_i  = sum_j w_ij vcode_j,   l_i = sum_j w_ij / vs_j,   out = O_i / l_i
 // Scales are constant over 16 keys, so they cost a few FP32 operations per 16
-// scores.  8-bit products want both operands in 8 bits.  Queries enter as two
+// scores.  8-bit products want both operands in 8 bits.  Queries enter S as two
 // E4M3 parts (sigma_i a power of two that brings the row's largest magnitude
-// to 2^7 .. 2^8: exact down to 2^-17 of it), weights as two parts times 2^6
-// (2^-8 relative, by way of FP16's 2^-11, down to 2^-16 of the largest).  Two
-// products at twice the BF16 rate cost what one of converted codes would, and
-// the tiles need no conversion pass: the SM's shared memory, which would be
-// the bound (a converted tile is read once and written twice over), carries
-// them once in and twice into the tensor cores.
+// to 2^7 .. 2^8: exact down to 2^-17 of it), against K's codes as they are: two
+// products at twice the BF16 rate.
 //
 // kWide : 256 rows (64 positions x 4 heads) share a CTA's tiles, 128 a row
 //         tile; while one row tile's softmax runs, the tensor cores work on
-//         the other's products.
+//         the other's products.  What bounds it is the softmax's arithmetic,
+//         so the weights enter as one FP16 value (2^-11 relative) and four
+//         warps convert each V tile to FP16, once for all rows.  (With two
+//         E4M3 parts of each weight the softmax of a tile took 900 cycles of
+//         a warp for its exponentials and parts, now as many as a prompt's.)
 // !kWide: up to kRows rows, 32, 64 or 128.  HBM is the bound, and a chain of
 //         scores, softmax and product is longer than a tile's transfer.  So
 //         the CTA's two halves take the even and the odd tiles of keys, and
 //         the query rows are laid out 128 / kRows times: a copy's threads do
 //         the softmax of kRows / 2 of a tile's 64 keys, with a maximum and a
 //         sum of their own (the other keys' weights are zeros).  At the end
-//         all copies and both halves are joined through shared memory.
+//         all copies and both halves are joined through shared memory.  V's
+//         codes enter as they are and the weights as two E4M3 parts times 2^6
+//         (2^-8 relative, by way of FP16, down to 2^-16 of the largest).
 //
 // Scores (64 columns), two buffers of weights (32 each) and O fill a row tile's
 // 256 columns of tensor memory.  The next scores are issued as soon as the
@@ -41,17 +43,21 @@
 // queries behind 4000 to 8000 tokens, 57 us for 37 x 7 behind 2,170.)
 //
 // Work is cut by tiles, not by requests: all (request, row tile, KV head) jobs
-// in a row are divided evenly among the CTAs, one per SM, whatever the
-// contexts' lengths are.  A job cut in two or more leaves un-normalised FP32
-// partials, at most two per CTA, which a second kernel joins.
+// in a row, each counted as its tiles and kCfJobCost more for its start and
+// end, are divided evenly among the CTAs, one per SM, whatever the contexts'
+// lengths are.  A job cut in two or more leaves un-normalised FP32 partials, at
+// most two per CTA, which a second kernel joins.
 //
-// CTA = 12 warps:
+// CTA = 16 warps:
 //   warps 0-7: softmax, one thread per row (TMEM lane), a warpgroup per row
-//             tile (or half of the tiles); they also write the query operand.
-//   warp 8  : TMA producer of K and V (16-token boxes of 2 KiB, 128-byte
-//             swizzle; blocks past the range arrive as zeros).
+//             tile (or half of the tiles).
+//   warp 8  : TMA producer of K (kWide: and V): 16-token boxes of 2 KiB, 128-byte
+//             swizzle; blocks past the range arrive as zeros.  A box takes some
+//             70 cycles to issue.
 //   warps 9, 10: MMA issuers, one per row tile (or half).
 //   warp 11 : finds the CTA's pieces and fetches the blocks' scales.
+//   warps 12-15: the query operand, a piece ahead; kWide: V to FP16; !kWide: warp
+//             12 is V's producer instead.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -68,40 +74,52 @@ constexpr int kCfTokens = 64;                         // keys of a tile
 constexpr int kCfTileBlocks = kCfTokens / kBlockSize;  // 4
 constexpr int kCfTileBytes = kCfTokens * kHeadDim;    // K or V of a tile: 8 KiB
 constexpr int kCfBoxBytes = kBlockSize * kHeadDim;
-constexpr int kCfSlots = 20;                          // ring: K, V, K, V, ...
 constexpr int kCfScaleSlots = 16;                     // tiles whose scales are held
 constexpr int kCfGroupTiles = 32 / kCfTileBlocks;     // tiles whose blocks a warp looks up at a time
-constexpr int kCfThreads = 384;
+constexpr int kCfThreads = 512;
 constexpr int kCfRows = 128;
 constexpr int kCfPos = kCfRows / kGroup;              // positions of a row tile
-constexpr int kCfOffQ = 0;                            // [row tile][high, low parts]; !kWide: one, then the join's buffer
 constexpr int kCfPartBytes = kCfRows * kHeadDim;      // one part of a row tile's queries: 16 KiB
-constexpr int kCfOffJoin = 2 * kCfPartBytes;          // FP32 [2 x 128][32]
-constexpr int kCfOffRing = 4 * kCfPartBytes;
-constexpr int kCfOffScale = kCfOffRing + kCfSlots * kCfTileBytes;
+constexpr int kCfV16Bytes = 2 * kCfTileBytes;         // a V tile in FP16, two 64-dim halves
+constexpr int kCfV16Stages = 3;
 constexpr int kCfScaleFloats = 3 * kCfTileBlocks;     // ks, log2 vs, 1 / vs
-constexpr int kCfOffSigma = kCfOffScale + kCfScaleSlots * kCfScaleFloats * 4;  // FP32 [2][128]: scale / sigma
-constexpr int kCfOffBar = kCfOffSigma + 2 * kCfRows * 4;
-constexpr int kCfSmem = kCfOffBar + 832;
-static_assert(kCfSmem <= 227 * 1024, "one CTA per SM");
-static_assert(kCfOffBar % 16 == 0 && kCfOffScale % 16 == 0, "alignment");
+constexpr int kCfHelpers = 4;                         // warps 12-15
+
+template <bool kWide>
+struct CfShape {
+  static constexpr int kSlots = kWide ? 14 : 16;      // ring: K, V, K, V, ...
+  // queries, [row tile] or [buffer], each [high, low parts]
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffExtra = 4 * kCfPartBytes;  // V in FP16, or the join's buffer, FP32 [2 x 128][32]
+  static constexpr int kOffRing = kOffExtra + (kWide ? kCfV16Stages * kCfV16Bytes : 2 * kCfRows * 32 * 4);
+  static constexpr int kOffScale = kOffRing + kSlots * kCfTileBytes;
+  static constexpr int kOffSigma = kOffScale + kCfScaleSlots * kCfScaleFloats * 4;  // FP32 [2][128]: scale / sigma
+  static constexpr int kOffBar = kOffSigma + 2 * kCfRows * 4;
+  static constexpr int kSmem = kOffBar + 896;
+  static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+  static_assert(kOffBar % 16 == 0 && kOffScale % 16 == 0 && kOffRing % 1024 == 0, "alignment");
+};
+
 constexpr uint32_t kCfTileCols = 256;                 // S, two buffers of weights (high parts, low parts), O
 constexpr uint32_t kCfColP = 64;
 constexpr uint32_t kCfPCols = 32;
 constexpr uint32_t kCfColLow = 16;                    // low parts, within a buffer
 constexpr uint32_t kCfColO = 128;
-constexpr int kCfSoftmaxRegs = 208;
-constexpr int kCfIssueRegs = 80;
-static_assert((2 * kCfSoftmaxRegs + kCfIssueRegs) * 128 <= 168 * kCfThreads, "register split");
-constexpr float kCfLag = 2.f;     // base 2: weights stay at or below 2^2, 2^8 with the factor below
-// Weights enter times 2^6 (E4M3 reaches 448).  They are held in FP16 times
+constexpr int kCfSoftmaxRegs = 168;
+constexpr int kCfOtherRegs = 88;
+static_assert((2 * kCfSoftmaxRegs + 2 * kCfOtherRegs) * 128 <= 128 * kCfThreads, "register split");
+// Base 2: how far the weights' maximum may lag.  E4M3 parts: weights stay at
+// or below 2^2, 2^8 with the factor below (E4M3 reaches 448).  FP16: 2^8.
+constexpr float kCfLagParts = 2.f;
+constexpr float kCfLagHalf = 8.f;
+// The parts stand for 2^6 times the weight.  They are cut from an FP16 value
 // 2^-8 of that: FP16's exponent field then is E4M3's, subnormals included, and
-// the parts come by masks and shifts (E4M3 conversions run at an eighth of
-// their rate: five to a pair of weights took 5100 cycles a tile).
+// the parts come by masks and shifts.
 constexpr float kCfFactor = -2.f;
 constexpr float kCfCodeUnit = 256.f;
-// A CTA's share is at least this many tiles: a shorter one would not pay for its joining.
-constexpr int kCfMinTiles = 4;
+// In tiles: what a job costs besides its tiles, and the least worth a CTA.
+constexpr int kCfJobCost = 4;
+constexpr int kCfMinShare = 8;
 
 struct alignas(16) CfPiece {
   int32_t r, rt, kvh;   // request, row tile (pair), KV head
@@ -110,20 +128,22 @@ struct alignas(16) CfPiece {
   int32_t pad0, pad1;
 };
 
+template <bool kWide>
 struct CfBars {
-  uint64_t full[kCfSlots], empty[kCfSlots];
+  uint64_t full[CfShape<kWide>::kSlots], empty[CfShape<kWide>::kSlots];
   uint64_t sc_full[kCfScaleSlots], sc_empty[kCfScaleSlots];
-  uint64_t q_full[2];
-  uint64_t q_empty;               // !kWide: the other half is done with the queries
-  uint64_t join_full, join_free;  // !kWide: the join's buffer is written, is read
+  uint64_t q_full[2], q_empty[2];  // per row tile, or buffer
+  uint64_t v16_full[kCfV16Stages], v16_empty[kCfV16Stages];
+  uint64_t join_full, join_free;   // !kWide: the join's buffer is written, is read
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2][2];
-  uint64_t o_done[2][2];
+  uint64_t o_done[2][2];           // (two: nobody waits for each of them in turn)
   uint64_t u_full[2], u_empty[2];
   CfPiece piece[2];
   uint32_t tmem_base;
 };
-static_assert(sizeof(CfBars) <= 832 && offsetof(CfBars, piece) % 16 == 0, "barrier area");
+static_assert(sizeof(CfBars<true>) <= 896 && offsetof(CfBars<true>, piece) % 16 == 0, "barrier area");
+static_assert(sizeof(CfBars<false>) <= 896 && offsetof(CfBars<false>, piece) % 16 == 0, "barrier area");
 
 template <int kRegs>
 __device__ __forceinline__ void cf_regs_up() {
@@ -177,6 +197,25 @@ __device__ __forceinline__ float cf_sigma(uint32_t amax_bits) {
   return __int_as_float((127 + min(max(7 - e, -120), 120)) << 23);
 }
 
+// 16 E4M3 codes as FP16 (exact).
+__device__ __forceinline__ void cf_to_half(const uint4& c, uint4& a, uint4& b) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint16_t pair = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(pair));
+  }
+  a = make_uint4(h[0], h[1], h[2], h[3]);
+  b = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+__device__ __forceinline__ uint32_t cf_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Tiles of keys that a row tile of a request reads.
 __device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int64_t pair, int n_rt, int pos) {
   const int r = static_cast<int>(pair / n_rt);
@@ -190,26 +229,34 @@ template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kCfThreads, 1)
     paged_chunk_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                               const ChunkScaledArgs a) {
+  using S = CfShape<kWide>;
+  constexpr uint32_t kSlots = S::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
-  auto* bars = reinterpret_cast<CfBars*>(smem + kCfOffBar);
+  auto* bars = reinterpret_cast<CfBars<kWide>*>(smem + S::kOffBar);
   auto uniform = [](int x) -> int { return __shfl_sync(0xffffffffu, x, 0); };
   const int warp = uniform(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  constexpr int kQWarps = kWide ? kCfHelpers : kCfHelpers - 1;  // that write the query operand
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kCfSlots; ++s) {
+    for (uint32_t s = 0; s < kSlots; ++s) {
       mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], kWide ? 2 : 1);
+      // K (even places): both issuers, or the half's; V: the converting warps, or the half's
+      mbar_init(&bars->empty[s], kWide ? ((s & 1) ? kCfHelpers : 2) : 1);
     }
     for (int s = 0; s < kCfScaleSlots; ++s) {
       mbar_init(&bars->sc_full[s], 1);
       mbar_init(&bars->sc_empty[s], kWide ? 8 : 4);
     }
-    mbar_init(&bars->q_empty, 5);  // warps 4-7, the second MMA issuer
+    for (int s = 0; s < kCfV16Stages; ++s) {
+      mbar_init(&bars->v16_full[s], kCfHelpers);
+      mbar_init(&bars->v16_empty[s], 2);
+    }
     mbar_init(&bars->join_full, 256);
     mbar_init(&bars->join_free, 256);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->q_full[t], 128);
+      mbar_init(&bars->q_full[t], kQWarps);
+      mbar_init(&bars->q_empty[t], kWide ? 5 : 10);  // the softmax warps and issuers that use it
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->s_free[t], 128);
       for (int b = 0; b < 2; ++b) {
@@ -217,7 +264,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         mbar_init(&bars->o_done[t][b], 1);
       }
       mbar_init(&bars->u_full[t], 1);
-      mbar_init(&bars->u_empty[t], 11);  // every other warp
+      mbar_init(&bars->u_empty[t], 15);  // every other warp
     }
     fence_barrier_init();
   }
@@ -261,32 +308,36 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     u.n = uniform(y.y);
     return u.n > 0;
   };
+  // The query buffer of the k-th piece for row tile t, and its phase there.
+  auto q_slot = [](uint32_t k, int t) -> uint32_t { return kWide ? t : k & 1; };
+  auto q_phase = [](uint32_t k) -> uint32_t { return kWide ? k & 1 : (k >> 1) & 1; };
   // tiles of the piece that half t works on
   auto tiles_of = [&](const CfPiece& u, int t) -> int { return kWide ? u.take : (u.take - t + 1) >> 1; };
 
   if (warp >= 8) {
-    cf_regs_down<kCfIssueRegs>();
+    cf_regs_down<kCfOtherRegs>();
     if (warp == 11) {
       // ------------------------ pieces and scales ------------------------
+      auto cost = [](int tiles) -> int64_t { return tiles > 0 ? tiles + kCfJobCost : 0; };
       int64_t total = 0;
-      for (int64_t p = lane; p < pairs; p += 32) total += cf_tiles(a, p, n_rt, kPos);
+      for (int64_t p = lane; p < pairs; p += 32) total += cost(cf_tiles(a, p, n_rt, kPos));
       if (blockIdx.x == 0)
         for (int r = lane; r < a.num_seqs; r += 32)
           if (a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
       total *= a.num_kv_heads;
-      const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kCfMinTiles));
+      const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kCfMinShare));
       const int64_t t0 = per * blockIdx.x;
-      int64_t left = min(per, total - t0);  // tiles of this CTA (<= 0: none)
-      // the job that tile t0 belongs to
-      int64_t pair = 0;
-      int n = 0, kvh = 0, begin = 0;
+      int64_t left = min(per, total - t0);  // of this CTA's share (<= 0: none)
+      // the job that the share starts in, and how far into its cost
+      int64_t pair = 0, into = 0;
+      int n = 0, kvh = 0;
       if (left > 0) {
         int64_t before = 0;
         for (int64_t p0 = 0;; p0 += 32) {
           const int x = p0 + lane < pairs ? cf_tiles(a, p0 + lane, n_rt, kPos) : 0;
-          int64_t upto = static_cast<int64_t>(x) * a.num_kv_heads;
+          int64_t upto = cost(x) * a.num_kv_heads;
 #pragma unroll
           for (int off = 1; off < 32; off <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
@@ -296,10 +347,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           if (past != 0) {
             const int at = __ffs(past) - 1;
             n = __shfl_sync(0xffffffffu, x, at);
-            const int64_t start = before + __shfl_sync(0xffffffffu, upto, at) - static_cast<int64_t>(n) * a.num_kv_heads;
+            const int64_t start = before + __shfl_sync(0xffffffffu, upto, at) - cost(n) * a.num_kv_heads;
             pair = p0 + at;
-            kvh = static_cast<int>((t0 - start) / n);
-            begin = static_cast<int>((t0 - start) - static_cast<int64_t>(kvh) * n);
+            kvh = static_cast<int>((t0 - start) / cost(n));
+            into = (t0 - start) - kvh * cost(n);
             break;
           }
           before += __shfl_sync(0xffffffffu, upto, 31);
@@ -310,8 +361,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         cut.r = static_cast<int32_t>(pair / n_rt);
         cut.rt = static_cast<int32_t>(pair - static_cast<int64_t>(cut.r) * n_rt);
         cut.kvh = kvh;
-        cut.begin = begin;
         cut.n = n;
+        cut.into = into;
         cut.per = per;
         a.cuts[blockIdx.x] = cut;
       }
@@ -343,7 +394,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             if (tiles >= kCfScaleSlots)
               ok = __all_sync(0xffffffffu, mbar_wait(&bars->sc_empty[slot], ((tiles / kCfScaleSlots) & 1) ^ 1));
             if (!ok) break;
-            float* dst = reinterpret_cast<float*>(smem + kCfOffScale) + slot * kCfScaleFloats + lane % kCfTileBlocks;
+            float* dst = reinterpret_cast<float*>(smem + S::kOffScale) + slot * kCfScaleFloats + lane % kCfTileBlocks;
             if (lane / kCfTileBlocks == k) {
               dst[0] = ks;
               dst[kCfTileBlocks] = lv;
@@ -360,16 +411,21 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       for (uint32_t round = 0;; ++round) {
         was = now;
         now = CfPiece{};
-        if (left > 0) {
-          now.r = static_cast<int32_t>(pair / n_rt);
-          now.rt = static_cast<int32_t>(pair - static_cast<int64_t>(now.r) * n_rt);
-          now.kvh = kvh;
-          now.begin = begin;
-          now.take = static_cast<int32_t>(min(left, static_cast<int64_t>(n - begin)));
-          now.n = n;
-          left -= now.take;
-          begin = 0;
-          if (++kvh == a.num_kv_heads) {  // (used only if tiles are left: the next job then starts here)
+        while (left > 0 && now.n == 0) {
+          const int64_t end = min(into + left, cost(n));
+          const int begin = static_cast<int>(max(into - kCfJobCost, int64_t{0}));
+          const int take = static_cast<int>(max(end - kCfJobCost, int64_t{0})) - begin;
+          if (take > 0) {  // (none: the share ends before the job's first tile)
+            now.r = static_cast<int32_t>(pair / n_rt);
+            now.rt = static_cast<int32_t>(pair - static_cast<int64_t>(now.r) * n_rt);
+            now.kvh = kvh;
+            now.begin = begin;
+            now.take = take;
+            now.n = n;
+          }
+          left -= end - into;
+          into = 0;
+          if (++kvh == a.num_kv_heads) {  // (the next job starts here, if anything is left)
             kvh = 0;
             for (++pair; left > 0 && pair < pairs && (n = cf_tiles(a, pair, n_rt, kPos)) == 0; ++pair) {
             }
@@ -387,13 +443,14 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         if (!ok || now.n == 0) break;
       }
       if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
-    } else if (warp == 8) {
-      // ---------------------------- TMA producer ----------------------------
-      // K of a tile: lanes 0-3, V: lanes 4-7.
+    } else if (warp == 8 || (!kWide && warp == 12)) {
+      // ---------------------------- TMA producers ----------------------------
+      // kWide: K of a tile in lanes 0-3, V in lanes 4-7.
       // read once, unless several row tiles of the request read the same blocks
       const uint64_t policy = n_rt > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
       const int oob_row = a.num_blocks * a.num_kv_heads * kBlockSize;  // first row past the pool
-      const bool is_v = lane >= kCfTileBlocks;
+      const bool is_v = kWide ? lane >= kCfTileBlocks : warp == 12;
+      constexpr int kLanes = kWide ? 2 * kCfTileBlocks : kCfTileBlocks;
       uint32_t filled = 0;  // tiles so far
       CfPiece u;
       while (next_piece(u)) {
@@ -417,72 +474,198 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           const int y = __shfl_sync(0xffffffffu, cur, in_group * kCfTileBlocks + lane % kCfTileBlocks);
           if (in_group == kCfGroupTiles - 1) cur = row_of(kCfTileBlocks * (j + 1) + lane, next);
           const uint32_t place = 2 * filled + (is_v ? 1 : 0);
-          const uint32_t slot = place % kCfSlots;
+          const uint32_t slot = place % kSlots;
           bool mine = true;
-          if (place >= kCfSlots) mine = mbar_wait(&bars->empty[slot], ((place / kCfSlots) & 1) ^ 1);
+          if (place >= kSlots) mine = mbar_wait(&bars->empty[slot], ((place / kSlots) & 1) ^ 1);
           ok = __all_sync(0xffffffffu, mine);
           if (!ok) break;
-          if (lane == 0 || lane == kCfTileBlocks) mbar_arrive_expect_tx(&bars->full[slot], kCfTileBytes);
+          if (lane < kLanes && lane % kCfTileBlocks == 0) mbar_arrive_expect_tx(&bars->full[slot], kCfTileBytes);
           __syncwarp();
-          if (lane < 2 * kCfTileBlocks)
-            tc::tma_load_2d(smem + kCfOffRing + slot * kCfTileBytes + lane % kCfTileBlocks * kCfBoxBytes, is_v ? &v_map : &k_map, 0,
-                            y, &bars->full[slot], policy);
+          if (lane < kLanes)
+            tc::tma_load_2d(smem + S::kOffRing + slot * kCfTileBytes + lane % kCfTileBlocks * kCfBoxBytes,
+                            is_v ? &v_map : &k_map, 0, y, &bars->full[slot], policy);
         }
         if (!ok) break;
       }
-      if (lane == 0 && !ok) {
+      if (lane < kLanes && lane % kCfTileBlocks == 0 && !ok) {
         report(a.err, PKV_DEVERR_TIMEOUT);
         // copies under way must land before shared memory is released
-        for (uint32_t f = 2 * filled > kCfSlots ? 2 * filled - kCfSlots : 0; f < 2 * filled; ++f)
-          mbar_wait(&bars->full[f % kCfSlots], (f / kCfSlots) & 1);
+        for (uint32_t f = filled > kSlots / 2 ? filled - kSlots / 2 : 0; f < filled; ++f) {
+          const uint32_t place = 2 * f + (is_v ? 1 : 0);
+          mbar_wait(&bars->full[place % kSlots], (place / kSlots) & 1);
+        }
       }
+      __syncwarp();
+    } else if (warp >= 12) {
+      // ---------------- the query operand; kWide: V to FP16 ----------------
+      const int who = warp - (16 - kQWarps);
+      const int c16 = lane & 7;  // 8 lanes a row, 16 dims each
+      // the queries of piece u (its number in the walk: k), 4 rows an iteration
+      auto queries = [&](const CfPiece& u, uint32_t k) {
+        for (int t = 0; t < (kWide ? 2 : 1) && ok; ++t) {
+          const uint32_t buf = q_slot(k, t);
+          const uint32_t uses = kWide ? k : k >> 1;  // of the buffer before
+          if (uses > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty[buf], (uses & 1) ^ 1));
+          if (!ok) break;
+          const int pos0 = u.rt * kPos + t * kCfPos;
+          const int live_rows = max(min(pos0 + kCfPos, a.q_len) - pos0, 0) * kGroup;
+          uint8_t* qa = smem + S::kOffQ + buf * 2 * kCfPartBytes;
+          float* inv_sigma = reinterpret_cast<float*>(smem + S::kOffSigma) + buf * kCfRows;
+          constexpr int kIters = kRows / 4;
+          for (int i0 = who; i0 < kIters && 4 * i0 < live_rows; i0 += 4 * kQWarps) {
+            uint4 w[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int m = 4 * (i0 + i * kQWarps) + (lane >> 3);
+              w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+              if (m < live_rows) {
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(a.q) +
+                    ((static_cast<int64_t>(u.r) * a.q_len + pos0 + (m >> 2)) * hq + u.kvh * kGroup + (m & 3)) * kHeadDim +
+                    16 * c16);
+                w[i][0] = src[0];
+                w[i][1] = src[1];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int m = 4 * (i0 + i * kQWarps) + (lane >> 3);
+              if (4 * (i0 + i * kQWarps) >= kRows) break;
+              const uint32_t wv[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w,
+                                      w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+              uint32_t amax = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) amax = max(amax, max(wv[e] & 0x7fffu, (wv[e] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+              const float sigma = cf_sigma(amax);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t h0, l0, h1, l1;
+                cf_parts(bf16_lo(wv[2 * e]) * sigma, bf16_hi(wv[2 * e]) * sigma, h0, l0);
+                cf_parts(bf16_lo(wv[2 * e + 1]) * sigma, bf16_hi(wv[2 * e + 1]) * sigma, h1, l1);
+                hi[e] = h0 | (h1 << 16);
+                lo[e] = l0 | (l1 << 16);
+              }
+#pragma unroll
+              for (int copy = 0; copy < kCfRows / kRows; ++copy) {
+                const uint32_t at = tc::sw128_offset_b8(m + copy * kRows, 16 * c16);
+                *reinterpret_cast<uint4*>(qa + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(qa + kCfPartBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (c16 == 0) inv_sigma[m + copy * kRows] = a.scale_log2 / sigma;
+              }
+            }
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->q_full[buf]);
+        }
+      };
+      uint32_t k = 0;     // pieces so far
+      uint32_t tile = 0;  // kWide: V tiles so far
+      CfPiece u;
+      while (next_piece(u)) {
+        queries(u, k);
+        ++k;
+        if constexpr (kWide) {
+          const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
+          for (int j = 0; j < u.take && ok; ++j, ++tile) {
+            const uint32_t place = 2 * tile + 1, slot = place % kSlots, st = tile % kCfV16Stages;
+            bool there = mbar_wait(&bars->full[slot], (place / kSlots) & 1);
+            if (tile >= kCfV16Stages)
+              there = there && mbar_wait(&bars->v16_empty[st], ((tile / kCfV16Stages) & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, there);
+            if (!ok) break;
+            const uint8_t* raw = smem + S::kOffRing + slot * kCfTileBytes;
+            uint8_t* half = smem + S::kOffExtra + st * kCfV16Bytes;
+            const int end = ctx - (u.begin + j) * kCfTokens;  // rows from here on hold nothing: zeros
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // 16 codes a lane, 4 rows a warp
+              const int row = who * 16 + 4 * i + (lane >> 3);
+              uint4 code = *reinterpret_cast<const uint4*>(raw + row * 128 + ((c16 ^ (row & 7)) << 4));
+              if (row >= end) code = make_uint4(0, 0, 0, 0);
+              uint4 h[2];
+              cf_to_half(code, h[0], h[1]);
+              // 64-dim half c16 / 4; the halves' lanes store in opposite order (banks)
+              uint8_t* dst = half + (c16 >> 2) * kCfTileBytes + row * 128;
+              const int o = c16 >> 2;
+              const int ch = 2 * (c16 & 3);
+              *reinterpret_cast<uint4*>(dst + (((ch + o) ^ (row & 7)) << 4)) = o ? h[1] : h[0];
+              *reinterpret_cast<uint4*>(dst + (((ch + 1 - o) ^ (row & 7)) << 4)) = o ? h[0] : h[1];
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bars->empty[slot]);
+              mbar_arrive(&bars->v16_full[st]);
+            }
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
       __syncwarp();
     } else {
       // ---------------------------- MMA issuers ----------------------------
       constexpr uint32_t kIdS = tc::idesc_e4m3_f32(kCfRows, kCfTokens, false, false);
-      constexpr uint32_t kIdO = tc::idesc_e4m3_f32(kCfRows, kHeadDim, false, true);
+      constexpr uint32_t kIdO = kWide ? tc::idesc_f16_f32(kCfRows, kHeadDim, false, true)
+                                      : tc::idesc_e4m3_f32(kCfRows, kHeadDim, false, true);
       const int t = warp - 9;
       const bool leader = lane == 0;
       const uint32_t scol = tmem + t * kCfTileCols;
-      const uint64_t q_desc = tc::smem_desc(sbase + kCfOffQ + (kWide ? t * 2 * kCfPartBytes : 0), 16, 1024);
-      const uint64_t ring = tc::smem_desc(sbase + kCfOffRing, 16, 1024);
+      const uint64_t q_desc = tc::smem_desc(sbase + S::kOffQ, 16, 1024);
+      const uint64_t ring = tc::smem_desc(sbase + S::kOffRing, 16, 1024);
+      const uint64_t v16 = tc::smem_desc(sbase + S::kOffExtra, kCfTileBytes, 1024);
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
-      auto wait_full = [&](uint32_t place) -> bool { return wait(&bars->full[place % kCfSlots], (place / kCfSlots) & 1); };
-      // a place of the ring and another barrier, both tried before either result is looked at
-      auto wait_both = [&](uint32_t place, uint64_t* y, uint32_t yp) -> bool {
-        uint64_t* x = &bars->full[place % kCfSlots];
-        const uint32_t xp = (place / kCfSlots) & 1;
+      auto wait_full = [&](uint32_t place) -> bool { return wait(&bars->full[place % kSlots], (place / kSlots) & 1); };
+      // two barriers, both tried before either result is looked at
+      auto wait2 = [&](uint64_t* x, uint32_t xp, uint64_t* y, uint32_t yp) -> bool {
         const bool rx = mbar_try_wait(x, xp), ry = mbar_try_wait(y, yp);
         return __all_sync(0xffffffffu, (rx || mbar_wait(x, xp)) && (ry || mbar_wait(y, yp)));
       };
       // Stages go back by plain arrivals once a later wait has shown that the
       // products that read them are done.
       auto give_back = [&](uint32_t place) {
-        if (leader) mbar_arrive(&bars->empty[place % kCfSlots]);
+        if (leader) mbar_arrive(&bars->empty[place % kSlots]);
+      };
+      auto give_back_v = [&](uint32_t place, uint32_t tile) {  // (kWide: the converted tile)
+        if (!kWide) {
+          give_back(place);
+        } else if (leader) {
+          mbar_arrive(&bars->v16_empty[tile % kCfV16Stages]);
+        }
       };
       // S = (high + low parts of the queries) K^T
-      auto issue_s = [&](uint32_t place) {
-        const uint64_t kd = ring + (place % kCfSlots) * (kCfTileBytes >> 4);
+      auto issue_s = [&](uint32_t place, uint32_t buf, bool last) {
+        const uint64_t qd = q_desc + buf * (2 * kCfPartBytes >> 4);
+        const uint64_t kd = ring + (place % kSlots) * (kCfTileBytes >> 4);
         tc::fence_after_sync();
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_f8(scol, q_desc + (((kk >> 2) * kCfPartBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
+            tc::mma_f8(scol, qd + (((kk >> 2) * kCfPartBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
                        kk > 0 ? 1u : 0u);
           tc::commit(&bars->s_full[t]);
+          if (last) tc::commit(&bars->q_empty[buf]);  // other queries may come
         }
         __syncwarp();
       };
-      // O += (high + low parts of the weights) V
-      auto issue_pv = [&](uint32_t place, uint32_t buf, bool first) {
-        const uint64_t vd = ring + (place % kCfSlots) * (kCfTileBytes >> 4);
+      // O += P V: FP16, or (high + low parts of the weights) V's codes
+      auto issue_pv = [&](uint32_t place, uint32_t tile, uint32_t buf, bool first) {
+        const uint64_t vd = kWide ? v16 + (tile % kCfV16Stages) * (kCfV16Bytes >> 4)
+                                  : ring + (place % kSlots) * (kCfTileBytes >> 4);
         const uint32_t pcol = scol + kCfColP + buf * kCfPCols;
         tc::fence_after_sync();
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (kWide) {  // 16 keys
+              tc::mma_bf16_tmem_a(scol + kCfColO, pcol + 8 * kk, vd + kk * (2048 >> 4), kIdO, (!first || kk > 0) ? 1u : 0u);
+              continue;
+            }
             const int slice = kk & 1;  // of 32 keys
             mma_f8_tmem_a(scol + kCfColO, pcol + kCfColLow * (kk >> 1) + 8 * slice, vd + slice * (4096 >> 4), kIdO,
                           (!first || kk > 0) ? 1u : 0u);
@@ -500,31 +683,36 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         const int n_t = tiles_of(u, t);
         uint32_t c = c0 + (kWide ? 0 : 2 * t);  // place of the present tile's K; its V is at c + 1
         c0 += 2 * u.take;
-        ok = wait(&bars->q_full[kWide ? t : 0], pieces & 1);
+        const uint32_t qb = q_slot(pieces, t);
+        ok = wait(&bars->q_full[qb], q_phase(pieces));
         ++pieces;
         if (ok && n_t > 0) {
           ok = wait_full(c);
-          if (ok) issue_s(c);
+          if (ok) issue_s(c, qb, n_t == 1);
         }
         for (int j = 0; j < n_t && ok; ++j, ++g, c += kStep) {
           // The scores are in registers.  (They were committed after the
           // product of two tiles before, so that is done too.)
-          ok = j + 1 < n_t ? wait_both(c + kStep, &bars->s_free[t], g & 1) : wait(&bars->s_free[t], g & 1);
+          const uint32_t ahead = c + kStep;
+          ok = j + 1 < n_t ? wait2(&bars->full[ahead % kSlots], (ahead / kSlots) & 1, &bars->s_free[t], g & 1)
+                           : wait(&bars->s_free[t], g & 1);
           if (!ok) break;
           give_back(c);
-          if (j >= 2) give_back(c + 1 - 2 * kStep);
-          if (j + 1 < n_t) issue_s(c + kStep);
-          ok = wait_both(c + 1, &bars->p_full[t][g & 1], (g >> 1) & 1);
+          if (j >= 2) give_back_v(c + 1 - 2 * kStep, g - 2);
+          if (j + 1 < n_t) issue_s(ahead, qb, j + 2 == n_t);
+          const uint32_t vp = c + 1;
+          ok = kWide ? wait2(&bars->v16_full[g % kCfV16Stages], (g / kCfV16Stages) & 1, &bars->p_full[t][g & 1], (g >> 1) & 1)
+                     : wait2(&bars->full[vp % kSlots], (vp / kSlots) & 1, &bars->p_full[t][g & 1], (g >> 1) & 1);
           if (!ok) break;
-          issue_pv(c + 1, g & 1, j == 0);
+          issue_pv(vp, g, g & 1, j == 0);
         }
         // the last two tiles' V, once their products are done
         for (int back = min(n_t, 2); back > 0 && ok; --back) {
           ok = wait(&bars->o_done[t][(g - back) & 1], ((g - back) >> 1) & 1);
-          if (ok) give_back(c + 1 - back * kStep);
+          if (ok) give_back_v(c + 1 - back * kStep, g - back);
         }
         if (!ok) break;
-        if (!kWide && t == 1 && leader) mbar_arrive(&bars->q_empty);
+        if (n_t == 0 && leader) mbar_arrive(&bars->q_empty[qb]);
       }
       if (!ok && leader) report(a.err, PKV_DEVERR_TIMEOUT);
       __syncwarp();
@@ -536,7 +724,6 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     const int quad = warp & 3;  // TMEM sub-partition of this warp
     const int row = quad * 32 + lane;
     const uint32_t scol = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * kCfTileCols;
-    float* inv_sigma = reinterpret_cast<float*>(smem + kCfOffSigma) + (kWide ? t * kCfRows : 0);
     const int row_tile = kWide ? t : 0;  // row tile of this warpgroup's rows
 
     // rows that see no key at all belong to no piece: zeros
@@ -570,70 +757,15 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       const int first_key = ctx - a.q_len + pos0 + 1;    // keys that query 0 of the row tile sees
       const int seen = first_key + (qrow >> 2);          // that this row sees (<= 0: none)
       const int warp_seen = first_key + (warp_row >> 2);  // its warp's first row
-      // ---- the query operand: 8 lanes a row, 16 dims each ----
-      if (kWide || t == 0) {
-        uint8_t* qa = smem + kCfOffQ + row_tile * 2 * kCfPartBytes;
-        if (!kWide && pieces > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (pieces & 1) ^ 1));
-          if (!ok) break;
-        }
-        const int c16 = lane & 7;
-#pragma unroll
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-          if (!warp_live) break;
-          uint4 w[4][2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = warp_row + 4 * (i0 + i) + (lane >> 3);
-            w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-            if (m < live_rows) {
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  static_cast<const uint16_t*>(a.q) +
-                  ((static_cast<int64_t>(u.r) * a.q_len + pos0 + (m >> 2)) * hq + u.kvh * kGroup + (m & 3)) * kHeadDim +
-                  16 * c16);
-              w[i][0] = src[0];
-              w[i][1] = src[1];
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = quad * 32 + 4 * (i0 + i) + (lane >> 3);
-            const uint32_t wv[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w,
-                                    w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
-            uint32_t amax = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = max(amax, max(wv[e] & 0x7fffu, (wv[e] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            const float sigma = cf_sigma(amax);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t h0, l0, h1, l1;
-              cf_parts(bf16_lo(wv[2 * k]) * sigma, bf16_hi(wv[2 * k]) * sigma, h0, l0);
-              cf_parts(bf16_lo(wv[2 * k + 1]) * sigma, bf16_hi(wv[2 * k + 1]) * sigma, h1, l1);
-              hi[k] = h0 | (h1 << 16);
-              lo[k] = l0 | (l1 << 16);
-            }
-            const uint32_t at = tc::sw128_offset_b8(m, 16 * c16);
-            *reinterpret_cast<uint4*>(qa + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(qa + kCfPartBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (c16 == 0) inv_sigma[m] = a.scale_log2 / sigma;
-          }
-        }
-        tc::fence_proxy_async_smem();
-        mbar_arrive(&bars->q_full[row_tile]);
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[row_tile], pieces & 1));
+      const uint32_t qb = q_slot(pieces, t);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[qb], q_phase(pieces)));
       ++pieces;
       if (!ok) break;
-      const float c = inv_sigma[row];
-      if (!kWide && t == 1) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_empty);
-      }
-      float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum by at most 2)
-      float l = 0.f;        // sum of w / vs, times 2^-2
+      const float c = reinterpret_cast<const float*>(smem + S::kOffSigma)[qb * kCfRows + row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_empty[qb]);
+      float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum)
+      float l = 0.f;        // sum of w / vs, in the weights' unit
       for (int j = 0; j < n_t; ++j, ++g) {
         const int in_piece = kWide ? j : 2 * j + t;
         const int tok = (u.begin + in_piece) * kCfTokens;
@@ -644,7 +776,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
                             mbar_wait(&bars->s_full[t], g & 1));
         if (!ok) break;
         // the blocks' ks, log2 vs, 1 / vs (read twice: registers are dearer)
-        const float* sc = reinterpret_cast<const float*>(smem + kCfOffScale) + sl * kCfScaleFloats + key0 / kBlockSize;
+        const float* sc = reinterpret_cast<const float*>(smem + S::kOffScale) + sl * kCfScaleFloats + key0 / kBlockSize;
         tc::fence_after_sync();
         if (warp_live) {
           float s[kCols];
@@ -686,7 +818,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             for (int e = 2; e < 16; e += 2) x = fmaxf(fmaxf(x, s[16 * b + e]), s[16 * b + e + 1]);
             mx = fmaxf(mx, fmaf(x, sc[b] * c, sc[kCfTileBlocks + b]));  // (the factor is > 0)
           }
-          const bool grow = mx > m + kCfLag;  // also true the first time a row sees a key
+          const bool grow = mx > m + (kWide ? kCfLagHalf : kCfLagParts);  // also true the first time a row sees a key
           const float m_new = grow ? mx : m;
           const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
           if (__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY)) {
@@ -708,39 +840,59 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           }
           l *= alpha;
           m = m_new;
-          const float nm = (m == -INFINITY ? 0.f : -m) + kCfFactor;
-          uint32_t hi[kCols / 4], lo[kCols / 4];
+          const float nm = (m == -INFINITY ? 0.f : -m) + (kWide ? 0.f : kCfFactor);
+          if constexpr (kWide) {
 #pragma unroll
-          for (int b = 0; b < kCols / kBlockSize; ++b) {
-            const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
-            const float2 k2 = make_float2(kc, kc);
-            const float2 n2 = make_float2(off, off);
-            float2 acc = make_float2(0.f, 0.f);
+            for (int b = 0; b < kCfTileBlocks; ++b) {
+              const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
+              const float2 k2 = make_float2(kc, kc);
+              const float2 n2 = make_float2(off, off);
+              float2 acc = make_float2(0.f, 0.f);
+              uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 16 * b + 4 * e;
-              const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), k2, n2);
-              const float2 y = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), k2, n2);
-              const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
-              const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
-              acc = __fadd2_rn(acc, make_float2(p0, p1));
-              acc = __fadd2_rn(acc, make_float2(p2, p3));
-              cf_weights(p0, p1, p2, p3, hi[4 * b + e], lo[4 * b + e]);
+              for (int e = 0; e < 8; ++e) {
+                const float2 x = __ffma2_rn(make_float2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), k2, n2);
+                const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
+                acc = __fadd2_rn(acc, make_float2(p0, p1));
+                w[e] = cf_half2(p0, p1);
+              }
+              l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
+              tc::tmem_st8(pcol + 8 * b, w);
             }
-            l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
-          }
-          store(pcol + copy * (kCols / 4), hi);
-          store(pcol + kCfColLow + copy * (kCols / 4), lo);
-          if (ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
-            // slots past the context may hold any code: V's rows there are
-            // zeroed (a weight of zero is not enough)
-            const uint32_t vp = 2 * (tile0 + in_piece) + 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kCfSlots], (vp / kCfSlots) & 1));
-            if (!ok) break;
-            const int z0 = ctx - tok, z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
-            uint8_t* vt = smem + kCfOffRing + (vp % kCfSlots) * kCfTileBytes;
-            for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) reinterpret_cast<uint4*>(vt)[i] = make_uint4(0, 0, 0, 0);
-            tc::fence_proxy_async_smem();
+          } else {
+            uint32_t hi[kCols / 4], lo[kCols / 4];
+#pragma unroll
+            for (int b = 0; b < kCols / kBlockSize; ++b) {
+              const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
+              const float2 k2 = make_float2(kc, kc);
+              const float2 n2 = make_float2(off, off);
+              float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = 16 * b + 4 * e;
+                const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), k2, n2);
+                const float2 y = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), k2, n2);
+                const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
+                const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
+                acc = __fadd2_rn(acc, make_float2(p0, p1));
+                acc = __fadd2_rn(acc, make_float2(p2, p3));
+                cf_weights(p0, p1, p2, p3, hi[4 * b + e], lo[4 * b + e]);
+              }
+              l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
+            }
+            store(pcol + copy * (kCols / 4), hi);
+            store(pcol + kCfColLow + copy * (kCols / 4), lo);
+            if (ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
+              // slots past the context may hold any code: V's rows there are
+              // zeroed (a weight of zero is not enough)
+              const uint32_t vp = 2 * (tile0 + in_piece) + 1;
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[vp % kSlots], (vp / kSlots) & 1));
+              if (!ok) break;
+              const int z0 = ctx - tok, z1 = (z0 + kBlockSize - 1) & ~(kBlockSize - 1);
+              uint8_t* vt = smem + S::kOffRing + (vp % kSlots) * kCfTileBytes;
+              for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) reinterpret_cast<uint4*>(vt)[i] = make_uint4(0, 0, 0, 0);
+              tc::fence_proxy_async_smem();
+            }
           }
           tc::tmem_wait_st();
           tc::fence_before_sync();
@@ -754,7 +906,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       }
       tile0 += u.take;
       if (!ok) break;
-      l *= kCfCodeUnit;  // in O's unit
+      if (!kWide) l *= kCfCodeUnit;  // in O's unit
       // ---- results ----
       if (n_t > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
@@ -799,7 +951,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         // pass.  A thread joins 4 dims of up to kTake rows.
         constexpr int kParts = 2 * kCopies;  // partials of a row
         constexpr int kTake = kRows / 32;
-        float4* buf = reinterpret_cast<float4*>(smem + kCfOffJoin);
+        float4* buf = reinterpret_cast<float4*>(smem + S::kOffExtra);
         const int who = t * kCfRows + row;
         auto written = [&]() -> bool {  // everyone's part of a pass is there
           mbar_arrive(&bars->join_full);
@@ -902,24 +1054,32 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a
   pdl_trigger();
   const int i = blockIdx.x + 1;
   const CfCut cut = a.cuts[i];
-  if (cut.begin == 0) return;  // no cut here
-  const int64_t start = cut.per * i - cut.begin;  // the job's first tile
+  if (cut.into == 0) return;                      // no cut here
+  const int64_t start = cut.per * i - cut.into;   // where the job's cost begins
   if (start / cut.per != i - 1) return;           // cut earlier already
-  const int pieces = static_cast<int>((start + cut.n - 1) / cut.per) - (i - 1) + 1;
+  const int pieces = static_cast<int>((start + cut.n + kCfJobCost - 1) / cut.per) - (i - 1) + 1;
+  // tiles of the job's k-th piece, in CTA i - 1 + k
+  auto tile_at = [&](int64_t cta) -> int {
+    return static_cast<int>(min(max(cta * cut.per - start - kCfJobCost, int64_t{0}), static_cast<int64_t>(cut.n)));
+  };
+  if (tile_at(i) == 0 && pieces == 2) return;     // the cut fell before its first tile: one piece
   const int lane = threadIdx.x & 31;
   const int rows = min(pos, a.q_len - cut.rt * pos) * kGroup;
   const int hq = a.num_kv_heads * kGroup;
   for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.y * 8) {
-    // the first piece lies in the second place of CTA i - 1, the others in the first of their CTAs
-    auto at = [&](int k) -> int64_t { return static_cast<int64_t>(2 * (i - 1 + k) + (k == 0 ? 1 : 0)) * a.rows_slot + row; };
+    // a piece that begins the job lies in the second place of its CTA, others in the first
+    const int first = tile_at(i) == 0 ? 1 : 0;
+    auto at = [&](int k) -> int64_t {
+      return static_cast<int64_t>(2 * (i - 1 + k) + (k == first ? 1 : 0)) * a.rows_slot + row;
+    };
     float m = -INFINITY;
-    for (int k = lane; k < pieces; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
+    for (int k = first + lane; k < pieces; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
+    for (int k = first; k < pieces; ++k) {
       const int64_t p = at(k);
       const float2 ml = a.part_ml[p];
       const float4 x = *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + 4 * lane);
@@ -947,7 +1107,7 @@ cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t strea
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CfShape<kWide>::kSmem);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
@@ -955,7 +1115,8 @@ cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t strea
   CUtensorMap kmap, vmap;
   if (!make_pool_map_e4m3(&kmap, a.k_cache, rows) || !make_pool_map_e4m3(&vmap, a.v_cache, rows))
     return cudaErrorInvalidValue;
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), kCfSmem, stream, 1, kmap, vmap, a);
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), CfShape<kWide>::kSmem, stream,
+                 1, kmap, vmap, a);
   if (e != cudaSuccess || grid == 1) return e;
   // 8 rows a block at a time; a job of few rows is joined by one block
   const int32_t pos = kWide ? 2 * kCfPos : kCfPos;
@@ -970,8 +1131,8 @@ bool cf_wide(int32_t q_len) { return q_len > kCfPos; }
 int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t sm_count) {
   const int32_t pos = cf_wide(q_len) ? 2 * kCfPos : kCfPos;
   const int64_t jobs = static_cast<int64_t>(num_seqs) * num_kv_heads * ((q_len + pos - 1) / pos);
-  const int64_t tiles = jobs * ((max_blocks + kCfTileBlocks - 1) / kCfTileBlocks);  // at most
-  return static_cast<int32_t>(std::min<int64_t>(sm_count, (tiles + kCfMinTiles - 1) / kCfMinTiles));
+  const int64_t cost = jobs * ((max_blocks + kCfTileBlocks - 1) / kCfTileBlocks + kCfJobCost);  // at most
+  return static_cast<int32_t>(std::min<int64_t>(sm_count, (cost + kCfMinShare - 1) / kCfMinShare));
 }
 
 int32_t chunk_scaled_rows(int32_t q_len) { return cf_wide(q_len) ? 2 * kCfRows : kGroup * q_len; }

@@ -290,11 +290,11 @@ cudaError_t launch_copy_blocks_scaled(uint8_t* k_cache, uint8_t* v_cache, float*
                                       const int32_t* dst, int32_t num_pairs, unsigned int* err, cudaStream_t stream);
 
 // Attention of several queries per request over such pools (paged_chunk_fp8_tc.cu).
-struct CfCut {  // where a CTA's share of the tiles starts, for the joining kernel
+struct CfCut {  // where a CTA's share of the work starts, for the joining kernel
   int32_t r, rt, kvh;
-  int32_t begin, n;  // tile `begin` of the job's n
-  int32_t pad;
-  int64_t per;       // tiles of a share
+  int32_t n;     // tiles of the job
+  int64_t into;  // how far into the job's cost
+  int64_t per;   // cost of a share
 };
 struct ChunkScaledArgs {
   void* out;                    // BF16 [B][q_len][Hq][D]
