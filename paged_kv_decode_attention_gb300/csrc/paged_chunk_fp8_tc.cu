@@ -112,9 +112,8 @@ static_assert((2 * kCfSoftmaxRegs + 2 * kCfOtherRegs) * 128 <= 128 * kCfThreads,
 // or below 2^2, 2^8 with the factor below (E4M3 reaches 448).  FP16: 2^8.
 constexpr float kCfLagParts = 2.f;
 constexpr float kCfLagHalf = 8.f;
-// The parts stand for 2^6 times the weight.  They are cut from an FP16 value
-// 2^-8 of that: FP16's exponent field then is E4M3's, subnormals included, and
-// the parts come by masks and shifts.
+// The parts stand for 2^6 times the weight; they are cut from an FP16 value 2^-8
+// of that.
 constexpr float kCfFactor = -2.f;
 constexpr float kCfCodeUnit = 256.f;
 // In tiles: what a job costs besides its tiles, and the least worth a CTA.
@@ -165,21 +164,10 @@ __device__ __forceinline__ void mma_f8_tmem_a(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// Two FP32 values (the first in the low half) as FP16, as E4M3 and what that leaves as E4M3.
-__device__ __forceinline__ void cf_parts(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  uint32_t h, back;
-  uint16_t a, b;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(back));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
-  hi = a;
-  lo = b;
-}
-
-// 4 weights (0 .. 1) as the bytes of their high parts, cut to 4 significant
-// bits, and of what that leaves, rounded to 4.
+// 4 weights (0 .. 1, 2^-8 of what the parts stand for) as the bytes of their
+// high parts, cut to 4 significant bits, and of what that leaves, rounded to 4.
+// (FP16's exponent field is E4M3's here, subnormals included, so both parts
+// come by masks and shifts.)
 __device__ __forceinline__ void cf_weights(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
   uint32_t h0, h1, r0, r1;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h0) : "f"(p1), "f"(p0));
@@ -190,11 +178,28 @@ __device__ __forceinline__ void cf_weights(float p0, float p1, float p2, float p
   lo = __byte_perm(r0 * 2 + 0x00800080u, r1 * 2 + 0x00800080u, 0x7531);
 }
 
-// The power of two that brings a row's largest |q| (BF16 bits) into [2^7, 2^8); 1 for zeros.
-__device__ __forceinline__ float cf_sigma(uint32_t amax_bits) {
-  if (amax_bits == 0) return 1.f;
-  const int e = max(static_cast<int>((amax_bits >> 7) & 0xffu) - 127, -126);
-  return __int_as_float((127 + min(max(7 - e, -120), 120)) << 23);
+// The same for 4 signed values.
+__device__ __forceinline__ void cf_signed(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+  uint32_t h0, h1;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h0) : "f"(x1), "f"(x0));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h1) : "f"(x3), "f"(x2));
+  const uint32_t a0 = h0 & 0x7fff7fffu, a1 = h1 & 0x7fff7fffu;
+  uint32_t r0, r1;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(a0), "r"(a0 & 0xff80ff80u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(a1), "r"(a1 & 0xff80ff80u));
+  uint32_t sign;  // each value's sign over its byte
+  asm("prmt.b32 %0, %1, %2, 0xfdb9;" : "=r"(sign) : "r"(h0), "r"(h1));
+  sign &= 0x80808080u;
+  hi = __byte_perm(a0 << 1, a1 << 1, 0x7531) | sign;
+  lo = __byte_perm(r0 * 2 + 0x00800080u, r1 * 2 + 0x00800080u, 0x7531) | sign;
+}
+
+// sigma, the power of two that brings a row's largest |q| (BF16 bits) into
+// [2^7, 2^8), over the parts' unit, 2^8; `inv` = 1 / sigma.  1 for zeros.
+__device__ __forceinline__ float cf_sigma(uint32_t amax_bits, float& inv) {
+  const int e = amax_bits == 0 ? 7 : max(static_cast<int>(amax_bits >> 7) - 127, -113);  // (subnormals: as 2^-113)
+  inv = __int_as_float((127 + e - 7) << 23);
+  return __int_as_float((127 + 7 - e) << 23) * (1.f / kCfCodeUnit);
 }
 
 // 16 E4M3 codes as FP16 (exact).
@@ -217,9 +222,9 @@ __device__ __forceinline__ uint32_t cf_half2(float lo, float hi) {
 }
 
 // Tiles of keys that a row tile of a request reads.
-__device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int64_t pair, int n_rt, int pos) {
-  const int r = static_cast<int>(pair / n_rt);
-  const int rt = static_cast<int>(pair - static_cast<int64_t>(r) * n_rt);
+__device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int pair, int n_rt, int pos) {
+  const int r = n_rt == 1 ? pair : pair / n_rt;
+  const int rt = pair - r * n_rt;
   const int ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
   const int end = ctx - max(a.q_len - (rt + 1) * pos, 0);
   return end > 0 ? (end + kCfTokens - 1) / kCfTokens : 0;
@@ -283,8 +288,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
   pdl_trigger();
 
   constexpr int kPos = kWide ? 2 * kCfPos : kCfPos;  // positions of a piece
-  const int n_rt = (a.q_len + kPos - 1) / kPos;
-  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * n_rt;
+  const int n_rt = kWide ? (a.q_len + kPos - 1) / kPos : 1;
+  const int pairs = a.num_seqs * n_rt;
   const int hq = a.num_kv_heads * kGroup;
   const uint32_t tmem = uniform(bars->tmem_base);
   const uint32_t sbase = uniform(smem_addr(smem));
@@ -318,48 +323,54 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     cf_regs_down<kCfOtherRegs>();
     if (warp == 11) {
       // ------------------------ pieces and scales ------------------------
-      auto cost = [](int tiles) -> int64_t { return tiles > 0 ? tiles + kCfJobCost : 0; };
-      int64_t total = 0;
-      for (int64_t p = lane; p < pairs; p += 32) total += cost(cf_tiles(a, p, n_rt, kPos));
+      // (the host has seen to it that all costs together fit into 31 bits)
+      auto cost = [](int tiles) -> int { return tiles > 0 ? tiles + kCfJobCost : 0; };
+      int total = 0, first32 = 0;  // (and of the first 32 pairs, one a lane)
+      for (int p = lane; p < pairs; p += 32) {
+        const int x = cf_tiles(a, p, n_rt, kPos);
+        if (p < 32) first32 = x;
+        total += cost(x);
+      }
       if (blockIdx.x == 0)
         for (int r = lane; r < a.num_seqs; r += 32)
           if (a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-      total *= a.num_kv_heads;
-      const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kCfMinShare));
-      const int64_t t0 = per * blockIdx.x;
-      int64_t left = min(per, total - t0);  // of this CTA's share (<= 0: none)
+      total = __reduce_add_sync(0xffffffffu, total) * a.num_kv_heads;
+      const int grid = gridDim.x;
+      const int per = max((total + grid - 1) / grid, kCfMinShare);
+      const int t0 = per * static_cast<int>(blockIdx.x);
+      int left = min(per, total - t0);  // of this CTA's share (<= 0: none)
       // the job that the share starts in, and how far into its cost
-      int64_t pair = 0, into = 0;
-      int n = 0, kvh = 0;
+      int pair = 0, into = 0, n = 0, kvh = 0;
       if (left > 0) {
-        int64_t before = 0;
-        for (int64_t p0 = 0;; p0 += 32) {
-          const int x = p0 + lane < pairs ? cf_tiles(a, p0 + lane, n_rt, kPos) : 0;
-          int64_t upto = cost(x) * a.num_kv_heads;
+        int before = 0;
+        for (int p0 = 0;; p0 += 32) {
+          const int x = p0 == 0 ? first32 : (p0 + lane < pairs ? cf_tiles(a, p0 + lane, n_rt, kPos) : 0);
+          int upto = cost(x) * a.num_kv_heads;
 #pragma unroll
           for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+            const int y = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += y;
           }
           const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
           if (past != 0) {
             const int at = __ffs(past) - 1;
             n = __shfl_sync(0xffffffffu, x, at);
-            const int64_t start = before + __shfl_sync(0xffffffffu, upto, at) - cost(n) * a.num_kv_heads;
+            const int start = before + __shfl_sync(0xffffffffu, upto, at) - cost(n) * a.num_kv_heads;
             pair = p0 + at;
-            kvh = static_cast<int>((t0 - start) / cost(n));
+            kvh = (t0 - start) / cost(n);
             into = (t0 - start) - kvh * cost(n);
             break;
           }
           before += __shfl_sync(0xffffffffu, upto, 31);
         }
       }
+      auto place = [&](int& r, int& rt) {  // of the pair
+        r = n_rt == 1 ? pair : pair / n_rt;
+        rt = pair - r * n_rt;
+      };
       if (lane == 0) {  // for the joining kernel
         CfCut cut{};
-        cut.r = static_cast<int32_t>(pair / n_rt);
-        cut.rt = static_cast<int32_t>(pair - static_cast<int64_t>(cut.r) * n_rt);
+        place(cut.r, cut.rt);
         cut.kvh = kvh;
         cut.n = n;
         cut.into = into;
@@ -412,12 +423,11 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         was = now;
         now = CfPiece{};
         while (left > 0 && now.n == 0) {
-          const int64_t end = min(into + left, cost(n));
-          const int begin = static_cast<int>(max(into - kCfJobCost, int64_t{0}));
-          const int take = static_cast<int>(max(end - kCfJobCost, int64_t{0})) - begin;
+          const int end = min(into + left, cost(n));
+          const int begin = max(into - kCfJobCost, 0);
+          const int take = max(end - kCfJobCost, 0) - begin;
           if (take > 0) {  // (none: the share ends before the job's first tile)
-            now.r = static_cast<int32_t>(pair / n_rt);
-            now.rt = static_cast<int32_t>(pair - static_cast<int64_t>(now.r) * n_rt);
+            place(now.r, now.rt);
             now.kvh = kvh;
             now.begin = begin;
             now.take = take;
@@ -533,27 +543,24 @@ __global__ void __launch_bounds__(kCfThreads, 1)
               if (4 * (i0 + i * kQWarps) >= kRows) break;
               const uint32_t wv[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w,
                                       w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
-              uint32_t amax = 0;
+              uint32_t top = wv[0] & 0x7fff7fffu;  // pairs of magnitudes: BF16 bits in the order of integers
 #pragma unroll
-              for (int e = 0; e < 8; ++e) amax = max(amax, max(wv[e] & 0x7fffu, (wv[e] >> 16) & 0x7fffu));
+              for (int e = 1; e < 8; ++e) top = __vmaxu2(top, wv[e] & 0x7fff7fffu);
 #pragma unroll
-              for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-              const float sigma = cf_sigma(amax);
+              for (int off = 1; off < 8; off <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, off));
+              float inv;
+              const float f = cf_sigma(max(top & 0xffffu, top >> 16), inv);
               uint32_t hi[4], lo[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t h0, l0, h1, l1;
-                cf_parts(bf16_lo(wv[2 * e]) * sigma, bf16_hi(wv[2 * e]) * sigma, h0, l0);
-                cf_parts(bf16_lo(wv[2 * e + 1]) * sigma, bf16_hi(wv[2 * e + 1]) * sigma, h1, l1);
-                hi[e] = h0 | (h1 << 16);
-                lo[e] = l0 | (l1 << 16);
-              }
+              for (int e = 0; e < 4; ++e)
+                cf_signed(bf16_lo(wv[2 * e]) * f, bf16_hi(wv[2 * e]) * f, bf16_lo(wv[2 * e + 1]) * f,
+                          bf16_hi(wv[2 * e + 1]) * f, hi[e], lo[e]);
 #pragma unroll
               for (int copy = 0; copy < kCfRows / kRows; ++copy) {
                 const uint32_t at = tc::sw128_offset_b8(m + copy * kRows, 16 * c16);
                 *reinterpret_cast<uint4*>(qa + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4*>(qa + kCfPartBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (c16 == 0) inv_sigma[m + copy * kRows] = a.scale_log2 / sigma;
+                if (c16 == 0) inv_sigma[m + copy * kRows] = a.scale_log2 * inv;
               }
             }
           }
@@ -564,11 +571,20 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       };
       uint32_t k = 0;     // pieces so far
       uint32_t tile = 0;  // kWide: V tiles so far
-      CfPiece u;
-      while (next_piece(u)) {
+      CfPiece u, after{};
+      for (bool more = next_piece(u); more; u = after) {
         queries(u, k);
         ++k;
+        more = next_piece(after);
         if constexpr (kWide) {
+          if (more) {  // its queries towards L2: they are wanted in a hurry
+            const int pos0 = after.rt * kPos;
+            const uint16_t* q0 = static_cast<const uint16_t*>(a.q) +
+                                 ((static_cast<int64_t>(after.r) * a.q_len + pos0) * hq + after.kvh * kGroup) * kHeadDim;
+            const int lines = min(kPos, a.q_len - pos0) * (kGroup * kHeadDim * 2 / 128);
+            for (int i = who * 32 + lane; i < lines; i += kCfHelpers * 32)
+              prefetch_l2(q0 + static_cast<int64_t>(i >> 3) * hq * kHeadDim + (i & 7) * 64);
+          }
           const int ctx = min(max(a.context_lens[u.r], 0), a.max_blocks * kBlockSize);
           for (int j = 0; j < u.take && ok; ++j, ++tile) {
             const uint32_t place = 2 * tile + 1, slot = place % kSlots, st = tile % kCfV16Stages;
@@ -727,10 +743,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     const int row_tile = kWide ? t : 0;  // row tile of this warpgroup's rows
 
     // rows that see no key at all belong to no piece: zeros
-    for (int64_t p = blockIdx.x; p < pairs; p += gridDim.x) {
+    for (int p = blockIdx.x; p < pairs; p += gridDim.x) {
       if (cf_tiles(a, p, n_rt, kPos) > 0) continue;
       const int64_t r = p / n_rt;
-      const int pos0 = static_cast<int>(p - r * n_rt) * kPos;
+      const int pos0 = (p - static_cast<int>(r) * n_rt) * kPos;
       const int64_t chunks = static_cast<int64_t>(min(kPos, a.q_len - pos0)) * hq * (kHeadDim * 2 / 16);
       uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (r * a.q_len + pos0) * hq * kHeadDim);
       for (int64_t i = threadIdx.x; i < chunks; i += 256) o[i] = make_uint4(0, 0, 0, 0);
@@ -1055,13 +1071,11 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a
   const int i = blockIdx.x + 1;
   const CfCut cut = a.cuts[i];
   if (cut.into == 0) return;                      // no cut here
-  const int64_t start = cut.per * i - cut.into;   // where the job's cost begins
+  const int start = cut.per * i - cut.into;       // where the job's cost begins
   if (start / cut.per != i - 1) return;           // cut earlier already
-  const int pieces = static_cast<int>((start + cut.n + kCfJobCost - 1) / cut.per) - (i - 1) + 1;
+  const int pieces = (start + cut.n + kCfJobCost - 1) / cut.per - (i - 1) + 1;
   // tiles of the job's k-th piece, in CTA i - 1 + k
-  auto tile_at = [&](int64_t cta) -> int {
-    return static_cast<int>(min(max(cta * cut.per - start - kCfJobCost, int64_t{0}), static_cast<int64_t>(cut.n)));
-  };
+  auto tile_at = [&](int cta) -> int { return min(max(cta * cut.per - start - kCfJobCost, 0), cut.n); };
   if (tile_at(i) == 0 && pieces == 2) return;     // the cut fell before its first tile: one piece
   const int lane = threadIdx.x & 31;
   const int rows = min(pos, a.q_len - cut.rt * pos) * kGroup;
@@ -1132,6 +1146,8 @@ int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
   const int32_t pos = cf_wide(q_len) ? 2 * kCfPos : kCfPos;
   const int64_t jobs = static_cast<int64_t>(num_seqs) * num_kv_heads * ((q_len + pos - 1) / pos);
   const int64_t cost = jobs * ((max_blocks + kCfTileBlocks - 1) / kCfTileBlocks + kCfJobCost);  // at most
+  // (shares are rounded up, so the last one may end behind the work)
+  if (cost + int64_t{kCfMinShare} * sm_count > 0x7fffffff) return 0;
   return static_cast<int32_t>(std::min<int64_t>(sm_count, (cost + kCfMinShare - 1) / kCfMinShare));
 }
 

@@ -1255,6 +1255,7 @@ ScaledPlan scaled_plan(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads, in
     return p;
   }
   p.grid = chunk_scaled_grid(num_seqs, num_kv_heads, q_len, max_blocks, sms);
+  if (p.grid == 0) return p;
   const size_t rows = static_cast<size_t>(p.grid) * 2 * chunk_scaled_rows(q_len);
   p.ml_at = align_up(rows * kHeadDim * sizeof(float), 256);
   p.cuts_at = p.ml_at + align_up(rows * sizeof(float2), 256);
@@ -1374,7 +1375,7 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
     return PKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_seqs) * q_len * num_q_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   const ScaledPlan p = scaled_plan(num_seqs, q_len, cache->num_kv_heads, max_blocks_per_seq);
-  if (q_len == 1 && static_cast<int64_t>(num_seqs) * cache->num_kv_heads * p.splits > 0x7fffffff)
+  if (p.grid == 0 || (q_len == 1 && static_cast<int64_t>(num_seqs) * cache->num_kv_heads * p.splits > 0x7fffffff))
     return PKV_ERR_UNSUPPORTED;
   if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes || !aligned({workspace}, 256)))
     return PKV_ERR_WORKSPACE;

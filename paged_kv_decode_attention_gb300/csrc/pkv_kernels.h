@@ -293,8 +293,8 @@ cudaError_t launch_copy_blocks_scaled(uint8_t* k_cache, uint8_t* v_cache, float*
 struct CfCut {  // where a CTA's share of the work starts, for the joining kernel
   int32_t r, rt, kvh;
   int32_t n;     // tiles of the job
-  int64_t into;  // how far into the job's cost
-  int64_t per;   // cost of a share
+  int32_t into;  // how far into the job's cost
+  int32_t per;   // cost of a share
 };
 struct ChunkScaledArgs {
   void* out;                    // BF16 [B][q_len][Hq][D]
@@ -317,6 +317,7 @@ struct ChunkScaledArgs {
   int32_t rows_slot;            // chunk_scaled_rows
   float scale_log2;
 };
+// CTAs of a call, 0 for more work than it can count.
 int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t sm_count);
 int32_t chunk_scaled_rows(int32_t q_len);
 cudaError_t launch_paged_chunk_fp8_tc(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream);
