@@ -803,8 +803,8 @@ pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scale
  *                  2^-32 and 2^32 (powers of two or not).
  *   scale        : > 0.
  *   workspace    : device, 256-byte aligned, pkv_workspace_size_fp8_scaled(...)
- *                  bytes (may be NULL when 0).  Its contents are overwritten;
- *                  calls that share it must be stream-ordered.
+ *                  bytes.  Its contents are overwritten; calls that share it
+ *                  must be stream-ordered.
  * Codes of every token of the context must be finite (no 0x7f, 0xff); slots
  * past it may hold anything.
  */

@@ -222,7 +222,7 @@ __device__ __forceinline__ uint32_t cf_half2(float lo, float hi) {
 }
 
 // Tiles of keys that a row tile of a request reads.
-__device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int pair, int n_rt, int pos) {
+__device__ __forceinline__ int cf_tiles(const ScaledArgs& a, int pair, int n_rt, int pos) {
   const int r = n_rt == 1 ? pair : pair / n_rt;
   const int rt = pair - r * n_rt;
   const int ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
@@ -233,7 +233,7 @@ __device__ __forceinline__ int cf_tiles(const ChunkScaledArgs& a, int pair, int 
 template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kCfThreads, 1)
     paged_chunk_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                              const ChunkScaledArgs a) {
+                              const ScaledArgs a) {
   using S = CfShape<kWide>;
   constexpr uint32_t kSlots = S::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
 // Joins the partials of a job that was cut.  Block x of the grid looks at the
 // cut where CTA x's share starts, and takes the job if that cut is its first;
 // one warp per row, 4 dims a lane.
-__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a, int32_t pos) {
+__global__ void __launch_bounds__(256) scaled_join_kernel(const ScaledArgs a, int32_t pos, int32_t job_cost) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x + 1;
@@ -1073,9 +1073,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a
   if (cut.into == 0) return;                      // no cut here
   const int start = cut.per * i - cut.into;       // where the job's cost begins
   if (start / cut.per != i - 1) return;           // cut earlier already
-  const int pieces = (start + cut.n + kCfJobCost - 1) / cut.per - (i - 1) + 1;
+  const int pieces = (start + cut.n + job_cost - 1) / cut.per - (i - 1) + 1;
   // tiles of the job's k-th piece, in CTA i - 1 + k
-  auto tile_at = [&](int cta) -> int { return min(max(cta * cut.per - start - kCfJobCost, 0), cut.n); };
+  auto tile_at = [&](int cta) -> int { return min(max(cta * cut.per - start - job_cost, 0), cut.n); };
   if (tile_at(i) == 0 && pieces == 2) return;     // the cut fell before its first tile: one piece
   const int lane = threadIdx.x & 31;
   const int rows = min(pos, a.q_len - cut.rt * pos) * kGroup;
@@ -1113,7 +1113,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkScaledArgs a
 }
 
 template <bool kWide, int kRows>
-cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
+cudaError_t launch_cf(const ScaledArgs& a, int32_t grid, cudaStream_t stream) {
   static std::atomic<bool> done[64];  // per device; host threads may race on a first call
   auto kernel = paged_chunk_fp8_tc_kernel<kWide, kRows>;
   int dev = 0;
@@ -1132,15 +1132,19 @@ cudaError_t launch_cf(const ChunkScaledArgs& a, int32_t grid, cudaStream_t strea
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), CfShape<kWide>::kSmem, stream,
                  1, kmap, vmap, a);
   if (e != cudaSuccess || grid == 1) return e;
-  // 8 rows a block at a time; a job of few rows is joined by one block
-  const int32_t pos = kWide ? 2 * kCfPos : kCfPos;
-  const unsigned parts = (std::min(pos, a.q_len) * kGroup + 7) / 8;
-  return launch_pdl(chunk_join_kernel, dim3(static_cast<unsigned>(grid - 1), parts), dim3(256), 0, stream, 1, a, pos);
+  return launch_scaled_join(a, grid, kWide ? 2 * kCfPos : kCfPos, kCfJobCost, stream);
 }
 
 bool cf_wide(int32_t q_len) { return q_len > kCfPos; }
 
 }  // namespace
+
+cudaError_t launch_scaled_join(const ScaledArgs& a, int32_t grid, int32_t pos, int32_t job_cost, cudaStream_t stream) {
+  // 8 rows a block at a time; a job of few rows is joined by one block
+  const unsigned parts = (std::min(pos, a.q_len) * kGroup + 7) / 8;
+  return launch_pdl(scaled_join_kernel, dim3(static_cast<unsigned>(grid - 1), parts), dim3(256), 0, stream, 1, a, pos,
+                    job_cost);
+}
 
 int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t sm_count) {
   const int32_t pos = cf_wide(q_len) ? 2 * kCfPos : kCfPos;
@@ -1153,7 +1157,7 @@ int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len,
 
 int32_t chunk_scaled_rows(int32_t q_len) { return cf_wide(q_len) ? 2 * kCfRows : kGroup * q_len; }
 
-cudaError_t launch_paged_chunk_fp8_tc(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream) {
+cudaError_t launch_paged_chunk_fp8_tc(const ScaledArgs& a, int32_t grid, cudaStream_t stream) {
   if (cf_wide(a.q_len)) return launch_cf<true, 128>(a, grid, stream);
   const int32_t rows = kGroup * a.q_len;
   if (rows <= 32) return launch_cf<false, 32>(a, grid, stream);

@@ -51,6 +51,7 @@
 //                and unit end passes one barrier of the 4 warps where each
 //                posts its health, so all four leave together if one gives up.
 // Every wait is bounded and reports PKV_DEVERR_TIMEOUT instead of hanging.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cuda_fp16.h>
@@ -122,8 +123,14 @@ enum class FtMode {
   kScaled  // codes times a scale for each block and KV head
 };
 
+// kScaled: in tiles, what a (request, KV head) costs besides its tiles, and the
+// least worth a CTA.
+constexpr int kFtJobCost = 1;
+constexpr int kFtMinShare = 2;
+
 struct FtUnit {
   int r, kvh, split, b0, b1, n_tiles, ctx_keys, ctx_raw;
+  bool whole;  // kScaled: all of the row's tiles
   // fused append: the tile and tile row holding the request's new token
   // (position ctx - 1) and its logical block; new_tile = -1 when the unit
   // does not hold it or there is no append
@@ -162,6 +169,115 @@ __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
   return x;
 }
 
+// kScaled: work is cut by tiles, not by requests.  All (request, KV head) rows,
+// each counted as its tiles and kFtJobCost more, are divided evenly among the
+// CTAs; a row cut in two or more leaves un-normalised partials, at most two per
+// CTA, which the joining kernel of the chunks puts together.  (64 requests of 16
+// to 16000 tokens: in equal splits of the longest context 184 us.)
+__device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
+  const int ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
+  return (ctx + kFtTileTokens - 1) / kFtTileTokens;
+}
+
+// The units that a CTA works on, in order.  Every warp walks them for itself.
+template <FtMode kMode>
+struct FtWalk {
+  int u;                            // !kScaled: the next unit
+  int r, kvh, tiles, into, left;    // kScaled: the next row, how far into its cost, what is left of the share
+
+  __device__ __forceinline__ bool next(const DecodeArgs& a, int num_units, FtUnit& x) {
+    if constexpr (kMode != FtMode::kScaled) {
+      if (u >= num_units) return false;
+      x = ft_unit<kMode>(a, u);
+      u += gridDim.x;
+      return true;
+    } else {
+      while (left > 0) {
+        const int cost = tiles + kFtJobCost;
+        const int end = min(into + left, cost);
+        const int begin = max(into - kFtJobCost, 0);
+        const int take = max(end - kFtJobCost, 0) - begin;
+        left -= end - into;
+        into = 0;
+        if (take > 0) {  // (none: the share ends before the row's first tile)
+          x.r = r;
+          x.kvh = kvh;
+          x.split = begin == 0 ? 1 : 0;  // place of a partial
+          x.ctx_raw = a.context_lens[r];
+          const int ctx = min(x.ctx_raw, a.max_blocks * kBlockSize);
+          x.b0 = begin * kFtTileBlocks;
+          x.b1 = min((ctx + kBlockSize - 1) / kBlockSize, (begin + take) * kFtTileBlocks);
+          x.n_tiles = take;
+          x.ctx_keys = min(ctx, x.b1 * kBlockSize);
+          x.whole = take == tiles;
+        }
+        if (++kvh == a.num_kv_heads) {
+          kvh = 0;
+          for (++r; left > 0 && r < a.num_seqs && (tiles = ft_tiles(a, r)) == 0; ++r) {
+          }
+        }
+        if (take > 0) return true;
+      }
+      return false;
+    }
+  }
+};
+
+// Where this CTA's walk starts (warp-collective).
+template <FtMode kMode>
+__device__ __forceinline__ FtWalk<kMode> ft_start(const DecodeArgs& a, int lane, CfCut* cut) {
+  FtWalk<kMode> w{};
+  w.u = blockIdx.x;
+  if constexpr (kMode == FtMode::kScaled) {
+    // (the host has seen to it that all costs together fit into 31 bits)
+    auto cost = [](int tiles) -> int { return tiles > 0 ? tiles + kFtJobCost : 0; };
+    int total = 0, first32 = 0;  // (and of the first 32 requests, one a lane)
+    for (int r = lane; r < a.num_seqs; r += 32) {
+      const int x = ft_tiles(a, r);
+      if (r < 32) first32 = x;
+      total += cost(x);
+    }
+    total = __reduce_add_sync(0xffffffffu, total) * a.num_kv_heads;
+    const int grid = gridDim.x;
+    const int per = max((total + grid - 1) / grid, kFtMinShare);
+    const int t0 = per * static_cast<int>(blockIdx.x);
+    w.left = min(per, total - t0);
+    if (w.left > 0) {
+      int before = 0;
+      for (int r0 = 0;; r0 += 32) {
+        const int x = r0 == 0 ? first32 : (r0 + lane < a.num_seqs ? ft_tiles(a, r0 + lane) : 0);
+        int upto = cost(x) * a.num_kv_heads;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
+        if (past != 0) {
+          const int at = __ffs(past) - 1;
+          w.tiles = __shfl_sync(0xffffffffu, x, at);
+          const int start = before + __shfl_sync(0xffffffffu, upto, at) - cost(w.tiles) * a.num_kv_heads;
+          w.r = r0 + at;
+          w.kvh = (t0 - start) / cost(w.tiles);
+          w.into = (t0 - start) - w.kvh * cost(w.tiles);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+    if (cut != nullptr && lane == 0) {
+      CfCut c{};
+      c.r = w.r;
+      c.kvh = w.kvh;
+      c.n = w.tiles;
+      c.into = w.into;
+      c.per = per;
+      *cut = c;
+    }
+  }
+  return w;
+}
+
 // Fused append: the caller's slot for the unit's new token, and whether it is
 // the slot the block table gives that position (only then is the row patched
 // into the tiles; any slot inside the pool is stored, as the append would).
@@ -192,8 +308,9 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
   const int oob_row = a.num_blocks * a.num_kv_heads * kBlockSize;  // first row past the pool
   bool ok = true;
   int i = 0;
-  for (int u = blockIdx.x; u < num_units && ok; u += gridDim.x) {
-    const FtUnit x = ft_unit<kMode>(a, u);
+  FtWalk<kMode> walk = ft_start<kMode>(a, lane, nullptr);
+  FtUnit x;
+  while (ok && walk.next(a, num_units, x)) {
     if (x.n_tiles == 0) continue;
     const int32_t* table = a.block_tables + static_cast<int64_t>(x.r) * a.max_blocks;
     // the load stays inside the table row whatever the context length, so it
@@ -359,37 +476,40 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     // Two cursors walk the tile sequence: one issues S, the other P.V.  The
     // thread polls both and issues whichever is ready, so a P.V whose weights
     // are done never waits behind the next tile's K arrival.
+    const FtWalk<kWalk> start = ft_start<kWalk>(a, lane, nullptr);
     if (lane == 0) {
       constexpr uint32_t kIdS = tc::idesc_e4m3_f32(128, kFtN, false, false);
       constexpr uint32_t kIdO = tc::idesc_e4m3_f32(128, kFtN, true, false);
       struct Cursor {
-        int u, j, i, seq, n;  // unit, tile in unit, tile overall, unit ordinal, tiles of the unit
+        FtWalk<kWalk> walk;
+        int j, i, seq, n;  // tile in unit, tile overall, unit ordinal, tiles of the unit (0: at the end)
       };
-      auto settle = [&](Cursor& c) {  // move to the first unit with a tile, from c.u on
-        for (; c.u < num_units; c.u += gridDim.x) {
-          c.n = ft_unit<kWalk>(a, c.u).n_tiles;
-          if (c.n > 0) return;
-        }
+      auto settle = [&](Cursor& c) {  // move to the next unit with a tile
+        FtUnit x;
+        do {
+          c.n = 0;
+          if (!c.walk.next(a, num_units, x)) return;
+          c.n = x.n_tiles;
+        } while (c.n == 0);
       };
       auto advance = [&](Cursor& c) {
         ++c.i;
         if (++c.j < c.n) return;
         c.j = 0;
         ++c.seq;
-        c.u += gridDim.x;
         settle(c);
       };
-      Cursor cs{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+      Cursor cs{start, 0, 0, 0, 0};
       settle(cs);
       Cursor cp = cs;
       uint64_t t_idle = 0;
       // fused append, K side: the S cursor's unit's new K row (tile << 8 | tile
       // row, or -1), published with the unit's query operand
       int kp_at = -1;
-      while (cp.u < num_units) {
+      while (cp.n > 0) {
         bool progressed = false;
         // ---- S of the next tile ----
-        if (cs.u < num_units) {
+        if (cs.n > 0) {
           const int i = cs.i, st = i % kFtStages, sb = i & 1, ub = cs.seq & 1;
           bool ready = mbar_test_wait(&bars->k_full[st], (i / kFtStages) & 1);
           if (ready && cs.j == 0) ready = mbar_test_wait(&bars->q_full[ub], (cs.seq >> 1) & 1);
@@ -467,8 +587,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     // lane = (head h = lane / 8, dims 16 * (lane % 8) .. + 15)
     const int h = lane >> 3, c = lane & 7;
     int seq = 0;
-    for (int u = blockIdx.x; u < num_units && ok; u += gridDim.x) {
-      const FtUnit x = ft_unit<kMode>(a, u);
+    FtWalk<kMode> walk = ft_start<kMode>(a, lane, kScaled ? a.cuts + blockIdx.x : nullptr);
+    FtUnit x;
+    while (ok && walk.next(a, num_units, x)) {
       if (x.n_tiles == 0) continue;
       const int ub = seq & 1;
       const uint4* src = reinterpret_cast<const uint4*>(
@@ -549,7 +670,15 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     const int t = threadIdx.x - 128;  // tokens t and 128 + t of the tile (TMEM lane t); at a unit's end, the output dim
     const uint32_t lane_off = static_cast<uint32_t>(w * 32) << 16;
     float* xch = reinterpret_cast<float*>(smem + kOffX);  // [2][4][8]
-    const bool direct = a.num_splits == 1;
+    if constexpr (kScaled) {
+      // requests without a token belong to no share: zeros
+      for (int r = blockIdx.x; r < a.num_seqs; r += gridDim.x) {
+        if (t == 0 && a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
+        if (ft_tiles(a, r) > 0) continue;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<int64_t>(r) * hq * kHeadDim);
+        for (int k = t; k < hq * (kHeadDim * 2 / 16); k += 128) o[k] = make_uint4(0, 0, 0, 0);
+      }
+    }
     bool ok_all = true;  // uniform across the 4 warps: changes only right after an exchange
     // Exchanges among the 4 warps alternate between two buffers: each warp
     // writes its 4 values and its health flag into its row, passes the
@@ -567,10 +696,12 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       return all;
     };
     int i = 0, seq = 0;
-    for (int u = blockIdx.x; u < num_units && ok_all; u += gridDim.x) {
-      const FtUnit x = ft_unit<kMode>(a, u);
+    FtWalk<kMode> walk = ft_start<kMode>(a, lane, nullptr);
+    FtUnit x;
+    while (ok_all && walk.next(a, num_units, x)) {
+      const bool direct = kScaled ? x.whole : a.num_splits == 1;
       const int64_t orow0 = static_cast<int64_t>(x.r) * hq + x.kvh * kGroup;
-      if (threadIdx.x == 128 && x.split == 0 && x.kvh == 0 && x.ctx_raw > a.max_blocks * kBlockSize)
+      if (!kScaled && threadIdx.x == 128 && x.split == 0 && x.kvh == 0 && x.ctx_raw > a.max_blocks * kBlockSize)
         report(a.err, PKV_DEVERR_CONTEXT);
       // fused append: a slot for an empty row has no position ctx - 1 to go
       // to; the token is not stored and the caller's error is reported
@@ -820,6 +951,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
             const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
             dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
           }
+        } else if constexpr (kScaled) {  // un-normalised
+          const int64_t row = (2 * static_cast<int64_t>(blockIdx.x) + x.split) * kGroup;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) a.part_o[(row + h) * kHeadDim + t] = o[h];
+          if (t < kGroup) a.part_ml[row + t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
         } else {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -878,13 +1014,44 @@ cudaError_t launch_ft(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
 
 cudaError_t launch_paged_decode_fp8_tc(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
   if (grid <= 0) return cudaSuccess;
-  const bool scaled = a.k_scales != nullptr, fused = a.k_new != nullptr;
-  if (a.q_len != 1 || a.num_splits < 1 ||
-      (a.num_splits > 1 && (a.part_o == nullptr || a.part_lse == nullptr)))
+  if (a.q_len != 1 || a.num_splits < 1 || (a.num_splits > 1 && (a.part_o == nullptr || a.part_lse == nullptr)))
     return cudaErrorInvalidValue;
-  if (fused && (a.v_new == nullptr || a.slot_mapping == nullptr || scaled)) return cudaErrorInvalidValue;
-  if (scaled) return launch_ft<FtMode::kScaled>(a, grid, stream);
+  const bool fused = a.k_new != nullptr;
+  if (fused && (a.v_new == nullptr || a.slot_mapping == nullptr)) return cudaErrorInvalidValue;
   return fused ? launch_ft<FtMode::kFused>(a, grid, stream) : launch_ft<FtMode::kPlain>(a, grid, stream);
+}
+
+int32_t decode_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks, int32_t sm_count) {
+  const int64_t cost = static_cast<int64_t>(num_seqs) * num_kv_heads *
+                       ((max_blocks + kFtTileBlocks - 1) / kFtTileBlocks + kFtJobCost);  // at most
+  // (shares are rounded up, so the last one may end behind the work)
+  if (cost + int64_t{kFtMinShare} * sm_count > 0x7fffffff) return 0;
+  return static_cast<int32_t>(std::min<int64_t>(sm_count, (cost + kFtMinShare - 1) / kFtMinShare));
+}
+
+cudaError_t launch_paged_decode_fp8_scaled(const ScaledArgs& a, int32_t grid, cudaStream_t stream) {
+  DecodeArgs d{};
+  d.out = a.out;
+  d.q = a.q;
+  d.k_cache = a.k_cache;
+  d.v_cache = a.v_cache;
+  d.k_scales = a.k_scales;
+  d.v_scales = a.v_scales;
+  d.block_tables = a.block_tables;
+  d.context_lens = a.context_lens;
+  d.part_o = a.part_o;
+  d.part_ml = a.part_ml;
+  d.cuts = a.cuts;
+  d.err = a.err;
+  d.max_blocks = a.max_blocks;
+  d.num_blocks = a.num_blocks;
+  d.num_kv_heads = a.num_kv_heads;
+  d.num_seqs = a.num_seqs;
+  d.q_len = 1;
+  d.num_splits = 1;
+  d.scale_log2 = a.scale_log2;
+  const cudaError_t e = launch_ft<FtMode::kScaled>(d, grid, stream);
+  return e != cudaSuccess || grid == 1 ? e : launch_scaled_join(a, grid, 1, kFtJobCost, stream);
 }
 
 }  // namespace pkv

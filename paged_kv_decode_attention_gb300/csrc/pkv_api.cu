@@ -12,9 +12,6 @@
 #include <cuda_runtime.h>
 #include <initializer_list>
 
-#ifndef PKV_X
-#define PKV_X 0
-#endif
 #include "pkv.h"
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
@@ -1230,11 +1227,11 @@ bool aligned(std::initializer_list<const void*> ps, uintptr_t align) {
 constexpr int32_t kScaledMaxBlocks = 1 << 26;
 constexpr int32_t kScaledMaxQLen = 1 << 26;
 
-// How a call over block-scaled pools runs, and what its workspace holds.
+// How a call over block-scaled pools runs, and what its workspace holds: two
+// partials of a CTA's rows, their maxima and sums, where the shares start.
 struct ScaledPlan {
-  int32_t grid = 0;     // CTAs that share the work
-  int32_t bps = 0;      // q_len 1: blocks per split
-  int32_t splits = 1;
+  int32_t grid = 0;               // CTAs that share the work; 0: more than they can count
+  int32_t rows_slot = 0;          // rows of a partial
   size_t ml_at = 0, cuts_at = 0;  // offsets in the workspace
   size_t bytes = 0;
 };
@@ -1242,21 +1239,11 @@ struct ScaledPlan {
 ScaledPlan scaled_plan(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads, int32_t max_blocks) {
   ScaledPlan p;
   const int sms = device_sm_count();
-  if (q_len == 1 && !PKV_X) {
-    const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
-    p.bps = std::min(persistent_blocks_per_split(rows, max_blocks, sms, 16), max_blocks);
-    p.splits = (max_blocks + p.bps - 1) / p.bps;
-    const int64_t units = rows * p.splits;
-    p.grid = static_cast<int32_t>(units < sms ? units : sms);
-    if (p.splits > 1) {
-      p.ml_at = align_up(static_cast<size_t>(rows) * kGroup * p.splits * kHeadDim * sizeof(float), 256);
-      p.bytes = p.ml_at + align_up(static_cast<size_t>(rows) * kGroup * p.splits * sizeof(float), 256);
-    }
-    return p;
-  }
-  p.grid = chunk_scaled_grid(num_seqs, num_kv_heads, q_len, max_blocks, sms);
+  p.grid = q_len == 1 ? decode_scaled_grid(num_seqs, num_kv_heads, max_blocks, sms)
+                      : chunk_scaled_grid(num_seqs, num_kv_heads, q_len, max_blocks, sms);
   if (p.grid == 0) return p;
-  const size_t rows = static_cast<size_t>(p.grid) * 2 * chunk_scaled_rows(q_len);
+  p.rows_slot = q_len == 1 ? kGroup : chunk_scaled_rows(q_len);
+  const size_t rows = static_cast<size_t>(p.grid) * 2 * p.rows_slot;
   p.ml_at = align_up(rows * kHeadDim * sizeof(float), 256);
   p.cuts_at = p.ml_at + align_up(rows * sizeof(float2), 256);
   p.bytes = p.cuts_at + align_up(static_cast<size_t>(p.grid) * sizeof(CfCut), 256);
@@ -1375,36 +1362,10 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
     return PKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_seqs) * q_len * num_q_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   const ScaledPlan p = scaled_plan(num_seqs, q_len, cache->num_kv_heads, max_blocks_per_seq);
-  if (p.grid == 0 || (q_len == 1 && static_cast<int64_t>(num_seqs) * cache->num_kv_heads * p.splits > 0x7fffffff))
-    return PKV_ERR_UNSUPPORTED;
-  if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes || !aligned({workspace}, 256)))
-    return PKV_ERR_WORKSPACE;
+  if (p.grid == 0) return PKV_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < p.bytes || !aligned({workspace}, 256)) return PKV_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q_len > 1 || PKV_X) {
-    ChunkScaledArgs a{};
-    a.out = out;
-    a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.k_scales = k_scales;
-    a.v_scales = v_scales;
-    a.block_tables = block_tables;
-    a.context_lens = context_lens;
-    a.part_o = reinterpret_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
-    a.cuts = reinterpret_cast<CfCut*>(ws + p.cuts_at);
-    a.err = error_word();
-    a.max_blocks = max_blocks_per_seq;
-    a.num_blocks = cache->num_blocks;
-    a.num_kv_heads = cache->num_kv_heads;
-    a.num_seqs = num_seqs;
-    a.q_len = q_len;
-    a.rows_slot = chunk_scaled_rows(q_len);
-    a.scale_log2 = scale * 1.4426950408889634f;
-    return launch_paged_chunk_fp8_tc(a, p.grid, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-  }
-  DecodeArgs a{};
+  ScaledArgs a{};
   a.out = out;
   a.q = q;
   a.k_cache = k_cache;
@@ -1413,25 +1374,20 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
   a.v_scales = v_scales;
   a.block_tables = block_tables;
   a.context_lens = context_lens;
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
+  a.cuts = reinterpret_cast<CfCut*>(ws + p.cuts_at);
   a.err = error_word();
   a.max_blocks = max_blocks_per_seq;
   a.num_blocks = cache->num_blocks;
   a.num_kv_heads = cache->num_kv_heads;
   a.num_seqs = num_seqs;
-  a.q_len = 1;
-  a.blocks_per_split = p.bps;
-  a.num_splits = p.splits;
+  a.q_len = q_len;
+  a.rows_slot = p.rows_slot;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.part_slots = p.splits;
-  if (p.splits > 1) {
-    a.part_o = reinterpret_cast<float*>(ws);
-    a.part_lse = reinterpret_cast<float*>(ws + p.ml_at);
-  }
-  if (launch_paged_decode_fp8_tc(a, p.grid, s) != cudaSuccess) return PKV_ERR_CUDA;
-  if (p.splits == 1) return PKV_OK;
-  return launch_attn_combine(out, nullptr, a.part_o, a.part_lse, num_seqs * num_q_heads, p.splits, s) == cudaSuccess
-             ? PKV_OK
-             : PKV_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = q_len == 1 ? launch_paged_decode_fp8_scaled(a, p.grid, s) : launch_paged_chunk_fp8_tc(a, p.grid, s);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_copy_blocks_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,

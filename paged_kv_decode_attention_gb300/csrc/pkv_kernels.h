@@ -48,6 +48,13 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // splits go through the workspace and the combine kernel.
 constexpr int kMaxClusterSplits = 8;
 
+struct CfCut {  // where a CTA's share of the work starts, for the joining kernel
+  int32_t r, rt, kvh;
+  int32_t n;     // tiles of the job
+  int32_t into;  // how far into the job's cost
+  int32_t per;   // cost of a share
+};
+
 // One decode/split launch: grid (rows, splits, kv heads); see paged_decode.cu.
 struct DecodeArgs {
   void* out;                  // BF16 [B][q_len][Hq][D]; written when num_splits == 1
@@ -102,6 +109,8 @@ struct DecodeArgs {
   // E4M3 pools with block scales: FP32 [num_blocks][Hkv] (paged_decode_fp8_tc.cu); NULL = no scales
   const float* k_scales;
   const float* v_scales;
+  float2* part_ml;
+  CfCut* cuts;
 };
 
 cudaError_t launch_kv_append(void* k_cache, void* v_cache, int32_t num_blocks, int32_t num_kv_heads,
@@ -289,14 +298,9 @@ cudaError_t launch_copy_blocks_scaled(uint8_t* k_cache, uint8_t* v_cache, float*
                                       int32_t num_blocks, int32_t num_kv_heads, const int32_t* src,
                                       const int32_t* dst, int32_t num_pairs, unsigned int* err, cudaStream_t stream);
 
-// Attention of several queries per request over such pools (paged_chunk_fp8_tc.cu).
-struct CfCut {  // where a CTA's share of the work starts, for the joining kernel
-  int32_t r, rt, kvh;
-  int32_t n;     // tiles of the job
-  int32_t into;  // how far into the job's cost
-  int32_t per;   // cost of a share
-};
-struct ChunkScaledArgs {
+// Attention over such pools: single queries (paged_decode_fp8_tc.cu), several
+// per request (paged_chunk_fp8_tc.cu).
+struct ScaledArgs {
   void* out;                    // BF16 [B][q_len][Hq][D]
   const void* q;
   const void* k_cache;
@@ -318,9 +322,13 @@ struct ChunkScaledArgs {
   float scale_log2;
 };
 // CTAs of a call, 0 for more work than it can count.
+int32_t decode_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks, int32_t sm_count);
 int32_t chunk_scaled_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t q_len, int32_t max_blocks, int32_t sm_count);
 int32_t chunk_scaled_rows(int32_t q_len);
-cudaError_t launch_paged_chunk_fp8_tc(const ChunkScaledArgs& a, int32_t grid, cudaStream_t stream);
+cudaError_t launch_paged_decode_fp8_scaled(const ScaledArgs& a, int32_t grid, cudaStream_t stream);
+cudaError_t launch_paged_chunk_fp8_tc(const ScaledArgs& a, int32_t grid, cudaStream_t stream);
+// Joins the jobs that the CTAs' shares cut: `pos` positions to a job, `job_cost` counted besides its tiles.
+cudaError_t launch_scaled_join(const ScaledArgs& a, int32_t grid, int32_t pos, int32_t job_cost, cudaStream_t stream);
 
 // Device error word of the current device (PKV_DEVERR_* bits).
 unsigned int* device_error_word();
