@@ -1086,24 +1086,45 @@ __global__ void __launch_bounds__(256) scaled_join_kernel(const ScaledArgs a, in
     auto at = [&](int k) -> int64_t {
       return static_cast<int64_t>(2 * (i - 1 + k) + (k == first ? 1 : 0)) * a.rows_slot + row;
     };
-    float m = -INFINITY;
-    for (int k = first + lane; k < pieces; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float l = 0.f;
+    // 32 pieces at a time: lane k holds the k-th one's maximum and sum, and
+    // what is summed so far is taken against the maximum so far
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = first; k < pieces; ++k) {
-      const int64_t p = at(k);
-      const float2 ml = a.part_ml[p];
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + 4 * lane);
-      if (ml.y == 0.f) continue;  // it saw nothing: its O holds anything
-      const float f = exp2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      o.x = fmaf(x.x, f, o.x);
-      o.y = fmaf(x.y, f, o.y);
-      o.z = fmaf(x.z, f, o.z);
-      o.w = fmaf(x.w, f, o.w);
+    constexpr int kFlight = 8;  // partials in flight
+    for (int k0 = first; k0 < pieces; k0 += 32) {
+      const int n = min(32, pieces - k0);
+      float4 x[kFlight];
+      auto fetch = [&](int b) {
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k)
+          if (b + k < n) x[k] = *reinterpret_cast<const float4*>(a.part_o + at(k0 + b + k) * kHeadDim + 4 * lane);
+      };
+      fetch(0);
+      const float2 ml = lane < n ? a.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.f);
+      float top = ml.x;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float m_new = fmaxf(m, top);
+      const float old = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
+      const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m_new);  // (0: it saw nothing, its O holds anything)
+      float sum = ml.y * f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      l = l * old + sum;
+      o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+      m = m_new;
+      for (int b = 0; b < n; b += kFlight) {
+        if (b > 0) fetch(b);
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const float g = __shfl_sync(0xffffffffu, f, (b + k) & 31);
+          if (b + k >= n || g == 0.f) continue;
+          o.x = fmaf(x[k].x, g, o.x);
+          o.y = fmaf(x[k].y, g, o.y);
+          o.z = fmaf(x[k].z, g, o.z);
+          o.w = fmaf(x[k].w, g, o.w);
+        }
+      }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t out_row = (static_cast<int64_t>(cut.r) * a.q_len + cut.rt * pos + (row >> 2)) * hq + cut.kvh * kGroup + (row & 3);

@@ -81,7 +81,8 @@ constexpr int kOffKn = kOffX + 2 * 4 * 8 * 4;              // fused append: 2 ne
 constexpr int kOffKnAt = kOffKn + 2 * kHeadDim;            // int [2]: where each row goes (tile << 8 | row), or -1
 constexpr int kFtScaleSlots = 8;                           // block scales: tiles held
 constexpr int kOffScale = kOffKnAt + 16;                   // float [8 tiles][K, V][16 blocks]
-constexpr int kOffBar = kOffScale + kFtScaleSlots * 2 * kFtTileBlocks * 4;
+constexpr int kOffPart = kOffScale + kFtScaleSlots * 2 * kFtTileBlocks * 4;  // float2 [4]: a partial's maxima and sums
+constexpr int kOffBar = kOffPart + 32;
 constexpr int kSmemFt = kOffBar + 512;
 constexpr uint32_t kColS = 0;    // S^T buffers at columns 0 and 32 (16 columns per half)
 constexpr uint32_t kColO = 64;   // O^T buffers at columns 64 and 80
@@ -116,12 +117,14 @@ struct FtBars {
 };
 static_assert(sizeof(FtBars) <= 512, "barrier area");
 
-// The three decodes of this file.
+// The decodes of this file.
 enum class FtMode {
   kPlain,
-  kFused,  // stores each request's new token and uses it
-  kScaled  // codes times a scale for each block and KV head
+  kFused,         // stores each request's new token and uses it
+  kScaled,        // codes times a scale for each block and KV head
+  kScaledCluster  // the same, a thread-block cluster to a (request, KV head)
 };
+__host__ __device__ constexpr bool ft_scaled(FtMode m) { return m == FtMode::kScaled || m == FtMode::kScaledCluster; }
 
 // kScaled: in tiles, what a (request, KV head) costs besides its tiles, and the
 // least worth a CTA.
@@ -179,17 +182,41 @@ __device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
   return (ctx + kFtTileTokens - 1) / kFtTileTokens;
 }
 
+// kScaledCluster: where there are so few rows that kMaxClusterSplits CTAs for
+// each are resident at once, they take equal parts of it and join them through
+// distributed shared memory: one launch.  (One request of 8,300 tokens, 8 KV
+// heads: 14.4 us with shares and their joining.)
+//
 // The units that a CTA works on, in order.  Every warp walks them for itself.
 template <FtMode kMode>
 struct FtWalk {
   int u;                            // !kScaled: the next unit
   int r, kvh, tiles, into, left;    // kScaled: the next row, how far into its cost, what is left of the share
 
+  // The unit of `take` tiles from tile `begin` of row (r, kvh).
+  __device__ __forceinline__ void fill(const DecodeArgs& a, FtUnit& x, int begin, int take) const {
+    x.r = r;
+    x.kvh = kvh;
+    x.split = begin == 0 ? 1 : 0;  // place of a partial
+    x.ctx_raw = a.context_lens[r];
+    const int ctx = min(x.ctx_raw, a.max_blocks * kBlockSize);
+    x.b0 = begin * kFtTileBlocks;
+    x.b1 = min((ctx + kBlockSize - 1) / kBlockSize, (begin + take) * kFtTileBlocks);
+    x.n_tiles = take;
+    x.ctx_keys = min(ctx, x.b1 * kBlockSize);
+    x.whole = take == tiles;
+  }
+
   __device__ __forceinline__ bool next(const DecodeArgs& a, int num_units, FtUnit& x) {
-    if constexpr (kMode != FtMode::kScaled) {
+    if constexpr (!ft_scaled(kMode)) {
       if (u >= num_units) return false;
       x = ft_unit<kMode>(a, u);
       u += gridDim.x;
+      return true;
+    } else if constexpr (kMode == FtMode::kScaledCluster) {
+      if (left <= 0) return false;
+      fill(a, x, into, left);
+      left = 0;
       return true;
     } else {
       while (left > 0) {
@@ -199,18 +226,7 @@ struct FtWalk {
         const int take = max(end - kFtJobCost, 0) - begin;
         left -= end - into;
         into = 0;
-        if (take > 0) {  // (none: the share ends before the row's first tile)
-          x.r = r;
-          x.kvh = kvh;
-          x.split = begin == 0 ? 1 : 0;  // place of a partial
-          x.ctx_raw = a.context_lens[r];
-          const int ctx = min(x.ctx_raw, a.max_blocks * kBlockSize);
-          x.b0 = begin * kFtTileBlocks;
-          x.b1 = min((ctx + kBlockSize - 1) / kBlockSize, (begin + take) * kFtTileBlocks);
-          x.n_tiles = take;
-          x.ctx_keys = min(ctx, x.b1 * kBlockSize);
-          x.whole = take == tiles;
-        }
+        if (take > 0) fill(a, x, begin, take);  // (none: the share ends before the row's first tile)
         if (++kvh == a.num_kv_heads) {
           kvh = 0;
           for (++r; left > 0 && r < a.num_seqs && (tiles = ft_tiles(a, r)) == 0; ++r) {
@@ -228,7 +244,14 @@ template <FtMode kMode>
 __device__ __forceinline__ FtWalk<kMode> ft_start(const DecodeArgs& a, int lane, CfCut* cut) {
   FtWalk<kMode> w{};
   w.u = blockIdx.x;
-  if constexpr (kMode == FtMode::kScaled) {
+  if constexpr (kMode == FtMode::kScaledCluster) {
+    w.r = blockIdx.x / a.num_kv_heads;
+    w.kvh = blockIdx.x - w.r * a.num_kv_heads;
+    w.tiles = ft_tiles(a, w.r);
+    const int part = (w.tiles + kMaxClusterSplits - 1) / kMaxClusterSplits;
+    w.into = part * blockIdx.y;  // (the first tile here)
+    w.left = min(part, w.tiles - w.into);
+  } else if constexpr (kMode == FtMode::kScaled) {
     // (the host has seen to it that all costs together fit into 31 bits)
     auto cost = [](int tiles) -> int { return tiles > 0 ? tiles + kFtJobCost : 0; };
     int total = 0, first32 = 0;  // (and of the first 32 requests, one a lane)
@@ -329,7 +352,7 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[st], kFtStageBytes);
       __syncwarp();
-      if (kMode == FtMode::kScaled && scales != nullptr) {
+      if (ft_scaled(kMode) && scales != nullptr) {
         float* slot_of = scales + (i % kFtScaleSlots) * 2 * kFtTileBlocks + lane;
         if (x.b0 + j * kFtTileBlocks + (lane & 15) < x.b1) {
           const int b = blk < 0 || blk >= a.num_blocks ? 0 : blk;
@@ -355,7 +378,7 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
   // copies still in flight must land before shared memory is released
   if (lane == 0)
     for (int k = max(0, i - kFtStages); k < i; ++k) mbar_wait(&full[k % kFtStages], (k / kFtStages) & 1);
-  if (kMode == FtMode::kScaled) cp_async_wait_all();
+  if (ft_scaled(kMode)) cp_async_wait_all();
   return ok;
 }
 
@@ -412,13 +435,18 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                                const DecodeArgs a) {
   pdl_trigger();
   constexpr bool kFused = kMode == FtMode::kFused;
-  constexpr bool kScaled = kMode == FtMode::kScaled;
+  constexpr bool kScaled = ft_scaled(kMode);
+  constexpr bool kCluster = kMode == FtMode::kScaledCluster;
   constexpr FtMode kWalk = kScaled ? kMode : FtMode::kPlain;  // of the warps that need not know the new tokens
   extern __shared__ __align__(1024) uint8_t smem[];
   FtBars* bars = reinterpret_cast<FtBars*>(smem + kOffBar);
   float* scale_ring = reinterpret_cast<float*>(smem + kOffScale);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  // kCluster: the partial, over the K ring once its tiles are used; its maxima
+  // and sums behind it
+  float* part_o = reinterpret_cast<float*>(smem + kOffK);
+  float2* part_ml = reinterpret_cast<float2*>(smem + kOffPart);
   const int num_units = a.num_seqs * a.num_kv_heads * a.num_splits;
   const int hq = a.num_kv_heads * kGroup;
 
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     // lane = (head h = lane / 8, dims 16 * (lane % 8) .. + 15)
     const int h = lane >> 3, c = lane & 7;
     int seq = 0;
-    FtWalk<kMode> walk = ft_start<kMode>(a, lane, kScaled ? a.cuts + blockIdx.x : nullptr);
+    FtWalk<kMode> walk = ft_start<kMode>(a, lane, kScaled && !kCluster ? a.cuts + blockIdx.x : nullptr);
     FtUnit x;
     while (ok && walk.next(a, num_units, x)) {
       if (x.n_tiles == 0) continue;
@@ -670,7 +698,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     const int t = threadIdx.x - 128;  // tokens t and 128 + t of the tile (TMEM lane t); at a unit's end, the output dim
     const uint32_t lane_off = static_cast<uint32_t>(w * 32) << 16;
     float* xch = reinterpret_cast<float*>(smem + kOffX);  // [2][4][8]
-    if constexpr (kScaled) {
+    if constexpr (kCluster) {
+      if (t == 0 && blockIdx.y == 0 && a.context_lens[blockIdx.x / a.num_kv_heads] > a.max_blocks * kBlockSize)
+        report(a.err, PKV_DEVERR_CONTEXT);
+      if (t < kGroup) part_ml[t] = make_float2(-INFINITY, 0.f);  // until there is a result
+    } else if constexpr (kScaled) {
       // requests without a token belong to no share: zeros
       for (int r = blockIdx.x; r < a.num_seqs; r += gridDim.x) {
         if (t == 0 && a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
@@ -944,7 +976,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         float o[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) o[h] = (o8[h] + o8[4 + h]) * kFtPUnscale;
-        if (direct) {
+        if constexpr (kCluster) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
+          if (t < kGroup) part_ml[t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
+        } else if (direct) {
           uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -980,6 +1016,38 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kFtTmemCols);
   }
+
+  if constexpr (kCluster) {
+    // every CTA joins its 16 dims of the 4 heads
+    cluster_sync_all();
+    const uint32_t rank = cluster_cta_rank();
+    if (threadIdx.x < 64) {
+      const int h = threadIdx.x >> 4, d = static_cast<int>(rank) * 16 + (threadIdx.x & 15);
+      float ms[kMaxClusterSplits], ls[kMaxClusterSplits], os[kMaxClusterSplits];
+#pragma unroll
+      for (int k = 0; k < kMaxClusterSplits; ++k) {
+        const uint32_t ml = map_shared_to_rank(part_ml + h, k);
+        ms[k] = ld_cluster_f32(ml);
+        ls[k] = ld_cluster_f32(ml + 4);
+        os[k] = ld_cluster_f32(map_shared_to_rank(part_o + h * kHeadDim + d, k));
+      }
+      float mx = -INFINITY, sum = 0.f, o = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxClusterSplits; ++k) mx = fmaxf(mx, ms[k]);
+#pragma unroll
+      for (int k = 0; k < kMaxClusterSplits; ++k) {
+        if (ls[k] == 0.f) continue;  // saw nothing: its O holds anything
+        const float f = exp2_approx(ms[k] - mx);
+        sum = fmaf(ls[k], f, sum);
+        o = fmaf(os[k], f, o);
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const int r = blockIdx.x / a.num_kv_heads, kvh = blockIdx.x - r * a.num_kv_heads;
+      static_cast<uint16_t*>(a.out)[(static_cast<int64_t>(r) * hq + kvh * kGroup + h) * kHeadDim + d] =
+          static_cast<uint16_t>(pack_bf16x2(o * inv, 0.f) & 0xffffu);
+    }
+    cluster_sync_all();  // a partial stays until every CTA has read it
+  }
 }
 
 template <FtMode kMode>
@@ -997,6 +1065,40 @@ cudaError_t allow_smem_ft() {
   return cudaSuccess;
 }
 
+// Clusters of the scaled decode that are resident at once on the current
+// device; 0 when that cannot be asked.
+int max_clusters_ft() {
+  static std::atomic<int> known[64];  // per device, + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int c = 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1, kMaxClusterSplits);
+    cfg.blockDim = dim3(kFtThreads);
+    cfg.dynamicSmemBytes = kSmemFt;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1;
+    attr.val.clusterDim.y = kMaxClusterSplits;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (allow_smem_ft<FtMode::kScaledCluster>() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&c, paged_decode_fp8_tc_kernel<FtMode::kScaledCluster>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    n = c + 1;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
 template <FtMode kMode>
 cudaError_t launch_ft(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.num_kv_heads * kBlockSize;
@@ -1006,8 +1108,9 @@ cudaError_t launch_ft(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem_ft<kMode>();
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_decode_fp8_tc_kernel<kMode>, dim3(static_cast<unsigned>(grid)), dim3(kFtThreads), kSmemFt,
-                    stream, 1, kmap, vmap, a);
+  constexpr unsigned kSplits = kMode == FtMode::kScaledCluster ? kMaxClusterSplits : 1;
+  return launch_pdl(paged_decode_fp8_tc_kernel<kMode>, dim3(static_cast<unsigned>(grid), kSplits), dim3(kFtThreads),
+                    kSmemFt, stream, kSplits, kmap, vmap, a);
 }
 
 }  // namespace
@@ -1050,6 +1153,8 @@ cudaError_t launch_paged_decode_fp8_scaled(const ScaledArgs& a, int32_t grid, cu
   d.q_len = 1;
   d.num_splits = 1;
   d.scale_log2 = a.scale_log2;
+  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  if (rows <= max_clusters_ft()) return launch_ft<FtMode::kScaledCluster>(d, static_cast<int32_t>(rows), stream);
   const cudaError_t e = launch_ft<FtMode::kScaled>(d, grid, stream);
   return e != cudaSuccess || grid == 1 ? e : launch_scaled_join(a, grid, 1, kFtJobCost, stream);
 }
