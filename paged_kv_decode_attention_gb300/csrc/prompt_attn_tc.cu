@@ -56,11 +56,13 @@ constexpr int kPaHalfBytes = kPaTokens * 128;          // 64 dims of a tile of K
 constexpr int kPaTileBytes = 2 * kPaHalfBytes;         // 16 KiB
 constexpr int kPaQHalfBytes = kPaRows * 128;
 constexpr int kPaQBytes = 2 * kPaQHalfBytes;           // a row tile of Q: 32 KiB
-constexpr int kPaStages = 10;                          // ring of K and V tiles, in turn
+constexpr int kPaStages = 8;                           // ring of K and V tiles, in turn (10: no faster, 6: 20 % slower)
 constexpr int kPaThreads = 384;
 constexpr int kPaOffQ = 0;                             // 2 row tiles
 constexpr int kPaOffRing = 2 * kPaQBytes;
-constexpr int kPaOffBar = kPaOffRing + kPaStages * kPaTileBytes;
+constexpr int kPaOffOut = kPaOffRing + kPaStages * kPaTileBytes;  // results on their way out: 4 KiB a softmax warp
+constexpr int kPaOutBytes = 32 * 128;
+constexpr int kPaOffBar = kPaOffOut + 8 * kPaOutBytes;
 constexpr int kPaSmem = kPaOffBar + 512;
 constexpr uint32_t kPaTileCols = 256;                  // per row tile: S, two buffers of P, O
 constexpr uint32_t kPaColP = 64;
@@ -114,18 +116,6 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
-}
-
-// 32 bytes of a row: whole sectors where its address is a multiple of 32.
-__device__ __forceinline__ void store_32b(void* dst, const uint32_t* v, bool wide) {
-  if (!wide) {
-    static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // Key tiles that the positions up to `last` see.
@@ -452,7 +442,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int warp_pos = quad * 32 / a.group;  // the warp's first row's
     const float c = a.scale_log2;              // > 0: the max of raw scores scales to the max of scaled ones
     const int hq = a.num_kv_heads * a.group;
-    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+    uint8_t* stage = smem + kPaOffOut + warp * kPaOutBytes;
     uint32_t g = 0;       // tiles of this row tile so far
     uint32_t place = 1;   // ring place of the present tile's V
     PaUnit u;
@@ -557,22 +547,35 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (!ok) break;
       tc::fence_after_sync();
       const float inv = 1.f / l;  // (a row sees its own key: l > 0, or NaN)
-      const int64_t out_row = static_cast<int64_t>(u.tok0 + pos) * hq + u.kvh * a.group + row_head;
-      uint8_t* dst = static_cast<uint8_t*>(a.out) + out_row * (kHeadDim * 2);
+      // Results leave as whole 128-byte lines, 64 dims of the warp's rows at a
+      // time: a thread's own row in pieces costs 32 separate lines an
+      // instruction (3000 to 4000 cycles a unit; 64 short prompts 49 us).
+      const int64_t row0 = static_cast<int64_t>(u.tok0 + u.pos0 + t * per_tile) * hq + u.kvh * a.group;
+      const int mine = valid ? row_pos * hq + row_head : -1;  // row of the output, from row0
+      uint8_t* out0 = static_cast<uint8_t*>(a.out) + row0 * (kHeadDim * 2) + (lane & 7) * 16;
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        float o[32];
-        tc::tmem_ld32(scol + kPaColO + 32 * cc, o);
+      for (int pass = 0; pass < 2; ++pass) {
+        float o[64];
+        tc::tmem_ld32(scol + kPaColO + 64 * pass, o);
+        tc::tmem_ld32(scol + kPaColO + 64 * pass + 32, o + 32);
         tc::tmem_wait_ld();
-        uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-        if (valid) {
-          store_32b(dst + 64 * cc, w, wide);
-          store_32b(dst + 64 * cc + 32, w + 8, wide);
+        for (int e = 0; e < 8; ++e)  // 16-byte chunk e of row r sits at chunk e ^ (r % 8)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                         pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                         pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const int to = __shfl_sync(0xffffffffu, mine, r);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(to) * (kHeadDim * 2) + 128 * pass) = w;
         }
+        __syncwarp();
       }
-      if (valid && a.lse != nullptr) a.lse[out_row] = (m + log2f(l)) * kPaLn2;
+      if (valid && a.lse != nullptr) a.lse[row0 + mine] = (m + log2f(l)) * kPaLn2;
       tc::fence_before_sync();  // O is read before the next unit's weights arrive
     }
     if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
