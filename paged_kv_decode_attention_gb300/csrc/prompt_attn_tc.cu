@@ -35,10 +35,11 @@
 // CTA = 12 warps:
 //   warps 0-7: softmax, one thread per row (TMEM lane), one warpgroup for each
 //             of the two row tiles.
-//   warp 8  : TMA producer of Q, and of K and V into one ring of 16 KiB stages.
+//   warp 8  : TMA producer of K and V, into one ring of 16 KiB stages.
 //   warps 9, 10: MMA issuers, one per row tile: while one tile's softmax runs,
 //             the tensor cores work on the other's products.
-//   warp 11 : finds the CTA's units, one ahead of the others.
+//   warp 11 : finds the CTA's units, one ahead of the others, and loads Q.  (By
+//             the producer of K and V, each row tile waits for the other's queries.)
 #include <climits>
 #include <cmath>
 #include <cstddef>
@@ -226,9 +227,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         for (int s0 = 32; s0 < a.num_seqs; s0 += 32) c += __popc(__ballot_sync(0xffffffffu, units_of(s0 + lane) > i));
         return c;
       };
+      uint32_t loaded[2] = {0, 0};
+      // a unit's queries, once the row tile's last product with those before is done
+      const uint64_t once = l2_policy_evict_first();
+      const uint32_t q_bytes = static_cast<uint32_t>(per_tile) * a.group * 256;
+      auto queries = [&](const PaUnit& u, uint32_t k) {
+        if (lane == 0) {
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (k > 0) ok = mbar_wait(&bars->q_empty[t], (k & 1) ^ 1);
+            if (!ok) break;
+            uint8_t* dst = smem + kPaOffQ + t * kPaQBytes;
+            const int tok = u.tok0 + u.pos0 + t * per_tile;  // (past the last token: zeros)
+            mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
+            tma_load_3d(dst, &q_map, 0, u.kvh * a.group, tok, &bars->q_full[t], once);
+            tma_load_3d(dst + kPaQHalfBytes, &q_map, 64, u.kvh * a.group, tok, &bars->q_full[t], once);
+            loaded[t] = k + 1;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      };
       int index = most - 1;  // of the units in turn
       int64_t before = 0;    // (prompt, index) pairs ahead of this index
       int here = index >= 0 ? count(index) : 0;
+      PaUnit was{0, 0, 0, 0};
       for (uint32_t round = 0;; ++round) {
         const int64_t w = static_cast<int64_t>(round) * gridDim.x +
                           ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -263,16 +284,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           mbar_arrive(&bars->u_full[slot]);
         }
         __syncwarp();
-        if (u.len == 0) break;
+        if (round > 0) queries(was, round - 1);
+        if (!ok || u.len == 0) break;
+        was = u;
       }
-      if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
+      if (!ok && lane == 0) {
+        report(a.err, PKV_DEVERR_TIMEOUT);
+        // copies under way must land before shared memory is released
+        for (int t = 0; t < 2; ++t)
+          if (loaded[t] > 0) mbar_wait(&bars->q_full[t], (loaded[t] - 1) & 1);
+      }
+      __syncwarp();
     } else if (warp == 8) {
       // ---------------------------- TMA producer ----------------------------
       const uint64_t keep = l2_policy_evict_last();
-      const uint64_t once = l2_policy_evict_first();
-      const uint32_t q_bytes = static_cast<uint32_t>(per_tile) * a.group * 256;
       uint32_t filled = 0;  // ring stages so far
-      uint32_t units = 0;
       PaUnit u;
       auto ring = [&](const CUtensorMap* map, int tok, int kvh) {
         const int st = filled % kPaStages;
@@ -287,23 +313,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       while (next_unit(u)) {
         const int n = max(tiles_of(u, 0), tiles_of(u, 1));
         if (lane == 0) {
-          ring(&k_map, u.tok0, u.kvh);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (units > 0) ok = mbar_wait(&bars->q_empty[t], (units & 1) ^ 1);
-            if (!ok) break;
-            uint8_t* dst = smem + kPaOffQ + t * kPaQBytes;
-            const int tok = u.tok0 + u.pos0 + t * per_tile;  // (past the last token: zeros)
-            mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
-            tma_load_3d(dst, &q_map, 0, u.kvh * a.group, tok, &bars->q_full[t], once);
-            tma_load_3d(dst + kPaQHalfBytes, &q_map, 64, u.kvh * a.group, tok, &bars->q_full[t], once);
-          }
-          if (ok) ring(&v_map, u.tok0, u.kvh);
-          for (int j = 1; j < n && ok; ++j) {
+          for (int j = 0; j < n && ok; ++j) {
             ring(&k_map, u.tok0 + j * kPaTokens, u.kvh);
             if (ok) ring(&v_map, u.tok0 + j * kPaTokens, u.kvh);
           }
         }
-        ++units;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
@@ -566,12 +580,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                          pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                          pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
         __syncwarp();
+        uint4 w[8];  // (all read before the first is stored: the compiler cannot know that they do not overlap)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * i + (lane >> 3);
-          const int to = __shfl_sync(0xffffffffu, mine, r);
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if (to >= 0) *reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(to) * (kHeadDim * 2) + 128 * pass) = w;
+          w[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int to = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
+          if (to >= 0) *reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(to) * (kHeadDim * 2) + 128 * pass) = w[i];
         }
         __syncwarp();
       }
