@@ -567,6 +567,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int64_t row0 = static_cast<int64_t>(u.tok0 + u.pos0 + t * per_tile) * hq + u.kvh * a.group;
       const int mine = valid ? row_pos * hq + row_head : -1;  // row of the output, from row0
       uint8_t* out0 = static_cast<uint8_t*>(a.out) + row0 * (kHeadDim * 2) + (lane & 7) * 16;
+      int to[8];  // the rows that this lane stores a piece of
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {
         float o[64];
@@ -588,8 +591,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int to = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
-          if (to >= 0) *reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(to) * (kHeadDim * 2) + 128 * pass) = w[i];
+          if (to[i] >= 0) *reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(to[i]) * (kHeadDim * 2) + 128 * pass) = w[i];
         }
         __syncwarp();
       }
