@@ -74,8 +74,8 @@ constexpr int kCfTokens = 64;                         // keys of a tile
 constexpr int kCfTileBlocks = kCfTokens / kBlockSize;  // 4
 constexpr int kCfTileBytes = kCfTokens * kHeadDim;    // K or V of a tile: 8 KiB
 constexpr int kCfBoxBytes = kBlockSize * kHeadDim;
-constexpr int kCfScaleSlots = 16;                     // tiles whose scales are held
 constexpr int kCfGroupTiles = 32 / kCfTileBlocks;     // tiles whose blocks a warp looks up at a time
+constexpr int kCfScaleGroups = 2;                     // groups whose scales are held
 constexpr int kCfThreads = 512;
 constexpr int kCfRows = 128;
 constexpr int kCfPos = kCfRows / kGroup;              // positions of a row tile
@@ -93,7 +93,7 @@ struct CfShape {
   static constexpr int kOffExtra = 4 * kCfPartBytes;  // V in FP16, or the join's buffer, FP32 [2 x 128][32]
   static constexpr int kOffRing = kOffExtra + (kWide ? kCfV16Stages * kCfV16Bytes : 2 * kCfRows * 32 * 4);
   static constexpr int kOffScale = kOffRing + kSlots * kCfTileBytes;
-  static constexpr int kOffSigma = kOffScale + kCfScaleSlots * kCfScaleFloats * 4;  // FP32 [2][128]: scale / sigma
+  static constexpr int kOffSigma = kOffScale + kCfScaleGroups * kCfGroupTiles * kCfScaleFloats * 4;  // FP32 [2][128]: scale / sigma
   static constexpr int kOffBar = kOffSigma + 2 * kCfRows * 4;
   static constexpr int kSmem = kOffBar + 896;
   static_assert(kSmem <= 227 * 1024, "one CTA per SM");
@@ -117,8 +117,8 @@ constexpr float kCfLagHalf = 8.f;
 constexpr float kCfFactor = -2.f;
 constexpr float kCfCodeUnit = 256.f;
 // In tiles: what a job costs besides its tiles, and the least worth a CTA.
-constexpr int kCfJobCost = 4;
-constexpr int kCfMinShare = 8;
+constexpr int kCfJobCost = 8;
+constexpr int kCfMinShare = 12;
 
 struct alignas(16) CfPiece {
   int32_t r, rt, kvh;   // request, row tile (pair), KV head
@@ -130,7 +130,7 @@ struct alignas(16) CfPiece {
 template <bool kWide>
 struct CfBars {
   uint64_t full[CfShape<kWide>::kSlots], empty[CfShape<kWide>::kSlots];
-  uint64_t sc_full[kCfScaleSlots], sc_empty[kCfScaleSlots];
+  uint64_t sc_full[kCfScaleGroups], sc_empty[kCfScaleGroups];
   uint64_t q_full[2], q_empty[2];  // per row tile, or buffer
   uint64_t v16_full[kCfV16Stages], v16_empty[kCfV16Stages];
   uint64_t join_full, join_free;   // !kWide: the join's buffer is written, is read
@@ -249,9 +249,9 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       // K (even places): both issuers, or the half's; V: the converting warps, or the half's
       mbar_init(&bars->empty[s], kWide ? ((s & 1) ? kCfHelpers : 2) : 1);
     }
-    for (int s = 0; s < kCfScaleSlots; ++s) {
+    for (int s = 0; s < kCfScaleGroups; ++s) {
       mbar_init(&bars->sc_full[s], 1);
-      mbar_init(&bars->sc_empty[s], kWide ? 8 : 4);
+      mbar_init(&bars->sc_empty[s], 8);  // the softmax warps
     }
     for (int s = 0; s < kCfV16Stages; ++s) {
       mbar_init(&bars->v16_full[s], kCfHelpers);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         cut.per = per;
         a.cuts[blockIdx.x] = cut;
       }
-      uint32_t tiles = 0;  // scale slots written so far
+      uint32_t sets = 0;  // groups of scales written so far
       // the scales of a piece's blocks, 32 blocks (8 tiles) at a time, fetched a group ahead
       auto scales_of = [&](const CfPiece& u) {
         const int32_t* table = a.block_tables + static_cast<int64_t>(u.r) * a.max_blocks;
@@ -399,21 +399,18 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         fetch(0, ks, vs);
         for (int g = 0; g < groups && ok; ++g) {
           if (g + 1 < groups) fetch(g + 1, ks_next, vs_next);
-          const float lv = log2f(vs), iv = 1.f / vs;
-          for (int k = 0; k < kCfGroupTiles && kCfGroupTiles * g + k < u.take && ok; ++k, ++tiles) {
-            const int slot = tiles % kCfScaleSlots;
-            if (tiles >= kCfScaleSlots)
-              ok = __all_sync(0xffffffffu, mbar_wait(&bars->sc_empty[slot], ((tiles / kCfScaleSlots) & 1) ^ 1));
-            if (!ok) break;
-            float* dst = reinterpret_cast<float*>(smem + S::kOffScale) + slot * kCfScaleFloats + lane % kCfTileBlocks;
-            if (lane / kCfTileBlocks == k) {
-              dst[0] = ks;
-              dst[kCfTileBlocks] = lv;
-              dst[2 * kCfTileBlocks] = iv;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->sc_full[slot]);
-          }
+          const int slot = sets % kCfScaleGroups;
+          if (sets >= kCfScaleGroups)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->sc_empty[slot], ((sets / kCfScaleGroups) & 1) ^ 1));
+          if (!ok) break;
+          float* dst = reinterpret_cast<float*>(smem + S::kOffScale) +
+                       (slot * kCfGroupTiles + lane / kCfTileBlocks) * kCfScaleFloats + lane % kCfTileBlocks;
+          dst[0] = ks;
+          dst[kCfTileBlocks] = log2f(vs);
+          dst[2 * kCfTileBlocks] = 1.f / vs;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->sc_full[slot]);
+          ++sets;
           ks = ks_next;
           vs = vs_next;
         }
@@ -763,6 +760,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     uint32_t tile0 = 0;  // tiles of the pieces so far
     uint32_t pieces = 0;
     uint32_t passes = 0;  // of the join's buffer
+    uint32_t sets = 0;    // groups of scales so far
     CfPiece u;
     while (next_piece(u)) {
       const int n_t = tiles_of(u, t);
@@ -782,17 +780,36 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       if (lane == 0) mbar_arrive(&bars->q_empty[qb]);
       float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum)
       float l = 0.f;        // sum of w / vs, in the weights' unit
+      // Scales come in groups of 8 tiles, so that a tile need not wait for them.
+      const uint32_t set0 = sets;
+      sets += (u.take + kCfGroupTiles - 1) / kCfGroupTiles;
+      uint32_t set = set0;  // the present one
+      auto enter = [&]() -> bool {
+        return __all_sync(0xffffffffu,
+                          mbar_wait(&bars->sc_full[set % kCfScaleGroups], (set / kCfScaleGroups) & 1));
+      };
+      auto leave = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->sc_empty[set % kCfScaleGroups]);
+        ++set;
+      };
+      ok = enter();
+      if (!ok) break;
       for (int j = 0; j < n_t; ++j, ++g) {
         const int in_piece = kWide ? j : 2 * j + t;
         const int tok = (u.begin + in_piece) * kCfTokens;
-        const uint32_t sl = (tile0 + in_piece) % kCfScaleSlots;
+        if (set0 + in_piece / kCfGroupTiles != set) {
+          leave();
+          ok = enter();
+          if (!ok) break;
+        }
         // (`ok` stays warp-uniform: the loads below are warp-collective)
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(&bars->sc_full[sl], ((tile0 + in_piece) / kCfScaleSlots) & 1) &&
-                            mbar_wait(&bars->s_full[t], g & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], g & 1));
         if (!ok) break;
         // the blocks' ks, log2 vs, 1 / vs (read twice: registers are dearer)
-        const float* sc = reinterpret_cast<const float*>(smem + S::kOffScale) + sl * kCfScaleFloats + key0 / kBlockSize;
+        const float* sc = reinterpret_cast<const float*>(smem + S::kOffScale) +
+                          (set % kCfScaleGroups * kCfGroupTiles + in_piece % kCfGroupTiles) * kCfScaleFloats +
+                          key0 / kBlockSize;
         tc::fence_after_sync();
         if (warp_live) {
           float s[kCols];
@@ -917,11 +934,15 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           mbar_arrive(&bars->s_free[t]);
           mbar_arrive(&bars->p_full[t][g & 1]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->sc_empty[sl]);
       }
       tile0 += u.take;
       if (!ok) break;
+      leave();
+      if (set != sets) {  // (a last group of one tile, the other half's)
+        ok = enter();
+        if (!ok) break;
+        leave();
+      }
       if (!kWide) l *= kCfCodeUnit;  // in O's unit
       // ---- results ----
       if (n_t > 0) {

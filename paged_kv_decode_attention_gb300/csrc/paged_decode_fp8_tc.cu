@@ -128,8 +128,8 @@ __host__ __device__ constexpr bool ft_scaled(FtMode m) { return m == FtMode::kSc
 
 // kScaled: in tiles, what a (request, KV head) costs besides its tiles, and the
 // least worth a CTA.
-constexpr int kFtJobCost = 1;
-constexpr int kFtMinShare = 2;
+constexpr int kFtJobCost = 2;
+constexpr int kFtMinShare = 3;
 
 struct FtUnit {
   int r, kvh, split, b0, b1, n_tiles, ctx_keys, ctx_raw;
@@ -176,7 +176,8 @@ __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
 // each counted as its tiles and kFtJobCost more, are divided evenly among the
 // CTAs; a row cut in two or more leaves un-normalised partials, at most two per
 // CTA, which the joining kernel of the chunks puts together.  (64 requests of 16
-// to 16000 tokens: in equal splits of the longest context 184 us.)
+// to 16000 tokens: in equal splits of the longest context 184 us; a row counted
+// with 1, 2, 3 or 4 tiles more: 76, 74, 77, 82.)
 __device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
   const int ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
   return (ctx + kFtTileTokens - 1) / kFtTileTokens;
