@@ -105,6 +105,7 @@ constexpr uint32_t kCfColP = 64;
 constexpr uint32_t kCfPCols = 32;
 constexpr uint32_t kCfColLow = 16;                    // low parts, within a buffer
 constexpr uint32_t kCfColO = 128;
+constexpr uint32_t kCfColQ = 96;                      // kWide: one buffer of weights, then the queries' high parts
 constexpr int kCfSoftmaxRegs = 168;
 constexpr int kCfOtherRegs = 88;
 static_assert((2 * kCfSoftmaxRegs + 2 * kCfOtherRegs) * 128 <= 128 * kCfThreads, "register split");
@@ -132,6 +133,7 @@ struct CfBars {
   uint64_t full[CfShape<kWide>::kSlots], empty[CfShape<kWide>::kSlots];
   uint64_t sc_full[kCfScaleGroups], sc_empty[kCfScaleGroups];
   uint64_t q_full[2], q_empty[2];  // per row tile, or buffer
+  uint64_t qt_full[2];             // kWide: the high parts are in tensor memory
   uint64_t v16_full[kCfV16Stages], v16_empty[kCfV16Stages];
   uint64_t join_full, join_free;   // !kWide: the join's buffer is written, is read
   uint64_t s_full[2], s_free[2];
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], kQWarps);
       mbar_init(&bars->q_empty[t], kWide ? 5 : 10);  // the softmax warps and issuers that use it
+      mbar_init(&bars->qt_full[t], 128);
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->s_free[t], 128);
       for (int b = 0; b < 2; ++b) {
@@ -659,7 +662,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_f8(scol, qd + (((kk >> 2) * kCfPartBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
+            if (kWide && kk < 4)
+              mma_f8_tmem_a(scol, scol + kCfColQ + 8 * kk, kd + ((32 * kk) >> 4), kIdS, kk > 0 ? 1u : 0u);
+            else
+              tc::mma_f8(scol, qd + (((kk >> 2) * kCfPartBytes + 32 * (kk & 3)) >> 4), kd + ((32 * (kk & 3)) >> 4), kIdS,
                        kk > 0 ? 1u : 0u);
           tc::commit(&bars->s_full[t]);
           if (last) tc::commit(&bars->q_empty[buf]);  // other queries may come
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       auto issue_pv = [&](uint32_t place, uint32_t tile, uint32_t buf, bool first) {
         const uint64_t vd = kWide ? v16 + (tile % kCfV16Stages) * (kCfV16Bytes >> 4)
                                   : ring + (place % kSlots) * (kCfTileBytes >> 4);
-        const uint32_t pcol = scol + kCfColP + buf * kCfPCols;
+        const uint32_t pcol = scol + kCfColP + (kWide ? 0 : buf * kCfPCols);
         tc::fence_after_sync();
         if (tc::elect_one()) {
 #pragma unroll
@@ -698,6 +704,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         c0 += 2 * u.take;
         const uint32_t qb = q_slot(pieces, t);
         ok = wait(&bars->q_full[qb], q_phase(pieces));
+        if (kWide) ok = ok && wait(&bars->qt_full[t], pieces & 1);
         ++pieces;
         if (ok && n_t > 0) {
           ok = wait_full(c);
@@ -776,6 +783,26 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       ++pieces;
       if (!ok) break;
       const float c = reinterpret_cast<const float*>(smem + S::kOffSigma)[qb * kCfRows + row];
+      if constexpr (kWide) {
+        // the queries' high parts to tensor memory: S is bound by what its
+        // operands read of shared memory (with all of them there, 0.84 ms for 4 x
+        // 2000 queries behind 4000 to 8000 tokens)
+        const uint8_t* q = smem + S::kOffQ + qb * 2 * kCfPartBytes + row * 128;
+        uint32_t w[32];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 x = *reinterpret_cast<const uint4*>(q + ((ch ^ (row & 7)) << 4));
+          w[4 * ch] = x.x;
+          w[4 * ch + 1] = x.y;
+          w[4 * ch + 2] = x.z;
+          w[4 * ch + 3] = x.w;
+        }
+        tc::tmem_st16u(scol + kCfColQ, w);
+        tc::tmem_st16u(scol + kCfColQ + 16, w + 16);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&bars->qt_full[t]);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_empty[qb]);
       float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum)
@@ -823,7 +850,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           tc::fence_before_sync();
           mbar_arrive(&bars->s_free[t]);
           // the weights' buffer: its last product is done (see the issuers)
-          const uint32_t pcol = scol + kCfColP + (g & 1) * kCfPCols;
+          const uint32_t pcol = scol + kCfColP + (kWide ? 0 : (g & 1) * kCfPCols);
           auto store = [&](uint32_t col, const uint32_t* w) {
             if constexpr (kCols == 64) tc::tmem_st16u(col, w);
             if constexpr (kCols == 32) tc::tmem_st8(col, w);
@@ -875,23 +902,29 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           m = m_new;
           const float nm = (m == -INFINITY ? 0.f : -m) + (kWide ? 0.f : kCfFactor);
           if constexpr (kWide) {
+            uint32_t w[8 * kCfTileBlocks];
 #pragma unroll
             for (int b = 0; b < kCfTileBlocks; ++b) {
               const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
               const float2 k2 = make_float2(kc, kc);
               const float2 n2 = make_float2(off, off);
               float2 acc = make_float2(0.f, 0.f);
-              uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float2 x = __ffma2_rn(make_float2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), k2, n2);
                 const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
                 acc = __fadd2_rn(acc, make_float2(p0, p1));
-                w[e] = cf_half2(p0, p1);
+                w[8 * b + e] = cf_half2(p0, p1);
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
-              tc::tmem_st8(pcol + 8 * b, w);
             }
+            if (j > 0) {  // the weights' place is free once the product before is done
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
+              if (!ok) break;
+              tc::fence_after_sync();
+            }
+            tc::tmem_st16u(pcol, w);
+            tc::tmem_st16u(pcol + 16, w + 16);
           } else {
             uint32_t hi[kCols / 4], lo[kCols / 4];
 #pragma unroll
