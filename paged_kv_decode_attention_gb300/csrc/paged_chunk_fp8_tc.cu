@@ -28,10 +28,12 @@
 // !kWide: up to kRows rows, 32, 64 or 128.  HBM is the bound, and a chain of
 //         scores, softmax and product is longer than a tile's transfer.  So
 //         the CTA's two halves take the even and the odd tiles of keys, and
-//         the query rows are laid out 128 / kRows times: a copy's threads do
-//         the softmax of kRows / 2 of a tile's 64 keys, with a maximum and a
+//         where there are few query rows they are laid out twice: a copy's
+//         threads do the softmax of half of a tile's keys, with a maximum and a
 //         sum of their own (the other keys' weights are zeros).  At the end
-//         all copies and both halves are joined through shared memory.  V's
+//         all copies and both halves are joined through shared memory.  Up to
+//         32 rows the products have M = 64, which reads half as much of the
+//         queries per product, and two threads share a row.  V's
 //         codes enter as they are and the weights as two E4M3 parts times 2^6
 //         (2^-8 relative, by way of FP16, down to 2^-16 of the largest).
 //
@@ -232,11 +234,23 @@ __device__ __forceinline__ int cf_tiles(const ScaledArgs& a, int pair, int n_rt,
   return end > 0 ? (end + kCfTokens - 1) / kCfTokens : 0;
 }
 
+// How the query rows of a call lie in the products and the threads.
+template <bool kWide, int kRows>
+struct CfRowsOf {
+  static constexpr bool kHalf = !kWide && kRows == 32;           // M = 64: 16 rows and two threads a row in a warp
+  static constexpr int kMma = kHalf ? 64 : kCfRows;              // M
+  static constexpr int kWarpRows = kHalf ? 16 : 32;
+  static constexpr int kCopies = kMma / kRows;
+  static constexpr int kCopyKeys = kCfTokens / kCopies;          // of a tile's keys
+  static constexpr int kCols = kHalf ? kCopyKeys / 2 : kCopyKeys;  // a thread's
+};
+
 template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kCfThreads, 1)
     paged_chunk_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                               const ScaledArgs a) {
   using S = CfShape<kWide>;
+  using R = CfRowsOf<kWide, kRows>;
   constexpr uint32_t kSlots = S::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
   auto* bars = reinterpret_cast<CfBars<kWide>*>(smem + S::kOffBar);
@@ -556,7 +570,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
                 cf_signed(bf16_lo(wv[2 * e]) * f, bf16_hi(wv[2 * e]) * f, bf16_lo(wv[2 * e + 1]) * f,
                           bf16_hi(wv[2 * e + 1]) * f, hi[e], lo[e]);
 #pragma unroll
-              for (int copy = 0; copy < kCfRows / kRows; ++copy) {
+              for (int copy = 0; copy < R::kCopies; ++copy) {
                 const uint32_t at = tc::sw128_offset_b8(m + copy * kRows, 16 * c16);
                 *reinterpret_cast<uint4*>(qa + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4*>(qa + kCfPartBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -624,9 +638,9 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       __syncwarp();
     } else {
       // ---------------------------- MMA issuers ----------------------------
-      constexpr uint32_t kIdS = tc::idesc_e4m3_f32(kCfRows, kCfTokens, false, false);
+      constexpr uint32_t kIdS = tc::idesc_e4m3_f32(R::kMma, kCfTokens, false, false);
       constexpr uint32_t kIdO = kWide ? tc::idesc_f16_f32(kCfRows, kHeadDim, false, true)
-                                      : tc::idesc_e4m3_f32(kCfRows, kHeadDim, false, true);
+                                      : tc::idesc_e4m3_f32(R::kMma, kHeadDim, false, true);
       const int t = warp - 9;
       const bool leader = lane == 0;
       const uint32_t scol = tmem + t * kCfTileCols;
@@ -742,7 +756,6 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     cf_regs_up<kCfSoftmaxRegs>();
     const int t = warp >> 2;
     const int quad = warp & 3;  // TMEM sub-partition of this warp
-    const int row = quad * 32 + lane;
     const uint32_t scol = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * kCfTileCols;
     const int row_tile = kWide ? t : 0;  // row tile of this warpgroup's rows
 
@@ -757,12 +770,13 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     }
 
     // this warp's copy of the query rows, and the keys of a tile that are its
-    constexpr int kCopies = kCfRows / kRows;
-    constexpr int kCols = kCfTokens / kCopies;
-    const int copy = quad * 32 / kRows;
-    const int key0 = copy * kCols;
+    constexpr int kCopies = R::kCopies, kCols = R::kCols;
+    const int row = quad * R::kWarpRows + (lane & (R::kWarpRows - 1));
+    const int side = R::kHalf ? lane >> 4 : 0;     // of two threads that share a row
+    const int copy = quad * R::kWarpRows / kRows;
+    const int key0 = copy * R::kCopyKeys + side * kCols;
     const int qrow = row & (kRows - 1);            // query row
-    const int warp_row = quad * 32 & (kRows - 1);  // its warp's first
+    const int warp_row = quad * R::kWarpRows & (kRows - 1);  // its warp's first
     uint32_t g = 0;      // tiles of this half so far
     uint32_t tile0 = 0;  // tiles of the pieces so far
     uint32_t pieces = 0;
@@ -840,8 +854,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         tc::fence_after_sync();
         if (warp_live) {
           float s[kCols];
-          if constexpr (kCols == 16) {
-            tc::tmem_ld16(scol + key0, s);
+          if constexpr (R::kHalf) {
+            tc::tmem_ld16x2_16<kCols>(scol + copy * R::kCopyKeys, s);
           } else {
 #pragma unroll
             for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(scol + key0 + e, s + e);
@@ -852,19 +866,20 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           // the weights' buffer: its last product is done (see the issuers)
           const uint32_t pcol = scol + kCfColP + (kWide ? 0 : (g & 1) * kCfPCols);
           auto store = [&](uint32_t col, const uint32_t* w) {
-            if constexpr (kCols == 64) tc::tmem_st16u(col, w);
-            if constexpr (kCols == 32) tc::tmem_st8(col, w);
-            if constexpr (kCols == 16) tc::tmem_st4(col, reinterpret_cast<const float*>(w));
-          };
-          if constexpr (kCopies > 1) {  // the other copies' keys: weights of zero
-            const uint32_t zeros[kCols / 4] = {};
-#pragma unroll
-            for (int o = 1; o < kCopies; ++o) {
-              store(pcol + (copy ^ o) * (kCols / 4), zeros);
-              store(pcol + kCfColLow + (copy ^ o) * (kCols / 4), zeros);
+            if constexpr (R::kHalf) {
+              tc::tmem_st16x2_4<kCols / 4>(col, w);
+            } else if constexpr (kCols == 64) {
+              tc::tmem_st16u(col, w);
+            } else {
+              tc::tmem_st8(col, w);
             }
+          };
+          if constexpr (kCopies > 1) {  // the other copy's keys: weights of zero
+            const uint32_t zeros[kCols / 4] = {};
+            store(pcol + (copy ^ 1) * (R::kCopyKeys / 4), zeros);
+            store(pcol + kCfColLow + (copy ^ 1) * (R::kCopyKeys / 4), zeros);
           }
-          if (warp_seen - tok - key0 < kCols) {  // some row of the warp sees its keys in part
+          if (warp_seen - tok - copy * R::kCopyKeys < R::kCopyKeys) {  // some row of the warp sees its keys in part
             const int lim = seen - tok - key0;
 #pragma unroll
             for (int e = 0; e < kCols; ++e)
@@ -878,6 +893,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             for (int e = 2; e < 16; e += 2) x = fmaxf(fmaxf(x, s[16 * b + e]), s[16 * b + e + 1]);
             mx = fmaxf(mx, fmaf(x, sc[b] * c, sc[kCfTileBlocks + b]));  // (the factor is > 0)
           }
+          if constexpr (R::kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           const bool grow = mx > m + (kWide ? kCfLagHalf : kCfLagParts);  // also true the first time a row sees a key
           const float m_new = grow ? mx : m;
           const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
@@ -886,15 +902,27 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
             if (!ok) break;
             tc::fence_after_sync();
+            if constexpr (R::kHalf) {
 #pragma unroll
-            for (int cc = 0; cc < 8; ++cc) {
-              float o[16];
-              tc::tmem_ld16(scol + kCfColO + 16 * cc, o);
-              tc::tmem_wait_ld();
-              uint32_t w[16];
+              for (int cc = 0; cc < 2; ++cc) {
+                float o[32];
+                tc::tmem_ld16x2_32<64>(scol + kCfColO + 32 * cc, o);
+                tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-              tc::tmem_st16u(scol + kCfColO + 16 * cc, w);
+                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                tc::tmem_st16x2_32<64>(scol + kCfColO + 32 * cc, o);
+              }
+            } else {
+#pragma unroll
+              for (int cc = 0; cc < 8; ++cc) {
+                float o[16];
+                tc::tmem_ld16(scol + kCfColO + 16 * cc, o);
+                tc::tmem_wait_ld();
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                tc::tmem_st16u(scol + kCfColO + 16 * cc, w);
+              }
             }
             tc::tmem_wait_st();
           }
@@ -946,8 +974,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
             }
-            store(pcol + copy * (kCols / 4), hi);
-            store(pcol + kCfColLow + copy * (kCols / 4), lo);
+            store(pcol + copy * (R::kCopyKeys / 4), hi);
+            store(pcol + kCfColLow + copy * (R::kCopyKeys / 4), lo);
             if (ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
               // slots past the context may hold any code: V's rows there are
               // zeroed (a weight of zero is not enough)
@@ -977,6 +1005,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         leave();
       }
       if (!kWide) l *= kCfCodeUnit;  // in O's unit
+      if constexpr (R::kHalf) l += __shfl_xor_sync(0xffffffffu, l, 16);
       // ---- results ----
       if (n_t > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
@@ -1017,12 +1046,13 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         }
         if (valid && !whole) a.part_ml[part_row0 + qrow] = l != 0.f ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
       } else {
-        // Join the two halves' copies: maxima and sums first, then 32 dims a
-        // pass.  A thread joins 4 dims of up to kTake rows.
-        constexpr int kParts = 2 * kCopies;  // partials of a row
-        constexpr int kTake = kRows / 32;
+        // Join the two halves' copies: maxima and sums first, then 32 dims of
+        // each thread a pass.  A thread joins 4 dims of up to kTake rows.
+        constexpr int kParts = 2 * kCopies;          // partials of a row
+        constexpr int kChunks = R::kHalf ? 16 : 8;   // of 4 dims, in a row of the buffer
+        constexpr int kTake = kRows * kChunks / 256;
         float4* buf = reinterpret_cast<float4*>(smem + S::kOffExtra);
-        const int who = t * kCfRows + row;
+        const int who = t * R::kMma + row;
         auto written = [&]() -> bool {  // everyone's part of a pass is there
           mbar_arrive(&bars->join_full);
           return __all_sync(0xffffffffu, mbar_wait(&bars->join_full, passes & 1));
@@ -1040,10 +1070,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         ok = written();
         if (!ok) break;
         float f[kTake][kParts];
-        const int ch = threadIdx.x & 7;
+        const int ch = threadIdx.x & (kChunks - 1);
 #pragma unroll
         for (int k = 0; k < kTake; ++k) {
-          const int rr = (threadIdx.x >> 3) + 32 * k;
+          const int rr = (threadIdx.x + 256 * k) / kChunks;
           float2 ml[kParts];
           float mm = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -1064,28 +1094,32 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         }
         read();
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < 32 / kChunks; ++cc) {
           ok = may_write();
           if (!ok) break;
           if (warp_live && n_t > 0) {
             float o[32];
-            tc::tmem_ld32(scol + kCfColO + 32 * cc, o);
+            if constexpr (R::kHalf)
+              tc::tmem_ld16x2_32<64>(scol + kCfColO + 32 * cc, o);
+            else
+              tc::tmem_ld32(scol + kCfColO + 32 * cc, o);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              buf[who * 8 + (e ^ (row & 7))] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              buf[who * kChunks + side * 8 + (e ^ (row & 7))] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           ok = written();
           if (!ok) break;
+          const int dim0 = 32 * cc + (ch >> 3) * 64;
 #pragma unroll
           for (int k = 0; k < kTake; ++k) {
-            const int rr = (threadIdx.x >> 3) + 32 * k;
+            const int rr = (threadIdx.x + 256 * k) / kChunks;
             if (rr >= live_rows) continue;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < kParts; ++q) {
               if (f[k][q] == 0.f) continue;  // nothing was written for it, or it adds nothing
-              const float4 x = buf[(q * kRows + rr) * 8 + (ch ^ (rr & 7))];
+              const float4 x = buf[(q * kRows + rr) * kChunks + (ch ^ (rr & 7))];
               o.x = fmaf(x.x, f[k][q], o.x);
               o.y = fmaf(x.y, f[k][q], o.y);
               o.z = fmaf(x.z, f[k][q], o.z);
@@ -1093,10 +1127,10 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             }
             if (whole) {
               const int64_t out_row = out_row0 + static_cast<int64_t>(rr >> 2) * hq + (rr & 3);
-              reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim + 32 * cc)[ch] =
+              reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * kHeadDim + dim0)[ch & 7] =
                   make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
             } else {
-              reinterpret_cast<float4*>(a.part_o + (part_row0 + rr) * kHeadDim + 32 * cc)[ch] = o;
+              reinterpret_cast<float4*>(a.part_o + (part_row0 + rr) * kHeadDim + dim0)[ch & 7] = o;
             }
           }
           read();
