@@ -44,11 +44,8 @@
 // keys with scores and weights in one buffer, one chain: 1.09 ms for 4 x 2000
 // queries behind 4000 to 8000 tokens, 57 us for 37 x 7 behind 2,170.)
 //
-// Work is cut by tiles, not by requests: all (request, row tile, KV head) jobs
-// in a row, each counted as its tiles and kCfJobCost more for its start and
-// end, are divided evenly among the CTAs, one per SM, whatever the contexts'
-// lengths are.  A job cut in two or more leaves un-normalised FP32 partials, at
-// most two per CTA, which a second kernel joins.
+// Work is cut by tiles, not by requests (pkv_shares.cuh); a cut job leaves
+// un-normalised FP32 partials.
 //
 // CTA = 16 warps:
 //   warps 0-7: softmax, one thread per row (TMEM lane), a warpgroup per row
@@ -67,6 +64,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
+#include "pkv_shares.cuh"
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
@@ -340,47 +338,12 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     cf_regs_down<kCfOtherRegs>();
     if (warp == 11) {
       // ------------------------ pieces and scales ------------------------
-      // (the host has seen to it that all costs together fit into 31 bits)
-      auto cost = [](int tiles) -> int { return tiles > 0 ? tiles + kCfJobCost : 0; };
-      int total = 0, first32 = 0;  // (and of the first 32 pairs, one a lane)
-      for (int p = lane; p < pairs; p += 32) {
-        const int x = cf_tiles(a, p, n_rt, kPos);
-        if (p < 32) first32 = x;
-        total += cost(x);
-      }
       if (blockIdx.x == 0)
         for (int r = lane; r < a.num_seqs; r += 32)
           if (a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
-      total = __reduce_add_sync(0xffffffffu, total) * a.num_kv_heads;
-      const int grid = gridDim.x;
-      const int per = max((total + grid - 1) / grid, kCfMinShare);
-      const int t0 = per * static_cast<int>(blockIdx.x);
-      int left = min(per, total - t0);  // of this CTA's share (<= 0: none)
-      // the job that the share starts in, and how far into its cost
-      int pair = 0, into = 0, n = 0, kvh = 0;
-      if (left > 0) {
-        int before = 0;
-        for (int p0 = 0;; p0 += 32) {
-          const int x = p0 == 0 ? first32 : (p0 + lane < pairs ? cf_tiles(a, p0 + lane, n_rt, kPos) : 0);
-          int upto = cost(x) * a.num_kv_heads;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
-          }
-          const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
-          if (past != 0) {
-            const int at = __ffs(past) - 1;
-            n = __shfl_sync(0xffffffffu, x, at);
-            const int start = before + __shfl_sync(0xffffffffu, upto, at) - cost(n) * a.num_kv_heads;
-            pair = p0 + at;
-            kvh = (t0 - start) / cost(n);
-            into = (t0 - start) - kvh * cost(n);
-            break;
-          }
-          before += __shfl_sync(0xffffffffu, upto, 31);
-        }
-      }
+      const Share share = find_share(pairs, a.num_kv_heads, kCfJobCost, kCfMinShare, lane,
+                                     [&](int p) -> int { return cf_tiles(a, p, n_rt, kPos); });
+      int pair = share.row, kvh = share.kvh, n = share.tiles, into = share.into, left = share.left;
       auto place = [&](int& r, int& rt) {  // of the pair
         r = n_rt == 1 ? pair : pair / n_rt;
         rt = pair - r * n_rt;
@@ -391,7 +354,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         cut.kvh = kvh;
         cut.n = n;
         cut.into = into;
-        cut.per = per;
+        cut.per = share.per;
         a.cuts[blockIdx.x] = cut;
       }
       uint32_t sets = 0;  // groups of scales written so far
@@ -437,18 +400,15 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         was = now;
         now = CfPiece{};
         while (left > 0 && now.n == 0) {
-          const int end = min(into + left, cost(n));
-          const int begin = max(into - kCfJobCost, 0);
-          const int take = max(end - kCfJobCost, 0) - begin;
-          if (take > 0) {  // (none: the share ends before the job's first tile)
+          int begin, take;
+          take_of_job(n, kCfJobCost, into, left, begin, take);
+          if (take > 0) {
             place(now.r, now.rt);
             now.kvh = kvh;
             now.begin = begin;
             now.take = take;
             now.n = n;
           }
-          left -= end - into;
-          into = 0;
           if (++kvh == a.num_kv_heads) {  // (the next job starts here, if anything is left)
             kvh = 0;
             for (++pair; left > 0 && pair < pairs && (n = cf_tiles(a, pair, n_rt, kPos)) == 0; ++pair) {

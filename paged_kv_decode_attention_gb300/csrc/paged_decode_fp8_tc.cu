@@ -58,6 +58,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
+#include "pkv_shares.cuh"
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
@@ -172,10 +173,8 @@ __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
   return x;
 }
 
-// kScaled: work is cut by tiles, not by requests.  All (request, KV head) rows,
-// each counted as its tiles and kFtJobCost more, are divided evenly among the
-// CTAs; a row cut in two or more leaves un-normalised partials, at most two per
-// CTA, which the joining kernel of the chunks puts together.  (64 requests of 16
+// kScaled: work is cut by tiles, not by requests (pkv_shares.cuh); a cut row
+// leaves un-normalised partials for the chunks' joining kernel.  (64 requests of 16
 // to 16000 tokens: in equal splits of the longest context 184 us; a row counted
 // with 1, 2, 3 or 4 tiles more: 76, 74, 77, 82.)
 __device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
@@ -221,13 +220,9 @@ struct FtWalk {
       return true;
     } else {
       while (left > 0) {
-        const int cost = tiles + kFtJobCost;
-        const int end = min(into + left, cost);
-        const int begin = max(into - kFtJobCost, 0);
-        const int take = max(end - kFtJobCost, 0) - begin;
-        left -= end - into;
-        into = 0;
-        if (take > 0) fill(a, x, begin, take);  // (none: the share ends before the row's first tile)
+        int begin, take;
+        take_of_job(tiles, kFtJobCost, into, left, begin, take);
+        if (take > 0) fill(a, x, begin, take);
         if (++kvh == a.num_kv_heads) {
           kvh = 0;
           for (++r; left > 0 && r < a.num_seqs && (tiles = ft_tiles(a, r)) == 0; ++r) {
@@ -253,49 +248,20 @@ __device__ __forceinline__ FtWalk<kMode> ft_start(const DecodeArgs& a, int lane,
     w.into = part * blockIdx.y;  // (the first tile here)
     w.left = min(part, w.tiles - w.into);
   } else if constexpr (kMode == FtMode::kScaled) {
-    // (the host has seen to it that all costs together fit into 31 bits)
-    auto cost = [](int tiles) -> int { return tiles > 0 ? tiles + kFtJobCost : 0; };
-    int total = 0, first32 = 0;  // (and of the first 32 requests, one a lane)
-    for (int r = lane; r < a.num_seqs; r += 32) {
-      const int x = ft_tiles(a, r);
-      if (r < 32) first32 = x;
-      total += cost(x);
-    }
-    total = __reduce_add_sync(0xffffffffu, total) * a.num_kv_heads;
-    const int grid = gridDim.x;
-    const int per = max((total + grid - 1) / grid, kFtMinShare);
-    const int t0 = per * static_cast<int>(blockIdx.x);
-    w.left = min(per, total - t0);
-    if (w.left > 0) {
-      int before = 0;
-      for (int r0 = 0;; r0 += 32) {
-        const int x = r0 == 0 ? first32 : (r0 + lane < a.num_seqs ? ft_tiles(a, r0 + lane) : 0);
-        int upto = cost(x) * a.num_kv_heads;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, off);
-          if (lane >= off) upto += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
-        if (past != 0) {
-          const int at = __ffs(past) - 1;
-          w.tiles = __shfl_sync(0xffffffffu, x, at);
-          const int start = before + __shfl_sync(0xffffffffu, upto, at) - cost(w.tiles) * a.num_kv_heads;
-          w.r = r0 + at;
-          w.kvh = (t0 - start) / cost(w.tiles);
-          w.into = (t0 - start) - w.kvh * cost(w.tiles);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
+    const Share s = find_share(a.num_seqs, a.num_kv_heads, kFtJobCost, kFtMinShare, lane,
+                               [&](int r) -> int { return ft_tiles(a, r); });
+    w.r = s.row;
+    w.kvh = s.kvh;
+    w.tiles = s.tiles;
+    w.into = s.into;
+    w.left = s.left;
     if (cut != nullptr && lane == 0) {
       CfCut c{};
-      c.r = w.r;
-      c.kvh = w.kvh;
-      c.n = w.tiles;
-      c.into = w.into;
-      c.per = per;
+      c.r = s.row;
+      c.kvh = s.kvh;
+      c.n = s.tiles;
+      c.into = s.into;
+      c.per = s.per;
       *cut = c;
     }
   }
