@@ -723,8 +723,8 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
  *
  * Packed sequences: the tokens of num_seqs sequences lie one behind the other,
  * sequence s at rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device int32
- * [num_seqs + 1], not falling, from 0 up to num_tokens; lengths may be 0).
- * Rows behind the last sequence are padding.  Entries that fall or leave
+ * [num_seqs + 1], not falling, within 0 .. num_tokens; lengths may be 0).
+ * Rows before the first and behind the last sequence are padding.  Entries that fall or leave
  * 0 .. num_tokens set PKV_DEVERR_SEQLENS; they are clamped and a sequence of
  * negative length counts as empty.
  * ---------------------------------------------------------------------------

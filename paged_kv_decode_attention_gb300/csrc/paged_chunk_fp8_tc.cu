@@ -338,9 +338,6 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     cf_regs_down<kCfOtherRegs>();
     if (warp == 11) {
       // ------------------------ pieces and scales ------------------------
-      if (blockIdx.x == 0)
-        for (int r = lane; r < a.num_seqs; r += 32)
-          if (a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
       const Share share = find_share(pairs, a.num_kv_heads, kCfJobCost, kCfMinShare, lane,
                                      [&](int p) -> int { return cf_tiles(a, p, n_rt, kPos); });
       int pair = share.row, kvh = share.kvh, n = share.tiles, into = share.into, left = share.left;
@@ -719,6 +716,9 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     const uint32_t scol = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * kCfTileCols;
     const int row_tile = kWide ? t : 0;  // row tile of this warpgroup's rows
 
+    if (blockIdx.x == 0)
+      for (int r = threadIdx.x; r < a.num_seqs; r += 256)
+        if (a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
     // rows that see no key at all belong to no piece: zeros
     for (int p = blockIdx.x; p < pairs; p += gridDim.x) {
       if (cf_tiles(a, p, n_rt, kPos) > 0) continue;

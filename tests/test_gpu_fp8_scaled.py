@@ -331,8 +331,8 @@ def run_attention(q, kc, vc, ks, vs, t, ctx):
 @pytest.mark.parametrize("hkv", [1, 2, 8])
 @pytest.mark.parametrize("q_len,ctx", [
     (1, [1]), (1, [16, 17, 15, 0]), (1, [300, 1, 255, 256, 257, 1000]), (1, [5000]), (1, [33] * 60),
-    (2, [2, 1, 0, 40]), (3, [700, 2]), (7, [129, 128, 7, 3, 0, 260]), (16, [16, 500]), (31, [31, 200]),
-    (33, [33, 40, 1000]), (64, [300, 64, 20]), (65, [65, 1500]), (200, [200, 777])])
+    (2, [2, 1, 0, 40]), (3, [700, 2]), (4, [65, 600]), (5, [66, 300]), (7, [129, 128, 7, 3, 0, 260]), (8, [8, 400, 64]),
+    (9, [9, 63, 400]), (16, [16, 500]), (17, [17, 900]), (31, [31, 200]), (32, [32, 33, 500]), (33, [33, 40, 1000]), (64, [300, 64, 20]), (65, [65, 1500]), (200, [200, 777])])
 def test_attention(q_len, ctx, hkv):
     case = attention_case(ctx, q_len, hkv)
     out = run_attention(*case, ctx)
@@ -426,6 +426,29 @@ def test_captured_and_two_streams(q_len):
         graph.replay()
         torch.cuda.synchronize()
         check(out, reference(q, kc, vc, ks, vs, t, c), c)
+
+
+def test_pools_beyond_32_bits():
+    """Blocks whose codes lie past 4 GiB of their pool: appended to, copied and attended."""
+    pkv = _pkv()
+    hkv, nb = 16, 140000  # 4.6 GB a pool
+    kc, vc = (torch.zeros((nb, hkv, BLOCK, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((nb, hkv), device="cuda") for _ in range(2))
+    t = np.array([[nb - 1, 7, nb - 2, nb - 3], [nb - 9, nb - 5, 3, -1]], np.int32)
+    ctx = [60, 33]
+    x = [torch.randn((93, hkv, D), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    pkv.kv_append_fp8_scaled(kc, vc, ks, vs, dev(t), dev(ctx), x[0], x[1], dev([0, 60, 93]))
+    pkv.copy_blocks_fp8_scaled(kc, vc, ks, vs, dev([nb - 3]), dev([nb - 4]))
+    t[0, 3] = nb - 4
+    used = sorted({int(b) for b in t.reshape(-1) if b >= 0})
+    small = {b: i for i, b in enumerate(used)}
+    u = np.vectorize(lambda b: small.get(int(b), -1))(t).astype(np.int32)
+    parts = [z[dev(used, torch.int64)] for z in (kc, vc, ks, vs)]
+    for q_len in (1, 6, 40):
+        q = torch.randn((2, q_len, 4 * hkv, D), device="cuda").to(torch.bfloat16)
+        out = run_attention(q, kc, vc, ks, vs, t, ctx)
+        check(out, reference(q, *parts, u, ctx), ctx)
+    assert pkv.get_device_error() == 0
 
 
 # ---------------------------------------------------------------------------

@@ -210,6 +210,22 @@ def test_captured_with_other_lengths_and_on_another_stream():
         assert bool((out[sum(lens):] == 7).all())
 
 
+def test_rows_beyond_32_bits():
+    """A prompt whose rows lie past 4 GiB of q and of out, behind rows of none."""
+    pkv = _pkv()
+    t, n = 560000, 300
+    q, k, v, _ = _inputs([n], 8, 4)
+    big = [torch.empty((t, x.shape[1], D), dtype=torch.bfloat16, device="cuda") for x in (q, k, v)]
+    for b, x in zip(big, (q, k, v)):
+        b[t - n - 5:t - 5] = x
+    out = torch.empty_like(big[0])
+    pkv.prompt_attention(out, *big, torch.tensor([t - n - 5, t - 5], dtype=torch.int32, device="cuda"), SCALE)
+    want = torch.empty_like(q.contiguous())
+    pkv.prompt_attention(want, q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), SCALE)
+    assert pkv.get_device_error() == 0
+    assert torch.equal(out[t - n - 5:t - 5], want)
+
+
 def test_two_streams_at_once():
     pkv = _pkv()
     lens = [[700, 300], [64, 1100]]
