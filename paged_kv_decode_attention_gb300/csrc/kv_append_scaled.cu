@@ -12,8 +12,8 @@
 // E4M3's normal range (2^-6), and rounded to nearest there.  A block's first
 // token starts it anew, whatever it held.
 //
-// One warp owns a (block, KV head, K or V) of the call, so nothing is shared:
-// 16 lanes a token of 16 bytes, up to 8 loads in flight, the largest magnitude
+// One warp owns a (block, KV head) of the call, K and V, so nothing is shared:
+// 16 lanes a token of 16 bytes, up to 16 loads in flight, the largest magnitude
 // by one reduction over BF16 bits (their order is that of integers).  Bound by
 // HBM for prompts and by a chain of four dependent reads (request, context,
 // block, its scale) for single tokens.
@@ -23,7 +23,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kAsWarps = 4;
+constexpr int kAsWarps = 1;
 constexpr int kAsLowest = -32, kAsHighest = 32;  // exponents of the scales
 
 // 4 BF16 values (two words) times `f`, as E4M3 bytes (nearest even, saturating).
@@ -84,11 +84,9 @@ __global__ void __launch_bounds__(kAsWarps * 32) kv_append_scaled_kernel(const A
     if (bad) report(a.err, PKV_DEVERR_SEQLENS);
   }
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kAsWarps + (threadIdx.x >> 5); item < items; item += warps) {
-    // item = (place * 2 + which) * Hkv + h
-    const int h = static_cast<int>(item % a.num_kv_heads);
-    const int64_t rest = item / a.num_kv_heads;
-    const int which = static_cast<int>(rest & 1);
-    const int64_t place = rest >> 1;
+    // item = place * Hkv + h
+    const int64_t place = item / a.num_kv_heads;
+    const int h = static_cast<int>(item - place * a.num_kv_heads);
     int r;
     if (a.cu_new == nullptr) {
       r = static_cast<int>(place);
@@ -104,7 +102,7 @@ __global__ void __launch_bounds__(kAsWarps * 32) kv_append_scaled_kernel(const A
       }
       r = lo;
     }
-    const bool once = lane == 0 && which == 0 && h == 0;
+    const bool once = lane == 0 && h == 0;
     const int64_t nth = place - first_place(a, r);  // of the request's touched blocks
     const int t0 = a.cu_new == nullptr ? r : a.cu_new[r];
     const int t1 = a.cu_new == nullptr ? r + 1 : a.cu_new[r + 1];
@@ -123,62 +121,72 @@ __global__ void __launch_bounds__(kAsWarps * 32) kv_append_scaled_kernel(const A
     const int first = max(p0 - static_cast<int>(lb) * kBlockSize, 0);          // offsets [first, end) are new,
     const int end = min(ctx - static_cast<int>(lb) * kBlockSize, kBlockSize);  // [0, first) hold tokens
     const int tok = t0 + static_cast<int>(lb) * kBlockSize + first - p0;       // the token at offset `first`
-    const uint16_t* src = (which ? a.v_new : a.k_new) + static_cast<int64_t>(tok) * (which ? a.v_stride : a.k_stride) +
-                          static_cast<int64_t>(h) * kHeadDim + (lane & 15) * 8;
-    const int64_t stride = which ? a.v_stride : a.k_stride;
     // lane l: 8 values of the tokens first + l / 16, + 2, + 4, ...
-    uint4 w[8];
     const int half = lane >> 4;
+    const int64_t in_row = static_cast<int64_t>(h) * kHeadDim + (lane & 15) * 8;
+    uint4 w[2][8];  // K, V
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      w[k] = make_uint4(0, 0, 0, 0);
-      if (first + 2 * k + half < end) w[k] = *reinterpret_cast<const uint4*>(src + (2 * k + half) * stride);
+    for (int which = 0; which < 2; ++which) {
+      const int64_t stride = which ? a.v_stride : a.k_stride;
+      const uint16_t* src = (which ? a.v_new : a.k_new) + (static_cast<int64_t>(tok) + half) * stride + in_row;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[which][k] = make_uint4(0, 0, 0, 0);
+        if (first + 2 * k + half < end) w[which][k] = *reinterpret_cast<const uint4*>(src + 2 * k * stride);
+      }
     }
     if (blk < 0 || blk >= a.num_blocks) {
       if (once) report(a.err, PKV_DEVERR_BLOCK_ID);
       continue;
     }
     const int64_t at = static_cast<int64_t>(blk) * a.num_kv_heads + h;
-    float* scale_at = (which ? a.v_scales : a.k_scales) + at;
-    const float old = first > 0 ? *scale_at : 0.f;
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
+    float old[2] = {0.f, 0.f};
+    if (first > 0) {
+      old[0] = a.k_scales[at];
+      old[1] = a.v_scales[at];
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    // 448 = 1.75 * 2^8: the exponent field less (127 + 8), one more above 1.75
-    int e = static_cast<int>(top >> 7) - 135 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-    e = min(max(e, kAsLowest), kAsHighest);
-    const float need = __int_as_float((127 + e) << 23);
-    const float scale = fmaxf(old, need);
-    uint8_t* tile = (which ? a.v_cache : a.k_cache) + at * kFp8TileBytes + (lane & 15) * 8;
-    const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
-    const float inv = 1.f / scale;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int off = first + 2 * k + half;
-      if (off < end) {
-        uint2 c;
-        if (power) {
-          c = make_uint2(as_codes(w[k].x, w[k].y, inv), as_codes(w[k].z, w[k].w, inv));
-        } else {
-          c = make_uint2(as_codes_div(w[k].x, w[k].y, scale), as_codes_div(w[k].z, w[k].w, scale));
+    for (int which = 0; which < 2; ++which) {
+      uint32_t top = 0;  // pairs of magnitudes
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint4 x = w[which][k];
+        top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+      }
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+      // 448 = 1.75 * 2^8: the exponent field less (127 + 8), one more above 1.75
+      int e = static_cast<int>(top >> 7) - 135 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+      e = min(max(e, kAsLowest), kAsHighest);
+      const float need = __int_as_float((127 + e) << 23);
+      const float scale = fmaxf(old[which], need);
+      uint8_t* tile = (which ? a.v_cache : a.k_cache) + at * kFp8TileBytes + (lane & 15) * 8;
+      const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
+      const float inv = 1.f / scale;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int off = first + 2 * k + half;
+        if (off < end) {
+          const uint4 x = w[which][k];
+          uint2 c;
+          if (power) {
+            c = make_uint2(as_codes(x.x, x.y, inv), as_codes(x.z, x.w, inv));
+          } else {
+            c = make_uint2(as_codes_div(x.x, x.y, scale), as_codes_div(x.z, x.w, scale));
+          }
+          *reinterpret_cast<uint2*>(tile + off * kHeadDim) = c;
         }
-        *reinterpret_cast<uint2*>(tile + off * kHeadDim) = c;
       }
-    }
-    if (first > 0 && scale > old) {  // the earlier tokens follow the scale
-      const float f = __fdiv_rn(old, scale);
-      for (int off = half; off < first; off += 2) {
-        uint2* p = reinterpret_cast<uint2*>(tile + off * kHeadDim);
-        const uint2 c = *p;
-        *p = make_uint2(as_rescale(c.x, f), as_rescale(c.y, f));
+      if (first > 0 && scale > old[which]) {  // the earlier tokens follow the scale
+        const float f = __fdiv_rn(old[which], scale);
+        for (int off = half; off < first; off += 2) {
+          uint2* p = reinterpret_cast<uint2*>(tile + off * kHeadDim);
+          const uint2 c = *p;
+          *p = make_uint2(as_rescale(c.x, f), as_rescale(c.y, f));
+        }
       }
+      if (lane == 0 && scale != old[which]) (which ? a.v_scales : a.k_scales)[at] = scale;
     }
-    if (lane == 0 && scale != old) *scale_at = scale;
   }
 }
 
@@ -210,7 +218,7 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_kv_append_scaled(const AppendScaledArgs& a, cudaStream_t stream) {
   const int64_t places =
       a.cu_new == nullptr ? a.num_seqs : static_cast<int64_t>(a.num_tokens) / kBlockSize + 2 * static_cast<int64_t>(a.num_seqs);
-  const int64_t items = places * 2 * a.num_kv_heads;
+  const int64_t items = places * a.num_kv_heads;
   int64_t blocks = (items + kAsWarps - 1) / kAsWarps;
   if (blocks > 1 << 20) blocks = 1 << 20;
   return launch_pdl(kv_append_scaled_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kAsWarps * 32), 0, stream, 1, a,
