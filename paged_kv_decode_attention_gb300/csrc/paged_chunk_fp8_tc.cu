@@ -117,6 +117,9 @@ constexpr float kCfLagHalf = 8.f;
 // of that.
 constexpr float kCfFactor = -2.f;
 constexpr float kCfCodeUnit = 256.f;
+// Least factor of a score: below it scores are as good as zero, and a product
+// of scales that vanishes would turn masked ones, -inf, into NaN.
+constexpr float kCfLeast = 0x1p-100f;
 // In tiles: what a job costs besides its tiles, and the least worth a CTA.
 constexpr int kCfJobCost = 8;
 constexpr int kCfMinShare = 12;
@@ -851,7 +854,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             float x = fmaxf(s[16 * b], s[16 * b + 1]);
 #pragma unroll
             for (int e = 2; e < 16; e += 2) x = fmaxf(fmaxf(x, s[16 * b + e]), s[16 * b + e + 1]);
-            mx = fmaxf(mx, fmaf(x, sc[b] * c, sc[kCfTileBlocks + b]));  // (the factor is > 0)
+            mx = fmaxf(mx, fmaf(x, fmaxf(sc[b] * c, kCfLeast), sc[kCfTileBlocks + b]));  // (the factor is > 0)
           }
           if constexpr (R::kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           const bool grow = mx > m + (kWide ? kCfLagHalf : kCfLagParts);  // also true the first time a row sees a key
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             uint32_t w[8 * kCfTileBlocks];
 #pragma unroll
             for (int b = 0; b < kCfTileBlocks; ++b) {
-              const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
+              const float kc = fmaxf(sc[b] * c, kCfLeast), off = sc[kCfTileBlocks + b] + nm;
               const float2 k2 = make_float2(kc, kc);
               const float2 n2 = make_float2(off, off);
               float2 acc = make_float2(0.f, 0.f);
@@ -917,7 +920,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             uint32_t hi[kCols / 4], lo[kCols / 4];
 #pragma unroll
             for (int b = 0; b < kCols / kBlockSize; ++b) {
-              const float kc = sc[b] * c, off = sc[kCfTileBlocks + b] + nm;
+              const float kc = fmaxf(sc[b] * c, kCfLeast), off = sc[kCfTileBlocks + b] + nm;
               const float2 k2 = make_float2(kc, kc);
               const float2 n2 = make_float2(off, off);
               float2 acc = make_float2(0.f, 0.f);

@@ -386,6 +386,17 @@ def test_small_v_scale_under_most_of_the_weight(q_len):
     check(run_attention(*case, ctx), reference(*case, ctx), ctx)
 
 
+@pytest.mark.parametrize("q_len", [1, 3, 12, 20, 48])
+def test_queries_and_scales_whose_product_vanishes(q_len):
+    """Scores whose factor leaves FP32's range: the masked places stay masked, the others weigh the same."""
+    ctx = [200, 70]
+    q, kc, vc, ks, vs, t = attention_case(ctx, q_len, 2)
+    q = (q.float() * 2.0 ** -124).to(torch.bfloat16)
+    ks.fill_(2.0 ** -32)
+    case = (q, kc, vc, ks, vs, t)
+    check(run_attention(*case, ctx), reference(*case, ctx), ctx)
+
+
 @pytest.mark.parametrize("q_len", [1, 5, 70])
 def test_bad_tables_and_contexts_are_reported(q_len):
     pkv = _pkv()
