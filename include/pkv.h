@@ -724,9 +724,8 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
  * Packed sequences: the tokens of num_seqs sequences lie one behind the other,
  * sequence s at rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device int32
  * [num_seqs + 1], not falling, within 0 .. num_tokens; lengths may be 0).
- * Rows before the first and behind the last sequence are padding.  Entries that fall or leave
- * 0 .. num_tokens set PKV_DEVERR_SEQLENS; they are clamped and a sequence of
- * negative length counts as empty.
+ * Rows before the first and behind the last sequence are padding.  Entries that
+ * fall or leave 0 .. num_tokens set PKV_DEVERR_SEQLENS.
  * ---------------------------------------------------------------------------
  */
 
@@ -734,7 +733,9 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
  * pkv_prompt_attention -- causal attention of packed prompts: token i of a
  * prompt sees its tokens 0 .. i.
  *   out          : device BF16 [num_tokens][num_q_heads][128], 16-byte aligned.
- *                  Rows of no prompt are left as they are.
+ *                  Rows of no prompt are left as they are.  (A wrong entry of
+ *                  cu_seqlens is clamped to 0 .. num_tokens, and a prompt of
+ *                  negative length counts as empty.)
  *   out_lse      : device FP32 [num_tokens][num_q_heads] or NULL: the natural
  *                  log-sum-exp of each row's scaled logits (what
  *                  pkv_attn_combine takes).
@@ -783,7 +784,8 @@ pkv_status pkv_prompt_attention(void* out, float* out_lse, const void* q, int64_
  *                  rows cu_new[r] .. cu_new[r + 1] - 1 of k_new and v_new
  *                  (packed as above); NULL = one each, num_tokens == num_seqs.
  *   k_new, v_new : device BF16, strides as for pkv_prompt_attention.  Finite.
- * A request with context_lens[r] <= 0 is a padding row.  One whose context is
+ * A request whose entries of cu_new fall or leave 0 .. num_tokens is not stored.
+ * One with context_lens[r] <= 0 is a padding row.  One whose context is
  * shorter than its new tokens or longer than its table sets
  * PKV_DEVERR_CONTEXT and nothing of it is stored; a block id outside the pool
  * sets PKV_DEVERR_BLOCK_ID and that block is skipped.  A block that new tokens
@@ -807,6 +809,13 @@ pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scale
  *                  must be stream-ordered.
  * Codes of every token of the context must be finite (no 0x7f, 0xff); slots
  * past it may hold anything.
+ * Queries enter as two E4M3 parts (off by at most 2^-17 of a head's largest
+ * value).  Weights times their V scale enter, up to q_len 32, as two E4M3 parts
+ * (off by at most 2^-8 of each or 2^-16 of the row's largest one), beyond that
+ * as FP16 (2^-11 of each or 2^-25 of the largest); the sum that divides them is
+ * that of the unrounded ones.  A call's result is bitwise
+ * reproducible, but where a request's keys are divided among CTAs, and so its
+ * last bits, follow from the whole batch's lengths.
  */
 size_t pkv_workspace_size_fp8_scaled(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
                                      int32_t max_blocks_per_seq);

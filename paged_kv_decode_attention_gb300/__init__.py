@@ -902,7 +902,8 @@ def paged_attention_fp8_scaled(out: torch.Tensor, q: torch.Tensor, k_cache: torc
     """paged_attention over pools of E4M3 codes with block scales (value = code * scale): one query token per request
     or a causal chunk of q_len.  q, out [B][q_len][Hq][128]; workspace >= workspace_size_fp8_scaled(...) bytes."""
     _done(_binding().paged_attention_fp8_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
-                                                context_lens, q_len, scale, workspace, _raw(stream)), "pkv_paged_attention_fp8_scaled")
+                                                context_lens, q_len, scale, workspace, _raw(stream)),
+          "pkv_paged_attention_fp8_scaled")
 
 
 def copy_blocks_fp8_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
