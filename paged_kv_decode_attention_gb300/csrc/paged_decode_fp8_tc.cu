@@ -65,7 +65,16 @@ namespace pkv {
 namespace {
 
 constexpr int kFtStages = 3;
-constexpr int kFtThreads = 256;
+// The decodes of this file.
+enum class FtMode {
+  kPlain,
+  kFused,         // stores each request's new token and uses it
+  kScaled,        // codes times a scale for each block and KV head
+  kScaledCluster  // the same, a thread-block cluster to a (request, KV head)
+};
+__host__ __device__ constexpr bool ft_scaled(FtMode m) { return m == FtMode::kScaled || m == FtMode::kScaledCluster; }
+// (kScaled: four warps more, for the results)
+__host__ __device__ constexpr int ft_threads(FtMode m) { return m == FtMode::kScaled ? 384 : 256; }
 constexpr int kFtTileBlocks = 16;                          // blocks per tile
 constexpr int kFtTileTokens = kFtTileBlocks * kBlockSize;  // 256 tokens: two 128-token halves
 constexpr int kFtBoxBytes = kBlockSize * kHeadDim;         // one block's 16 x 128 bytes: 2 KiB
@@ -83,7 +92,10 @@ constexpr int kOffKnAt = kOffKn + 2 * kHeadDim;            // int [2]: where eac
 constexpr int kFtScaleSlots = 8;                           // block scales: tiles held
 constexpr int kOffScale = kOffKnAt + 16;                   // float [8 tiles][K, V][16 blocks]
 constexpr int kOffPart = kOffScale + kFtScaleSlots * 2 * kFtTileBlocks * 4;  // float2 [4]: a partial's maxima and sums
-constexpr int kOffBar = kOffPart + 32;
+constexpr int kFtSigmaSlots = 4;                           // a slot is written again once S of the unit 2 on is done
+constexpr int kOffSigma = kOffPart + 32;                   // kScaled: float [4 units][4 heads], scale / sigma
+constexpr int kOffEnds = kOffSigma + kFtSigmaSlots * kGroup * 4;  // FtEnd [2], by unit parity
+constexpr int kOffBar = kOffEnds + 2 * 96;
 constexpr int kSmemFt = kOffBar + 512;
 constexpr uint32_t kColS = 0;    // S^T buffers at columns 0 and 32 (16 columns per half)
 constexpr uint32_t kColO = 64;   // O^T buffers at columns 64 and 80
@@ -95,10 +107,19 @@ constexpr float kFtLn2 = 0.6931471805599453f;
 constexpr int kFtNamedBar = 1;          // the softmax warps' barrier
 
 static_assert(kSmemFt <= 227 * 1024, "one CTA per SM");
+static_assert(kOffSigma % 16 == 0 && kOffEnds % 16 == 0 && kOffBar % 8 == 0, "alignment");
 static_assert(kFtTileTokens == 2 * 128, "a tile is two 128-token MMA halves");
 static_assert(kOffV % 1024 == 0 && kOffQp % 1024 == 0 && kOffPt % 1024 == 0 && kFtOpBytes % 1024 == 0,
               "swizzled operands need 1 KiB alignment");
 static_assert(kFtLazyMax + 6.f <= 8.f, "scaled weights must stay inside E4M3's range");
+
+// What the softmax leaves of a unit for the warps that finish it.
+struct alignas(16) FtEnd {
+  float l[4][4];  // a warp's sums, by head
+  float m[4];
+  int4 unit;      // output row, place of a partial, whole or not; w = 0: no more units
+};
+static_assert(sizeof(FtEnd) == 96, "size");
 
 struct FtBars {
   uint64_t k_full[kFtStages];
@@ -113,19 +134,12 @@ struct FtBars {
   uint64_t p_empty[2];
   uint64_t o_full[2];
   uint64_t o_empty[2];
+  uint64_t fin_full[2], fin_empty[2];  // kScaled: a unit's end is there, is read
   uint64_t scale_full[kFtScaleSlots];  // kScaled; a slot is written again 8 tiles on, past what the rings let run ahead
   uint32_t tmem_base;
 };
 static_assert(sizeof(FtBars) <= 512, "barrier area");
 
-// The decodes of this file.
-enum class FtMode {
-  kPlain,
-  kFused,         // stores each request's new token and uses it
-  kScaled,        // codes times a scale for each block and KV head
-  kScaledCluster  // the same, a thread-block cluster to a (request, KV head)
-};
-__host__ __device__ constexpr bool ft_scaled(FtMode m) { return m == FtMode::kScaled || m == FtMode::kScaledCluster; }
 
 // kScaled: in tiles, what a (request, KV head) costs besides its tiles, and the
 // least worth a CTA.
@@ -192,14 +206,19 @@ template <FtMode kMode>
 struct FtWalk {
   int u;                            // !kScaled: the next unit
   int r, kvh, tiles, into, left;    // kScaled: the next row, how far into its cost, what is left of the share
+  int ctx;                          // the row's
+
+  // Tiles of row r, which the walk comes to.
+  __device__ __forceinline__ int enter(const DecodeArgs& a) {
+    ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
+    return (ctx + kFtTileTokens - 1) / kFtTileTokens;
+  }
 
   // The unit of `take` tiles from tile `begin` of row (r, kvh).
   __device__ __forceinline__ void fill(const DecodeArgs& a, FtUnit& x, int begin, int take) const {
     x.r = r;
     x.kvh = kvh;
     x.split = begin == 0 ? 1 : 0;  // place of a partial
-    x.ctx_raw = a.context_lens[r];
-    const int ctx = min(x.ctx_raw, a.max_blocks * kBlockSize);
     x.b0 = begin * kFtTileBlocks;
     x.b1 = min((ctx + kBlockSize - 1) / kBlockSize, (begin + take) * kFtTileBlocks);
     x.n_tiles = take;
@@ -225,7 +244,7 @@ struct FtWalk {
         if (take > 0) fill(a, x, begin, take);
         if (++kvh == a.num_kv_heads) {
           kvh = 0;
-          for (++r; left > 0 && r < a.num_seqs && (tiles = ft_tiles(a, r)) == 0; ++r) {
+          for (++r; left > 0 && r < a.num_seqs && (tiles = enter(a)) == 0; ++r) {
           }
         }
         if (take > 0) return true;
@@ -243,7 +262,7 @@ __device__ __forceinline__ FtWalk<kMode> ft_start(const DecodeArgs& a, int lane,
   if constexpr (kMode == FtMode::kScaledCluster) {
     w.r = blockIdx.x / a.num_kv_heads;
     w.kvh = blockIdx.x - w.r * a.num_kv_heads;
-    w.tiles = ft_tiles(a, w.r);
+    w.tiles = w.enter(a);
     const int part = (w.tiles + kMaxClusterSplits - 1) / kMaxClusterSplits;
     w.into = part * blockIdx.y;  // (the first tile here)
     w.left = min(part, w.tiles - w.into);
@@ -252,7 +271,7 @@ __device__ __forceinline__ FtWalk<kMode> ft_start(const DecodeArgs& a, int lane,
                                [&](int r) -> int { return ft_tiles(a, r); });
     w.r = s.row;
     w.kvh = s.kvh;
-    w.tiles = s.tiles;
+    w.tiles = s.left > 0 ? w.enter(a) : 0;
     w.into = s.into;
     w.left = s.left;
     if (cut != nullptr && lane == 0) {
@@ -349,6 +368,18 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
   return ok;
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ float ft_sel4(const float* v, int k) {
   return k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
 }
@@ -397,13 +428,14 @@ __device__ __forceinline__ float q_sigma(uint32_t amax_bits) {
 // the softmax's own weights is that of w_t / (v scale_t), all on the CUDA cores
 // in FP32.  (Scales between 2^-32 and 2^32 leave the sum 62 binades.)
 template <FtMode kMode>
-__global__ void __launch_bounds__(kFtThreads, 1)
+__global__ void __launch_bounds__(ft_threads(kMode), 1)
     paged_decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                                const DecodeArgs a) {
   pdl_trigger();
   constexpr bool kFused = kMode == FtMode::kFused;
   constexpr bool kScaled = ft_scaled(kMode);
   constexpr bool kCluster = kMode == FtMode::kScaledCluster;
+  constexpr bool kFinish = kMode == FtMode::kScaled;  // units are finished by warps of their own
   constexpr FtMode kWalk = kScaled ? kMode : FtMode::kPlain;  // of the warps that need not know the new tokens
   extern __shared__ __align__(1024) uint8_t smem[];
   FtBars* bars = reinterpret_cast<FtBars*>(smem + kOffBar);
@@ -414,12 +446,13 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   // and sums behind it
   float* part_o = reinterpret_cast<float*>(smem + kOffK);
   float2* part_ml = reinterpret_cast<float2*>(smem + kOffPart);
+  FtEnd* ends = reinterpret_cast<FtEnd*>(smem + kOffEnds);
   const int num_units = a.num_seqs * a.num_kv_heads * a.num_splits;
   const int hq = a.num_kv_heads * kGroup;
 
   // ---------------- set-up ----------------
   // Qp and P^T rows past the ones written per unit / tile stay zero.
-  for (int idx = threadIdx.x; idx < 6 * kFtOpBytes / 16; idx += kFtThreads)
+  for (int idx = threadIdx.x; idx < 6 * kFtOpBytes / 16; idx += ft_threads(kMode))
     reinterpret_cast<uint4*>(smem + kOffQp)[idx] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async_smem();
   if (threadIdx.x == 0) {
@@ -438,6 +471,10 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       mbar_init(&bars->p_empty[b], 1);
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_empty[b], 128);
+    }
+    for (int s = 0; kFinish && s < 2; ++s) {
+      mbar_init(&bars->fin_full[s], 4);
+      mbar_init(&bars->fin_empty[s], 4);
     }
     for (int s = 0; kScaled && s < kFtScaleSlots; ++s) mbar_init(&bars->scale_full[s], 32);
     fence_barrier_init();
@@ -459,6 +496,53 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   const uint32_t sbase = smem_addr(smem);
   bool ok = true;
+
+  // A unit's result (the nth in turn), by the 128 threads of four warps: dim t of
+  // the 4 heads.
+  auto results = [&](int t, int nth, int64_t orow0, bool direct, int split, const float (&m)[4], const float (&lsum)[4]) {
+    const int ub = nth & 1;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (nth >> 1) & 1));
+    if (ok) {
+      tc::fence_after_sync();
+      float o8[8];
+      tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o8);  // dim t: heads 0..3, high parts then remainders
+      tc::tmem_wait_ld();
+      tc::fence_before_sync();
+      mbar_arrive(&bars->o_empty[ub]);
+      float o[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) o[h] = (o8[h] + o8[4 + h]) * kFtPUnscale;
+      if constexpr (kCluster) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
+        if (t < kGroup) part_ml[t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
+      } else if (direct) {
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
+          dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
+        }
+      } else if constexpr (kScaled) {  // un-normalised
+        const int64_t row = (2 * static_cast<int64_t>(blockIdx.x) + split) * kGroup;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) a.part_o[(row + h) * kHeadDim + t] = o[h];
+        if (t < kGroup) a.part_ml[row + t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
+          a.part_o[((orow0 + h) * a.num_splits + split) * kHeadDim + t] = o[h] * inv;
+        }
+        if (t < kGroup) {
+          const float ls = ft_sel4(lsum, t);
+          a.part_lse[(orow0 + t) * a.num_splits + split] =
+              ls > 0.f ? (ft_sel4(m, t) + log2f(ls)) * kFtLn2 : -INFINITY;
+        }
+      }
+    }
+  };
 
   if (warp == 0 || warp == 1) {
     // ------------------------------ producers ------------------------------
@@ -650,6 +734,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       uint8_t* dst = smem + kOffQp + ub * kFtOpBytes;
       *reinterpret_cast<uint4*>(dst + tc::sw128_offset_b8(h, 16 * c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(dst + tc::sw128_offset_b8(4 + h, 16 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if (kScaled && c == 0)
+        reinterpret_cast<float*>(smem + kOffSigma)[(seq % kFtSigmaSlots) * kGroup + h] = a.scale_log2 * (1.f / sigma);
       if (kFused) {
         reinterpret_cast<uint32_t*>(smem + kOffKn + ub * kHeadDim)[lane] = kn_word;
         if (lane == 0) reinterpret_cast<int*>(smem + kOffKnAt)[ub] = kn_at;
@@ -659,7 +745,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       ++seq;
     }
     if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
-  } else {
+  } else if (!kFinish || warp < 8) {
     // ------------------------------ softmax ------------------------------
     const int w = warp & 3;           // TMEM sub-partition
     const int t = threadIdx.x - 128;  // tokens t and 128 + t of the tile (TMEM lane t); at a unit's end, the output dim
@@ -717,8 +803,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       const int ub = seq & 1;
       // the query operand's scale of each head, taken from the query exactly
       // as the query-operand warp takes it: scores / sigma_h in base 2
-      float c[4];
-      {
+      // (kScaled: read from where that warp leaves it, with the first scores)
+      float c[4] = {};
+      if (!kScaled) {
         const int hh = lane >> 3, cc = lane & 7;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
                                                           (orow0 + hh) * kHeadDim + 16 * cc);
@@ -757,6 +844,13 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         const int sb = i & 1;
         float s8[2][8] = {};
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (i >> 1) & 1));
+        if (kScaled && j == 0) {  // (before the scores' buffer goes back: see kFtSigmaSlots)
+          const float4 v = reinterpret_cast<const float4*>(smem + kOffSigma)[seq % kFtSigmaSlots];
+          c[0] = v.x;
+          c[1] = v.y;
+          c[2] = v.z;
+          c[3] = v.w;
+        }
         if (ok) {
           tc::fence_after_sync();
           // per half: heads 0..3 from the high parts, then from the remainders
@@ -775,8 +869,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           for (int hf = 0; hf < 2; ++hf) {
             ks[hf] = sl[8 * hf];
             const float vs = sl[kFtTileBlocks + 8 * hf];
-            lv[hf] = log2f(vs);
-            inv_vs[hf] = 1.f / vs;
+            lv[hf] = log2_approx(vs);  // (to 2^-22; exact for powers of two)
+            inv_vs[hf] = rcp_approx(vs);
           }
         }
         const int tok0 = (x.b0 + j * kFtTileBlocks) * kBlockSize + t;  // token of half 0; half 1 is 128 further
@@ -912,69 +1006,80 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       }
       if (!ok_all) break;
 
-      // ---- unit epilogue: l over the 128 tokens, O / l from tensor memory ----
+      // ---- unit end: l over the 128 tokens, O / l from tensor memory ----
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int h = 0; h < 4; ++h) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-      float* xl = xbuf();
-      if (lane < 4) xl[w * 8 + lane] = ft_sel4(l, lane);
-      if (!all_healthy(xl)) {
-        ok_all = false;
-        break;
+      if constexpr (kFinish) {
+        const int slot = seq & 1;
+        if (ok && seq >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&bars->fin_empty[slot], ((seq >> 1) - 1) & 1));
+        if (ok) {
+          FtEnd* end = ends + slot;
+          if (lane < 4) {
+            end->l[w][lane] = ft_sel4(l, lane);
+            if (w == 0) end->m[lane] = ft_sel4(m, lane);
+          }
+          if (t == 0) end->unit = make_int4(static_cast<int>(orow0), x.split, x.whole ? 1 : 0, 1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->fin_full[slot]);
+        }
+      } else {
+        float* xl = xbuf();
+        if (lane < 4) xl[w * 8 + lane] = ft_sel4(l, lane);
+        if (!all_healthy(xl)) {
+          ok_all = false;
+          break;
+        }
+        float lsum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ww = 0; ww < 4; ++ww) {
+          const float4 v = *reinterpret_cast<const float4*>(xl + ww * 8);
+          lsum[0] += v.x;
+          lsum[1] += v.y;
+          lsum[2] += v.z;
+          lsum[3] += v.w;
+        }
+        results(t, seq, orow0, direct, x.split, m, lsum);
       }
+      ++seq;
+    }
+    if constexpr (kFinish) {  // no more units
+      const int slot = seq & 1;
+      if (ok && ok_all && seq >= 2)
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->fin_empty[slot], ((seq >> 1) - 1) & 1));
+      if (ok && ok_all) {
+        if (t == 0) ends[slot].unit = make_int4(0, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->fin_full[slot]);
+      }
+    }
+    if ((!ok || !ok_all) && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
+  } else {
+    // ------------------------------ results ------------------------------
+    for (int seq = 0; ok; ++seq) {
+      const int slot = seq & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->fin_full[slot], (seq >> 1) & 1));
+      if (!ok) break;
+      const FtEnd* end = ends + slot;
+      const int4 unit = end->unit;
+      const float4 m4 = *reinterpret_cast<const float4*>(end->m);
+      const float m[4] = {m4.x, m4.y, m4.z, m4.w};
       float lsum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ww = 0; ww < 4; ++ww) {
-        const float4 v = *reinterpret_cast<const float4*>(xl + ww * 8);
+        const float4 v = *reinterpret_cast<const float4*>(end->l[ww]);
         lsum[0] += v.x;
         lsum[1] += v.y;
         lsum[2] += v.z;
         lsum[3] += v.w;
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (seq >> 1) & 1));
-      if (ok) {
-        tc::fence_after_sync();
-        float o8[8];
-        tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o8);  // dim t: heads 0..3, high parts then remainders
-        tc::tmem_wait_ld();
-        tc::fence_before_sync();
-        mbar_arrive(&bars->o_empty[ub]);
-        float o[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) o[h] = (o8[h] + o8[4 + h]) * kFtPUnscale;
-        if constexpr (kCluster) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
-          if (t < kGroup) part_ml[t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
-        } else if (direct) {
-          uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
-            dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
-          }
-        } else if constexpr (kScaled) {  // un-normalised
-          const int64_t row = (2 * static_cast<int64_t>(blockIdx.x) + x.split) * kGroup;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) a.part_o[(row + h) * kHeadDim + t] = o[h];
-          if (t < kGroup) a.part_ml[row + t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
-        } else {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
-            a.part_o[((orow0 + h) * a.num_splits + x.split) * kHeadDim + t] = o[h] * inv;
-          }
-          if (t < kGroup) {
-            const float ls = ft_sel4(lsum, t);
-            a.part_lse[(orow0 + t) * a.num_splits + x.split] =
-                ls > 0.f ? (ft_sel4(m, t) + log2f(ls)) * kFtLn2 : -INFINITY;
-          }
-        }
-      }
-      ++seq;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->fin_empty[slot]);
+      if (unit.w == 0) break;
+      results(threadIdx.x & 127, seq, unit.x, unit.z != 0, unit.y, m, lsum);
     }
-    if ((!ok || !ok_all) && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
+    if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
   }
 
   tc::fence_before_sync();
@@ -1046,7 +1151,7 @@ int max_clusters_ft() {
     int c = 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1, kMaxClusterSplits);
-    cfg.blockDim = dim3(kFtThreads);
+    cfg.blockDim = dim3(ft_threads(FtMode::kScaledCluster));
     cfg.dynamicSmemBytes = kSmemFt;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1076,7 +1181,7 @@ cudaError_t launch_ft(const DecodeArgs& a, int32_t grid, cudaStream_t stream) {
   const cudaError_t e = allow_smem_ft<kMode>();
   if (e != cudaSuccess) return e;
   constexpr unsigned kSplits = kMode == FtMode::kScaledCluster ? kMaxClusterSplits : 1;
-  return launch_pdl(paged_decode_fp8_tc_kernel<kMode>, dim3(static_cast<unsigned>(grid), kSplits), dim3(kFtThreads),
+  return launch_pdl(paged_decode_fp8_tc_kernel<kMode>, dim3(static_cast<unsigned>(grid), kSplits), dim3(ft_threads(kMode)),
                     kSmemFt, stream, kSplits, kmap, vmap, a);
 }
 

@@ -28,61 +28,69 @@ struct Share {
 template <typename TilesOf>
 __device__ __forceinline__ Share find_share(int rows, int num_kv_heads, int job_cost, int min_share, int lane,
                                             TilesOf tiles_of) {
-  constexpr int kFlight = 4;  // reads in flight: their latency is what this costs
+  constexpr int kFlight = 4;  // rows of a lane, neighbours: their reads are in flight together
   auto cost = [&](int tiles) -> int { return tiles > 0 ? tiles + job_cost : 0; };
-  auto read = [&](int r0, int* x) {
+  auto read = [&](int r0, int (&x)[kFlight]) -> int {
+    int sum = 0;
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      const int r = r0 + 32 * k + lane;
+      const int r = r0 + kFlight * lane + k;
       x[k] = r < rows ? tiles_of(r) : 0;
     }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) sum += cost(x[k]);
+    return sum;
   };
-  int first[kFlight], total = 0;
-  read(0, first);
-#pragma unroll
-  for (int k = 0; k < kFlight; ++k) total += cost(first[k]);
+  // (Loops stay rolled: a warp runs this once, from a cold instruction cache.)
+  int x[kFlight];
+  int sum = read(0, x);  // costs of the lane's rows, once for each KV head
+  int all = sum;
+#pragma unroll 1
   for (int r0 = 32 * kFlight; r0 < rows; r0 += 32 * kFlight) {
-    int x[kFlight];
-    read(r0, x);
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) total += cost(x[k]);
+    int y[kFlight];
+    all += read(r0, y);
   }
-  total = __reduce_add_sync(0xffffffffu, total) * num_kv_heads;
-  const int grid = gridDim.x;
+  const uint32_t total = __reduce_add_sync(0xffffffffu, all) * num_kv_heads;
+  const uint32_t grid = gridDim.x;
   Share s{};
-  s.per = max((total + grid - 1) / grid, min_share);
+  s.per = max(static_cast<int>((total + grid - 1) / grid), min_share);
   const int t0 = s.per * static_cast<int>(blockIdx.x);
-  s.left = min(s.per, total - t0);
+  s.left = min(s.per, static_cast<int>(total) - t0);
   if (s.left <= 0) return s;
   int before = 0;
+#pragma unroll 1
   for (int r0 = 0;; r0 += 32 * kFlight) {
-    int x[kFlight];
-    if (r0 == 0) {
+    if (r0 > 0) sum = read(r0, x);
+    const int mine = sum * num_kv_heads;
+    int upto = mine;
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k) x[k] = first[k];
-    } else {
-      read(r0, x);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
     }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
+    if (past == 0) {
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      continue;
+    }
+    const int at = __ffs(past) - 1;
+    int start = before + __shfl_sync(0xffffffffu, upto - mine, at);
+    bool found = false;
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      int upto = cost(x[k]) * num_kv_heads;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += y;
+      const int tiles = __shfl_sync(0xffffffffu, x[k], at);
+      const int c = cost(tiles) * num_kv_heads;
+      if (!found && t0 < start + c) {
+        found = true;
+        s.tiles = tiles;
+        s.row = r0 + kFlight * at + k;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > t0);
-      if (past != 0) {
-        const int at = __ffs(past) - 1;
-        s.tiles = __shfl_sync(0xffffffffu, x[k], at);
-        const int start = before + __shfl_sync(0xffffffffu, upto, at) - cost(s.tiles) * num_kv_heads;
-        s.row = r0 + 32 * k + at;
-        s.kvh = (t0 - start) / cost(s.tiles);
-        s.into = (t0 - start) - s.kvh * cost(s.tiles);
-        return s;
-      }
-      before += __shfl_sync(0xffffffffu, upto, 31);
+      if (!found) start += c;
     }
+    const uint32_t c = cost(s.tiles);
+    s.kvh = static_cast<uint32_t>(t0 - start) / c;
+    s.into = (t0 - start) - s.kvh * static_cast<int>(c);
+    return s;
   }
 }
 
