@@ -143,7 +143,7 @@ static_assert(sizeof(FtBars) <= 512, "barrier area");
 
 // kScaled: in tiles, what a (request, KV head) costs besides its tiles, and the
 // least worth a CTA.
-constexpr int kFtJobCost = 2;
+constexpr int kFtJobCost = 1;
 constexpr int kFtMinShare = 3;
 
 struct FtUnit {
