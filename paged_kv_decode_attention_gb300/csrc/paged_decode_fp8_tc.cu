@@ -73,8 +73,10 @@ enum class FtMode {
   kScaledCluster  // the same, a thread-block cluster to a (request, KV head)
 };
 __host__ __device__ constexpr bool ft_scaled(FtMode m) { return m == FtMode::kScaled || m == FtMode::kScaledCluster; }
-// (kScaled: four warps more, for the results)
-__host__ __device__ constexpr int ft_threads(FtMode m) { return m == FtMode::kScaled ? 384 : 256; }
+// Groups of four softmax warps, which take the tiles in turn.
+__host__ __device__ constexpr int ft_groups(FtMode m) { return ft_scaled(m) ? 2 : 1; }
+// (scaled: four warps more, for the results)
+__host__ __device__ constexpr int ft_threads(FtMode m) { return 128 + ft_groups(m) * 128 + (ft_scaled(m) ? 128 : 0); }
 constexpr int kFtTileBlocks = 16;                          // blocks per tile
 constexpr int kFtTileTokens = kFtTileBlocks * kBlockSize;  // 256 tokens: two 128-token halves
 constexpr int kFtBoxBytes = kBlockSize * kHeadDim;         // one block's 16 x 128 bytes: 2 KiB
@@ -86,8 +88,8 @@ constexpr int kOffK = 0;
 constexpr int kOffV = kOffK + kFtStages * kFtStageBytes;
 constexpr int kOffQp = kOffV + kFtStages * kFtStageBytes;  // 2 buffers (unit parity)
 constexpr int kOffPt = kOffQp + 2 * kFtOpBytes;            // 2 buffers (tile parity) of 2 halves
-constexpr int kOffX = kOffPt + 4 * kFtOpBytes;             // float [2][4 warps][8]: exchanges
-constexpr int kOffKn = kOffX + 2 * 4 * 8 * 4;              // fused append: 2 new K rows (unit parity), E4M3
+constexpr int kOffX = kOffPt + 4 * kFtOpBytes;             // float [2 groups][2][4 warps][8]: exchanges
+constexpr int kOffKn = kOffX + 2 * 2 * 4 * 8 * 4;              // fused append: 2 new K rows (unit parity), E4M3
 constexpr int kOffKnAt = kOffKn + 2 * kHeadDim;            // int [2]: where each row goes (tile << 8 | row), or -1
 constexpr int kFtScaleSlots = 8;                           // block scales: tiles held
 constexpr int kOffScale = kOffKnAt + 16;                   // float [8 tiles][K, V][16 blocks]
@@ -95,7 +97,7 @@ constexpr int kOffPart = kOffScale + kFtScaleSlots * 2 * kFtTileBlocks * 4;  // 
 constexpr int kFtSigmaSlots = 4;                           // a slot is written again once S of the unit 2 on is done
 constexpr int kOffSigma = kOffPart + 32;                   // kScaled: float [4 units][4 heads], scale / sigma
 constexpr int kOffEnds = kOffSigma + kFtSigmaSlots * kGroup * 4;  // FtEnd [2], by unit parity
-constexpr int kOffWalk = kOffEnds + 2 * 96;                // kScaled: FtWalk, where the CTA's walk starts
+constexpr int kOffWalk = kOffEnds + 2 * 176;               // kScaled: FtWalk, where the CTA's walk starts
 constexpr int kOffBar = kOffWalk + 32;
 constexpr int kSmemFt = kOffBar + 512;
 constexpr uint32_t kColS = 0;    // S^T buffers at columns 0 and 32 (16 columns per half)
@@ -116,11 +118,11 @@ static_assert(kFtLazyMax + 6.f <= 8.f, "scaled weights must stay inside E4M3's r
 
 // What the softmax leaves of a unit for the warps that finish it.
 struct alignas(16) FtEnd {
-  float l[4][4];  // a warp's sums, by head
-  float m[4];
-  int4 unit;      // output row, place of a partial, whole or not; w = 0: no more units
+  float l[2][4][4];  // a group's warps' sums, by head
+  float m[2][4];     // a group's maxima
+  int4 unit;         // output row, place of a partial, whole or not; w = 0: no more units
 };
-static_assert(sizeof(FtEnd) == 96, "size");
+static_assert(sizeof(FtEnd) == 176, "size");
 
 struct FtBars {
   uint64_t k_full[kFtStages];
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
   constexpr bool kFused = kMode == FtMode::kFused;
   constexpr bool kScaled = ft_scaled(kMode);
   constexpr bool kCluster = kMode == FtMode::kScaledCluster;
-  constexpr bool kFinish = kMode == FtMode::kScaled;  // units are finished by warps of their own
+  constexpr int kGroups = ft_groups(kMode);
   constexpr FtMode kWalk = kScaled ? kMode : FtMode::kPlain;  // of the warps that need not know the new tokens
   extern __shared__ __align__(1024) uint8_t smem[];
   FtBars* bars = reinterpret_cast<FtBars*>(smem + kOffBar);
@@ -467,8 +469,8 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_empty[b], 128);
     }
-    for (int s = 0; kFinish && s < 2; ++s) {
-      mbar_init(&bars->fin_full[s], 4);
+    for (int s = 0; kScaled && s < 2; ++s) {
+      mbar_init(&bars->fin_full[s], 8);
       mbar_init(&bars->fin_empty[s], 4);
     }
     for (int s = 0; kScaled && s < kFtScaleSlots; ++s) mbar_init(&bars->scale_full[s], 32);
@@ -518,21 +520,33 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
   bool ok = true;
 
   // A unit's result (the nth in turn), by the 128 threads of four warps: dim t of
-  // the 4 heads.
-  auto results = [&](int t, int nth, int64_t orow0, bool direct, int split, const float (&m)[4], const float (&lsum)[4]) {
+  // the 4 heads.  f: the factor of a group's part (0: it saw nothing).
+  auto results = [&](int t, int nth, int64_t orow0, bool direct, int split, const float (&m)[4], const float (&lsum)[4],
+                     const float (&f)[kGroups][4]) {
     const int ub = nth & 1;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (nth >> 1) & 1));
     if (ok) {
       tc::fence_after_sync();
-      float o8[8];
-      tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o8);  // dim t: heads 0..3, high parts then remainders
+      float o8[kGroups][8];  // dim t: heads 0..3, high parts then remainders
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+        tc::tmem_ld8(tmem + lane_off + kColO + (kGroups == 2 ? 32 * ub + 16 * g : 16 * ub), o8[g]);
       tc::tmem_wait_ld();
       tc::fence_before_sync();
       mbar_arrive(&bars->o_empty[ub]);
       float o[4];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) o[h] = (o8[h] + o8[4 + h]) * kFtPUnscale;
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (kGroups == 1) {
+          o[h] = (o8[0][h] + o8[0][4 + h]) * kFtPUnscale;
+        } else {
+          o[h] = 0.f;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+            if (f[g][h] != 0.f) o[h] = fmaf((o8[g][h] + o8[g][4 + h]) * kFtPUnscale, f[g][h], o[h]);
+        }
+      }
       if constexpr (kCluster) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
@@ -541,7 +555,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
         uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
+          const float inv = (kScaled ? lsum[h] != 0.f : lsum[h] > 0.f) ? 1.f / lsum[h] : 0.f;  // (kScaled: NaN stays)
           dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
         }
       } else if constexpr (kScaled) {  // un-normalised
@@ -659,9 +673,10 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
             // P^T's tokens 128-255 are its second 16-row operand
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 32 tokens per step
-              tc::mma_f8(tmem + kColO + 16 * ub, tc::smem_desc(vst + 4096 * kk, kFtHalfBytes, 1024),
+              tc::mma_f8(tmem + kColO + (kGroups == 2 ? 32 * ub + 16 * pb : 16 * ub),
+                         tc::smem_desc(vst + 4096 * kk, kFtHalfBytes, 1024),
                          tc::smem_desc(pt + (kk >> 2) * kFtOpBytes + 32 * (kk & 3), 16, 1024), kIdO,
-                         (cp.j > 0 || kk > 0) ? 1u : 0u);
+                         (cp.j >= kGroups || kk > 0) ? 1u : 0u);
             tc::commit(&bars->v_empty[st]);
             tc::commit(&bars->p_empty[pb]);
             if (cp.j == cp.n - 1) tc::commit(&bars->o_full[ub]);
@@ -765,19 +780,20 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
       ++seq;
     }
     if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
-  } else if (!kFinish || warp < 8) {
+  } else if (!kScaled || warp < 4 + 4 * kGroups) {
     // ------------------------------ softmax ------------------------------
     const int w = warp & 3;           // TMEM sub-partition
-    const int t = threadIdx.x - 128;  // tokens t and 128 + t of the tile (TMEM lane t); at a unit's end, the output dim
+    const int g = kGroups == 2 ? (warp >> 2) - 1 : 0;  // group
+    const int t = threadIdx.x & 127;  // tokens t and 128 + t of the tile (TMEM lane t); at a unit's end, the output dim
     const uint32_t lane_off = static_cast<uint32_t>(w * 32) << 16;
-    float* xch = reinterpret_cast<float*>(smem + kOffX);  // [2][4][8]
+    float* xch = reinterpret_cast<float*>(smem + kOffX) + 64 * g;  // [2][4][8]
     if constexpr (kCluster) {
-      if (t == 0 && blockIdx.y == 0 && a.context_lens[blockIdx.x / a.num_kv_heads] > a.max_blocks * kBlockSize)
+      if (threadIdx.x == 128 && blockIdx.y == 0 &&
+          a.context_lens[blockIdx.x / a.num_kv_heads] > a.max_blocks * kBlockSize)
         report(a.err, PKV_DEVERR_CONTEXT);
-      if (t < kGroup) part_ml[t] = make_float2(-INFINITY, 0.f);  // until there is a result
     } else if constexpr (kScaled) {
       // requests without a token belong to no share: zeros
-      for (int r = blockIdx.x; r < a.num_seqs; r += gridDim.x) {
+      for (int r = blockIdx.x; g == 0 && r < a.num_seqs; r += gridDim.x) {
         if (t == 0 && a.context_lens[r] > a.max_blocks * kBlockSize) report(a.err, PKV_DEVERR_CONTEXT);
         if (ft_tiles(a, r) > 0) continue;
         uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<int64_t>(r) * hq * kHeadDim);
@@ -793,7 +809,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     auto xbuf = [&]() -> float* { return xch + (nx & 1) * 32; };
     auto all_healthy = [&](float* buf) -> bool {
       if (lane == 4) buf[w * 8 + 4] = ok ? 1.f : 0.f;
-      named_barrier_sync(kFtNamedBar, 128);
+      named_barrier_sync(kFtNamedBar + g, 128);
       ++nx;
       bool all = true;
 #pragma unroll
@@ -821,6 +837,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
         continue;
       }
       const int ub = seq & 1;
+      const uint32_t ocol = kColO + (kGroups == 2 ? 32 * ub + 16 * g : 16 * ub);
       // the query operand's scale of each head, taken from the query exactly
       // as the query-operand warp takes it: scores / sigma_h in base 2
       // (kScaled: read from where that warp leaves it, with the first scores)
@@ -860,11 +877,14 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
         m[h] = -INFINITY;
         l[h] = 0.f;
       }
-      for (int j = 0; j < x.n_tiles; ++j, ++i) {
+      const int first = kGroups == 2 ? (g ^ i) & 1 : 0;  // tile of this group
+      const int i_end = i + x.n_tiles;
+      i += first;
+      for (int j = first; j < x.n_tiles; j += kGroups, i += kGroups) {
         const int sb = i & 1;
         float s8[2][8] = {};
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (i >> 1) & 1));
-        if (kScaled && j == 0) {  // (before the scores' buffer goes back: see kFtSigmaSlots)
+        if (kScaled && j < kGroups) {  // (before the scores' buffer goes back: see kFtSigmaSlots)
           const float4 v = reinterpret_cast<const float4*>(smem + kOffSigma)[seq % kFtSigmaSlots];
           c[0] = v.x;
           c[1] = v.y;
@@ -938,18 +958,19 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
           grow_any = grow_any || grow;
         }
         if (grow_any) {  // uniform
-          if (j > 0) {
+          if (j >= kGroups) {
             // O holds weights taken against the old maxima: rescale this warp's 32 dims
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
+            const int prev = i - kGroups;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[prev & 1], (prev >> 1) & 1));
             if (ok) {
               tc::fence_after_sync();
               float o[8];  // columns h (high parts) and 4 + h (remainders) of head h
-              tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o);
+              tc::tmem_ld8(tmem + lane_off + ocol, o);
               tc::tmem_wait_ld();
               uint32_t ob[8];
 #pragma unroll
               for (int h = 0; h < 8; ++h) ob[h] = __float_as_uint(o[h] * alpha[h & 3]);
-              tc::tmem_st8(tmem + lane_off + kColO + 16 * ub, ob);
+              tc::tmem_st8(tmem + lane_off + ocol, ob);
               tc::tmem_wait_st();
               tc::fence_before_sync();
             }
@@ -1025,22 +1046,23 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
         }
       }
       if (!ok_all) break;
+      i = i_end;
 
       // ---- unit end: l over the 128 tokens, O / l from tensor memory ----
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int h = 0; h < 4; ++h) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-      if constexpr (kFinish) {
+      if constexpr (kScaled) {
         const int slot = seq & 1;
         if (ok && seq >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&bars->fin_empty[slot], ((seq >> 1) - 1) & 1));
         if (ok) {
           FtEnd* end = ends + slot;
           if (lane < 4) {
-            end->l[w][lane] = ft_sel4(l, lane);
-            if (w == 0) end->m[lane] = ft_sel4(m, lane);
+            end->l[g][w][lane] = ft_sel4(l, lane);
+            if (w == 0) end->m[g][lane] = ft_sel4(m, lane);
           }
-          if (t == 0) end->unit = make_int4(static_cast<int>(orow0), x.split, x.whole ? 1 : 0, 1);
+          if (g == 0 && t == 0) end->unit = make_int4(static_cast<int>(orow0), x.split, x.whole ? 1 : 0, 1);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->fin_full[slot]);
         }
@@ -1060,16 +1082,16 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
           lsum[2] += v.z;
           lsum[3] += v.w;
         }
-        results(t, seq, orow0, direct, x.split, m, lsum);
+        results(t, seq, orow0, direct, x.split, m, lsum, {});
       }
       ++seq;
     }
-    if constexpr (kFinish) {  // no more units
+    if constexpr (kScaled) {  // no more units
       const int slot = seq & 1;
       if (ok && ok_all && seq >= 2)
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->fin_empty[slot], ((seq >> 1) - 1) & 1));
       if (ok && ok_all) {
-        if (t == 0) ends[slot].unit = make_int4(0, 0, 0, 0);
+        if (g == 0 && t == 0) ends[slot].unit = make_int4(0, 0, 0, 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->fin_full[slot]);
       }
@@ -1077,27 +1099,46 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     if ((!ok || !ok_all) && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
   } else {
     // ------------------------------ results ------------------------------
+    if (kCluster && threadIdx.x % 128 < kGroup) part_ml[threadIdx.x % 128] = make_float2(-INFINITY, 0.f);  // nothing yet
     for (int seq = 0; ok; ++seq) {
       const int slot = seq & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->fin_full[slot], (seq >> 1) & 1));
       if (!ok) break;
       const FtEnd* end = ends + slot;
       const int4 unit = end->unit;
-      const float4 m4 = *reinterpret_cast<const float4*>(end->m);
-      const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-      float lsum[4] = {0.f, 0.f, 0.f, 0.f};
+      // the groups' maxima and sums
+      float ms[2][4], ls[2][4] = {};
 #pragma unroll
-      for (int ww = 0; ww < 4; ++ww) {
-        const float4 v = *reinterpret_cast<const float4*>(end->l[ww]);
-        lsum[0] += v.x;
-        lsum[1] += v.y;
-        lsum[2] += v.z;
-        lsum[3] += v.w;
+      for (int g = 0; g < 2; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(end->m[g]);
+        ms[g][0] = v.x;
+        ms[g][1] = v.y;
+        ms[g][2] = v.z;
+        ms[g][3] = v.w;
+#pragma unroll
+        for (int ww = 0; ww < 4; ++ww) {
+          const float4 s4 = *reinterpret_cast<const float4*>(end->l[g][ww]);
+          ls[g][0] += s4.x;
+          ls[g][1] += s4.y;
+          ls[g][2] += s4.z;
+          ls[g][3] += s4.w;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->fin_empty[slot]);
       if (unit.w == 0) break;
-      results(threadIdx.x & 127, seq, unit.x, unit.z != 0, unit.y, m, lsum);
+      float m[4], lsum[4], f[2][4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        m[h] = fmaxf(ms[0][h], ms[1][h]);
+        lsum[h] = 0.f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          f[g][h] = ls[g][h] == 0.f ? 0.f : exp2_approx(ms[g][h] - m[h]);
+          lsum[h] = fmaf(ls[g][h], f[g][h], lsum[h]);
+        }
+      }
+      if constexpr (kScaled) results(threadIdx.x & 127, seq, unit.x, unit.z != 0, unit.y, m, lsum, f);
     }
     if (!ok && lane == 0) report(a.err, PKV_DEVERR_TIMEOUT);
   }
