@@ -333,7 +333,11 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
       const int st = i % kFtStages;
       if (i >= kFtStages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((i / kFtStages) - 1) & 1));
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], kFtStageBytes);
+      // (K of the scaled caches: blocks behind the unit's are left out, their
+      // scores are masked)
+      const int boxes = ft_scaled(kMode) && scales != nullptr ? min(kFtTileBlocks, x.b1 - x.b0 - j * kFtTileBlocks)
+                                                              : kFtTileBlocks;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * kFtBoxBytes);
       __syncwarp();
       if (ft_scaled(kMode) && scales != nullptr) {
         float* slot_of = scales + (i % kFtScaleSlots) * 2 * kFtTileBlocks + lane;
@@ -344,7 +348,7 @@ __device__ __forceinline__ bool ft_produce(const DecodeArgs& a, const CUtensorMa
         }
         cp_async_arrive(&scale_full[i % kFtScaleSlots]);
       }
-      if (lane < kFtTileBlocks) {
+      if (lane < boxes) {
         int y = oob_row;
         if (x.b0 + j * kFtTileBlocks + lane < x.b1) {
           int b = blk;
