@@ -16,7 +16,9 @@
 // 16 lanes a token of 16 bytes, up to 16 loads in flight, the largest magnitude
 // by one reduction over BF16 bits (their order is that of integers).  Bound by
 // HBM for prompts and by a chain of four dependent reads (request, context,
-// block, its scale) for single tokens.
+// block, its scale) for single tokens.  Measured, 8 KV heads: 4 prompts of 8100
+// to 8192 tokens 37 us (5.4 TB/s), 24 chunks of 5 to 700 7 us, one token each of
+// 37 requests 2.8 us from a graph.  (Prompts with 2, 4 or 8 warps a CTA: no faster.)
 #include "pkv_common.cuh"
 #include "pkv_kernels.h"
 

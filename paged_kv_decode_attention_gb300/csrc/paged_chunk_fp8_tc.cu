@@ -40,9 +40,17 @@
 // Scores (64 columns), two buffers of weights (32 each) and O fill a row tile's
 // 256 columns of tensor memory.  The next scores are issued as soon as the
 // softmax holds the present ones in registers, ahead of the product that waits
-// for their weights: neither side waits for the other's latency.  (Tiles of 128
-// keys with scores and weights in one buffer, one chain: 1.09 ms for 4 x 2000
-// queries behind 4000 to 8000 tokens, 57 us for 37 x 7 behind 2,170.)
+// for their weights: neither side waits for the other's latency.
+//
+// Measured, 32 query and 8 KV heads: 4 x 2000 queries behind 4000 to 8000
+// tokens 0.78 ms, 1.3 PFLOP/s (tiles of 128 keys with scores and weights in one
+// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 39 us, 4.4 TB/s (57).  A
+// tile of the latter takes 720 cycles, as long as its transfer; the rest is the
+// start, 6000 cycles to the first scores, the ends of jobs, 3,500 each, and the
+// joining kernel.  37 requests behind 2100 tokens, by the rows' layout: 8 queries
+// 35.5 us with M = 64, 41 with 64 rows of M = 128, 51 with 128; 16
+// queries 46 with 64 rows, 56 with 128, 60 as kWide; 32 queries 62 with 128, 70
+// as kWide.
 //
 // Work is cut by tiles, not by requests (pkv_shares.cuh); a cut job leaves
 // un-normalised FP32 partials.
@@ -1203,7 +1211,7 @@ cudaError_t launch_cf(const ScaledArgs& a, int32_t grid, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCfThreads), CfShape<kWide>::kSmem, stream,
                  1, kmap, vmap, a);
-  if (e != cudaSuccess || grid == 1) return e;
+  if (e != cudaSuccess || grid == 1 || a.max_blocks <= kCfTileBlocks) return e;  // (a job of one tile is not cut)
   return launch_scaled_join(a, grid, kWide ? 2 * kCfPos : kCfPos, kCfJobCost, stream);
 }
 

@@ -50,6 +50,18 @@
 //                a normalised split partial and its log-sum-exp).  Each tile
 //                and unit end passes one barrier of the 4 warps where each
 //                posts its health, so all four leave together if one gives up.
+//
+// The cache with block scales (FtMode::kScaled, kScaledCluster) runs on the same
+// tiles and products, with 16 warps: two groups of softmax warps take the tiles
+// in turn, each with a maximum, a sum and an accumulator of its own, and warps
+// 12-15 join the groups, divide and store while the softmax is at the next unit
+// (with one group that stores for itself a unit of one tile took 5000 cycles of
+// the softmax, 2,800 of them behind its tile).  What bounds it is HBM: 128
+// requests of 8192 to 8447 tokens, 8 KV heads, take 320 us, as long as a copy of
+// as many bytes; 64 of 16 to 16000 64 us (56), the rest being the start, 5 us to
+// the first scores, the ends of rows and the joining.  One request of 8300
+// tokens takes 11 us, all latency: bounds, table, tiles, four or five tiles of
+// softmax, the join.
 // Every wait is bounded and reports PKV_DEVERR_TIMEOUT instead of hanging.
 #include <algorithm>
 #include <climits>
@@ -193,7 +205,7 @@ __device__ __forceinline__ FtUnit ft_unit(const DecodeArgs& a, int u) {
 // kScaled: work is cut by tiles, not by requests (pkv_shares.cuh); a cut row
 // leaves un-normalised partials for the chunks' joining kernel.  (64 requests of 16
 // to 16000 tokens: in equal splits of the longest context 184 us; a row counted
-// with 1, 2, 3 or 4 tiles more: 76, 74, 77, 82.)
+// with 1, 2 or 3 tiles more: 64.1, 65.8, 72.5.)
 __device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
   const int ctx = min(max(a.context_lens[r], 0), a.max_blocks * kBlockSize);
   return (ctx + kFtTileTokens - 1) / kFtTileTokens;
@@ -201,8 +213,9 @@ __device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
 
 // kScaledCluster: where there are so few rows that kMaxClusterSplits CTAs for
 // each are resident at once, they take equal parts of it and join them through
-// distributed shared memory: one launch.  (One request of 8,300 tokens, 8 KV
-// heads: 14.4 us with shares and their joining.)
+// distributed shared memory: one launch.  (8 KV heads, one request: 8300 tokens
+// 10.7 us against 12.1 with shares and their joining, 1000 tokens 6.2 against
+// 10.1.)
 //
 // The units that a CTA works on, in order.  Every warp walks them for itself.
 struct alignas(16) FtWalk {
@@ -1293,7 +1306,8 @@ cudaError_t launch_paged_decode_fp8_scaled(const ScaledArgs& a, int32_t grid, cu
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   if (rows <= max_clusters_ft()) return launch_ft<FtMode::kScaledCluster>(d, static_cast<int32_t>(rows), stream);
   const cudaError_t e = launch_ft<FtMode::kScaled>(d, grid, stream);
-  return e != cudaSuccess || grid == 1 ? e : launch_scaled_join(a, grid, 1, kFtJobCost, stream);
+  if (e != cudaSuccess || grid == 1 || a.max_blocks <= kFtTileBlocks) return e;  // (a row of one tile is not cut)
+  return launch_scaled_join(a, grid, 1, kFtJobCost, stream);
 }
 
 }  // namespace pkv
