@@ -44,7 +44,7 @@
 //
 // Measured, 32 query and 8 KV heads: 4 x 2000 queries behind 4000 to 8000
 // tokens 0.78 ms, 1.3 PFLOP/s (tiles of 128 keys with scores and weights in one
-// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 39 us, 4.4 TB/s (57).  A
+// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 38 us, 4.5 TB/s (57).  A
 // tile of the latter takes 720 cycles, as long as its transfer; the rest is the
 // start, 6000 cycles to the first scores, the ends of jobs, 3,500 each, and the
 // joining kernel.  37 requests behind 2100 tokens, by the rows' layout: 8 queries
@@ -1145,43 +1145,64 @@ __global__ void __launch_bounds__(256) scaled_join_kernel(const ScaledArgs a, in
     auto at = [&](int k) -> int64_t {
       return static_cast<int64_t>(2 * (i - 1 + k) + (k == first ? 1 : 0)) * a.rows_slot + row;
     };
-    // 32 pieces at a time: lane k holds the k-th one's maximum and sum, and
-    // what is summed so far is taken against the maximum so far
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kFlight = 8;  // partials in flight
-    for (int k0 = first; k0 < pieces; k0 += 32) {
-      const int n = min(32, pieces - k0);
-      float4 x[kFlight];
-      auto fetch = [&](int b) {
+    if (pieces - first == 2) {  // the usual cut
+      float2 ml[2];
+      float4 x[2];
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k)
-          if (b + k < n) x[k] = *reinterpret_cast<const float4*>(a.part_o + at(k0 + b + k) * kHeadDim + 4 * lane);
-      };
-      fetch(0);
-      const float2 ml = lane < n ? a.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.f);
-      float top = ml.x;
+      for (int k = 0; k < 2; ++k) {
+        ml[k] = a.part_ml[at(first + k)];
+        x[k] = *reinterpret_cast<const float4*>(a.part_o + at(first + k) * kHeadDim + 4 * lane);
+      }
+      m = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const float m_new = fmaxf(m, top);
-      const float old = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
-      const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m_new);  // (0: it saw nothing, its O holds anything)
-      float sum = ml.y * f;
+      for (int k = 0; k < 2; ++k) {
+        if (ml[k].y == 0.f) continue;  // it saw nothing, its O holds anything
+        const float f = exp2_approx(ml[k].x - m);
+        l = fmaf(ml[k].y, f, l);
+        o.x = fmaf(x[k].x, f, o.x);
+        o.y = fmaf(x[k].y, f, o.y);
+        o.z = fmaf(x[k].z, f, o.z);
+        o.w = fmaf(x[k].w, f, o.w);
+      }
+    } else {
+      // 32 pieces at a time: lane k holds the k-th one's maximum and sum, and
+      // what is summed so far is taken against the maximum so far
+      constexpr int kFlight = 8;  // partials in flight
+      for (int k0 = first; k0 < pieces; k0 += 32) {
+        const int n = min(32, pieces - k0);
+        float4 x[kFlight];
+        auto fetch = [&](int b) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      l = l * old + sum;
-      o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
-      m = m_new;
-      for (int b = 0; b < n; b += kFlight) {
-        if (b > 0) fetch(b);
+          for (int k = 0; k < kFlight; ++k)
+            if (b + k < n) x[k] = *reinterpret_cast<const float4*>(a.part_o + at(k0 + b + k) * kHeadDim + 4 * lane);
+        };
+        fetch(0);
+        const float2 ml = lane < n ? a.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-          const float g = __shfl_sync(0xffffffffu, f, (b + k) & 31);
-          if (b + k >= n || g == 0.f) continue;
-          o.x = fmaf(x[k].x, g, o.x);
-          o.y = fmaf(x[k].y, g, o.y);
-          o.z = fmaf(x[k].z, g, o.z);
-          o.w = fmaf(x[k].w, g, o.w);
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float m_new = fmaxf(m, top);
+        const float old = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
+        const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m_new);  // (0: it saw nothing, its O holds anything)
+        float sum = ml.y * f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l = l * old + sum;
+        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+        m = m_new;
+        for (int b = 0; b < n; b += kFlight) {
+          if (b > 0) fetch(b);
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k) {
+            const float g = __shfl_sync(0xffffffffu, f, (b + k) & 31);
+            if (b + k >= n || g == 0.f) continue;
+            o.x = fmaf(x[k].x, g, o.x);
+            o.y = fmaf(x[k].y, g, o.y);
+            o.z = fmaf(x[k].z, g, o.z);
+            o.w = fmaf(x[k].w, g, o.w);
+          }
         }
       }
     }
