@@ -397,6 +397,23 @@ def test_queries_and_scales_whose_product_vanishes(q_len):
     check(run_attention(*case, ctx), reference(*case, ctx), ctx)
 
 
+@pytest.mark.parametrize("count", [3, 40])
+@pytest.mark.parametrize("q_len", [1, 2, 12, 24, 50])
+def test_a_broken_request_breaks_no_other(q_len, count):
+    """NaN codes in one request's context: its rows are NaN, the others' are what they were, bit for bit."""
+    ctx = ([300, 70, 500] * count)[:count]
+    q, kc, vc, ks, vs, t = attention_case(ctx, q_len, 2)
+    want = run_attention(q, kc, vc, ks, vs, t, ctx)
+    for broken in (kc, vc):
+        kept = broken.clone()
+        broken[t[1][0], :, 3] = 0x7F
+        out = run_attention(q, kc, vc, ks, vs, t, ctx)
+        broken.copy_(kept)
+        assert bool(out[1].isnan().all())
+        rest = [r for r in range(count) if r != 1]
+        assert torch.equal(out[rest], want[rest])
+
+
 @pytest.mark.parametrize("q_len", [1, 5, 70])
 def test_bad_tables_and_contexts_are_reported(q_len):
     pkv = _pkv()
