@@ -536,62 +536,43 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
   const uint32_t sbase = smem_addr(smem);
   bool ok = true;
 
-  // A unit's result (the nth in turn), by the 128 threads of four warps: dim t of
-  // the 4 heads.  f: the factor of a group's part (0: it saw nothing).
-  auto results = [&](int t, int nth, int64_t orow0, bool direct, int split, const float (&m)[4], const float (&lsum)[4],
-                     const float (&f)[kGroups][4]) {
+  // kScaled: a unit's result (the nth in turn), by the 128 threads of four warps:
+  // dim t of the 4 heads.  f: the factor of a group's part (0: it saw nothing).
+  auto results = [&](int t, int nth, int64_t orow0, bool whole, int split, const float (&m)[4], const float (&lsum)[4],
+                     const float (&f)[2][4]) {
     const int ub = nth & 1;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (nth >> 1) & 1));
-    if (ok) {
-      tc::fence_after_sync();
-      float o8[kGroups][8];  // dim t: heads 0..3, high parts then remainders
+    if (!ok) return;
+    tc::fence_after_sync();
+    float o8[2][8];  // dim t: heads 0..3, high parts then remainders
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-        tc::tmem_ld8(tmem + lane_off + kColO + (kGroups == 2 ? 32 * ub + 16 * g : 16 * ub), o8[g]);
-      tc::tmem_wait_ld();
-      tc::fence_before_sync();
-      mbar_arrive(&bars->o_empty[ub]);
-      float o[4];
+    for (int g = 0; g < 2; ++g) tc::tmem_ld8(tmem + lane_off + kColO + 32 * ub + 16 * g, o8[g]);
+    tc::tmem_wait_ld();
+    tc::fence_before_sync();
+    mbar_arrive(&bars->o_empty[ub]);
+    float o[4] = {};
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (f[g][h] != 0.f) o[h] = fmaf((o8[g][h] + o8[g][4 + h]) * kFtPUnscale, f[g][h], o[h]);
+    if constexpr (kCluster) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
+      if (t < kGroup) part_ml[t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
+    } else if (whole) {
+      uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        if constexpr (kGroups == 1) {
-          o[h] = (o8[0][h] + o8[0][4 + h]) * kFtPUnscale;
-        } else {
-          o[h] = 0.f;
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-            if (f[g][h] != 0.f) o[h] = fmaf((o8[g][h] + o8[g][4 + h]) * kFtPUnscale, f[g][h], o[h]);
-        }
+        const float inv = lsum[h] != 0.f ? 1.f / lsum[h] : 0.f;  // (a NaN sum stays one)
+        dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
       }
-      if constexpr (kCluster) {
+    } else {  // un-normalised
+      const int64_t row = (2 * static_cast<int64_t>(blockIdx.x) + split) * kGroup;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
-        if (t < kGroup) part_ml[t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
-      } else if (direct) {
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const float inv = (kScaled ? lsum[h] != 0.f : lsum[h] > 0.f) ? 1.f / lsum[h] : 0.f;  // (kScaled: NaN stays)
-          dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
-        }
-      } else if constexpr (kScaled) {  // un-normalised
-        const int64_t row = (2 * static_cast<int64_t>(blockIdx.x) + split) * kGroup;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) a.part_o[(row + h) * kHeadDim + t] = o[h];
-        if (t < kGroup) a.part_ml[row + t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
-      } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
-          a.part_o[((orow0 + h) * a.num_splits + split) * kHeadDim + t] = o[h] * inv;
-        }
-        if (t < kGroup) {
-          const float ls = ft_sel4(lsum, t);
-          a.part_lse[(orow0 + t) * a.num_splits + split] =
-              ls > 0.f ? (ft_sel4(m, t) + log2f(ls)) * kFtLn2 : -INFINITY;
-        }
-      }
+      for (int h = 0; h < 4; ++h) a.part_o[(row + h) * kHeadDim + t] = o[h];
+      if (t < kGroup) a.part_ml[row + t] = make_float2(ft_sel4(m, t), ft_sel4(lsum, t));
     }
   };
 
@@ -1099,7 +1080,37 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
           lsum[2] += v.z;
           lsum[3] += v.w;
         }
-        results(t, seq, orow0, direct, x.split, m, lsum, {});
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (seq >> 1) & 1));
+        if (ok) {
+          tc::fence_after_sync();
+          float o8[8];
+          tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o8);  // dim t: heads 0..3, high parts then remainders
+          tc::tmem_wait_ld();
+          tc::fence_before_sync();
+          mbar_arrive(&bars->o_empty[ub]);
+          float o[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) o[h] = (o8[h] + o8[4 + h]) * kFtPUnscale;
+          if (direct) {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
+              dst[h * kHeadDim] = static_cast<uint16_t>(pack_bf16x2(o[h] * inv, 0.f) & 0xffffu);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const float inv = lsum[h] > 0.f ? 1.f / lsum[h] : 0.f;
+              a.part_o[((orow0 + h) * a.num_splits + x.split) * kHeadDim + t] = o[h] * inv;
+            }
+            if (t < kGroup) {
+              const float ls = ft_sel4(lsum, t);
+              a.part_lse[(orow0 + t) * a.num_splits + x.split] =
+                  ls > 0.f ? (ft_sel4(m, t) + log2f(ls)) * kFtLn2 : -INFINITY;
+            }
+          }
+        }
       }
       ++seq;
     }
