@@ -34,6 +34,8 @@
 //     2^-8 out of E4M3's subnormal range.  The sum of the weights is kept in
 //     FP32 from the unrounded values; the epilogue divides O by 2^6 again.
 //
+// (The cache with block scales: three E5M2 parts of the weights instead, see below.)
+//
 // The persistent CTAs stride through the units.  CTA = 8 warps:
 //   warp 0 / 1 : K / V producer -- one TMA load per block (16 tokens x 128
 //                bytes, 128-byte swizzle: the layout the MMA reads) into
@@ -56,7 +58,13 @@
 // in turn, each with a maximum, a sum and an accumulator of its own, and warps
 // 12-15 join the groups, divide and store while the softmax is at the next unit
 // (with one group that stores for itself a unit of one tile took 5000 cycles of
-// the softmax, 2,800 of them behind its tile).  What bounds it is HBM: 128
+// the softmax, 2,800 of them behind its tile).  The weights enter by way of FP16
+// as three E5M2 parts times 2^13, rows 0-3, 4-7 and 8-11 of P^T: E5M2 is FP16's
+// upper byte, so the parts come by two subtractions, and its range, 2^-16 .. 2^15,
+// holds a weight to 2^-8 of itself down to 2^-21 of the row's largest and to an
+// absolute 2^-30 of that below.  (Two E4M3 parts drop what lies under 2^-16 of the
+// largest, while the sum that divides keeps it: where the first key held nine
+// tenths of the weight of 32,768, the row was off by a third.)  What bounds it is HBM: 128
 // requests of 8192 to 8447 tokens, 8 KV heads, take 320 us, as long as a copy of
 // as many bytes; 64 of 16 to 16000 64 us (56), the rest being the start, 5 us to
 // the first scores, the ends of rows and the joining.  One request of 8300
@@ -118,6 +126,10 @@ constexpr uint32_t kFtTmemCols = 128;
 constexpr float kFtLazyMax = 2.f;       // base-2 units: weights stay at or below 2^2
 constexpr float kFtPScale = 64.f;       // weights enter P^T times 2^6 (at most 2^8 < 448)
 constexpr float kFtPUnscale = 1.f / 64.f;
+// kScaled: times 2^13, at most 2^15, so that E5M2 holds them down to 2^-29 of the maximum.
+constexpr float kFtWideScale = 8192.f;
+constexpr float kFtWideUnscale = 1.f / 8192.f;
+constexpr int kFtWideCols = 12;         // columns of O^T: three parts of four heads
 constexpr float kFtLn2 = 0.6931471805599453f;
 constexpr int kFtNamedBar = 1;          // the softmax warps' barrier
 
@@ -545,9 +557,12 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (nth >> 1) & 1));
     if (!ok) return;
     tc::fence_after_sync();
-    float o8[2][8];  // dim t: heads 0..3, high parts then remainders
+    float o12[2][kFtWideCols];  // dim t: heads 0..3 of each part
 #pragma unroll
-    for (int g = 0; g < 2; ++g) tc::tmem_ld8(tmem + lane_off + kColO + 32 * ub + 16 * g, o8[g]);
+    for (int g = 0; g < 2; ++g) {
+      tc::tmem_ld8(tmem + lane_off + kColO + 32 * ub + 16 * g, o12[g]);
+      tc::tmem_ld4(tmem + lane_off + kColO + 32 * ub + 16 * g + 8, o12[g] + 8);
+    }
     tc::tmem_wait_ld();
     tc::fence_before_sync();
     mbar_arrive(&bars->o_empty[ub]);
@@ -556,7 +571,8 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     for (int h = 0; h < 4; ++h)
 #pragma unroll
       for (int g = 0; g < 2; ++g)
-        if (f[g][h] != 0.f) o[h] = fmaf((o8[g][h] + o8[g][4 + h]) * kFtPUnscale, f[g][h], o[h]);
+        if (f[g][h] != 0.f)
+          o[h] = fmaf((o12[g][h] + (o12[g][4 + h] + o12[g][8 + h])) * kFtWideUnscale, f[g][h], o[h]);
     if constexpr (kCluster) {
 #pragma unroll
       for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
@@ -590,7 +606,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     // are done never waits behind the next tile's K arrival.
     if (lane == 0) {
       constexpr uint32_t kIdS = tc::idesc_e4m3_f32(128, kFtN, false, false);
-      constexpr uint32_t kIdO = tc::idesc_e4m3_f32(128, kFtN, true, false);
+      constexpr uint32_t kIdO = tc::idesc_e4m3_f32(128, kFtN, true, false) | (kScaled ? tc::kIdescE5m2B : 0u);
       struct Cursor {
         FtWalk walk;
         int j, i, seq, n;  // tile in unit, tile overall, unit ordinal, tiles of the unit (0: at the end)
@@ -962,13 +978,19 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[prev & 1], (prev >> 1) & 1));
             if (ok) {
               tc::fence_after_sync();
-              float o[8];  // columns h (high parts) and 4 + h (remainders) of head h
+              float o[kFtWideCols];  // columns h, 4 + h (kScaled: and 8 + h) of head h
               tc::tmem_ld8(tmem + lane_off + ocol, o);
+              if constexpr (kScaled) tc::tmem_ld4(tmem + lane_off + ocol + 8, o + 8);
               tc::tmem_wait_ld();
               uint32_t ob[8];
 #pragma unroll
               for (int h = 0; h < 8; ++h) ob[h] = __float_as_uint(o[h] * alpha[h & 3]);
               tc::tmem_st8(tmem + lane_off + ocol, ob);
+              if constexpr (kScaled) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) o[8 + h] *= alpha[h];
+                tc::tmem_st4(tmem + lane_off + ocol + 8, o + 8);
+              }
               tc::tmem_wait_st();
               tc::fence_before_sync();
             }
@@ -976,8 +998,10 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h) l[h] *= alpha[h];
         }
-        // the weights, and as E4M3 high parts and remainders times 2^6
-        uint32_t phi[2][2], plo[2][2];  // [half][pair]: head 2k in the low byte, 2k + 1 in the high byte
+        // the weights, and as E4M3 high parts and remainders times 2^6, head 2k in
+        // the low byte, 2k + 1 in the high byte; kScaled: as three E5M2 parts times
+        // 2^13, in the upper bytes of the two halves
+        uint32_t phi[2][2], plo[2][2], pmid[2][2];  // [half][pair]
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           float p[4];
@@ -992,6 +1016,13 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
+            if constexpr (kScaled) {
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                  : "=r"(phi[hf][k])
+                  : "f"(p[2 * k + 1] * kFtWideScale), "f"(p[2 * k] * kFtWideScale));
+              tc::e5m2_parts(phi[hf][k], pmid[hf][k], plo[hf][k]);
+              continue;
+            }
             const float x0 = p[2 * k] * kFtPScale, x1 = p[2 * k + 1] * kFtPScale;
             phi[hf][k] = f32x2_to_e4m3x2(x1, x0);
             float r0, r1;
@@ -1035,8 +1066,14 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
             uint8_t* pt = smem + kOffPt + (2 * sb + hf) * kFtOpBytes;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              pt[tc::sw128_offset_b8(h, t)] = static_cast<uint8_t>(phi[hf][h >> 1] >> (8 * (h & 1)));
-              pt[tc::sw128_offset_b8(4 + h, t)] = static_cast<uint8_t>(plo[hf][h >> 1] >> (8 * (h & 1)));
+              if constexpr (kScaled) {
+                pt[tc::sw128_offset_b8(h, t)] = static_cast<uint8_t>(phi[hf][h >> 1] >> (8 + 16 * (h & 1)));
+                pt[tc::sw128_offset_b8(4 + h, t)] = static_cast<uint8_t>(pmid[hf][h >> 1] >> (8 + 16 * (h & 1)));
+                pt[tc::sw128_offset_b8(8 + h, t)] = static_cast<uint8_t>(plo[hf][h >> 1] >> (8 + 16 * (h & 1)));
+              } else {
+                pt[tc::sw128_offset_b8(h, t)] = static_cast<uint8_t>(phi[hf][h >> 1] >> (8 * (h & 1)));
+                pt[tc::sw128_offset_b8(4 + h, t)] = static_cast<uint8_t>(plo[hf][h >> 1] >> (8 * (h & 1)));
+              }
             }
           }
           tc::fence_proxy_async_smem();  // P^T and zeroed V rows before the tensor core reads them

@@ -73,6 +73,20 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, bool a_mn_ma
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The same with E5M2 A or B (type code 1): the types of the two are independent.
+constexpr uint32_t kIdescE5m2A = 1u << 7;
+constexpr uint32_t kIdescE5m2B = 1u << 10;
+
+// 2 FP16 values, not negative, as three E5M2 parts each: `hi` and `mid` cut to 3
+// significant bits, `lo` rounded, each in the upper byte of its half (E5M2 is
+// FP16's upper byte), so that the parts sum to the value within 2^-9 of it, down
+// to E5M2's smallest step, 2^-16.
+__device__ __forceinline__ void e5m2_parts(uint32_t hi, uint32_t& mid, uint32_t& lo) {
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(mid) : "r"(hi), "r"(hi & 0xff00ff00u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(mid), "r"(mid & 0xff00ff00u));
+  lo += 0x00800080u;
+}
+
 // D[tmem] (+)= A[smem] * B[smem] for 8-bit floating-point operands; issued by one thread.
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
