@@ -810,10 +810,9 @@ pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scale
  * Codes of every token of the context must be finite (no 0x7f, 0xff); slots
  * past it may hold anything.
  * Queries enter as two E4M3 parts (off by at most 2^-17 of a head's largest
- * value).  Weights times their V scale enter, for single queries, as three E5M2
- * parts (off by at most 2^-8 of each or 2^-30 of the row's largest one), up to
- * q_len 32 as two E4M3 parts (2^-8 of each or 2^-16 of the largest), beyond that
- * as FP16 (2^-11 of each or 2^-25 of the largest); the sum that divides them is
+ * value).  Weights times their V scale enter, up to q_len 32, as three E5M2 parts
+ * (off by at most 2^-8 of each or 2^-30 of the row's largest one), beyond that
+ * as FP16 (2^-11 of each or 2^-32 of the largest); the sum that divides them is
  * that of the unrounded ones.  A call's result is bitwise
  * reproducible, but where a request's keys are divided among CTAs, and so its
  * last bits, follow from the whole batch's lengths.

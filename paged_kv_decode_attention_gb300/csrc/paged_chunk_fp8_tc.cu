@@ -25,6 +25,8 @@
 //         warps convert each V tile to FP16, once for all rows.  (With two
 //         E4M3 parts of each weight the softmax of a tile took 900 cycles of
 //         a warp for its exponentials and parts, now as many as a prompt's.)
+//         They enter times 2^7, so that FP16's range, 2^-24 .. 2^15, reaches
+//         down to 2^-31 of the largest.
 // !kWide: up to kRows rows, 32, 64 or 128.  HBM is the bound, and a chain of
 //         scores, softmax and product is longer than a tile's transfer.  So
 //         the CTA's two halves take the even and the odd tiles of keys, and
@@ -33,24 +35,26 @@
 //         sum of their own (the other keys' weights are zeros).  At the end
 //         all copies and both halves are joined through shared memory.  Up to
 //         32 rows the products have M = 64, which reads half as much of the
-//         queries per product, and two threads share a row.  V's
-//         codes enter as they are and the weights as two E4M3 parts times 2^6
-//         (2^-8 relative, by way of FP16, down to 2^-16 of the largest).
+//         queries per product, and two threads share a row.  V's codes enter
+//         as they are and the weights as three E5M2 parts times 2^13, by way
+//         of FP16 (2^-8 relative, down to 2^-30 of the largest).  (With two
+//         E4M3 parts, which lose what lies below 2^-16 of the largest, and
+//         two buffers for them, 37 x 7 took 38 us, not 42: half of the
+//         difference is the third part's two products.)
 //
-// Scores (64 columns), two buffers of weights (32 each) and O fill a row tile's
-// 256 columns of tensor memory.  The next scores are issued as soon as the
+// Scores (64 columns), the weights (32, their parts 48) and O lie in a row
+// tile's 256 columns of tensor memory.  The next scores are issued as soon as the
 // softmax holds the present ones in registers, ahead of the product that waits
 // for their weights: neither side waits for the other's latency.
 //
 // Measured, 32 query and 8 KV heads: 4 x 2000 queries behind 4000 to 8000
 // tokens 0.78 ms, 1.3 PFLOP/s (tiles of 128 keys with scores and weights in one
-// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 38 us, 4.5 TB/s (57).  A
-// tile of the latter takes 720 cycles, as long as its transfer; the rest is the
-// start, 6000 cycles to the first scores, the ends of jobs, 3,500 each, and the
-// joining kernel.  37 requests behind 2100 tokens, by the rows' layout: 8 queries
-// 35.5 us with M = 64, 41 with 64 rows of M = 128, 51 with 128; 16
-// queries 46 with 64 rows, 56 with 128, 60 as kWide; 32 queries 62 with 128, 70
-// as kWide.
+// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 42 us, 4.0 TB/s (57): the
+// products' issue, the start, 6000 cycles to the first scores, the ends of jobs,
+// 3,500 each, and the joining kernel.  37 requests behind 2100 tokens, by the
+// rows' layout: 8 queries 41 us with M = 64, 49 with 64 rows of M = 128, 60 with
+// 128; 16 queries 55 with 64 rows, 65 with 128, 67 as kWide; 24 queries 68 with
+// 128, 73 as kWide; 32 queries 72 with 128, 77 as kWide.
 //
 // Work is cut by tiles, not by requests (pkv_shares.cuh); a cut job leaves
 // un-normalised FP32 partials.
@@ -108,22 +112,19 @@ struct CfShape {
   static_assert(kOffBar % 16 == 0 && kOffScale % 16 == 0 && kOffRing % 1024 == 0, "alignment");
 };
 
-constexpr uint32_t kCfTileCols = 256;                 // S, two buffers of weights (high parts, low parts), O
+constexpr uint32_t kCfTileCols = 256;                 // S, weights, O
 constexpr uint32_t kCfColP = 64;
-constexpr uint32_t kCfPCols = 32;
-constexpr uint32_t kCfColLow = 16;                    // low parts, within a buffer
+constexpr uint32_t kCfPartCols = 16;                  // !kWide: a part of the weights
 constexpr uint32_t kCfColO = 128;
-constexpr uint32_t kCfColQ = 96;                      // kWide: one buffer of weights, then the queries' high parts
+constexpr uint32_t kCfColQ = 96;                      // kWide: the queries' high parts, behind the weights
 constexpr int kCfSoftmaxRegs = 168;
 constexpr int kCfOtherRegs = 88;
 static_assert((2 * kCfSoftmaxRegs + 2 * kCfOtherRegs) * 128 <= 128 * kCfThreads, "register split");
-// Base 2: how far the weights' maximum may lag.  E4M3 parts: weights stay at
-// or below 2^2, 2^8 with the factor below (E4M3 reaches 448).  FP16: 2^8.
-constexpr float kCfLagParts = 2.f;
-constexpr float kCfLagHalf = 8.f;
-// The parts stand for 2^6 times the weight; they are cut from an FP16 value 2^-8
-// of that.
-constexpr float kCfFactor = -2.f;
+// Base 2: how far the weights' maximum may lag, and what they are taken times, so
+// that they stay at or below 2^15: E5M2 reaches 1.75 times that, FP16 twice.
+constexpr float cf_lag(bool wide) { return wide ? 8.f : 2.f; }
+constexpr float cf_factor(bool wide) { return 15.f - cf_lag(wide); }
+// The queries' parts are cut from FP16 values 2^-8 of what they stand for.
 constexpr float kCfCodeUnit = 256.f;
 // Least factor of a score: below it scores are as good as zero, and a product
 // of scales that vanishes would turn masked ones, -inf, into NaN.
@@ -177,21 +178,23 @@ __device__ __forceinline__ void mma_f8_tmem_a(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// 4 weights (0 .. 1, 2^-8 of what the parts stand for) as the bytes of their
-// high parts, cut to 4 significant bits, and of what that leaves, rounded to 4.
-// (FP16's exponent field is E4M3's here, subnormals included, so both parts
-// come by masks and shifts.)
-__device__ __forceinline__ void cf_weights(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
-  uint32_t h0, h1, r0, r1;
+// 4 weights as the bytes of their three E5M2 parts.
+__device__ __forceinline__ void cf_weights(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& mid,
+                                           uint32_t& lo) {
+  uint32_t h0, h1, m0, m1, l0, l1;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h0) : "f"(p1), "f"(p0));
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h1) : "f"(p3), "f"(p2));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(h0), "r"(h0 & 0xff80ff80u));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(h1), "r"(h1 & 0xff80ff80u));
-  hi = __byte_perm(h0 << 1, h1 << 1, 0x7531);
-  lo = __byte_perm(r0 * 2 + 0x00800080u, r1 * 2 + 0x00800080u, 0x7531);
+  tc::e5m2_parts(h0, m0, l0);
+  tc::e5m2_parts(h1, m1, l1);
+  hi = __byte_perm(h0, h1, 0x7531);
+  mid = __byte_perm(m0, m1, 0x7531);
+  lo = __byte_perm(l0, l1, 0x7531);
 }
 
-// The same for 4 signed values.
+// 4 signed values (2^-8 of what the parts stand for) as the bytes of their high
+// parts, E4M3 cut to 4 significant bits, and of what that leaves, rounded to 4.
+// (FP16's exponent field is E4M3's here, subnormals included, so both parts
+// come by masks and shifts.)
 __device__ __forceinline__ void cf_signed(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
   uint32_t h0, h1;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h0) : "f"(x1), "f"(x0));
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       // ---------------------------- MMA issuers ----------------------------
       constexpr uint32_t kIdS = tc::idesc_e4m3_f32(R::kMma, kCfTokens, false, false);
       constexpr uint32_t kIdO = kWide ? tc::idesc_f16_f32(kCfRows, kHeadDim, false, true)
-                                      : tc::idesc_e4m3_f32(R::kMma, kHeadDim, false, true);
+                                      : tc::idesc_e4m3_f32(R::kMma, kHeadDim, false, true) | tc::kIdescE5m2A;
       const int t = warp - 9;
       const bool leader = lane == 0;
       const uint32_t scol = tmem + t * kCfTileCols;
@@ -654,21 +657,21 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         }
         __syncwarp();
       };
-      // O += P V: FP16, or (high + low parts of the weights) V's codes
+      // O += P V: FP16, or (the three parts of the weights) V's codes
       auto issue_pv = [&](uint32_t place, uint32_t tile, uint32_t buf, bool first) {
         const uint64_t vd = kWide ? v16 + (tile % kCfV16Stages) * (kCfV16Bytes >> 4)
                                   : ring + (place % kSlots) * (kCfTileBytes >> 4);
-        const uint32_t pcol = scol + kCfColP + (kWide ? 0 : buf * kCfPCols);
+        const uint32_t pcol = scol + kCfColP;
         tc::fence_after_sync();
         if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < (kWide ? 4 : 6); ++kk) {
             if constexpr (kWide) {  // 16 keys
               tc::mma_bf16_tmem_a(scol + kCfColO, pcol + 8 * kk, vd + kk * (2048 >> 4), kIdO, (!first || kk > 0) ? 1u : 0u);
               continue;
             }
             const int slice = kk & 1;  // of 32 keys
-            mma_f8_tmem_a(scol + kCfColO, pcol + kCfColLow * (kk >> 1) + 8 * slice, vd + slice * (4096 >> 4), kIdO,
+            mma_f8_tmem_a(scol + kCfColO, pcol + kCfPartCols * (kk >> 1) + 8 * slice, vd + slice * (4096 >> 4), kIdO,
                           (!first || kk > 0) ? 1u : 0u);
           }
           tc::commit(&bars->o_done[t][buf]);
@@ -834,8 +837,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           tc::tmem_wait_ld();
           tc::fence_before_sync();
           mbar_arrive(&bars->s_free[t]);
-          // the weights' buffer: its last product is done (see the issuers)
-          const uint32_t pcol = scol + kCfColP + (kWide ? 0 : (g & 1) * kCfPCols);
+          const uint32_t pcol = scol + kCfColP;
           auto store = [&](uint32_t col, const uint32_t* w) {
             if constexpr (R::kHalf) {
               tc::tmem_st16x2_4<kCols / 4>(col, w);
@@ -845,11 +847,6 @@ __global__ void __launch_bounds__(kCfThreads, 1)
               tc::tmem_st8(col, w);
             }
           };
-          if constexpr (kCopies > 1) {  // the other copy's keys: weights of zero
-            const uint32_t zeros[kCols / 4] = {};
-            store(pcol + (copy ^ 1) * (R::kCopyKeys / 4), zeros);
-            store(pcol + kCfColLow + (copy ^ 1) * (R::kCopyKeys / 4), zeros);
-          }
           if (warp_seen - tok - copy * R::kCopyKeys < R::kCopyKeys) {  // some row of the warp sees its keys in part
             const int lim = seen - tok - key0;
 #pragma unroll
@@ -865,7 +862,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             mx = fmaxf(mx, fmaf(x, fmaxf(sc[b] * c, kCfLeast), sc[kCfTileBlocks + b]));  // (the factor is > 0)
           }
           if constexpr (R::kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const bool grow = mx > m + (kWide ? kCfLagHalf : kCfLagParts);  // also true the first time a row sees a key
+          const bool grow = mx > m + cf_lag(kWide);  // also true the first time a row sees a key
           const float m_new = grow ? mx : m;
           const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
           if (__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY)) {
@@ -899,7 +896,14 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           }
           l *= alpha;
           m = m_new;
-          const float nm = (m == -INFINITY ? 0.f : -m) + (kWide ? 0.f : kCfFactor);
+          const float nm = (m == -INFINITY ? 0.f : -m) + cf_factor(kWide);
+          auto weights_free = [&]() {  // their place is free once the product before is done
+            if (j > 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
+              tc::fence_after_sync();
+            }
+            return ok;
+          };
           if constexpr (kWide) {
             uint32_t w[8 * kCfTileBlocks];
 #pragma unroll
@@ -917,15 +921,11 @@ __global__ void __launch_bounds__(kCfThreads, 1)
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
             }
-            if (j > 0) {  // the weights' place is free once the product before is done
-              ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
-              if (!ok) break;
-              tc::fence_after_sync();
-            }
+            if (!weights_free()) break;
             tc::tmem_st16u(pcol, w);
             tc::tmem_st16u(pcol + 16, w + 16);
           } else {
-            uint32_t hi[kCols / 4], lo[kCols / 4];
+            uint32_t hi[kCols / 4], mid[kCols / 4], lo[kCols / 4];
 #pragma unroll
             for (int b = 0; b < kCols / kBlockSize; ++b) {
               const float kc = fmaxf(sc[b] * c, kCfLeast), off = sc[kCfTileBlocks + b] + nm;
@@ -941,12 +941,21 @@ __global__ void __launch_bounds__(kCfThreads, 1)
                 const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
                 acc = __fadd2_rn(acc, make_float2(p0, p1));
                 acc = __fadd2_rn(acc, make_float2(p2, p3));
-                cf_weights(p0, p1, p2, p3, hi[4 * b + e], lo[4 * b + e]);
+                cf_weights(p0, p1, p2, p3, hi[4 * b + e], mid[4 * b + e], lo[4 * b + e]);
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
             }
-            store(pcol + copy * (R::kCopyKeys / 4), hi);
-            store(pcol + kCfColLow + copy * (R::kCopyKeys / 4), lo);
+            if (!weights_free()) break;
+            const uint32_t at = pcol + copy * (R::kCopyKeys / 4);
+            store(at, hi);
+            store(at + kCfPartCols, mid);
+            store(at + 2 * kCfPartCols, lo);
+            if constexpr (kCopies > 1) {  // the other copy's keys: weights of zero
+              const uint32_t zeros[kCols / 4] = {};
+              const uint32_t other = pcol + (copy ^ 1) * (R::kCopyKeys / 4);
+#pragma unroll
+              for (int part = 0; part < 3; ++part) store(other + part * kCfPartCols, zeros);
+            }
             if (ctx - tok < kCfTokens && (ctx & (kBlockSize - 1)) != 0) {
               // slots past the context may hold any code: V's rows there are
               // zeroed (a weight of zero is not enough)
@@ -975,7 +984,6 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         if (!ok) break;
         leave();
       }
-      if (!kWide) l *= kCfCodeUnit;  // in O's unit
       if constexpr (R::kHalf) l += __shfl_xor_sync(0xffffffffu, l, 16);
       // ---- results ----
       if (n_t > 0) {

@@ -57,7 +57,7 @@ def sink_error(case, out, ctx):
 @pytest.mark.parametrize("requests", [1, 152])
 @pytest.mark.parametrize("ctx,share,v_sink", [(2048, 0.9, 0.02), (8192, 0.9, 0.02), (32768, 0.5, 1.0), (32768, 0.9, 0.02),
                                               (131072, 0.5, 1.0), (131072, 0.99, 0.02)])
-@pytest.mark.parametrize("q_len", [1])
+@pytest.mark.parametrize("q_len", [1, 2, 8, 9, 16, 17, 32, 40])
 def test_most_of_the_weight_on_one_key(q_len, ctx, share, v_sink, requests):
     """Each weight is off by at most 2^-8 of itself, whatever the largest one is: of the row no more than that, and the
     result's rounding to BF16, 2^-8 of each value at most and evenly spread, 2^-8 / sqrt(3) of the row's norm."""
