@@ -9,8 +9,9 @@
 // scales of a key's block:
 //   S_ij = sum_d (sigma_i q_id) kcode_jd      (tensor cores, codes as they are)
 //   y_ij = S_ij (scale / sigma_i) ks_j + log2(vs_j), in base 2
-//   w_ij = 2^(y_ij - m_i), m_i a running maximum of y: so that the weights are
-//          what the second product needs, inside E4M3's range whatever vs is
+//   w_ij = 2^(y_ij - m_i), m_i a running maximum of y less a constant: so that
+//          the weights are what the second product needs, in the range of their
+//          type whatever vs is
 //   O_i  = sum_j w_ij vcode_j,   l_i = sum_j w_ij / vs_j,   out = O_i / l_i
 // Scales are constant over 16 keys, so they cost a few FP32 operations per 16
 // scores.  8-bit products want both operands in 8 bits.  Queries enter S as two
@@ -39,7 +40,7 @@
 //         as they are and the weights as three E5M2 parts times 2^13, by way
 //         of FP16 (2^-8 relative, down to 2^-30 of the largest).  (With two
 //         E4M3 parts, which lose what lies below 2^-16 of the largest, and
-//         two buffers for them, 37 x 7 took 38 us, not 42: half of the
+//         two buffers for them, 37 x 7 took 38 us, not 43: half of the
 //         difference is the third part's two products.)
 //
 // Scores (64 columns), the weights (32, their parts 48) and O lie in a row
@@ -48,8 +49,8 @@
 // for their weights: neither side waits for the other's latency.
 //
 // Measured, 32 query and 8 KV heads: 4 x 2000 queries behind 4000 to 8000
-// tokens 0.78 ms, 1.3 PFLOP/s (tiles of 128 keys with scores and weights in one
-// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 42 us, 4.0 TB/s (57): the
+// tokens 0.79 ms, 1.3 PFLOP/s (tiles of 128 keys with scores and weights in one
+// buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 43 us, 4.0 TB/s (57): the
 // products' issue, the start, 6000 cycles to the first scores, the ends of jobs,
 // 3,500 each, and the joining kernel.  37 requests behind 2100 tokens, by the
 // rows' layout: 8 queries 41 us with M = 64, 49 with 64 rows of M = 128, 60 with
@@ -120,10 +121,10 @@ constexpr uint32_t kCfColQ = 96;                      // kWide: the queries' hig
 constexpr int kCfSoftmaxRegs = 168;
 constexpr int kCfOtherRegs = 88;
 static_assert((2 * kCfSoftmaxRegs + 2 * kCfOtherRegs) * 128 <= 128 * kCfThreads, "register split");
-// Base 2: how far the weights' maximum may lag, and what they are taken times, so
-// that they stay at or below 2^15: E5M2 reaches 1.75 times that, FP16 twice.
-constexpr float cf_lag(bool wide) { return wide ? 8.f : 2.f; }
-constexpr float cf_factor(bool wide) { return 15.f - cf_lag(wide); }
+// Base 2: weights stay at or below 2^15 (E5M2 reaches 1.75 times that, FP16
+// twice).  A new maximum is given 2^13, or 2^7, and room to be exceeded.
+constexpr float kCfTop = 15.f;
+constexpr float cf_start(bool wide) { return wide ? 7.f : 13.f; }
 // The queries' parts are cut from FP16 values 2^-8 of what they stand for.
 constexpr float kCfCodeUnit = 256.f;
 // Least factor of a score: below it scores are as good as zero, and a product
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_empty[qb]);
-      float m = -INFINITY;  // of y, what the weights are taken against (lags the true maximum)
+      float m = -INFINITY;  // what the weights are taken against (see kCfTop)
       float l = 0.f;        // sum of w / vs, in the weights' unit
       // Scales come in groups of 8 tiles, so that a tile need not wait for them.
       const uint32_t set0 = sets;
@@ -862,8 +863,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             mx = fmaxf(mx, fmaf(x, fmaxf(sc[b] * c, kCfLeast), sc[kCfTileBlocks + b]));  // (the factor is > 0)
           }
           if constexpr (R::kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const bool grow = mx > m + cf_lag(kWide);  // also true the first time a row sees a key
-          const float m_new = grow ? mx : m;
+          const bool grow = mx - m > kCfTop;  // also true the first time a row sees a key
+          const float m_new = grow ? __fsub_ru(mx, cf_start(kWide)) : m;  // (upwards: far from zero no weight above)
           const float alpha = grow ? exp2_approx(m - m_new) : 1.f;  // 0 while m is -inf
           if (__any_sync(0xffffffffu, grow && j > 0 && m != -INFINITY)) {
             // O holds weights taken against the old maxima: rescale this warp's rows
@@ -896,7 +897,16 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           }
           l *= alpha;
           m = m_new;
-          const float nm = (m == -INFINITY ? 0.f : -m) + cf_factor(kWide);
+          // The weights' exponents, y - m: y rounded as for the maximum, then the
+          // difference, which is exact near m.  (Fused, y is not rounded and m is:
+          // where scores reach 2^25 the largest weight was off by factors of 2 and
+          // more and left its parts' range.  Chunks took 2 % less time, drafts as much.)
+          const float less = m == -INFINITY ? 0.f : -m;
+          auto weights_of = [&](int i, float kc, float lv) -> float2 {
+            float2 y = __ffma2_rn(make_float2(s[i], s[i + 1]), make_float2(kc, kc), make_float2(lv, lv));
+            y = __fadd2_rn(y, make_float2(less, less));
+            return make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          };
           auto weights_free = [&]() {  // their place is free once the product before is done
             if (j > 0) {
               ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[t][(g - 1) & 1], ((g - 1) >> 1) & 1));
@@ -908,16 +918,13 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             uint32_t w[8 * kCfTileBlocks];
 #pragma unroll
             for (int b = 0; b < kCfTileBlocks; ++b) {
-              const float kc = fmaxf(sc[b] * c, kCfLeast), off = sc[kCfTileBlocks + b] + nm;
-              const float2 k2 = make_float2(kc, kc);
-              const float2 n2 = make_float2(off, off);
+              const float kc = fmaxf(sc[b] * c, kCfLeast), lv = sc[kCfTileBlocks + b];
               float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float2 x = __ffma2_rn(make_float2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), k2, n2);
-                const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
-                acc = __fadd2_rn(acc, make_float2(p0, p1));
-                w[8 * b + e] = cf_half2(p0, p1);
+                const float2 p = weights_of(16 * b + 2 * e, kc, lv);
+                acc = __fadd2_rn(acc, p);
+                w[8 * b + e] = cf_half2(p.x, p.y);
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
             }
@@ -928,20 +935,14 @@ __global__ void __launch_bounds__(kCfThreads, 1)
             uint32_t hi[kCols / 4], mid[kCols / 4], lo[kCols / 4];
 #pragma unroll
             for (int b = 0; b < kCols / kBlockSize; ++b) {
-              const float kc = fmaxf(sc[b] * c, kCfLeast), off = sc[kCfTileBlocks + b] + nm;
-              const float2 k2 = make_float2(kc, kc);
-              const float2 n2 = make_float2(off, off);
+              const float kc = fmaxf(sc[b] * c, kCfLeast), lv = sc[kCfTileBlocks + b];
               float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int i = 16 * b + 4 * e;
-                const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), k2, n2);
-                const float2 y = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), k2, n2);
-                const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
-                const float p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
-                acc = __fadd2_rn(acc, make_float2(p0, p1));
-                acc = __fadd2_rn(acc, make_float2(p2, p3));
-                cf_weights(p0, p1, p2, p3, hi[4 * b + e], mid[4 * b + e], lo[4 * b + e]);
+                const float2 p = weights_of(16 * b + 4 * e, kc, lv), q = weights_of(16 * b + 4 * e + 2, kc, lv);
+                acc = __fadd2_rn(acc, p);
+                acc = __fadd2_rn(acc, q);
+                cf_weights(p.x, p.y, q.x, q.y, hi[4 * b + e], mid[4 * b + e], lo[4 * b + e]);
               }
               l = fmaf(acc.x + acc.y, sc[2 * kCfTileBlocks + b], l);
             }

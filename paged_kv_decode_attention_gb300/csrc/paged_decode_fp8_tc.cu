@@ -966,7 +966,8 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
         bool grow_any = false;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const bool grow = tm[h] > m[h] + kFtLazyMax || (m[h] == -INFINITY && tm[h] != -INFINITY);
+          // (the difference, exact near m as the sum is not; infinite the first time)
+          const bool grow = tm[h] - m[h] > kFtLazyMax;
           alpha[h] = grow ? exp2_approx(m[h] - tm[h]) : 1.f;  // 0 while m is -inf
           if (grow) m[h] = tm[h];
           grow_any = grow_any || grow;

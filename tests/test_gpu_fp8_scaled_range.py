@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_fp8_scaled import BLOCK, D, SCALE, run_attention
+from test_gpu_fp8_scaled import BLOCK, D, SCALE, attention_case, dev, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,36 @@ def test_most_of_the_weight_on_one_key(q_len, ctx, share, v_sink, requests):
     case = sink_case(requests, ctx, share, v_sink, q_len)
     out = run_attention(*case, [ctx] * requests)
     assert sink_error(case, out, ctx) < 5e-3
+
+
+@pytest.mark.parametrize("q_len", [1, 4, 8, 16, 20, 32, 40, 100])
+@pytest.mark.parametrize("e", [-6, 10, 16, 18, 20, 25, 28, 32])
+def test_scores_far_from_zero(q_len, e):
+    """K scales up to the largest: the scores' differences are far beyond the rounding of the scores, so a row's result
+    is the value of its highest key, to the rounding of that one weight (2^-8) and of the result (2^-8)."""
+    ctx = [300, 64, 900]
+    q, kc, vc, ks, vs, t = attention_case(ctx, q_len, 2)
+    ks.fill_(2.0 ** e)
+    out = run_attention(q, kc, vc, ks, vs, t, ctx)
+    assert bool(out.isfinite().all())
+    clear, rows = 0, 0
+    for r, c in enumerate(ctx):
+        at = torch.arange(c, device="cuda")
+        blk, off = dev(t[r], torch.int64)[at // BLOCK], at % BLOCK
+        seen = at[None] <= torch.arange(c - q_len, c, device="cuda")[:, None]
+        for h in range(8):
+            k, v = (z.view(torch.float8_e4m3fn).float()[blk, h // 4, off].double() * s[blk, h // 4, None].double()
+                    for z, s in ((kc, ks), (vc, vs)))
+            x = (q[r, :, h].double() @ k.T * SCALE).masked_fill(~seen, -math.inf)
+            # a score is off by at most 2^-17 of sum |q| |k| twice over (see test_gpu_fp8_scaled.check), and its
+            # rounding; 40 more: the other keys' weights are below 2^-50
+            slack = SCALE * 2.0 ** -16 * (q[r, :, h].double().abs().amax(-1, keepdim=True) * k.abs().sum(-1)).amax(-1)
+            exp = x.amax(-1) - slack * 4 - 40
+            one = ((x > exp[:, None]).sum(-1) == 1) & (seen.sum(-1) > 0)
+            want = v[x.argmax(-1)]
+            err = (out[r, :, h].double() - want).abs()
+            assert bool((err[one] <= 2.0 ** -7 * 1.01 * want[one].abs()).all())
+            clear += int(one.sum())
+            rows += int((seen.sum(-1) > 0).sum())
+    if e >= 10:
+        assert clear > 0.9 * rows
