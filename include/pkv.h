@@ -808,7 +808,8 @@ pkv_status pkv_kv_append_fp8_scaled(void* k_cache, void* v_cache, float* k_scale
  *                  bytes.  Its contents are overwritten; calls that share it
  *                  must be stream-ordered.
  * Codes of every token of the context must be finite (no 0x7f, 0xff); slots
- * past it may hold anything.
+ * past it may hold anything.  A query head that holds an infinity or NaN gives
+ * NaN.
  * Queries enter as two E4M3 parts (off by at most 2^-17 of a head's largest
  * value).  Weights times their V scale enter, up to q_len 32, as three E5M2 parts
  * (off by at most 2^-8 of each or 2^-30 of the row's largest one), beyond that

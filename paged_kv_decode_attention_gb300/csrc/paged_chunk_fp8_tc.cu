@@ -212,11 +212,13 @@ __device__ __forceinline__ void cf_signed(float x0, float x1, float x2, float x3
 }
 
 // sigma, the power of two that brings a row's largest |q| (BF16 bits) into
-// [2^7, 2^8), over the parts' unit, 2^8; `inv` = 1 / sigma.  1 for zeros.
+// [2^7, 2^8), over the parts' unit, 2^8; `inv` = 1 / sigma.  1 for zeros; NaN for
+// infinities and NaN, so that all the row's parts and scores are NaN (an
+// infinity's bits would be those of a finite code).
 __device__ __forceinline__ float cf_sigma(uint32_t amax_bits, float& inv) {
   const int e = amax_bits == 0 ? 7 : max(static_cast<int>(amax_bits >> 7) - 127, -113);  // (subnormals: as 2^-113)
   inv = __int_as_float((127 + e - 7) << 23);
-  return __int_as_float((127 + 7 - e) << 23) * (1.f / kCfCodeUnit);
+  return amax_bits >= 0x7f80u ? NAN : __int_as_float((127 + 7 - e) << 23) * (1.f / kCfCodeUnit);
 }
 
 // 16 E4M3 codes as FP16 (exact).

@@ -743,7 +743,8 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
       for (int e = 0; e < 8; ++e) amax = max(amax, max(wv[e] & 0x7fffu, (wv[e] >> 16) & 0x7fffu));
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-      const float sigma = q_sigma(amax);
+      // (kScaled: a head with an infinity or NaN is all NaN; an infinity would saturate)
+      const float sigma = kScaled && amax >= 0x7f80u ? NAN : q_sigma(amax);
       uint32_t hi[4], lo[4];  // 16 E4M3 bytes each, dim 16c + 4k + b in byte b of word k
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

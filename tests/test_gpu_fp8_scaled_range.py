@@ -97,3 +97,26 @@ def test_scores_far_from_zero(q_len, e):
             rows += int((seen.sum(-1) > 0).sum())
     if e >= 10:
         assert clear > 0.9 * rows
+
+
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("q_len", [1, 7, 20, 32, 40])
+@pytest.mark.parametrize("count", [2, 40])
+def test_queries_that_are_not_finite(q_len, count, small):
+    """A query with an infinity or NaN gives NaN, however small the keys are; the others' rows are what they were, bit
+    for bit."""
+    ctx = ([300, 70] * count)[:count]
+    case = attention_case(ctx, q_len, 2)
+    q, kc = case[:2]
+    if small:
+        kc[:] = (2.0 ** -7 * torch.randn(kc.shape, device="cuda")).to(torch.float8_e4m3fn).view(torch.uint8)
+    want = run_attention(*case, ctx)
+    assert bool(want.isfinite().all())
+    bad = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    for i, x in enumerate((math.inf, -math.inf, math.nan)):
+        r, at, h = i % count, (3 * i) % q_len, (3 * i + 1) % 8
+        q[r, at, h, 17 * i + 5] = x
+        bad[r, at, h] = True
+    out = run_attention(*case, ctx)
+    assert bool(out[bad].isnan().all())
+    assert torch.equal(out[~bad], want[~bad])
