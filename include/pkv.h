@@ -827,7 +827,7 @@ pkv_status pkv_paged_attention_fp8_scaled(void* out, const void* q, const void* 
                                           int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
                                           void* stream);
 
-/* pkv_copy_blocks for pools with block scales: codes and scales. */
+/* pkv_copy_blocks for pools with block scales: codes and scales.  Fewer than 2^30 pairs. */
 pkv_status pkv_copy_blocks_fp8_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
                                       const pkv_cache_desc* cache, const int32_t* src_blocks,
                                       const int32_t* dst_blocks, int32_t num_pairs, void* stream);

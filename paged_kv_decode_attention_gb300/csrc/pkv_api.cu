@@ -1396,7 +1396,7 @@ pkv_status pkv_copy_blocks_fp8_scaled(void* k_cache, void* v_cache, float* k_sca
   const pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
   if (num_pairs < 0) return PKV_ERR_SHAPE;
-  if (num_pairs > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+  if (num_pairs >= (1 << 30)) return PKV_ERR_UNSUPPORTED;  // (two CTAs each, below 2^31 to a grid)
   if (num_pairs == 0) return PKV_OK;
   if (!k_cache || !v_cache || !k_scales || !v_scales || !src_blocks || !dst_blocks) return PKV_ERR_NULL;
   if (!aligned({k_cache, v_cache}, 16) || !aligned({k_scales, v_scales, src_blocks, dst_blocks}, 4))
