@@ -784,7 +784,10 @@ pkv_status pkv_prompt_attention(void* out, float* out_lse, const void* q, int64_
  *                  rows cu_new[r] .. cu_new[r + 1] - 1 of k_new and v_new
  *                  (packed as above); NULL = one each, num_tokens == num_seqs.
  *   k_new, v_new : device BF16, strides as for pkv_prompt_attention.  Finite.
- * A request whose entries of cu_new fall or leave 0 .. num_tokens is not stored.
+ * A request whose entries of cu_new fall or leave 0 .. num_tokens is not stored
+ * (PKV_DEVERR_SEQLENS), and of the call's other requests any blocks may then be
+ * left as they were: the call has to be made again with right entries.  No block
+ * is stored in part.
  * One with context_lens[r] <= 0 is a padding row.  One whose context is
  * shorter than its new tokens or longer than its table sets
  * PKV_DEVERR_CONTEXT and nothing of it is stored; a block id outside the pool

@@ -69,7 +69,11 @@ __device__ __forceinline__ uint32_t as_rescale(uint32_t codes, float f) {
 
 // Places: request r's blocks have the places first_place(r) .. : a request of
 // n new tokens touches at most n / 16 + 2 blocks, which is no more than the
-// distance to the next request's first place.
+// distance to the next request's first place.  (Where cu_new falls, places no
+// longer rise with the requests, and some find another request than theirs: their
+// blocks are left out, which the report of the wrong entry stands for.  With a
+// check of all entries by each warp, to refuse the call: 64 requests of up to 200
+// tokens 9.6 us, not 9.2, 300 of one 7.8, not 6.8, 4096 of one 147, not 105.)
 __device__ __forceinline__ int64_t first_place(const AppendScaledArgs& a, int r) {
   return a.cu_new == nullptr ? r : (int64_t{max(a.cu_new[r], 0)} >> 4) + 2 * int64_t{r};
 }

@@ -1,9 +1,10 @@
 """The FP8 cache with block scales at the edges of its calls: a workspace of just the stated size, rows cut into more
-pieces than a warp has lanes."""
+pieces than a warp has lanes, new tokens whose boundaries are wrong."""
 import pytest
 import torch
 
-from test_gpu_fp8_scaled import SCALE, _pkv, attention_case, check, dev, reference, run_attention
+from test_gpu_fp8_scaled import (BLOCK, D, SCALE, _pkv, append_reference, attention_case, check, dev, pool, reference,
+                                 run_attention, tables, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,37 @@ def test_rows_cut_into_many_pieces(q_len, hkv, ctx):
     assert _pkv().get_device_error() == 0
     check(out, reference(*case, ctx), ctx)
     assert torch.equal(out, run_attention(*case, ctx))
+
+
+@pytest.mark.parametrize("cu,ctx", [([0, 100, 3, 8], [100, 30, 5]), ([0, 40, 20, 90], [40, 20, 75]),
+                                    ([10, 60, 60, 201], [57, 0, 150]), ([-3, 50, 90, 200], [60, 43, 115]),
+                                    ([150, 100, 50, 0], [50, 50, 50]), ([0, 64, 0, 64], [70, 64, 64])])
+def test_wrong_boundaries_store_whole_blocks_or_nothing(cu, ctx):
+    """Each block is what it was or what its request's tokens make of it, and a request whose own entries are wrong is
+    left alone."""
+    pkv = _pkv()
+    tokens, hkv, nb = 200, 2, 40
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((2, tokens, hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+    t = tables([-(-c // BLOCK) for c in ctx], nb)
+    kc, ks = pool(nb, hkv, 5)
+    vc, vs = pool(nb, hkv, 6)
+    before = [y.clone() for y in (kc, vc, ks, vs)]
+    pkv.kv_append_fp8_scaled(kc, vc, ks, vs, dev(t), dev(ctx), x[0], x[1], dev(cu))
+    assert pkv.get_device_error() == pkv.DEVERR_SEQLENS
+    stored = 0
+    for codes, scales, old, old_s, y in ((kc, ks, before[0], before[2], x[0]), (vc, vs, before[1], before[3], x[1])):
+        got, got_s = values(codes), scales.double().cpu()
+        was, was_s = values(old), old_s.double().cpu()
+        left = torch.ones(nb, dtype=torch.bool)
+        for r, c in enumerate(ctx):
+            if not 0 <= cu[r] <= cu[r + 1] <= tokens:
+                continue
+            want, want_s = was.clone(), was_s.clone()
+            append_reference(want, want_s, t[r:r + 1], [c], [0, cu[r + 1] - cu[r]], y[cu[r]:cu[r + 1]].double().cpu())
+            for b in t[r][t[r] >= 0]:
+                here = torch.equal(got[b], want[b]) and torch.equal(got_s[b], want_s[b])
+                left[b] = not here
+                stored += here
+        assert torch.equal(got[left], was[left]) and torch.equal(got_s[left], was_s[left])
+    assert stored > 0 or cu == [150, 100, 50, 0]
