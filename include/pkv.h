@@ -749,10 +749,10 @@ pkv_status pkv_kv_compact(void* const* k_caches, void* const* v_caches, int32_t 
  *   head_dim     : 128.
  *   scale        : > 0.
  * K and V of a prompt's tokens must be finite; padding rows may hold anything.
+ * Scores (scale times q.k) must lie within +-2^30; rows with others may be NaN.
  * The weights enter the second product rounded to BF16, off by at most 2^-8 of
- * each (2^-9 where they are not next to a power of two); their sum is that of
- * the unrounded ones.  No workspace; bitwise reproducible, and a prompt's
- * result does not depend on the other prompts.
+ * each; their sum is that of the unrounded ones.  No workspace; bitwise
+ * reproducible, and a prompt's result does not depend on the other prompts.
  */
 pkv_status pkv_prompt_attention(void* out, float* out_lse, const void* q, int64_t q_stride, const void* k,
                                 int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_seqlens,

@@ -549,6 +549,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 make_uint4(0, 0, 0, 0);
           tc::fence_proxy_async_smem();  // before the product that the weights' arrival lets go
         }
+        // Exponents in one fused multiply-add: its product is not rounded and m is, so
+        // the largest weight is 2^(half a step of m), which FP32 holds up to 2^31.
+        // (Differences of raw scores times c, right for any: 1 to 2 % more time.)
         const float nm = (m == -INFINITY) ? 0.f : -m;
         const float2 c2 = make_float2(c, c);
         const float2 nm2 = make_float2(nm, nm);
