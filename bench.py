@@ -715,7 +715,7 @@ def bench_one(args, name: str, world: int, rank: int, local: int, headline: bool
         "metric": METRIC, "value": round(value, 2), "unit": "GB/s", "n_gpus": world, "steps": args.steps,
         "warmup": args.warmup, "ms_per_step": round(ms_per_step, 4), "higher_is_better": True, "scaling": "weak",
         "vs_baseline": None,
-        "dtype": ("fp8_e4m3 KV, e4m3 tensor-core Q.K and P.V (query and weights as e4m3 high + low parts), "
+        "dtype": ("fp8_e4m3 KV, e4m3 tensor-core Q.K and P.V (query as two e4m3, weights as three e5m2 parts), "
                   "f32 accumulation and softmax" if fp8 else
                   f"{args.kv} KV, f16 tensor-core Q.K, f32 softmax and P.V" if q8 else "bf16"),
         "data": "synthetic",

@@ -517,7 +517,9 @@ int32_t pkv_choose_kv_blocks_per_split_fp8_e4m3(int32_t num_seqs, int32_t num_kv
 /*
  * pkv_paged_attention_fp8_e4m3 -- one decode step over E4M3 pools with the
  * query in BF16: out = softmax(scale * q . K^T) V on the stored values
- * (Ch8 §8.4.4: K and V in FP8, the query in BF16).  Arguments, workspace
+ * (Ch8 §8.4.4: K and V in FP8, the query in BF16).  Queries enter as two E4M3
+ * parts (off by at most 2^-17 of a head's largest value), weights as three E5M2
+ * parts (2^-8 of each or 2^-30 of the row's largest).  Arguments, workspace
  * (pkv_workspace_size_q8_0) and errors exactly as pkv_paged_attention_q8_0;
  * kv_blocks_per_split 0 = pkv_choose_kv_blocks_per_split_fp8_e4m3.
  */

@@ -19,22 +19,24 @@
 // warps agreeing on the maxima) is what bounds an SM: each thread takes two
 // tokens per agreement.
 // Both operands of an 8-bit MMA are 8-bit, so the BF16 query and the FP32
-// weights enter as sums of E4M3 parts, which keeps them exact or nearly so:
+// weights enter as sums of 8-bit parts, which keeps them exact or nearly so:
 //   - Qp rows 0-3 are the 4 query heads of the GQA group scaled by a power of
 //     two sigma_h (the largest |q| lands in [128, 256)) and rounded to E4M3;
 //     rows 4-7 are the E4M3 rounding of what that left.  A BF16 value has 8
 //     significant bits and each part holds 4, so q * sigma_h = row h + row
 //     4 + h exactly, down to E4M3's smallest step (2^-9, i.e. 2^-16 of the
 //     largest element).  The softmax divides the scores by sigma_h again.
-//   - P^T rows 0-3 are the weights times 2^6, rounded to E4M3, rows 4-7 the
-//     rounding of the remainders: about 2^-8 relative per weight.  The
-//     running maximum moves lazily (when a score exceeds it by more than
-//     2^2), so a weight is at most 2^2 and 2^6 times it at most 2^8, inside
-//     E4M3's range (448); the factor keeps the remainders of weights above
-//     2^-8 out of E4M3's subnormal range.  The sum of the weights is kept in
-//     FP32 from the unrounded values; the epilogue divides O by 2^6 again.
-//
-// (The cache with block scales: three E5M2 parts of the weights instead, see below.)
+//   - P^T rows 0-3, 4-7 and 8-11 are three E5M2 parts of the weights times 2^13,
+//     by way of FP16, whose upper byte E5M2 is: the parts come by two
+//     subtractions.  The running maximum moves lazily (when a score exceeds it
+//     by more than 2^2), so a weight is at most 2^2 and 2^13 times it at most
+//     2^15.  E5M2's range down from there, to 2^-16, holds a weight to 2^-8 of
+//     itself down to 2^-21 of the row's largest one and to 2^-30 of that one
+//     below.  The sum of the weights is kept in FP32 from the unrounded values;
+//     the epilogue divides O by 2^13 again.  (Two E4M3 parts times 2^6 drop what
+//     lies under 2^-16 of the largest, while the sum that divides keeps it: where
+//     the first of 32,768 keys held nine tenths of the weight, the row was off by
+//     up to 0.65.  They took 1 to 2 % less time here, as much with block scales.)
 //
 // The persistent CTAs stride through the units.  CTA = 8 warps:
 //   warp 0 / 1 : K / V producer -- one TMA load per block (16 tokens x 128
@@ -58,14 +60,8 @@
 // in turn, each with a maximum, a sum and an accumulator of its own, and warps
 // 12-15 join the groups, divide and store while the softmax is at the next unit
 // (with one group that stores for itself a unit of one tile took 5000 cycles of
-// the softmax, 2,800 of them behind its tile).  The weights enter by way of FP16
-// as three E5M2 parts times 2^13, rows 0-3, 4-7 and 8-11 of P^T: E5M2 is FP16's
-// upper byte, so the parts come by two subtractions, and its range, 2^-16 .. 2^15,
-// holds a weight to 2^-8 of itself down to 2^-21 of the row's largest and to an
-// absolute 2^-30 of that below.  (Two E4M3 parts drop what lies under 2^-16 of the
-// largest, while the sum that divides keeps it: where the first key held nine
-// tenths of the weight of 32,768, the row was off by a third.)  What bounds it is HBM: 128
-// requests of 8192 to 8447 tokens, 8 KV heads, take 320 us, as long as a copy of
+// the softmax, 2,800 of them behind its tile).  What bounds it is HBM: 128
+// requests of 8192 to 8447 tokens, 8 KV heads, take 325 us, as long as a copy of
 // as many bytes; 64 of 16 to 16000 64 us (56), the rest being the start, 5 us to
 // the first scores, the ends of rows and the joining.  One request of 8300
 // tokens takes 11 us, all latency: bounds, table, tiles, four or five tiles of
@@ -124,12 +120,10 @@ constexpr uint32_t kColS = 0;    // S^T buffers at columns 0 and 32 (16 columns 
 constexpr uint32_t kColO = 64;   // O^T buffers at columns 64 and 80
 constexpr uint32_t kFtTmemCols = 128;
 constexpr float kFtLazyMax = 2.f;       // base-2 units: weights stay at or below 2^2
-constexpr float kFtPScale = 64.f;       // weights enter P^T times 2^6 (at most 2^8 < 448)
-constexpr float kFtPUnscale = 1.f / 64.f;
-// kScaled: times 2^13, at most 2^15, so that E5M2 holds them down to 2^-29 of the maximum.
-constexpr float kFtWideScale = 8192.f;
-constexpr float kFtWideUnscale = 1.f / 8192.f;
-constexpr int kFtWideCols = 12;         // columns of O^T: three parts of four heads
+// Weights enter P^T times 2^13, at most 2^15, so that E5M2 holds them down to 2^-29 of the maximum.
+constexpr float kFtPScale = 8192.f;
+constexpr float kFtPUnscale = 1.f / 8192.f;
+constexpr int kFtPCols = 12;            // columns of O^T: three parts of four heads
 constexpr float kFtLn2 = 0.6931471805599453f;
 constexpr int kFtNamedBar = 1;          // the softmax warps' barrier
 
@@ -138,7 +132,7 @@ static_assert(kOffSigma % 16 == 0 && kOffEnds % 16 == 0 && kOffWalk % 16 == 0 &&
 static_assert(kFtTileTokens == 2 * 128, "a tile is two 128-token MMA halves");
 static_assert(kOffV % 1024 == 0 && kOffQp % 1024 == 0 && kOffPt % 1024 == 0 && kFtOpBytes % 1024 == 0,
               "swizzled operands need 1 KiB alignment");
-static_assert(kFtLazyMax + 6.f <= 8.f, "scaled weights must stay inside E4M3's range");
+static_assert(kFtLazyMax + 13.f <= 15.f, "scaled weights must stay inside FP16's range, and E5M2's");
 
 // What the softmax leaves of a unit for the warps that finish it.
 struct alignas(16) FtEnd {
@@ -557,7 +551,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (nth >> 1) & 1));
     if (!ok) return;
     tc::fence_after_sync();
-    float o12[2][kFtWideCols];  // dim t: heads 0..3 of each part
+    float o12[2][kFtPCols];  // dim t: heads 0..3 of each part
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       tc::tmem_ld8(tmem + lane_off + kColO + 32 * ub + 16 * g, o12[g]);
@@ -572,7 +566,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
 #pragma unroll
       for (int g = 0; g < 2; ++g)
         if (f[g][h] != 0.f)
-          o[h] = fmaf((o12[g][h] + (o12[g][4 + h] + o12[g][8 + h])) * kFtWideUnscale, f[g][h], o[h]);
+          o[h] = fmaf((o12[g][h] + (o12[g][4 + h] + o12[g][8 + h])) * kFtPUnscale, f[g][h], o[h]);
     if constexpr (kCluster) {
 #pragma unroll
       for (int h = 0; h < 4; ++h) part_o[h * kHeadDim + t] = o[h];
@@ -606,7 +600,7 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
     // are done never waits behind the next tile's K arrival.
     if (lane == 0) {
       constexpr uint32_t kIdS = tc::idesc_e4m3_f32(128, kFtN, false, false);
-      constexpr uint32_t kIdO = tc::idesc_e4m3_f32(128, kFtN, true, false) | (kScaled ? tc::kIdescE5m2B : 0u);
+      constexpr uint32_t kIdO = tc::idesc_e4m3_f32(128, kFtN, true, false) | tc::kIdescE5m2B;
       struct Cursor {
         FtWalk walk;
         int j, i, seq, n;  // tile in unit, tile overall, unit ordinal, tiles of the unit (0: at the end)
@@ -980,19 +974,17 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[prev & 1], (prev >> 1) & 1));
             if (ok) {
               tc::fence_after_sync();
-              float o[kFtWideCols];  // columns h, 4 + h (kScaled: and 8 + h) of head h
+              float o[kFtPCols];  // columns h, 4 + h and 8 + h of head h
               tc::tmem_ld8(tmem + lane_off + ocol, o);
-              if constexpr (kScaled) tc::tmem_ld4(tmem + lane_off + ocol + 8, o + 8);
+              tc::tmem_ld4(tmem + lane_off + ocol + 8, o + 8);
               tc::tmem_wait_ld();
               uint32_t ob[8];
 #pragma unroll
               for (int h = 0; h < 8; ++h) ob[h] = __float_as_uint(o[h] * alpha[h & 3]);
               tc::tmem_st8(tmem + lane_off + ocol, ob);
-              if constexpr (kScaled) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) o[8 + h] *= alpha[h];
-                tc::tmem_st4(tmem + lane_off + ocol + 8, o + 8);
-              }
+              for (int h = 0; h < 4; ++h) o[8 + h] *= alpha[h];
+              tc::tmem_st4(tmem + lane_off + ocol + 8, o + 8);
               tc::tmem_wait_st();
               tc::fence_before_sync();
             }
@@ -1000,9 +992,8 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h) l[h] *= alpha[h];
         }
-        // the weights, and as E4M3 high parts and remainders times 2^6, head 2k in
-        // the low byte, 2k + 1 in the high byte; kScaled: as three E5M2 parts times
-        // 2^13, in the upper bytes of the two halves
+        // the weights, and as three E5M2 parts times 2^13, heads 2k and 2k + 1 in the
+        // upper bytes of the two halves
         uint32_t phi[2][2], plo[2][2], pmid[2][2];  // [half][pair]
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -1018,18 +1009,10 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if constexpr (kScaled) {
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                  : "=r"(phi[hf][k])
-                  : "f"(p[2 * k + 1] * kFtWideScale), "f"(p[2 * k] * kFtWideScale));
-              tc::e5m2_parts(phi[hf][k], pmid[hf][k], plo[hf][k]);
-              continue;
-            }
-            const float x0 = p[2 * k] * kFtPScale, x1 = p[2 * k + 1] * kFtPScale;
-            phi[hf][k] = f32x2_to_e4m3x2(x1, x0);
-            float r0, r1;
-            e4m3x2_to_f32x2(phi[hf][k], r0, r1);
-            plo[hf][k] = f32x2_to_e4m3x2(x1 - r1, x0 - r0);
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                : "=r"(phi[hf][k])
+                : "f"(p[2 * k + 1] * kFtPScale), "f"(p[2 * k] * kFtPScale));
+            tc::e5m2_parts(phi[hf][k], pmid[hf][k], plo[hf][k]);
           }
         }
         // P^T buffer sb is free once P.V(i - 2) has read it
@@ -1068,14 +1051,9 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
             uint8_t* pt = smem + kOffPt + (2 * sb + hf) * kFtOpBytes;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              if constexpr (kScaled) {
-                pt[tc::sw128_offset_b8(h, t)] = static_cast<uint8_t>(phi[hf][h >> 1] >> (8 + 16 * (h & 1)));
-                pt[tc::sw128_offset_b8(4 + h, t)] = static_cast<uint8_t>(pmid[hf][h >> 1] >> (8 + 16 * (h & 1)));
-                pt[tc::sw128_offset_b8(8 + h, t)] = static_cast<uint8_t>(plo[hf][h >> 1] >> (8 + 16 * (h & 1)));
-              } else {
-                pt[tc::sw128_offset_b8(h, t)] = static_cast<uint8_t>(phi[hf][h >> 1] >> (8 * (h & 1)));
-                pt[tc::sw128_offset_b8(4 + h, t)] = static_cast<uint8_t>(plo[hf][h >> 1] >> (8 * (h & 1)));
-              }
+              pt[tc::sw128_offset_b8(h, t)] = static_cast<uint8_t>(phi[hf][h >> 1] >> (8 + 16 * (h & 1)));
+              pt[tc::sw128_offset_b8(4 + h, t)] = static_cast<uint8_t>(pmid[hf][h >> 1] >> (8 + 16 * (h & 1)));
+              pt[tc::sw128_offset_b8(8 + h, t)] = static_cast<uint8_t>(plo[hf][h >> 1] >> (8 + 16 * (h & 1)));
             }
           }
           tc::fence_proxy_async_smem();  // P^T and zeroed V rows before the tensor core reads them
@@ -1122,14 +1100,15 @@ __global__ void __launch_bounds__(ft_threads(kMode), 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[ub], (seq >> 1) & 1));
         if (ok) {
           tc::fence_after_sync();
-          float o8[8];
-          tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o8);  // dim t: heads 0..3, high parts then remainders
+          float o12[kFtPCols];  // dim t: heads 0..3 of each part
+          tc::tmem_ld8(tmem + lane_off + kColO + 16 * ub, o12);
+          tc::tmem_ld4(tmem + lane_off + kColO + 16 * ub + 8, o12 + 8);
           tc::tmem_wait_ld();
           tc::fence_before_sync();
           mbar_arrive(&bars->o_empty[ub]);
           float o[4];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) o[h] = (o8[h] + o8[4 + h]) * kFtPUnscale;
+          for (int h = 0; h < 4; ++h) o[h] = (o12[h] + (o12[4 + h] + o12[8 + h])) * kFtPUnscale;
           if (direct) {
             uint16_t* dst = static_cast<uint16_t*>(a.out) + orow0 * kHeadDim + t;
 #pragma unroll

@@ -11,8 +11,9 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("e", [13, 20, 24, 27])
 def test_scores_far_from_zero(e):
-    """Scores of deviation 2^e, up to the largest that the call takes: their differences are far beyond the rounding of the scores, so a row's result is the
-    value of its highest key, to the rounding of that one weight (2^-8) and of the result (2^-8)."""
+    """Scores of deviation 2^e, up to the largest that the call takes: their differences are far beyond the rounding of
+    the scores, so a row's result is the value of its highest key, to the rounding of that one weight (2^-8) and of the
+    result (2^-8)."""
     lens = [300, 17, 900]
     q, k, v, cu = _inputs(lens, 2, 4, q_scale=1.0)
     q *= 2.0 ** (e // 2)
