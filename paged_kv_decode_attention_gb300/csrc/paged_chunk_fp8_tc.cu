@@ -53,9 +53,9 @@
 // buffer, one chain: 1.09); 37 x 7 behind 2048 to 2303 43 us, 4.0 TB/s (57): the
 // products' issue, the start, 6000 cycles to the first scores, the ends of jobs,
 // 3,500 each, and the joining kernel.  37 requests behind 2100 tokens, by the
-// rows' layout: 8 queries 41 us with M = 64, 49 with 64 rows of M = 128, 60 with
-// 128; 16 queries 55 with 64 rows, 65 with 128, 67 as kWide; 24 queries 68 with
-// 128, 73 as kWide; 32 queries 72 with 128, 77 as kWide.
+// rows' layout: 8 queries 42 us with M = 64, 50 with 64 rows of M = 128, 62 with
+// 128; 16 queries 55 with 64 rows, 67 with 128, 67 as kWide; 24 queries 70 with
+// 128, 74 as kWide; 32 queries 74 with 128, 78 as kWide.
 //
 // Work is cut by tiles, not by requests (pkv_shares.cuh); a cut job leaves
 // un-normalised FP32 partials.

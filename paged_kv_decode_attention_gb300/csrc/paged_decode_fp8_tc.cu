@@ -219,9 +219,14 @@ __device__ __forceinline__ int ft_tiles(const DecodeArgs& a, int r) {
 
 // kScaledCluster: where there are so few rows that kMaxClusterSplits CTAs for
 // each are resident at once, they take equal parts of it and join them through
-// distributed shared memory: one launch.  (8 KV heads, one request: 8300 tokens
-// 10.7 us against 12.1 with shares and their joining, 1000 tokens 6.2 against
-// 10.1.)
+// distributed shared memory: one launch.  One request, clusters against shares
+// and their joining, in us (from a graph):
+//     tokens      1000        4000        8300        16,000      32,768      131,072
+//     8 KV heads  6.3   9.9   7.3  10.3   10.6  11.3  13.7  12.5  22.7  16.6  75  47
+//     1 KV head   5.9   8.3   6.9   9.9   10.1  10.8  13.4  11.0  22.0  13.2  74  22
+// The rule goes by the rows alone, so beyond some 10,000 tokens it takes the
+// slower side.  (The host knows the tables' width, which bounds the contexts, and
+// not the contexts: by the width, short ones in wide tables would lose.)
 //
 // The units that a CTA works on, in order.  Every warp walks them for itself.
 struct alignas(16) FtWalk {

@@ -19,12 +19,12 @@
 // tile and pair of row tiles (an MMA with N = 64 takes 48 cycles where its
 // multiplications need 32, as it re-reads its 128-row operand), and for long
 // prompts the power limit.  Measured, 32 query and 8 KV heads: 2 prompts of
-// 16000 tokens 2.65 ms, 1.6 PFLOP/s, nine tenths of what a library's matrix
+// 16000 tokens 2.64 to 2.69 ms, 1.6 PFLOP/s, nine tenths of what a library's matrix
 // product holds for seconds (with tiles of 128 keys and one buffer for scores and
 // weights, one chain of S, softmax and P.V, 3.27; 64 keys, two such buffers, S
 // two tiles ahead and after the product that frees its buffer 3.15).  64 prompts
-// of 16 to 500 tokens 43.6 us (4.3 TB/s): 3.4 units a CTA, of which a start, a
-// first tile and an end are not hidden.  (Results by four or eight warps of
+// of 16 to 500 tokens 43.5 us (4.3 TB/s): 3.4 units a CTA, of which a start, a
+// first tile and an end are not hidden, and a last round that most CTAs sit out.  (Results by four or eight warps of
 // their own, as the softmax goes on: 54 us, as their registers are the
 // softmax's.)
 //
