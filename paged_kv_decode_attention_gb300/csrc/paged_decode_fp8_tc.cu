@@ -36,7 +36,7 @@
 //     the epilogue divides O by 2^13 again.  (Two E4M3 parts times 2^6 drop what
 //     lies under 2^-16 of the largest, while the sum that divides keeps it: where
 //     the first of 32,768 keys held nine tenths of the weight, the row was off by
-//     up to 0.65.  They took 1 to 2 % less time here, as much with block scales.)
+//     up to 0.65.  They took 1 to 2 % less time, with block scales as much.)
 //
 // The persistent CTAs stride through the units.  CTA = 8 warps:
 //   warp 0 / 1 : K / V producer -- one TMA load per block (16 tokens x 128
